@@ -9,6 +9,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+from .build import build  # noqa: F401  (bound here once: a later import of the submodule leaves the name alone)
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtinfer.so")
 
@@ -23,6 +25,8 @@ TINFER_EPI_STORE, TINFER_EPI_RESIDUAL, TINFER_EPI_SWIGLU, TINFER_EPI_ARGMAX = ra
 TINFER_S_INFLIGHT, TINFER_S_INFLIGHT_LM, TINFER_S_L2_LOOKAHEAD, TINFER_S_L2_PACE, TINFER_S_SYNC, TINFER_S_ATTN_CHUNKS = range(6)
 TINFER_SYNC_STAMPS, TINFER_SYNC_GRID_BARRIER = 0, 1
 TINFER_NOALLOC_SCRATCH_BYTES = 1 << 20
+TINFER_KV8_E4M3, TINFER_KV8_INT8 = 0, 1
+TINFER_DTYPE_F32, TINFER_DTYPE_F16, TINFER_DTYPE_BF16 = range(3)
 TRACE_FIELDS = 10  # stamps per CTA and phase of the timeline (tinfer_set_trace)
 
 EXPORTS = [
@@ -32,7 +36,8 @@ EXPORTS = [
     "tinfer_debug_withhold_results", "tinfer_set_schedule", "tinfer_get_schedule", "tinfer_destroy",
     "tinfer_packed_row_bytes", "tinfer_pack_matrix", "tinfer_op_gemv", "tinfer_op_attention",
     "tinfer_op_attention_noalloc", "tinfer_op_gemv_batch", "tinfer_moe_packed_bytes", "tinfer_pack_moe", "tinfer_op_moe",
-    "tinfer_op_gemm_bf16",
+    "tinfer_op_gemm_bf16", "tinfer_op_kv8_append", "tinfer_op_kv8_read", "tinfer_kv8_attention_workspace",
+    "tinfer_op_kv8_attention", "tinfer_op_logprobs",
 ]
 
 
@@ -61,12 +66,17 @@ class tinfer_weights(ctypes.Structure):
                 ("final_norm", ctypes.c_void_p), ("layer_blobs", ctypes.POINTER(ctypes.c_void_p))]
 
 
+class tinfer_kv8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("format", "n_seqs", "n_kv_heads", "head_dim", "max_ctx", "block")] + [
+        (n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales")]
+
+
+class tinfer_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int)] + [
+        (n, ctypes.c_longlong) for n in ("seq_stride", "token_stride", "head_stride")]
+
+
 _lib = None
-
-
-def build(force: bool = False) -> str:
-    from .build import build as _build
-    return _build(force=force)
 
 
 def lib():
@@ -78,6 +88,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I, D, Z, LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_double, ctypes.c_size_t, ctypes.c_longlong
         cfgp = ctypes.POINTER(tinfer_config)
+        kvp, rowp = ctypes.POINTER(tinfer_kv8), ctypes.POINTER(tinfer_rows)
         sig = {
             "tinfer_status_string": ([I], ctypes.c_char_p),
             "tinfer_check_config": ([cfgp], I),
@@ -107,6 +118,11 @@ def lib():
             "tinfer_pack_moe": ([I, I, I, I, I, I, P, P, P, P, P, P, P, P, P], I),
             "tinfer_op_moe": ([I, I, I, I, I, I, I, P, P, P, P, P, P, P, I, P, P], I),
             "tinfer_op_gemm_bf16": ([I, I, I, P, P, P, P], I),
+            "tinfer_op_kv8_append": ([kvp, rowp, rowp, I, P, P, D, P, P], I),
+            "tinfer_op_kv8_read": ([kvp, I, P, P, rowp, rowp, P, P], I),
+            "tinfer_kv8_attention_workspace": ([kvp, I, I], Z),
+            "tinfer_op_kv8_attention": ([kvp, I, I, rowp, P, P, D, rowp, P, P, Z, P, P], I),
+            "tinfer_op_logprobs": ([I, I, I, P, LL, P, I, P, P, P, P, P], I),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -281,6 +297,33 @@ def tinfer_op_gemm_bf16(m, n, k, x, w, y, stream=None) -> int:
     return lib().tinfer_op_gemm_bf16(m, n, k, _ptr(x), _ptr(w), _ptr(y), _stream(stream))
 
 
+def tinfer_op_kv8_append(cache: tinfer_kv8, k: tinfer_rows, v: tinfer_rows, n_tokens, pos, counts=None,
+                         rope_theta=0.0, status=None, stream=None) -> int:
+    return lib().tinfer_op_kv8_append(cache, k, v, n_tokens, _ptr(pos), _ptr(counts), rope_theta, _ptr(status),
+                                      _stream(stream))
+
+
+def tinfer_op_kv8_read(cache: tinfer_kv8, n_tokens, pos, counts, k: tinfer_rows, v: tinfer_rows, status=None,
+                       stream=None) -> int:
+    return lib().tinfer_op_kv8_read(cache, n_tokens, _ptr(pos), _ptr(counts), k, v, _ptr(status), _stream(stream))
+
+
+def tinfer_kv8_attention_workspace(cache: tinfer_kv8, n_heads, n_tokens) -> int:
+    return lib().tinfer_kv8_attention_workspace(cache, n_heads, n_tokens)
+
+
+def tinfer_op_kv8_attention(cache: tinfer_kv8, n_heads, n_tokens, q: tinfer_rows, pos, counts, rope_theta,
+                            out: tinfer_rows, lse, workspace, workspace_bytes, status=None, stream=None) -> int:
+    return lib().tinfer_op_kv8_attention(cache, n_heads, n_tokens, q, _ptr(pos), _ptr(counts), rope_theta, out,
+                                         _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream))
+
+
+def tinfer_op_logprobs(rows, vocab, dtype, logits, row_stride, targets, top_k, logp, entropy, top_ids, top_logp,
+                       stream=None) -> int:
+    return lib().tinfer_op_logprobs(rows, vocab, dtype, _ptr(logits), row_stride, _ptr(targets), top_k, _ptr(logp),
+                                    _ptr(entropy), _ptr(top_ids), _ptr(top_logp), _stream(stream))
+
+
 def make_config(c: dict, exec_mode: int = TINFER_MEGAKERNEL) -> tinfer_config:
     """tinfer_config from a workload description (synth.CONFIGS entries or the same keys)."""
     cfg = tinfer_config()
@@ -406,3 +449,165 @@ class Engine:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------------ the 8-bit cache and token scores on tensors
+
+def _dtype(t) -> int:
+    """TINFER_DTYPE_* of a tensor (ValueError for the others)."""
+    import torch
+    d = {torch.float32: TINFER_DTYPE_F32, torch.float16: TINFER_DTYPE_F16, torch.bfloat16: TINFER_DTYPE_BF16}.get(t.dtype)
+    if d is None:
+        raise ValueError(f"float32, float16 or bfloat16 is wanted, got {t.dtype}")
+    return d
+
+
+def _on(what: str, t, device, dtype=None, shape=None):
+    """Checks a tensor argument: its device, and its dtype and shape where given."""
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: {dtype} is wanted, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
+
+
+class Kv8Cache:
+    """An 8-bit KV cache of n_seqs sequences on one device, and the operators on it (tinfer_op_kv8_*). Rows are
+    tensors [n_seqs, n_tokens, heads, head_dim] with contiguous rows, of any strides that keep each row on 16
+    bytes. pos and counts are int32 tensors [n_seqs] on the device; pos[s] is where the first of the call's
+    tokens of sequence s stands. Work runs on `stream`, or on torch's current stream of the device.
+
+    buffers: (k_codes, v_codes, k_scales, v_scales) to use instead of new ones: uint8
+    [n_seqs, n_kv_heads, max_ctx, head_dim] and float32 [n_seqs, n_kv_heads, ceil(max_ctx / block)], contiguous.
+
+    The cache keeps one workspace for the attention, large enough for every call. A call that may overlap another
+    one in time (another stream, a graph replayed beside it) passes a workspace of its own (a uint8 tensor of
+    workspace_bytes(n_heads, n_tokens))."""
+
+    def __init__(self, n_kv_heads: int, head_dim: int, max_ctx: int, n_seqs: int = 1, fmt: int = TINFER_KV8_E4M3,
+                 block: int = 64, device="cuda", buffers=None):
+        import torch
+        codes = torch.Size((n_seqs, n_kv_heads, max_ctx, head_dim))
+        scales = torch.Size((n_seqs, n_kv_heads, -(-max_ctx // max(1, block))))
+        if buffers is None:
+            device = torch.device(device)
+            buffers = tuple(torch.zeros(codes, dtype=torch.uint8, device=device) for _ in range(2)) + tuple(
+                torch.zeros(scales, dtype=torch.float32, device=device) for _ in range(2))
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = buffers
+        self.device = self.k_codes.device
+        if self.device.type != "cuda":
+            raise ValueError("the cache lives on a CUDA device")
+        for what, t, dt, shape in zip(("k_codes", "v_codes", "k_scales", "v_scales"), buffers,
+                                      (torch.uint8, torch.uint8, torch.float32, torch.float32),
+                                      (codes, codes, scales, scales)):
+            _on(what, t, self.device, dt, shape)
+            if not t.is_contiguous():
+                raise ValueError(f"{what} is not contiguous")
+        self.n_seqs, self.n_kv_heads, self.head_dim, self.max_ctx = n_seqs, n_kv_heads, head_dim, max_ctx
+        self.c = tinfer_kv8(fmt, n_seqs, n_kv_heads, head_dim, max_ctx, block, *(t.data_ptr() for t in buffers))
+        need = self.workspace_bytes(n_kv_heads, 1)
+        if need == 0:
+            raise TinferError(TINFER_ERR_UNSUPPORTED, "Kv8Cache")
+        self._workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def _rows(self, what, t, heads=None, tokens=None) -> tinfer_rows:
+        s = t.shape
+        if (len(s) != 4 or s[0] != self.n_seqs or s[3] != self.head_dim or (heads is not None and s[2] != heads)
+                or (tokens is not None and s[1] != tokens)):
+            raise ValueError(f"{what}: rows [{self.n_seqs}, n_tokens, heads, {self.head_dim}] are wanted, got {tuple(s)}")
+        if t.device != self.device:
+            raise ValueError(f"{what} is on {t.device}, not on {self.device}")
+        st = t.stride()
+        if st[3] != 1:
+            raise ValueError(f"{what}: the elements of a row are not contiguous")
+        return tinfer_rows(t.data_ptr(), _dtype(t), st[0], st[1], st[2])
+
+    def _seqs(self, pos, counts, status):
+        import torch
+        for what, t, n in (("pos", pos, self.n_seqs), ("counts", counts, self.n_seqs), ("status", status, 1)):
+            if t is not None:
+                if t.dtype != torch.int32 or t.numel() != n or t.device != self.device or not t.is_contiguous():
+                    raise ValueError(f"{what}: a contiguous int32 tensor of {n} on {self.device} is wanted")
+
+    def _run(self, what, fn, args, status, stream):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, _ptr(status), _stream(stream))
+        else:
+            rc = fn(*args, _ptr(status), _stream(stream))
+        if rc != TINFER_OK:
+            raise TinferError(rc, what)
+
+    def append(self, k, v, pos, counts=None, rope_theta: float = 0.0, status=None, stream=None) -> None:
+        """Quantises rows k and v into the cache at pos (keys rotated first; rope_theta 0: they already are)."""
+        kr, vr = self._rows("k", k, self.n_kv_heads), self._rows("v", v, self.n_kv_heads, k.shape[1])
+        self._seqs(pos, counts, status)
+        self._run("tinfer_op_kv8_append", lib().tinfer_op_kv8_append,
+                  (self.c, kr, vr, k.shape[1], pos.data_ptr(), _ptr(counts), rope_theta), status, stream)
+
+    def read(self, n_tokens: int, pos, counts=None, out=None, dtype=None, status=None, stream=None):
+        """Reads n_tokens tokens of each sequence from pos on back into rows (k, v): `out`, or new ones of dtype
+        (bfloat16 when None), zero where a sequence has fewer tokens."""
+        import torch
+        if out is None:
+            out = tuple(torch.zeros((self.n_seqs, n_tokens, self.n_kv_heads, self.head_dim),
+                                    dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2))
+        kr, vr = (self._rows(what, t, self.n_kv_heads, n_tokens) for what, t in zip(("k", "v"), out))
+        self._seqs(pos, counts, status)
+        self._run("tinfer_op_kv8_read", lib().tinfer_op_kv8_read,
+                  (self.c, n_tokens, pos.data_ptr(), _ptr(counts), kr, vr), status, stream)
+        return out
+
+    def workspace_bytes(self, n_heads: int, n_tokens: int) -> int:
+        return lib().tinfer_kv8_attention_workspace(self.c, n_heads, n_tokens)
+
+    def attention(self, q, pos, counts=None, rope_theta: float = 0.0, out=None, lse=None, workspace=None, status=None,
+                  stream=None):
+        """Attention of the query rows q over the cache: token i of sequence s attends to positions
+        [0, pos[s] + i]. Returns `out` (rows like q; a new tensor, zero where a sequence has fewer tokens, when None)."""
+        import torch
+        qr = self._rows("q", q)
+        n_tokens, n_heads = q.shape[1], q.shape[2]
+        if out is None:
+            out = torch.zeros(q.shape, dtype=q.dtype, device=self.device)
+        orow = self._rows("out", out, n_heads, n_tokens)
+        self._seqs(pos, counts, status)
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or lse.device != self.device
+                                or not lse.is_contiguous()):
+            raise ValueError("lse: a contiguous float32 tensor [n_seqs, n_tokens, n_heads] is wanted")
+        if workspace is None:
+            workspace = self._workspace
+        elif workspace.dtype != torch.uint8 or workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous uint8 tensor on the cache's device is wanted")
+        self._run("tinfer_op_kv8_attention", lib().tinfer_op_kv8_attention,
+                  (self.c, n_heads, n_tokens, qr, pos.data_ptr(), _ptr(counts), rope_theta, orow, _ptr(lse),
+                   workspace.data_ptr(), workspace.numel()), status, stream)
+        return out
+
+
+def logprobs(logits, targets=None, top_k: int = 0, stream=None):
+    """(logp, entropy, top_ids, top_logp) of the rows of logits [rows, vocab] (tinfer_op_logprobs): the log
+    probability of each row's target token, the row's entropy, and its top_k likeliest tokens with theirs. logp
+    is None without targets, the last two are None when top_k is 0."""
+    import torch
+    if logits.dim() != 2 or logits.stride(1) != 1 or logits.device.type != "cuda":
+        raise ValueError("logits: [rows, vocab] on a CUDA device with contiguous rows is wanted")
+    rows, vocab = logits.shape
+    dev = logits.device
+    if targets is not None and (targets.dtype != torch.int32 or targets.shape != (rows,) or targets.device != dev
+                                or not targets.is_contiguous()):
+        raise ValueError(f"targets: a contiguous int32 tensor [{rows}] on {dev} is wanted")
+    logp = torch.empty(rows, dtype=torch.float32, device=dev) if targets is not None else None
+    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+    ids = torch.empty((rows, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
+    top = torch.empty((rows, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
+    with torch.cuda.device(dev):
+        rc = tinfer_op_logprobs(rows, vocab, _dtype(logits), logits, logits.stride(0) if rows > 1 else vocab, targets,
+                                top_k, logp, entropy, ids, top,
+                                torch.cuda.current_stream(dev) if stream is None else stream)
+    _check(rc, "tinfer_op_logprobs")
+    return logp, entropy, ids, top

@@ -355,6 +355,106 @@ tinfer_status tinfer_op_attention_noalloc(int n_heads, int n_kv_heads, int head_
                                           const float* qkv_dev, void* k_layer_dev,
                                           void* v_layer_dev, float* out_dev, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * A KV cache in 8 bits, and attention over it. The pages keep the cache in bf16; this is an addition for
+ * programs that serve longer contexts or several sequences at once, and verify drafted tokens (flint,
+ * "speculative decode": K + 1 positions verified in one pass).
+ *
+ * A code stands for code * scale. Each block of `block` consecutive positions of one sequence and KV head
+ * has one scale for K and one for V. format TINFER_KV8_E4M3: 8-bit floating point with 4 exponent and 3
+ * fraction bits (largest value 448; the codes 0x7F and 0xFF, its NaN, are never written and must not
+ * occur); TINFER_KV8_INT8: signed integers -127..127.
+ *
+ * The buffers are caller-owned device memory. k_codes, v_codes: [n_seqs][n_kv_heads][max_ctx][head_dim],
+ * 16-byte aligned; k_scales, v_scales: fp32 [n_seqs][n_kv_heads][ceil(max_ctx / block)]. They need no
+ * initial values: a block is defined by the append that writes its first position. head_dim 64 or 128,
+ * block 16, 32, 64 or 128, n_seqs <= 1024, n_kv_heads <= 1024, max_ctx <= 2^24.
+ *
+ * A tinfer_rows names rows of head_dim contiguous elements: the row of (sequence, token, head) starts
+ * seq*seq_stride + token*token_stride + head*head_stride elements after data. data 16-byte aligned, the
+ * strides not negative and multiples of 16 bytes; an operator that writes the rows also wants them apart
+ * (each stride of more than one element at least head_dim). So the projections of a step, slices of a
+ * fused buffer, and one layer of the bf16 cache of tinfer_create all serve as they are.
+ *
+ * pos_dev (int32 [n_seqs]) and counts_dev (int32 [n_seqs], NULL: n_tokens everywhere) are read on the
+ * device when the kernels run: token i < counts[s] of sequence s stands at position pos[s] + i. So a call
+ * captured in a CUDA graph follows the positions from replay to replay. A sequence whose positions are
+ * outside [0, max_ctx), or its count outside [0, n_tokens], is passed over: nothing of it is read or
+ * written, and bit 0 of *status_dev is set (int32, may be NULL; cleared first). Rows of tokens at or
+ * past counts[s] are neither read nor written. Every call is asynchronous on `stream`, allocates nothing
+ * and keeps no state between calls. rope_theta: the base of the rotary positions applied to keys as they
+ * are stored and to queries (half-split pairs, as in the decode step); 0: rows come already rotated;
+ * else at least 1. Arguments that the host can check return TINFER_ERR_INVALID_ARG or
+ * TINFER_ERR_UNSUPPORTED before anything is launched.
+ * --------------------------------------------------------------------------------------------- */
+enum { TINFER_KV8_E4M3 = 0, TINFER_KV8_INT8 = 1 };                                /* format */
+enum { TINFER_DTYPE_F32 = 0, TINFER_DTYPE_F16 = 1, TINFER_DTYPE_BF16 = 2 };       /* element types */
+
+typedef struct {
+  int format, n_seqs, n_kv_heads, head_dim, max_ctx, block;
+  void *k_codes, *v_codes;
+  float *k_scales, *v_scales;
+} tinfer_kv8;
+
+typedef struct {
+  void* data;
+  int dtype;
+  long long seq_stride, token_stride, head_stride; /* in elements */
+} tinfer_rows;
+
+/* Quantises the rows k and v (n_tokens tokens of each sequence, n_kv_heads heads, one dtype) into the
+ * cache at their positions; keys are rotated first. A block that the call starts (its first position is
+ * among the new ones) gets scale = max(max|x| / QMAX, 2^-126) over its new values in fp32, QMAX = 448 or
+ * 127; 0 when they are all 0. A block started by earlier calls keeps its scale while max|x| <= QMAX *
+ * scale; else the scale grows by the smallest power of two that makes them fit and the held codes of
+ * the positions below the first new one are rounded again in its units (a scale of 0 is replaced as in
+ * a new block). Codes are x / scale in fp32, rounded to the nearest code, ties to even. A NaN or an
+ * infinity among the values makes the block's scale NaN, and so everything read from the block until
+ * it is started again. Codes of positions past the new ones are left as they were and mean nothing
+ * until they are written. */
+tinfer_status tinfer_op_kv8_append(const tinfer_kv8* cache, const tinfer_rows* k, const tinfer_rows* v,
+                                   int n_tokens, const int32_t* pos_dev, const int32_t* counts_dev,
+                                   double rope_theta, int32_t* status_dev, void* stream);
+
+/* Reads tokens [pos[s], pos[s] + counts[s]) of every sequence back into rows k and v: code * scale in
+ * fp32, rounded once to the rows' dtype. Nothing is rotated back. */
+tinfer_status tinfer_op_kv8_read(const tinfer_kv8* cache, int n_tokens, const int32_t* pos_dev,
+                                 const int32_t* counts_dev, const tinfer_rows* k, const tinfer_rows* v,
+                                 int32_t* status_dev, void* stream);
+
+/* Attention of n_tokens query tokens of each sequence over the cache, whose positions up to the last
+ * query's must have been appended: token i of sequence s attends to positions [0, pos[s] + i], scale
+ * 1/sqrt(head_dim), query head h reading KV head h / (n_heads / n_kv_heads). q and out: rows of n_heads
+ * heads, one dtype; fp32 and fp16 queries are multiplied in fp32-like precision (two fp16 parts), bf16
+ * ones in fp16. out may be the memory of q. lse_dev: fp32 [n_seqs][n_tokens][n_heads], may be NULL: the natural
+ * logarithm of the sum of exp(score). workspace_dev: tinfer_kv8_attention_workspace bytes of device
+ * memory, 16-byte aligned, no initial values; calls that may overlap in time (other streams, other
+ * graphs) need one each. Bit 1 of *status_dev: a device wait ran out, and the outputs are not valid.
+ * tinfer_kv8_attention_workspace returns 0 for arguments that the call would refuse. */
+size_t tinfer_kv8_attention_workspace(const tinfer_kv8* cache, int n_heads, int n_tokens);
+tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int n_tokens,
+                                      const tinfer_rows* q, const int32_t* pos_dev,
+                                      const int32_t* counts_dev, double rope_theta,
+                                      const tinfer_rows* out, float* lse_dev, void* workspace_dev,
+                                      size_t workspace_bytes, int32_t* status_dev, void* stream);
+
+/* Log probabilities of given tokens, with the entropy and the likeliest alternatives of each row of
+ * logits (the decode step's and the verify shapes' output beyond its argmax). logits_dev: [rows][vocab]
+ * of `dtype`, rows row_stride elements apart (at least vocab); any element alignment. For each row, with
+ * p the softmax of its logits:
+ *   logp_dev[r]    = log p[targets_dev[r]]   (targets int32 [rows]; a target outside [0, vocab): NaN)
+ *   entropy_dev[r] = -sum p log p            (natural logarithm)
+ *   top_ids_dev, top_logp_dev [rows][top_k]: the top_k largest in order, equal logits by the lower id.
+ * A logit of -infinity is a masked token: probability 0, no part of the entropy, never an alternative (where fewer
+ * are left, the rest is id -1 with -infinity). A row whose tokens are all masked has logp -infinity
+ * and entropy 0. A row with a NaN or +infinity has NaN, and ids -1. logp_dev, entropy_dev and targets_dev
+ * may be NULL (logp_dev needs targets_dev); top_k in [0, 32], the top outputs NULL when it is 0.
+ * Results do not depend on timing.
+ * Asynchronous on `stream`, no workspace. vocab <= 2^18, else TINFER_ERR_UNSUPPORTED. */
+tinfer_status tinfer_op_logprobs(int rows, int vocab, int dtype, const void* logits_dev, long long row_stride,
+                                 const int32_t* targets_dev, int top_k, float* logp_dev, float* entropy_dev,
+                                 int32_t* top_ids_dev, float* top_logp_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
