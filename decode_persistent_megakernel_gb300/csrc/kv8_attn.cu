@@ -11,9 +11,10 @@
 //
 // Inside a CTA each warp streams its own tiles: a ring of bulk asynchronous copies per warp that runs on
 // across the boundaries of the units, no barrier between the warps until a unit ends. Products run on the
-// legacy warp-level tensor instruction (m16n8k16, fp16 in, fp32 accumulation): at 16 or 32 rows the
-// kernel is bound by the cache's bytes, the tensor pipe is not the limit, and register operands let the
-// codes go from shared memory to the product without being stored again in 16 bits.
+// legacy warp-level tensor instruction (m16n8k16, fp16 in, fp32 accumulation): with so few rows the tensor pipe
+// is not the limit, and register operands let the codes go from shared memory to the product without being
+// stored again in 16 bits. Keys (and dimensions of V) are the 16 rows of a product and query rows its
+// 8 columns, so a group of 8 query heads or fewer wastes nothing on padding.
 //
 // Precision. Codes widen to fp16 exactly. A query row is divided by the power of two above its largest
 // magnitude, which keeps it in fp16's range, and multiplied back in the scores' fp32 scale. Query and
@@ -33,9 +34,6 @@
 namespace tinfer {
 namespace kv8 {
 
-constexpr int NW = 8;               // warps of a CTA
-constexpr int NTHREADS_ATTN = NW * 32;
-constexpr int STAGES = 3;
 constexpr int WEIGHT_SHIFT = 14;    // weights are held times 2^14: fp16 keeps 11 bits of them down to 2^-28
 // Exponents of V scales that enter the running maximum. Of a row whose keys all have the smallest one the
 // sum of the softmax is 2^(WEIGHT_SHIFT - E_MIN) for each key: 2^24 keys stay below fp32's 2^128. A smaller
@@ -164,6 +162,11 @@ __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t high) {
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&high));
   return pack_half(a - h.x, b - h.y);
 }
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -182,42 +185,54 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
 }
 
 // ---- the kernel ----------------------------------------------------------------------------------
-template <int D, int MT>
+// A CTA's shape: NG groups of 8 query rows, NW warps, STAGES slots of 8 KiB in each warp's ring. Two groups
+// (one at 128 dimensions with two-part operands) leave registers for 12 warps; beyond that 8.
+template <int D, int NG, int SPLIT>
+struct Cfg {
+  static constexpr int NW = D * NG * (SPLIT + 1) <= 384 ? 12 : 8;
+  static constexpr int STAGES = NW == 12 ? 2 : 3;
+  static constexpr int NT = NW * 32;
+  static constexpr int ROWS = 8 * NG;
+};
+
+template <int D, int NG, int SPLIT>
 struct Smem {
-  static constexpr int ROWS = 16 * MT;
+  using C = Cfg<D, NG, SPLIT>;
   static constexpr int SCALES = Shape<D>::KT / 16;  // scales of one tile, at most (blocks of 16)
-  alignas(128) uint8_t ring[NW][STAGES][Shape<D>::STAGE_BYTES];
-  float ring_scale[NW][STAGES][2][SCALES];
-  alignas(16) float part[NW][16][32 + 4];  // one pass of the merge of the warps: 16 rows x 32 dimensions
-  float m[NW][ROWS], l[NW][ROWS];
-  alignas(16) uint32_t qf[2][MT][D / 16][32][4];  // query fragments: high and remainder
-  float row_scale[ROWS];
-  alignas(8) unsigned long long full[NW][STAGES];
-  int scan[NW];
+  alignas(128) uint8_t ring[C::NW][C::STAGES][Shape<D>::STAGE_BYTES];
+  float ring_scale[C::NW][C::STAGES][2][SCALES];
+  union alignas(16) {
+    float part[C::NW][8][64 + 4];               // one pass of the merge of the warps: 8 rows x 64 dimensions
+    uint32_t qf[SPLIT][NG][D / 16][32][2];      // query fragments: high and remainder; read before the merge
+  } u;
+  float m[C::NW][C::ROWS], l[C::NW][C::ROWS];
+  float row_scale[C::ROWS];
+  alignas(8) unsigned long long full[C::NW][C::STAGES];
+  int scan[C::NW];
   int failed;
 };
 
-template <int FMT, int D, int MT, int SPLIT, typename T>
-__global__ void __launch_bounds__(NTHREADS_ATTN, 1) kv8_attn_kernel(const __grid_constant__ AttnParams q) {
-  constexpr int KT = Shape<D>::KT, NT = KT / 8, ROWS = 16 * MT, DB = D / 8;
+template <int FMT, int D, int NG, int SPLIT, typename T>
+__global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(const __grid_constant__ AttnParams q) {
+  using C = Cfg<D, NG, SPLIT>;
+  constexpr int KT = Shape<D>::KT, MK = KT / 16, MD = D / 16, ROWS = C::ROWS, DB = D / 8, NW = C::NW, STAGES = C::STAGES;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  Smem<D, MT>& sm = *reinterpret_cast<Smem<D, MT>*>(smem_raw);
-  int* prefix = reinterpret_cast<int*>(smem_raw + sizeof(Smem<D, MT>));
+  Smem<D, NG, SPLIT>& sm = *reinterpret_cast<Smem<D, NG, SPLIT>*>(smem_raw);
+  int* prefix = reinterpret_cast<int*>(smem_raw + sizeof(sm));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
   if (lane == 0)
     for (int s = 0; s < STAGES; ++s) mbar_init(smem_addr(&sm.full[warp][s]), 33);  // the copy and 32 lanes' scales
   if (tid == 0) sm.failed = 0;
   mbar_fence_init();
-  const int total = build_prefix<D, NTHREADS_ATTN>(q, prefix, sm.scan);
+  const int total = build_prefix<D, C::NT>(q, prefix, sm.scan);
   const int per = tiles_per_cta(q, total, gridDim.x);
   const int lo = (int)min((long long)per * blockIdx.x, (long long)total), hi = min(lo + per, total);
   if (lo >= hi) return;
 
-  // this warp's tiles: those of [lo, hi) congruent to its index, so that the warps' shares stay even
-  const int first = lo + ((warp - lo) & (NW - 1));
+  // this warp's tiles: every NW-th of [lo, hi), across the units' boundaries
   Place<D> in, at;
-  in.seek(q, prefix, first);
+  in.seek(q, prefix, lo + warp);
   int put = 0, got = 0;
   const uint64_t policy = q.keep_l2 ? policy_evict_normal() : policy_evict_first();
   auto issue = [&]() {  // the next tile that has keys to read goes into the ring
@@ -246,7 +261,7 @@ __global__ void __launch_bounds__(NTHREADS_ATTN, 1) kv8_attn_kernel(const __grid
   __syncwarp();
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) issue();
-  at.seek(q, prefix, first);
+  at.seek(q, prefix, lo + warp);
 
   Place<D> seg;  // the unit that the CTA works on
   seg.seek(q, prefix, lo);
@@ -256,8 +271,8 @@ __global__ void __launch_bounds__(NTHREADS_ATTN, 1) kv8_attn_kernel(const __grid
     const int head = seg.unit / q.row_tiles, rt = seg.unit % q.row_tiles;
     const int rows = min(q.group * seg.count - rt * ROWS, ROWS);  // rows of this unit (may be <= 0)
 
-    // query rows: rotated, divided by a power of two, laid out as the products' left operands. Warp w
-    // takes rows w, w + 8, ...; a lane the rotary pairs of D / 64 dimensions (lane and lane + 32).
+    // query rows: rotated, divided by a power of two, laid out as the scores' right operands. Warp w takes
+    // rows w, w + NW, ...; a lane the rotary pairs of dimensions lane (and lane + 32).
     for (int r = warp; r < ROWS; r += NW) {
       float v[D / 32];
 #pragma unroll
@@ -290,46 +305,49 @@ __global__ void __launch_bounds__(NTHREADS_ATTN, 1) kv8_attn_kernel(const __grid
       if (lane == 0) sm.row_scale[r] = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        // dimension e belongs to thread e / (D/4) of the quad, fragment (e % (D/4)) / 4, and to the
-        // words a0/a1 (rows g, g + 8) or a2/a3, low or high half
+        // dimension e belongs to thread e / (D/4) of the quad, product step (e % (D/4)) / 4, word b0 or b1,
+        // low or high half
         const int e = (i < D / 64 ? lane + 32 * i : D / 2 + lane + 32 * (i - D / 64));
-        const int qt = e / (D / 4), in4 = e % (D / 4), ks = in4 / 4, w = (in4 & 2) + ((r & 8) ? 1 : 0);
+        const int qt = e / (D / 4), in4 = e % (D / 4);
         const float y = v[i] * down;
         const __half h = __float2half_rn(y);
-        __half* f0 = reinterpret_cast<__half*>(&sm.qf[0][r / 16][ks][(r & 7) * 4 + qt][w]) + (in4 & 1);
-        *f0 = h;
+        reinterpret_cast<__half*>(&sm.u.qf[0][r / 8][in4 / 4][(r & 7) * 4 + qt][(in4 >> 1) & 1])[in4 & 1] = h;
         if (SPLIT == 2)
-          reinterpret_cast<__half*>(&sm.qf[1][r / 16][ks][(r & 7) * 4 + qt][w])[in4 & 1] = __float2half_rn(y - __half2float(h));
+          reinterpret_cast<__half*>(&sm.u.qf[SPLIT - 1][r / 8][in4 / 4][(r & 7) * 4 + qt][(in4 >> 1) & 1])[in4 & 1] =
+              __float2half_rn(y - __half2float(h));
       }
     }
     __syncthreads();
-    uint32_t qf[SPLIT][MT][D / 16][4];
-    float rs[MT][2];
-    int limit[MT][2];  // first key that a row does not see
+    uint32_t qf[SPLIT][NG][MD][2];
+    float rs[NG][2];
+    int limit[NG][2];  // first key that a row does not see
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int n = 0; n < NG; ++n) {
 #pragma unroll
       for (int h = 0; h < SPLIT; ++h)
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint4 w = *reinterpret_cast<const uint4*>(sm.qf[h][m][k][lane]);
-          qf[h][m][k][0] = w.x; qf[h][m][k][1] = w.y; qf[h][m][k][2] = w.z; qf[h][m][k][3] = w.w;
+        for (int k = 0; k < MD; ++k) {
+          const uint2 w = *reinterpret_cast<const uint2*>(sm.u.qf[h][n][k][lane]);
+          qf[h][n][k][0] = w.x;
+          qf[h][n][k][1] = w.y;
         }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        rs[m][h] = sm.row_scale[m * 16 + h * 8 + g];
-        limit[m][h] = seg.pos + min((rt * ROWS + m * 16 + h * 8 + g) / q.group, seg.count - 1) + 1;
+        const int r = n * 8 + 2 * t + h;
+        rs[n][h] = sm.row_scale[r];
+        limit[n][h] = seg.pos + min((rt * ROWS + r) / q.group, seg.count - 1) + 1;
       }
     }
-    float o[MT][DB][4], mx[MT][2], l[MT][2];
+    const int all_see = seg.pos + min(rt * ROWS / q.group, seg.count - 1) + 1;  // keys that every row sees
+    float o[MD][NG][4], mx[NG][2], l[NG][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int n = 0; n < NG; ++n) {
 #pragma unroll
-      for (int j = 0; j < DB; ++j)
+      for (int j = 0; j < MD; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[m][j][i] = 0.f;
-      mx[m][0] = mx[m][1] = -INFINITY;
-      l[m][0] = l[m][1] = 0.f;
+        for (int i = 0; i < 4; ++i) o[j][n][i] = 0.f;
+      mx[n][0] = mx[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
     }
 
     while (at.x < seg_end) {
@@ -350,34 +368,35 @@ __global__ void __launch_bounds__(NTHREADS_ATTN, 1) kv8_attn_kernel(const __grid
         __syncwarp();
       }
       const int rel = key0 & ((1 << q.c.lg_block) - 1);
-      // ---- scores: n-tile j holds keys 8j .. 8j+7, column n of it key 8j + (n >> 1) + 4 (n & 1)
-      float s[MT][NT][4];
+      // ---- scores, keys by rows: m-tile j holds keys 16j .. 16j + 15, row r of it key
+      // 8 (r / 8) + ((r % 8) >> 1) + 4 (r & 1), so that the value products find a thread's keys in rows t, t + 4, ...
+      float s[MK][NG][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int j = 0; j < MK; ++j) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) s[m][j][0] = s[m][j][1] = s[m][j][2] = s[m][j][3] = 0.f;
-        const uint8_t* kr = kbuf + (8 * j + (g >> 1) + 4 * (g & 1)) * D + t * (D / 4);
+        for (int n = 0; n < NG; ++n) s[j][n][0] = s[j][n][1] = s[j][n][2] = s[j][n][3] = 0.f;
+        const uint8_t* kr = kbuf + (16 * j + (g >> 1) + 4 * (g & 1)) * D + t * (D / 4);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          const uint4 w = *reinterpret_cast<const uint4*>(kr + 16 * c);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+          const uint4 x = *reinterpret_cast<const uint4*>(kr + 16 * c), y = *reinterpret_cast<const uint4*>(kr + 8 * D + 16 * c);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t b0, b1;
-            codes_to_half<FMT>(ws[k], b0, b1);
+            uint32_t a[4];
+            codes_to_half<FMT>(xs[k], a[0], a[2]);
+            codes_to_half<FMT>(ys[k], a[1], a[3]);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int n = 0; n < NG; ++n)
 #pragma unroll
-              for (int h = 0; h < SPLIT; ++h) mma16816(s[m][j], qf[h][m][c * 4 + k], b0, b1);
+              for (int h = 0; h < SPLIT; ++h) mma16816(s[j][n], a, qf[h][n][c * 4 + k][0], qf[h][n][c * 4 + k][1]);
           }
         }
       }
       // ---- x + e for every score, masked; the rows' maxima
-      float vf[NT], vinv[NT];
-      const bool edge = keys < KT || key0 + KT > limit[0][0];
+      float vf[MK], vinv[MK];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int b = (rel + 8 * j) >> q.c.lg_block;
+      for (int j = 0; j < MK; ++j) {
+        const int b = (rel + 16 * j) >> q.c.lg_block;
         const float ks = sm.ring_scale[warp][st][0][b], vs = sm.ring_scale[warp][st][1][b];
         const int e = min(max((int)((__float_as_uint(vs) >> 23) & 0xFF) - 127, E_MIN), E_MAX);
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
@@ -387,69 +406,90 @@ __global__ void __launch_bounds__(NTHREADS_ATTN, 1) kv8_attn_kernel(const __grid
         vinv[j] = inv;
         const float fe = fine ? (float)e : __uint_as_float(0x7FC00000u);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[m][j][i] = fmaf(s[m][j][i], ks * rs[m][i >> 1], fe);
+        for (int n = 0; n < NG; ++n) {
+          const float f0 = ks * rs[n][0], f1 = ks * rs[n][1];
+          s[j][n][0] = fmaf(s[j][n][0], f0, fe);
+          s[j][n][1] = fmaf(s[j][n][1], f1, fe);
+          s[j][n][2] = fmaf(s[j][n][2], f0, fe);
+          s[j][n][3] = fmaf(s[j][n][3], f1, fe);
+        }
       }
-      if (edge) {
+      if (keys < KT || key0 + KT > all_see) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < MK; ++j)
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int n = 0; n < NG; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int key = 8 * j + t + 4 * (i & 1);
-              if (key >= keys || key0 + key >= limit[m][i >> 1]) s[m][j][i] = -INFINITY;
+              const int key = 16 * j + 8 * (i >> 1) + (g >> 1) + 4 * (g & 1);
+              if (key >= keys || key0 + key >= limit[n][i & 1]) s[j][n][i] = -INFINITY;
             }
       }
+      float now[NG][2];
+      bool grew = false;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float top = -INFINITY;
+          float top = fmaxf(s[0][n][h], s[0][n][2 + h]);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(s[m][j][2 * h], s[m][j][2 * h + 1]));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-          const float now = fmaxf(mx[m][h], top);
-          const float ref = now == -INFINITY ? 0.f : now;
-          const float shrink = exp2_fast(mx[m][h] - ref);
-          mx[m][h] = now;
-          l[m][h] *= shrink;
+          for (int j = 1; j < MK; ++j) top = fmaxf(top, fmaxf(s[j][n][h], s[j][n][2 + h]));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+          now[n][h] = fmaxf(mx[n][h], top);
+          grew |= now[n][h] != mx[n][h];
+        }
+      if (__any_sync(~0u, grew)) {  // after the first tiles the maxima seldom move
 #pragma unroll
-          for (int j = 0; j < DB; ++j) {
-            o[m][j][2 * h] *= shrink;
-            o[m][j][2 * h + 1] *= shrink;
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float shrink = mx[n][h] == now[n][h] ? 1.f : exp2_fast(mx[n][h] - now[n][h]);
+            mx[n][h] = now[n][h];
+            l[n][h] *= shrink;
+#pragma unroll
+            for (int j = 0; j < MD; ++j) {
+              o[j][n][h] *= shrink;
+              o[j][n][2 + h] *= shrink;
+            }
           }
-          const float from = ref - (float)WEIGHT_SHIFT;
+      }
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-            for (int i = 2 * h; i < 2 * h + 2; ++i) {
-              const float w = exp2_fast(s[m][j][i] - from);
-              l[m][h] = fmaf(w, vinv[j], l[m][h]);
-              s[m][j][i] = w * vf[j];
+        for (int h = 0; h < 2; ++h) {
+          const float from = mx[n][h] == -INFINITY ? 0.f : mx[n][h] - (float)WEIGHT_SHIFT;
+#pragma unroll
+          for (int j = 0; j < MK; ++j)
+#pragma unroll
+            for (int i = h; i < 4; i += 2) {
+              const float w = exp2_fast(s[j][n][i] - from);
+              l[n][h] = fmaf(w, vinv[j], l[n][h]);
+              s[j][n][i] = w * vf[j];
             }
         }
-      // ---- o += weights V, 16 keys at a time
+      // ---- o^T += V^T weights, 16 keys at a time; an 8 x 8 transpose turns the scores' layout (keys by
+      // rows) into that of a right operand (keys down the columns)
 #pragma unroll
-      for (int p = 0; p < NT / 2; ++p) {
-        uint32_t a[SPLIT][MT][4];
+      for (int p = 0; p < MK; ++p) {
+        uint32_t b[SPLIT][NG][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float u = s[m][2 * p + (i >> 1)][2 * (i & 1)], w = s[m][2 * p + (i >> 1)][2 * (i & 1) + 1];
-            a[0][m][i] = pack_half(u, w);
-            if (SPLIT == 2) a[SPLIT - 1][m][i] = pack_rest(u, w, a[0][m][i]);
+          for (int h = 0; h < 2; ++h) {
+            const float u = s[p][n][2 * h], w = s[p][n][2 * h + 1];
+            const uint32_t high = pack_half(u, w);
+            b[0][n][h] = transpose8(high);
+            if (SPLIT == 2) b[SPLIT - 1][n][h] = transpose8(pack_rest(u, w, high));
           }
-        // four keys of this thread; dimensions g * DB .. g * DB + DB - 1, n-tile j of the product
-        // holding dimension g * DB + j in column g
+        // four keys of this thread; dimensions g DB .. g DB + DB - 1: m-tile m takes g DB + 2m as its row g
+        // and g DB + 2m + 1 as its row g + 8
         const uint8_t* vr = vbuf + (16 * p + t) * D + g * DB;
         uint32_t w[4][DB / 4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint8_t* row = vr + 4 * i * D;  // keys t, t + 4 (first n-tile), t + 8, t + 12 (second)
+          const uint8_t* row = vr + 4 * i * D;  // keys t, t + 4, t + 8, t + 12
           if (DB == 8) {
             const uint2 y = *reinterpret_cast<const uint2*>(row);
             w[i][0] = y.x; w[i][1] = y.y;
@@ -463,15 +503,13 @@ __global__ void __launch_bounds__(NTHREADS_ATTN, 1) kv8_attn_kernel(const __grid
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // dimensions 4c + 2h and 4c + 2h + 1: interleave the two keys' bytes
             const uint32_t sel = h ? 0x7362 : 0x5140;
-            uint32_t b0[2], b1[2];
-            codes_to_half<FMT>(__byte_perm(w[0][c], w[1][c], sel), b0[0], b0[1]);
-            codes_to_half<FMT>(__byte_perm(w[2][c], w[3][c], sel), b1[0], b1[1]);
+            uint32_t a[4];
+            codes_to_half<FMT>(__byte_perm(w[0][c], w[1][c], sel), a[0], a[1]);
+            codes_to_half<FMT>(__byte_perm(w[2][c], w[3][c], sel), a[2], a[3]);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int n = 0; n < NG; ++n)
 #pragma unroll
-              for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int sp = 0; sp < SPLIT; ++sp) mma16816(o[m][4 * c + 2 * h + u], a[sp][m], b0[u], b1[u]);
+              for (int sp = 0; sp < SPLIT; ++sp) mma16816(o[2 * c + h][n], a, b[sp][n][0], b[sp][n][1]);
           }
       }
       __syncwarp();
@@ -482,68 +520,69 @@ __global__ void __launch_bounds__(NTHREADS_ATTN, 1) kv8_attn_kernel(const __grid
 
     // ---- the warps' parts of this unit, joined in order of the warps
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        l[m][h] += __shfl_xor_sync(~0u, l[m][h], 1);
-        l[m][h] += __shfl_xor_sync(~0u, l[m][h], 2);
-        if (t == 0) {
-          sm.m[warp][m * 16 + h * 8 + g] = mx[m][h];
-          sm.l[warp][m * 16 + h * 8 + g] = l[m][h];
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[n][h] += __shfl_xor_sync(~0u, l[n][h], x);
+        if (g == 0) {
+          sm.m[warp][n * 8 + 2 * t + h] = mx[n][h];
+          sm.l[warp][n * 8 + 2 * t + h] = l[n][h];
         }
       }
     __syncthreads();
-    const int slot = 2 * blockIdx.x + (seg.tile == 0 ? 1 : 0);
-    float* part = q.part + (size_t)slot * ROWS * (D + 2);
+    float* part = q.part + (size_t)(2 * blockIdx.x + (seg.tile == 0 ? 1 : 0)) * ROWS * (D + 2);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int n = 0; n < NG; ++n) {
+      if (8 * n >= rows) break;
       float shrink[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) top = fmaxf(top, sm.m[w][m * 16 + h * 8 + g]);
-        shrink[h] = mx[m][h] == -INFINITY ? 0.f : exp2_fast(mx[m][h] - top);
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, sm.m[w][n * 8 + 2 * t + h]);
+        shrink[h] = mx[n][h] == -INFINITY ? 0.f : exp2_fast(mx[n][h] - top);
+        if (l[n][h] != l[n][h]) shrink[h] = l[n][h];  // scores that are not finite
       }
 #pragma unroll
-      for (int pass = 0; pass < D / 32; ++pass) {
-        // dimension of o[m][j][i] is (2t + (i & 1)) * DB + j; a pass holds dimensions [32 pass, 32 pass + 32)
-        if (2 * t * DB / 32 == pass) {
+      for (int pass = 0; pass < D / 64; ++pass) {
+        if (g * DB / 64 == pass) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int d0 = (2 * t + (i & 1)) * DB - 32 * pass;
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < DB; j += 4)
-              *reinterpret_cast<float4*>(&sm.part[warp][(i >> 1) * 8 + g][d0 + j]) =
-                  make_float4(o[m][j][i] * shrink[i >> 1], o[m][j + 1][i] * shrink[i >> 1],
-                              o[m][j + 2][i] * shrink[i >> 1], o[m][j + 3][i] * shrink[i >> 1]);
-          }
+            for (int j = 0; j < DB; j += 4)  // dimension j of the thread's DB: o[j / 2], rows g (even) and g + 8 (odd)
+              *reinterpret_cast<float4*>(&sm.u.part[warp][2 * t + h][g * DB - 64 * pass + j]) =
+                  make_float4(o[j / 2][n][h] * shrink[h], o[j / 2][n][2 + h] * shrink[h], o[j / 2 + 1][n][h] * shrink[h],
+                              o[j / 2 + 1][n][2 + h] * shrink[h]);
         }
         __syncthreads();
-        const int r = tid >> 3, c = (tid & 7) * 4;  // 16 rows x 8 threads of four dimensions
-        const int row = m * 16 + r;
-        if (r < 16 && row < rows) {
+        const int r = tid >> 4, c = (tid & 15) * 4;  // 8 rows x 16 threads of four dimensions
+        const int row = n * 8 + r;
+        if (r < 8 && row < rows) {
           float top = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
           for (int w = 0; w < NW; ++w) top = fmaxf(top, sm.m[w][row]);
+#pragma unroll
           for (int w = 0; w < NW; ++w) {
             const float lw = sm.l[w][row];
-            if (lw == 0.f) continue;  // this warp saw no key of the row
-            sum = fmaf(lw, exp2_fast(sm.m[w][row] - top), sum);
-            const float4 y = *reinterpret_cast<const float4*>(&sm.part[w][r][c]);
-            acc[0] += y.x; acc[1] += y.y; acc[2] += y.z; acc[3] += y.w;
+            if (lw != 0.f) {  // else this warp saw no key of the row
+              sum = fmaf(lw, exp2_fast(sm.m[w][row] - top), sum);
+              const float4 y = *reinterpret_cast<const float4*>(&sm.u.part[w][r][c]);
+              acc[0] += y.x; acc[1] += y.y; acc[2] += y.z; acc[3] += y.w;
+            }
           }
           if (whole) {
             const float inv = 1.f / sum;
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] *= inv;
             const int qrow = rt * ROWS + row, tok = qrow / q.group, hq = head * q.group + qrow % q.group;
-            T* dst = static_cast<T*>(q.out.data) + seg.seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + 32 * pass + c;
+            T* dst = static_cast<T*>(q.out.data) + seg.seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + 64 * pass + c;
             store4(dst, acc);
             if (q.lse && pass == 0 && c == 0)
               q.lse[((size_t)seg.seq * q.sp.n_tokens + tok) * q.n_heads + hq] =
                   (log2f(sum) + top - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
           } else {
-            *reinterpret_cast<float4*>(part + (size_t)row * D + 32 * pass + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            *reinterpret_cast<float4*>(part + (size_t)row * D + 64 * pass + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
             if (pass == 0 && c == 0) {
               part[ROWS * D + row] = top;
               part[ROWS * D + ROWS + row] = sum;
@@ -558,98 +597,138 @@ __global__ void __launch_bounds__(NTHREADS_ATTN, 1) kv8_attn_kernel(const __grid
   if (tid == 0 && sm.failed && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
 }
 
-// Joins the parts of one unit that several CTAs hold, in order. One CTA per unit of a sequence, one warp
-// per row at a time, a lane D / 32 dimensions.
-template <int D, int MT, typename T>
-__global__ void __launch_bounds__(NTHREADS_ATTN) kv8_merge_kernel(const __grid_constant__ AttnParams q) {
-  constexpr int KT = Shape<D>::KT, ROWS = 16 * MT, N = D / 32;
+// Joins the parts of one unit that several CTAs hold. One CTA per unit of a sequence: its warps take the
+// parts in turn, 8 rows at a time in registers (a lane D / 32 dimensions of each), and meet in shared
+// memory in order of the warps.
+template <int D>
+constexpr int MERGE_WARPS = 1024 / D;
+
+template <int D, int NG, typename T>
+__global__ void __launch_bounds__(MERGE_WARPS<D> * 32) kv8_merge_kernel(const __grid_constant__ AttnParams q) {
+  constexpr int KT = Shape<D>::KT, ROWS = 8 * NG, N = D / 32, NW = MERGE_WARPS<D>;
   extern __shared__ int prefix[];
   __shared__ int scan[NW];
-  pdl_wait();  // the parts are complete
-  const int total = build_prefix<D, NTHREADS_ATTN>(q, prefix, scan);
+  __shared__ alignas(16) float acc_s[NW][8][32 * N];
+  __shared__ float sum_s[NW][8], top_s[8];
+  // the list depends on the call's inputs alone, so it is built while the parts are still being made
+  const int total = build_prefix<D, NW * 32>(q, prefix, scan);
   const int per = tiles_per_cta(q, total, q.grid);
   const int seq = blockIdx.x / q.units, unit = blockIdx.x % q.units;
   int pos, count;
-  if (!span_of(q.sp, seq, q.c.max_ctx, pos, count) || count == 0) return;
+  const bool ok = span_of(q.sp, seq, q.c.max_ctx, pos, count) && count > 0;
   const int tiles = (pos + count + KT - 1) / KT;
   const int a = prefix[seq] + unit * tiles, c0 = a / per, c1 = (a + tiles - 1) / per;
-  if (c0 == c1) return;  // one CTA had it whole
   const int head = unit / q.row_tiles, rt = unit % q.row_tiles;
   const int rows = min(q.group * count - rt * ROWS, ROWS);
+  pdl_wait();  // the parts are complete
+  if (!ok || c0 == c1) return;  // one CTA had it whole
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const size_t stride = (size_t)ROWS * (D + 2);
-  for (int row = warp; row < rows; row += NW) {
-    auto part = [&](int c) { return q.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * stride; };
-    float top = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part(c)[ROWS * D + row]);
+  auto part = [&](int c) { return q.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * ROWS * (D + 2); };
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    const int nr = min(rows - r0, 8);
+    for (int r = warp; r < nr; r += NW) {
+      float top = -INFINITY;
+      for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part(c)[ROWS * D + r0 + r]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    float sum = 0.f, acc[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float* p = part(c);
-      const float m = p[ROWS * D + row];
-      const float lc = p[ROWS * D + ROWS + row];
-      const float w = lc == 0.f ? 0.f : exp2_fast(m - top);
-      sum = fmaf(lc, w, sum);
-      const float* y = p + (size_t)row * D + lane * N;
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float2 f = *reinterpret_cast<const float2*>(y + i);
-        acc[i] = fmaf(f.x, w, acc[i]);
-        acc[i + 1] = fmaf(f.y, w, acc[i + 1]);
-      }
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      if (lane == 0) top_s[r] = top;
     }
-    const float inv = 1.f / sum;
-    const int qrow = rt * ROWS + row, tok = qrow / q.group, hq = head * q.group + qrow % q.group;
-    T* dst = static_cast<T*>(q.out.data) + seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + lane * N;
+    __syncthreads();
+    float sum[8], acc[8][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) store_one(dst + i, acc[i] * inv);
-    if (q.lse && lane == 0)
-      q.lse[((size_t)seq * q.sp.n_tokens + tok) * q.n_heads + hq] =
-          (log2f(sum) + top - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
+    for (int r = 0; r < 8; ++r) {
+      sum[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[r][i] = 0.f;
+    }
+#pragma unroll 2
+    for (int c = c0 + warp; c <= c1; c += NW) {
+      const float* p = part(c);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < nr) {
+          const float lc = p[ROWS * D + ROWS + r0 + r];
+          const float w = lc == 0.f ? 0.f : exp2_fast(p[ROWS * D + r0 + r] - top_s[r]);
+          sum[r] = fmaf(lc, w, sum[r]);
+          const float* y = p + (size_t)(r0 + r) * D + lane * N;
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(y + i);
+            acc[r][i] = fmaf(f.x, w, acc[r][i]);
+            acc[r][i + 1] = fmaf(f.y, w, acc[r][i + 1]);
+          }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc_s[warp][r][lane * N + i] = acc[r][i];
+      if (lane == 0) sum_s[warp][r] = sum[r];
+    }
+    __syncthreads();
+    for (int r = warp; r < nr; r += NW) {
+      const int used = min(NW, c1 - c0 + 1);
+      float total_l = 0.f, y[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = 0.f;
+      for (int w = 0; w < used; ++w) {
+        total_l += sum_s[w][r];
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] += acc_s[w][r][lane * N + i];
+      }
+      const float inv = 1.f / total_l;
+      const int qrow = rt * ROWS + r0 + r, tok = qrow / q.group, hq = head * q.group + qrow % q.group;
+      T* dst = static_cast<T*>(q.out.data) + seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + lane * N;
+#pragma unroll
+      for (int i = 0; i < N; ++i) store_one(dst + i, y[i] * inv);
+      if (q.lse && lane == 0)
+        q.lse[((size_t)seq * q.sp.n_tokens + tok) * q.n_heads + hq] =
+            (log2f(total_l) + top_s[r] - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------------------- host
 namespace {
 
-// Row tiles of 16, or of 32 where 16 would read the cache more than once and the registers allow it.
-int rows_per_tile(int rows, int head_dim) { return rows > 16 && head_dim == 64 ? 32 : 16; }
+// Rows of a unit: 8, 16 or 32 (16 at 128 dimensions, whose accumulators are twice as wide).
+int rows_per_tile(long long rows, int head_dim) { return rows <= 8 ? 8 : rows <= 16 || head_dim == 128 ? 16 : 32; }
 
-template <int FMT, int D, int MT, int SPLIT, typename T>
+template <int FMT, int D, int NG, int SPLIT, typename T>
 cudaError_t launch_t(const AttnParams& q, cudaStream_t st) {
-  auto kernel = kv8_attn_kernel<FMT, D, MT, SPLIT, T>;
-  const size_t smem = sizeof(Smem<D, MT>) + (size_t)(q.c.n_seqs + 1) * 4;
+  auto kernel = kv8_attn_kernel<FMT, D, NG, SPLIT, T>;
+  const size_t list = (size_t)(q.c.n_seqs + 1) * 4, smem = sizeof(Smem<D, NG, SPLIT>) + list;
+  static_assert(sizeof(Smem<D, NG, SPLIT>) + (MAX_SEQS + 1) * 4 <= 227 * 1024, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<q.grid, NTHREADS_ATTN, smem, st>>>(q);
+  kernel<<<q.grid, Cfg<D, NG, SPLIT>::NT, smem, st>>>(q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units));
-  cfg.blockDim = dim3(NTHREADS_ATTN);
-  cfg.dynamicSmemBytes = (size_t)(q.c.n_seqs + 1) * 4;
+  cfg.blockDim = dim3(MERGE_WARPS<D> * 32);
+  cfg.dynamicSmemBytes = list;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D, MT, T>, q);
+  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D, NG, T>, q);
 }
 
-template <int FMT, int D, int MT>
-cudaError_t launch_m(const AttnParams& q, int dtype, cudaStream_t st) {
-  if (dtype == TINFER_DTYPE_F32) return launch_t<FMT, D, MT, 2, float>(q, st);
-  if (dtype == TINFER_DTYPE_F16) return launch_t<FMT, D, MT, 2, __half>(q, st);
-  return launch_t<FMT, D, MT, 1, __nv_bfloat16>(q, st);
+template <int FMT, int D, int NG>
+cudaError_t launch_n(const AttnParams& q, int dtype, cudaStream_t st) {
+  if (dtype == TINFER_DTYPE_F32) return launch_t<FMT, D, NG, 2, float>(q, st);
+  if (dtype == TINFER_DTYPE_F16) return launch_t<FMT, D, NG, 2, __half>(q, st);
+  return launch_t<FMT, D, NG, 1, __nv_bfloat16>(q, st);
 }
 template <int FMT>
 cudaError_t launch_f(const AttnParams& q, int head_dim, int rows, int dtype, cudaStream_t st) {
-  if (head_dim == 128) return launch_m<FMT, 128, 1>(q, dtype, st);
-  return rows == 32 ? launch_m<FMT, 64, 2>(q, dtype, st) : launch_m<FMT, 64, 1>(q, dtype, st);
+  if (head_dim == 128) return rows == 8 ? launch_n<FMT, 128, 1>(q, dtype, st) : launch_n<FMT, 128, 2>(q, dtype, st);
+  return rows == 8    ? launch_n<FMT, 64, 1>(q, dtype, st)
+         : rows == 16 ? launch_n<FMT, 64, 2>(q, dtype, st)
+                      : launch_n<FMT, 64, 4>(q, dtype, st);
 }
 
 // Multiprocessors of the current device.
@@ -675,7 +754,7 @@ size_t tinfer_kv8_attention_workspace(const tinfer_kv8* cache, int n_heads, int 
   tinfer_status rc;
   if (!kv8::cache_of(cache, c, rc) || n_heads < 1 || n_heads % cache->n_kv_heads || n_tokens < 1) return 0;
   // one size for every number of rows, so that a program can keep one workspace for all its calls
-  return (size_t)kv8::MAX_GRID * 2 * kv8::rows_per_tile(17, cache->head_dim) * (cache->head_dim + 2) * 4;
+  return (size_t)kv8::MAX_GRID * 2 * kv8::rows_per_tile(1 << 20, cache->head_dim) * (cache->head_dim + 2) * 4;
 }
 
 tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int n_tokens, const tinfer_rows* q_rows,
@@ -698,7 +777,7 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   q.group = n_heads / cache->n_kv_heads;
   q.n_heads = n_heads;
   const long long rows = (long long)q.group * n_tokens;
-  const int per = kv8::rows_per_tile(rows > 16 ? 17 : 1, cache->head_dim);
+  const int per = kv8::rows_per_tile(rows, cache->head_dim);
   const long long row_tiles = (rows + per - 1) / per, units = row_tiles * cache->n_kv_heads;
   const int kt = 4096 / cache->head_dim;
   // the list of tiles is counted in 32 bits
