@@ -25,6 +25,9 @@
 // A key's V scale 2^e * f (1 <= f < 2) enters its weight: the running maximum M is taken over x + e (x
 // the score in units of log 2), the weight of V is w * f with w = 2^(x + e - M), and the sum of the
 // softmax adds w * 2^-e. So weights are near 1 where they matter whatever the scales of the blocks are.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -32,6 +35,9 @@
 #include "kv8_attn.cuh"
 
 namespace tinfer {
+namespace gemm {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // gemm.cu
+}
 namespace kv8 {
 
 constexpr int WEIGHT_SHIFT = 14;    // weights are held times 2^14: fp16 keeps 11 bits of them down to 2^-28
@@ -40,6 +46,13 @@ constexpr int WEIGHT_SHIFT = 14;    // weights are held times 2^14: fp16 keeps 1
 // scale's remainder makes its weights smaller than 1, a scale of 0 makes them 0 and counts in the sum.
 constexpr int E_MIN = -85, E_MAX = 120;
 constexpr long long WAIT_NS = 200LL * 1000 * 1000;
+
+// Byte of 16-byte chunk c of a row in its tile as the copies' swizzle leaves it: 128-byte rows exchange chunks
+// by the row's number modulo 8, 64-byte rows by half of it modulo 4.
+template <int D>
+__device__ __forceinline__ int swizzled(int c, int row) {
+  return (D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) * 16;
+}
 
 template <int D>
 struct Shape {
@@ -100,44 +113,33 @@ __device__ __forceinline__ int seq_of(const int* prefix, int n, int x) {
   return lo;
 }
 
-// A place in the list.
-template <int D>
+// A place in the list, with what the tiles of its unit share.
+template <int D, int ROWS>
 struct Place {
   int x, seq, unit, tile, tiles;  // tiles: of one unit of this sequence
-  int pos, count;
+  int limit;                      // keys that some row of the unit sees
+  int row0;                       // the KV head's first row among all rows of the cache
   __device__ void enter(const AttnParams& q) {
-    pos = q.sp.pos[seq];
-    count = q.sp.counts ? q.sp.counts[seq] : q.sp.n_tokens;
-    tiles = (pos + count + Shape<D>::KT - 1) / Shape<D>::KT;
+    const int pos = q.sp.pos[seq], count = q.sp.counts ? q.sp.counts[seq] : q.sp.n_tokens;
+    const int head = unit / q.row_tiles, rt = unit - head * q.row_tiles;
+    row0 = (seq * q.c.n_kv + head) * q.c.max_ctx;
+    limit = rt * ROWS >= q.group * count ? 0 : pos + min((rt * ROWS + ROWS - 1) / q.group, count - 1) + 1;
   }
   __device__ void seek(const AttnParams& q, const int* prefix, int at) {
     x = at;
+    limit = tile = 0;
     if (at >= prefix[q.c.n_seqs]) return;
     seq = seq_of(prefix, q.c.n_seqs, at);
-    enter(q);
+    tiles = (prefix[seq + 1] - prefix[seq]) / q.units;
     const int in = at - prefix[seq];
     unit = in / tiles;
     tile = in - unit * tiles;
+    enter(q);
   }
   __device__ void advance(const AttnParams& q, const int* prefix, int by, int end) {
     x += by;
     tile += by;
-    if (x >= end || tile < tiles) return;
-    if (x < prefix[seq + 1]) {
-      const int up = tile / tiles;
-      unit += up;
-      tile -= up * tiles;
-    } else {
-      seek(q, prefix, x);
-    }
-  }
-  // Keys that the rows of this unit can see, counted from the first key of the tile.
-  template <int ROWS>
-  __device__ int keys(const AttnParams& q) const {
-    const int rt = unit % q.row_tiles;
-    if (rt * ROWS >= q.group * count) return 0;  // no rows here: the sequence has fewer new tokens
-    const int last = min(min((rt * ROWS + ROWS - 1) / q.group, q.sp.n_tokens - 1), count - 1);
-    return min(pos + last + 1 - tile * Shape<D>::KT, Shape<D>::KT);
+    if (tile >= tiles && x < end) seek(q, prefix, x);
   }
 };
 
@@ -166,6 +168,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+// KT rows of codes from row y on; rows past the cache's end arrive as zeros.
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int y, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
 }
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -199,12 +209,13 @@ template <int D, int NG, int SPLIT>
 struct Smem {
   using C = Cfg<D, NG, SPLIT>;
   static constexpr int SCALES = Shape<D>::KT / 16;  // scales of one tile, at most (blocks of 16)
-  alignas(128) uint8_t ring[C::NW][C::STAGES][Shape<D>::STAGE_BYTES];
+  alignas(1024) uint8_t ring[C::NW][C::STAGES][Shape<D>::STAGE_BYTES];
   float ring_scale[C::NW][C::STAGES][2][SCALES];
   union alignas(16) {
     float part[C::NW][8][64 + 4];               // one pass of the merge of the warps: 8 rows x 64 dimensions
     uint32_t qf[SPLIT][NG][D / 16][32][2];      // query fragments: high and remainder; read before the merge
   } u;
+  int4 slot[C::NW][C::STAGES];  // of a tile in the ring: place in the list, first key, keys
   float m[C::NW][C::ROWS], l[C::NW][C::ROWS];
   float row_scale[C::ROWS];
   alignas(8) unsigned long long full[C::NW][C::STAGES];
@@ -213,10 +224,12 @@ struct Smem {
 };
 
 template <int FMT, int D, int NG, int SPLIT, typename T>
-__global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(const __grid_constant__ AttnParams q) {
+__global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(const __grid_constant__ CUtensorMap map_k,
+                                                                              const __grid_constant__ CUtensorMap map_v,
+                                                                              const __grid_constant__ AttnParams q) {
   using C = Cfg<D, NG, SPLIT>;
   constexpr int KT = Shape<D>::KT, MK = KT / 16, MD = D / 16, ROWS = C::ROWS, DB = D / 8, NW = C::NW, STAGES = C::STAGES;
-  extern __shared__ __align__(128) unsigned char smem_raw[];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem<D, NG, SPLIT>& sm = *reinterpret_cast<Smem<D, NG, SPLIT>*>(smem_raw);
   int* prefix = reinterpret_cast<int*>(smem_raw + sizeof(sm));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -231,45 +244,45 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   if (lo >= hi) return;
 
   // this warp's tiles: every NW-th of [lo, hi), across the units' boundaries
-  Place<D> in, at;
+  Place<D, ROWS> in;
   in.seek(q, prefix, lo + warp);
   int put = 0, got = 0;
   const uint64_t policy = q.keep_l2 ? policy_evict_normal() : policy_evict_first();
   auto issue = [&]() {  // the next tile that has keys to read goes into the ring
-    int keys = 0;
-    while (in.x < hi && (keys = in.template keys<ROWS>(q)) <= 0) in.advance(q, prefix, NW, hi);
+    while (in.x < hi && in.tile * KT >= in.limit) in.advance(q, prefix, NW, hi);
     if (in.x >= hi) return;
-    const int st = put % STAGES;
+    const int st = put % STAGES, key0 = in.tile * KT, keys = min(in.limit - key0, KT);
     const uint32_t bar = smem_addr(&sm.full[warp][st]);
-    const size_t plane = (size_t)in.seq * q.c.n_kv + in.unit / q.row_tiles;
-    const size_t off = (plane * q.c.max_ctx + (size_t)in.tile * KT) * D;
     if (lane == 0) {
-      const uint32_t dst = smem_addr(sm.ring[warp][st]), bytes = (uint32_t)keys * D;
-      mbar_arrive_expect_tx(bar, 2 * bytes);
-      bulk_g2s(dst, q.c.k + off, bytes, bar, policy);
-      bulk_g2s(dst + KT * D, q.c.v + off, bytes, bar, policy);
+      const uint32_t dst = smem_addr(sm.ring[warp][st]);
+      sm.slot[warp][st] = make_int4(in.x, key0, keys, 0);
+      mbar_arrive_expect_tx(bar, 2 * KT * D);
+      load_tile(dst, &map_k, in.row0 + key0, bar, policy);
+      load_tile(dst + KT * D, &map_v, in.row0 + key0, bar, policy);
     }
-    const int b0 = in.tile * KT >> q.c.lg_block, nb = ((in.tile * KT + keys - 1) >> q.c.lg_block) - b0 + 1;
+    const int b0 = key0 >> q.c.lg_block, nb = ((key0 + keys - 1) >> q.c.lg_block) - b0 + 1;
     if (lane < nb) {
-      cp_async_4(smem_addr(&sm.ring_scale[warp][st][0][lane]), q.c.ks + plane * q.c.n_blocks + b0 + lane);
-      cp_async_4(smem_addr(&sm.ring_scale[warp][st][1][lane]), q.c.vs + plane * q.c.n_blocks + b0 + lane);
+      const size_t at = (size_t)(in.seq * q.c.n_kv + in.unit / q.row_tiles) * q.c.n_blocks + b0 + lane;
+      cp_async_4(smem_addr(&sm.ring_scale[warp][st][0][lane]), q.c.ks + at);
+      cp_async_4(smem_addr(&sm.ring_scale[warp][st][1][lane]), q.c.vs + at);
     }
     cp_async_arrive(bar);
     ++put;
     in.advance(q, prefix, NW, hi);
   };
   __syncwarp();
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < STAGES; ++s) issue();
-  at.seek(q, prefix, lo + warp);
+  __syncwarp();
 
-  Place<D> seg;  // the unit that the CTA works on
+  Place<D, ROWS> seg;  // the unit that the CTA works on
   seg.seek(q, prefix, lo);
   while (seg.x < hi) {
     const int seg_end = min(hi, seg.x + seg.tiles - seg.tile);
     const bool whole = seg.tile == 0 && seg_end - seg.x == seg.tiles;
     const int head = seg.unit / q.row_tiles, rt = seg.unit % q.row_tiles;
-    const int rows = min(q.group * seg.count - rt * ROWS, ROWS);  // rows of this unit (may be <= 0)
+    const int pos = q.sp.pos[seg.seq], count = q.sp.counts ? q.sp.counts[seg.seq] : q.sp.n_tokens;
+    const int rows = min(q.group * count - rt * ROWS, ROWS);  // rows of this unit (may be <= 0)
 
     // query rows: rotated, divided by a power of two, laid out as the scores' right operands. Warp w takes
     // rows w, w + NW, ...; a lane the rotary pairs of dimensions lane (and lane + 32).
@@ -286,7 +299,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
           float a = (float)p[e], z = (float)p[e + D / 2];
           if (q.rope.on) {
             float cs, sn;
-            rope_cos_sin(q.rope.f[e], seg.pos + tok, cs, sn);
+            rope_cos_sin(q.rope.f[e], pos + tok, cs, sn);
             const float a2 = a * cs - z * sn;
             z = z * cs + a * sn;
             a = a2;
@@ -335,10 +348,10 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       for (int h = 0; h < 2; ++h) {
         const int r = n * 8 + 2 * t + h;
         rs[n][h] = sm.row_scale[r];
-        limit[n][h] = seg.pos + min((rt * ROWS + r) / q.group, seg.count - 1) + 1;
+        limit[n][h] = pos + min((rt * ROWS + r) / q.group, count - 1) + 1;
       }
     }
-    const int all_see = seg.pos + min(rt * ROWS / q.group, seg.count - 1) + 1;  // keys that every row sees
+    const int all_see = pos + min(rt * ROWS / q.group, count - 1) + 1;  // keys that every row sees
     float o[MD][NG][4], mx[NG][2], l[NG][2];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
@@ -350,14 +363,11 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       l[n][0] = l[n][1] = 0.f;
     }
 
-    while (at.x < seg_end) {
-      const int keys = at.template keys<ROWS>(q);
-      if (keys <= 0) {
-        at.advance(q, prefix, NW, hi);
-        continue;
-      }
+    while (got < put) {
       const int st = got % STAGES;
-      const int key0 = at.tile * KT;
+      const int4 slot = sm.slot[warp][st];
+      if (slot.x >= seg_end) break;
+      const int key0 = slot.y, keys = slot.z;
       if (!wait_bounded(smem_addr(&sm.full[warp][st]), (got / STAGES) & 1)) sm.failed = 1;
       uint8_t* kbuf = sm.ring[warp][st];
       uint8_t* vbuf = kbuf + KT * D;
@@ -368,17 +378,19 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
         __syncwarp();
       }
       const int rel = key0 & ((1 << q.c.lg_block) - 1);
-      // ---- scores, keys by rows: m-tile j holds keys 16j .. 16j + 15, row r of it key
-      // 8 (r / 8) + ((r % 8) >> 1) + 4 (r & 1), so that the value products find a thread's keys in rows t, t + 4, ...
+      // ---- scores, keys by rows: m-tile j holds keys 16j .. 16j + 15. The contraction's order is free, so
+      // a thread takes D / 4 neighbouring dimensions of its keys g and g + 8: 16-byte loads, spread over the
+      // banks by the swizzle that the copies wrote the tile in
       float s[MK][NG][4];
 #pragma unroll
       for (int j = 0; j < MK; ++j) {
 #pragma unroll
         for (int n = 0; n < NG; ++n) s[j][n][0] = s[j][n][1] = s[j][n][2] = s[j][n][3] = 0.f;
-        const uint8_t* kr = kbuf + (16 * j + (g >> 1) + 4 * (g & 1)) * D + t * (D / 4);
+        const uint8_t* kr = kbuf + (16 * j + g) * D;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          const uint4 x = *reinterpret_cast<const uint4*>(kr + 16 * c), y = *reinterpret_cast<const uint4*>(kr + 8 * D + 16 * c);
+          const int at = swizzled<D>(t * (D / 64) + c, g);
+          const uint4 x = *reinterpret_cast<const uint4*>(kr + at), y = *reinterpret_cast<const uint4*>(kr + 8 * D + at);
           const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -421,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
           for (int n = 0; n < NG; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int key = 16 * j + 8 * (i >> 1) + (g >> 1) + 4 * (g & 1);
+              const int key = 16 * j + 8 * (i >> 1) + g;
               if (key >= keys || key0 + key >= limit[n][i & 1]) s[j][n][i] = -INFINITY;
             }
       }
@@ -485,11 +497,11 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
           }
         // four keys of this thread; dimensions g DB .. g DB + DB - 1: m-tile m takes g DB + 2m as its row g
         // and g DB + 2m + 1 as its row g + 8
-        const uint8_t* vr = vbuf + (16 * p + t) * D + g * DB;
         uint32_t w[4][DB / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t* row = vr + 4 * i * D;  // keys t, t + 4, t + 8, t + 12
+        for (int i = 0; i < 4; ++i) {  // keys 2t, 2t + 1, 2t + 8, 2t + 9
+          const int key = 2 * t + (i & 1) + 4 * (i & 2);
+          const uint8_t* row = vbuf + (16 * p + key) * D + swizzled<D>(g * DB / 16, key) + (DB == 8 ? (g & 1) * 8 : 0);
           if (DB == 8) {
             const uint2 y = *reinterpret_cast<const uint2*>(row);
             w[i][0] = y.x; w[i][1] = y.y;
@@ -514,8 +526,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       }
       __syncwarp();
       ++got;
-      at.advance(q, prefix, NW, hi);
       issue();
+      __syncwarp();
     }
 
     // ---- the warps' parts of this unit, joined in order of the warps
@@ -597,19 +609,18 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   if (tid == 0 && sm.failed && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
 }
 
-// Joins the parts of one unit that several CTAs hold. One CTA per unit of a sequence: its warps take the
-// parts in turn, 8 rows at a time in registers (a lane D / 32 dimensions of each), and meet in shared
-// memory in order of the warps.
-template <int D>
-constexpr int MERGE_WARPS = 1024 / D;
+// Joins the parts of one unit that several CTAs hold: CTA (unit of a sequence, slice of its rows). A row with
+// few parts is one warp's work; the parts of a long one are dealt out to all warps and meet in shared
+// memory. Either way they add up in a fixed order.
+constexpr int MERGE_WARPS = 8;
 
 template <int D, int NG, typename T>
-__global__ void __launch_bounds__(MERGE_WARPS<D> * 32) kv8_merge_kernel(const __grid_constant__ AttnParams q) {
-  constexpr int KT = Shape<D>::KT, ROWS = 8 * NG, N = D / 32, NW = MERGE_WARPS<D>;
+__global__ void __launch_bounds__(MERGE_WARPS * 32) kv8_merge_kernel(const __grid_constant__ AttnParams q) {
+  constexpr int KT = Shape<D>::KT, ROWS = 8 * NG, N = D / 32, NW = MERGE_WARPS;
   extern __shared__ int prefix[];
   __shared__ int scan[NW];
-  __shared__ alignas(16) float acc_s[NW][8][32 * N];
-  __shared__ float sum_s[NW][8], top_s[8];
+  __shared__ alignas(16) float acc_s[NW][D];
+  __shared__ float sum_s[NW];
   // the list depends on the call's inputs alone, so it is built while the parts are still being made
   const int total = build_prefix<D, NW * 32>(q, prefix, scan);
   const int per = tiles_per_cta(q, total, q.grid);
@@ -617,75 +628,65 @@ __global__ void __launch_bounds__(MERGE_WARPS<D> * 32) kv8_merge_kernel(const __
   int pos, count;
   const bool ok = span_of(q.sp, seq, q.c.max_ctx, pos, count) && count > 0;
   const int tiles = (pos + count + KT - 1) / KT;
-  const int a = prefix[seq] + unit * tiles, c0 = a / per, c1 = (a + tiles - 1) / per;
+  const int a = prefix[seq] + unit * tiles, c0 = a / per, parts = (a + tiles - 1) / per - c0 + 1;
   const int head = unit / q.row_tiles, rt = unit % q.row_tiles;
   const int rows = min(q.group * count - rt * ROWS, ROWS);
   pdl_wait();  // the parts are complete
-  if (!ok || c0 == c1) return;  // one CTA had it whole
+  if (!ok || parts <= 1) return;  // one CTA had it whole
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto part = [&](int c) { return q.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * ROWS * (D + 2); };
-  for (int r0 = 0; r0 < rows; r0 += 8) {
-    const int nr = min(rows - r0, 8);
-    for (int r = warp; r < nr; r += NW) {
-      float top = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part(c)[ROWS * D + r0 + r]);
+  const bool few = parts <= NW;
+  auto part = [&](int c) { return q.part + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * ROWS * (D + 2); };
+  const int row_step = few ? NW * gridDim.y : gridDim.y;
+  for (int row = few ? blockIdx.y * NW + warp : blockIdx.y; row < rows; row += row_step) {
+    float top = -INFINITY;
+    for (int c = lane; c < parts; c += 32) top = fmaxf(top, part(c)[ROWS * D + row]);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-      if (lane == 0) top_s[r] = top;
-    }
-    __syncthreads();
-    float sum[8], acc[8][N];
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    float sum = 0.f, y[N];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      sum[r] = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) acc[r][i] = 0.f;
-    }
-#pragma unroll 2
-    for (int c = c0 + warp; c <= c1; c += NW) {
+    for (int i = 0; i < N; ++i) y[i] = 0.f;
+#pragma unroll 8
+    for (int c = few ? 0 : warp; c < parts; c += few ? 1 : NW) {
       const float* p = part(c);
+      const float lc = p[ROWS * D + ROWS + row], mc = p[ROWS * D + row];
+      float f[N];
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < nr) {
-          const float lc = p[ROWS * D + ROWS + r0 + r];
-          const float w = lc == 0.f ? 0.f : exp2_fast(p[ROWS * D + r0 + r] - top_s[r]);
-          sum[r] = fmaf(lc, w, sum[r]);
-          const float* y = p + (size_t)(r0 + r) * D + lane * N;
+      for (int i = 0; i < N; i += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p + (size_t)row * D + lane * N + i);
+        f[i] = v.x;
+        f[i + 1] = v.y;
+      }
+      const float w = lc == 0.f ? 0.f : exp2_fast(mc - top);
+      sum = fmaf(lc, w, sum);
 #pragma unroll
-          for (int i = 0; i < N; i += 2) {
-            const float2 f = *reinterpret_cast<const float2*>(y + i);
-            acc[r][i] = fmaf(f.x, w, acc[r][i]);
-            acc[r][i + 1] = fmaf(f.y, w, acc[r][i + 1]);
-          }
-        }
+      for (int i = 0; i < N; ++i) y[i] = fmaf(f[i], w, y[i]);
     }
+    if (!few) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) acc_s[warp][r][lane * N + i] = acc[r][i];
-      if (lane == 0) sum_s[warp][r] = sum[r];
-    }
-    __syncthreads();
-    for (int r = warp; r < nr; r += NW) {
-      const int used = min(NW, c1 - c0 + 1);
-      float total_l = 0.f, y[N];
+      for (int i = 0; i < N; ++i) acc_s[warp][lane * N + i] = y[i];
+      if (lane == 0) sum_s[warp] = sum;
+      __syncthreads();
+      sum = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) y[i] = 0.f;
-      for (int w = 0; w < used; ++w) {
-        total_l += sum_s[w][r];
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] += acc_s[w][r][lane * N + i];
+      for (int w = 0; w < NW; ++w) {
+        sum += sum_s[w];
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] += acc_s[w][lane * N + i];
       }
-      const float inv = 1.f / total_l;
-      const int qrow = rt * ROWS + r0 + r, tok = qrow / q.group, hq = head * q.group + qrow % q.group;
+      __syncthreads();
+    }
+    if (few || warp == 0) {
+      const float inv = 1.f / sum;
+      const int qrow = rt * ROWS + row, tok = qrow / q.group, hq = head * q.group + qrow % q.group;
       T* dst = static_cast<T*>(q.out.data) + seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + lane * N;
 #pragma unroll
       for (int i = 0; i < N; ++i) store_one(dst + i, y[i] * inv);
       if (q.lse && lane == 0)
         q.lse[((size_t)seq * q.sp.n_tokens + tok) * q.n_heads + hq] =
-            (log2f(total_l) + top_s[r] - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
+            (log2f(sum) + top - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
     }
-    __syncthreads();
   }
 }
 
@@ -695,6 +696,18 @@ namespace {
 // Rows of a unit: 8, 16 or 32 (16 at 128 dimensions, whose accumulators are twice as wide).
 int rows_per_tile(long long rows, int head_dim) { return rows <= 8 ? 8 : rows <= 16 || head_dim == 128 ? 16 : 32; }
 
+// The codes of K or V as rows of D bytes, read KT at a time with the swizzle as wide as a row.
+bool code_map(CUtensorMap* map, const void* codes, long long rows, int d, int kt) {
+  const auto fn = gemm::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d};
+  const cuuint32_t box[2] = {(cuuint32_t)d, (cuuint32_t)kt}, step[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int FMT, int D, int NG, int SPLIT, typename T>
 cudaError_t launch_t(const AttnParams& q, cudaStream_t st) {
   auto kernel = kv8_attn_kernel<FMT, D, NG, SPLIT, T>;
@@ -702,11 +715,16 @@ cudaError_t launch_t(const AttnParams& q, cudaStream_t st) {
   static_assert(sizeof(Smem<D, NG, SPLIT>) + (MAX_SEQS + 1) * 4 <= 227 * 1024, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<q.grid, Cfg<D, NG, SPLIT>::NT, smem, st>>>(q);
+  CUtensorMap maps[2];
+  const long long cache_rows = (long long)q.c.n_seqs * q.c.n_kv * q.c.max_ctx;
+  if (!code_map(&maps[0], q.c.k, cache_rows, D, Shape<D>::KT) || !code_map(&maps[1], q.c.v, cache_rows, D, Shape<D>::KT))
+    return cudaErrorNotSupported;
+  kernel<<<q.grid, Cfg<D, NG, SPLIT>::NT, smem, st>>>(maps[0], maps[1], q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units));
-  cfg.blockDim = dim3(MERGE_WARPS<D> * 32);
+  // few units: a CTA for each row, so that long rows are joined side by side
+  cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units), q.c.n_seqs * q.units <= 64 ? 8 * NG : 1);
+  cfg.blockDim = dim3(MERGE_WARPS * 32);
   cfg.dynamicSmemBytes = list;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -782,6 +800,8 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   const int kt = 4096 / cache->head_dim;
   // the list of tiles is counted in 32 bits
   if (units * cache->n_seqs > (1LL << 30) / ((cache->max_ctx + kt - 1) / kt)) return TINFER_ERR_UNSUPPORTED;
+  // and so are the rows of the cache (their coordinates in the copies)
+  if ((long long)cache->n_seqs * cache->n_kv_heads * cache->max_ctx > 0x7FFFFFFFLL) return TINFER_ERR_UNSUPPORTED;
   q.row_tiles = (int)row_tiles;
   q.units = (int)units;
   q.sp = kv8::Span{pos_dev, counts_dev, n_tokens, status_dev};
