@@ -61,48 +61,65 @@ struct Shape {
 };
 
 // ---- the list of work -------------------------------------------------------------------------
-// Sequence s holds ceil(len / KT) tiles for each of its units (KV head, row tile). prefix[s] counts the
-// tiles before it. Called by all threads of a CTA; returns the total.
+// Sequence s has units (KV head, row tile); each is FIXED empty places, which stand for what a unit costs beside its
+// tiles (its queries, its end), and ceil(len / KT) tiles. prefix[s] counts the places before it. Called by
+// all threads of a CTA; returns the total.
+constexpr int FIXED = 1;
+
+template <int D>
+__device__ __forceinline__ int places_of(const AttnParams& q, int s) {
+  int pos, count;
+  if (!span_of(q.sp, s, q.c.max_ctx, pos, count) && blockIdx.x == 0 && q.sp.status) atomicOr(q.sp.status, STATUS_BAD_POS);
+  return count > 0 ? ((pos + count + Shape<D>::KT - 1) / Shape<D>::KT + FIXED) * q.units : 0;
+}
+
 template <int D, int NT>
 __device__ int build_prefix(const AttnParams& q, int* prefix, int* scan) {
-  constexpr int KT = Shape<D>::KT;
-  int carry = 0;
-  for (int base = 0; base < q.c.n_seqs; base += NT) {
-    const int s = base + threadIdx.x;
-    int tiles = 0;
-    if (s < q.c.n_seqs) {
-      int pos, count;
-      if (!span_of(q.sp, s, q.c.max_ctx, pos, count) && blockIdx.x == 0 && q.sp.status)
-        atomicOr(q.sp.status, STATUS_BAD_POS);
-      if (count > 0) tiles = (pos + count + KT - 1) / KT * q.units;
-    }
-    int incl = tiles;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = q.c.n_seqs;
+  if (n <= 32) {  // every warp for itself: all write the same words, and no barrier stands before the first copy
+    const int mine = lane < n ? places_of<D>(q, lane) : 0;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int y = __shfl_up_sync(~0u, incl, o);
-      if ((threadIdx.x & 31) >= o) incl += y;
+      if (lane >= o) incl += y;
     }
-    if ((threadIdx.x & 31) == 31) scan[threadIdx.x >> 5] = incl;
+    const int total = __shfl_sync(~0u, incl, 31);
+    if (lane < n) prefix[lane] = incl - mine;
+    if (lane == 0) prefix[n] = total;
+    __syncwarp();
+    return total;
+  }
+  int carry = 0;
+  for (int base = 0; base < n; base += NT) {
+    const int s = base + threadIdx.x;
+    const int mine = s < n ? places_of<D>(q, s) : 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int y = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) scan[warp] = incl;
     __syncthreads();
     int before = carry;
     for (int w = 0; w < NT / 32; ++w) {
       const int y = scan[w];
-      if (w < (int)(threadIdx.x >> 5)) before += y;
+      if (w < warp) before += y;
       carry += y;
     }
-    if (s < q.c.n_seqs) prefix[s] = before + incl - tiles;
+    if (s < n) prefix[s] = before + incl - mine;
     __syncthreads();
   }
-  if (threadIdx.x == 0) prefix[q.c.n_seqs] = carry;
+  if (threadIdx.x == 0) prefix[n] = carry;
   __syncthreads();
   return carry;
 }
 
-__device__ __forceinline__ int tiles_per_cta(const AttnParams& q, int total, int grid) {
-  return max((total + grid - 1) / grid, q.min_tiles);
-}
+// The list is dealt out in equal runs of places to the warps of all CTAs, neighbouring runs to the warps of one CTA.
+__device__ __forceinline__ int places_per_warp(int total, int warps) { return (total + warps - 1) / warps; }
 
-// The sequence that holds tile x of the list.
+// The sequence that holds place x of the list.
 __device__ __forceinline__ int seq_of(const int* prefix, int n, int x) {
   int lo = 0, hi = n;  // prefix[lo] <= x < prefix[hi]
   while (hi - lo > 1) {
@@ -116,30 +133,26 @@ __device__ __forceinline__ int seq_of(const int* prefix, int n, int x) {
 // A place in the list, with what the tiles of its unit share.
 template <int D, int ROWS>
 struct Place {
-  int x, seq, unit, tile, tiles;  // tiles: of one unit of this sequence
+  int x, seq, unit, tile, tiles;  // tile < 0: an empty place; tiles: of one unit of this sequence
   int limit;                      // keys that some row of the unit sees
   int row0;                       // the KV head's first row among all rows of the cache
-  __device__ void enter(const AttnParams& q) {
-    const int pos = q.sp.pos[seq], count = q.sp.counts ? q.sp.counts[seq] : q.sp.n_tokens;
-    const int head = unit / q.row_tiles, rt = unit - head * q.row_tiles;
-    row0 = (seq * q.c.n_kv + head) * q.c.max_ctx;
-    limit = rt * ROWS >= q.group * count ? 0 : pos + min((rt * ROWS + ROWS - 1) / q.group, count - 1) + 1;
-  }
   __device__ void seek(const AttnParams& q, const int* prefix, int at) {
     x = at;
     limit = tile = 0;
     if (at >= prefix[q.c.n_seqs]) return;
     seq = seq_of(prefix, q.c.n_seqs, at);
-    tiles = (prefix[seq + 1] - prefix[seq]) / q.units;
-    const int in = at - prefix[seq];
-    unit = in / tiles;
-    tile = in - unit * tiles;
-    enter(q);
+    const int places = (prefix[seq + 1] - prefix[seq]) / q.units, in = at - prefix[seq];
+    tiles = places - FIXED;
+    unit = in / places;
+    tile = in - unit * places - FIXED;
+    const int pos = q.sp.pos[seq], count = q.sp.counts ? q.sp.counts[seq] : q.sp.n_tokens;
+    const int head = unit / q.row_tiles, rt = unit - head * q.row_tiles;
+    row0 = (seq * q.c.n_kv + head) * q.c.max_ctx;
+    limit = rt * ROWS >= q.group * count ? 0 : pos + min((rt * ROWS + ROWS - 1) / q.group, count - 1) + 1;
   }
-  __device__ void advance(const AttnParams& q, const int* prefix, int by, int end) {
-    x += by;
-    tile += by;
-    if (tile >= tiles && x < end) seek(q, prefix, x);
+  __device__ void next(const AttnParams& q, const int* prefix, int end) {
+    ++x;
+    if (++tile >= tiles && x < end) seek(q, prefix, x);
   }
 };
 
@@ -205,23 +218,40 @@ struct Cfg {
   static constexpr int ROWS = 8 * NG;
 };
 
+// A part of a unit that a warp leaves to be joined: the unit, by its first place in the list (-1: none), its
+// tiles, and whether it holds the unit's first and last.
+struct Part {
+  int unit, first, last, pad;
+};
+
 template <int D, int NG, int SPLIT>
 struct Smem {
   using C = Cfg<D, NG, SPLIT>;
   static constexpr int SCALES = Shape<D>::KT / 16;  // scales of one tile, at most (blocks of 16)
+  static_assert(C::ROWS * D * 4 <= Shape<D>::STAGE_BYTES, "a warp's outputs fit its first ring slot");
   alignas(1024) uint8_t ring[C::NW][C::STAGES][Shape<D>::STAGE_BYTES];
+  alignas(16) __half q[C::NW][8][D + 8];  // eight query rows on their way to the products' operands
+  int4 slot[C::NW][C::STAGES];            // of a tile in the ring: place in the list, first key, keys
+  Part tail[C::NW], head[C::NW];          // a warp's last part (outputs in its ring) and its first (in the workspace)
+  float m[2][C::NW][C::ROWS], l[2][C::NW][C::ROWS];  // of the tails and of the heads
   float ring_scale[C::NW][C::STAGES][2][SCALES];
-  union alignas(16) {
-    float part[C::NW][8][64 + 4];               // one pass of the merge of the warps: 8 rows x 64 dimensions
-    uint32_t qf[SPLIT][NG][D / 16][32][2];      // query fragments: high and remainder; read before the merge
-  } u;
-  int4 slot[C::NW][C::STAGES];  // of a tile in the ring: place in the list, first key, keys
-  float m[C::NW][C::ROWS], l[C::NW][C::ROWS];
-  float row_scale[C::ROWS];
   alignas(8) unsigned long long full[C::NW][C::STAGES];
   int scan[C::NW];
   int failed;
 };
+
+// A thread's outputs as rows of D floats: DB dimensions from g DB on of rows 2t and 2t + 1 of each group.
+template <int D, int NG>
+__device__ __forceinline__ void store_part(float* rows, const float (&o)[D / 16][NG][4], int g, int t) {
+#pragma unroll
+  for (int n = 0; n < NG; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < D / 8; j += 4)
+        *reinterpret_cast<float4*>(rows + (n * 8 + 2 * t + h) * D + g * (D / 8) + j) =
+            make_float4(o[j / 2][n][h], o[j / 2][n][2 + h], o[j / 2 + 1][n][h], o[j / 2 + 1][n][2 + h]);
+}
 
 template <int FMT, int D, int NG, int SPLIT, typename T>
 __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(const __grid_constant__ CUtensorMap map_k,
@@ -239,17 +269,17 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   if (tid == 0) sm.failed = 0;
   mbar_fence_init();
   const int total = build_prefix<D, C::NT>(q, prefix, sm.scan);
-  const int per = tiles_per_cta(q, total, gridDim.x);
-  const int lo = (int)min((long long)per * blockIdx.x, (long long)total), hi = min(lo + per, total);
-  if (lo >= hi) return;
+  const int per = places_per_warp(total, gridDim.x * NW), run = blockIdx.x * NW + warp;
+  if ((long long)per * NW * blockIdx.x >= total) return;
+  const int lo = (int)min((long long)per * run, (long long)total), hi = min(lo + per, total);
 
-  // this warp's tiles: every NW-th of [lo, hi), across the units' boundaries
+  // this warp's tiles, across the units' boundaries
   Place<D, ROWS> in;
-  in.seek(q, prefix, lo + warp);
+  in.seek(q, prefix, lo);
   int put = 0, got = 0;
   const uint64_t policy = q.keep_l2 ? policy_evict_normal() : policy_evict_first();
   auto issue = [&]() {  // the next tile that has keys to read goes into the ring
-    while (in.x < hi && in.tile * KT >= in.limit) in.advance(q, prefix, NW, hi);
+    while (in.x < hi && (in.tile < 0 || in.tile * KT >= in.limit)) in.next(q, prefix, hi);
     if (in.x >= hi) return;
     const int st = put % STAGES, key0 = in.tile * KT, keys = min(in.limit - key0, KT);
     const uint32_t bar = smem_addr(&sm.full[warp][st]);
@@ -268,91 +298,97 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
     }
     cp_async_arrive(bar);
     ++put;
-    in.advance(q, prefix, NW, hi);
+    in.next(q, prefix, hi);
   };
   __syncwarp();
 #pragma unroll 1
   for (int s = 0; s < STAGES; ++s) issue();
   __syncwarp();
 
-  Place<D, ROWS> seg;  // the unit that the CTA works on
+  Part tail{-1, 0, 0, 0}, front{-1, 0, 0, 0};
+  float o[MD][NG][4], mx[NG][2], l[NG][2];
+  Place<D, ROWS> seg;  // the unit that the warp works on
   seg.seek(q, prefix, lo);
   while (seg.x < hi) {
+    if (seg.tile < 0) {  // past the empty places
+      seg.x -= seg.tile;
+      seg.tile = 0;
+      if (seg.x >= hi) break;
+    }
     const int seg_end = min(hi, seg.x + seg.tiles - seg.tile);
-    const bool whole = seg.tile == 0 && seg_end - seg.x == seg.tiles;
-    const int head = seg.unit / q.row_tiles, rt = seg.unit % q.row_tiles;
+    const int head = seg.unit / q.row_tiles, rt = seg.unit - head * q.row_tiles;
     const int pos = q.sp.pos[seg.seq], count = q.sp.counts ? q.sp.counts[seg.seq] : q.sp.n_tokens;
     const int rows = min(q.group * count - rt * ROWS, ROWS);  // rows of this unit (may be <= 0)
 
-    // query rows: rotated, divided by a power of two, laid out as the scores' right operands. Warp w takes
-    // rows w, w + NW, ...; a lane the rotary pairs of dimensions lane (and lane + 32).
-    for (int r = warp; r < ROWS; r += NW) {
-      float v[D / 32];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) v[i] = 0.f;
-      if (r < rows) {
-        const int row = rt * ROWS + r, tok = row / q.group, hq = head * q.group + row % q.group;
-        const T* p = static_cast<const T*>(q.q.data) + seg.seq * q.q.ss + tok * q.q.ts + hq * q.q.hs;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const int e = lane + 32 * i;
-          float a = (float)p[e], z = (float)p[e + D / 2];
-          if (q.rope.on) {
-            float cs, sn;
-            rope_cos_sin(q.rope.f[e], pos + tok, cs, sn);
-            const float a2 = a * cs - z * sn;
-            z = z * cs + a * sn;
-            a = a2;
-          }
-          v[i] = a;
-          v[D / 64 + i] = z;
-        }
-      }
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) top = fmaxf(top, fabsf(v[i]));
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-      const int e2 = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 100) : 0;  // top < 2^e2
-      const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-      if (lane == 0) sm.row_scale[r] = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        // dimension e belongs to thread e / (D/4) of the quad, product step (e % (D/4)) / 4, word b0 or b1,
-        // low or high half
-        const int e = (i < D / 64 ? lane + 32 * i : D / 2 + lane + 32 * (i - D / 64));
-        const int qt = e / (D / 4), in4 = e % (D / 4);
-        const float y = v[i] * down;
-        const __half h = __float2half_rn(y);
-        reinterpret_cast<__half*>(&sm.u.qf[0][r / 8][in4 / 4][(r & 7) * 4 + qt][(in4 >> 1) & 1])[in4 & 1] = h;
-        if (SPLIT == 2)
-          reinterpret_cast<__half*>(&sm.u.qf[SPLIT - 1][r / 8][in4 / 4][(r & 7) * 4 + qt][(in4 >> 1) & 1])[in4 & 1] =
-              __float2half_rn(y - __half2float(h));
-      }
-    }
-    __syncthreads();
+    // query rows: rotated, divided by a power of two, laid out as the scores' right operands, eight at a
+    // time. A lane holds the rotary pairs of dimensions lane (and lane + 32) of every row; a thread's operands are
+    // dimensions t D/4 .. of row g, four for each product.
     uint32_t qf[SPLIT][NG][MD][2];
     float rs[NG][2];
     int limit[NG][2];  // first key that a row does not see
+    int angle_of = -1;
+    float cs[D / 64], sn[D / 64];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
+      float v[8][D / 32];
 #pragma unroll
-      for (int h = 0; h < SPLIT; ++h)
+      for (int r = 0; r < 8; ++r) {
+        const bool there = n * 8 + r < rows;
+        const int row = rt * ROWS + n * 8 + r, tok = row / q.group;
+        const T* p = static_cast<const T*>(q.q.data) + seg.seq * q.q.ss + tok * q.q.ts +
+                     (head * q.group + row - tok * q.group) * q.q.hs + lane;
 #pragma unroll
-        for (int k = 0; k < MD; ++k) {
-          const uint2 w = *reinterpret_cast<const uint2*>(sm.u.qf[h][n][k][lane]);
-          qf[h][n][k][0] = w.x;
-          qf[h][n][k][1] = w.y;
+        for (int i = 0; i < D / 32; ++i) v[r][i] = there ? (float)p[32 * i] : 0.f;
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const int tok = (rt * ROWS + n * 8 + r) / q.group;
+        if (q.rope.on) {
+          if (tok != angle_of) {
+            angle_of = tok;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) rope_cos_sin(q.rope.f[lane + 32 * i], pos + tok, cs[i], sn[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            const float a = v[r][i], z = v[r][D / 64 + i];
+            v[r][i] = a * cs[i] - z * sn[i];
+            v[r][D / 64 + i] = z * cs[i] + a * sn[i];
+          }
         }
+        unsigned top = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = n * 8 + 2 * t + h;
-        rs[n][h] = sm.row_scale[r];
-        limit[n][h] = pos + min((rt * ROWS + r) / q.group, count - 1) + 1;
+        for (int i = 0; i < D / 32; ++i) top = max(top, __float_as_uint(v[r][i]) & 0x7FFFFFFFu);
+        top = __reduce_max_sync(~0u, top);
+        const int e2 = top ? min(max((int)(top >> 23) - 126, -100), 100) : 0;  // every magnitude below 2^e2
+        const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+        if (r == 2 * t) rs[n][0] = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
+        if (r == 2 * t + 1) rs[n][1] = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) v[r][i] *= down;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) limit[n][h] = pos + min((rt * ROWS + n * 8 + 2 * t + h) / q.group, count - 1) + 1;
+#pragma unroll
+      for (int sp = 0; sp < SPLIT; ++sp) {
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const __half h = __float2half_rn(v[r][i]);
+            sm.q[warp][r][lane + 32 * i] = h;
+            v[r][i] -= __half2float(h);
+          }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < MD; k += 2) {
+          const uint4 w = *reinterpret_cast<const uint4*>(&sm.q[warp][g][t * (D / 4) + 4 * k]);
+          qf[sp][n][k][0] = w.x; qf[sp][n][k][1] = w.y; qf[sp][n][k + 1][0] = w.z; qf[sp][n][k + 1][1] = w.w;
+        }
       }
     }
     const int all_see = pos + min(rt * ROWS / q.group, count - 1) + 1;  // keys that every row sees
-    float o[MD][NG][4], mx[NG][2], l[NG][2];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -530,81 +566,118 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       __syncwarp();
     }
 
-    // ---- the warps' parts of this unit, joined in order of the warps
 #pragma unroll
     for (int n = 0; n < NG; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) l[n][h] += __shfl_xor_sync(~0u, l[n][h], x);
-        if (g == 0) {
-          sm.m[warp][n * 8 + 2 * t + h] = mx[n][h];
-          sm.l[warp][n * 8 + 2 * t + h] = l[n][h];
-        }
-      }
-    __syncthreads();
-    float* part = q.part + (size_t)(2 * blockIdx.x + (seg.tile == 0 ? 1 : 0)) * ROWS * (D + 2);
+    const Part mine{seg.x - seg.tile, seg.tile == 0, seg_end - seg.x + seg.tile == seg.tiles, 0};
+    if (mine.first && mine.last) {  // the whole unit: a thread holds DB dimensions of rows 2t and 2t + 1 of each group
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      if (8 * n >= rows) break;
-      float shrink[2];
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float top = -INFINITY;
+        for (int h = 0; h < 2; ++h) {
+          const int row = n * 8 + 2 * t + h;
+          if (row < rows) {
+            const int qrow = rt * ROWS + row, tok = qrow / q.group, hq = head * q.group + qrow - tok * q.group;
+            T* dst = static_cast<T*>(q.out.data) + seg.seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + g * DB;
+            const float inv = 1.f / l[n][h];
 #pragma unroll
-        for (int w = 0; w < NW; ++w) top = fmaxf(top, sm.m[w][n * 8 + 2 * t + h]);
-        shrink[h] = mx[n][h] == -INFINITY ? 0.f : exp2_fast(mx[n][h] - top);
-        if (l[n][h] != l[n][h]) shrink[h] = l[n][h];  // scores that are not finite
-      }
-#pragma unroll
-      for (int pass = 0; pass < D / 64; ++pass) {
-        if (g * DB / 64 == pass) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < DB; j += 4)  // dimension j of the thread's DB: o[j / 2], rows g (even) and g + 8 (odd)
-              *reinterpret_cast<float4*>(&sm.u.part[warp][2 * t + h][g * DB - 64 * pass + j]) =
-                  make_float4(o[j / 2][n][h] * shrink[h], o[j / 2][n][2 + h] * shrink[h], o[j / 2 + 1][n][h] * shrink[h],
-                              o[j / 2 + 1][n][2 + h] * shrink[h]);
-        }
-        __syncthreads();
-        const int r = tid >> 4, c = (tid & 15) * 4;  // 8 rows x 16 threads of four dimensions
-        const int row = n * 8 + r;
-        if (r < 8 && row < rows) {
-          float top = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int w = 0; w < NW; ++w) top = fmaxf(top, sm.m[w][row]);
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const float lw = sm.l[w][row];
-            if (lw != 0.f) {  // else this warp saw no key of the row
-              sum = fmaf(lw, exp2_fast(sm.m[w][row] - top), sum);
-              const float4 y = *reinterpret_cast<const float4*>(&sm.u.part[w][r][c]);
-              acc[0] += y.x; acc[1] += y.y; acc[2] += y.z; acc[3] += y.w;
+            for (int j = 0; j < DB; j += 4) {  // dimension j of the thread's DB: o[j / 2], rows g (even) and g + 8 (odd)
+              const float y[4] = {o[j / 2][n][h] * inv, o[j / 2][n][2 + h] * inv, o[j / 2 + 1][n][h] * inv,
+                                  o[j / 2 + 1][n][2 + h] * inv};
+              store4(dst + j, y);
             }
-          }
-          if (whole) {
-            const float inv = 1.f / sum;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] *= inv;
-            const int qrow = rt * ROWS + row, tok = qrow / q.group, hq = head * q.group + qrow % q.group;
-            T* dst = static_cast<T*>(q.out.data) + seg.seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + 64 * pass + c;
-            store4(dst, acc);
-            if (q.lse && pass == 0 && c == 0)
+            if (q.lse && g == 0)
               q.lse[((size_t)seg.seq * q.sp.n_tokens + tok) * q.n_heads + hq] =
-                  (log2f(sum) + top - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
-          } else {
-            *reinterpret_cast<float4*>(part + (size_t)row * D + 64 * pass + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            if (pass == 0 && c == 0) {
-              part[ROWS * D + row] = top;
-              part[ROWS * D + ROWS + row] = sum;
-            }
+                  (log2f(l[n][h]) + mx[n][h] - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
           }
         }
-        __syncthreads();
+    } else {
+      const int which = seg_end >= hi ? 0 : 1;  // the run's last unit stays in registers, its first goes to the workspace
+      if (g == 0)
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            sm.m[which][warp][n * 8 + 2 * t + h] = mx[n][h];
+            sm.l[which][warp][n * 8 + 2 * t + h] = l[n][h];
+          }
+      if (which == 0) {
+        tail = mine;
+      } else {
+        front = mine;
+        store_part<D, NG>(q.part + (size_t)(2 * gridDim.x + run) * ROWS * (D + 2), o, g, t);
       }
     }
-    seg.advance(q, prefix, seg_end - seg.x, hi);
+    seg.seek(q, prefix, seg_end);
+  }
+
+  // ---- the parts that the warps of this CTA left, joined in order of the warps. A unit's parts are the tails of
+  // neighbouring warps and perhaps the head of the next; all threads share the sums
+  if (lane == 0) {
+    sm.tail[warp] = tail;
+    sm.head[warp] = front;
+  }
+  if (tail.unit >= 0) store_part<D, NG>(reinterpret_cast<float*>(sm.ring[warp][0]), o, g, t);
+  __syncthreads();
+  constexpr int QUADS = D / 4;
+  for (int item = tid; item < (NW + 1) * ROWS * QUADS; item += C::NT) {
+    const int group = item / (ROWS * QUADS) - 1, row = item / QUADS % ROWS, c = item % QUADS * 4;
+    // group -1: the head of warp 0, begun by an earlier CTA; group w >= 0: the parts that begin with warp w's tail
+    int w0, w1;
+    Part p;
+    if (group < 0) {
+      p = sm.head[0];
+      w0 = w1 = 0;
+      if (p.unit < 0) continue;
+    } else {
+      p = sm.tail[group];
+      if (p.unit < 0 || (group > 0 && sm.tail[group - 1].unit == p.unit)) continue;
+      w0 = group;
+      w1 = group + 1;
+      while (w1 < NW && sm.tail[w1].unit == p.unit) ++w1;  // tails of warps w0 .. w1 - 1
+    }
+    const bool joins = group >= 0 && w1 < NW && sm.head[w1].unit == p.unit;  // and the head of warp w1
+    const bool last = group < 0 ? p.last : joins ? sm.head[w1].last : sm.tail[w1 - 1].last;
+    float top = -INFINITY;
+    for (int w = w0; w < w1; ++w) top = fmaxf(top, sm.m[0][w][row]);
+    const bool use_head = group < 0 || joins;
+    if (use_head) top = fmaxf(top, sm.m[1][w1][row]);
+    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](float lw, float mw, const float* y) {
+      if (lw == 0.f) return;  // no key of the row
+      const float f = exp2_fast(mw - top);
+      const float4 v = *reinterpret_cast<const float4*>(y + row * D + c);
+      sum = fmaf(lw, f, sum);
+      acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]); acc[2] = fmaf(v.z, f, acc[2]); acc[3] = fmaf(v.w, f, acc[3]);
+    };
+    for (int w = w0; w < w1; ++w) add(sm.l[0][w][row], sm.m[0][w][row], reinterpret_cast<const float*>(sm.ring[w][0]));
+    if (use_head)
+      add(sm.l[1][w1][row], sm.m[1][w1][row], q.part + (size_t)(2 * gridDim.x + blockIdx.x * NW + w1) * ROWS * (D + 2));
+    Place<D, ROWS> u;
+    u.seek(q, prefix, p.unit);
+    const int head = u.unit / q.row_tiles, rt = u.unit - head * q.row_tiles;
+    const int count = q.sp.counts ? q.sp.counts[u.seq] : q.sp.n_tokens;
+    const int qrow = rt * ROWS + row, tok = qrow / q.group, hq = head * q.group + qrow - tok * q.group;
+    if (qrow >= q.group * count) continue;
+    if (p.first && last) {
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] *= inv;
+      store4(static_cast<T*>(q.out.data) + u.seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + c, acc);
+      if (q.lse && c == 0)
+        q.lse[((size_t)u.seq * q.sp.n_tokens + tok) * q.n_heads + hq] =
+            (log2f(sum) + top - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
+    } else {  // more of the unit in other CTAs: slot 1 of the CTA that begins it, slot 0 of the others
+      float* part = q.part + (size_t)(2 * blockIdx.x + (p.first ? 1 : 0)) * ROWS * (D + 2);
+      *reinterpret_cast<float4*>(part + row * D + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (c == 0) {
+        part[ROWS * D + row] = top;
+        part[ROWS * D + ROWS + row] = sum;
+      }
+    }
   }
   if (tid == 0 && sm.failed && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
 }
@@ -623,12 +696,12 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) kv8_merge_kernel(const __gri
   __shared__ float sum_s[NW];
   // the list depends on the call's inputs alone, so it is built while the parts are still being made
   const int total = build_prefix<D, NW * 32>(q, prefix, scan);
-  const int per = tiles_per_cta(q, total, q.grid);
+  const int per = places_per_warp(total, q.grid * q.warps) * q.warps;  // of a CTA
   const int seq = blockIdx.x / q.units, unit = blockIdx.x % q.units;
   int pos, count;
   const bool ok = span_of(q.sp, seq, q.c.max_ctx, pos, count) && count > 0;
   const int tiles = (pos + count + KT - 1) / KT;
-  const int a = prefix[seq] + unit * tiles, c0 = a / per, parts = (a + tiles - 1) / per - c0 + 1;
+  const int a = prefix[seq] + unit * (tiles + FIXED) + FIXED, c0 = a / per, parts = (a + tiles - 1) / per - c0 + 1;
   const int head = unit / q.row_tiles, rt = unit % q.row_tiles;
   const int rows = min(q.group * count - rt * ROWS, ROWS);
   pdl_wait();  // the parts are complete
@@ -709,7 +782,8 @@ bool code_map(CUtensorMap* map, const void* codes, long long rows, int d, int kt
 }
 
 template <int FMT, int D, int NG, int SPLIT, typename T>
-cudaError_t launch_t(const AttnParams& q, cudaStream_t st) {
+cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
+  q.warps = Cfg<D, NG, SPLIT>::NW;
   auto kernel = kv8_attn_kernel<FMT, D, NG, SPLIT, T>;
   const size_t list = (size_t)(q.c.n_seqs + 1) * 4, smem = sizeof(Smem<D, NG, SPLIT>) + list;
   static_assert(sizeof(Smem<D, NG, SPLIT>) + (MAX_SEQS + 1) * 4 <= 227 * 1024, "shared memory of a CTA");
@@ -736,13 +810,13 @@ cudaError_t launch_t(const AttnParams& q, cudaStream_t st) {
 }
 
 template <int FMT, int D, int NG>
-cudaError_t launch_n(const AttnParams& q, int dtype, cudaStream_t st) {
+cudaError_t launch_n(AttnParams& q, int dtype, cudaStream_t st) {
   if (dtype == TINFER_DTYPE_F32) return launch_t<FMT, D, NG, 2, float>(q, st);
   if (dtype == TINFER_DTYPE_F16) return launch_t<FMT, D, NG, 2, __half>(q, st);
   return launch_t<FMT, D, NG, 1, __nv_bfloat16>(q, st);
 }
 template <int FMT>
-cudaError_t launch_f(const AttnParams& q, int head_dim, int rows, int dtype, cudaStream_t st) {
+cudaError_t launch_f(AttnParams& q, int head_dim, int rows, int dtype, cudaStream_t st) {
   if (head_dim == 128) return rows == 8 ? launch_n<FMT, 128, 1>(q, dtype, st) : launch_n<FMT, 128, 2>(q, dtype, st);
   return rows == 8    ? launch_n<FMT, 64, 1>(q, dtype, st)
          : rows == 16 ? launch_n<FMT, 64, 2>(q, dtype, st)
@@ -757,7 +831,7 @@ int device_sms(int& sms) {
 }
 
 // CTAs of the attention kernel, at most: the workspace is sized by this on every device alike.
-constexpr int MAX_GRID = 256;
+constexpr int MAX_GRID = 160;
 
 }  // namespace
 }  // namespace kv8
@@ -772,7 +846,8 @@ size_t tinfer_kv8_attention_workspace(const tinfer_kv8* cache, int n_heads, int 
   tinfer_status rc;
   if (!kv8::cache_of(cache, c, rc) || n_heads < 1 || n_heads % cache->n_kv_heads || n_tokens < 1) return 0;
   // one size for every number of rows, so that a program can keep one workspace for all its calls
-  return (size_t)kv8::MAX_GRID * 2 * kv8::rows_per_tile(1 << 20, cache->head_dim) * (cache->head_dim + 2) * 4;
+  // two parts of each CTA and one of each of its warps: 12 warps of 16 rows, or 8 of 32 at 64 dimensions
+  return (size_t)kv8::MAX_GRID * (cache->head_dim == 128 ? (2 + 12) * 16 : (2 + 8) * 32) * (cache->head_dim + 2) * 4;
 }
 
 tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int n_tokens, const tinfer_rows* q_rows,
@@ -799,7 +874,7 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   const long long row_tiles = (rows + per - 1) / per, units = row_tiles * cache->n_kv_heads;
   const int kt = 4096 / cache->head_dim;
   // the list of tiles is counted in 32 bits
-  if (units * cache->n_seqs > (1LL << 30) / ((cache->max_ctx + kt - 1) / kt)) return TINFER_ERR_UNSUPPORTED;
+  if (units * cache->n_seqs > (1LL << 30) / ((cache->max_ctx + kt - 1) / kt + kv8::FIXED)) return TINFER_ERR_UNSUPPORTED;
   // and so are the rows of the cache (their coordinates in the copies)
   if ((long long)cache->n_seqs * cache->n_kv_heads * cache->max_ctx > 0x7FFFFFFFLL) return TINFER_ERR_UNSUPPORTED;
   q.row_tiles = (int)row_tiles;
@@ -808,7 +883,6 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   q.lse = lse_dev;
   q.part = static_cast<float*>(workspace_dev);
   q.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->head_dim));
-  q.min_tiles = 1;
   q.keep_l2 = row_tiles > 1;
   int sms = 0;
   if (!kv8::device_sms(sms)) return TINFER_ERR_CUDA;

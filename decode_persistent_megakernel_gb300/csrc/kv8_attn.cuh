@@ -11,9 +11,9 @@ struct AttnParams {
   Span sp;
   Rope rope;
   float* lse;    // [n_seqs][n_tokens][n_heads], may be null
-  float* part;   // workspace: two parts per CTA, [rows][d] outputs, [rows] maxima, [rows] sums
+  float* part;   // workspace: two parts of each CTA, one of each warp; a part is [rows][d] outputs, [rows] maxima, [rows] sums
   int n_heads, group, row_tiles, units;  // units: KV heads x row tiles
-  int grid, min_tiles, keep_l2;
+  int grid, warps, keep_l2;  // warps of a CTA
   float scale_log2;  // log2(e) / sqrt(d)
 };
 
