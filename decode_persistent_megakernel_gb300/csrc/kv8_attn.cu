@@ -64,7 +64,7 @@ struct Shape {
 // Sequence s has units (KV head, row tile); each is FIXED empty places, which stand for what a unit costs beside its
 // tiles (its queries, its end), and ceil(len / KT) tiles. prefix[s] counts the places before it. Called by
 // all threads of a CTA; returns the total.
-constexpr int FIXED = 1;
+constexpr int FIXED = 4;
 
 template <int D>
 __device__ __forceinline__ int places_of(const AttnParams& q, int s) {
@@ -117,7 +117,14 @@ __device__ int build_prefix(const AttnParams& q, int* prefix, int* scan) {
 }
 
 // The list is dealt out in equal runs of places to the warps of all CTAs, neighbouring runs to the warps of one CTA.
-__device__ __forceinline__ int places_per_warp(int total, int warps) { return (total + warps - 1) / warps; }
+// Short lists use fewer warps of every CTA rather than fewer CTAs.
+struct Deal {
+  int warps, per;  // warps of a CTA, places of a warp
+};
+__device__ __forceinline__ Deal deal(int total, int grid, int max_warps) {
+  const int warps = min(max((total + grid - 1) / grid, 1), max_warps);
+  return Deal{warps, (total + grid * warps - 1) / (grid * warps)};
+}
 
 // The sequence that holds place x of the list.
 __device__ __forceinline__ int seq_of(const int* prefix, int n, int x) {
@@ -230,7 +237,7 @@ struct Smem {
   static constexpr int SCALES = Shape<D>::KT / 16;  // scales of one tile, at most (blocks of 16)
   static_assert(C::ROWS * D * 4 <= Shape<D>::STAGE_BYTES, "a warp's outputs fit its first ring slot");
   alignas(1024) uint8_t ring[C::NW][C::STAGES][Shape<D>::STAGE_BYTES];
-  alignas(16) __half q[C::NW][8][D + 8];  // eight query rows on their way to the products' operands
+  alignas(16) float2 angle[C::NW][D / 2];  // cosine and sine of one token's rotary pairs
   int4 slot[C::NW][C::STAGES];            // of a tile in the ring: place in the list, first key, keys
   Part tail[C::NW], head[C::NW];          // a warp's last part (outputs in its ring) and its first (in the workspace)
   float m[2][C::NW][C::ROWS], l[2][C::NW][C::ROWS];  // of the tails and of the heads
@@ -269,9 +276,10 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   if (tid == 0) sm.failed = 0;
   mbar_fence_init();
   const int total = build_prefix<D, C::NT>(q, prefix, sm.scan);
-  const int per = places_per_warp(total, gridDim.x * NW), run = blockIdx.x * NW + warp;
-  if ((long long)per * NW * blockIdx.x >= total) return;
-  const int lo = (int)min((long long)per * run, (long long)total), hi = min(lo + per, total);
+  const Deal share = deal(total, gridDim.x, NW);
+  if ((long long)share.per * share.warps * blockIdx.x >= total) return;
+  const int lo = warp < share.warps ? (int)min((long long)share.per * (blockIdx.x * share.warps + warp), (long long)total) : total;
+  const int hi = min(lo + share.per, total);
 
   // this warp's tiles, across the units' boundaries
   Place<D, ROWS> in;
@@ -321,71 +329,72 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
     const int rows = min(q.group * count - rt * ROWS, ROWS);  // rows of this unit (may be <= 0)
 
     // query rows: rotated, divided by a power of two, laid out as the scores' right operands, eight at a
-    // time. A lane holds the rotary pairs of dimensions lane (and lane + 32) of every row; a thread's operands are
-    // dimensions t D/4 .. of row g, four for each product.
+    // time. A thread's operands are dimensions t D/4 .. of row g, four for each product, so it loads just those
+    // and their rotary partners (which are thread t ^ 2's). The angles of a token are shared by its rows.
     uint32_t qf[SPLIT][NG][MD][2];
     float rs[NG][2];
     int limit[NG][2];  // first key that a row does not see
-    int angle_of = -1;
-    float cs[D / 64], sn[D / 64];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
-      float v[8][D / 32];
+      constexpr int E = D / 4;
+      const int row = rt * ROWS + n * 8 + g, tok = row / q.group;
+      const bool there = n * 8 + g < rows;
+      float v[E];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const bool there = n * 8 + r < rows;
-        const int row = rt * ROWS + n * 8 + r, tok = row / q.group;
-        const T* p = static_cast<const T*>(q.q.data) + seg.seq * q.q.ss + tok * q.q.ts +
-                     (head * q.group + row - tok * q.group) * q.q.hs + lane;
+      for (int i = 0; i < E; ++i) v[i] = 0.f;
+      const T* p = static_cast<const T*>(q.q.data) + seg.seq * q.q.ss + tok * q.q.ts + (head * q.group + row - tok * q.group) * q.q.hs;
+      if (there) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) v[r][i] = there ? (float)p[32 * i] : 0.f;
+        for (int i = 0; i < E; i += 8) load8(p + t * E + i, reinterpret_cast<float(&)[8]>(v[i]));
       }
+      if (q.rope.on && n * 8 < rows) {
+        float z[E];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int tok = (rt * ROWS + n * 8 + r) / q.group;
-        if (q.rope.on) {
-          if (tok != angle_of) {
-            angle_of = tok;
+        for (int i = 0; i < E; ++i) z[i] = 0.f;
+        if (there) {
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) rope_cos_sin(q.rope.f[lane + 32 * i], pos + tok, cs[i], sn[i]);
-          }
+          for (int i = 0; i < E; i += 8) load8(p + (t ^ 2) * E + i, reinterpret_cast<float(&)[8]>(z[i]));
+        }
+        const float sign = t < 2 ? -1.f : 1.f;
+        const int last_tok = (rt * ROWS + min(n * 8 + 7, rows - 1)) / q.group;
+        for (int x = (rt * ROWS + n * 8) / q.group; x <= last_tok; ++x) {
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
-            const float a = v[r][i], z = v[r][D / 64 + i];
-            v[r][i] = a * cs[i] - z * sn[i];
-            v[r][D / 64 + i] = z * cs[i] + a * sn[i];
+            float c, s;
+            rope_cos_sin(q.rope.f[lane + 32 * i], pos + x, c, s);
+            sm.angle[warp][lane + 32 * i] = make_float2(c, s);
+          }
+          __syncwarp();
+          if (tok == x) {
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+              const float4 cs = *reinterpret_cast<const float4*>(&sm.angle[warp][(t & 1) * E + i]);
+              v[i] = fmaf(z[i] * sign, cs.y, v[i] * cs.x);
+              v[i + 1] = fmaf(z[i + 1] * sign, cs.w, v[i + 1] * cs.z);
+            }
           }
         }
-        unsigned top = 0;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) top = max(top, __float_as_uint(v[r][i]) & 0x7FFFFFFFu);
-        top = __reduce_max_sync(~0u, top);
-        const int e2 = top ? min(max((int)(top >> 23) - 126, -100), 100) : 0;  // every magnitude below 2^e2
-        const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-        if (r == 2 * t) rs[n][0] = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
-        if (r == 2 * t + 1) rs[n][1] = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) v[r][i] *= down;
       }
+      unsigned top = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) limit[n][h] = pos + min((rt * ROWS + n * 8 + 2 * t + h) / q.group, count - 1) + 1;
+      for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      top = max(top, __shfl_xor_sync(~0u, top, 1));
+      top = max(top, __shfl_xor_sync(~0u, top, 2));
+      const int e2 = top ? min(max((int)(top >> 23) - 126, -100), 100) : 0;  // every magnitude below 2^e2
+      const float down = __uint_as_float((uint32_t)(127 - e2) << 23), up = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll
-      for (int sp = 0; sp < SPLIT; ++sp) {
-        __syncwarp();
+      for (int k = 0; k < MD; ++k)
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const __half h = __float2half_rn(v[r][i]);
-            sm.q[warp][r][lane + 32 * i] = h;
-            v[r][i] -= __half2float(h);
-          }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < MD; k += 2) {
-          const uint4 w = *reinterpret_cast<const uint4*>(&sm.q[warp][g][t * (D / 4) + 4 * k]);
-          qf[sp][n][k][0] = w.x; qf[sp][n][k][1] = w.y; qf[sp][n][k + 1][0] = w.z; qf[sp][n][k + 1][1] = w.w;
+        for (int h = 0; h < 2; ++h) {
+          const float a = v[4 * k + 2 * h] * down, b = v[4 * k + 2 * h + 1] * down;
+          qf[0][n][k][h] = pack_half(a, b);
+          if (SPLIT == 2) qf[SPLIT - 1][n][k][h] = pack_rest(a, b, qf[0][n][k][h]);
         }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        rs[n][h] = __shfl_sync(~0u, up, 8 * t + 4 * h);  // of rows 2t and 2t + 1
+        limit[n][h] = pos + min((rt * ROWS + n * 8 + 2 * t + h) / q.group, count - 1) + 1;
       }
     }
     const int all_see = pos + min(rt * ROWS / q.group, count - 1) + 1;  // keys that every row sees
@@ -608,7 +617,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
         tail = mine;
       } else {
         front = mine;
-        store_part<D, NG>(q.part + (size_t)(2 * gridDim.x + run) * ROWS * (D + 2), o, g, t);
+        store_part<D, NG>(q.part + (size_t)(2 * gridDim.x + blockIdx.x * NW + warp) * ROWS * (D + 2), o, g, t);
       }
     }
     seg.seek(q, prefix, seg_end);
@@ -696,7 +705,8 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) kv8_merge_kernel(const __gri
   __shared__ float sum_s[NW];
   // the list depends on the call's inputs alone, so it is built while the parts are still being made
   const int total = build_prefix<D, NW * 32>(q, prefix, scan);
-  const int per = places_per_warp(total, q.grid * q.warps) * q.warps;  // of a CTA
+  const Deal share = deal(total, q.grid, q.warps);
+  const int per = share.per * share.warps;  // of a CTA
   const int seq = blockIdx.x / q.units, unit = blockIdx.x % q.units;
   int pos, count;
   const bool ok = span_of(q.sp, seq, q.c.max_ctx, pos, count) && count > 0;
