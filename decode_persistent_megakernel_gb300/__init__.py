@@ -481,12 +481,12 @@ class Kv8Cache:
     buffers: (k_codes, v_codes, k_scales, v_scales) to use instead of new ones: uint8
     [n_seqs, n_kv_heads, max_ctx, head_dim] and float32 [n_seqs, n_kv_heads, ceil(max_ctx / block)], contiguous.
 
-    The cache keeps one workspace for the attention, large enough for every call. A call that may overlap another
-    one in time (another stream, a graph replayed beside it) passes a workspace of its own (a uint8 tensor of
-    workspace_bytes(n_heads, n_tokens))."""
+    The cache keeps one workspace for the attention, large enough for every call (workspace_bytes(): 22 or 43 MB at
+    head_dim 64 or 128): `workspace`, a uint8 tensor that the caches of several layers may share, or a new one. A call
+    that may overlap another one in time (another stream, a graph replayed beside it) passes one of its own."""
 
     def __init__(self, n_kv_heads: int, head_dim: int, max_ctx: int, n_seqs: int = 1, fmt: int = TINFER_KV8_E4M3,
-                 block: int = 64, device="cuda", buffers=None):
+                 block: int = 64, device="cuda", buffers=None, workspace=None):
         import torch
         codes = torch.Size((n_seqs, n_kv_heads, max_ctx, head_dim))
         scales = torch.Size((n_seqs, n_kv_heads, -(-max_ctx // max(1, block))))
@@ -509,7 +509,9 @@ class Kv8Cache:
         need = self.workspace_bytes(n_kv_heads, 1)
         if need == 0:
             raise TinferError(TINFER_ERR_UNSUPPORTED, "Kv8Cache")
-        self._workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        self._workspace = self._check_workspace(workspace)
 
     def _rows(self, what, t, heads=None, tokens=None) -> tinfer_rows:
         s = t.shape
@@ -562,8 +564,14 @@ class Kv8Cache:
                   (self.c, n_tokens, pos.data_ptr(), _ptr(counts), kr, vr), status, stream)
         return out
 
-    def workspace_bytes(self, n_heads: int, n_tokens: int) -> int:
-        return lib().tinfer_kv8_attention_workspace(self.c, n_heads, n_tokens)
+    def workspace_bytes(self, n_heads: int | None = None, n_tokens: int = 1) -> int:
+        return lib().tinfer_kv8_attention_workspace(self.c, n_heads or self.n_kv_heads, n_tokens)
+
+    def _check_workspace(self, t):
+        import torch
+        if t.dtype != torch.uint8 or t.device != self.device or not t.is_contiguous():
+            raise ValueError("workspace: a contiguous uint8 tensor on the cache's device is wanted")
+        return t
 
     def attention(self, q, pos, counts=None, rope_theta: float = 0.0, out=None, lse=None, workspace=None, status=None,
                   stream=None):
@@ -581,8 +589,8 @@ class Kv8Cache:
             raise ValueError("lse: a contiguous float32 tensor [n_seqs, n_tokens, n_heads] is wanted")
         if workspace is None:
             workspace = self._workspace
-        elif workspace.dtype != torch.uint8 or workspace.device != self.device or not workspace.is_contiguous():
-            raise ValueError("workspace: a contiguous uint8 tensor on the cache's device is wanted")
+        else:
+            self._check_workspace(workspace)
         self._run("tinfer_op_kv8_attention", lib().tinfer_op_kv8_attention,
                   (self.c, n_heads, n_tokens, qr, pos.data_ptr(), _ptr(counts), rope_theta, orow, _ptr(lse),
                    workspace.data_ptr(), workspace.numel()), status, stream)

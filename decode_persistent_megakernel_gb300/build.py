@@ -11,7 +11,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtinfer.so")
-SOURCES = ["mega_bf16.cu", "mega_int4.cu", "kernels.cu", "api.cu", "gemm.cu", "kv8.cu", "kv8_attn.cu",
+SOURCES = ["mega_bf16.cu", "mega_int4.cu", "kernels.cu", "api.cu", "gemm.cu", "kv8.cu", "kv8_attn.cu", "kv8_prefill.cu",
            "logprobs.cu"]
 HEADERS = ["engine.h", "kernels.h", "ptx.cuh", "step.cuh", "megakernel.cuh", "kv8.cuh", "kv8_attn.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -40,13 +40,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // gemm.cu
 }
 namespace kv8 {
 
-constexpr int WEIGHT_SHIFT = 14;    // weights are held times 2^14: fp16 keeps 11 bits of them down to 2^-28
-// Exponents of V scales that enter the running maximum. Of a row whose keys all have the smallest one the
-// sum of the softmax is 2^(WEIGHT_SHIFT - E_MIN) for each key: 2^24 keys stay below fp32's 2^128. A smaller
-// scale's remainder makes its weights smaller than 1, a scale of 0 makes them 0 and counts in the sum.
-constexpr int E_MIN = -85, E_MAX = 120;
-constexpr long long WAIT_NS = 200LL * 1000 * 1000;
-
 // Byte of 16-byte chunk c of a row in its tile as the copies' swizzle leaves it: 128-byte rows exchange chunks
 // by the row's number modulo 8, 64-byte rows by half of it modulo 4.
 template <int D>
@@ -126,17 +119,6 @@ __device__ __forceinline__ Deal deal(int total, int grid, int max_warps) {
   return Deal{warps, (total + grid * warps - 1) / (grid * warps)};
 }
 
-// The sequence that holds place x of the list.
-__device__ __forceinline__ int seq_of(const int* prefix, int n, int x) {
-  int lo = 0, hi = n;  // prefix[lo] <= x < prefix[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (prefix[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 // A place in the list, with what the tiles of its unit share.
 template <int D, int ROWS>
 struct Place {
@@ -170,15 +152,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 // The remainder of a pair after its rounding to fp16, again in fp16.
 __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t high) {
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&high));
@@ -203,17 +176,6 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const float* src) {
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void fence_proxy_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity))
-    if ((long long)(globaltimer() - t0) > WAIT_NS) return false;
-  return true;
-}
-
 // ---- the kernel ----------------------------------------------------------------------------------
 // A CTA's shape: NG groups of 8 query rows, NW warps, STAGES slots of 8 KiB in each warp's ring. Two groups
 // (one at 128 dimensions with two-part operands) leave registers for 12 warps; beyond that 8.
@@ -231,6 +193,12 @@ struct Part {
   int unit, first, last, pad;
 };
 
+// The parts of one unit within a CTA: tails of warps w0 .. w1 - 1 and the head of head_warp (-1: none); rows counts
+// the KV head's query rows, row0 the unit's first; ends: 2 if the first tile is among the parts, + 1 if the last is.
+struct Group {
+  int seq, head, row0, rows, w0, w1, head_warp, ends;
+};
+
 template <int D, int NG, int SPLIT>
 struct Smem {
   using C = Cfg<D, NG, SPLIT>;
@@ -240,6 +208,7 @@ struct Smem {
   alignas(16) float2 angle[C::NW][D / 2];  // cosine and sine of one token's rotary pairs
   int4 slot[C::NW][C::STAGES];            // of a tile in the ring: place in the list, first key, keys
   Part tail[C::NW], head[C::NW];          // a warp's last part (outputs in its ring) and its first (in the workspace)
+  Group group[C::NW + 1];
   float m[2][C::NW][C::ROWS], l[2][C::NW][C::ROWS];  // of the tails and of the heads
   float ring_scale[C::NW][C::STAGES][2][SCALES];
   alignas(8) unsigned long long full[C::NW][C::STAGES];
@@ -631,29 +600,34 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   }
   if (tail.unit >= 0) store_part<D, NG>(reinterpret_cast<float*>(sm.ring[warp][0]), o, g, t);
   __syncthreads();
+  // group 0: the head of warp 0, begun by an earlier CTA; group 1 + w: the parts that begin with warp w's tail
+  if (tid <= NW) {
+    Group u{-1, 0, 0, 0, 0, 0, 0, 0};
+    const Part p = tid ? sm.tail[tid - 1] : sm.head[0];
+    if (p.unit >= 0 && !(tid > 1 && sm.tail[tid - 2].unit == p.unit)) {
+      int w0 = max(tid - 1, 0), w1 = tid;
+      while (tid && w1 < NW && sm.tail[w1].unit == p.unit) ++w1;  // tails of warps w0 .. w1 - 1 (group 0: none)
+      const bool joins = !tid || (w1 < NW && sm.head[w1].unit == p.unit);  // and the head of warp w1
+      const int last = joins ? sm.head[w1].last : sm.tail[w1 - 1].last;
+      Place<D, ROWS> at;
+      at.seek(q, prefix, p.unit);
+      const int head = at.unit / q.row_tiles;
+      u = Group{at.seq, head, (at.unit - head * q.row_tiles) * ROWS, q.group * (q.sp.counts ? q.sp.counts[at.seq] : q.sp.n_tokens),
+                w0, w1, joins ? w1 : -1, 2 * (p.first != 0) + (last != 0)};
+    }
+    sm.group[tid] = u;
+  }
+  __syncthreads();
   constexpr int QUADS = D / 4;
   for (int item = tid; item < (NW + 1) * ROWS * QUADS; item += C::NT) {
-    const int group = item / (ROWS * QUADS) - 1, row = item / QUADS % ROWS, c = item % QUADS * 4;
-    // group -1: the head of warp 0, begun by an earlier CTA; group w >= 0: the parts that begin with warp w's tail
-    int w0, w1;
-    Part p;
-    if (group < 0) {
-      p = sm.head[0];
-      w0 = w1 = 0;
-      if (p.unit < 0) continue;
-    } else {
-      p = sm.tail[group];
-      if (p.unit < 0 || (group > 0 && sm.tail[group - 1].unit == p.unit)) continue;
-      w0 = group;
-      w1 = group + 1;
-      while (w1 < NW && sm.tail[w1].unit == p.unit) ++w1;  // tails of warps w0 .. w1 - 1
-    }
-    const bool joins = group >= 0 && w1 < NW && sm.head[w1].unit == p.unit;  // and the head of warp w1
-    const bool last = group < 0 ? p.last : joins ? sm.head[w1].last : sm.tail[w1 - 1].last;
+    const Group u = sm.group[item / (ROWS * QUADS)];
+    const int row = item / QUADS % ROWS, c = item % QUADS * 4, qrow = u.row0 + row;
+    if (u.seq < 0 || qrow >= u.rows) continue;
+    const int w0 = u.w0, w1 = u.w1;
+    const bool use_head = u.head_warp >= 0, first = u.ends & 2, last = u.ends & 1;
     float top = -INFINITY;
     for (int w = w0; w < w1; ++w) top = fmaxf(top, sm.m[0][w][row]);
-    const bool use_head = group < 0 || joins;
-    if (use_head) top = fmaxf(top, sm.m[1][w1][row]);
+    if (use_head) top = fmaxf(top, sm.m[1][u.head_warp][row]);
     float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     auto add = [&](float lw, float mw, const float* y) {
       if (lw == 0.f) return;  // no key of the row
@@ -664,14 +638,10 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
     };
     for (int w = w0; w < w1; ++w) add(sm.l[0][w][row], sm.m[0][w][row], reinterpret_cast<const float*>(sm.ring[w][0]));
     if (use_head)
-      add(sm.l[1][w1][row], sm.m[1][w1][row], q.part + (size_t)(2 * gridDim.x + blockIdx.x * NW + w1) * ROWS * (D + 2));
-    Place<D, ROWS> u;
-    u.seek(q, prefix, p.unit);
-    const int head = u.unit / q.row_tiles, rt = u.unit - head * q.row_tiles;
-    const int count = q.sp.counts ? q.sp.counts[u.seq] : q.sp.n_tokens;
-    const int qrow = rt * ROWS + row, tok = qrow / q.group, hq = head * q.group + qrow - tok * q.group;
-    if (qrow >= q.group * count) continue;
-    if (p.first && last) {
+      add(sm.l[1][u.head_warp][row], sm.m[1][u.head_warp][row],
+          q.part + (size_t)(2 * gridDim.x + blockIdx.x * NW + u.head_warp) * ROWS * (D + 2));
+    const int tok = qrow / q.group, hq = u.head * q.group + qrow - tok * q.group;
+    if (first && last) {
       const float inv = 1.f / sum;
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] *= inv;
@@ -680,7 +650,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
         q.lse[((size_t)u.seq * q.sp.n_tokens + tok) * q.n_heads + hq] =
             (log2f(sum) + top - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
     } else {  // more of the unit in other CTAs: slot 1 of the CTA that begins it, slot 0 of the others
-      float* part = q.part + (size_t)(2 * blockIdx.x + (p.first ? 1 : 0)) * ROWS * (D + 2);
+      float* part = q.part + (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * ROWS * (D + 2);
       *reinterpret_cast<float4*>(part + row * D + c) = make_float4(acc[0], acc[1], acc[2], acc[3]);
       if (c == 0) {
         part[ROWS * D + row] = top;
@@ -691,20 +661,14 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   if (tid == 0 && sm.failed && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
 }
 
-// Joins the parts of one unit that several CTAs hold: CTA (unit of a sequence, slice of its rows). A row with
-// few parts is one warp's work; the parts of a long one are dealt out to all warps and meet in shared
-// memory. Either way they add up in a fixed order.
-constexpr int MERGE_WARPS = 8;
-
+// Joins the units that several CTAs hold: CTA (unit of a sequence, slice of its rows).
 template <int D, int NG, typename T>
-__global__ void __launch_bounds__(MERGE_WARPS * 32) kv8_merge_kernel(const __grid_constant__ AttnParams q) {
-  constexpr int KT = Shape<D>::KT, ROWS = 8 * NG, N = D / 32, NW = MERGE_WARPS;
+__global__ void __launch_bounds__(JOIN_WARPS * 32) kv8_merge_kernel(const __grid_constant__ AttnParams q) {
+  constexpr int KT = Shape<D>::KT, ROWS = 8 * NG;
   extern __shared__ int prefix[];
-  __shared__ int scan[NW];
-  __shared__ alignas(16) float acc_s[NW][D];
-  __shared__ float sum_s[NW];
+  __shared__ int scan[JOIN_WARPS];
   // the list depends on the call's inputs alone, so it is built while the parts are still being made
-  const int total = build_prefix<D, NW * 32>(q, prefix, scan);
+  const int total = build_prefix<D, JOIN_WARPS * 32>(q, prefix, scan);
   const Deal share = deal(total, q.grid, q.warps);
   const int per = share.per * share.warps;  // of a CTA
   const int seq = blockIdx.x / q.units, unit = blockIdx.x % q.units;
@@ -713,71 +677,12 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) kv8_merge_kernel(const __gri
   const int tiles = (pos + count + KT - 1) / KT;
   const int a = prefix[seq] + unit * (tiles + FIXED) + FIXED, c0 = a / per, parts = (a + tiles - 1) / per - c0 + 1;
   const int head = unit / q.row_tiles, rt = unit % q.row_tiles;
-  const int rows = min(q.group * count - rt * ROWS, ROWS);
   pdl_wait();  // the parts are complete
   if (!ok || parts <= 1) return;  // one CTA had it whole
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool few = parts <= NW;
-  auto part = [&](int c) { return q.part + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * ROWS * (D + 2); };
-  const int row_step = few ? NW * gridDim.y : gridDim.y;
-  for (int row = few ? blockIdx.y * NW + warp : blockIdx.y; row < rows; row += row_step) {
-    float top = -INFINITY;
-    for (int c = lane; c < parts; c += 32) top = fmaxf(top, part(c)[ROWS * D + row]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    float sum = 0.f, y[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = 0.f;
-#pragma unroll 8
-    for (int c = few ? 0 : warp; c < parts; c += few ? 1 : NW) {
-      const float* p = part(c);
-      const float lc = p[ROWS * D + ROWS + row], mc = p[ROWS * D + row];
-      float f[N];
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(p + (size_t)row * D + lane * N + i);
-        f[i] = v.x;
-        f[i + 1] = v.y;
-      }
-      const float w = lc == 0.f ? 0.f : exp2_fast(mc - top);
-      sum = fmaf(lc, w, sum);
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = fmaf(f[i], w, y[i]);
-    }
-    if (!few) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) acc_s[warp][lane * N + i] = y[i];
-      if (lane == 0) sum_s[warp] = sum;
-      __syncthreads();
-      sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        sum += sum_s[w];
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] += acc_s[w][lane * N + i];
-      }
-      __syncthreads();
-    }
-    if (few || warp == 0) {
-      const float inv = 1.f / sum;
-      const int qrow = rt * ROWS + row, tok = qrow / q.group, hq = head * q.group + qrow % q.group;
-      T* dst = static_cast<T*>(q.out.data) + seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + lane * N;
-#pragma unroll
-      for (int i = 0; i < N; ++i) store_one(dst + i, y[i] * inv);
-      if (q.lse && lane == 0)
-        q.lse[((size_t)seq * q.sp.n_tokens + tok) * q.n_heads + hq] =
-            (log2f(sum) + top - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
-    }
-  }
+  join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * count - rt * ROWS, ROWS), c0, parts, WEIGHT_SHIFT);
 }
 
 // ---------------------------------------------------------------------------------------- host
-namespace {
-
-// Rows of a unit: 8, 16 or 32 (16 at 128 dimensions, whose accumulators are twice as wide).
-int rows_per_tile(long long rows, int head_dim) { return rows <= 8 ? 8 : rows <= 16 || head_dim == 128 ? 16 : 32; }
 
 // The codes of K or V as rows of D bytes, read KT at a time with the swizzle as wide as a row.
 bool code_map(CUtensorMap* map, const void* codes, long long rows, int d, int kt) {
@@ -790,6 +695,11 @@ bool code_map(CUtensorMap* map, const void* codes, long long rows, int d, int kt
             CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
+
+// Rows of a unit: 8, 16 or 32 (16 at 128 dimensions, whose accumulators are twice as wide).
+int rows_per_tile(long long rows, int head_dim) { return rows <= 8 ? 8 : rows <= 16 || head_dim == 128 ? 16 : 32; }
 
 template <int FMT, int D, int NG, int SPLIT, typename T>
 cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
@@ -808,7 +718,7 @@ cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   // few units: a CTA for each row, so that long rows are joined side by side
   cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units), q.c.n_seqs * q.units <= 64 ? 8 * NG : 1);
-  cfg.blockDim = dim3(MERGE_WARPS * 32);
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
   cfg.dynamicSmemBytes = list;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -840,8 +750,6 @@ int device_sms(int& sms) {
   return cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
 }
 
-// CTAs of the attention kernel, at most: the workspace is sized by this on every device alike.
-constexpr int MAX_GRID = 160;
 
 }  // namespace
 }  // namespace kv8
@@ -855,9 +763,10 @@ size_t tinfer_kv8_attention_workspace(const tinfer_kv8* cache, int n_heads, int 
   kv8::Cache c;
   tinfer_status rc;
   if (!kv8::cache_of(cache, c, rc) || n_heads < 1 || n_heads % cache->n_kv_heads || n_tokens < 1) return 0;
-  // one size for every number of rows, so that a program can keep one workspace for all its calls
-  // two parts of each CTA and one of each of its warps: 12 warps of 16 rows, or 8 of 32 at 64 dimensions
-  return (size_t)kv8::MAX_GRID * (cache->head_dim == 128 ? (2 + 12) * 16 : (2 + 8) * 32) * (cache->head_dim + 2) * 4;
+  // One size for every call, so that a program can keep one workspace for all: two parts of each CTA and one of each
+  // of its warps (12 warps of 16 rows, or 8 of 32 at 64 dimensions), or two parts of 256 rows of each CTA.
+  const size_t few = (size_t)kv8::MAX_GRID * (cache->head_dim == 128 ? (2 + 12) * 16 : (2 + 8) * 32) * (cache->head_dim + 2) * 4;
+  return std::max(few, kv8::prefill_workspace(cache->head_dim));
 }
 
 tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int n_tokens, const tinfer_rows* q_rows,
@@ -879,28 +788,34 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   if (reinterpret_cast<uintptr_t>(lse_dev) & 3) return TINFER_ERR_INVALID_ARG;
   q.group = n_heads / cache->n_kv_heads;
   q.n_heads = n_heads;
-  const long long rows = (long long)q.group * n_tokens;
-  const int per = kv8::rows_per_tile(rows, cache->head_dim);
-  const long long row_tiles = (rows + per - 1) / per, units = row_tiles * cache->n_kv_heads;
-  const int kt = 4096 / cache->head_dim;
-  // the list of tiles is counted in 32 bits
-  if (units * cache->n_seqs > (1LL << 30) / ((cache->max_ctx + kt - 1) / kt + kv8::FIXED)) return TINFER_ERR_UNSUPPORTED;
-  // and so are the rows of the cache (their coordinates in the copies)
-  if ((long long)cache->n_seqs * cache->n_kv_heads * cache->max_ctx > 0x7FFFFFFFLL) return TINFER_ERR_UNSUPPORTED;
-  q.row_tiles = (int)row_tiles;
-  q.units = (int)units;
   q.sp = kv8::Span{pos_dev, counts_dev, n_tokens, status_dev};
   q.lse = lse_dev;
   q.part = static_cast<float*>(workspace_dev);
   q.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->head_dim));
+  // rows of the cache are counted in 32 bits (their coordinates in the copies)
+  if ((long long)cache->n_seqs * cache->n_kv_heads * cache->max_ctx > 0x7FFFFFFFLL) return TINFER_ERR_UNSUPPORTED;
+  const long long rows = (long long)q.group * n_tokens;
+  const bool prefill = kv8::is_prefill(q_rows->dtype, rows);
+  const int per = prefill ? kv8::PREFILL_ROWS : kv8::rows_per_tile(rows, cache->head_dim);
+  const long long row_tiles = (rows + per - 1) / per, units = row_tiles * cache->n_kv_heads;
+  const int kt = 4096 / cache->head_dim;
+  // the list of tiles and the units are counted in 32 bits
+  if (units * cache->n_seqs > (1LL << 30) / (prefill ? 1 : (cache->max_ctx + kt - 1) / kt + kv8::FIXED))
+    return TINFER_ERR_UNSUPPORTED;
+  q.row_tiles = (int)row_tiles;
+  q.units = (int)units;
   q.keep_l2 = row_tiles > 1;
   int sms = 0;
   if (!kv8::device_sms(sms)) return TINFER_ERR_CUDA;
   q.grid = std::min(sms, kv8::MAX_GRID);
   cudaStream_t st = (cudaStream_t)stream;
   if (status_dev && cudaMemsetAsync(status_dev, 0, 4, st) != cudaSuccess) return TINFER_ERR_CUDA;
-  const cudaError_t e = cache->format == kv8::E4M3 ? kv8::launch_f<kv8::E4M3>(q, cache->head_dim, per, q_rows->dtype, st)
-                                                   : kv8::launch_f<kv8::INT8>(q, cache->head_dim, per, q_rows->dtype, st);
+  cudaError_t e;
+  if (prefill)
+    e = kv8::launch_prefill(q, cache->format, cache->head_dim, st);
+  else
+    e = cache->format == kv8::E4M3 ? kv8::launch_f<kv8::E4M3>(q, cache->head_dim, per, q_rows->dtype, st)
+                                   : kv8::launch_f<kv8::INT8>(q, cache->head_dim, per, q_rows->dtype, st);
   return e == cudaSuccess ? TINFER_OK : TINFER_ERR_CUDA;
 }
 

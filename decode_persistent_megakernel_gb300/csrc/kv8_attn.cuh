@@ -1,5 +1,7 @@
 // kv8_attn.cuh -- parameters of the attention kernels over the 8-bit cache.
 #pragma once
+#include <cuda.h>
+
 #include "kv8.cuh"
 
 namespace tinfer {
@@ -16,6 +18,121 @@ struct AttnParams {
   int grid, warps, keep_l2;  // warps of a CTA
   float scale_log2;  // log2(e) / sqrt(d)
 };
+
+constexpr int WEIGHT_SHIFT = 14;    // weights are held times 2^14: fp16 keeps 11 bits of them down to 2^-28
+// Exponents of V scales that enter the running maximum. Of a row whose keys all have the smallest one the
+// sum of the softmax is 2^(WEIGHT_SHIFT - E_MIN) for each key: 2^24 keys stay below fp32's 2^128. A smaller
+// scale's remainder makes its weights smaller than 1, a scale of 0 makes them 0 and counts in the sum.
+constexpr int E_MIN = -85, E_MAX = 120;
+constexpr long long WAIT_NS = 200LL * 1000 * 1000;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The sequence that holds place x of a list of work, of which prefix[s] places stand before sequence s.
+template <typename I>
+__device__ __forceinline__ int seq_of(const I* prefix, int n, I x) {
+  int lo = 0, hi = n;  // prefix[lo] <= x < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if ((long long)(globaltimer() - t0) > WAIT_NS) return false;
+  return true;
+}
+
+
+// The parts of a unit's rows that several CTAs hold (CTA c0's in its slot 1, the others' in their slot 0), joined in
+// order. Called by all warps of a CTA of JOIN_WARPS; blockIdx.y takes a slice of the rows. A row with few parts is
+// one warp's work; the parts of a long one are dealt out to all warps and meet in shared memory.
+constexpr int JOIN_WARPS = 8;
+
+template <int D, int ROWS, typename T>
+__device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int rows, int c0, int parts, int weight_shift) {
+  constexpr int N = D / 32, NW = JOIN_WARPS;
+  __shared__ alignas(16) float acc_s[NW][D];
+  __shared__ float sum_s[NW];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool few = parts <= NW;
+  auto part = [&](int c) { return q.part + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * ROWS * (D + 2); };
+  const int row_step = few ? NW * gridDim.y : gridDim.y;
+  for (int row = few ? blockIdx.y * NW + warp : blockIdx.y; row < rows; row += row_step) {
+    float top = -INFINITY;
+    for (int c = lane; c < parts; c += 32) top = fmaxf(top, part(c)[ROWS * D + row]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    float sum = 0.f, y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = 0.f;
+#pragma unroll 8
+    for (int c = few ? 0 : warp; c < parts; c += few ? 1 : NW) {
+      const float* p = part(c);
+      const float lc = p[ROWS * D + ROWS + row], mc = p[ROWS * D + row];
+      float f[N];
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p + (size_t)row * D + lane * N + i);
+        f[i] = v.x;
+        f[i + 1] = v.y;
+      }
+      const float w = lc == 0.f ? 0.f : exp2_fast(mc - top);
+      sum = fmaf(lc, w, sum);
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = fmaf(f[i], w, y[i]);
+    }
+    if (!few) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc_s[warp][lane * N + i] = y[i];
+      if (lane == 0) sum_s[warp] = sum;
+      __syncthreads();
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        sum += sum_s[w];
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] += acc_s[w][lane * N + i];
+      }
+      __syncthreads();
+    }
+    if (few || warp == 0) {
+      const float inv = 1.f / sum;
+      const int qrow = row0 + row, tok = qrow / q.group, hq = head * q.group + qrow - tok * q.group;
+      T* dst = static_cast<T*>(q.out.data) + seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + lane * N;
+#pragma unroll
+      for (int i = 0; i < N; ++i) store_one(dst + i, y[i] * inv);
+      if (q.lse && lane == 0)
+        q.lse[((size_t)seq * q.sp.n_tokens + tok) * q.n_heads + hq] =
+            (log2f(sum) + top - (float)weight_shift) * 0.6931471805599453f;
+    }
+  }
+}
+
+// Host: CTAs of the attention kernels, at most (workspaces are sized by it on every device alike).
+constexpr int MAX_GRID = 160;
+bool code_map(CUtensorMap* map, const void* codes, long long rows, int d, int kt);
+// Prompts (kv8_prefill.cu): whether a call's rows are many enough, its workspace, and the launch.
+constexpr int PREFILL_ROWS = 256;  // query rows of a unit there
+bool is_prefill(int dtype, long long rows);
+size_t prefill_workspace(int head_dim);
+cudaError_t launch_prefill(AttnParams& q, int format, int head_dim, cudaStream_t st);
 
 }  // namespace kv8
 }  // namespace tinfer

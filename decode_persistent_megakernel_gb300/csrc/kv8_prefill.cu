@@ -1,0 +1,610 @@
+// kv8_prefill.cu -- attention of many tokens (a prompt, or a chunk of one) over the 8-bit KV cache, on the
+// fifth-generation tensor cores. The mathematics is kv8_attn.cu's; here both products are large, and the
+// bound is shared between the tensor pipe, the exponentials (16 a clock on an SM) and shared memory.
+//
+// A unit is one KV head of one sequence with 256 of its token x group query rows, as two tiles of 128. Roles of
+// a CTA (one on each SM):
+//   warps 0-3, 4-7   softmax of tile 0 and of tile 1, a thread to a row: rotates and scales the row's query into
+//                    shared memory, then for each 128 keys reads its scores from tensor memory, and writes
+//                    the weights back over them in fp16, the left operand of the second product
+//   warps 8-11       widen the codes of K and V to fp16 in the operands' swizzled layouts, two tiles ahead
+//   warp 12          one thread issues tcgen05.mma: scores = Q K^T (both from shared memory), outputs += P V (P from
+//                    tensor memory), the two tiles in turn, so that one's softmax runs under the other's products
+// Tensor memory: two 128-column score tiles and two D-column outputs. Products are issued by one thread and
+// run in order, so new scores may follow the product that read the weights lying in their place.
+//
+// A row's running maximum is replaced only when it would grow by more than 2^8: the outputs in tensor memory
+// are then rescaled by the row's thread, which happens in the first tiles of a row and rarely after. Weights
+// are held times 2^WEIGHT_SHIFT, so they stay below 2^15 and fp16 keeps 11 bits of them down to 2^-14.
+//
+// Work is dealt out in equal runs over all CTAs by the number of keys that the units see (a causal prompt's
+// last rows see the whole prompt, its first almost nothing); a unit cut by a run's end leaves parts that
+// prefill_merge_kernel joins.
+#include <algorithm>
+
+#include "kv8_attn.cuh"
+
+namespace tinfer {
+namespace kv8 {
+namespace prefill {
+
+constexpr int KT = 128, ROWS = PREFILL_ROWS, TILE = 128;
+constexpr int NT = 512;
+constexpr int KV_STAGES = 2, SCALE_SLOTS = 4;
+constexpr int SHIFT = 5;           // of the weights
+constexpr float GROW = 8.f;        // a maximum may lag behind by 2^8
+constexpr int FIXED_KEYS = 192;    // what a unit costs beside its keys, in keys
+// registers of the four warpgroups: 2 x 184 (softmax), 104 (widening), 40 (products): 128 each at launch
+constexpr int REG_SOFTMAX = 184, REG_WIDEN = 104, REG_MMA = 40;
+static_assert(2 * REG_SOFTMAX + REG_WIDEN + REG_MMA <= 512, "register split exceeds the launch allocation");
+
+template <int D>
+struct Smem {
+  alignas(1024) uint8_t q[2][TILE * D * 2];            // D / 64 blocks of [128 rows][128 bytes], swizzled
+  alignas(1024) uint8_t k[KV_STAGES][KT * D * 2];      // the same: keys by rows
+  alignas(1024) uint8_t v[KV_STAGES][KT * D * 2];
+  float4 scale[SCALE_SLOTS][KT / 16];                  // of 16 keys: K scale, V scale's exponent, mantissa, 2^-exponent
+  alignas(8) unsigned long long k_full[KV_STAGES], v_full[KV_STAGES], k_empty[KV_STAGES], v_empty[KV_STAGES];
+  unsigned long long s_full[2], p_full[2], o_full[2], q_full[2];
+  uint32_t tmem;
+  int failed;
+};
+
+// ---- the list: sequence s has, for each KV head, row tiles rt whose weight is FIXED_KEYS + pos + 1 + step (rt + 1),
+// at least the keys that the tile sees, and easily summed
+struct Span64 {
+  int pos, count, n;  // n: row tiles
+  long long base, step;
+  __device__ void of(const AttnParams& q, int seq) {
+    if (!span_of(q.sp, seq, q.c.max_ctx, pos, count) && blockIdx.x == 0 && q.sp.status) atomicOr(q.sp.status, STATUS_BAD_POS);
+    n = (int)(((long long)q.group * count + ROWS - 1) / ROWS);
+    base = FIXED_KEYS + pos + 1;
+    step = (ROWS + q.group - 1) / q.group;
+  }
+  __device__ long long before(long long rt) const { return rt * base + step * (rt * (rt + 1) / 2); }  // of one head
+  __device__ int keys(const AttnParams& q, int rt) const {
+    return pos + (int)min(((long long)rt * ROWS + ROWS - 1) / q.group, (long long)count - 1) + 1;
+  }
+};
+
+template <int NTH>
+__device__ long long build_prefix(const AttnParams& q, long long* prefix) {
+  for (int s = threadIdx.x; s < q.c.n_seqs; s += NTH) {
+    Span64 sp;
+    sp.of(q, s);
+    prefix[s + 1] = sp.before(sp.n) * q.c.n_kv;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {  // one warp sums, 32 sequences at a time
+    long long carry = 0;
+    for (int s0 = 0; s0 < q.c.n_seqs; s0 += 32) {
+      const int s = s0 + threadIdx.x;
+      long long x = s < q.c.n_seqs ? prefix[s + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const long long y = __shfl_up_sync(~0u, x, o);
+        if ((int)threadIdx.x >= o) x += y;
+      }
+      if (s < q.c.n_seqs) prefix[s + 1] = carry + x;
+      carry += __shfl_sync(~0u, x, 31);
+    }
+    if (threadIdx.x == 0) prefix[0] = 0;
+  }
+  __syncthreads();
+  return prefix[q.c.n_seqs];
+}
+
+// A run is at least one tile long, so that each run between a unit's first and last tile holds one of its tiles.
+__device__ __forceinline__ long long run_length(long long total, int grid) {
+  return max((total + grid - 1) / grid, (long long)KT);
+}
+
+// The units of a CTA's run [lo, hi), with the tiles of each that fall into it.
+struct Walk {
+  long long at, hi;  // where the next unit is looked for
+  int seq, head, rt, first, last;  // tiles [first, last)
+  int tiles, keys, pos, count;     // of the unit
+  __device__ void init(long long lo, long long end) {
+    at = lo;
+    hi = end;
+  }
+  __device__ bool next(const AttnParams& q, const long long* prefix) {
+    while (at < hi) {
+      seq = seq_of(prefix, q.c.n_seqs, at);
+      Span64 sp;
+      sp.of(q, seq);
+      const long long per_head = sp.before(sp.n), in = at - prefix[seq];
+      head = (int)(in / per_head);
+      const long long off = in - head * per_head;
+      int a = 0, b = sp.n;  // before(a) <= off < before(b)
+      while (b - a > 1) {
+        const int mid = (a + b) >> 1;
+        if (sp.before(mid) <= off) a = mid;
+        else b = mid;
+      }
+      rt = a;
+      const long long start = prefix[seq] + head * per_head + sp.before(rt);
+      keys = sp.keys(q, rt);
+      tiles = (keys + KT - 1) / KT;
+      pos = sp.pos;
+      count = sp.count;
+      // tile t lies at start + FIXED_KEYS + t KT
+      auto tile_at = [&](long long x) { return (int)min(max((x - start - FIXED_KEYS + KT - 1) / KT, 0LL), (long long)tiles); };
+      first = at <= start + FIXED_KEYS ? 0 : tile_at(at);
+      last = hi <= start + FIXED_KEYS ? 0 : tile_at(hi);
+      at = start + sp.before(rt + 1) - sp.before(rt);
+      if (first < last) return true;
+    }
+    return false;
+  }
+};
+
+// ---- tensor cores ---------------------------------------------------------------------------------
+// Operand tiles in shared memory: 128-byte rows, 128-byte swizzle, groups of 8 rows 1024 bytes apart. K-major (Q
+// and K: a row is a query or key, its 128 bytes 64 dimensions): 32 bytes further for the next 16 dimensions, the
+// next 64 in the next block. V is read across: a row is a key, its 128 bytes 64 columns of the product
+// (N-major), 16 keys are 2048 bytes, and the leading byte offset leads to the next 64 columns.
+__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lead) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16, fp16 operands, fp32 accumulator, M 128; b_across: the right operand is N-major
+__host__ __device__ constexpr uint32_t instr(int n, bool b_across) {
+  return (1u << 4) | (b_across ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t i, int accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(i), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t i, int accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(i), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_load(uint32_t a, float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(a));
+}
+__device__ __forceinline__ void tmem_store(uint32_t a, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
+      "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
+      "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A wait that gives up at once when another role has: every role then runs through its loops without waiting.
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*failed) return;
+    if ((long long)(globaltimer() - t0) > WAIT_NS) {
+      *failed = 1;
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+template <int FMT, int D, typename T>
+__global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ AttnParams q) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
+  long long* prefix = reinterpret_cast<long long*>(smem_raw + sizeof(Smem<D>));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int s = 0; s < KV_STAGES; ++s) {
+      mbar_init(smem_addr(&sm.k_full[s]), 4);
+      mbar_init(smem_addr(&sm.v_full[s]), 4);
+      mbar_init(smem_addr(&sm.k_empty[s]), 1);
+      mbar_init(smem_addr(&sm.v_empty[s]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_addr(&sm.s_full[t]), 1);
+      mbar_init(smem_addr(&sm.o_full[t]), 1);
+      mbar_init(smem_addr(&sm.p_full[t]), 4);
+      mbar_init(smem_addr(&sm.q_full[t]), 4);
+    }
+    sm.failed = 0;
+    mbar_fence_init();
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  const long long total = build_prefix<NT>(q, prefix);  // ends with a barrier
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+  volatile int* failed = &sm.failed;
+  const long long per = run_length(total, gridDim.x);
+  Walk u;
+  u.init(min(per * blockIdx.x, total), min(per * (blockIdx.x + 1), total));
+
+  if (warp < 8) {
+    // ---- softmax: thread r of tile `tile`
+    reg_alloc<REG_SOFTMAX>();
+    const int tile = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + tile * 128, o_at = tmem + lanes + 256 + tile * D;
+    const uint32_t q_smem = smem_addr(sm.q[tile]);
+    int it = 0, units = 0, tiles_done = 0;  // key tiles of the CTA, units and key tiles of this half
+    while (u.next(q, prefix)) {
+      const int qrow = u.rt * ROWS + tile * TILE + r, all = q.group * u.count;
+      if (u.rt * ROWS + tile * TILE >= all) {  // the unit ends in the first tile
+        it += u.last - u.first;
+        continue;
+      }
+      const bool there = qrow < all;
+      const int tok = min(qrow / q.group, u.count - 1), hq = u.head * q.group + qrow - qrow / q.group * q.group;
+      const int sees = u.pos + tok + 1, first_sees = u.pos + (u.rt * ROWS + tile * TILE) / q.group + 1;
+      // the query row: rotated, divided by the power of two above its largest magnitude, in fp16
+      float scale;
+      {
+        const T* p = static_cast<const T*>(q.q.data) + u.seq * q.q.ss + tok * q.q.ts + hq * q.q.hs;
+        unsigned top = 0;
+        float x[8], y[8];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          if (there) {
+            load8(p + 8 * c, x);
+            load8(p + D / 2 + 8 * c, y);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = max(top, max(__float_as_uint(x[i]) & 0x7FFFFFFFu, __float_as_uint(y[i]) & 0x7FFFFFFFu));
+        }
+        // a rotation makes no magnitude larger than sqrt(2) times the largest: one power of two of room
+        const int e2 = top ? min(max((int)(top >> 23) - 125, -100), 100) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+        scale = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          if (there) {
+            load8(p + 8 * c, x);
+            load8(p + D / 2 + 8 * c, y);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
+          }
+          if (q.rope.on) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float cs, sn;
+              rope_cos_sin(q.rope.f[8 * c + i], u.pos + tok, cs, sn);
+              const float a = x[i], z = y[i];
+              x[i] = a * cs - z * sn;
+              y[i] = z * cs + a * sn;
+            }
+          }
+          auto put = [&](int chunk, const float (&z)[8]) {  // a 16-byte chunk of the row: block chunk / 8, swizzled by the row
+            sts128(q_smem + (chunk / 8) * (TILE * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), pack2(z[0] * down, z[1] * down),
+                   pack2(z[2] * down, z[3] * down), pack2(z[4] * down, z[5] * down), pack2(z[6] * down, z[7] * down));
+          };
+          put(c, x);
+          put(D / 16 + c, y);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.q_full[tile]));
+      }
+      float ref = -INFINITY, sum = 0.f;
+      for (int kt = u.first; kt < u.last; ++kt, ++it, ++tiles_done) {
+        wait(smem_addr(&sm.s_full[tile]), tiles_done & 1, failed);
+        fence_after();
+        float s[KT];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_load(s_at + 32 * c, s + 32 * c);
+        tmem_load_wait();
+        const float4* sc = sm.scale[it % SCALE_SLOTS];
+        float top = -INFINITY;
+        const bool edge = (kt + 1) * KT > first_sees;
+#pragma unroll
+        for (int j = 0; j < KT / 16; ++j) {
+          const float4 f = sc[j];
+          const float a = f.x * scale;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[16 * j + i] = fmaf(s[16 * j + i], a, f.y);
+        }
+        if (edge) {
+          const int n = sees - kt * KT;
+#pragma unroll
+          for (int i = 0; i < KT; ++i)
+            if (i >= n) s[i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < KT; ++i) top = fmaxf(top, s[i]);
+        float shrink = 1.f;
+        if (top > ref + GROW || ref == -INFINITY) {  // (also the row's first keys)
+          shrink = ref == -INFINITY ? 1.f : exp2_fast(ref - top);
+          ref = top;
+          sum *= shrink;
+        }
+        if (kt > u.first && __any_sync(~0u, shrink != 1.f)) {
+          // the product before has to be complete before its outputs are rescaled
+          wait(smem_addr(&sm.o_full[tile]), (tiles_done - 1) & 1, failed);
+          fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_load(o_at + 32 * c, o);
+            tmem_load_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= shrink;
+            tmem_store(o_at + 32 * c, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+        const float from = ref == -INFINITY ? 0.f : ref - (float)SHIFT;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 f = sc[4 * c + j];
+            float part = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float e0 = exp2_fast(s[64 * c + 16 * j + i] - from), e1 = exp2_fast(s[64 * c + 16 * j + i + 1] - from);
+              part += e0;
+              part += e1;
+              w[8 * j + i / 2] = pack2(e0 * f.z, e1 * f.z);
+            }
+            sum = fmaf(part, f.w, sum);
+          }
+          tmem_store(s_at + 32 * c, w);
+        }
+        tmem_store_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[tile]));
+      }
+      ++units;
+      // ---- the unit's end
+      wait(smem_addr(&sm.o_full[tile]), (tiles_done - 1) & 1, failed);
+      fence_after();
+      const bool whole = u.first == 0 && u.last == u.tiles;
+      float* part = q.part + (size_t)(2 * blockIdx.x + (u.first == 0 ? 1 : 0)) * ROWS * (D + 2);
+      const int row = tile * TILE + r;
+      const float inv = whole ? 1.f / sum : 1.f;
+      T* dst = static_cast<T*>(q.out.data) + u.seq * q.out.ss + tok * q.out.ts + hq * q.out.hs;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        tmem_load(o_at + 32 * c, o);
+        tmem_load_wait();
+        if (there) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= inv;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            if (whole) store4(dst + 32 * c + i, o + i);
+            else store4(part + (size_t)row * D + 32 * c + i, o + i);
+          }
+        }
+      }
+      if (there && !whole) {
+        part[ROWS * D + row] = ref;
+        part[ROWS * D + ROWS + row] = sum;
+      } else if (there && q.lse) {
+        q.lse[((size_t)u.seq * q.sp.n_tokens + tok) * q.n_heads + hq] = (log2f(sum) + ref - (float)SHIFT) * 0.6931471805599453f;
+      }
+      fence_before();  // the next unit's products come after these loads
+    }
+  } else if (warp < 12) {
+    // ---- widening
+    reg_dealloc<REG_WIDEN>();
+    const int t = tid - 256;
+    constexpr int CPR = D / 16, ITEMS = KT * CPR / 128;  // 16-byte pieces of a row, and of a thread
+    int it = 0;
+    while (u.next(q, prefix)) {
+      const size_t plane = (size_t)u.seq * q.c.n_kv + u.head;
+      const uint8_t* kp = q.c.k + plane * q.c.max_ctx * D;
+      const uint8_t* vp = q.c.v + plane * q.c.max_ctx * D;
+      auto load = [&](const uint8_t* p, int kt, uint4 (&w)[ITEMS]) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+          const int item = t + 128 * i, key = kt * KT + item / CPR;
+          w[i] = key < u.keys ? *reinterpret_cast<const uint4*>(p + (size_t)key * D + item % CPR * 16) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      auto widen = [&](uint32_t to, const uint4 (&w)[ITEMS], int kt) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+          const int item = t + 128 * i, row = item / CPR, c = item % CPR;
+          // 128 dimensions: eight threads hold one row, whose halves lie in two blocks; the second half stores its
+          // chunks in the other order, so that the eight meet in different banks
+          const int swap = CPR == 8 && c >= 4;
+          const uint32_t a = swap ? w[i].z : w[i].x, b = swap ? w[i].w : w[i].y, e = swap ? w[i].x : w[i].z, f = swap ? w[i].y : w[i].w;
+          uint32_t h[8];
+          codes_to_half<FMT>(a, h[0], h[1]);
+          codes_to_half<FMT>(b, h[2], h[3]);
+          codes_to_half<FMT>(e, h[4], h[5]);
+          codes_to_half<FMT>(f, h[6], h[7]);
+          const uint32_t base = to + (c / 4) * (KT * 128) + row * 128;
+          const int c0 = 2 * (c & 3) + swap, c1 = 2 * (c & 3) + 1 - swap;
+          sts128(base + ((c0 ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+          sts128(base + ((c1 ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
+        }
+      };
+      uint4 wk[ITEMS], wv[ITEMS];
+      load(kp, u.first, wk);
+      for (int kt = u.first; kt < u.last; ++kt, ++it) {
+        const int st = it % KV_STAGES;
+        const uint32_t parity = ((it / KV_STAGES) & 1) ^ 1;
+        load(vp, kt, wv);
+        wait(smem_addr(&sm.k_empty[st]), parity, failed);
+        widen(smem_addr(sm.k[st]), wk, kt);
+        if (t < KT / 16) {
+          const int key = kt * KT + 16 * t;
+          float4 f = make_float4(0.f, 0.f, 0.f, 1.f);
+          if (key < u.keys) {
+            const size_t b = plane * q.c.n_blocks + (key >> q.c.lg_block);
+            const float ks = q.c.ks[b], vs = q.c.vs[b];
+            const int e = min(max((int)((__float_as_uint(vs) >> 23) & 0xFF) - 127, E_MIN), E_MAX);
+            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+            const bool fine = vs < INFINITY;  // a scale that is not finite reaches its scores
+            f = make_float4(ks, fine ? (float)e : __uint_as_float(0x7FC00000u), fine && vs > 0.f ? vs * inv : 0.f, inv);
+          }
+          sm.scale[it % SCALE_SLOTS][t] = f;
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.k_full[st]));
+        if (kt + 1 < u.last) load(kp, kt + 1, wk);
+        wait(smem_addr(&sm.v_empty[st]), parity, failed);
+        widen(smem_addr(sm.v[st]), wv, kt);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.v_full[st]));
+      }
+    }
+  } else {
+    reg_dealloc<REG_MMA>();
+    if (warp == 12 && lane == 0) {
+      // ---- products
+      constexpr uint32_t i_s = instr(KT, false), i_o = instr(D, true);
+      int it = 0, units[2] = {0, 0}, done[2] = {0, 0};
+      while (u.next(q, prefix)) {
+        const int n = u.last - u.first, halves = u.rt * ROWS + TILE < q.group * u.count ? 2 : 1;
+        auto scores = [&](int tile, int i) {  // of the unit's i-th key tile
+          const int st = (it + i) % KV_STAGES;
+          const uint32_t a = smem_addr(sm.q[tile]), b = smem_addr(sm.k[st]);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + tile * 128, desc(a + (k / 4) * (TILE * 128) + (k % 4) * 32, 16), desc(b + (k / 4) * (KT * 128) + (k % 4) * 32, 16),
+                   i_s, k > 0);
+          commit(smem_addr(&sm.s_full[tile]));
+        };
+        for (int tile = 0; tile < halves; ++tile) {
+          wait(smem_addr(&sm.q_full[tile]), units[tile]++ & 1, failed);
+          if (tile == 0) wait(smem_addr(&sm.k_full[it % KV_STAGES]), (it / KV_STAGES) & 1, failed);
+          fence_after();
+          scores(tile, 0);
+        }
+        commit(smem_addr(&sm.k_empty[it % KV_STAGES]));
+        for (int i = 0; i < n; ++i) {
+          const int st = (it + i) % KV_STAGES, st1 = (it + i + 1) % KV_STAGES;
+          for (int tile = 0; tile < halves; ++tile) {
+            if (tile == 0) wait(smem_addr(&sm.v_full[st]), ((it + i) / KV_STAGES) & 1, failed);
+            wait(smem_addr(&sm.p_full[tile]), done[tile]++ & 1, failed);
+            fence_after();
+            const uint32_t p = tmem + tile * 128, b = smem_addr(sm.v[st]);
+#pragma unroll
+            for (int k = 0; k < KT / 16; ++k)
+              mma_ts(tmem + 256 + tile * D, p + 8 * k, desc(b + k * 2048, KT * 128), i_o, i > 0 || k > 0);
+            commit(smem_addr(&sm.o_full[tile]));
+            if (i + 1 < n) {
+              if (tile == 0) {
+                wait(smem_addr(&sm.k_full[st1]), ((it + i + 1) / KV_STAGES) & 1, failed);
+                fence_after();
+              }
+              scores(tile, i + 1);
+            }
+          }
+          commit(smem_addr(&sm.v_empty[st]));
+          if (i + 1 < n) commit(smem_addr(&sm.k_empty[st1]));
+        }
+        it += n;
+      }
+    }
+    __syncwarp();
+  }
+  fence_before();
+  __syncthreads();
+  if (tid == 0 && sm.failed && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
+  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) prefill_merge_kernel(const __grid_constant__ AttnParams q) {
+  extern __shared__ long long prefix64[];
+  const long long total = build_prefix<JOIN_WARPS * 32>(q, prefix64);
+  const long long per = run_length(total, q.grid);
+  const int seq = blockIdx.x / q.units, unit = blockIdx.x % q.units, head = unit / q.row_tiles, rt = unit % q.row_tiles;
+  Span64 sp;
+  sp.of(q, seq);
+  int c0 = 0, parts = 0;
+  if (rt < sp.n) {
+    const long long start = prefix64[seq] + head * sp.before(sp.n) + sp.before(rt) + FIXED_KEYS;
+    c0 = (int)(start / per);
+    parts = (int)((start + (sp.keys(q, rt) - 1) / KT * KT) / per) - c0 + 1;
+  }
+  pdl_wait();
+  if (parts <= 1) return;
+  join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * sp.count - rt * ROWS, ROWS), c0, parts, SHIFT);
+}
+
+template <int FMT, int D, typename T>
+cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
+  auto kernel = prefill_kernel<FMT, D, T>;
+  const size_t list = (size_t)(q.c.n_seqs + 1) * 8, smem = sizeof(Smem<D>) + list;
+  static_assert(sizeof(Smem<D>) + (MAX_SEQS + 1) * 8 <= 227 * 1024, "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<q.grid, NT, smem, st>>>(q);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units), q.c.n_seqs * q.units <= 256 ? 16 : 4);
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
+  cfg.dynamicSmemBytes = list;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D, T>, q);
+}
+
+template <int FMT>
+cudaError_t launch_f(AttnParams& q, int head_dim, cudaStream_t st) {
+  return head_dim == 64 ? launch_t<FMT, 64, __nv_bfloat16>(q, st) : launch_t<FMT, 128, __nv_bfloat16>(q, st);
+}
+
+}  // namespace prefill
+
+// bf16 rows beyond one row tile of the other kernel. fp32 and fp16 rows stay there: their two-part operands keep
+// the precision of their type, which one fp16 operand would not.
+bool is_prefill(int dtype, long long rows) { return dtype == TINFER_DTYPE_BF16 && rows > 64; }
+size_t prefill_workspace(int head_dim) { return (size_t)MAX_GRID * 2 * PREFILL_ROWS * (head_dim + 2) * 4; }
+
+cudaError_t launch_prefill(AttnParams& q, int format, int head_dim, cudaStream_t st) {
+  return format == E4M3 ? prefill::launch_f<E4M3>(q, head_dim, st) : prefill::launch_f<INT8>(q, head_dim, st);
+}
+
+}  // namespace kv8
+}  // namespace tinfer
