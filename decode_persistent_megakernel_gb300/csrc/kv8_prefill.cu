@@ -4,13 +4,11 @@
 //
 // A unit is one KV head of one sequence with 256 of its token x group query rows, as two tiles of 128. Roles of
 // a CTA (one on each SM):
-//   warps 0-7, 8-15  softmax of tile 0 and of tile 1, two threads to a row: they rotate and scale the row's query
-//                    into shared memory, then for each 128 keys read their 64 scores from tensor memory, once for
-//                    the maximum and once for the weights, and write those back over them in fp16, the left operand
-//                    of the second product. (One thread to a row left two warps of each scheduler to hide the
-//                    latency of tensor memory and exponentials: 2.3 and 3.0 us for 128 keys at 64 and 128 dimensions.)
-//   warps 16-23      widen the codes of K and V to fp16 in the operands' swizzled layouts, two tiles ahead
-//   warp 24          one thread issues tcgen05.mma: scores = Q K^T (both from shared memory), outputs += P V (P from
+//   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a thread to a row: it rotates and scales the row's query into
+//                   shared memory, then for each 128 keys takes their scores from tensor memory into registers, and
+//                   writes the weights back over them in fp16, the left operand of the second product
+//   4 or 7 warps    widen the codes of K and V to fp16 in the operands' swizzled layouts, two tiles ahead
+//   the next warp   one thread issues tcgen05.mma: scores = Q K^T (both from shared memory), outputs += P V (P from
 //                    tensor memory), the two tiles in turn, so that one's softmax runs under the other's products
 // Tensor memory: two 128-column score tiles and two D-column outputs. Products are issued by one thread and
 // run in order, so new scores may follow the product that read the weights lying in their place.
@@ -31,29 +29,28 @@ namespace tinfer {
 namespace kv8 {
 namespace prefill {
 
-constexpr int KT = 128, ROWS = PREFILL_ROWS, TILE = 128;
+constexpr int KT = 128, HALF = KT / 2, ROWS = PREFILL_ROWS, TILE = 128;
 static_assert(TILE == KT, "blocks of Q and K are alike");
-constexpr int WARP_WIDEN = 16;     // first warp of the widening role; before it the softmax, after it the products
-// 24 warps at most, so that each may have 80 registers
+constexpr int WARP_WIDEN = 8;      // first warp of the widening role; before it the softmax, after it the products
 template <int D>
 struct Roles {
-  static constexpr int WIDEN = D == 64 ? 4 : 7, MMA = WARP_WIDEN + WIDEN, NT = (MMA + 1) * 32;
+  static constexpr int WIDEN = D == 64 ? 4 : 7, MMA = WARP_WIDEN + WIDEN;
 };
+constexpr int NT = 512;
 constexpr int KV_STAGES = 2, SCALE_SLOTS = 4;
 constexpr int SHIFT = 5;           // of the weights
 constexpr float GROW = 8.f;        // a maximum may lag behind by 2^8
-constexpr int FIXED_KEYS = 192;    // what a unit costs beside its keys, in keys
+constexpr int FIXED_KEYS = 512;    // what a unit costs beside its keys, in keys
 
 template <int D>
 struct Smem {
   alignas(1024) uint8_t q[2][TILE * D * 2];            // D / 64 blocks of [128 rows][128 bytes], swizzled
   alignas(1024) uint8_t k[KV_STAGES][KT * D * 2];      // the same: keys by rows
   alignas(1024) uint8_t v[KV_STAGES][KT * D * 2];
-  alignas(16) float2 angle[2][2][TILE * 4];            // cosines and sines of four dimensions at the tile's tokens
-  float swap[2][2][2][TILE];                           // between the two threads of a row, in turns
+  alignas(16) float2 angle[2][TILE * 8];               // cosines and sines of eight dimensions at the tile's tokens
   float4 scale[SCALE_SLOTS][KT / 16];                  // of 16 keys: K scale, V scale's exponent, mantissa, 2^-exponent
   alignas(8) unsigned long long k_full[KV_STAGES], v_full[KV_STAGES], k_empty[KV_STAGES], v_empty[KV_STAGES];
-  unsigned long long s_full[2], p_full[2], o_full[2], q_full[2];
+  unsigned long long s_full[2][2], p_full[2][2], o_full[2][2], q_full[2];  // [tile][half of its keys]
   uint32_t tmem;
   int failed;
 };
@@ -191,14 +188,14 @@ __device__ __forceinline__ void tmem_load(uint32_t a, float* v) {
         "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
       : "r"(a));
 }
-__device__ __forceinline__ void tmem_store32(uint32_t a, const uint32_t* u) {
+// 16 columns, complete on return.
+__device__ __forceinline__ void tmem_load16(uint32_t a, uint32_t* u) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
-      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
-      "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
-      "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+      : "r"(a)
       : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t a, const uint32_t* u) {
@@ -242,8 +239,8 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 }
 
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_constant__ AttnParams q) {
-  constexpr int WARP_MMA = Roles<D>::MMA, NT = Roles<D>::NT, NT_WIDEN = Roles<D>::WIDEN * 32;
+__global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ AttnParams q) {
+  constexpr int WARP_MMA = Roles<D>::MMA, NT_WIDEN = Roles<D>::WIDEN * 32;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
   long long* prefix = reinterpret_cast<long long*>(smem_raw + sizeof(Smem<D>));
@@ -257,10 +254,12 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
       mbar_init(smem_addr(&sm.v_empty[s]), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_addr(&sm.s_full[t]), 1);
-      mbar_init(smem_addr(&sm.o_full[t]), 1);
-      mbar_init(smem_addr(&sm.p_full[t]), 8);
-      mbar_init(smem_addr(&sm.q_full[t]), 8);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(smem_addr(&sm.s_full[t][h]), 1);
+        mbar_init(smem_addr(&sm.p_full[t][h]), 4);
+        mbar_init(smem_addr(&sm.o_full[t][h]), 1);
+      }
+      mbar_init(smem_addr(&sm.q_full[t]), 4);
     }
     sm.failed = 0;
     mbar_fence_init();
@@ -279,17 +278,12 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
   u.init(min(per * blockIdx.x, total), min(per * (blockIdx.x + 1), total));
 
   if (warp < WARP_WIDEN) {
-    // ---- softmax: a thread has row r of tile `tile`, and of it keys (and outputs, and rotary pairs) of `half`
-    const int tile = warp >> 3, half = (warp >> 2) & 1, r = tid & 127;
+    // ---- softmax: thread r of tile `tile`
+    const int tile = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + tile * 128 + half * 64, o_at = tmem + lanes + 256 + tile * D + half * (D / 2);
+    const uint32_t s_at = tmem + lanes + tile * 128, o_at = tmem + lanes + 256 + tile * D;
     const uint32_t q_smem = smem_addr(sm.q[tile]) + r * 128;
     int it = 0, tiles_done = 0;  // key tiles of the CTA and of this tile's rows
-    auto other = [&](float x, int turn) {  // what the thread with the row's other half has
-      sm.swap[tile][turn & 1][half][r] = x;
-      named_sync(1 + tile, 256);
-      return sm.swap[tile][turn & 1][half ^ 1][r];
-    };
     while (u.next(q, prefix)) {
       const int row0 = u.rt * ROWS + tile * TILE, qrow = row0 + r, all = q.group * u.count;
       if (row0 >= all) {  // the unit ends in the first tile
@@ -302,62 +296,53 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
       const int sees = u.pos + tok + 1, first_sees = u.pos + tok0 + 1;
       float scale;
       {
-        // the query row: rotated, divided by a power of two above its largest magnitude, in fp16. A thread takes
-        // D / 4 neighbouring dimensions and their rotary partners; the angles of four of them at a time are
-        // worked out once for every token of the tile
-        constexpr int P = D / 4;
-        const T* p = static_cast<const T*>(q.q.data) + u.seq * q.q.ss + tok * q.q.ts + hq * q.q.hs + half * P;
-        uint4 raw[2][P / 8];
+        // the query row: rotated, divided by a power of two above its largest magnitude, in fp16. The angles of
+        // eight dimensions at a time are worked out once for every token of the tile
+        const T* p = static_cast<const T*>(q.q.data) + u.seq * q.q.ss + tok * q.q.ts + hq * q.q.hs;
+        uint4 raw[D / 8];
 #pragma unroll
-        for (int c = 0; c < P / 8; ++c) {
-          raw[0][c] = there ? *reinterpret_cast<const uint4*>(p + 8 * c) : make_uint4(0, 0, 0, 0);
-          raw[1][c] = there ? *reinterpret_cast<const uint4*>(p + D / 2 + 8 * c) : make_uint4(0, 0, 0, 0);
-        }
+        for (int c = 0; c < D / 8; ++c) raw[c] = there ? *reinterpret_cast<const uint4*>(p + 8 * c) : make_uint4(0, 0, 0, 0);
         float x[8], y[8];
         unsigned most = 0;
 #pragma unroll
-        for (int c = 0; c < 2 * (P / 8); ++c) {
-          load8(reinterpret_cast<const T*>(&raw[c & 1][c >> 1]), x);
+        for (int c = 0; c < D / 8; ++c) {
+          load8(reinterpret_cast<const T*>(&raw[c]), x);
 #pragma unroll
           for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(x[i]) & 0x7FFFFFFFu);
         }
-        most = max(most, __float_as_uint(other(__uint_as_float(most), tiles_done + 1)));
         // a rotation makes no magnitude larger than sqrt(2) times the largest: one power of two of room
         const int e2 = most ? min(max((int)(most >> 23) - 125, -100), 100) : 0;
         const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
         scale = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll
-        for (int c = 0; c < P / 8; ++c) {
-          load8(reinterpret_cast<const T*>(&raw[0][c]), x);
-          load8(reinterpret_cast<const T*>(&raw[1][c]), y);
+        for (int c = 0; c < D / 16; ++c) {
+          load8(reinterpret_cast<const T*>(&raw[c]), x);
+          load8(reinterpret_cast<const T*>(&raw[D / 16 + c]), y);
           if (q.rope.on) {
+            named_sync(1 + tile, TILE);
+            for (int i = r; i < ntok * 8; i += TILE) {
+              float cs, sn;
+              rope_cos_sin(q.rope.f[8 * c + (i & 7)], u.pos + tok0 + (i >> 3), cs, sn);
+              sm.angle[tile][i] = make_float2(cs, sn);
+            }
+            named_sync(1 + tile, TILE);
+            const float4* at = reinterpret_cast<const float4*>(&sm.angle[tile][(tok - tok0) * 8]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              named_sync(3 + 2 * tile + half, TILE);
-              for (int i = r; i < ntok * 4; i += TILE) {
-                float cs, sn;
-                rope_cos_sin(q.rope.f[half * P + 8 * c + 4 * h + (i & 3)], u.pos + tok0 + (i >> 2), cs, sn);
-                sm.angle[tile][half][i] = make_float2(cs, sn);
-              }
-              named_sync(3 + 2 * tile + half, TILE);
-              const float4* at = reinterpret_cast<const float4*>(&sm.angle[tile][half][(tok - tok0) * 4]);
-#pragma unroll
-              for (int i = 0; i < 4; i += 2) {
-                const float4 f = at[i / 2];
-                const float a0 = x[4 * h + i], z0 = y[4 * h + i], a1 = x[4 * h + i + 1], z1 = y[4 * h + i + 1];
-                x[4 * h + i] = a0 * f.x - z0 * f.y;
-                y[4 * h + i] = z0 * f.x + a0 * f.y;
-                x[4 * h + i + 1] = a1 * f.z - z1 * f.w;
-                y[4 * h + i + 1] = z1 * f.z + a1 * f.w;
-              }
+            for (int i = 0; i < 8; i += 2) {
+              const float4 f = at[i / 2];
+              const float a0 = x[i], z0 = y[i], a1 = x[i + 1], z1 = y[i + 1];
+              x[i] = a0 * f.x - z0 * f.y;
+              y[i] = z0 * f.x + a0 * f.y;
+              x[i + 1] = a1 * f.z - z1 * f.w;
+              y[i + 1] = z1 * f.z + a1 * f.w;
             }
           }
           auto put = [&](int chunk, const float (&z)[8]) {  // a 16-byte chunk of the row: block chunk / 8, swizzled by the row
             sts128(q_smem + (chunk / 8) * (TILE * 128) + (((chunk & 7) ^ (r & 7)) << 4), pack2(z[0] * down, z[1] * down),
                    pack2(z[2] * down, z[3] * down), pack2(z[4] * down, z[5] * down), pack2(z[6] * down, z[7] * down));
           };
-          put(half * (P / 8) + c, x);
-          put(D / 16 + half * (P / 8) + c, y);
+          put(c, x);
+          put(D / 16 + c, y);
         }
         fence_proxy_async_shared();
         __syncwarp();
@@ -366,123 +351,117 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
 
       float ref = -INFINITY, sum = 0.f;
       for (int kt = u.first; kt < u.last; ++kt, ++it, ++tiles_done) {
-        wait(smem_addr(&sm.s_full[tile]), tiles_done & 1, failed);
-        fence_after();
-        const float4* sc = sm.scale[it % SCALE_SLOTS] + half * 4;
-        // keys of this half of the tile that the row sees
-        const int n = (kt + 1) * KT > first_sees ? sees - kt * KT - half * 64 : 64;
-        const bool all_seen = __all_sync(~0u, n >= 64);
-        float a[32];
-        // the row's maximum: of each 16 keys' plain products first, whose scale is one
-        float top = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int n = (kt + 1) * KT > first_sees ? sees - kt * KT - h * HALF : HALF;  // keys of this half that the row sees
+          const bool all_seen = __all_sync(~0u, n >= HALF);
+          const float4* sc = sm.scale[it % SCALE_SLOTS] + h * (HALF / 16);
+          const uint32_t at = s_at + h * HALF;
+          wait(smem_addr(&sm.s_full[tile][h]), tiles_done & 1, failed);
+          fence_after();
+          float s[2][32];
+          tmem_load(at, s[0]);
+          tmem_load(at + 32, s[1]);
+          tmem_wait(s[0]);
+          tmem_wait(s[1]);
+          // the row's maximum: of each 16 keys' plain products first, whose scale is one
+          float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          tmem_load(s_at + 32 * c, a);
-          tmem_wait(a);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < HALF / 16; ++j) {
             float m = -INFINITY;
+            const float* v = s[j / 2] + 16 * (j & 1);
             if (all_seen) {
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) m = fmaxf(m, fmaxf(a[16 * j + i], a[16 * j + i + 1]));
+              for (int i = 0; i < 16; i += 2) m = fmaxf(m, fmaxf(v[i], v[i + 1]));
             } else {
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (32 * c + 16 * j + i < n) m = fmaxf(m, a[16 * j + i]);
+                if (16 * j + i < n) m = fmaxf(m, v[i]);
             }
-            const float4 f = sc[2 * c + j];
+            const float4 f = sc[j];
             top = fmaxf(top, fmaf(m, f.x * scale, f.y));
           }
-        }
-        tmem_load(s_at, a);  // again, for the weights: on its way during the exchange
-        top = fmaxf(top, other(top, tiles_done));
-        float shrink = 1.f;
-        if (top > ref + GROW || ref == -INFINITY) {  // (also the row's first keys)
-          shrink = ref == -INFINITY ? 1.f : exp2_fast(ref - top);
-          ref = top;
-          sum *= shrink;
-        }
-        tmem_wait(a);
-        if (kt > u.first && __any_sync(~0u, shrink != 1.f)) {
-          // the product before has to be complete before its outputs are rescaled
-          wait(smem_addr(&sm.o_full[tile]), (tiles_done - 1) & 1, failed);
-          fence_after();
+          float shrink = 1.f;
+          if (top > ref + GROW || ref == -INFINITY) {  // (also the row's first keys)
+            shrink = ref == -INFINITY ? 1.f : exp2_fast(ref - top);
+            ref = top;
+            sum *= shrink;
+          }
+          if (__any_sync(~0u, shrink != 1.f)) {
+            // the product before has to be complete before its outputs are rescaled
+            wait(smem_addr(&sm.o_full[tile][h ^ 1]), (h ? tiles_done : tiles_done - 1) & 1, failed);
+            fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
-            float o[32];
-            tmem_load(o_at + 32 * c, o);
-            tmem_wait(o);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_load16(o_at + 16 * c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= shrink;
-            tmem_store32(o_at + 32 * c, reinterpret_cast<const uint32_t*>(o));
-          }
-        }
-        // weights, 32 keys at a time, over the scores of this half that have been read
-        const float from = ref == -INFINITY ? 0.f : ref - (float)SHIFT;
-        auto some = [&](int c, auto cut) {
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float4 f = sc[2 * c + j];
-            const float fx = f.x * scale, fy = f.y - from;
-            const float2 f2 = make_float2(fx, fx), g2 = make_float2(fy, fy), v2 = make_float2(f.z, f.z);
-            float2 part = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float2 e = fma2(make_float2(a[16 * j + i], a[16 * j + i + 1]), f2, g2);
-              if (cut.value) {  // masked after the scaling, whatever the scale of keys that are not seen
-                if (32 * c + 16 * j + i >= n) e.x = -INFINITY;
-                if (32 * c + 16 * j + i + 1 >= n) e.y = -INFINITY;
-              }
-              e.x = exp2_fast(e.x);
-              e.y = exp2_fast(e.y);
-              part = add2(part, e);
-              e = __fmul2_rn(e, v2);
-              w[8 * j + i / 2] = pack2(e.x, e.y);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+              tmem_store16(o_at + 16 * c, o);
             }
-            sum = fmaf(part.x + part.y, f.w, sum);
           }
-          tmem_store16(s_at + 16 * c, w);
-        };
+          // weights, over the scores, which are all in registers
+          const float from = ref == -INFINITY ? 0.f : ref - (float)SHIFT;
+          auto weights = [&](auto cut) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c) {
-            tmem_load(s_at + 32, a);
-            tmem_wait(a);
-          }
-          if (all_seen) some(c, std::false_type{});  // the warp's choice: tensor memory is stored to by whole warps
-          else some(c, std::true_type{});
+            for (int c = 0; c < 2; ++c) {
+              uint32_t w[16];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float4 f = sc[2 * c + j];
+                const float fx = f.x * scale, fy = f.y - from;
+                const float2 f2 = make_float2(fx, fx), g2 = make_float2(fy, fy), v2 = make_float2(f.z, f.z);
+                float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                  float2 e = fma2(make_float2(s[c][16 * j + i], s[c][16 * j + i + 1]), f2, g2);
+                  if (cut.value) {  // masked after the scaling, whatever the scale of keys that are not seen
+                    if (32 * c + 16 * j + i >= n) e.x = -INFINITY;
+                    if (32 * c + 16 * j + i + 1 >= n) e.y = -INFINITY;
+                  }
+                  e.x = exp2_fast(e.x);
+                  e.y = exp2_fast(e.y);
+                  part = add2(part, e);
+                  e = __fmul2_rn(e, v2);
+                  w[8 * j + i / 2] = pack2(e.x, e.y);
+                }
+                sum = fmaf(part.x + part.y, f.w, sum);
+              }
+              tmem_store16(at + 16 * c, w);
+            }
+          };
+          if (all_seen) weights(std::false_type{});  // the warp's choice: tensor memory is stored to by whole warps
+          else weights(std::true_type{});
+          tmem_store_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[tile][h]));
         }
-        tmem_store_wait();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[tile]));
       }
       // ---- the unit's end
-      sum += other(sum, tiles_done);
-      wait(smem_addr(&sm.o_full[tile]), (tiles_done - 1) & 1, failed);
+      wait(smem_addr(&sm.o_full[tile][1]), (tiles_done - 1) & 1, failed);
       fence_after();
       const bool whole = u.first == 0 && u.last == u.tiles;
       float* part = q.part + (size_t)(2 * blockIdx.x + (u.first == 0 ? 1 : 0)) * ROWS * (D + 2);
       const int row = tile * TILE + r;
       const float inv = whole ? 1.f / sum : 1.f;
-      T* dst = static_cast<T*>(q.out.data) + u.seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + half * (D / 2);
-#pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        float o[32];
-        tmem_load(o_at + 32 * c, o);
-        tmem_wait(o);
-        if (there) {
+      T* dst = static_cast<T*>(q.out.data) + u.seq * q.out.ss + tok * q.out.ts + hq * q.out.hs;
+      float o[D / 32][32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= inv;
+      for (int c = 0; c < D / 32; ++c) tmem_load(o_at + 32 * c, o[c]);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) tmem_wait(o[c]);
+      fence_before();  // the next unit's products come after these loads
+      if (there) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
-            if (whole) store4(dst + 32 * c + i, o + i);
-            else store4(part + (size_t)row * D + half * (D / 2) + 32 * c + i, o + i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[c][i + k] *= inv;
+            if (whole) store4(dst + 32 * c + i, o[c] + i);
+            else store4(part + (size_t)row * D + 32 * c + i, o[c] + i);
           }
-        }
-      }
-      if (there && half == 0) {
         if (!whole) {
           part[ROWS * D + row] = ref;
           part[ROWS * D + ROWS + row] = sum;
@@ -490,7 +469,6 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           q.lse[((size_t)u.seq * q.sp.n_tokens + tok) * q.n_heads + hq] = (log2f(sum) + ref - (float)SHIFT) * 0.6931471805599453f;
         }
       }
-      fence_before();  // the next unit's products come after these loads
     }
   } else if (warp < WARP_MMA) {
     // ---- widening
@@ -561,49 +539,50 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
       }
     }
   } else {
-    if (lane == 0) {
+    if (warp == WARP_MMA && lane == 0) {
       // ---- products
-      constexpr uint32_t i_s = instr(KT, false), i_o = instr(D, true);
+      constexpr uint32_t i_s = instr(HALF, false), i_o = instr(D, true);
       const uint64_t q_desc = desc(smem_addr(sm.q[0]), 16), k_desc = desc(smem_addr(sm.k[0]), 16), v_desc = desc(smem_addr(sm.v[0]), KT * 128);
-      int it = 0, units[2] = {0, 0}, done[2] = {0, 0};
+      int it = 0, units[2] = {0, 0}, done = 0;  // key tiles of the CTA, units of each row tile, key tiles of row tile 1
       while (u.next(q, prefix)) {
         const int n = u.last - u.first, halves = u.rt * ROWS + TILE < q.group * u.count ? 2 : 1;
-        auto scores = [&](int tile, int i) {  // of the unit's i-th key tile
-          const uint64_t a = q_desc + (uint64_t)tile * (sizeof(sm.q[0]) >> 4), b = k_desc + (uint64_t)((it + i) % KV_STAGES) * (sizeof(sm.k[0]) >> 4);
+        auto scores = [&](int tile, int h, int i) {  // of half the keys of the unit's i-th key tile
+          const uint64_t a = q_desc + (uint64_t)tile * (sizeof(sm.q[0]) >> 4);
+          const uint64_t b = k_desc + (uint64_t)((it + i) % KV_STAGES) * (sizeof(sm.k[0]) >> 4) + h * (HALF * 128 >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {  // 32 bytes further in the block, then the next block
             constexpr int BLOCK = TILE * 128 >> 4;
-            mma_ss(tmem + tile * 128, a + (k / 4) * BLOCK + (k % 4) * 2, b + (k / 4) * BLOCK + (k % 4) * 2, i_s, k > 0);
+            mma_ss(tmem + tile * 128 + h * HALF, a + (k / 4) * BLOCK + (k % 4) * 2, b + (k / 4) * BLOCK + (k % 4) * 2, i_s, k > 0);
           }
-          commit(smem_addr(&sm.s_full[tile]));
+          commit(smem_addr(&sm.s_full[tile][h]));
         };
+        wait(smem_addr(&sm.k_full[it % KV_STAGES]), (it / KV_STAGES) & 1, failed);
         for (int tile = 0; tile < halves; ++tile) {
           wait(smem_addr(&sm.q_full[tile]), units[tile]++ & 1, failed);
-          if (tile == 0) wait(smem_addr(&sm.k_full[it % KV_STAGES]), (it / KV_STAGES) & 1, failed);
           fence_after();
-          scores(tile, 0);
+          scores(tile, 0, 0);
+          scores(tile, 1, 0);
         }
         commit(smem_addr(&sm.k_empty[it % KV_STAGES]));
         for (int i = 0; i < n; ++i) {
           const int st = (it + i) % KV_STAGES, st1 = (it + i + 1) % KV_STAGES;
-          for (int tile = 0; tile < halves; ++tile) {
-            if (tile == 0) wait(smem_addr(&sm.v_full[st]), ((it + i) / KV_STAGES) & 1, failed);
-            wait(smem_addr(&sm.p_full[tile]), done[tile]++ & 1, failed);
+          wait(smem_addr(&sm.v_full[st]), ((it + i) / KV_STAGES) & 1, failed);
+          if (i + 1 < n) wait(smem_addr(&sm.k_full[st1]), ((it + i + 1) / KV_STAGES) & 1, failed);
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            const int tile = x & 1, h = x >> 1;
+            if (tile >= halves) continue;
+            wait(smem_addr(&sm.p_full[tile][h]), (tile ? done : it + i) & 1, failed);
             fence_after();
-            const uint32_t p = tmem + tile * 128;  // weights of keys 64 on begin at column 64
-            const uint64_t b = v_desc + (uint64_t)st * (sizeof(sm.v[0]) >> 4);
+            const uint32_t p = tmem + tile * 128 + h * HALF;
+            const uint64_t b = v_desc + (uint64_t)st * (sizeof(sm.v[0]) >> 4) + h * (HALF * 128 >> 4);
 #pragma unroll
-            for (int k = 0; k < KT / 16; ++k)
-              mma_ts(tmem + 256 + tile * D, p + 8 * k + 32 * (k / 4), b + k * (2048 >> 4), i_o, k > 0 || i > 0);
-            commit(smem_addr(&sm.o_full[tile]));
-            if (i + 1 < n) {
-              if (tile == 0) {
-                wait(smem_addr(&sm.k_full[st1]), ((it + i + 1) / KV_STAGES) & 1, failed);
-                fence_after();
-              }
-              scores(tile, i + 1);
-            }
+            for (int k = 0; k < HALF / 16; ++k)
+              mma_ts(tmem + 256 + tile * D, p + 8 * k, b + k * (2048 >> 4), i_o, k > 0 || h > 0 || i > 0);
+            commit(smem_addr(&sm.o_full[tile][h]));
+            if (i + 1 < n) scores(tile, h, i + 1);
           }
+          if (halves == 2) ++done;
           commit(smem_addr(&sm.v_empty[st]));
           if (i + 1 < n) commit(smem_addr(&sm.k_empty[st1]));
         }
@@ -644,7 +623,7 @@ cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
   static_assert(sizeof(Smem<D>) + (MAX_SEQS + 1) * 8 <= 227 * 1024, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<q.grid, Roles<D>::NT, smem, st>>>(q);
+  kernel<<<q.grid, NT, smem, st>>>(q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units), q.c.n_seqs * q.units <= 256 ? 16 : 4);
