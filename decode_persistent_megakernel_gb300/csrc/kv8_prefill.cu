@@ -8,7 +8,7 @@
 //                   shared memory, then for each 128 keys takes their scores from tensor memory into registers, and
 //                   writes the weights back over them in fp16, the left operand of the second product
 //   4 or 7 warps    widen the codes of K and V to fp16 in the operands' swizzled layouts, two tiles ahead
-//   the next warp   one thread issues tcgen05.mma: scores = Q K^T (both from shared memory), outputs += P V (P from
+//   the next warp   issues tcgen05.mma (one of its lanes): scores = Q K^T (both from shared memory), outputs += P V (P from
 //                    tensor memory), the two tiles in turn, so that one's softmax runs under the other's products
 // Tensor memory: two 128-column score tiles and two D-column outputs. Products are issued by one thread and
 // run in order, so new scores may follow the product that read the weights lying in their place.
@@ -157,22 +157,32 @@ __device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lead) {
 __host__ __device__ constexpr uint32_t instr(int n, bool b_across) {
   return (1u << 4) | (b_across ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t i, int accumulate) {
+// Issued by the one lane that `leader` names. The whole warp comes here with the same operands: they stay in uniform
+// registers, where a single thread's would be moved there for every instruction (75 to 90 cycles a product of 64 columns).
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t leader;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
+  return leader;
+}
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t i, int accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(i), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(i), "r"(accumulate), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t i, int accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t i, int accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(i), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(i), "r"(accumulate), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(leader)
+      : "memory");
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -539,10 +549,11 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
       }
     }
   } else {
-    if (warp == WARP_MMA && lane == 0) {
+    if (warp == WARP_MMA) {
       // ---- products
       constexpr uint32_t i_s = instr(HALF, false), i_o = instr(D, true);
       const uint64_t q_desc = desc(smem_addr(sm.q[0]), 16), k_desc = desc(smem_addr(sm.k[0]), 16), v_desc = desc(smem_addr(sm.v[0]), KT * 128);
+      const uint32_t leader = elect();
       int it = 0, units[2] = {0, 0}, done = 0;  // key tiles of the CTA, units of each row tile, key tiles of row tile 1
       while (u.next(q, prefix)) {
         const int n = u.last - u.first, halves = u.rt * ROWS + TILE < q.group * u.count ? 2 : 1;
@@ -552,9 +563,9 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {  // 32 bytes further in the block, then the next block
             constexpr int BLOCK = TILE * 128 >> 4;
-            mma_ss(tmem + tile * 128 + h * HALF, a + (k / 4) * BLOCK + (k % 4) * 2, b + (k / 4) * BLOCK + (k % 4) * 2, i_s, k > 0);
+            mma_ss(leader, tmem + tile * 128 + h * HALF, a + (k / 4) * BLOCK + (k % 4) * 2, b + (k / 4) * BLOCK + (k % 4) * 2, i_s, k > 0);
           }
-          commit(smem_addr(&sm.s_full[tile][h]));
+          commit(leader, smem_addr(&sm.s_full[tile][h]));
         };
         wait(smem_addr(&sm.k_full[it % KV_STAGES]), (it / KV_STAGES) & 1, failed);
         for (int tile = 0; tile < halves; ++tile) {
@@ -563,7 +574,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
           scores(tile, 0, 0);
           scores(tile, 1, 0);
         }
-        commit(smem_addr(&sm.k_empty[it % KV_STAGES]));
+        commit(leader, smem_addr(&sm.k_empty[it % KV_STAGES]));
         for (int i = 0; i < n; ++i) {
           const int st = (it + i) % KV_STAGES, st1 = (it + i + 1) % KV_STAGES;
           wait(smem_addr(&sm.v_full[st]), ((it + i) / KV_STAGES) & 1, failed);
@@ -578,13 +589,13 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
             const uint64_t b = v_desc + (uint64_t)st * (sizeof(sm.v[0]) >> 4) + h * (HALF * 128 >> 4);
 #pragma unroll
             for (int k = 0; k < HALF / 16; ++k)
-              mma_ts(tmem + 256 + tile * D, p + 8 * k, b + k * (2048 >> 4), i_o, k > 0 || h > 0 || i > 0);
-            commit(smem_addr(&sm.o_full[tile][h]));
+              mma_ts(leader, tmem + 256 + tile * D, p + 8 * k, b + k * (2048 >> 4), i_o, k > 0 || h > 0 || i > 0);
+            commit(leader, smem_addr(&sm.o_full[tile][h]));
             if (i + 1 < n) scores(tile, h, i + 1);
           }
           if (halves == 2) ++done;
-          commit(smem_addr(&sm.v_empty[st]));
-          if (i + 1 < n) commit(smem_addr(&sm.k_empty[st1]));
+          commit(leader, smem_addr(&sm.v_empty[st]));
+          if (i + 1 < n) commit(leader, smem_addr(&sm.k_empty[st1]));
         }
         it += n;
       }
