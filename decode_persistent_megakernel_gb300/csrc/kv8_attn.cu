@@ -799,7 +799,8 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   const int per = prefill ? kv8::PREFILL_ROWS : kv8::rows_per_tile(rows, cache->head_dim);
   const long long row_tiles = (rows + per - 1) / per, units = row_tiles * cache->n_kv_heads;
   const int kt = 4096 / cache->head_dim;
-  // the list of tiles and the units are counted in 32 bits
+  // rows, the list of tiles and the units are counted in 32 bits
+  if (rows > (1LL << 30)) return TINFER_ERR_UNSUPPORTED;
   if (units * cache->n_seqs > (1LL << 30) / (prefill ? 1 : (cache->max_ctx + kt - 1) / kt + kv8::FIXED))
     return TINFER_ERR_UNSUPPORTED;
   q.row_tiles = (int)row_tiles;

@@ -35,19 +35,20 @@ constexpr int WARP_WIDEN = 8;      // first warp of the widening role; before it
 template <int D>
 struct Roles {
   static constexpr int WIDEN = D == 64 ? 4 : 7, MMA = WARP_WIDEN + WIDEN;
+  static constexpr int ANGLES = D == 64 ? 4096 : 1472;  // of a tile: all of 128 tokens, or of 23 (or 8 at a time)
 };
 constexpr int NT = 512;
 constexpr int KV_STAGES = 2, SCALE_SLOTS = 4;
 constexpr int SHIFT = 5;           // of the weights
 constexpr float GROW = 8.f;        // a maximum may lag behind by 2^8
-constexpr int FIXED_KEYS = 512;    // what a unit costs beside its keys, in keys
+constexpr int FIXED_KEYS = 384;    // what a unit costs beside its keys, in keys
 
 template <int D>
 struct Smem {
   alignas(1024) uint8_t q[2][TILE * D * 2];            // D / 64 blocks of [128 rows][128 bytes], swizzled
   alignas(1024) uint8_t k[KV_STAGES][KT * D * 2];      // the same: keys by rows
   alignas(1024) uint8_t v[KV_STAGES][KT * D * 2];
-  alignas(16) float2 angle[2][TILE * 8];               // cosines and sines of eight dimensions at the tile's tokens
+  alignas(16) float2 angle[2][Roles<D>::ANGLES];       // cosines and sines at the tile's tokens
   float4 scale[SCALE_SLOTS][KT / 16];                  // of 16 keys: K scale, V scale's exponent, mantissa, 2^-exponent
   alignas(8) unsigned long long k_full[KV_STAGES], v_full[KV_STAGES], k_empty[KV_STAGES], v_empty[KV_STAGES];
   unsigned long long s_full[2][2], p_full[2][2], o_full[2][2], q_full[2];  // [tile][half of its keys]
@@ -58,18 +59,17 @@ struct Smem {
 // ---- the list: sequence s has, for each KV head, row tiles rt whose weight is FIXED_KEYS + pos + 1 + step (rt + 1),
 // at least the keys that the tile sees, and easily summed
 struct Span64 {
-  int pos, count, n;  // n: row tiles
+  int pos, count, n, last;  // n: row tiles; last: its last row
   long long base, step;
   __device__ void of(const AttnParams& q, int seq) {
     if (!span_of(q.sp, seq, q.c.max_ctx, pos, count) && blockIdx.x == 0 && q.sp.status) atomicOr(q.sp.status, STATUS_BAD_POS);
-    n = (int)(((long long)q.group * count + ROWS - 1) / ROWS);
+    last = q.group * count - 1;  // rows are counted in 31 bits
+    n = (last + ROWS) / ROWS;
     base = FIXED_KEYS + pos + 1;
     step = (ROWS + q.group - 1) / q.group;
   }
-  __device__ long long before(long long rt) const { return rt * base + step * (rt * (rt + 1) / 2); }  // of one head
-  __device__ int keys(const AttnParams& q, int rt) const {
-    return pos + (int)min(((long long)rt * ROWS + ROWS - 1) / q.group, (long long)count - 1) + 1;
-  }
+  __device__ long long before(int rt) const { return rt * base + step * ((long long)rt * (rt + 1) / 2); }  // of one head
+  __device__ int keys(const AttnParams& q, int rt) const { return pos + min(rt * ROWS + ROWS - 1, last) / q.group + 1; }
 };
 
 template <int NTH>
@@ -119,7 +119,9 @@ struct Walk {
       Span64 sp;
       sp.of(q, seq);
       const long long per_head = sp.before(sp.n), in = at - prefix[seq];
-      head = (int)(in / per_head);
+      head = (int)((float)in / (float)per_head);  // 64-bit divisions take a microsecond
+      while (head * per_head > in) --head;
+      while ((head + 1) * per_head <= in) ++head;
       const long long off = in - head * per_head;
       int a = 0, b = sp.n;  // before(a) <= off < before(b)
       while (b - a > 1) {
@@ -244,6 +246,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -292,7 +298,8 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
     const int tile = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + tile * 128, o_at = tmem + lanes + 256 + tile * D;
-    const uint32_t q_smem = smem_addr(sm.q[tile]) + r * 128;
+    constexpr int ANGLES = Roles<D>::ANGLES;
+    const uint32_t q_smem = smem_addr(sm.q[tile]) + r * 128, stage = smem_addr(sm.q[tile]) + (warp & 3) * (32 * D * 2);
     int it = 0, tiles_done = 0;  // key tiles of the CTA and of this tile's rows
     while (u.next(q, prefix)) {
       const int row0 = u.rt * ROWS + tile * TILE, qrow = row0 + r, all = q.group * u.count;
@@ -306,12 +313,30 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
       const int sees = u.pos + tok + 1, first_sees = u.pos + tok0 + 1;
       float scale;
       {
-        // the query row: rotated, divided by a power of two above its largest magnitude, in fp16. The angles of
-        // eight dimensions at a time are worked out once for every token of the tile
+        // the query row: rotated, divided by a power of two above its largest magnitude, in fp16. The angles are
+        // worked out once for every token of the tile
         const T* p = static_cast<const T*>(q.q.data) + u.seq * q.q.ss + tok * q.q.ts + hq * q.q.hs;
+        // the warp loads its rows one after another, whole lines at a time, and hands them out through shared memory
         uint4 raw[D / 8];
+        {
+          constexpr int LANES = D / 8;  // to a row
+          const uint64_t mine = there ? reinterpret_cast<uint64_t>(p) : 0;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) raw[c] = there ? *reinterpret_cast<const uint4*>(p + 8 * c) : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < LANES; ++i) {
+            const int from = i * (32 / LANES) + lane / LANES;
+            const char* src = reinterpret_cast<const char*>(__shfl_sync(~0u, mine, from));
+            raw[i] = src ? *reinterpret_cast<const uint4*>(src + lane % LANES * 16) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < LANES; ++i) {
+            const int from = i * (32 / LANES) + lane / LANES;
+            sts128(stage + from * (D * 2) + ((lane % LANES ^ (from & (LANES - 1))) << 4), raw[i].x, raw[i].y, raw[i].z, raw[i].w);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < LANES; ++c) raw[c] = lds128(stage + lane * (D * 2) + ((c ^ (lane & (LANES - 1))) << 4));
+          __syncwarp();
+        }
         float x[8], y[8];
         unsigned most = 0;
 #pragma unroll
@@ -323,20 +348,31 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
         // a rotation makes no magnitude larger than sqrt(2) times the largest: one power of two of room
         const int e2 = most ? min(max((int)(most >> 23) - 125, -100), 100) : 0;
         const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+        // chunks of eight dimensions whose angles are held at once: a power of two
+        int lg_pairs = 3;
+        while ((16 << (lg_pairs - 3)) <= D / 2 && ntok * (2 << lg_pairs) <= ANGLES) ++lg_pairs;
+        const int cpp = 1 << (lg_pairs - 3);
         scale = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           load8(reinterpret_cast<const T*>(&raw[c]), x);
           load8(reinterpret_cast<const T*>(&raw[D / 16 + c]), y);
           if (q.rope.on) {
-            named_sync(1 + tile, TILE);
-            for (int i = r; i < ntok * 8; i += TILE) {
-              float cs, sn;
-              rope_cos_sin(q.rope.f[8 * c + (i & 7)], u.pos + tok0 + (i >> 3), cs, sn);
-              sm.angle[tile][i] = make_float2(cs, sn);
+            if (c % cpp == 0) {
+              named_sync(1 + tile, TILE);
+              // [chunk][token][dimension]; a thread has one dimension of the chunks and every so many tokens
+              const int pairs = 8 * cpp, pair = r & (pairs - 1);
+              const unsigned long long freq = q.rope.f[8 * c + pair];
+              float2* to = sm.angle[tile] + (pair >> 3) * ntok * 8 + (pair & 7);
+#pragma unroll 4
+              for (int i = r >> lg_pairs; i < ntok; i += TILE >> lg_pairs) {
+                float cs, sn;
+                rope_cos_sin(freq, u.pos + tok0 + i, cs, sn);
+                to[8 * i] = make_float2(cs, sn);
+              }
+              named_sync(1 + tile, TILE);
             }
-            named_sync(1 + tile, TILE);
-            const float4* at = reinterpret_cast<const float4*>(&sm.angle[tile][(tok - tok0) * 8]);
+            const float4* at = reinterpret_cast<const float4*>(&sm.angle[tile][(c % cpp * ntok + tok - tok0) * 8]);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
               const float4 f = at[i / 2];
@@ -375,22 +411,31 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
           tmem_wait(s[0]);
           tmem_wait(s[1]);
           // the row's maximum: of each 16 keys' plain products first, whose scale is one
-          float top = -INFINITY;
+          float4 f[HALF / 16];
+          float m[HALF / 16];
 #pragma unroll
-          for (int j = 0; j < HALF / 16; ++j) {
-            float m = -INFINITY;
-            const float* v = s[j / 2] + 16 * (j & 1);
-            if (all_seen) {
+          for (int j = 0; j < HALF / 16; ++j) f[j] = sc[j];
+          if (all_seen) {
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) m = fmaxf(m, fmaxf(v[i], v[i + 1]));
-            } else {
+            for (int j = 0; j < HALF / 16; ++j) {
+              const float* v = s[j / 2] + 16 * (j & 1);
+              // a tree of three-way maxima
+              const float a = fmaxf(fmaxf(v[0], v[1]), v[2]), b = fmaxf(fmaxf(v[3], v[4]), v[5]), c = fmaxf(fmaxf(v[6], v[7]), v[8]),
+                          d = fmaxf(fmaxf(v[9], v[10]), v[11]), e = fmaxf(fmaxf(v[12], v[13]), v[14]);
+              m[j] = fmaxf(fmaxf(fmaxf(a, b), c), fmaxf(fmaxf(d, e), v[15]));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < HALF / 16; ++j) {
+              m[j] = -INFINITY;
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (16 * j + i < n) m = fmaxf(m, v[i]);
+                if (16 * j + i < n) m[j] = fmaxf(m[j], s[j / 2][16 * (j & 1) + i]);
             }
-            const float4 f = sc[j];
-            top = fmaxf(top, fmaf(m, f.x * scale, f.y));
           }
+          float top = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < HALF / 16; ++j) top = fmaxf(top, fmaf(m[j], f[j].x * scale, f[j].y));
           float shrink = 1.f;
           if (top > ref + GROW || ref == -INFINITY) {  // (also the row's first keys)
             shrink = ref == -INFINITY ? 1.f : exp2_fast(ref - top);
@@ -418,9 +463,9 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
               uint32_t w[16];
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const float4 f = sc[2 * c + j];
-                const float fx = f.x * scale, fy = f.y - from;
-                const float2 f2 = make_float2(fx, fx), g2 = make_float2(fy, fy), v2 = make_float2(f.z, f.z);
+                const float4 g = f[2 * c + j];
+                const float fx = g.x * scale, fy = g.y - from;
+                const float2 f2 = make_float2(fx, fx), g2 = make_float2(fy, fy), v2 = make_float2(g.z, g.z);
                 float2 part = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
@@ -435,7 +480,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
                   e = __fmul2_rn(e, v2);
                   w[8 * j + i / 2] = pack2(e.x, e.y);
                 }
-                sum = fmaf(part.x + part.y, f.w, sum);
+                sum = fmaf(part.x + part.y, g.w, sum);
               }
               tmem_store16(at + 16 * c, w);
             }
@@ -456,22 +501,40 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
       const int row = tile * TILE + r;
       const float inv = whole ? 1.f / sum : 1.f;
       T* dst = static_cast<T*>(q.out.data) + u.seq * q.out.ss + tok * q.out.ts + hq * q.out.hs;
-      float o[D / 32][32];
+      // rows leave by whole lines: through the query tile's memory, whose products are done, 2 D bytes of a row at a time
+      constexpr int LANES = D / 8;
+      const uint64_t mine = !there ? 0 : whole ? reinterpret_cast<uint64_t>(dst) : reinterpret_cast<uint64_t>(part + (size_t)row * D);
+#pragma unroll 1
+      for (int c32 = 0; c32 < D / 32; ++c32) {
+        float o[32];
+        tmem_load(o_at + 32 * c32, o);
+        tmem_wait(o);
+        const int in_pass = c32 % (D / 64);  // a part's pass is D / 2 columns in fp32, a result's all D in 16 bits
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) tmem_load(o_at + 32 * c, o[c]);
+        for (int k = 0; k < 8; ++k) {
+          if (whole && k >= 4) break;
+          const int c = whole ? 4 * c32 + k : 8 * in_pass + k;
+          const uint32_t to = stage + lane * (D * 2) + ((c ^ (lane & (LANES - 1))) << 4);
+          if (whole)
+            sts128(to, pack_bf16(o[8 * (k & 3)] * inv, o[8 * (k & 3) + 1] * inv), pack_bf16(o[8 * (k & 3) + 2] * inv, o[8 * (k & 3) + 3] * inv),
+                   pack_bf16(o[8 * (k & 3) + 4] * inv, o[8 * (k & 3) + 5] * inv), pack_bf16(o[8 * (k & 3) + 6] * inv, o[8 * (k & 3) + 7] * inv));
+          else
+            sts128(to, __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+        }
+        if (whole ? c32 < D / 32 - 1 : in_pass < D / 64 - 1) continue;
+        __syncwarp();
+        const int pass = whole ? 0 : c32 / (D / 64);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) tmem_wait(o[c]);
+        for (int i = 0; i < LANES; ++i) {
+          const int from = i * (32 / LANES) + lane / LANES;
+          char* to = reinterpret_cast<char*>(__shfl_sync(~0u, mine, from));
+          const uint4 w = lds128(stage + from * (D * 2) + ((lane % LANES ^ (from & (LANES - 1))) << 4));
+          if (to) *reinterpret_cast<uint4*>(to + pass * (D * 2) + lane % LANES * 16) = w;
+        }
+        __syncwarp();
+      }
       fence_before();  // the next unit's products come after these loads
       if (there) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[c][i + k] *= inv;
-            if (whole) store4(dst + 32 * c + i, o[c] + i);
-            else store4(part + (size_t)row * D + 32 * c + i, o[c] + i);
-          }
         if (!whole) {
           part[ROWS * D + row] = ref;
           part[ROWS * D + ROWS + row] = sum;
