@@ -71,8 +71,63 @@ __device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool few = parts <= NW;
   auto part = [&](int c) { return q.part + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * ROWS * (D + 2); };
-  const int row_step = few ? NW * gridDim.y : gridDim.y;
-  for (int row = few ? blockIdx.y * NW + warp : blockIdx.y; row < rows; row += row_step) {
+  auto finish = [&](int row, float top, float sum, const float (&y)[N]) {
+    const float inv = 1.f / sum;
+    const int qrow = row0 + row, tok = qrow / q.group, hq = head * q.group + qrow - tok * q.group;
+    T* dst = static_cast<T*>(q.out.data) + seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + lane * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) store_one(dst + i, y[i] * inv);
+    if (q.lse && lane == 0)
+      q.lse[((size_t)seq * q.sp.n_tokens + tok) * q.n_heads + hq] = (log2f(sum) + top - (float)weight_shift) * 0.6931471805599453f;
+  };
+  auto load = [&](const float* p, int row, float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(p + (size_t)row * D + lane * N + i);
+      f[i] = v.x;
+      f[i + 1] = v.y;
+    }
+  };
+  if (few) {  // four rows of a warp at a time, their loads side by side
+    constexpr int R = 4;
+    for (int r0 = (blockIdx.y * NW + warp) * R; r0 < rows; r0 += NW * R * gridDim.y) {
+      float top[R], sum[R], y[R][N];
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        top[k] = -INFINITY;
+        sum[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[k][i] = 0.f;
+      }
+#pragma unroll 2
+      for (int c = 0; c < parts; ++c) {
+        const float* p = part(c);
+        float mc[R], lc[R], f[R][N];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          const int row = min(r0 + k, rows - 1);
+          mc[k] = p[ROWS * D + row];
+          lc[k] = p[ROWS * D + ROWS + row];
+          load(p, row, f[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          if (lc[k] == 0.f) continue;  // no key of the row
+          const float now = fmaxf(top[k], mc[k]);
+          const float a = top[k] == now ? 1.f : exp2_fast(top[k] - now), b = mc[k] == now ? 1.f : exp2_fast(mc[k] - now);
+          top[k] = now;
+          sum[k] = fmaf(lc[k], b, sum[k] * a);
+#pragma unroll
+          for (int i = 0; i < N; ++i) y[k][i] = fmaf(f[k][i], b, y[k][i] * a);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+        if (r0 + k < rows) finish(r0 + k, top[k], sum[k], y[k]);
+    }
+    return;
+  }
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     float top = -INFINITY;
     for (int c = lane; c < parts; c += 32) top = fmaxf(top, part(c)[ROWS * D + row]);
 #pragma unroll
@@ -81,26 +136,21 @@ __device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int
 #pragma unroll
     for (int i = 0; i < N; ++i) y[i] = 0.f;
 #pragma unroll 8
-    for (int c = few ? 0 : warp; c < parts; c += few ? 1 : NW) {
+    for (int c = warp; c < parts; c += NW) {
       const float* p = part(c);
       const float lc = p[ROWS * D + ROWS + row], mc = p[ROWS * D + row];
       float f[N];
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(p + (size_t)row * D + lane * N + i);
-        f[i] = v.x;
-        f[i + 1] = v.y;
-      }
+      load(p, row, f);
       const float w = lc == 0.f ? 0.f : exp2_fast(mc - top);
       sum = fmaf(lc, w, sum);
 #pragma unroll
       for (int i = 0; i < N; ++i) y[i] = fmaf(f[i], w, y[i]);
     }
-    if (!few) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc_s[warp][lane * N + i] = y[i];
-      if (lane == 0) sum_s[warp] = sum;
-      __syncthreads();
+    for (int i = 0; i < N; ++i) acc_s[warp][lane * N + i] = y[i];
+    if (lane == 0) sum_s[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
       sum = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) y[i] = 0.f;
@@ -110,18 +160,9 @@ __device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int
 #pragma unroll
         for (int i = 0; i < N; ++i) y[i] += acc_s[w][lane * N + i];
       }
-      __syncthreads();
+      finish(row, top, sum, y);
     }
-    if (few || warp == 0) {
-      const float inv = 1.f / sum;
-      const int qrow = row0 + row, tok = qrow / q.group, hq = head * q.group + qrow - tok * q.group;
-      T* dst = static_cast<T*>(q.out.data) + seq * q.out.ss + tok * q.out.ts + hq * q.out.hs + lane * N;
-#pragma unroll
-      for (int i = 0; i < N; ++i) store_one(dst + i, y[i] * inv);
-      if (q.lse && lane == 0)
-        q.lse[((size_t)seq * q.sp.n_tokens + tok) * q.n_heads + hq] =
-            (log2f(sum) + top - (float)weight_shift) * 0.6931471805599453f;
-    }
+    __syncthreads();
   }
 }
 

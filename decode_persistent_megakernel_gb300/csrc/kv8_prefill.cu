@@ -10,8 +10,10 @@
 //   4 or 7 warps    widen the codes of K and V to fp16 in the operands' swizzled layouts, two tiles ahead
 //   the next warp   issues tcgen05.mma (one of its lanes): scores = Q K^T (both from shared memory), outputs += P V (P from
 //                    tensor memory), the two tiles in turn, so that one's softmax runs under the other's products
-// Tensor memory: two 128-column score tiles and two D-column outputs. Products are issued by one thread and
-// run in order, so new scores may follow the product that read the weights lying in their place.
+// Tensor memory: two (three at 64 dimensions) 128-column score buffers and two D-column outputs. Products are issued
+// by one warp and run in order, so new scores may follow the product that read the weights lying in their place.
+// The softmax and the second product go by halves of 64 keys, so that the first half's product runs under the
+// second half's exponentials. (Scores by halves as well cost a 128-row operand read twice: 115 us against DDD.)
 //
 // A row's running maximum is replaced only when it would grow by more than 2^8: the outputs in tensor memory
 // are then rescaled by the row's thread, which happens in the first tiles of a row and rarely after. Weights
@@ -35,6 +37,7 @@ constexpr int WARP_WIDEN = 8;      // first warp of the widening role; before it
 template <int D>
 struct Roles {
   static constexpr int WIDEN = D == 64 ? 4 : 7, MMA = WARP_WIDEN + WIDEN;
+  static constexpr int BUFFERS = D == 64 ? 3 : 2;       // of 128 x 128 scores in tensor memory, beside two outputs of D columns
   static constexpr int ANGLES = D == 64 ? 4096 : 1472;  // of a tile: all of 128 tokens, or of 23 (or 8 at a time)
 };
 constexpr int NT = 512;
@@ -51,7 +54,7 @@ struct Smem {
   alignas(16) float2 angle[2][Roles<D>::ANGLES];       // cosines and sines at the tile's tokens
   float4 scale[SCALE_SLOTS][KT / 16];                  // of 16 keys: K scale, V scale's exponent, mantissa, 2^-exponent
   alignas(8) unsigned long long k_full[KV_STAGES], v_full[KV_STAGES], k_empty[KV_STAGES], v_empty[KV_STAGES];
-  unsigned long long s_full[2][2], p_full[2][2], o_full[2][2], q_full[2];  // [tile][half of its keys]
+  unsigned long long s_full[3], p_full[3][2], o_full[2][2], q_full[2];  // of score buffers and row tiles, [half of the keys]
   uint32_t tmem;
   int failed;
 };
@@ -256,6 +259,7 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 
 template <int FMT, int D, typename T>
 __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ AttnParams q) {
+  constexpr int BUFFERS = Roles<D>::BUFFERS, O_AT = BUFFERS * KT;
   constexpr int WARP_MMA = Roles<D>::MMA, NT_WIDEN = Roles<D>::WIDEN * 32;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
@@ -269,12 +273,12 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
       mbar_init(smem_addr(&sm.k_empty[s]), 1);
       mbar_init(smem_addr(&sm.v_empty[s]), 1);
     }
+    for (int t = 0; t < 3; ++t) {
+      mbar_init(smem_addr(&sm.s_full[t]), 1);
+      for (int h = 0; h < 2; ++h) mbar_init(smem_addr(&sm.p_full[t][h]), 4);
+    }
     for (int t = 0; t < 2; ++t) {
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(smem_addr(&sm.s_full[t][h]), 1);
-        mbar_init(smem_addr(&sm.p_full[t][h]), 4);
-        mbar_init(smem_addr(&sm.o_full[t][h]), 1);
-      }
+      for (int h = 0; h < 2; ++h) mbar_init(smem_addr(&sm.o_full[t][h]), 1);
       mbar_init(smem_addr(&sm.q_full[t]), 4);
     }
     sm.failed = 0;
@@ -297,16 +301,19 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
     // ---- softmax: thread r of tile `tile`
     const int tile = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + tile * 128, o_at = tmem + lanes + 256 + tile * D;
+    const uint32_t o_at = tmem + lanes + O_AT + tile * D;
     constexpr int ANGLES = Roles<D>::ANGLES;
     const uint32_t q_smem = smem_addr(sm.q[tile]) + r * 128, stage = smem_addr(sm.q[tile]) + (warp & 3) * (32 * D * 2);
-    int it = 0, tiles_done = 0;  // key tiles of the CTA and of this tile's rows
+    int it = 0, jobs = 0, tiles_done = 0;  // key tiles of the CTA, of both its row tiles, and of this one
     while (u.next(q, prefix)) {
       const int row0 = u.rt * ROWS + tile * TILE, qrow = row0 + r, all = q.group * u.count;
       if (row0 >= all) {  // the unit ends in the first tile
         it += u.last - u.first;
+        jobs += u.last - u.first;
         continue;
       }
+      const int halves = u.rt * ROWS + TILE < all ? 2 : 1;  // row tiles of the unit
+      jobs += tile;
       const bool there = qrow < all;
       const int tok = min(qrow / q.group, u.count - 1), hq = u.head * q.group + qrow - qrow / q.group * q.group;
       const int tok0 = row0 / q.group, ntok = (min(row0 + TILE, all) - 1) / q.group - tok0 + 1;
@@ -396,14 +403,15 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
       }
 
       float ref = -INFINITY, sum = 0.f;
-      for (int kt = u.first; kt < u.last; ++kt, ++it, ++tiles_done) {
+      for (int kt = u.first; kt < u.last; ++kt, ++it, ++tiles_done, jobs += halves) {
+        const int buf = jobs % BUFFERS;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int n = (kt + 1) * KT > first_sees ? sees - kt * KT - h * HALF : HALF;  // keys of this half that the row sees
           const bool all_seen = __all_sync(~0u, n >= HALF);
           const float4* sc = sm.scale[it % SCALE_SLOTS] + h * (HALF / 16);
-          const uint32_t at = s_at + h * HALF;
-          wait(smem_addr(&sm.s_full[tile][h]), tiles_done & 1, failed);
+          const uint32_t at = tmem + lanes + buf * KT + h * HALF;
+          wait(smem_addr(&sm.s_full[buf]), jobs / BUFFERS & 1, failed);
           fence_after();
           float s[2][32];
           tmem_load(at, s[0]);
@@ -490,9 +498,10 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
           tmem_store_wait();
           fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[tile][h]));
+          if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[buf][h]));
         }
       }
+      jobs -= tile;  // (all jobs of the unit are counted)
       // ---- the unit's end
       wait(smem_addr(&sm.o_full[tile][1]), (tiles_done - 1) & 1, failed);
       fence_after();
@@ -614,53 +623,49 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
   } else {
     if (warp == WARP_MMA) {
       // ---- products
-      constexpr uint32_t i_s = instr(HALF, false), i_o = instr(D, true);
+      constexpr uint32_t i_s = instr(KT, false), i_o = instr(D, true);
       const uint64_t q_desc = desc(smem_addr(sm.q[0]), 16), k_desc = desc(smem_addr(sm.k[0]), 16), v_desc = desc(smem_addr(sm.v[0]), KT * 128);
       const uint32_t leader = elect();
-      int it = 0, units[2] = {0, 0}, done = 0;  // key tiles of the CTA, units of each row tile, key tiles of row tile 1
+      int it = 0, jobs = 0, units[2] = {0, 0};  // key tiles of the CTA, of both its row tiles; units of each row tile
       while (u.next(q, prefix)) {
-        const int n = u.last - u.first, halves = u.rt * ROWS + TILE < q.group * u.count ? 2 : 1;
-        auto scores = [&](int tile, int h, int i) {  // of half the keys of the unit's i-th key tile
-          const uint64_t a = q_desc + (uint64_t)tile * (sizeof(sm.q[0]) >> 4);
-          const uint64_t b = k_desc + (uint64_t)((it + i) % KV_STAGES) * (sizeof(sm.k[0]) >> 4) + h * (HALF * 128 >> 4);
+        // job j of the unit: row tile j % halves against key tile j / halves. Its scores go into buffer (jobs + j) %
+        // BUFFERS, where its weights replace them; `ahead` jobs have their scores before the first has its weights
+        const int halves = u.rt * ROWS + TILE < q.group * u.count ? 2 : 1, n = (u.last - u.first) * halves;
+        const int ahead = min(halves == 2 ? BUFFERS : 2, n);
+        auto scores = [&](int j) {
+          const int i = it + (halves == 2 ? j >> 1 : j), tile = halves == 2 ? j & 1 : 0, st = i % KV_STAGES, buf = (jobs + j) % BUFFERS;
+          if (tile == 0) wait(smem_addr(&sm.k_full[st]), i / KV_STAGES & 1, failed);
+          if (j < halves) wait(smem_addr(&sm.q_full[tile]), units[tile]++ & 1, failed);
+          fence_after();
+          const uint64_t a = q_desc + (uint64_t)tile * (sizeof(sm.q[0]) >> 4), b = k_desc + (uint64_t)st * (sizeof(sm.k[0]) >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {  // 32 bytes further in the block, then the next block
             constexpr int BLOCK = TILE * 128 >> 4;
-            mma_ss(leader, tmem + tile * 128 + h * HALF, a + (k / 4) * BLOCK + (k % 4) * 2, b + (k / 4) * BLOCK + (k % 4) * 2, i_s, k > 0);
+            mma_ss(leader, tmem + buf * KT, a + (k / 4) * BLOCK + (k % 4) * 2, b + (k / 4) * BLOCK + (k % 4) * 2, i_s, k > 0);
           }
-          commit(leader, smem_addr(&sm.s_full[tile][h]));
+          commit(leader, smem_addr(&sm.s_full[buf]));
+          if (tile == halves - 1) commit(leader, smem_addr(&sm.k_empty[st]));
         };
-        wait(smem_addr(&sm.k_full[it % KV_STAGES]), (it / KV_STAGES) & 1, failed);
-        for (int tile = 0; tile < halves; ++tile) {
-          wait(smem_addr(&sm.q_full[tile]), units[tile]++ & 1, failed);
-          fence_after();
-          scores(tile, 0, 0);
-          scores(tile, 1, 0);
-        }
-        commit(leader, smem_addr(&sm.k_empty[it % KV_STAGES]));
-        for (int i = 0; i < n; ++i) {
-          const int st = (it + i) % KV_STAGES, st1 = (it + i + 1) % KV_STAGES;
-          wait(smem_addr(&sm.v_full[st]), ((it + i) / KV_STAGES) & 1, failed);
-          if (i + 1 < n) wait(smem_addr(&sm.k_full[st1]), ((it + i + 1) / KV_STAGES) & 1, failed);
+        for (int j = 0; j < ahead; ++j) scores(j);
+        for (int j = 0; j < n; ++j) {
+          const int i = it + (halves == 2 ? j >> 1 : j), tile = halves == 2 ? j & 1 : 0, st = i % KV_STAGES, buf = (jobs + j) % BUFFERS;
+          if (tile == 0) wait(smem_addr(&sm.v_full[st]), i / KV_STAGES & 1, failed);
 #pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
-            const int tile = x & 1, h = x >> 1;
-            if (tile >= halves) continue;
-            wait(smem_addr(&sm.p_full[tile][h]), (tile ? done : it + i) & 1, failed);
+          for (int h = 0; h < 2; ++h) {
+            wait(smem_addr(&sm.p_full[buf][h]), (jobs + j) / BUFFERS & 1, failed);
             fence_after();
-            const uint32_t p = tmem + tile * 128 + h * HALF;
+            const uint32_t p = tmem + buf * KT + h * HALF;
             const uint64_t b = v_desc + (uint64_t)st * (sizeof(sm.v[0]) >> 4) + h * (HALF * 128 >> 4);
 #pragma unroll
             for (int k = 0; k < HALF / 16; ++k)
-              mma_ts(leader, tmem + 256 + tile * D, p + 8 * k, b + k * (2048 >> 4), i_o, k > 0 || h > 0 || i > 0);
+              mma_ts(leader, tmem + O_AT + tile * D, p + 8 * k, b + k * (2048 >> 4), i_o, k > 0 || h > 0 || j >= halves);
             commit(leader, smem_addr(&sm.o_full[tile][h]));
-            if (i + 1 < n) scores(tile, h, i + 1);
           }
-          if (halves == 2) ++done;
-          commit(leader, smem_addr(&sm.v_empty[st]));
-          if (i + 1 < n) commit(leader, smem_addr(&sm.k_empty[st1]));
+          if (tile == halves - 1) commit(leader, smem_addr(&sm.v_empty[st]));
+          if (j + ahead < n) scores(j + ahead);
         }
-        it += n;
+        it += u.last - u.first;
+        jobs += n;
       }
     }
     __syncwarp();
@@ -700,7 +705,7 @@ cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
   kernel<<<q.grid, NT, smem, st>>>(q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units), q.c.n_seqs * q.units <= 256 ? 16 : 4);
+  cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units), 8);
   cfg.blockDim = dim3(JOIN_WARPS * 32);
   cfg.dynamicSmemBytes = list;
   cfg.stream = st;
