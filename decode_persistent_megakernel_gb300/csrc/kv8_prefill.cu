@@ -626,46 +626,70 @@ __global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ 
       constexpr uint32_t i_s = instr(KT, false), i_o = instr(D, true);
       const uint64_t q_desc = desc(smem_addr(sm.q[0]), 16), k_desc = desc(smem_addr(sm.k[0]), 16), v_desc = desc(smem_addr(sm.v[0]), KT * 128);
       const uint32_t leader = elect();
-      int it = 0, jobs = 0, units[2] = {0, 0};  // key tiles of the CTA, of both its row tiles; units of each row tile
+      // Jobs: a row tile against a key tile, the unit's row tiles in turn for each key tile. A job's scores go into the
+      // next score buffer, where its weights replace them; `ahead` jobs have their scores before the first has its
+      // weights. Two cursors over the jobs, kept by counting: between a job's scores and the next one's values the
+      // tensor pipe waits for this warp.
+      struct Cursor {
+        uint32_t buf, buf_phase, stage, stage_phase, tile;
+        __device__ __forceinline__ void step(uint32_t last_tile) {
+          if (++buf == BUFFERS) {
+            buf = 0;
+            buf_phase ^= 1;
+          }
+          if (tile == last_tile) {
+            tile = 0;
+            stage_phase ^= stage;
+            stage ^= 1;
+          } else {
+            tile = 1;
+          }
+        }
+      };
+      static_assert(KV_STAGES == 2, "a cursor's stage is one bit");
+      Cursor sc{0, 0, 0, 0, 0}, va{0, 0, 0, 0, 0};
+      uint32_t q_phase[2] = {0, 0};
+      const uint32_t bar_k = smem_addr(sm.k_full), bar_v = smem_addr(sm.v_full), bar_ke = smem_addr(sm.k_empty), bar_ve = smem_addr(sm.v_empty);
+      const uint32_t bar_s = smem_addr(sm.s_full), bar_p = smem_addr(sm.p_full), bar_o = smem_addr(sm.o_full), bar_q = smem_addr(sm.q_full);
       while (u.next(q, prefix)) {
-        // job j of the unit: row tile j % halves against key tile j / halves. Its scores go into buffer (jobs + j) %
-        // BUFFERS, where its weights replace them; `ahead` jobs have their scores before the first has its weights
-        const int halves = u.rt * ROWS + TILE < q.group * u.count ? 2 : 1, n = (u.last - u.first) * halves;
-        const int ahead = min(halves == 2 ? BUFFERS : 2, n);
-        auto scores = [&](int j) {
-          const int i = it + (halves == 2 ? j >> 1 : j), tile = halves == 2 ? j & 1 : 0, st = i % KV_STAGES, buf = (jobs + j) % BUFFERS;
-          if (tile == 0) wait(smem_addr(&sm.k_full[st]), i / KV_STAGES & 1, failed);
-          if (j < halves) wait(smem_addr(&sm.q_full[tile]), units[tile]++ & 1, failed);
+        const uint32_t last_tile = u.rt * ROWS + TILE < q.group * u.count ? 1 : 0;
+        const int n = (u.last - u.first) << last_tile, ahead = min(last_tile ? BUFFERS : 2, n);
+        auto scores = [&](bool new_query) {
+          if (sc.tile == 0) wait(bar_k + 8 * sc.stage, sc.stage_phase, failed);
+          if (new_query) {
+            wait(bar_q + 8 * sc.tile, q_phase[0] ^ (sc.tile ? q_phase[1] ^ q_phase[0] : 0), failed);
+            if (sc.tile) q_phase[1] ^= 1;
+            else q_phase[0] ^= 1;
+          }
           fence_after();
-          const uint64_t a = q_desc + (uint64_t)tile * (sizeof(sm.q[0]) >> 4), b = k_desc + (uint64_t)st * (sizeof(sm.k[0]) >> 4);
+          const uint64_t a = q_desc + sc.tile * (uint32_t)(sizeof(sm.q[0]) >> 4), b = k_desc + sc.stage * (uint32_t)(sizeof(sm.k[0]) >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {  // 32 bytes further in the block, then the next block
             constexpr int BLOCK = TILE * 128 >> 4;
-            mma_ss(leader, tmem + buf * KT, a + (k / 4) * BLOCK + (k % 4) * 2, b + (k / 4) * BLOCK + (k % 4) * 2, i_s, k > 0);
+            mma_ss(leader, tmem + sc.buf * KT, a + (k / 4) * BLOCK + (k % 4) * 2, b + (k / 4) * BLOCK + (k % 4) * 2, i_s, k > 0);
           }
-          commit(leader, smem_addr(&sm.s_full[buf]));
-          if (tile == halves - 1) commit(leader, smem_addr(&sm.k_empty[st]));
+          commit(leader, bar_s + 8 * sc.buf);
+          if (sc.tile == last_tile) commit(leader, bar_ke + 8 * sc.stage);
+          sc.step(last_tile);
         };
-        for (int j = 0; j < ahead; ++j) scores(j);
+        for (int j = 0; j < ahead; ++j) scores(j <= (int)last_tile);
         for (int j = 0; j < n; ++j) {
-          const int i = it + (halves == 2 ? j >> 1 : j), tile = halves == 2 ? j & 1 : 0, st = i % KV_STAGES, buf = (jobs + j) % BUFFERS;
-          if (tile == 0) wait(smem_addr(&sm.v_full[st]), i / KV_STAGES & 1, failed);
-#pragma unroll 1
+          if (va.tile == 0) wait(bar_v + 8 * va.stage, va.stage_phase, failed);
+          const uint32_t p = tmem + va.buf * KT, o = tmem + O_AT + va.tile * D;
+          const uint64_t b = v_desc + va.stage * (uint32_t)(sizeof(sm.v[0]) >> 4);
+#pragma unroll
           for (int h = 0; h < 2; ++h) {
-            wait(smem_addr(&sm.p_full[buf][h]), (jobs + j) / BUFFERS & 1, failed);
+            wait(bar_p + 16 * va.buf + 8 * h, va.buf_phase, failed);
             fence_after();
-            const uint32_t p = tmem + buf * KT + h * HALF;
-            const uint64_t b = v_desc + (uint64_t)st * (sizeof(sm.v[0]) >> 4) + h * (HALF * 128 >> 4);
 #pragma unroll
             for (int k = 0; k < HALF / 16; ++k)
-              mma_ts(leader, tmem + O_AT + tile * D, p + 8 * k, b + k * (2048 >> 4), i_o, k > 0 || h > 0 || j >= halves);
-            commit(leader, smem_addr(&sm.o_full[tile][h]));
+              mma_ts(leader, o, p + h * HALF + 8 * k, b + h * (HALF * 128 >> 4) + k * (2048 >> 4), i_o, k > 0 || h > 0 || j > (int)last_tile);
+            commit(leader, bar_o + 16 * va.tile + 8 * h);
           }
-          if (tile == halves - 1) commit(leader, smem_addr(&sm.v_empty[st]));
-          if (j + ahead < n) scores(j + ahead);
+          if (va.tile == last_tile) commit(leader, bar_ve + 8 * va.stage);
+          va.step(last_tile);
+          if (j + ahead < n) scores(false);
         }
-        it += u.last - u.first;
-        jobs += n;
       }
     }
     __syncwarp();
