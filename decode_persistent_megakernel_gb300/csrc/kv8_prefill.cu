@@ -7,8 +7,8 @@
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a thread to a row: it rotates and scales the row's query into
 //                   shared memory, then for each 128 keys takes their scores from tensor memory into registers, and
 //                   writes the weights back over them in fp16, the left operand of the second product
-//   4 or 7 warps    widen the codes of K and V to fp16 in the operands' swizzled layouts, two tiles ahead
-//   the next warp   issues tcgen05.mma (one of its lanes): scores = Q K^T (both from shared memory), outputs += P V (P from
+//   warps 8-11      widen the codes of K and V to fp16 in the operands' swizzled layouts, two tiles ahead
+//   warp 12         issues tcgen05.mma (one of its lanes): scores = Q K^T (both from shared memory), outputs += P V (P from
 //                    tensor memory), the two tiles in turn, so that one's softmax runs under the other's products
 // Tensor memory: two (three at 64 dimensions) 128-column score buffers and two D-column outputs. Products are issued
 // by one warp and run in order, so new scores may follow the product that read the weights lying in their place.
@@ -36,11 +36,10 @@ static_assert(TILE == KT, "blocks of Q and K are alike");
 constexpr int WARP_WIDEN = 8;      // first warp of the widening role; before it the softmax, after it the products
 template <int D>
 struct Roles {
-  static constexpr int WIDEN = D == 64 ? 4 : 7, MMA = WARP_WIDEN + WIDEN;
+  static constexpr int WIDEN = 4, MMA = WARP_WIDEN + WIDEN, NT = (MMA + 1) * 32;
   static constexpr int BUFFERS = D == 64 ? 3 : 2;       // of 128 x 128 scores in tensor memory, beside two outputs of D columns
   static constexpr int ANGLES = D == 64 ? 4096 : 1472;  // of a tile: all of 128 tokens, or of 23 (or 8 at a time)
 };
-constexpr int NT = 512;
 constexpr int KV_STAGES = 2, SCALE_SLOTS = 4;
 constexpr int SHIFT = 5;           // of the weights
 constexpr float GROW = 8.f;        // a maximum may lag behind by 2^8
@@ -258,7 +257,8 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 }
 
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(NT, 1) prefill_kernel(const __grid_constant__ AttnParams q) {
+__global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_constant__ AttnParams q) {
+  constexpr int NT = Roles<D>::NT;
   constexpr int BUFFERS = Roles<D>::BUFFERS, O_AT = BUFFERS * KT;
   constexpr int WARP_MMA = Roles<D>::MMA, NT_WIDEN = Roles<D>::WIDEN * 32;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -726,7 +726,7 @@ cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
   static_assert(sizeof(Smem<D>) + (MAX_SEQS + 1) * 8 <= 227 * 1024, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<q.grid, NT, smem, st>>>(q);
+  kernel<<<q.grid, Roles<D>::NT, smem, st>>>(q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units), 8);
