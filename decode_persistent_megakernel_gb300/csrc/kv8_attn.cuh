@@ -49,10 +49,23 @@ __device__ __forceinline__ int seq_of(const I* prefix, int n, I x) {
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+// Waits for a phase of an mbarrier for a while: the hardware suspends the thread meanwhile, where polling
+// would take issue slots from the warps that compute.
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_sleep(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity))
+  while (!mbar_sleep(bar, parity))
     if ((long long)(globaltimer() - t0) > WAIT_NS) return false;
   return true;
 }

@@ -233,9 +233,9 @@ __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::
 
 // A wait that gives up at once when another role has: every role then runs through its loops without waiting.
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int* failed) {
-  if (mbar_try_wait(bar, parity)) return;
+  if (mbar_sleep(bar, parity)) return;
   const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!mbar_sleep(bar, parity)) {
     if (*failed) return;
     if ((long long)(globaltimer() - t0) > WAIT_NS) {
       *failed = 1;

@@ -3,14 +3,15 @@
 //   logp[t] = x_t - m - log S0,   H = log S0 - S1 / S0,   S0 = sum e^(x - m),   S1 = sum (x - m) e^(x - m)
 //
 // A row is read from memory once: a cluster of up to 8 CTAs takes it in slices, each slice lands in shared
-// memory by one bulk copy, and the maximum, the two sums and the alternatives are three walks over it there.
+// memory by bulk copies that a first walk follows (each thread's maximum and sums); a second walk over shared
+// memory finds the alternatives.
 // The slices' (m, S0, S1) and sorted alternatives meet in the first CTA's shared memory. Bound by HBM for
 // many rows, by latency for one.
 //
-// Alternatives: the slice's values fall into 64 groups (four threads each); the k-th largest of the groups'
-// maxima is a floor that at least k values reach, and for k <= 32 few others do. The values at or above it
-// are listed and ranked by counting, on (value, lower id first) as one 64-bit key, so that the order is
-// exact and independent of timing. A list that overflows falls back to k maxima one after another.
+// Alternatives: the slice's values fall to 32 groups of threads; the k-th largest of the groups' maxima is a floor
+// that at least k values reach, and few others do (31 on average for k = 20). The values at or above it are listed
+// and ranked by counting, on (value, lower id first) as one 64-bit key, so that the order is exact and
+// independent of timing. A list that overflows falls back to k maxima one after another.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,8 +29,12 @@ namespace cg = cooperative_groups;
 namespace tinfer {
 namespace logprobs {
 
-constexpr int NT = 256, NWARPS = NT / 32;
-constexpr int MAX_K = 32, MAX_CLUSTER = 8, GROUPS = 64;
+constexpr int NT = 512, NWARPS = NT / 32;
+constexpr int MAX_K = 32, MAX_CLUSTER = 8;
+constexpr int GROUPS = 32;             // of threads, whose maxima give the alternatives' floor: one to a lane
+static_assert(MAX_CLUSTER * MAX_K <= NT, "a thread for every alternative of the slices");
+static_assert(MAX_K <= GROUPS, "a floor for every k");
+constexpr int CHUNKS = 4;             // copies of a slice: the first are walked while the last are on their way
 constexpr int LIST = 512;             // listed candidates of a slice, at most
 constexpr int MAX_VOCAB = 1 << 18;    // 8 slices of 128 KiB of fp32
 constexpr float LOG2E = 1.4426950408889634f;
@@ -76,6 +81,20 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&x)[8], const __nv
   }
 }
 
+// Waits for a phase of an mbarrier for a while: the hardware suspends the thread meanwhile, where polling
+// would take issue slots from the warps that compute.
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -107,10 +126,9 @@ template <typename T>
 __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Params q) {
   constexpr int N = 16 / sizeof(T);  // elements of a word
   extern __shared__ __align__(128) unsigned char buf[];
-  __shared__ alignas(8) unsigned long long bar;
-  __shared__ float red[3][NWARPS];
+  __shared__ alignas(8) unsigned long long bar[CHUNKS];
+  __shared__ Part red[NWARPS];
   __shared__ float group_top[GROUPS];
-  __shared__ float floor_s;
   __shared__ int listed;
   __shared__ unsigned long long list[LIST];
   __shared__ unsigned long long best[MAX_K], warp_best[NWARPS];
@@ -132,14 +150,21 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Pa
   const int words = len ? (mis + len + N - 1) / N : 0;
   T* s = reinterpret_cast<T*>(buf);                   // slice element i is s[mis + i]
   const int w0 = mis ? 1 : 0, w1 = (mis + len) / N;   // whole words
+  const int per_chunk = (words + CHUNKS * NT - 1) / (CHUNKS * NT) * NT;  // words of a chunk, whole turns of the CTA
   if (tid == 0) {
-    mbar_init(smem_addr(&bar), 1);
+    for (int c = 0; c < CHUNKS; ++c) mbar_init(smem_addr(&bar[c]), 1);
     mbar_fence_init();
     listed = 0;
-    if (w1 > w0) {
-      mbar_arrive_expect_tx(smem_addr(&bar), (uint32_t)(w1 - w0) * 16u);
-      bulk_g2s(smem_addr(buf) + 16u * w0, reinterpret_cast<const void*>((from & ~(uintptr_t)15) + 16 * w0),
-               (uint32_t)(w1 - w0) * 16u, smem_addr(&bar), policy_evict_first());
+    const uint64_t policy = policy_evict_first();
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int f = max(w0, c * per_chunk), l = min(w1, (c + 1) * per_chunk);
+      if (l > f) {
+        mbar_arrive_expect_tx(smem_addr(&bar[c]), (uint32_t)(l - f) * 16u);
+        bulk_g2s(smem_addr(buf) + 16u * f, reinterpret_cast<const void*>((from & ~(uintptr_t)15) + 16 * (uintptr_t)f),
+                 (uint32_t)(l - f) * 16u, smem_addr(&bar[c]), policy);
+      } else {
+        mbar_arrive(smem_addr(&bar[c]));
+      }
     }
   }
   const T masked = (T)(-INFINITY);
@@ -152,86 +177,83 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Pa
   }
   float target_x = 0.f;
   bool target_in = false;
-  if (rank == 0 && tid == 0 && q.logp) {
-    const int t = q.targets[row];
-    target_in = t >= 0 && t < q.vocab;
-    if (target_in) target_x = value(x[t]);
-  }
+  const bool scores = rank == 0 && tid == 0 && q.logp;
+  const int target = scores ? q.targets[row] : -1;  // (on its way across the barrier)
   __syncthreads();
-  bool late = false;  // a copy that never arrived makes the row NaN
-  if (w1 > w0) {
-    const uint64_t t0 = globaltimer();
-    while (!late && !mbar_try_wait(smem_addr(&bar), 0)) late = (long long)(globaltimer() - t0) > WAIT_NS;
+  if (scores && target >= 0 && target < q.vocab) {
+    target_in = true;
+    target_x = value(x[target]);
   }
-
-  // ---- first walk: maxima
+  // ---- first walk, chunk by chunk as they arrive: every thread's own maximum and its sums relative to it
   const uint4* sw = reinterpret_cast<const uint4*>(buf);
-  float top = -INFINITY;
-  for (int w = tid; w < words; w += NT) {
-    float v[N];
-    unpack(sw[w], v, x);
+  bool late = false;  // a copy that never arrived makes the row NaN
+  Part p{-INFINITY, 0.f, 0.f};
+  for (int c = 0; c < CHUNKS; ++c) {
+    if (!late && !mbar_sleep(smem_addr(&bar[c]), 0)) {
+      const uint64_t t0 = globaltimer();
+      while (!late && !mbar_sleep(smem_addr(&bar[c]), 0)) late = (long long)(globaltimer() - t0) > WAIT_NS;
+    }
+    const int end = min(words, (c + 1) * per_chunk);
+    for (int w = c * per_chunk + tid; w < end; w += 2 * NT) {  // two words at a time
+      float v[2][N];
+      unpack(sw[w], v[0], x);
+      if (w + NT < end) {
+        unpack(sw[w + NT], v[1], x);
+      } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) top = fmaxf(top, v[i]);
+        for (int i = 0; i < N; ++i) v[1][i] = -INFINITY;
+      }
+      float top = fmaxf(v[0][0], v[1][0]);
+#pragma unroll
+      for (int i = 1; i < N; ++i) top = fmaxf(top, fmaxf(v[0][i], v[1][i]));
+      if (top > p.m) {
+        const float d = p.m == -INFINITY ? 0.f : fmaxf(p.m - top, -1e30f), f = exp2_fast(d * LOG2E);
+        p = Part{top, p.s0 * f, (p.s1 + p.s0 * d) * f};
+      }
+      const float m = p.m == -INFINITY ? 0.f : p.m;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float z = v[h][i] - m, e = exp2_fast(z * LOG2E);
+          p.s0 += e;
+          p.s1 = fmaf(e, fmaxf(z, -1e30f), p.s1);  // a masked token adds 0 * -1e30
+        }
+    }
   }
-  const float mine = top;
-  float quad = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-  quad = fmaxf(quad, __shfl_xor_sync(~0u, quad, 2));
-  if ((tid & 3) == 0) group_top[tid >> 2] = quad;
-  top = quad;
+  if (late) p.s0 = __uint_as_float(0x7FC00000u);
+  const float mine = p.m;
+  auto other = [&](int o) { return Part{__shfl_xor_sync(~0u, p.m, o), __shfl_xor_sync(~0u, p.s0, o), __shfl_xor_sync(~0u, p.s1, o)}; };
+  float top = mine;  // of this thread's group
 #pragma unroll
-  for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  if (lane == 0) red[0][warp] = top;
+  for (int o = 1; o < NT / GROUPS; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  if (tid % (NT / GROUPS) == 0) group_top[tid / (NT / GROUPS)] = top;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) p = join(p, other(o));
+  if (lane == 0) red[warp] = p;
   __syncthreads();
-  Part p;
-  p.m = red[0][0];
+  if (warp == 0) {
+    p = lane < NWARPS ? red[lane] : Part{-INFINITY, 0.f, 0.f};
 #pragma unroll
-  for (int w = 1; w < NWARPS; ++w) p.m = fmaxf(p.m, red[0][w]);
-
-  // the floor of the alternatives: the k-th largest of the groups' maxima, ties by the group
-  if (q.k && tid < GROUPS) {
-    const float g = group_top[tid];
+    for (int o = 1; o < NWARPS; o *= 2) p = join(p, other(o));
+  }
+  // the floor of the alternatives: the k-th largest of the groups' maxima (ties by the group), found by every warp
+  float floor_x = -INFINITY;
+  if (q.k) {
+    const float g = group_top[lane];
     int above = 0;
-    for (int i = 0; i < GROUPS; ++i) {
-      const float y = group_top[i];
-      above += y > g || (y == g && i < tid);
+#pragma unroll
+    for (int o = 1; o < GROUPS; ++o) {
+      const float y = __shfl_xor_sync(~0u, g, o);
+      above += y > g || (y == g && (lane ^ o) < lane);
     }
-    if (above == q.k - 1) floor_s = g;
-  }
-  // ---- second walk: the sums
-  float s0 = late ? __uint_as_float(0x7FC00000u) : 0.f, s1 = 0.f;
-  const float m = p.m == -INFINITY ? 0.f : p.m;
-  for (int w = tid; w < words; w += NT) {
-    float v[N];
-    unpack(sw[w], v, x);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float z = v[i] - m, e = exp2_fast(z * LOG2E);
-      s0 += e;
-      s1 = fmaf(e, fmaxf(z, -1e30f), s1);  // a masked token adds 0 * -1e30
-    }
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    s0 += __shfl_xor_sync(~0u, s0, o);
-    s1 += __shfl_xor_sync(~0u, s1, o);
-  }
-  if (lane == 0) {
-    red[1][warp] = s0;
-    red[2][warp] = s1;
-  }
-  __syncthreads();
-  p.s0 = p.s1 = 0.f;
-#pragma unroll
-  for (int w = 0; w < NWARPS; ++w) {
-    p.s0 += red[1][w];
-    p.s1 += red[2][w];
+    floor_x = __shfl_sync(~0u, g, __ffs(__ballot_sync(~0u, above == q.k - 1)) - 1);
   }
   cluster.barrier_wait(std::move(started));
   if (tid == 0) cluster.map_shared_rank(parts, 0)[rank] = p;
 
-  // ---- third walk: the values at or above the floor, ranked
+  // ---- second walk: the values at or above the floor, ranked
   if (q.k) {
-    const float floor_x = floor_s;
     if (mine >= floor_x && mine > -INFINITY)
       for (int w = tid; w < words; w += NT) {
         float v[N];
@@ -249,6 +271,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Pa
       for (int c = tid; c < n; c += NT) {
         const unsigned long long key = list[c];
         int above = 0;
+#pragma unroll 8
         for (int i = 0; i < n; ++i) above += list[i] > key;
         if (above < q.k) best[above] = key;
       }
@@ -298,12 +321,12 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Pa
   int* ids = q.top_ids + (size_t)row * q.k;
   float* lps = q.top_logp + (size_t)row * q.k;
   const int n = size * q.k;
-  int found = 0;
-  for (int i = 0; i < n; ++i) found += tops[i] != 0;
+  const int found = __syncthreads_count(tid < n && tops[tid] != 0);
   for (int c = tid; c < n; c += NT) {
     const unsigned long long key = tops[c];
     if (!key || bad) continue;
     int above = 0;
+#pragma unroll 8
     for (int i = 0; i < n; ++i) above += tops[i] > key;
     if (above < q.k) {
       ids[above] = id_of(key);
