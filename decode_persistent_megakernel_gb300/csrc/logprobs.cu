@@ -2,16 +2,17 @@
 //
 //   logp[t] = x_t - m - log S0,   H = log S0 - S1 / S0,   S0 = sum e^(x - m),   S1 = sum (x - m) e^(x - m)
 //
-// A row is read from memory once: a cluster of up to 8 CTAs takes it in slices, each slice lands in shared
-// memory by bulk copies that a first walk follows (each thread's maximum and sums); a second walk over shared
-// memory finds the alternatives.
-// The slices' (m, S0, S1) and sorted alternatives meet in the first CTA's shared memory. Bound by HBM for
-// many rows, by latency for one.
+// A row is one CTA's, or, where the rows are too few to fill the GPU, a cluster's of up to 8 CTAs in slices. Threads read
+// it in 16-byte words, several in flight, and keep their own maximum and sums relative to it; they meet once at
+// the end, the slices in the first CTA's shared memory. Bound by HBM for many rows, by latency for one. (Slices staged in
+// shared memory by bulk copies took 300 to 345 us for 2047 rows of 128256 fp32 logits: with 64 KiB of a row to a CTA, the
+// joins at its end are most of its life.)
 //
-// Alternatives: the slice's values fall to 32 groups of threads; the k-th largest of the groups' maxima is a floor
-// that at least k values reach, and few others do (31 on average for k = 20). The values at or above it are listed
-// and ranked by counting, on (value, lower id first) as one 64-bit key, so that the order is exact and
-// independent of timing. A list that overflows falls back to k maxima one after another.
+// Alternatives: a slice's values fall to 32 groups of threads; the k-th largest of the groups' maxima is a floor
+// that at least k values reach, and few others do (31 on average for k = 20). Only threads whose maximum reaches it
+// have any: their warp reads their words again. Those values are listed and ranked by counting, on (value, lower id
+// first) as one 64-bit key, so that the order is exact and independent of timing. A list that overflows falls back
+// to k maxima one after another.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -21,7 +22,6 @@
 #include <cstdint>
 #include <utility>
 
-#include "ptx.cuh"
 #include "tinfer.h"
 
 namespace cg = cooperative_groups;
@@ -34,11 +34,10 @@ constexpr int MAX_K = 32, MAX_CLUSTER = 8;
 constexpr int GROUPS = 32;             // of threads, whose maxima give the alternatives' floor: one to a lane
 static_assert(MAX_CLUSTER * MAX_K <= NT, "a thread for every alternative of the slices");
 static_assert(MAX_K <= GROUPS, "a floor for every k");
-constexpr int CHUNKS = 4;             // copies of a slice: the first are walked while the last are on their way
+constexpr int AHEAD = 4;              // words of a thread in flight
 constexpr int LIST = 512;             // listed candidates of a slice, at most
-constexpr int MAX_VOCAB = 1 << 18;    // 8 slices of 128 KiB of fp32
+constexpr int MAX_VOCAB = 1 << 18;
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr long long WAIT_NS = 200LL * 1000 * 1000;
 
 struct Params {
   const void* logits;
@@ -54,6 +53,11 @@ struct Params {
 struct Part {
   float m, s0, s1;
 };
+
+// 32 bits of logits of minus infinity.
+__device__ __forceinline__ uint32_t minus_infinity(const float*) { return 0xFF800000u; }
+__device__ __forceinline__ uint32_t minus_infinity(const __half*) { return 0xFC00FC00u; }
+__device__ __forceinline__ uint32_t minus_infinity(const __nv_bfloat16*) { return 0xFF80FF80u; }
 
 __device__ __forceinline__ float value(float x) { return x; }
 __device__ __forceinline__ float value(__half x) { return __half2float(x); }
@@ -79,20 +83,6 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&x)[8], const __nv
     x[2 * i] = __uint_as_float(u[i] << 16);
     x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
-}
-
-// Waits for a phase of an mbarrier for a while: the hardware suspends the thread meanwhile, where polling
-// would take issue slots from the warps that compute.
-__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -123,12 +113,10 @@ __device__ __forceinline__ Part join(const Part& a, const Part& b) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Params q) {
+__global__ void __launch_bounds__(NT, 3) logprobs_kernel(const __grid_constant__ Params q) {
   constexpr int N = 16 / sizeof(T);  // elements of a word
-  extern __shared__ __align__(128) unsigned char buf[];
-  __shared__ alignas(8) unsigned long long bar[CHUNKS];
   __shared__ Part red[NWARPS];
-  __shared__ float group_top[GROUPS];
+  __shared__ float group_top[GROUPS], floor_s;
   __shared__ int listed;
   __shared__ unsigned long long list[LIST];
   __shared__ unsigned long long best[MAX_K], warp_best[NWARPS];
@@ -143,85 +131,64 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Pa
   const T* x = static_cast<const T*>(q.logits) + row * q.row_stride;
   const int a = min(rank * q.slice, q.vocab), len = min(q.slice, q.vocab - a);
 
-  // the slice as it lies in memory, from the 16-byte word of its first element to that of its last: whole
-  // words by one bulk copy, the ends by ordinary loads, what is beside the row set to -infinity
+  // the slice as 16-byte words, from that of its first element to that of its last; of the words at its ends only the
+  // slice's own elements are read, the others stand for masked tokens
   const uintptr_t from = reinterpret_cast<uintptr_t>(x + a);
   const int mis = (int)(from & 15) / (int)sizeof(T);  // elements before the slice in its first word
   const int words = len ? (mis + len + N - 1) / N : 0;
-  T* s = reinterpret_cast<T*>(buf);                   // slice element i is s[mis + i]
-  const int w0 = mis ? 1 : 0, w1 = (mis + len) / N;   // whole words
-  const int per_chunk = (words + CHUNKS * NT - 1) / (CHUNKS * NT) * NT;  // words of a chunk, whole turns of the CTA
-  if (tid == 0) {
-    for (int c = 0; c < CHUNKS; ++c) mbar_init(smem_addr(&bar[c]), 1);
-    mbar_fence_init();
-    listed = 0;
-    const uint64_t policy = policy_evict_first();
-    for (int c = 0; c < CHUNKS; ++c) {
-      const int f = max(w0, c * per_chunk), l = min(w1, (c + 1) * per_chunk);
-      if (l > f) {
-        mbar_arrive_expect_tx(smem_addr(&bar[c]), (uint32_t)(l - f) * 16u);
-        bulk_g2s(smem_addr(buf) + 16u * f, reinterpret_cast<const void*>((from & ~(uintptr_t)15) + 16 * (uintptr_t)f),
-                 (uint32_t)(l - f) * 16u, smem_addr(&bar[c]), policy);
-      } else {
-        mbar_arrive(smem_addr(&bar[c]));
-      }
+  const uint4* base = reinterpret_cast<const uint4*>(from & ~(uintptr_t)15);
+  auto word = [&](int w) {
+    if (w * N >= mis && (w + 1) * N <= mis + len) return __ldcs(base + w);
+    union {
+      uint4 u;
+      T e[N];
+    } y;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = w * N + i - mis;
+      y.e[i] = at >= 0 && at < len ? x[a + at] : (T)(-INFINITY);
     }
-  }
-  const T masked = (T)(-INFINITY);
-  if (tid < N && words) {
-    if (w0 == 1) s[tid] = tid >= mis && tid - mis < len ? x[a + tid - mis] : masked;
-    if (w1 < words && (w1 > 0 || w0 == 0)) {
-      const int e = w1 * N + tid;
-      s[e] = e - mis < len ? x[a + e - mis] : masked;
-    }
-  }
-  float target_x = 0.f;
-  bool target_in = false;
+    return y.u;
+  };
+  const uint32_t minus = minus_infinity(x);
+  const uint4 none = make_uint4(minus, minus, minus, minus);
+  if (tid == 0) listed = 0;
   const bool scores = rank == 0 && tid == 0 && q.logp;
-  const int target = scores ? q.targets[row] : -1;  // (on its way across the barrier)
-  __syncthreads();
-  if (scores && target >= 0 && target < q.vocab) {
-    target_in = true;
-    target_x = value(x[target]);
-  }
-  // ---- first walk, chunk by chunk as they arrive: every thread's own maximum and its sums relative to it
-  const uint4* sw = reinterpret_cast<const uint4*>(buf);
-  bool late = false;  // a copy that never arrived makes the row NaN
+  const int target = scores ? q.targets[row] : -1;
+
+  // ---- the walk: every thread's own maximum and its sums relative to it
   Part p{-INFINITY, 0.f, 0.f};
-  for (int c = 0; c < CHUNKS; ++c) {
-    if (!late && !mbar_sleep(smem_addr(&bar[c]), 0)) {
-      const uint64_t t0 = globaltimer();
-      while (!late && !mbar_sleep(smem_addr(&bar[c]), 0)) late = (long long)(globaltimer() - t0) > WAIT_NS;
+  for (int w = tid; w < words; w += AHEAD * NT) {
+    uint4 y[AHEAD];
+#pragma unroll
+    for (int h = 0; h < AHEAD; ++h) y[h] = w + h * NT < words ? word(w + h * NT) : none;
+    float top = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < AHEAD; ++h) {
+      float v[N];
+      unpack(y[h], v, x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) top = fmaxf(top, v[i]);
     }
-    const int end = min(words, (c + 1) * per_chunk);
-    for (int w = c * per_chunk + tid; w < end; w += 2 * NT) {  // two words at a time
-      float v[2][N];
-      unpack(sw[w], v[0], x);
-      if (w + NT < end) {
-        unpack(sw[w + NT], v[1], x);
-      } else {
+    if (top > p.m) {
+      const float d = p.m == -INFINITY ? 0.f : fmaxf(p.m - top, -1e30f), f = exp2_fast(d * LOG2E);
+      p = Part{top, p.s0 * f, (p.s1 + p.s0 * d) * f};
+    }
+    const float m = p.m == -INFINITY ? 0.f : p.m;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[1][i] = -INFINITY;
+    for (int h = 0; h < AHEAD; ++h) {
+      float v[N];
+      unpack(y[h], v, x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float z = v[i] - m, e = exp2_fast(z * LOG2E);
+        p.s0 += e;
+        p.s1 = fmaf(e, fmaxf(z, -1e30f), p.s1);  // a masked token adds 0 * -1e30
       }
-      float top = fmaxf(v[0][0], v[1][0]);
-#pragma unroll
-      for (int i = 1; i < N; ++i) top = fmaxf(top, fmaxf(v[0][i], v[1][i]));
-      if (top > p.m) {
-        const float d = p.m == -INFINITY ? 0.f : fmaxf(p.m - top, -1e30f), f = exp2_fast(d * LOG2E);
-        p = Part{top, p.s0 * f, (p.s1 + p.s0 * d) * f};
-      }
-      const float m = p.m == -INFINITY ? 0.f : p.m;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float z = v[h][i] - m, e = exp2_fast(z * LOG2E);
-          p.s0 += e;
-          p.s1 = fmaf(e, fmaxf(z, -1e30f), p.s1);  // a masked token adds 0 * -1e30
-        }
     }
   }
-  if (late) p.s0 = __uint_as_float(0x7FC00000u);
+  const bool target_in = scores && target >= 0 && target < q.vocab;
+  const float target_x = target_in ? value(x[target]) : 0.f;
   const float mine = p.m;
   auto other = [&](int o) { return Part{__shfl_xor_sync(~0u, p.m, o), __shfl_xor_sync(~0u, p.s0, o), __shfl_xor_sync(~0u, p.s1, o)}; };
   float top = mine;  // of this thread's group
@@ -236,10 +203,8 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Pa
     p = lane < NWARPS ? red[lane] : Part{-INFINITY, 0.f, 0.f};
 #pragma unroll
     for (int o = 1; o < NWARPS; o *= 2) p = join(p, other(o));
-  }
-  // the floor of the alternatives: the k-th largest of the groups' maxima (ties by the group), found by every warp
-  float floor_x = -INFINITY;
-  if (q.k) {
+  } else if (warp == 1 && q.k) {
+    // the floor of the alternatives: the k-th largest of the groups' maxima, ties by the group
     const float g = group_top[lane];
     int above = 0;
 #pragma unroll
@@ -247,23 +212,29 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Pa
       const float y = __shfl_xor_sync(~0u, g, o);
       above += y > g || (y == g && (lane ^ o) < lane);
     }
-    floor_x = __shfl_sync(~0u, g, __ffs(__ballot_sync(~0u, above == q.k - 1)) - 1);
+    if (above == q.k - 1) floor_s = g;
   }
+  if (q.k) __syncthreads();
   cluster.barrier_wait(std::move(started));
   if (tid == 0) cluster.map_shared_rank(parts, 0)[rank] = p;
 
-  // ---- second walk: the values at or above the floor, ranked
+  // ---- the values at or above the floor, ranked
   if (q.k) {
-    if (mine >= floor_x && mine > -INFINITY)
-      for (int w = tid; w < words; w += NT) {
+    const float floor_x = floor_s;
+    unsigned have = __ballot_sync(~0u, mine >= floor_x && mine > -INFINITY);
+    for (; have; have &= have - 1) {  // the words of a thread that has some, a word to a lane
+      const int owner = warp * 32 + __ffs(have) - 1;
+      for (int w = owner + lane * NT; w < words; w += 32 * NT) {
         float v[N];
-        unpack(sw[w], v, x);
+        unpack(word(w), v, x);
+#pragma unroll
         for (int i = 0; i < N; ++i)
           if (v[i] >= floor_x && v[i] > -INFINITY) {
             const int n = atomicAdd(&listed, 1);
             if (n < LIST) list[n] = key_of(v[i], a + w * N + i - mis);
           }
       }
+    }
     if (tid < MAX_K) best[tid] = 0;
     __syncthreads();
     const int n = listed;
@@ -281,7 +252,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Pa
         unsigned long long b = 0;
         for (int w = tid; w < words; w += NT) {
           float v[N];
-          unpack(sw[w], v, x);
+          unpack(word(w), v, x);
           for (int i = 0; i < N; ++i) {
             const unsigned long long key = v[i] > -INFINITY ? key_of(v[i], a + w * N + i - mis) : 0;
             if (key < last && key > b) b = key;
@@ -341,13 +312,9 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const __grid_constant__ Pa
 
 template <typename T>
 cudaError_t launch(const Params& q, int cluster, cudaStream_t st) {
-  const size_t smem = ((size_t)q.slice * sizeof(T) + 15) / 16 * 16 + 32;
-  cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(q.rows * cluster));
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -376,10 +343,10 @@ extern "C" tinfer_status tinfer_op_logprobs(int rows, int vocab, int dtype, cons
                         (const void*)top_logp_dev})
     if (reinterpret_cast<uintptr_t>(p) & 3) return TINFER_ERR_INVALID_ARG;
   if (vocab > logprobs::MAX_VOCAB || rows > (1 << 27)) return TINFER_ERR_UNSUPPORTED;
-  // slices of 32 to 64 KiB keep three or more CTAs on an SM; few rows are cut finer to spread over more SMs
+  // a CTA to a row, and for few rows as many more as leave every thread a word or two and every SM a CTA
   const long long bytes = (long long)vocab * size;
   int cluster = 1;
-  while (cluster < logprobs::MAX_CLUSTER && bytes / cluster > (rows * cluster < 128 ? 8 : 48) * 1024) cluster *= 2;
+  while (cluster < logprobs::MAX_CLUSTER && (long long)rows * cluster < 304 && bytes / cluster > 16 * 1024) cluster *= 2;
   logprobs::Params q{logits_dev, row_stride, targets_dev, logp_dev, entropy_dev, top_ids_dev, top_logp_dev,
                      rows, vocab, top_k, ((vocab + cluster - 1) / cluster + 7) / 8 * 8};
   cudaStream_t st = (cudaStream_t)stream;
