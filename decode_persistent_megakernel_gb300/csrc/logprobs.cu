@@ -10,7 +10,7 @@
 //
 // Alternatives: a slice's values fall to 32 groups of threads; the k-th largest of the groups' maxima is a floor
 // that at least k values reach, and few others do (31 on average for k = 20). Only threads whose maximum reaches it
-// have any: their warp reads their words again. Those values are listed and ranked by counting, on (value, lower id
+// have any: their words are dealt out and read again. Those values are listed and ranked by counting, on (value, lower id
 // first) as one 64-bit key, so that the order is exact and independent of timing. A list that overflows falls back
 // to k maxima one after another.
 #include <cooperative_groups.h>
@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(NT, 3) logprobs_kernel(const __grid_constant__
   constexpr int N = 16 / sizeof(T);  // elements of a word
   __shared__ Part red[NWARPS];
   __shared__ float group_top[GROUPS], floor_s;
-  __shared__ int listed;
+  __shared__ int listed, owners;
+  __shared__ uint16_t owner[NT];
   __shared__ unsigned long long list[LIST];
   __shared__ unsigned long long best[MAX_K], warp_best[NWARPS];
   __shared__ Part parts[MAX_CLUSTER];
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(NT, 3) logprobs_kernel(const __grid_constant__
   };
   const uint32_t minus = minus_infinity(x);
   const uint4 none = make_uint4(minus, minus, minus, minus);
-  if (tid == 0) listed = 0;
+  if (tid == 0) listed = owners = 0;
   const bool scores = rank == 0 && tid == 0 && q.logp;
   const int target = scores ? q.targets[row] : -1;
 
@@ -221,19 +222,20 @@ __global__ void __launch_bounds__(NT, 3) logprobs_kernel(const __grid_constant__
   // ---- the values at or above the floor, ranked
   if (q.k) {
     const float floor_x = floor_s;
-    unsigned have = __ballot_sync(~0u, mine >= floor_x && mine > -INFINITY);
-    for (; have; have &= have - 1) {  // the words of a thread that has some, a word to a lane
-      const int owner = warp * 32 + __ffs(have) - 1;
-      for (int w = owner + lane * NT; w < words; w += 32 * NT) {
-        float v[N];
-        unpack(word(w), v, x);
+    if (mine >= floor_x && mine > -INFINITY) owner[atomicAdd(&owners, 1)] = (uint16_t)tid;
+    __syncthreads();
+    const int turns = (words + NT - 1) / NT;  // words of a thread, at most
+    for (int item = tid; item < owners * turns; item += NT) {
+      const int w = owner[item / turns] + item % turns * NT;
+      if (w >= words) continue;
+      float v[N];
+      unpack(word(w), v, x);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (v[i] >= floor_x && v[i] > -INFINITY) {
-            const int n = atomicAdd(&listed, 1);
-            if (n < LIST) list[n] = key_of(v[i], a + w * N + i - mis);
-          }
-      }
+      for (int i = 0; i < N; ++i)
+        if (v[i] >= floor_x && v[i] > -INFINITY) {
+          const int n = atomicAdd(&listed, 1);
+          if (n < LIST) list[n] = key_of(v[i], a + w * N + i - mis);
+        }
     }
     if (tid < MAX_K) best[tid] = 0;
     __syncthreads();
@@ -343,10 +345,13 @@ extern "C" tinfer_status tinfer_op_logprobs(int rows, int vocab, int dtype, cons
                         (const void*)top_logp_dev})
     if (reinterpret_cast<uintptr_t>(p) & 3) return TINFER_ERR_INVALID_ARG;
   if (vocab > logprobs::MAX_VOCAB || rows > (1 << 27)) return TINFER_ERR_UNSUPPORTED;
-  // a CTA to a row, and for few rows as many more as leave every thread a word or two and every SM a CTA
+  // a CTA to a row, or for few rows as many more as run at once (three on an SM) and leave every thread a word or two
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return TINFER_ERR_CUDA;
   const long long bytes = (long long)vocab * size;
   int cluster = 1;
-  while (cluster < logprobs::MAX_CLUSTER && (long long)rows * cluster < 304 && bytes / cluster > 16 * 1024) cluster *= 2;
+  while (cluster < logprobs::MAX_CLUSTER && 2LL * rows * cluster <= 3 * sms && bytes / cluster > 16 * 1024) cluster *= 2;
   logprobs::Params q{logits_dev, row_stride, targets_dev, logp_dev, entropy_dev, top_ids_dev, top_logp_dev,
                      rows, vocab, top_k, ((vocab + cluster - 1) / cluster + 7) / 8 * 8};
   cudaStream_t st = (cudaStream_t)stream;
