@@ -453,13 +453,33 @@ class Engine:
 
 # ------------------------------------------------------------------ the 8-bit cache and token scores on tensors
 
+_DTYPES: dict = {}  # torch dtype -> TINFER_DTYPE_*
+
+
 def _dtype(t) -> int:
     """TINFER_DTYPE_* of a tensor (ValueError for the others)."""
-    import torch
-    d = {torch.float32: TINFER_DTYPE_F32, torch.float16: TINFER_DTYPE_F16, torch.bfloat16: TINFER_DTYPE_BF16}.get(t.dtype)
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: TINFER_DTYPE_F32, torch.float16: TINFER_DTYPE_F16, torch.bfloat16: TINFER_DTYPE_BF16})
+    d = _DTYPES.get(t.dtype)
     if d is None:
         raise ValueError(f"float32, float16 or bfloat16 is wanted, got {t.dtype}")
     return d
+
+
+def _call(what, fn, args, device, stream) -> None:
+    """Calls fn(*args, stream) with `device` current, on `stream` or torch's current one; raises on an error status.
+    The raw getters are what torch.cuda's own wrappers call: a step's small calls are a few microseconds on the GPU."""
+    import torch
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != TINFER_OK:
+        raise TinferError(rc, what)
 
 
 def _on(what: str, t, device, dtype=None, shape=None):
@@ -505,6 +525,7 @@ class Kv8Cache:
             if not t.is_contiguous():
                 raise ValueError(f"{what} is not contiguous")
         self.n_seqs, self.n_kv_heads, self.head_dim, self.max_ctx = n_seqs, n_kv_heads, head_dim, max_ctx
+        self._int32, self._uint8 = torch.int32, torch.uint8
         self.c = tinfer_kv8(fmt, n_seqs, n_kv_heads, head_dim, max_ctx, block, *(t.data_ptr() for t in buffers))
         need = self.workspace_bytes(n_kv_heads, 1)
         if need == 0:
@@ -525,31 +546,20 @@ class Kv8Cache:
             raise ValueError(f"{what}: the elements of a row are not contiguous")
         return tinfer_rows(t.data_ptr(), _dtype(t), st[0], st[1], st[2])
 
-    def _seqs(self, pos, counts, status):
-        import torch
-        for what, t, n in (("pos", pos, self.n_seqs), ("counts", counts, self.n_seqs), ("status", status, 1)):
-            if t is not None:
-                if t.dtype != torch.int32 or t.numel() != n or t.device != self.device or not t.is_contiguous():
-                    raise ValueError(f"{what}: a contiguous int32 tensor of {n} on {self.device} is wanted")
-
-    def _run(self, what, fn, args, status, stream):
-        import torch
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
-                rc = fn(*args, _ptr(status), _stream(stream))
-        else:
-            rc = fn(*args, _ptr(status), _stream(stream))
-        if rc != TINFER_OK:
-            raise TinferError(rc, what)
+    def _ints(self, what, t, n):
+        """Address of an int32 argument of n values (None: no argument)."""
+        if t is None:
+            return None
+        if t.dtype != self._int32 or t.numel() != n or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{what}: a contiguous int32 tensor of {n} on {self.device} is wanted")
+        return t.data_ptr()
 
     def append(self, k, v, pos, counts=None, rope_theta: float = 0.0, status=None, stream=None) -> None:
         """Quantises rows k and v into the cache at pos (keys rotated first; rope_theta 0: they already are)."""
         kr, vr = self._rows("k", k, self.n_kv_heads), self._rows("v", v, self.n_kv_heads, k.shape[1])
-        self._seqs(pos, counts, status)
-        self._run("tinfer_op_kv8_append", lib().tinfer_op_kv8_append,
-                  (self.c, kr, vr, k.shape[1], pos.data_ptr(), _ptr(counts), rope_theta), status, stream)
+        _call("tinfer_op_kv8_append", lib().tinfer_op_kv8_append,
+              (self.c, kr, vr, k.shape[1], self._ints("pos", pos, self.n_seqs), self._ints("counts", counts, self.n_seqs),
+               rope_theta, self._ints("status", status, 1)), self.device, stream)
 
     def read(self, n_tokens: int, pos, counts=None, out=None, dtype=None, status=None, stream=None):
         """Reads n_tokens tokens of each sequence from pos on back into rows (k, v): `out`, or new ones of dtype
@@ -559,17 +569,16 @@ class Kv8Cache:
             out = tuple(torch.zeros((self.n_seqs, n_tokens, self.n_kv_heads, self.head_dim),
                                     dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2))
         kr, vr = (self._rows(what, t, self.n_kv_heads, n_tokens) for what, t in zip(("k", "v"), out))
-        self._seqs(pos, counts, status)
-        self._run("tinfer_op_kv8_read", lib().tinfer_op_kv8_read,
-                  (self.c, n_tokens, pos.data_ptr(), _ptr(counts), kr, vr), status, stream)
+        _call("tinfer_op_kv8_read", lib().tinfer_op_kv8_read,
+              (self.c, n_tokens, self._ints("pos", pos, self.n_seqs), self._ints("counts", counts, self.n_seqs), kr, vr,
+               self._ints("status", status, 1)), self.device, stream)
         return out
 
     def workspace_bytes(self, n_heads: int | None = None, n_tokens: int = 1) -> int:
         return lib().tinfer_kv8_attention_workspace(self.c, n_heads or self.n_kv_heads, n_tokens)
 
     def _check_workspace(self, t):
-        import torch
-        if t.dtype != torch.uint8 or t.device != self.device or not t.is_contiguous():
+        if t.dtype != self._uint8 or t.device != self.device or not t.is_contiguous():
             raise ValueError("workspace: a contiguous uint8 tensor on the cache's device is wanted")
         return t
 
@@ -577,23 +586,19 @@ class Kv8Cache:
                   stream=None):
         """Attention of the query rows q over the cache: token i of sequence s attends to positions
         [0, pos[s] + i]. Returns `out` (rows like q; a new tensor, zero where a sequence has fewer tokens, when None)."""
-        import torch
         qr = self._rows("q", q)
         n_tokens, n_heads = q.shape[1], q.shape[2]
         if out is None:
-            out = torch.zeros(q.shape, dtype=q.dtype, device=self.device)
+            out = q.new_zeros(q.shape)
         orow = self._rows("out", out, n_heads, n_tokens)
-        self._seqs(pos, counts, status)
-        if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or lse.device != self.device
+        if lse is not None and (lse.dtype != self.k_scales.dtype or lse.shape != q.shape[:3] or lse.device != self.device
                                 or not lse.is_contiguous()):
             raise ValueError("lse: a contiguous float32 tensor [n_seqs, n_tokens, n_heads] is wanted")
-        if workspace is None:
-            workspace = self._workspace
-        else:
-            self._check_workspace(workspace)
-        self._run("tinfer_op_kv8_attention", lib().tinfer_op_kv8_attention,
-                  (self.c, n_heads, n_tokens, qr, pos.data_ptr(), _ptr(counts), rope_theta, orow, _ptr(lse),
-                   workspace.data_ptr(), workspace.numel()), status, stream)
+        workspace = self._workspace if workspace is None else self._check_workspace(workspace)
+        _call("tinfer_op_kv8_attention", lib().tinfer_op_kv8_attention,
+              (self.c, n_heads, n_tokens, qr, self._ints("pos", pos, self.n_seqs), self._ints("counts", counts, self.n_seqs),
+               rope_theta, orow, _ptr(lse), workspace.data_ptr(), workspace.numel(), self._ints("status", status, 1)),
+              self.device, stream)
         return out
 
 
@@ -613,9 +618,7 @@ def logprobs(logits, targets=None, top_k: int = 0, stream=None):
     entropy = torch.empty(rows, dtype=torch.float32, device=dev)
     ids = torch.empty((rows, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
     top = torch.empty((rows, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
-    with torch.cuda.device(dev):
-        rc = tinfer_op_logprobs(rows, vocab, _dtype(logits), logits, logits.stride(0) if rows > 1 else vocab, targets,
-                                top_k, logp, entropy, ids, top,
-                                torch.cuda.current_stream(dev) if stream is None else stream)
-    _check(rc, "tinfer_op_logprobs")
+    _call("tinfer_op_logprobs", lib().tinfer_op_logprobs,
+          (rows, vocab, _dtype(logits), logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _ptr(targets), top_k,
+           _ptr(logp), entropy.data_ptr(), _ptr(ids), _ptr(top)), dev, stream)
     return logp, entropy, ids, top

@@ -109,6 +109,19 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
   *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(h);
 }
 
+// Eight values to 16-byte aligned memory.
+__device__ __forceinline__ void store8(float* p, const float* x) {
+  store4(p, x);
+  store4(p + 4, x + 4);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* x) {
+  T h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) store_one(h + i, x[i]);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+}
+
 // ---- 8-bit codes ----------------------------------------------------------------------------------
 constexpr int E4M3 = TINFER_KV8_E4M3, INT8 = TINFER_KV8_INT8;
 
@@ -148,8 +161,9 @@ __device__ __forceinline__ uint32_t floats_to_codes(float a, float b, float c, f
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
   }
-  auto one = [](float x) { return (uint32_t)(__float2int_rn(fminf(fmaxf(x, -127.f), 127.f)) & 0xFF); };
-  return one(a) | (one(b) << 8) | (one(c) << 16) | (one(d) << 24);
+  // adding 1.5 * 2^23 leaves the nearest integer (ties to even) in the low bits
+  auto one = [](float x) { return __float_as_uint(fminf(fmaxf(x, -127.f), 127.f) + 12582912.f); };
+  return __byte_perm(__byte_perm(one(a), one(b), 0x0040), __byte_perm(one(c), one(d), 0x0040), 0x5410);
 }
 
 // ---- host side, shared by the entry points (kv8.cu) ----------------------------------------------
