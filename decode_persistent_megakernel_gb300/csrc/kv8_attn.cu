@@ -59,18 +59,27 @@ struct Shape {
 // all threads of a CTA; returns the total.
 constexpr int FIXED = 4;
 
+// In shared memory: prefix, then position and count of every sequence's new tokens (0, 0 for one that is passed over).
+struct List {
+  int* prefix;
+  int2* span;
+  __device__ List(void* at, int n) : prefix(static_cast<int*>(at)), span(reinterpret_cast<int2*>(static_cast<int*>(at) + ((n + 2) & ~1))) {}
+};
+size_t list_bytes(int n) { return (size_t)((n + 2) & ~1) * 4 + (size_t)n * 8; }
+
 template <int D>
-__device__ __forceinline__ int places_of(const AttnParams& q, int s) {
+__device__ __forceinline__ int places_of(const AttnParams& q, int s, const List& list) {
   int pos, count;
   if (!span_of(q.sp, s, q.c.max_ctx, pos, count) && blockIdx.x == 0 && q.sp.status) atomicOr(q.sp.status, STATUS_BAD_POS);
+  list.span[s] = make_int2(pos, count);
   return count > 0 ? ((pos + count + Shape<D>::KT - 1) / Shape<D>::KT + FIXED) * q.units : 0;
 }
 
 template <int D, int NT>
-__device__ int build_prefix(const AttnParams& q, int* prefix, int* scan) {
+__device__ int build_list(const AttnParams& q, const List& list, int* scan) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = q.c.n_seqs;
   if (n <= 32) {  // every warp for itself: all write the same words, and no barrier stands before the first copy
-    const int mine = lane < n ? places_of<D>(q, lane) : 0;
+    const int mine = lane < n ? places_of<D>(q, lane, list) : 0;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -78,15 +87,15 @@ __device__ int build_prefix(const AttnParams& q, int* prefix, int* scan) {
       if (lane >= o) incl += y;
     }
     const int total = __shfl_sync(~0u, incl, 31);
-    if (lane < n) prefix[lane] = incl - mine;
-    if (lane == 0) prefix[n] = total;
+    if (lane < n) list.prefix[lane] = incl - mine;
+    if (lane == 0) list.prefix[n] = total;
     __syncwarp();
     return total;
   }
   int carry = 0;
   for (int base = 0; base < n; base += NT) {
     const int s = base + threadIdx.x;
-    const int mine = s < n ? places_of<D>(q, s) : 0;
+    const int mine = s < n ? places_of<D>(q, s, list) : 0;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -101,10 +110,10 @@ __device__ int build_prefix(const AttnParams& q, int* prefix, int* scan) {
       if (w < warp) before += y;
       carry += y;
     }
-    if (s < n) prefix[s] = before + incl - mine;
+    if (s < n) list.prefix[s] = before + incl - mine;
     __syncthreads();
   }
-  if (threadIdx.x == 0) prefix[n] = carry;
+  if (threadIdx.x == 0) list.prefix[n] = carry;
   __syncthreads();
   return carry;
 }
@@ -125,23 +134,32 @@ struct Place {
   int x, seq, unit, tile, tiles;  // tile < 0: an empty place; tiles: of one unit of this sequence
   int limit;                      // keys that some row of the unit sees
   int row0;                       // the KV head's first row among all rows of the cache
-  __device__ void seek(const AttnParams& q, const int* prefix, int at) {
+  int pos, count, head, rt;       // the sequence's new tokens; KV head and row tile of the unit
+  __device__ void seek(const AttnParams& q, const List& list, int at) {
     x = at;
     limit = tile = 0;
-    if (at >= prefix[q.c.n_seqs]) return;
-    seq = seq_of(prefix, q.c.n_seqs, at);
-    const int places = (prefix[seq + 1] - prefix[seq]) / q.units, in = at - prefix[seq];
-    tiles = places - FIXED;
-    unit = in / places;
-    tile = in - unit * places - FIXED;
-    const int pos = q.sp.pos[seq], count = q.sp.counts ? q.sp.counts[seq] : q.sp.n_tokens;
-    const int head = unit / q.row_tiles, rt = unit - head * q.row_tiles;
+    if (at >= list.prefix[q.c.n_seqs]) return;
+    seq = seq_of(list.prefix, q.c.n_seqs, at);
+    const int2 span = list.span[seq];
+    pos = span.x;
+    count = span.y;
+    tiles = (pos + count + Shape<D>::KT - 1) / Shape<D>::KT;
+    const int in = at - list.prefix[seq];
+    unit = in / (tiles + FIXED);
+    tile = in - unit * (tiles + FIXED) - FIXED;
+    head = unit;
+    rt = 0;
+    limit = pos + count;
+    if (q.row_tiles > 1) {
+      head = unit / q.row_tiles;
+      rt = unit - head * q.row_tiles;
+      limit = rt * ROWS >= q.group * count ? 0 : pos + min((rt * ROWS + ROWS - 1) / q.group, count - 1) + 1;
+    }
     row0 = (seq * q.c.n_kv + head) * q.c.max_ctx;
-    limit = rt * ROWS >= q.group * count ? 0 : pos + min((rt * ROWS + ROWS - 1) / q.group, count - 1) + 1;
   }
-  __device__ void next(const AttnParams& q, const int* prefix, int end) {
+  __device__ void next(const AttnParams& q, const List& list, int end) {
     ++x;
-    if (++tile >= tiles && x < end) seek(q, prefix, x);
+    if (++tile >= tiles && x < end) seek(q, list, x);
   }
 };
 
@@ -206,6 +224,7 @@ struct Smem {
   static_assert(C::ROWS * D * 4 <= Shape<D>::STAGE_BYTES, "a warp's outputs fit its first ring slot");
   alignas(1024) uint8_t ring[C::NW][C::STAGES][Shape<D>::STAGE_BYTES];
   alignas(16) float2 angle[C::NW][D / 2];  // cosine and sine of one token's rotary pairs
+  unsigned long long freq[D / 2];
   int4 slot[C::NW][C::STAGES];            // of a tile in the ring: place in the list, first key, keys
   Part tail[C::NW], head[C::NW];          // a warp's last part (outputs in its ring) and its first (in the workspace)
   Group group[C::NW + 1];
@@ -237,14 +256,15 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   constexpr int KT = Shape<D>::KT, MK = KT / 16, MD = D / 16, ROWS = C::ROWS, DB = D / 8, NW = C::NW, STAGES = C::STAGES;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem<D, NG, SPLIT>& sm = *reinterpret_cast<Smem<D, NG, SPLIT>*>(smem_raw);
-  int* prefix = reinterpret_cast<int*>(smem_raw + sizeof(sm));
+  const List list(smem_raw + sizeof(sm), q.c.n_seqs);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
   if (lane == 0)
     for (int s = 0; s < STAGES; ++s) mbar_init(smem_addr(&sm.full[warp][s]), 33);  // the copy and 32 lanes' scales
   if (tid == 0) sm.failed = 0;
   mbar_fence_init();
-  const int total = build_prefix<D, C::NT>(q, prefix, sm.scan);
+  if (tid < D / 2) sm.freq[tid] = q.rope.f[tid];  // (threads index it apart, which parameters do one by one)
+  const int total = build_list<D, C::NT>(q, list, sm.scan);
   const Deal share = deal(total, gridDim.x, NW);
   if ((long long)share.per * share.warps * blockIdx.x >= total) return;
   const int lo = warp < share.warps ? (int)min((long long)share.per * (blockIdx.x * share.warps + warp), (long long)total) : total;
@@ -252,11 +272,11 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
 
   // this warp's tiles, across the units' boundaries
   Place<D, ROWS> in;
-  in.seek(q, prefix, lo);
+  in.seek(q, list, lo);
   int put = 0, got = 0;
   const uint64_t policy = q.keep_l2 ? policy_evict_normal() : policy_evict_first();
   auto issue = [&]() {  // the next tile that has keys to read goes into the ring
-    while (in.x < hi && (in.tile < 0 || in.tile * KT >= in.limit)) in.next(q, prefix, hi);
+    while (in.x < hi && (in.tile < 0 || in.tile * KT >= in.limit)) in.next(q, list, hi);
     if (in.x >= hi) return;
     const int st = put % STAGES, key0 = in.tile * KT, keys = min(in.limit - key0, KT);
     const uint32_t bar = smem_addr(&sm.full[warp][st]);
@@ -269,23 +289,23 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
     }
     const int b0 = key0 >> q.c.lg_block, nb = ((key0 + keys - 1) >> q.c.lg_block) - b0 + 1;
     if (lane < nb) {
-      const size_t at = (size_t)(in.seq * q.c.n_kv + in.unit / q.row_tiles) * q.c.n_blocks + b0 + lane;
+      const size_t at = (size_t)(in.seq * q.c.n_kv + in.head) * q.c.n_blocks + b0 + lane;
       cp_async_4(smem_addr(&sm.ring_scale[warp][st][0][lane]), q.c.ks + at);
       cp_async_4(smem_addr(&sm.ring_scale[warp][st][1][lane]), q.c.vs + at);
     }
     cp_async_arrive(bar);
     ++put;
-    in.next(q, prefix, hi);
+    in.next(q, list, hi);
   };
   __syncwarp();
 #pragma unroll 1
   for (int s = 0; s < STAGES; ++s) issue();
-  __syncwarp();
+  __syncthreads();  // the frequencies are there
 
   Part tail{-1, 0, 0, 0}, front{-1, 0, 0, 0};
   float o[MD][NG][4], mx[NG][2], l[NG][2];
   Place<D, ROWS> seg;  // the unit that the warp works on
-  seg.seek(q, prefix, lo);
+  seg.seek(q, list, lo);
   while (seg.x < hi) {
     if (seg.tile < 0) {  // past the empty places
       seg.x -= seg.tile;
@@ -293,8 +313,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       if (seg.x >= hi) break;
     }
     const int seg_end = min(hi, seg.x + seg.tiles - seg.tile);
-    const int head = seg.unit / q.row_tiles, rt = seg.unit - head * q.row_tiles;
-    const int pos = q.sp.pos[seg.seq], count = q.sp.counts ? q.sp.counts[seg.seq] : q.sp.n_tokens;
+    const int head = seg.head, rt = seg.rt, pos = seg.pos, count = seg.count;
     const int rows = min(q.group * count - rt * ROWS, ROWS);  // rows of this unit (may be <= 0)
 
     // query rows: rotated, divided by a power of two, laid out as the scores' right operands, eight at a
@@ -331,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
             float c, s;
-            rope_cos_sin(q.rope.f[lane + 32 * i], pos + x, c, s);
+            rope_cos_sin(sm.freq[lane + 32 * i], pos + x, c, s);
             sm.angle[warp][lane + 32 * i] = make_float2(c, s);
           }
           __syncwarp();
@@ -589,7 +608,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
         store_part<D, NG>(q.part + (size_t)(2 * gridDim.x + blockIdx.x * NW + warp) * ROWS * (D + 2), o, g, t);
       }
     }
-    seg.seek(q, prefix, seg_end);
+    seg.seek(q, list, seg_end);
   }
 
   // ---- the parts that the warps of this CTA left, joined in order of the warps. A unit's parts are the tails of
@@ -610,10 +629,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       const bool joins = !tid || (w1 < NW && sm.head[w1].unit == p.unit);  // and the head of warp w1
       const int last = joins ? sm.head[w1].last : sm.tail[w1 - 1].last;
       Place<D, ROWS> at;
-      at.seek(q, prefix, p.unit);
-      const int head = at.unit / q.row_tiles;
-      u = Group{at.seq, head, (at.unit - head * q.row_tiles) * ROWS, q.group * (q.sp.counts ? q.sp.counts[at.seq] : q.sp.n_tokens),
-                w0, w1, joins ? w1 : -1, 2 * (p.first != 0) + (last != 0)};
+      at.seek(q, list, p.unit);
+      u = Group{at.seq, at.head, at.rt * ROWS, q.group * at.count, w0, w1, joins ? w1 : -1, 2 * (p.first != 0) + (last != 0)};
     }
     sm.group[tid] = u;
   }
@@ -665,20 +682,20 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
 template <int D, int NG, typename T>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) kv8_merge_kernel(const __grid_constant__ AttnParams q) {
   constexpr int KT = Shape<D>::KT, ROWS = 8 * NG;
-  extern __shared__ int prefix[];
+  extern __shared__ int list_raw[];
   __shared__ int scan[JOIN_WARPS];
+  const List list(list_raw, q.c.n_seqs);
   // the list depends on the call's inputs alone, so it is built while the parts are still being made
-  const int total = build_prefix<D, JOIN_WARPS * 32>(q, prefix, scan);
+  const int total = build_list<D, JOIN_WARPS * 32>(q, list, scan);
   const Deal share = deal(total, q.grid, q.warps);
   const int per = share.per * share.warps;  // of a CTA
   const int seq = blockIdx.x / q.units, unit = blockIdx.x % q.units;
-  int pos, count;
-  const bool ok = span_of(q.sp, seq, q.c.max_ctx, pos, count) && count > 0;
+  const int pos = list.span[seq].x, count = list.span[seq].y;
   const int tiles = (pos + count + KT - 1) / KT;
-  const int a = prefix[seq] + unit * (tiles + FIXED) + FIXED, c0 = a / per, parts = (a + tiles - 1) / per - c0 + 1;
+  const int a = list.prefix[seq] + unit * (tiles + FIXED) + FIXED, c0 = a / per, parts = (a + tiles - 1) / per - c0 + 1;
   const int head = unit / q.row_tiles, rt = unit % q.row_tiles;
   pdl_wait();  // the parts are complete
-  if (!ok || parts <= 1) return;  // one CTA had it whole
+  if (count == 0 || parts <= 1) return;  // one CTA had it whole
   join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * count - rt * ROWS, ROWS), c0, parts, WEIGHT_SHIFT);
 }
 
@@ -705,8 +722,8 @@ template <int FMT, int D, int NG, int SPLIT, typename T>
 cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
   q.warps = Cfg<D, NG, SPLIT>::NW;
   auto kernel = kv8_attn_kernel<FMT, D, NG, SPLIT, T>;
-  const size_t list = (size_t)(q.c.n_seqs + 1) * 4, smem = sizeof(Smem<D, NG, SPLIT>) + list;
-  static_assert(sizeof(Smem<D, NG, SPLIT>) + (MAX_SEQS + 1) * 4 <= 227 * 1024, "shared memory of a CTA");
+  const size_t list = list_bytes(q.c.n_seqs), smem = sizeof(Smem<D, NG, SPLIT>) + list;
+  static_assert(sizeof(Smem<D, NG, SPLIT>) + MAX_SEQS * 12 + 16 <= 227 * 1024, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   CUtensorMap maps[2];

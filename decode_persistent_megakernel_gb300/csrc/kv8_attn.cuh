@@ -80,7 +80,7 @@ template <int D, int ROWS, typename T>
 __device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int rows, int c0, int parts, int weight_shift) {
   constexpr int N = D / 32, NW = JOIN_WARPS;
   __shared__ alignas(16) float acc_s[NW][D];
-  __shared__ float sum_s[NW];
+  __shared__ float sum_s[NW], top_s[NW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool few = parts <= NW;
   auto part = [&](int c) { return q.part + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * ROWS * (D + 2); };
@@ -141,37 +141,52 @@ __device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int
     return;
   }
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-    float top = -INFINITY;
-    for (int c = lane; c < parts; c += 32) top = fmaxf(top, part(c)[ROWS * D + row]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    float sum = 0.f, y[N];
+    float top = -INFINITY, sum = 0.f, y[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) y[i] = 0.f;
-#pragma unroll 8
-    for (int c = warp; c < parts; c += NW) {
-      const float* p = part(c);
-      const float lc = p[ROWS * D + ROWS + row], mc = p[ROWS * D + row];
-      float f[N];
-      load(p, row, f);
-      const float w = lc == 0.f ? 0.f : exp2_fast(mc - top);
-      sum = fmaf(lc, w, sum);
+    auto add = [&](float mc, float lc, const float (&f)[N]) {
+      if (lc == 0.f) return;  // no key of the row
+      const float now = fmaxf(top, mc);
+      const float a = top == now ? 1.f : exp2_fast(top - now), b = mc == now ? 1.f : exp2_fast(mc - now);
+      top = now;
+      sum = fmaf(lc, b, sum * a);
 #pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = fmaf(f[i], w, y[i]);
+      for (int i = 0; i < N; ++i) y[i] = fmaf(f[i], b, y[i] * a);
+    };
+    constexpr int R = 8;  // parts of a warp whose loads go out together
+    for (int c = warp; c < parts; c += R * NW) {
+      float mc[R], lc[R], f[R][N];
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+        if (c + k * NW < parts) {
+          const float* p = part(c + k * NW);
+          mc[k] = p[ROWS * D + row];
+          lc[k] = p[ROWS * D + ROWS + row];
+          load(p, row, f[k]);
+        } else {
+          lc[k] = 0.f;
+        }
+#pragma unroll
+      for (int k = 0; k < R; ++k) add(mc[k], lc[k], f[k]);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) acc_s[warp][lane * N + i] = y[i];
-    if (lane == 0) sum_s[warp] = sum;
+    if (lane == 0) {
+      sum_s[warp] = sum;
+      top_s[warp] = top;
+    }
     __syncthreads();
     if (warp == 0) {
+      top = -INFINITY;
       sum = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) y[i] = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        sum += sum_s[w];
+        float f[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] += acc_s[w][lane * N + i];
+        for (int i = 0; i < N; ++i) f[i] = acc_s[w][lane * N + i];
+        add(top_s[w], sum_s[w], f);
       }
       finish(row, top, sum, y);
     }
