@@ -206,9 +206,10 @@ struct Cfg {
 };
 
 // A part of a unit that a warp leaves to be joined: the unit, by its first place in the list (-1: none), its
-// tiles, and whether it holds the unit's first and last.
+// tiles, whether it holds the unit's first and last, and where the unit's rows are (the first of the KV head's query
+// rows, how many the head has).
 struct Part {
-  int unit, first, last, pad;
+  int unit, first, last, seq, head, row0, rows;
 };
 
 // The parts of one unit within a CTA: tails of warps w0 .. w1 - 1 and the head of head_warp (-1: none); rows counts
@@ -228,6 +229,7 @@ struct Smem {
   int4 slot[C::NW][C::STAGES];            // of a tile in the ring: place in the list, first key, keys
   Part tail[C::NW], head[C::NW];          // a warp's last part (outputs in its ring) and its first (in the workspace)
   Group group[C::NW + 1];
+  int groups;
   float m[2][C::NW][C::ROWS], l[2][C::NW][C::ROWS];  // of the tails and of the heads
   float ring_scale[C::NW][C::STAGES][2][SCALES];
   alignas(8) unsigned long long full[C::NW][C::STAGES];
@@ -302,7 +304,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   for (int s = 0; s < STAGES; ++s) issue();
   __syncthreads();  // the frequencies are there
 
-  Part tail{-1, 0, 0, 0}, front{-1, 0, 0, 0};
+  bool tail = false;  // this warp leaves a part in its registers
+  if (lane == 0) sm.tail[warp].unit = sm.head[warp].unit = -1;
   float o[MD][NG][4], mx[NG][2], l[NG][2];
   Place<D, ROWS> seg;  // the unit that the warp works on
   seg.seek(q, list, lo);
@@ -569,8 +572,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) l[n][h] += __shfl_xor_sync(~0u, l[n][h], x);
-    const Part mine{seg.x - seg.tile, seg.tile == 0, seg_end - seg.x + seg.tile == seg.tiles, 0};
-    if (mine.first && mine.last) {  // the whole unit: a thread holds DB dimensions of rows 2t and 2t + 1 of each group
+    const bool first = seg.tile == 0, last = seg_end - seg.x + seg.tile == seg.tiles;
+    if (first && last) {  // the whole unit: a thread holds DB dimensions of rows 2t and 2t + 1 of each group
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -601,10 +604,11 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
             sm.m[which][warp][n * 8 + 2 * t + h] = mx[n][h];
             sm.l[which][warp][n * 8 + 2 * t + h] = l[n][h];
           }
+      if (lane == 0)
+        (which ? sm.head : sm.tail)[warp] = Part{seg.x - seg.tile, first, last, seg.seq, head, rt * ROWS, q.group * count};
       if (which == 0) {
-        tail = mine;
+        tail = true;
       } else {
-        front = mine;
         store_part<D, NG>(q.part + (size_t)(2 * gridDim.x + blockIdx.x * NW + warp) * ROWS * (D + 2), o, g, t);
       }
     }
@@ -613,33 +617,35 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
 
   // ---- the parts that the warps of this CTA left, joined in order of the warps. A unit's parts are the tails of
   // neighbouring warps and perhaps the head of the next; all threads share the sums
-  if (lane == 0) {
-    sm.tail[warp] = tail;
-    sm.head[warp] = front;
-  }
-  if (tail.unit >= 0) store_part<D, NG>(reinterpret_cast<float*>(sm.ring[warp][0]), o, g, t);
+  if (tail) store_part<D, NG>(reinterpret_cast<float*>(sm.ring[warp][0]), o, g, t);
   __syncthreads();
-  // group 0: the head of warp 0, begun by an earlier CTA; group 1 + w: the parts that begin with warp w's tail
-  if (tid <= NW) {
-    Group u{-1, 0, 0, 0, 0, 0, 0, 0};
-    const Part p = tid ? sm.tail[tid - 1] : sm.head[0];
-    if (p.unit >= 0 && !(tid > 1 && sm.tail[tid - 2].unit == p.unit)) {
-      int w0 = max(tid - 1, 0), w1 = tid;
-      while (tid && w1 < NW && sm.tail[w1].unit == p.unit) ++w1;  // tails of warps w0 .. w1 - 1 (group 0: none)
-      const bool joins = !tid || (w1 < NW && sm.head[w1].unit == p.unit);  // and the head of warp w1
-      const int last = joins ? sm.head[w1].last : sm.tail[w1 - 1].last;
-      Place<D, ROWS> at;
-      at.seek(q, list, p.unit);
-      u = Group{at.seq, at.head, at.rt * ROWS, q.group * at.count, w0, w1, joins ? w1 : -1, 2 * (p.first != 0) + (last != 0)};
+  // one group for the head of warp 0, begun by an earlier CTA, and one for the parts that begin with each warp's tail
+  // (not with one that continues its neighbour's); they are few, and kept without gaps
+  if (warp == 0) {
+    Group u{0, 0, 0, 0, 0, 0, -1, 0};
+    bool there = false;
+    if (lane <= NW) {
+      const Part p = lane ? sm.tail[lane - 1] : sm.head[0];
+      there = p.unit >= 0 && !(lane > 1 && sm.tail[lane - 2].unit == p.unit);
+      if (there) {
+        int w1 = lane;
+        while (lane && w1 < NW && sm.tail[w1].unit == p.unit) ++w1;  // tails of warps lane - 1 .. w1 - 1 (lane 0: none)
+        const bool joins = !lane || (w1 < NW && sm.head[w1].unit == p.unit);  // and the head of warp w1
+        const int last = joins ? sm.head[w1].last : sm.tail[w1 - 1].last;
+        u = Group{p.seq, p.head, p.row0, p.rows, max(lane - 1, 0), w1, joins ? w1 : -1, 2 * (p.first != 0) + (last != 0)};
+      }
     }
-    sm.group[tid] = u;
+    const unsigned set = __ballot_sync(~0u, there);
+    if (there) sm.group[__popc(set & ((1u << lane) - 1))] = u;
+    if (lane == 0) sm.groups = __popc(set);
   }
   __syncthreads();
   constexpr int QUADS = D / 4;
-  for (int item = tid; item < (NW + 1) * ROWS * QUADS; item += C::NT) {
+  const int items = sm.groups * ROWS * QUADS;
+  for (int item = tid; item < items; item += C::NT) {
     const Group u = sm.group[item / (ROWS * QUADS)];
     const int row = item / QUADS % ROWS, c = item % QUADS * 4, qrow = u.row0 + row;
-    if (u.seq < 0 || qrow >= u.rows) continue;
+    if (qrow >= u.rows) continue;
     const int w0 = u.w0, w1 = u.w1;
     const bool use_head = u.head_warp >= 0, first = u.ends & 2, last = u.ends & 1;
     float top = -INFINITY;
@@ -734,7 +740,7 @@ cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   // few units: a CTA for each row, so that long rows are joined side by side
-  cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units), q.c.n_seqs * q.units <= 64 ? 8 * NG : 1);
+  cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units), q.c.n_seqs * q.units <= 16 ? 8 * NG : q.c.n_seqs * q.units <= 64 ? NG : 1);
   cfg.blockDim = dim3(JOIN_WARPS * 32);
   cfg.dynamicSmemBytes = list;
   cfg.stream = st;
