@@ -440,8 +440,9 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
           }
         }
       }
-      // ---- x + e for every score, masked; the rows' maxima
-      float vf[MK], vinv[MK];
+      // ---- the rows' maxima of x + e = s kf rf + ef. The products stay as they are and the weights scale them again, so
+      // that an exponent is rounded once, near 0 where its weight counts
+      float vf[MK], vinv[MK], kf[MK], ef[MK];
 #pragma unroll
       for (int j = 0; j < MK; ++j) {
         const int b = (rel + 16 * j) >> q.c.lg_block;
@@ -450,18 +451,16 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
         // a scale that is not finite reaches its scores, so that the mask decides which rows it spoils
         const bool fine = vs < INFINITY;
-        vf[j] = fine && vs > 0.f ? vs * inv : 0.f;
-        vinv[j] = inv;
-        const float fe = fine ? (float)e : __uint_as_float(0x7FC00000u);
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          const float f0 = ks * rs[n][0], f1 = ks * rs[n][1];
-          s[j][n][0] = fmaf(s[j][n][0], f0, fe);
-          s[j][n][1] = fmaf(s[j][n][1], f1, fe);
-          s[j][n][2] = fmaf(s[j][n][2], f0, fe);
-          s[j][n][3] = fmaf(s[j][n][3], f1, fe);
-        }
+        vf[j] = fine && vs > 0.f ? vs * inv * (float)(1 << WEIGHT_SHIFT) : 0.f;
+        vinv[j] = inv * (float)(1 << WEIGHT_SHIFT);
+        kf[j] = ks;
+        ef[j] = fine ? (float)e : __uint_as_float(0x7FC00000u);
       }
+      float rf[NG][2];
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) rf[n][h] = rs[n][h];
       if (keys < KT || key0 + KT > all_see) {
 #pragma unroll
         for (int j = 0; j < MK; ++j)
@@ -470,8 +469,16 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int key = 16 * j + 8 * (i >> 1) + g;
-              if (key >= keys || key0 + key >= limit[n][i & 1]) s[j][n][i] = -INFINITY;
+              // scaled before it is masked, whatever the scale of keys that are not seen
+              s[j][n][i] = key >= keys || key0 + key >= limit[n][i & 1] ? -INFINITY : fmaf(s[j][n][i], kf[j] * rf[n][i & 1], ef[j]);
             }
+#pragma unroll
+        for (int j = 0; j < MK; ++j) {
+          kf[j] = 1.f;
+          ef[j] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) rf[n][0] = rf[n][1] = 1.f;
       }
       float now[NG][2];
       bool grew = false;
@@ -479,9 +486,9 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       for (int n = 0; n < NG; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float top = fmaxf(s[0][n][h], s[0][n][2 + h]);
+          float top = -INFINITY;  // scales are not negative: the largest product of 16 keys is their largest score
 #pragma unroll
-          for (int j = 1; j < MK; ++j) top = fmaxf(top, fmaxf(s[j][n][h], s[j][n][2 + h]));
+          for (int j = 0; j < MK; ++j) top = fmaxf(top, fmaf(fmaxf(s[j][n][h], s[j][n][2 + h]), kf[j] * rf[n][h], ef[j]));
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
@@ -507,12 +514,12 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       for (int n = 0; n < NG; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float from = mx[n][h] == -INFINITY ? 0.f : mx[n][h] - (float)WEIGHT_SHIFT;
+          const float from = mx[n][h] == -INFINITY ? 0.f : mx[n][h];
 #pragma unroll
           for (int j = 0; j < MK; ++j)
 #pragma unroll
             for (int i = h; i < 4; i += 2) {
-              const float w = exp2_fast(s[j][n][i] - from);
+              const float w = exp2_fast(fmaf(s[j][n][i], kf[j] * rf[n][h], ef[j] - from));
               l[n][h] = fmaf(w, vinv[j], l[n][h]);
               s[j][n][i] = w * vf[j];
             }

@@ -495,6 +495,10 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           };
           if (all_seen) weights(std::false_type{});  // the warp's choice: tensor memory is stored to by whole warps
           else weights(std::true_type{});
+          // With scores ahead, the weights could run a key tile ahead of their products. A phase of a barrier can be
+          // told from the one before it only, so every product is seen to be complete before the weights of the
+          // next one of its half are given: the waits above and at the unit's end are then never more than one phase off
+          wait(smem_addr(&sm.o_full[tile][h]), (tiles_done - 1) & 1, failed);
           tmem_store_wait();
           fence_before();
           __syncwarp();

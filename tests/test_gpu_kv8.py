@@ -304,6 +304,37 @@ def test_attention_prompts(hq, hk, d, dtype, lens, counts):
     check_attention(cache, lens, counts, hq, dtype, 10000.0)
 
 
+@pytest.mark.parametrize("hq,hk,d,n,t,fmt", [(32, 8, 64, 8192, 512, E4M3), (12, 2, 128, 8192, 512, INT8), (4, 4, 64, 5000, 300, INT8),
+                                             (16, 1, 128, 6001, 77, E4M3)])
+def test_long_prompts_whose_maxima_keep_rising(hq, hk, d, n, t, fmt):
+    # keys grow along the context, so that running maxima rise and outputs are rescaled far into a run of key
+    # tiles; the outcome is the same every time and within the bounds
+    k = normal((1, n, hk, d), 1) * torch.linspace(0.2, 4, n)[None, :, None, None]
+    v = normal((1, n, hk, d), 2)
+    cache = T.Kv8Cache(hk, d, n, fmt=fmt, block=64)
+    cache.append(k.cuda(), v.cuda(), ints(0))
+    q = normal((1, t, hq, d), 3, 1.5).to(BF16)
+    outs = [cache.attention(q.cuda(), ints(n - t)) for _ in range(20)]
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    kk, vv = values(cache, 0, n)
+    for a in range(0, t, 128):
+        b = min(t, a + 128)
+        want, _, size, mean = R.attend(q[0, a:b].double(), kk[:, :n - t + b], vv[:, :n - t + b], n - t + a)
+        far, _ = R.attend_bounds(want, size, mean, d, n, BF16, v_top(cache, 0, n))
+        assert bool(((outs[0][0, a:b].cpu().double() - want).abs() <= far).all()), a
+        # most elements are far nearer than the worst case: within a few roundings of the row's size
+        rms = want.square().mean().sqrt()
+        assert float((outs[0][0, a:b].cpu().double() - want).abs().max() / rms) < 0.1, a
+
+
+def test_prompts_of_a_ragged_batch():
+    lens, counts = [700, 64, 1300, 5, 0, 333], [300, 64, 513, 5, 0, 1]
+    lens[4] = 1  # nothing new there
+    for hq, hk, d in ((6, 2, 64), (8, 8, 128), (10, 1, 64)):
+        cache = filled(hk, d, lens, 1300, E4M3, 32, seed=hq, spread=0.3)
+        check_attention(cache, lens, counts, hq, BF16, 500000.0, t=520)
+
+
 @pytest.mark.parametrize("hq,hk,d,n,dtype", [(12, 2, 128, 40000, F32), (32, 8, 64, 9001, BF16), (4, 2, 64, 70000, BF16)])
 def test_attention_long_context_is_split_and_joined(hq, hk, d, n, dtype):
     cache = filled(hk, d, [n], n + 7, E4M3, 128, seed=9)
