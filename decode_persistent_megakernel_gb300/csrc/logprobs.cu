@@ -6,7 +6,7 @@
 // it in 16-byte words, several in flight, and keep their own maximum and sums relative to it; they meet once at
 // the end, the slices in the first CTA's shared memory. Bound by HBM for many rows, by latency for one. (Slices staged in
 // shared memory by bulk copies took 300 to 345 us for 2047 rows of 128256 fp32 logits: with 64 KiB of a row to a CTA, the
-// joins at its end are most of its life.)
+// joins at its end are most of its life. Three CTAs of 40 registers on an SM took 219 us, four of 32 take 199.)
 //
 // Alternatives: a slice's values fall to 32 groups of threads; the k-th largest of the groups' maxima is a floor
 // that at least k values reach, and few others do (31 on average for k = 20). Only threads whose maximum reaches it
@@ -34,7 +34,6 @@ constexpr int MAX_K = 32, MAX_CLUSTER = 8;
 constexpr int GROUPS = 32;             // of threads, whose maxima give the alternatives' floor: one to a lane
 static_assert(MAX_CLUSTER * MAX_K <= NT, "a thread for every alternative of the slices");
 static_assert(MAX_K <= GROUPS, "a floor for every k");
-constexpr int AHEAD = 4;              // words of a thread in flight
 constexpr int LIST = 512;             // listed candidates of a slice, at most
 constexpr int MAX_VOCAB = 1 << 18;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -113,8 +112,9 @@ __device__ __forceinline__ Part join(const Part& a, const Part& b) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(NT, 3) logprobs_kernel(const __grid_constant__ Params q) {
+__global__ void __launch_bounds__(NT, 4) logprobs_kernel(const __grid_constant__ Params q) {
   constexpr int N = 16 / sizeof(T);  // elements of a word
+  constexpr int AHEAD = sizeof(T);   // words of a thread in flight: 16 elements, and 32 registers for four CTAs on an SM
   __shared__ Part red[NWARPS];
   __shared__ float group_top[GROUPS], floor_s;
   __shared__ int listed, owners;
