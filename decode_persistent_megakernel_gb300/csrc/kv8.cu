@@ -30,16 +30,15 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
   return fmaf(fmaf(-q, s, x), r, q);
 }
 
-// One CTA per (block of the cache, HPC KV heads, K or V, sequence). A thread's item is eight dimensions and their
-// rotary partners d/2 further of one token; all items of the heads' blocks stay in registers between the maximum
-// and the rounding, so the rows are read once, and a token's angles serve all the heads. Bound by HBM and, close
-// behind, by issue for prompts (2 or 4 bytes read and 1 written per value), by launch latency for single tokens.
-// 32 sequences of up to 2048 tokens, 8 heads of 64, bf16 to e4m3 (193 MB): BBB us, of which the rotation is CCC; one head to
-// a CTA and plain divisions took 70.
-template <int FMT, int D, typename T, int NT, int IPT, int HPC>
+// One CTA per (block of the cache, KV head, K or V, sequence). A thread's item is eight dimensions and their rotary
+// partners d/2 further of one token; all items of the block stay in registers between the maximum and the rounding,
+// so the rows are read once. Bound by issue and HBM alike for prompts (2 or 4 bytes read and 1 written per
+// value), by launch latency for single tokens. 32 sequences of up to 2048 tokens, 8 heads of 64, bf16 to e4m3 (193 MB):
+// 52 us, 45 without the rotation. Plain divisions and accurate angles took 70, two heads to a CTA to share angles 52.
+template <int FMT, int D, typename T, int NT, int IPT>
 __global__ void __launch_bounds__(NT) kv8_append_kernel(const __grid_constant__ AppendParams q) {
   constexpr int CPR = D / 16;  // items per row
-  const int seq = blockIdx.z, head0 = (blockIdx.y >> 1) * HPC, is_v = blockIdx.y & 1;
+  const int seq = blockIdx.z, head = blockIdx.y >> 1, is_v = blockIdx.y & 1;
   int pos, count;
   if (!span_of(q.sp, seq, q.c.max_ctx, pos, count)) {
     if (threadIdx.x == 0 && q.sp.status) atomicOr(q.sp.status, STATUS_BAD_POS);
@@ -52,116 +51,95 @@ __global__ void __launch_bounds__(NT) kv8_append_kernel(const __grid_constant__ 
   if (count == 0 || start >= end_new) return;
   const int t0 = max(pos, start), t1 = (int)min(end_new, (long long)start + block);
   const Rows& r = is_v ? q.v : q.k;
-  const T* src = static_cast<const T*>(r.data) + seq * r.ss + head0 * r.hs;
-  const size_t plane0 = (size_t)seq * q.c.n_kv + head0;
-  uint8_t* codes0 = (is_v ? q.c.v : q.c.k) + plane0 * q.c.max_ctx * D;
-  float* scale0 = (is_v ? q.c.vs : q.c.ks) + plane0 * q.c.n_blocks + b;
-  const int heads = min(HPC, q.c.n_kv - head0);
-  float held[HPC];
-#pragma unroll
-  for (int h = 0; h < HPC; ++h) held[h] = t0 > start && h < heads ? scale0[(size_t)h * q.c.n_blocks] : 0.f;
+  const T* src = static_cast<const T*>(r.data) + seq * r.ss + head * r.hs;
+  const size_t plane = (size_t)seq * q.c.n_kv + head;
+  uint8_t* codes = (is_v ? q.c.v : q.c.k) + plane * q.c.max_ctx * D;
+  float* scale_p = (is_v ? q.c.vs : q.c.ks) + plane * q.c.n_blocks + b;
+  const float held = t0 > start ? *scale_p : 0.f;
 
-  float x[HPC][IPT][16];
-  unsigned top[HPC];  // largest magnitude as bits: infinities and NaN compare above every finite value
+  float x[IPT][16];
 #pragma unroll
-  for (int h = 0; h < HPC; ++h) {
-    top[h] = 0;
+  for (int i = 0; i < IPT; ++i) {
+    const int item = threadIdx.x + i * NT, row = start + item / CPR, c = (item % CPR) * 8;
+    if (row >= t0 && row < t1) {
+      const T* p = src + (row - pos) * r.ts;
+      load8(p + c, reinterpret_cast<float(&)[8]>(x[i][0]));
+      load8(p + D / 2 + c, reinterpret_cast<float(&)[8]>(x[i][8]));
+    } else {
 #pragma unroll
-    for (int i = 0; i < IPT; ++i) {
-      const int item = threadIdx.x + i * NT, row = start + item / CPR, c = (item % CPR) * 8;
-      if (row >= t0 && row < t1 && h < heads) {
-        const T* p = src + (row - pos) * r.ts + h * r.hs;
-        load8(p + c, reinterpret_cast<float(&)[8]>(x[h][i][0]));
-        load8(p + D / 2 + c, reinterpret_cast<float(&)[8]>(x[h][i][8]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[h][i][e] = 0.f;
-      }
+      for (int e = 0; e < 16; ++e) x[i][e] = 0.f;
     }
   }
+  __shared__ unsigned long long freq[D / 2];
+  __shared__ unsigned warp_top[NT / 32];
   if (!is_v && q.rope.on) {
+    for (int i = threadIdx.x; i < D / 2; i += NT) freq[i] = q.rope.f[i];  // (threads index it apart)
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < IPT; ++i) {
       const int item = threadIdx.x + i * NT, row = start + item / CPR, c = (item % CPR) * 8;
-      if (row < t0 || row >= t1) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float cs, sn;
-        rope_cos_sin(q.rope.f[c + e], row, cs, sn);
-#pragma unroll
-        for (int h = 0; h < HPC; ++h) {
-          const float a = x[h][i][e], z = x[h][i][8 + e];
-          x[h][i][e] = a * cs - z * sn;
-          x[h][i][8 + e] = z * cs + a * sn;
-        }
+        rope_cos_sin_fast(freq[c + e], row, cs, sn);
+        const float a = x[i][e], z = x[i][8 + e];
+        x[i][e] = a * cs - z * sn;
+        x[i][8 + e] = z * cs + a * sn;
       }
     }
   }
-  __shared__ unsigned warp_top[HPC][NT / 32];
+  unsigned top = 0;  // largest magnitude as bits: infinities and NaN compare above every finite value
 #pragma unroll
-  for (int h = 0; h < HPC; ++h) {
+  for (int i = 0; i < IPT; ++i)
 #pragma unroll
-    for (int i = 0; i < IPT; ++i)
+    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
+  top = __reduce_max_sync(~0u, top);
+  if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
+  __syncthreads();  // (and every thread has read the held scale)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top[h] = max(top[h], __float_as_uint(x[h][i][e]) & 0x7FFFFFFFu);
-    top[h] = __reduce_max_sync(~0u, top[h]);
-    if ((threadIdx.x & 31) == 0) warp_top[h][threadIdx.x >> 5] = top[h];
+  for (int w = 0; w < NT / 32; ++w) top = max(top, warp_top[w]);
+  // the scale: a value that is not finite makes it NaN, so that whatever reads the block shows it
+  const float amax = __uint_as_float(top);
+  float scale;
+  if (top >= 0x7F800000u || !(held < INFINITY)) {
+    scale = __uint_as_float(0x7FC00000u);
+  } else if (held > 0.f) {
+    scale = held;
+    while ((double)amax > (double)qmax<FMT>() * (double)scale) scale *= 2.f;
+  } else {
+    scale = top ? fmaxf(amax / qmax<FMT>(), 1.17549435e-38f) : 0.f;
   }
-  __syncthreads();  // (and every thread has read the held scales)
-#pragma unroll
-  for (int h = 0; h < HPC; ++h) {
-    if (h >= heads) break;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) top[h] = max(top[h], warp_top[h][w]);
-    // the scale: a value that is not finite makes it NaN, so that whatever reads the block shows it
-    const float amax = __uint_as_float(top[h]);
-    float scale;
-    if (top[h] >= 0x7F800000u || !(held[h] < INFINITY)) {
-      scale = __uint_as_float(0x7FC00000u);
-    } else if (held[h] > 0.f) {
-      scale = held[h];
-      while ((double)amax > (double)qmax<FMT>() * (double)scale) scale *= 2.f;
-    } else {
-      scale = top[h] ? fmaxf(amax / qmax<FMT>(), 1.17549435e-38f) : 0.f;
+  const bool usable = scale > 0.f;
+  if (held > 0.f && usable && scale != held) {  // the started block grew: its held codes in the new units
+    const float shrink = held / scale;
+    for (int i = threadIdx.x; i < (t0 - start) * (D / 4); i += NT) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(codes + (size_t)start * D) + i;
+      float f[4];
+      codes_to_float<FMT>(*w, f);
+      *w = floats_to_codes<FMT>(f[0] * shrink, f[1] * shrink, f[2] * shrink, f[3] * shrink);
     }
-    const bool usable = scale > 0.f;
-    uint8_t* codes = codes0 + (size_t)h * q.c.max_ctx * D;
-    if (held[h] > 0.f && usable && scale != held[h]) {  // the started block grew: its held codes in the new units
-      const float shrink = held[h] / scale;
-      for (int i = threadIdx.x; i < (t0 - start) * (D / 4); i += NT) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(codes + (size_t)start * D) + i;
-        float f[4];
-        codes_to_float<FMT>(*w, f);
-        *w = floats_to_codes<FMT>(f[0] * shrink, f[1] * shrink, f[2] * shrink, f[3] * shrink);
-      }
-    }
-    const float rcp = usable ? 1.f / scale : 0.f;
-    const bool plain = !(scale > 1e-30f && scale < 1e30f);  // far from the range's ends the remainder is exact
-#pragma unroll
-    for (int i = 0; i < IPT; ++i) {
-      const int item = threadIdx.x + i * NT, row = start + item / CPR, c = (item % CPR) * 8;
-      if (row < t0 || row >= t1) continue;
-      uint32_t w[4];
-      if (plain) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float* y = &x[h][i][4 * e];
-          w[e] = usable ? floats_to_codes<FMT>(y[0] / scale, y[1] / scale, y[2] / scale, y[3] / scale) : 0u;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float* y = &x[h][i][4 * e];
-          w[e] = floats_to_codes<FMT>(quotient(y[0], scale, rcp), quotient(y[1], scale, rcp), quotient(y[2], scale, rcp),
-                                      quotient(y[3], scale, rcp));
-        }
-      }
-      uint8_t* dst = codes + (size_t)row * D;
-      *reinterpret_cast<uint2*>(dst + c) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2*>(dst + D / 2 + c) = make_uint2(w[2], w[3]);
-    }
-    if (threadIdx.x == 0) scale0[(size_t)h * q.c.n_blocks] = scale;
   }
+  const float rcp = usable ? 1.f / scale : 0.f;
+  const bool plain = !(scale > 1e-30f && scale < 1e30f);  // far from the range's ends the remainder is exact
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const int item = threadIdx.x + i * NT, row = start + item / CPR, c = (item % CPR) * 8;
+    if (row < t0 || row >= t1) continue;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float* y = &x[i][4 * e];
+      if (plain)
+        w[e] = usable ? floats_to_codes<FMT>(y[0] / scale, y[1] / scale, y[2] / scale, y[3] / scale) : 0u;
+      else
+        w[e] = floats_to_codes<FMT>(quotient(y[0], scale, rcp), quotient(y[1], scale, rcp), quotient(y[2], scale, rcp),
+                                    quotient(y[3], scale, rcp));
+    }
+    uint8_t* dst = codes + (size_t)row * D;
+    *reinterpret_cast<uint2*>(dst + c) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(dst + D / 2 + c) = make_uint2(w[2], w[3]);
+  }
+  if (threadIdx.x == 0) *scale_p = scale;
 }
 
 struct ReadParams {
@@ -262,32 +240,18 @@ bool rope_of(double theta, int head_dim, Rope& out) {
 
 namespace {
 
-template <int FMT, int D, typename T, int NT, int IPT, int HPC>
-cudaError_t launch_append_h(const AppendParams& q, cudaStream_t st) {
-  const int block = 1 << q.c.lg_block, n = q.sp.n_tokens;
-  const dim3 grid((unsigned)((n + block - 2) / block + 1), (unsigned)(2 * ((q.c.n_kv + HPC - 1) / HPC)), (unsigned)q.c.n_seqs);
-  kv8_append_kernel<FMT, D, T, NT, IPT, HPC><<<grid, NT, 0, st>>>(q);
-  return cudaGetLastError();
-}
-template <int FMT, int D, typename T, int NT, int IPT>
-cudaError_t launch_append_n(const AppendParams& q, cudaStream_t st) {
-  // several heads to a CTA where there are blocks enough to fill the GPU all the same
-  constexpr int MOST = IPT == 1 ? 2 : 1;
-  const int block = 1 << q.c.lg_block;
-  const bool many = (long long)(q.sp.n_tokens / block) * q.c.n_seqs * q.c.n_kv * 2 > 4096;
-  if (MOST > 1 && many && q.c.n_kv > 1) return launch_append_h<FMT, D, T, NT, IPT, MOST>(q, st);
-  return launch_append_h<FMT, D, T, NT, IPT, 1>(q, st);
-}
-
 template <int FMT, int D, typename T>
 cudaError_t launch_append_t(const AppendParams& q, cudaStream_t st) {
-  switch ((1 << q.c.lg_block) * (D / 16)) {  // items of one block: 64 (16 tokens of 64) to 1024 (128 tokens of 128)
-    case 64: return launch_append_n<FMT, D, T, 64, 1>(q, st);
-    case 128: return launch_append_n<FMT, D, T, 128, 1>(q, st);
-    case 256: return launch_append_n<FMT, D, T, 256, 1>(q, st);
-    case 512: return launch_append_n<FMT, D, T, 256, 2>(q, st);
-    default: return launch_append_n<FMT, D, T, 256, 4>(q, st);
+  const int block = 1 << q.c.lg_block, n = q.sp.n_tokens;
+  const dim3 grid((unsigned)((n + block - 2) / block + 1), (unsigned)(2 * q.c.n_kv), (unsigned)q.c.n_seqs);
+  switch (block * (D / 16)) {  // items of one block: 64 (16 tokens of 64) to 1024 (128 tokens of 128)
+    case 64: kv8_append_kernel<FMT, D, T, 64, 1><<<grid, 64, 0, st>>>(q); break;
+    case 128: kv8_append_kernel<FMT, D, T, 128, 1><<<grid, 128, 0, st>>>(q); break;
+    case 256: kv8_append_kernel<FMT, D, T, 256, 1><<<grid, 256, 0, st>>>(q); break;
+    case 512: kv8_append_kernel<FMT, D, T, 256, 2><<<grid, 256, 0, st>>>(q); break;
+    default: kv8_append_kernel<FMT, D, T, 256, 4><<<grid, 256, 0, st>>>(q); break;
   }
+  return cudaGetLastError();
 }
 
 template <int FMT, int D, typename T>

@@ -13,7 +13,7 @@
 // Tensor memory: two (three at 64 dimensions) 128-column score buffers and two D-column outputs. Products are issued
 // by one warp and run in order, so new scores may follow the product that read the weights lying in their place.
 // The softmax and the second product go by halves of 64 keys, so that the first half's product runs under the
-// second half's exponentials. (Scores by halves as well cost a 128-row operand read twice: 115 us against DDD.)
+// second half's exponentials. (Scores by halves as well cost a 128-row operand read twice: 115 us for the 4096-token prompt against 114.)
 //
 // A row's running maximum is replaced only when it would grow by more than 2^8: the outputs in tensor memory
 // are then rescaled by the row's thread, which happens in the first tiles of a row and rarely after. Weights
