@@ -482,6 +482,17 @@ def _call(what, fn, args, device, stream) -> None:
         raise TinferError(rc, what)
 
 
+def _making(stream, device):
+    """Context in which new results of a call on `stream` are made: their memory and first values belong to that stream."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def _on(what: str, t, device, dtype=None, shape=None):
     """Checks a tensor argument: its device, and its dtype and shape where given."""
     if t.device != device:
@@ -514,6 +525,8 @@ class Kv8Cache:
             device = torch.device(device)
             buffers = tuple(torch.zeros(codes, dtype=torch.uint8, device=device) for _ in range(2)) + tuple(
                 torch.zeros(scales, dtype=torch.float32, device=device) for _ in range(2))
+            if device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(device).synchronize()  # the zeros come before an append on any stream
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = buffers
         self.device = self.k_codes.device
         if self.device.type != "cuda":
@@ -566,8 +579,9 @@ class Kv8Cache:
         (bfloat16 when None), zero where a sequence has fewer tokens."""
         import torch
         if out is None:
-            out = tuple(torch.zeros((self.n_seqs, n_tokens, self.n_kv_heads, self.head_dim),
-                                    dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2))
+            with _making(stream, self.device):
+                out = tuple(torch.zeros((self.n_seqs, n_tokens, self.n_kv_heads, self.head_dim),
+                                        dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2))
         kr, vr = (self._rows(what, t, self.n_kv_heads, n_tokens) for what, t in zip(("k", "v"), out))
         _call("tinfer_op_kv8_read", lib().tinfer_op_kv8_read,
               (self.c, n_tokens, self._ints("pos", pos, self.n_seqs), self._ints("counts", counts, self.n_seqs), kr, vr,
@@ -589,7 +603,8 @@ class Kv8Cache:
         qr = self._rows("q", q)
         n_tokens, n_heads = q.shape[1], q.shape[2]
         if out is None:
-            out = q.new_zeros(q.shape)
+            with _making(stream, self.device):
+                out = q.new_zeros(q.shape)
         orow = self._rows("out", out, n_heads, n_tokens)
         if lse is not None and (lse.dtype != self.k_scales.dtype or lse.shape != q.shape[:3] or lse.device != self.device
                                 or not lse.is_contiguous()):
@@ -614,10 +629,14 @@ def logprobs(logits, targets=None, top_k: int = 0, stream=None):
     if targets is not None and (targets.dtype != torch.int32 or targets.shape != (rows,) or targets.device != dev
                                 or not targets.is_contiguous()):
         raise ValueError(f"targets: a contiguous int32 tensor [{rows}] on {dev} is wanted")
-    logp = torch.empty(rows, dtype=torch.float32, device=dev) if targets is not None else None
-    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
-    ids = torch.empty((rows, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
-    top = torch.empty((rows, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
+    # one allocation, in pieces of 16 bytes: a step's scores are a few microseconds on the GPU
+    piece, most = -(-rows // 4) * 4, rows * max(top_k, 0)
+    with _making(stream, dev):
+        made = torch.empty(2 * piece + 2 * most, dtype=torch.float32, device=dev)
+    logp = made[:rows] if targets is not None else None
+    entropy = made[piece:piece + rows]
+    ids = made[2 * piece:2 * piece + most].view(torch.int32).view(rows, top_k) if top_k > 0 else None
+    top = made[2 * piece + most:].view(rows, top_k) if top_k > 0 else None
     _call("tinfer_op_logprobs", lib().tinfer_op_logprobs,
           (rows, vocab, _dtype(logits), logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _ptr(targets), top_k,
            _ptr(logp), entropy.data_ptr(), _ptr(ids), _ptr(top)), dev, stream)

@@ -7,8 +7,8 @@
 // of the new scale. The power of two keeps that harmless: an e4m3 code only moves its exponent (exact
 // but for subnormals), and an int8 code's errors form a geometric series below one step, however often
 // the block grows.
+#include <algorithm>
 #include <cmath>
-#include <mutex>
 
 #include "kv8.cuh"
 
@@ -211,19 +211,35 @@ bool cache_of(const tinfer_kv8* c, Cache& out, tinfer_status& st) {
   return true;
 }
 
-// Rows are read and written in 16-byte words: base and strides have to keep every row on one. Rows that
-// are only read may be shared (a stride of 0).
+// Rows are read and written in 16-byte words: base and strides have to keep every row on one. The stride of an extent of
+// one is not looked at. Rows that are only read may lie anywhere; those that are written must not share memory, which
+// the strides show if each, from the smallest on, is no less than what the ones below it span.
 bool rows_of(const tinfer_rows* r, const Extent& x, bool written, Rows& out) {
   if (!r || !r->data) return false;
   const int size = r->dtype == TINFER_DTYPE_F32 ? 4 : r->dtype == TINFER_DTYPE_F16 || r->dtype == TINFER_DTYPE_BF16 ? 2 : 0;
   if (!size || (reinterpret_cast<uintptr_t>(r->data) & 15)) return false;
-  const long long strides[3] = {r->seq_stride, r->token_stride, r->head_stride};
   const int extents[3] = {x.seqs, x.tokens, x.heads};
+  long long strides[3] = {r->seq_stride, r->token_stride, r->head_stride};
   for (int i = 0; i < 3; ++i) {
+    if (extents[i] == 1) strides[i] = 0;
     if (strides[i] < 0 || strides[i] % (16 / size) || strides[i] > (1LL << 40)) return false;
-    if (written && extents[i] > 1 && strides[i] < x.head_dim) return false;  // rows would overlap
   }
-  out = Rows{r->data, r->seq_stride, r->token_stride, r->head_stride};
+  out = Rows{r->data, strides[0], strides[1], strides[2]};
+  if (!written) return true;
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return strides[a] < strides[b]; });
+  long long span = x.head_dim;
+  for (int i : order) {
+    if (extents[i] == 1) continue;
+    if (strides[i] < span) return false;
+    span += strides[i] * (extents[i] - 1);
+  }
+  return true;
+}
+
+bool words_of(std::initializer_list<const void*> pointers) {
+  for (const void* p : pointers)
+    if (reinterpret_cast<uintptr_t>(p) & 3) return false;
   return true;
 }
 
@@ -289,8 +305,8 @@ tinfer_status tinfer_op_kv8_append(const tinfer_kv8* cache, const tinfer_rows* k
   kv8::AppendParams q{};
   tinfer_status rc;
   if (!kv8::cache_of(cache, q.c, rc)) return rc;
-  if (n_tokens < 1 || !pos_dev) return TINFER_ERR_INVALID_ARG;
-  if (n_tokens > cache->max_ctx) return TINFER_ERR_INVALID_ARG;
+  if (n_tokens < 1 || n_tokens > cache->max_ctx || !pos_dev || !kv8::words_of({pos_dev, counts_dev, status_dev}))
+    return TINFER_ERR_INVALID_ARG;
   const kv8::Extent x{cache->n_seqs, n_tokens, cache->n_kv_heads, cache->head_dim};
   if (!kv8::rows_of(k, x, false, q.k) || !kv8::rows_of(v, x, false, q.v)) return TINFER_ERR_INVALID_ARG;
   if (k->dtype != v->dtype || !kv8::rope_of(rope_theta, cache->head_dim, q.rope)) return TINFER_ERR_INVALID_ARG;
@@ -310,7 +326,8 @@ tinfer_status tinfer_op_kv8_read(const tinfer_kv8* cache, int n_tokens, const in
   kv8::ReadParams q{};
   tinfer_status rc;
   if (!kv8::cache_of(cache, q.c, rc)) return rc;
-  if (n_tokens < 1 || n_tokens > cache->max_ctx || !pos_dev) return TINFER_ERR_INVALID_ARG;
+  if (n_tokens < 1 || n_tokens > cache->max_ctx || !pos_dev || !kv8::words_of({pos_dev, counts_dev, status_dev}))
+    return TINFER_ERR_INVALID_ARG;
   const kv8::Extent x{cache->n_seqs, n_tokens, cache->n_kv_heads, cache->head_dim};
   if (!kv8::rows_of(k, x, true, q.k) || !kv8::rows_of(v, x, true, q.v)) return TINFER_ERR_INVALID_ARG;
   if (k->dtype != v->dtype) return TINFER_ERR_INVALID_ARG;

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "ptx.cuh"
 #include "tinfer.h"
@@ -183,6 +184,7 @@ struct Extent {
 };
 bool rows_of(const tinfer_rows* r, const Extent& x, bool written, Rows& out);
 bool rope_of(double theta, int head_dim, Rope& out);
+bool words_of(std::initializer_list<const void*> pointers);  // whether each is aligned to 4 bytes (or null)
 
 }  // namespace kv8
 }  // namespace tinfer

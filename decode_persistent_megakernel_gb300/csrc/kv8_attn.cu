@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
       top = max(top, __shfl_xor_sync(~0u, top, 1));
       top = max(top, __shfl_xor_sync(~0u, top, 2));
-      const int e2 = top ? min(max((int)(top >> 23) - 126, -100), 100) : 0;  // every magnitude below 2^e2
+      const int e2 = top ? min(max((int)(top >> 23) - 126, -100), 126) : 0;  // every magnitude below 2^e2 (below 4 2^e2 at the type's end)
       const float down = __uint_as_float((uint32_t)(127 - e2) << 23), up = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll
       for (int k = 0; k < MD; ++k)
@@ -736,8 +736,9 @@ cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
   q.warps = Cfg<D, NG, SPLIT>::NW;
   auto kernel = kv8_attn_kernel<FMT, D, NG, SPLIT, T>;
   const size_t list = list_bytes(q.c.n_seqs), smem = sizeof(Smem<D, NG, SPLIT>) + list;
-  static_assert(sizeof(Smem<D, NG, SPLIT>) + MAX_SEQS * 12 + 16 <= 227 * 1024, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr int MOST = sizeof(Smem<D, NG, SPLIT>) + MAX_SEQS * 12 + 16;  // the same in every call: others may be under way
+  static_assert(MOST <= 227 * 1024, "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
   if (e != cudaSuccess) return e;
   CUtensorMap maps[2];
   const long long cache_rows = (long long)q.c.n_seqs * q.c.n_kv * q.c.max_ctx;
@@ -780,7 +781,6 @@ int device_sms(int& sms) {
   return cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
 }
 
-
 }  // namespace
 }  // namespace kv8
 }  // namespace tinfer
@@ -815,7 +815,9 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   if (!workspace_dev || (reinterpret_cast<uintptr_t>(workspace_dev) & 15) ||
       workspace_bytes < tinfer_kv8_attention_workspace(cache, n_heads, n_tokens))
     return TINFER_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(lse_dev) & 3) return TINFER_ERR_INVALID_ARG;
+  if (!kv8::words_of({pos_dev, counts_dev, status_dev, lse_dev})) return TINFER_ERR_INVALID_ARG;
+  // over the queries' own memory a row may only replace itself
+  if (q.q.data == q.out.data && (q.q.ss != q.out.ss || q.q.ts != q.out.ts || q.q.hs != q.out.hs)) return TINFER_ERR_INVALID_ARG;
   q.group = n_heads / cache->n_kv_heads;
   q.n_heads = n_heads;
   q.sp = kv8::Span{pos_dev, counts_dev, n_tokens, status_dev};

@@ -66,10 +66,9 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
   if (mbar_sleep(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   while (!mbar_sleep(bar, parity))
-    if ((long long)(globaltimer() - t0) > WAIT_NS) return false;
+    if ((long long)(globaltimer() - t0) > WAIT_NS) return mbar_sleep(bar, parity);  // (time may have passed off the GPU)
   return true;
 }
-
 
 // The parts of a unit's rows that several CTAs hold (CTA c0's in its slot 1, the others' in their slot 0), joined in
 // order. Called by all warps of a CTA of JOIN_WARPS; blockIdx.y takes a slice of the rows. A row with few parts is

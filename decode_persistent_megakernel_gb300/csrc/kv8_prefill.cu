@@ -238,16 +238,12 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int
   while (!mbar_sleep(bar, parity)) {
     if (*failed) return;
     if ((long long)(globaltimer() - t0) > WAIT_NS) {
-      *failed = 1;
+      if (!mbar_sleep(bar, parity)) *failed = 1;  // (time may have passed off the GPU)
       return;
     }
   }
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -353,7 +349,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(x[i]) & 0x7FFFFFFFu);
         }
         // a rotation makes no magnitude larger than sqrt(2) times the largest: one power of two of room
-        const int e2 = most ? min(max((int)(most >> 23) - 125, -100), 100) : 0;
+        const int e2 = most ? min(max((int)(most >> 23) - 125, -100), 126) : 0;
         const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
         // chunks of eight dimensions whose angles are held at once: a power of two
         int lg_pairs = 3;
@@ -391,8 +387,8 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
             }
           }
           auto put = [&](int chunk, const float (&z)[8]) {  // a 16-byte chunk of the row: block chunk / 8, swizzled by the row
-            sts128(q_smem + (chunk / 8) * (TILE * 128) + (((chunk & 7) ^ (r & 7)) << 4), pack2(z[0] * down, z[1] * down),
-                   pack2(z[2] * down, z[3] * down), pack2(z[4] * down, z[5] * down), pack2(z[6] * down, z[7] * down));
+            sts128(q_smem + (chunk / 8) * (TILE * 128) + (((chunk & 7) ^ (r & 7)) << 4), pack_half(z[0] * down, z[1] * down),
+                   pack_half(z[2] * down, z[3] * down), pack_half(z[4] * down, z[5] * down), pack_half(z[6] * down, z[7] * down));
           };
           put(c, x);
           put(D / 16 + c, y);
@@ -486,7 +482,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
                   e.y = exp2_fast(e.y);
                   part = add2(part, e);
                   e = __fmul2_rn(e, v2);
-                  w[8 * j + i / 2] = pack2(e.x, e.y);
+                  w[8 * j + i / 2] = pack_half(e.x, e.y);
                 }
                 sum = fmaf(part.x + part.y, g.w, sum);
               }
@@ -688,9 +684,10 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
 #pragma unroll
             for (int k = 0; k < HALF / 16; ++k)
               mma_ts(leader, o, p + h * HALF + 8 * k, b + h * (HALF * 128 >> 4) + k * (2048 >> 4), i_o, k > 0 || h > 0 || j > (int)last_tile);
+            // (the last barrier that a unit's end waits for comes last)
+            if (h == 1 && va.tile == last_tile) commit(leader, bar_ve + 8 * va.stage);
             commit(leader, bar_o + 16 * va.tile + 8 * h);
           }
-          if (va.tile == last_tile) commit(leader, bar_ve + 8 * va.stage);
           va.step(last_tile);
           if (j + ahead < n) scores(false);
         }
@@ -727,8 +724,9 @@ template <int FMT, int D, typename T>
 cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
   auto kernel = prefill_kernel<FMT, D, T>;
   const size_t list = (size_t)(q.c.n_seqs + 1) * 8, smem = sizeof(Smem<D>) + list;
-  static_assert(sizeof(Smem<D>) + (MAX_SEQS + 1) * 8 <= 227 * 1024, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr int MOST = sizeof(Smem<D>) + (MAX_SEQS + 1) * 8;  // the same in every call: others may be under way
+  static_assert(MOST <= 227 * 1024, "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
   if (e != cudaSuccess) return e;
   kernel<<<q.grid, Roles<D>::NT, smem, st>>>(q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

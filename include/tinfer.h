@@ -372,9 +372,10 @@ tinfer_status tinfer_op_attention_noalloc(int n_heads, int n_kv_heads, int head_
  *
  * A tinfer_rows names rows of head_dim contiguous elements: the row of (sequence, token, head) starts
  * seq*seq_stride + token*token_stride + head*head_stride elements after data. data 16-byte aligned, the
- * strides not negative and multiples of 16 bytes; an operator that writes the rows also wants them apart
- * (each stride of more than one element at least head_dim). So the projections of a step, slices of a
- * fused buffer, and one layer of the bf16 cache of tinfer_create all serve as they are.
+ * strides not negative and multiples of 16 bytes (that of an extent of one is not looked at); an operator
+ * that writes the rows also wants them apart: each stride, from the smallest on, no less than what the
+ * ones below it span. So the projections of a step, slices of a fused buffer, and one layer of the bf16
+ * cache of tinfer_create all serve as they are.
  *
  * pos_dev (int32 [n_seqs]) and counts_dev (int32 [n_seqs], NULL: n_tokens everywhere) are read on the
  * device when the kernels run: token i < counts[s] of sequence s stands at position pos[s] + i. So a call
@@ -426,11 +427,14 @@ tinfer_status tinfer_op_kv8_read(const tinfer_kv8* cache, int n_tokens, const in
  * query's must have been appended: token i of sequence s attends to positions [0, pos[s] + i], scale
  * 1/sqrt(head_dim), query head h reading KV head h / (n_heads / n_kv_heads). q and out: rows of n_heads
  * heads, one dtype; fp32 and fp16 queries are multiplied in fp32-like precision (two fp16 parts), bf16
- * ones in fp16. out may be the memory of q. lse_dev: fp32 [n_seqs][n_tokens][n_heads], may be NULL: the natural
+ * ones in fp16 (scores have to stay in fp32's range). out may be q itself, with the same strides, and no other
+ * overlap of the two is sound. lse_dev: fp32 [n_seqs][n_tokens][n_heads], may be NULL: the natural
  * logarithm of the sum of exp(score). workspace_dev: tinfer_kv8_attention_workspace bytes of device
  * memory, 16-byte aligned, no initial values; calls that may overlap in time (other streams, other
  * graphs) need one each. Bit 1 of *status_dev: a device wait ran out, and the outputs are not valid.
- * tinfer_kv8_attention_workspace returns 0 for arguments that the call would refuse. */
+ * n_seqs * n_kv_heads * max_ctx below 2^31, the query rows of a KV head at most 2^30, and their number in units of
+ * work (row tiles times key tiles of max_ctx) below 2^30, else TINFER_ERR_UNSUPPORTED.
+ * tinfer_kv8_attention_workspace returns 0 for a cache or counts that every call would refuse. */
 size_t tinfer_kv8_attention_workspace(const tinfer_kv8* cache, int n_heads, int n_tokens);
 tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int n_tokens,
                                       const tinfer_rows* q, const int32_t* pos_dev,

@@ -380,6 +380,20 @@ def test_attention_query_sizes(q_scale):
     assert float((out[0].cpu().double() - want).abs().max()) <= 1e-5 * float(want.abs().max())
 
 
+@pytest.mark.parametrize("t,dtype", [(1, F32), (5, BF16), (150, BF16)])
+def test_queries_near_the_types_end(t, dtype):
+    # as large as the type holds, against keys as small: ordinary scores. The scales fall below 2^-126 and lose bits
+    # themselves (steps of 2^-149 at 2^-127), so the formula over the cache as it then is says what is right
+    cache = filled(2, 64, [400], 400, E4M3, 64, seed=12, spread=0.2)
+    q = normal((1, t, 8, 64), 13).clamp(-3, 3).to(dtype)
+    cache.k_scales.mul_(2.0 ** -120)
+    got = cache.attention((q * 2.0 ** 120).cuda(), ints(400 - t))[0].cpu().double()
+    k, v = values(cache, 0, 400)
+    want, _, size, mean = R.attend(q[0].double() * 2.0 ** 120, k, v, 400 - t)
+    far, _ = R.attend_bounds(want, size, mean, 64, 400, dtype, v_top(cache, 0, 400))
+    assert bool((size < 100).all()) and bool(got.isfinite().all()) and bool(((got - want).abs() <= far).all())
+
+
 def test_attention_scales_far_apart():
     # V blocks whose scales span 2^-40 .. 2^40, a block of zeros, one of the smallest scale
     cache = filled(2, 64, [320], 320, INT8, 32, seed=8)
@@ -449,6 +463,58 @@ def test_two_streams_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_results_made_for_another_stream_belong_to_it():
+    # the current stream is busy: what it fills later must not reach results that the other stream has written
+    cache = filled(2, 64, [700], 700, E4M3, 64, seed=7)
+    q = normal((1, 3, 8, 64), 20).to(BF16).cuda()
+    x, t = normal((5, 1000), 21).cuda(), ints(1, 2, 3, 4, 5)
+    pos, zero = ints(697), ints(0)
+    want = (cache.attention(q, pos), *cache.read(700, zero), *T.logprobs(x, t, 4))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (s, s.cuda_stream):
+        torch.cuda._sleep(20_000_000)
+        got = (cache.attention(q, pos, stream=handle), *cache.read(700, zero, stream=handle), *T.logprobs(x, t, 4, stream=handle))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_from_several_host_threads():
+    import threading
+    caches = [filled(1, 64, [50] * n, 50, E4M3, 64, seed=n) for n in (1, 40, 700)]
+    qs = [normal((c.n_seqs, 1, 2, 64), 30).cuda() for c in caches]
+    poss = [ints(*[49] * c.n_seqs) for c in caches]
+    want = [c.attention(q, p) for c, q, p in zip(caches, qs, poss)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(i):
+        stream = torch.cuda.Stream()
+        for _ in range(200):
+            try:
+                out = caches[i].attention(qs[i], poss[i], stream=stream)
+            except T.TinferError as e:
+                wrong.append(e)
+                return
+            stream.synchronize()
+            if not torch.equal(out, want[i]):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(3)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong
+
+
+def test_strides_of_single_extents_do_not_matter():
+    cache = filled(2, 64, [90], 90, E4M3, 64, seed=7)
+    q = normal((1, 1, 8, 64), 20).to(BF16).cuda()
+    odd = torch.as_strided(q, q.shape, (7, 3, 64, 1))
+    assert torch.equal(cache.attention(odd, ints(89)), cache.attention(q, ints(89)))
 
 
 def test_captured_step_follows_the_positions():

@@ -63,6 +63,27 @@ def test_written_rows_must_not_overlap():
         assert T.tinfer_op_kv8_attention(cache(), 4, 3, rows(), A, None, 0.0, r, None, A, 1 << 30) == BAD
 
 
+@pytest.mark.parametrize("ss,ts,hs", [(4096, 64, 64), (512, 256, 128), (128, 4096, 128), (256, 64, 256)])
+def test_written_rows_that_share_memory_are_refused(ss, ts, hs):
+    r = rows(ss=ss, ts=ts, hs=hs)  # each stride holds a row, but two rows of [2][3][4] (or [2][3][2]) meet
+    assert T.tinfer_op_kv8_attention(cache(), 4, 3, rows(), A, None, 0.0, r, None, A, 1 << 30) == BAD
+    assert T.tinfer_op_kv8_read(cache(n_kv_heads=4), 3, A, None, rows(), r) == BAD
+
+
+def test_results_over_the_queries_want_their_strides():
+    assert T.tinfer_op_kv8_attention(cache(), 4, 3, rows(), A, None, 0.0, rows(ts=512), None, A, 1 << 30) == BAD
+
+
+@pytest.mark.parametrize("at", ["pos", "counts", "status"])
+def test_words_off_their_boundary_are_refused(at):
+    a = dict(pos=A, counts=A, status=A)
+    a[at] = A + 2
+    assert T.tinfer_op_kv8_append(cache(), rows(), rows(), 3, a["pos"], a["counts"], 0.0, a["status"]) == BAD
+    assert T.tinfer_op_kv8_read(cache(), 3, a["pos"], a["counts"], rows(), rows(), a["status"]) == BAD
+    assert T.tinfer_op_kv8_attention(cache(), 4, 3, rows(), a["pos"], a["counts"], 0.0, rows(2 * A), None, A, 1 << 30,
+                                     a["status"]) == BAD
+
+
 def test_bad_angles_heads_and_workspaces_are_refused():
     for theta in (-1.0, 0.5, float("nan"), float("inf")):
         assert T.tinfer_op_kv8_append(cache(), rows(), rows(), 3, A, None, theta) == BAD
@@ -76,7 +97,7 @@ def test_bad_angles_heads_and_workspaces_are_refused():
         assert T.tinfer_op_kv8_attention(cache(), 4, 3, rows(), A, None, 0.0, rows(), None, ws, n) == BAD
     assert T.tinfer_op_kv8_attention(cache(), 4, 3, rows(), A, None, 0.0, rows(), A + 2, A, need) == BAD
     big = cache(n_seqs=1024, n_kv_heads=1024, max_ctx=1 << 24)
-    assert T.tinfer_op_kv8_attention(big, 1024, 1, rows(), A, None, 0.0, rows(ss=65536), None, A, 1 << 40) == NO
+    assert T.tinfer_op_kv8_attention(big, 1024, 1, rows(), A, None, 0.0, rows(2 * A, ss=65536), None, A, 1 << 40) == NO
 
 
 @pytest.mark.parametrize("over,want", [
