@@ -827,7 +827,7 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   // rows of the cache are counted in 32 bits (their coordinates in the copies)
   if ((long long)cache->n_seqs * cache->n_kv_heads * cache->max_ctx > 0x7FFFFFFFLL) return TINFER_ERR_UNSUPPORTED;
   const long long rows = (long long)q.group * n_tokens;
-  const bool prefill = kv8::is_prefill(q_rows->dtype, rows);
+  const bool prefill = kv8::is_prefill(q_rows->dtype, cache->head_dim, rows);
   const int per = prefill ? kv8::PREFILL_ROWS : kv8::rows_per_tile(rows, cache->head_dim);
   const long long row_tiles = (rows + per - 1) / per, units = row_tiles * cache->n_kv_heads;
   const int kt = 4096 / cache->head_dim;

@@ -198,7 +198,7 @@ constexpr int MAX_GRID = 160;
 bool code_map(CUtensorMap* map, const void* codes, long long rows, int d, int kt);
 // Prompts (kv8_prefill.cu): whether a call's rows are many enough, its workspace, and the launch.
 constexpr int PREFILL_ROWS = 256;  // query rows of a unit there
-bool is_prefill(int dtype, long long rows);
+bool is_prefill(int dtype, int head_dim, long long rows);
 size_t prefill_workspace(int head_dim);
 cudaError_t launch_prefill(AttnParams& q, int format, int head_dim, cudaStream_t st);
 

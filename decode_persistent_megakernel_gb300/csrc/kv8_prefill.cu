@@ -43,7 +43,7 @@ struct Roles {
 constexpr int KV_STAGES = 2, SCALE_SLOTS = 4;
 constexpr int SHIFT = 5;           // of the weights
 constexpr float GROW = 8.f;        // a maximum may lag behind by 2^8
-constexpr int FIXED_KEYS = 384;    // what a unit costs beside its keys, in keys
+constexpr int FIXED_KEYS = 768;    // what a unit costs beside its keys, in keys (4096-token prompt: 99 us, 109 with 384)
 
 template <int D>
 struct Smem {
@@ -731,7 +731,10 @@ cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
   kernel<<<q.grid, Roles<D>::NT, smem, st>>>(q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(q.c.n_seqs * q.units), 8);
+  // a CTA for 32 rows of few parts each, four rows of a warp; for fewer rows where units are few and have many parts
+  // (72 rows of 8000 keys, two heads of 128: 42 us by 32 rows, 24 by one)
+  const int units = q.c.n_seqs * q.units;
+  cfg.gridDim = dim3((unsigned)units, (unsigned)std::min(std::max(512 / units, ROWS / 32), std::min(ROWS, q.group * q.sp.n_tokens)));
   cfg.blockDim = dim3(JOIN_WARPS * 32);
   cfg.dynamicSmemBytes = list;
   cfg.stream = st;
@@ -750,9 +753,11 @@ cudaError_t launch_f(AttnParams& q, int head_dim, cudaStream_t st) {
 
 }  // namespace prefill
 
-// bf16 rows beyond one row tile of the other kernel. fp32 and fp16 rows stay there: their two-part operands keep
-// the precision of their type, which one fp16 operand would not.
-bool is_prefill(int dtype, long long rows) { return dtype == TINFER_DTYPE_BF16 && rows > 64; }
+// bf16 rows beyond one row tile of the other kernel, or four at 128 dimensions. fp32 and fp16 rows stay there: their
+// two-part operands keep the precision of their type, which one fp16 operand would not. Here against there, in us, at 40
+// rows of 8 heads of 64: 500 keys 17 : 22, 8000 keys 19 : 30, 32 sequences of 4000 keys 109 : 115; at 24 rows the last
+// takes 108 : 69. Two heads of 128, 64 rows: 23 : 22, 23 : 20, 49 : 65; 128 rows: 26 : 21, 27 : 31, 55 : 106.
+bool is_prefill(int dtype, int head_dim, long long rows) { return dtype == TINFER_DTYPE_BF16 && rows > (head_dim == 64 ? 32 : 64); }
 size_t prefill_workspace(int head_dim) { return (size_t)MAX_GRID * 2 * PREFILL_ROWS * (head_dim + 2) * 4; }
 
 cudaError_t launch_prefill(AttnParams& q, int format, int head_dim, cudaStream_t st) {

