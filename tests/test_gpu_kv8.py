@@ -305,7 +305,7 @@ def test_attention_prompts(hq, hk, d, dtype, lens, counts):
 
 
 @pytest.mark.parametrize("hq,hk,d,n,t,fmt", [(32, 8, 64, 8192, 512, E4M3), (12, 2, 128, 8192, 512, INT8), (4, 4, 64, 5000, 300, INT8),
-                                             (16, 1, 128, 6001, 77, E4M3)])
+                                             (16, 1, 128, 6001, 77, E4M3), (12, 2, 128, 2048, 2048, INT8), (16, 2, 64, 9000, 16, INT8)])
 def test_long_prompts_whose_maxima_keep_rising(hq, hk, d, n, t, fmt):
     # keys grow along the context, so that running maxima rise and outputs are rescaled far into a run of key
     # tiles; the outcome is the same every time and within the bounds
