@@ -40,10 +40,11 @@ struct Roles {
   static constexpr int BUFFERS = D == 64 ? 3 : 2;       // of 128 x 128 scores in tensor memory, beside two outputs of D columns
   static constexpr int ANGLES = D == 64 ? 4096 : 1472;  // of a tile: all of 128 tokens, or of 23 (or 8 at a time)
 };
+constexpr int FETCH = 4;           // key tiles that are fetched into L2 ahead (64 rows of 32 x 4000 keys 111 -> 102 us)
 constexpr int KV_STAGES = 2, SCALE_SLOTS = 4;
 constexpr int SHIFT = 5;           // of the weights
 constexpr float GROW = 8.f;        // a maximum may lag behind by 2^8
-constexpr int FIXED_KEYS = 768;    // what a unit costs beside its keys, in keys (4096-token prompt: 99 us, 109 with 384)
+constexpr int FIXED_KEYS = 768;    // what a unit costs beside its keys, in keys (4096-token prompt: 98 us, 109 with 384)
 
 template <int D>
 struct Smem {
@@ -601,9 +602,21 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           sts128(base + ((c1 ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
         }
       };
+      // the codes are on their way from HBM to L2 some tiles before they are loaded: a tile's lines, one to a thread
+      constexpr int LINES = KT * D / 128;
+      static_assert(LINES <= NT_WIDEN, "a line to a thread");
+      auto fetch = [&](int kt) {
+        const int at = kt * KT + t * (128 / D);
+        if (t < LINES && kt < u.last && at < u.keys) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(kp + (size_t)at * D));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(vp + (size_t)at * D));
+        }
+      };
       uint4 wk[ITEMS], wv[ITEMS];
       load(kp, u.first, wk);
+      for (int kt = u.first + 1; kt < u.first + FETCH; ++kt) fetch(kt);
       for (int kt = u.first; kt < u.last; ++kt, ++it) {
+        fetch(kt + FETCH);
         const int st = it % KV_STAGES;
         const uint32_t parity = ((it / KV_STAGES) & 1) ^ 1;
         load(vp, kt, wv);
