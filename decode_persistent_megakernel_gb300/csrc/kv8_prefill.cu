@@ -321,6 +321,9 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
       if (row0 >= all) {  // the unit ends in the first tile
         it += u.last - u.first;
         jobs += u.last - u.first;
+        // a phase of a barrier can be told from the one before it only: the first tile's warps say when every score of
+        // the jobs that are passed over here is complete
+        named_sync(3, 2 * TILE);
         continue;
       }
       const int halves = u.rt * ROWS + TILE < all ? 2 : 1;  // row tiles of the unit
@@ -520,6 +523,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
       // ---- the unit's end
       wait(smem_addr(&sm.o_full[tile][1]), (tiles_done - 1) & 1, failed);
       fence_after();
+      if (halves == 1) named_sync(3, 2 * TILE);
       const bool whole = u.first == 0 && u.last == u.tiles;
       float* part = q.part + (size_t)(2 * blockIdx.x + (u.first == 0 ? 1 : 0)) * ROWS * (D + 2);
       const int row = tile * TILE + r;

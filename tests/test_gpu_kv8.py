@@ -335,6 +335,16 @@ def test_prompts_of_a_ragged_batch():
         check_attention(cache, lens, counts, hq, BF16, 500000.0, t=520)
 
 
+@pytest.mark.parametrize("hq,hk,d", [(8, 8, 64), (6, 6, 128), (24, 8, 64)])
+def test_prompts_of_one_and_of_two_row_tiles_in_turn(hq, hk, d):
+    # more units of work than multiprocessors, so that one takes a unit of up to 128 query rows and then a larger one
+    lens = [700 + 37 * (s % 5) for s in range(64)]
+    counts = [(70, 200, 128, 129, 66)[s % 5] for s in range(64)]
+    cache = filled(hk, d, lens, max(lens), E4M3, 64, seed=hq, spread=0.3)
+    check_attention(cache, lens, counts, hq, BF16, 0.0, t=200)
+    check_attention(cache, lens, counts[::-1], hq, BF16, 10000.0, t=200)
+
+
 @pytest.mark.parametrize("hq,hk,d,n,dtype", [(12, 2, 128, 40000, F32), (32, 8, 64, 9001, BF16), (4, 2, 64, 70000, BF16)])
 def test_attention_long_context_is_split_and_joined(hq, hk, d, n, dtype):
     cache = filled(hk, d, [n], n + 7, E4M3, 128, seed=9)
