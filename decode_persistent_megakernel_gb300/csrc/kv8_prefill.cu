@@ -22,6 +22,11 @@
 // Work is dealt out in equal runs over all CTAs by the number of keys that the units see (a causal prompt's
 // last rows see the whole prompt, its first almost nothing); a unit cut by a run's end leaves parts that
 // prefill_merge_kernel joins.
+//
+// Measured: 4096-token prompt, 12 heads of 128 over 2, int8 (51.6 GFLOP): 98 us, 0.27 of the measured bf16 rate; 512 tokens over
+// 8192 keys, 32 heads of 64 over 8, e4m3 (33.3 GFLOP): 67 us, 0.26. Bound by the chain of a row tile: scores from
+// tensor memory, maximum, exponentials, weights, product (about 3800 clocks for 128 keys at 64 dimensions, 5500 at
+// 128), which the other row tile's covers in part. The legacy warp products of kv8_attn.cu took 590 and 192 us.
 #include <algorithm>
 #include <type_traits>
 

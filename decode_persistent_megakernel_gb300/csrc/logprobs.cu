@@ -6,7 +6,8 @@
 // it in 16-byte words, several in flight, and keep their own maximum and sums relative to it; they meet once at
 // the end, the slices in the first CTA's shared memory. Bound by HBM for many rows, by latency for one. (Slices staged in
 // shared memory by bulk copies took 300 to 345 us for 2047 rows of 128256 fp32 logits: with 64 KiB of a row to a CTA, the
-// joins at its end are most of its life. Three CTAs of 40 registers on an SM took 219 us, four of 32 take 199.)
+// joins at its end are most of its life. Three CTAs of 40 registers on an SM took 219 us, four of 32 take 199,
+// 0.79 of the measured copy rate. One row of 128256: 7.4 us; 64 rows of 151936 bf16, 20 alternatives: 11.8.)
 //
 // Alternatives: a slice's values fall to 32 groups of threads; the k-th largest of the groups' maxima is a floor
 // that at least k values reach, and few others do (31 on average for k = 20). Only threads whose maximum reaches it
