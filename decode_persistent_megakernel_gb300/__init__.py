@@ -629,14 +629,11 @@ def logprobs(logits, targets=None, top_k: int = 0, stream=None):
     if targets is not None and (targets.dtype != torch.int32 or targets.shape != (rows,) or targets.device != dev
                                 or not targets.is_contiguous()):
         raise ValueError(f"targets: a contiguous int32 tensor [{rows}] on {dev} is wanted")
-    # one allocation, in pieces of 16 bytes: a step's scores are a few microseconds on the GPU
-    piece, most = -(-rows // 4) * 4, rows * max(top_k, 0)
     with _making(stream, dev):
-        made = torch.empty(2 * piece + 2 * most, dtype=torch.float32, device=dev)
-    logp = made[:rows] if targets is not None else None
-    entropy = made[piece:piece + rows]
-    ids = made[2 * piece:2 * piece + most].view(torch.int32).view(rows, top_k) if top_k > 0 else None
-    top = made[2 * piece + most:].view(rows, top_k) if top_k > 0 else None
+        logp = torch.empty(rows, dtype=torch.float32, device=dev) if targets is not None else None
+        entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+        ids = torch.empty((rows, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
+        top = torch.empty((rows, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
     _call("tinfer_op_logprobs", lib().tinfer_op_logprobs,
           (rows, vocab, _dtype(logits), logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _ptr(targets), top_k,
            _ptr(logp), entropy.data_ptr(), _ptr(ids), _ptr(top)), dev, stream)

@@ -532,6 +532,20 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
         }
       // ---- o^T += V^T weights, 16 keys at a time; an 8 x 8 transpose turns the scores' layout (keys by
       // rows) into that of a right operand (keys down the columns)
+      // The instruction's own sums are cut off, not rounded, which adds up over a long run of keys: two-part operands, whose
+      // precision it would spoil, take a tile's products by themselves (32 sequences of 8000 keys, fp32: off by 4e-7 where
+      // they were off by 2.6e-6, in the same 52 us; at 128 dimensions, whose registers run short, 37 us against 35)
+      float part[SPLIT == 2 ? MD : 1][NG][4];
+      if (SPLIT == 2) {
+#pragma unroll
+        for (int j = 0; j < MD; ++j)
+#pragma unroll
+          for (int n = 0; n < NG; ++n) part[j][n][0] = part[j][n][1] = part[j][n][2] = part[j][n][3] = 0.f;
+      }
+      auto& into = *[&] {
+        if constexpr (SPLIT == 2) return &part;
+        else return &o;
+      }();
 #pragma unroll
       for (int p = 0; p < MK; ++p) {
         uint32_t b[SPLIT][NG][2];
@@ -570,8 +584,16 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
 #pragma unroll
             for (int n = 0; n < NG; ++n)
 #pragma unroll
-              for (int sp = 0; sp < SPLIT; ++sp) mma16816(o[2 * c + h][n], a, b[sp][n][0], b[sp][n][1]);
+              for (int sp = 0; sp < SPLIT; ++sp) mma16816(into[2 * c + h][n], a, b[sp][n][0], b[sp][n][1]);
           }
+      }
+      if (SPLIT == 2) {
+#pragma unroll
+        for (int j = 0; j < MD; ++j)
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][n][i] += into[j][n][i];
       }
       __syncwarp();
       ++got;

@@ -790,8 +790,8 @@ cudaError_t launch_f(AttnParams& q, int head_dim, cudaStream_t st) {
 
 // bf16 rows beyond one row tile of the other kernel, or four at 128 dimensions. fp32 and fp16 rows stay there: their
 // two-part operands keep the precision of their type, which one fp16 operand would not. Here against there, in us, at 40
-// rows of 8 heads of 64: 500 keys 17 : 22, 8000 keys 19 : 30, 32 sequences of 4000 keys 109 : 115; at 24 rows the last
-// takes 108 : 69. Two heads of 128, 64 rows: 23 : 22, 23 : 20, 49 : 65; 128 rows: 26 : 21, 27 : 31, 55 : 106.
+// rows of 8 heads of 64: 500 keys 17 : 22, 8000 keys 19 : 30, 32 sequences of 4000 keys 102 : 115; at 24 rows the last
+// takes 100 : 69. Two heads of 128, 64 rows: 22 : 21, 23 : 20, 50 : 65; 128 rows: 25 : 21, 27 : 31, 57 : 106.
 bool is_prefill(int dtype, int head_dim, long long rows) { return dtype == TINFER_DTYPE_BF16 && rows > (head_dim == 64 ? 32 : 64); }
 size_t prefill_workspace(int head_dim) { return (size_t)MAX_GRID * 2 * PREFILL_ROWS * (head_dim + 2) * 4; }
 

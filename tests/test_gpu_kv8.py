@@ -404,6 +404,22 @@ def test_queries_near_the_types_end(t, dtype):
     assert bool((size < 100).all()) and bool(got.isfinite().all()) and bool(((got - want).abs() <= far).all())
 
 
+@pytest.mark.parametrize("hq,hk,d", [(10, 2, 64), (6, 1, 128)])
+def test_fp32_rows_keep_their_precision_over_many_keys(hq, hk, d):
+    # sums that were cut off at each step would be off by half a step (2^-24) for each of the 200 or more products of 16
+    # keys in a warp's run, one way; rounded sums of tiles stay within a few steps: rms below 2^-20 of the outputs' rms
+    n, seqs = 8000, 40
+    cache = T.Kv8Cache(hk, d, n, n_seqs=seqs)
+    k, v = (normal((1, n, hk, d), i).expand(seqs, n, hk, d).cuda() for i in (1, 2))
+    cache.append(k, v, ints(*[0] * seqs))
+    q = normal((seqs, 1, hq, d), 3)
+    out = cache.attention(q.cuda(), ints(*[n - 1] * seqs))
+    kk, vv = values(cache, 0, n)
+    for s in (0, 17, 39):
+        want, _, _, _ = R.attend(q[s].double(), kk, vv, n - 1)
+        assert float((out[s].cpu().double() - want).square().mean().sqrt() / want.square().mean().sqrt()) <= 2.0 ** -20
+
+
 def test_attention_scales_far_apart():
     # V blocks whose scales span 2^-40 .. 2^40, a block of zeros, one of the smallest scale
     cache = filled(2, 64, [320], 320, INT8, 32, seed=8)
