@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       mx[n][0] = mx[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.f;
     }
+    int e_top = E_MIN;  // of the V scales so far
 
     while (got < put) {
       const int st = got % STAGES;
@@ -449,6 +450,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       // ---- the rows' maxima of x + e = s kf rf + ef. The products stay as they are and the weights scale them again, so
       // that an exponent is rounded once, near 0 where its weight counts
       float vf[MK], vinv[MK], kf[MK], ef[MK];
+      int e_low = E_MAX;
 #pragma unroll
       for (int j = 0; j < MK; ++j) {
         const int b = (rel + 16 * j) >> q.c.lg_block;
@@ -461,6 +463,10 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
         vinv[j] = inv * (float)(1 << WEIGHT_SHIFT);
         kf[j] = ks;
         ef[j] = fine ? (float)e : __uint_as_float(0x7FC00000u);
+        if (fine && 16 * j < keys) {
+          e_low = min(e_low, e);
+          e_top = max(e_top, e);
+        }
       }
       float rf[NG][2];
 #pragma unroll
@@ -506,15 +512,29 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
         for (int n = 0; n < NG; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float shrink = mx[n][h] == now[n][h] ? 1.f : exp2_fast(mx[n][h] - now[n][h]);
+            const float half = half_shrink(mx[n][h], now[n][h]), shrink = half * half;
             mx[n][h] = now[n][h];
-            l[n][h] *= shrink;
+            l[n][h] = l[n][h] * half * half;
 #pragma unroll
             for (int j = 0; j < MD; ++j) {
               o[j][n][h] *= shrink;
               o[j][n][2 + h] *= shrink;
             }
           }
+      }
+      if (e_top - e_low > E_SPAN) {  // the weights would lose keys: the sums take their own exponentials
+#pragma unroll
+        for (int j = 0; j < MK; ++j) {
+          const float back = lifted(vinv[j]);
+          vinv[j] = 0.f;
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float from = mx[n][i & 1] == -INFINITY ? 0.f : mx[n][i & 1];
+              l[n][i & 1] = fmaf(exp2_fast(fmaf(s[j][n][i], kf[j] * rf[n][i & 1], ef[j] - from) + back), 1.f / (1 << SUM_LIFT), l[n][i & 1]);
+            }
+        }
       }
 #pragma unroll
       for (int n = 0; n < NG; ++n)
@@ -689,9 +709,9 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
     float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     auto add = [&](float lw, float mw, const float* y) {
       if (lw == 0.f) return;  // no key of the row
-      const float f = exp2_fast(mw - top);
+      const float half = half_shrink(mw, top), f = half * half;
       const float4 v = *reinterpret_cast<const float4*>(y + row * D + c);
-      sum = fmaf(lw, f, sum);
+      sum = fmaf(lw * half, half, sum);
       acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]); acc[2] = fmaf(v.z, f, acc[2]); acc[3] = fmaf(v.w, f, acc[3]);
     };
     for (int w = w0; w < w1; ++w) add(sm.l[0][w][row], sm.m[0][w][row], reinterpret_cast<const float*>(sm.ring[w][0]));

@@ -24,6 +24,13 @@ constexpr int WEIGHT_SHIFT = 14;    // weights are held times 2^14: fp16 keeps 1
 // sum of the softmax is 2^(WEIGHT_SHIFT - E_MIN) for each key: 2^24 keys stay below fp32's 2^128. A smaller
 // scale's remainder makes its weights smaller than 1, a scale of 0 makes them 0 and counts in the sum.
 constexpr int E_MIN = -85, E_MAX = 120;
+// The sum of the softmax takes a weight 2^(x + e - M) times 2^-e. Where e lies far below the largest exponent that M may
+// come from, that weight falls below 2^-126 and is lost although its key may have the row's largest score: of keys with
+// e no more than E_SPAN below, what is lost is below 2^-40 of the largest score's term. A tile with others
+// sums 2^(x - M) itself, an exponential more for each key: between 2^-107 for the largest score and 2^(WEIGHT_SHIFT -
+// E_MIN), computed times 2^SUM_LIFT so that terms down to 2^-39 of the former stay above 2^-146. (Its exponent may be as large as 2^8 and is
+// rounded there, by 2^-17.) Sums are rescaled in two halves for the same reason: M moves by up to 2^206, the sum by far less.
+constexpr int E_SPAN = 86, SUM_LIFT = 20;
 constexpr long long WAIT_NS = 200LL * 1000 * 1000;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -31,6 +38,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The square root of 2^(from - to): outputs take its square, sums each factor by itself (see E_SPAN).
+__device__ __forceinline__ float half_shrink(float from, float to) {
+  return from == to ? 1.f : exp2_fast(0.5f * (from - to));
+}
+// SUM_LIFT and the exponent of a power of two.
+__device__ __forceinline__ float lifted(float x) { return (float)((int)(__float_as_uint(x) >> 23) - 127 + SUM_LIFT); }
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -126,11 +139,11 @@ __device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int
         for (int k = 0; k < R; ++k) {
           if (lc[k] == 0.f) continue;  // no key of the row
           const float now = fmaxf(top[k], mc[k]);
-          const float a = top[k] == now ? 1.f : exp2_fast(top[k] - now), b = mc[k] == now ? 1.f : exp2_fast(mc[k] - now);
+          const float a = half_shrink(top[k], now), b = half_shrink(mc[k], now);
           top[k] = now;
-          sum[k] = fmaf(lc[k], b, sum[k] * a);
+          sum[k] = fmaf(lc[k] * b, b, sum[k] * a * a);
 #pragma unroll
-          for (int i = 0; i < N; ++i) y[k][i] = fmaf(f[k][i], b, y[k][i] * a);
+          for (int i = 0; i < N; ++i) y[k][i] = fmaf(f[k][i], b * b, y[k][i] * (a * a));
         }
       }
 #pragma unroll
@@ -146,11 +159,11 @@ __device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int
     auto add = [&](float mc, float lc, const float (&f)[N]) {
       if (lc == 0.f) return;  // no key of the row
       const float now = fmaxf(top, mc);
-      const float a = top == now ? 1.f : exp2_fast(top - now), b = mc == now ? 1.f : exp2_fast(mc - now);
+      const float a = half_shrink(top, now), b = half_shrink(mc, now);
       top = now;
-      sum = fmaf(lc, b, sum * a);
+      sum = fmaf(lc * b, b, sum * a * a);
 #pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = fmaf(f[i], b, y[i] * a);
+      for (int i = 0; i < N; ++i) y[i] = fmaf(f[i], b * b, y[i] * (a * a));
     };
     constexpr int R = 8;  // parts of a warp whose loads go out together
     for (int c = warp; c < parts; c += R * NW) {

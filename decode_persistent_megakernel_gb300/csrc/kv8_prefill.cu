@@ -58,6 +58,7 @@ struct Smem {
   alignas(1024) uint8_t v[KV_STAGES][KT * D * 2];
   alignas(16) float2 angle[2][Roles<D>::ANGLES];       // cosines and sines at the tile's tokens
   float4 scale[SCALE_SLOTS][KT / 16];                  // of 16 keys: K scale, V scale's exponent, mantissa, 2^-exponent
+  int apart[SCALE_SLOTS];                              // whether a tile's V scales lie too far below earlier ones (E_SPAN)
   alignas(8) unsigned long long k_full[KV_STAGES], v_full[KV_STAGES], k_empty[KV_STAGES], v_empty[KV_STAGES];
   unsigned long long s_full[3], p_full[3][2], o_full[2][2], q_full[2];  // of score buffers and row tiles, [half of the keys]
   uint32_t tmem;
@@ -440,6 +441,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           // the row's maximum: of each 16 keys' plain products first, whose scale is one
           float4 f[HALF / 16];
           float m[HALF / 16];
+          const bool apart = sm.apart[it % SCALE_SLOTS];
 #pragma unroll
           for (int j = 0; j < HALF / 16; ++j) f[j] = sc[j];
           if (all_seen) {
@@ -465,9 +467,10 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           for (int j = 0; j < HALF / 16; ++j) top = fmaxf(top, fmaf(m[j], f[j].x * scale, f[j].y));
           float shrink = 1.f;
           if (top > ref + GROW || ref == -INFINITY) {  // (also the row's first keys)
-            shrink = ref == -INFINITY ? 1.f : exp2_fast(ref - top);
+            const float half = ref == -INFINITY ? 1.f : half_shrink(ref, top);
+            shrink = half * half;
             ref = top;
-            sum *= shrink;
+            sum = sum * half * half;
           }
           if (__any_sync(~0u, shrink != 1.f)) {
             // the product before has to be complete before its outputs are rescaled
@@ -484,7 +487,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           }
           // weights, over the scores, which are all in registers
           const float from = ref == -INFINITY ? 0.f : ref - (float)SHIFT;
-          auto weights = [&](auto cut) {
+          auto weights = [&](auto cut, auto apart) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               uint32_t w[16];
@@ -493,6 +496,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
                 const float4 g = f[2 * c + j];
                 const float fx = g.x * scale, fy = g.y - from;
                 const float2 f2 = make_float2(fx, fx), g2 = make_float2(fy, fy), v2 = make_float2(g.z, g.z);
+                const float back = lifted(g.w);
                 float2 part = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
@@ -501,19 +505,22 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
                     if (32 * c + 16 * j + i >= n) e.x = -INFINITY;
                     if (32 * c + 16 * j + i + 1 >= n) e.y = -INFINITY;
                   }
+                  if (apart.value) part = add2(part, make_float2(exp2_fast(e.x + back), exp2_fast(e.y + back)));
                   e.x = exp2_fast(e.x);
                   e.y = exp2_fast(e.y);
-                  part = add2(part, e);
+                  if (!apart.value) part = add2(part, e);
                   e = __fmul2_rn(e, v2);
                   w[8 * j + i / 2] = pack_half(e.x, e.y);
                 }
-                sum = fmaf(part.x + part.y, g.w, sum);
+                sum = fmaf(part.x + part.y, apart.value ? 1.f / (1 << SUM_LIFT) : g.w, sum);
               }
               tmem_store16(at + 16 * c, w);
             }
           };
-          if (all_seen) weights(std::false_type{});  // the warp's choice: tensor memory is stored to by whole warps
-          else weights(std::true_type{});
+          // the warp's choice: tensor memory is stored to by whole warps
+          if (apart) weights(std::true_type{}, std::true_type{});
+          else if (all_seen) weights(std::false_type{}, std::false_type{});
+          else weights(std::true_type{}, std::false_type{});
           // With scores ahead, the weights could run a key tile ahead of their products. A phase of a barrier can be
           // told from the one before it only, so every product is seen to be complete before the weights of the
           // next one of its half are given: the waits above and at the unit's end are then never more than one phase off
@@ -622,6 +629,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
         }
       };
       uint4 wk[ITEMS], wv[ITEMS];
+      int e_top = E_MIN;  // of the V scales so far
       load(kp, u.first, wk);
       for (int kt = u.first + 1; kt < u.first + FETCH; ++kt) fetch(kt);
       for (int kt = u.first; kt < u.last; ++kt, ++it) {
@@ -634,6 +642,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
         if (t < KT / 16) {
           const int key = kt * KT + 16 * t;
           float4 f = make_float4(0.f, 0.f, 0.f, 1.f);
+          int e_low = E_MAX, e_high = E_MIN;
           if (key < u.keys) {
             const size_t b = plane * q.c.n_blocks + (key >> q.c.lg_block);
             const float ks = q.c.ks[b], vs = q.c.vs[b];
@@ -641,8 +650,13 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
             const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
             const bool fine = vs < INFINITY;  // a scale that is not finite reaches its scores
             f = make_float4(ks, fine ? (float)e : __uint_as_float(0x7FC00000u), fine && vs > 0.f ? vs * inv : 0.f, inv);
+            if (fine) e_low = e_high = e;
           }
           sm.scale[it % SCALE_SLOTS][t] = f;
+          constexpr unsigned LANES = (1u << (KT / 16)) - 1;
+          e_top = max(e_top, __reduce_max_sync(LANES, e_high));
+          e_low = __reduce_min_sync(LANES, e_low);
+          if (t == 0) sm.apart[it % SCALE_SLOTS] = e_top - e_low > E_SPAN;
         }
         fence_proxy_async_shared();
         __syncwarp();

@@ -432,6 +432,42 @@ def test_attention_scales_far_apart():
     check_attention(cache, [320], [200], 6, BF16, 10000.0)
 
 
+@pytest.mark.parametrize("dtype,t", [(F32, 1), (BF16, 1), (F32, 40), (BF16, 40), (BF16, 100)])
+@pytest.mark.parametrize("far", [45, 70, 110])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 64), (2, 1, 128)])
+def test_blocks_of_zeros_count_beside_blocks_of_huge_values(hq, hk, d, far, dtype, t):
+    # a key whose values are zero has its weight in the softmax whatever the V scales of other keys are: zero and huge
+    # blocks within one tile of keys, and in both orders across tiles
+    n, block = 640, 16
+    zeros, huge = 0.0, 2.0 ** far
+    for row in ([zeros, huge] * 20, [zeros] * 20 + [huge] * 20, [huge] * 20 + [zeros] * 20, [zeros] * 39 + [huge],
+                [huge] + [zeros] * 39, [2.0 ** -60, huge, 2.0 ** -126, zeros] * 10):
+        cache = filled(hk, d, [n], n, INT8, block, seed=far)
+        cache.v_scales[0, :, :n // block] = torch.tensor(row, device="cuda")
+        check_attention(cache, [n], [t], hq, dtype, 10000.0)
+
+
+@pytest.mark.parametrize("dtype,t,n", [(F32, 1, 30000), (BF16, 1, 30000), (BF16, 60, 9200)])
+def test_parts_of_zeros_and_of_huge_values_are_joined(dtype, t, n):
+    # runs of keys in several warps and multiprocessors, some with zeros alone and some with huge values
+    for row in (torch.arange(n // 100) % 7 < 3, torch.arange(n // 100) < n // 150, torch.arange(n // 100) >= n // 150):
+        cache = filled(2, 64, [n], n, INT8, 16, seed=n)
+        cache.v_scales[0] = torch.where(row[torch.arange(n // 16) * 16 // 100], 0.0, 2.0 ** 100).cuda()[None]
+        check_attention(cache, [n], [t], 8, dtype, 0.0)
+
+
+@pytest.mark.parametrize("dtype,t", [(F32, 40), (BF16, 20), (BF16, 100)])
+def test_huge_values_that_a_row_does_not_see_leave_it_alone(dtype, t):
+    # the last block is huge: rows before it have the bits that they have with an ordinary block there
+    n = 200
+    cache = filled(2, 64, [n], n, INT8, 16, seed=5)
+    q = normal((1, t, 8, 64), 6).to(dtype).cuda()
+    want = cache.attention(q, ints(n - t))[:, :t - 8].cpu().double()
+    cache.v_scales[0, :, 192 // 16:] = 2.0 ** 115
+    got = cache.attention(q, ints(n - t))[:, :t - 8].cpu().double()
+    far = 2.0 ** -7 if dtype == BF16 else 2.0 ** -16  # (sums in another order: a few roundings of the type)
+    assert bool(((got - want).abs() <= far * want.abs().amax(dim=-1, keepdim=True)).all())
+
 @pytest.mark.parametrize("dtype,t", [(F32, 40), (BF16, 40), (BF16, 150)])
 def test_a_spoilt_block_reaches_the_rows_that_see_it_alone(dtype, t):
     block, n = 16, 200
