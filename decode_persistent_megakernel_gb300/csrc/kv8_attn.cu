@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv8_merge_kernel(const __grid
   const int head = unit / q.row_tiles, rt = unit % q.row_tiles;
   pdl_wait();  // the parts are complete
   if (count == 0 || parts <= 1) return;  // one CTA had it whole
-  join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * count - rt * ROWS, ROWS), c0, parts, WEIGHT_SHIFT);
+  join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * count - rt * ROWS, ROWS), c0, parts);
 }
 
 // ---------------------------------------------------------------------------------------- host

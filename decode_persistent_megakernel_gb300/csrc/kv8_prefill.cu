@@ -15,9 +15,11 @@
 // The softmax and the second product go by halves of 64 keys, so that the first half's product runs under the
 // second half's exponentials. (Scores by halves as well cost a 128-row operand read twice: 115 us for the 4096-token prompt against 114.)
 //
-// A row's running maximum is replaced only when it would grow by more than 2^8: the outputs in tensor memory
-// are then rescaled by the row's thread, which happens in the first tiles of a row and rarely after. Weights
-// are held times 2^WEIGHT_SHIFT, so they stay below 2^15 and fp16 keeps 11 bits of them down to 2^-14.
+// A row's running maximum is replaced only when it would nearly double: the outputs in tensor memory are then rescaled
+// by the row's thread, after the exponentials, when the product before is done and the scores have left their registers
+// (before them: 112 us for the 4096-token prompt against 105). Weights are held times 2^WEIGHT_SHIFT, below 2^16 with the
+// mantissa of their V scale: fp16 keeps 11 bits of them down to 2^-28 and steps of 2^-38 below. A maximum
+// that may lag behind by 2^4 (2^8) leaves 4 (7) bits less of the keys far below the largest, and takes 103 us (99).
 //
 // Work is dealt out in equal runs over all CTAs by the number of keys that the units see (a causal prompt's
 // last rows see the whole prompt, its first almost nothing); a unit cut by a run's end leaves parts that
@@ -47,8 +49,7 @@ struct Roles {
 };
 constexpr int FETCH = 4;           // key tiles that are fetched into L2 ahead (64 rows of 32 x 4000 keys 111 -> 102 us)
 constexpr int KV_STAGES = 2, SCALE_SLOTS = 4;
-constexpr int SHIFT = 5;           // of the weights
-constexpr float GROW = 8.f;        // a maximum may lag behind by 2^8
+constexpr float GROW = 0.99f;      // a maximum may lag behind by 2^GROW: 2^(WEIGHT_SHIFT + GROW) 2 is below fp16's 65504
 constexpr int FIXED_KEYS = 768;    // what a unit costs beside its keys, in keys (4096-token prompt: 98 us, 109 with 384)
 
 template <int D>
@@ -472,21 +473,8 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
             ref = top;
             sum = sum * half * half;
           }
-          if (__any_sync(~0u, shrink != 1.f)) {
-            // the product before has to be complete before its outputs are rescaled
-            wait(smem_addr(&sm.o_full[tile][h ^ 1]), (h ? tiles_done : tiles_done - 1) & 1, failed);
-            fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_load16(o_at + 16 * c, o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
-              tmem_store16(o_at + 16 * c, o);
-            }
-          }
           // weights, over the scores, which are all in registers
-          const float from = ref == -INFINITY ? 0.f : ref - (float)SHIFT;
+          const float from = ref == -INFINITY ? 0.f : ref - (float)WEIGHT_SHIFT;
           auto weights = [&](auto cut, auto apart) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -525,6 +513,21 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           // told from the one before it only, so every product is seen to be complete before the weights of the
           // next one of its half are given: the waits above and at the unit's end are then never more than one phase off
           wait(smem_addr(&sm.o_full[tile][h]), (tiles_done - 1) & 1, failed);
+          // The outputs are rescaled last, when the product before has had the time of the exponentials to end, and the scores'
+          // registers are free
+          if (__any_sync(~0u, shrink != 1.f)) {
+            wait(smem_addr(&sm.o_full[tile][h ^ 1]), (h ? tiles_done : tiles_done - 1) & 1, failed);
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t o[64];
+              tmem_load64(o_at + 64 * c, o);
+#pragma unroll
+              for (int i = 0; i < 64; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+#pragma unroll
+              for (int i = 0; i < 64; i += 16) tmem_store16(o_at + 64 * c + i, o + i);
+            }
+          }
           tmem_store_wait();
           fence_before();
           __syncwarp();
@@ -578,7 +581,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           part[ROWS * D + row] = ref;
           part[ROWS * D + ROWS + row] = sum;
         } else if (q.lse) {
-          q.lse[((size_t)u.seq * q.sp.n_tokens + tok) * q.n_heads + hq] = (log2f(sum) + ref - (float)SHIFT) * 0.6931471805599453f;
+          q.lse[((size_t)u.seq * q.sp.n_tokens + tok) * q.n_heads + hq] = (log2f(sum) + ref - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
         }
       }
     }
@@ -766,7 +769,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) prefill_merge_kernel(const __
   }
   pdl_wait();
   if (parts <= 1) return;
-  join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * sp.count - rt * ROWS, ROWS), c0, parts, SHIFT);
+  join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * sp.count - rt * ROWS, ROWS), c0, parts);
 }
 
 template <int FMT, int D, typename T>

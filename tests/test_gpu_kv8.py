@@ -468,6 +468,24 @@ def test_huge_values_that_a_row_does_not_see_leave_it_alone(dtype, t):
     far = 2.0 ** -7 if dtype == BF16 else 2.0 ** -16  # (sums in another order: a few roundings of the type)
     assert bool(((got - want).abs() <= far * want.abs().amax(dim=-1, keepdim=True)).all())
 
+@pytest.mark.parametrize("t,d", [(1, 64), (100, 64), (1, 128), (100, 128)])
+@pytest.mark.parametrize("below", [20.3, 22.4, 25.55, 28.7, 30.6, 33.4])
+def test_many_keys_far_below_the_leading_one(below, t, d):
+    # the first key has all but n 2^-below of the weight and values of 0: what comes out is the tail's sum, whose
+    # weights are held to 2^-39 of the largest
+    n = 600
+    cache = T.Kv8Cache(1, d, n, block=16)
+    k, v = torch.zeros(1, n, 1, d), torch.ones(1, n, 1, d)
+    k[0, 0], v[0, 0] = 1.0, 0.0
+    cache.append(k.cuda(), v.cuda(), ints(0))
+    cache.k_scales[0, 0, 0] = below / math.log2(math.e) / math.sqrt(d) / 448
+    q = torch.ones(1, t, 2, d)
+    got = cache.attention(q.to(BF16).cuda(), ints(n - t))[0].cpu().double()
+    kk, vv = values(cache, 0, n)
+    want, _, size, mean = R.attend(q[0].double(), kk, vv, n - t)
+    far, _ = R.attend_bounds(want, size, mean, d, n, BF16, v_top(cache, 0, n))
+    assert bool(((got - want).abs() <= far).all()), float((got / want - 1).abs().max())
+
 @pytest.mark.parametrize("dtype,t", [(F32, 40), (BF16, 40), (BF16, 150)])
 def test_a_spoilt_block_reaches_the_rows_that_see_it_alone(dtype, t):
     block, n = 16, 200
