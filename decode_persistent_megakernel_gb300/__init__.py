@@ -26,6 +26,7 @@ TINFER_S_INFLIGHT, TINFER_S_INFLIGHT_LM, TINFER_S_L2_LOOKAHEAD, TINFER_S_L2_PACE
 TINFER_SYNC_STAMPS, TINFER_SYNC_GRID_BARRIER = 0, 1
 TINFER_NOALLOC_SCRATCH_BYTES = 1 << 20
 TINFER_KV8_E4M3, TINFER_KV8_INT8 = 0, 1
+TINFER_KV8_DEBUG_WITHHOLD = 0x200
 TINFER_DTYPE_F32, TINFER_DTYPE_F16, TINFER_DTYPE_BF16 = range(3)
 TRACE_FIELDS = 10  # stamps per CTA and phase of the timeline (tinfer_set_trace)
 

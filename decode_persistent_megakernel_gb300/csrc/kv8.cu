@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ R
 bool cache_of(const tinfer_kv8* c, Cache& out, tinfer_status& st) {
   st = TINFER_ERR_INVALID_ARG;
   if (!c || !c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return false;
-  if ((c->format != E4M3 && c->format != INT8) || c->n_seqs < 1 || c->n_kv_heads < 1 || c->max_ctx < 1) return false;
+  if ((format_of(c) != E4M3 && format_of(c) != INT8) || c->n_seqs < 1 || c->n_kv_heads < 1 || c->max_ctx < 1) return false;
   if (c->block < 16 || c->block > 128 || (c->block & (c->block - 1))) return false;
   if ((reinterpret_cast<uintptr_t>(c->k_codes) & 15) || (reinterpret_cast<uintptr_t>(c->v_codes) & 15) ||
       (reinterpret_cast<uintptr_t>(c->k_scales) & 3) || (reinterpret_cast<uintptr_t>(c->v_scales) & 3))
@@ -315,7 +315,7 @@ tinfer_status tinfer_op_kv8_append(const tinfer_kv8* cache, const tinfer_rows* k
   cudaStream_t st = (cudaStream_t)stream;
   if (status_dev && cudaMemsetAsync(status_dev, 0, 4, st) != cudaSuccess) return TINFER_ERR_CUDA;
   cudaError_t e;
-  if (cache->format == kv8::E4M3)
+  if (kv8::format_of(cache) == kv8::E4M3)
     e = cache->head_dim == 64 ? kv8::launch_append<kv8::E4M3, 64>(q, k->dtype, st) : kv8::launch_append<kv8::E4M3, 128>(q, k->dtype, st);
   else
     e = cache->head_dim == 64 ? kv8::launch_append<kv8::INT8, 64>(q, k->dtype, st) : kv8::launch_append<kv8::INT8, 128>(q, k->dtype, st);
@@ -336,7 +336,7 @@ tinfer_status tinfer_op_kv8_read(const tinfer_kv8* cache, int n_tokens, const in
   cudaStream_t st = (cudaStream_t)stream;
   if (status_dev && cudaMemsetAsync(status_dev, 0, 4, st) != cudaSuccess) return TINFER_ERR_CUDA;
   cudaError_t e;
-  if (cache->format == kv8::E4M3)
+  if (kv8::format_of(cache) == kv8::E4M3)
     e = cache->head_dim == 64 ? kv8::launch_read<kv8::E4M3, 64>(q, k->dtype, st) : kv8::launch_read<kv8::E4M3, 128>(q, k->dtype, st);
   else
     e = cache->head_dim == 64 ? kv8::launch_read<kv8::INT8, 64>(q, k->dtype, st) : kv8::launch_read<kv8::INT8, 128>(q, k->dtype, st);

@@ -178,6 +178,7 @@ __device__ __forceinline__ uint32_t floats_to_codes(float a, float b, float c, f
 }
 
 // ---- host side, shared by the entry points (kv8.cu) ----------------------------------------------
+inline int format_of(const tinfer_kv8* c) { return c->format & ~TINFER_KV8_DEBUG_WITHHOLD; }
 bool cache_of(const tinfer_kv8* c, Cache& out, tinfer_status& st);
 struct Extent {
   int seqs, tokens, heads, head_dim;

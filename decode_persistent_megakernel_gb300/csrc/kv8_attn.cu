@@ -283,7 +283,9 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   in.seek(q, list, lo);
   int put = 0, got = 0;
   const uint64_t policy = q.keep_l2 ? policy_evict_normal() : policy_evict_first();
+  volatile int* failed = &sm.failed;
   auto issue = [&]() {  // the next tile that has keys to read goes into the ring
+    if (__any_sync(~0u, *failed)) return;  // what is under way is still waited for, a ring's tiles at most
     while (in.x < hi && (in.tile < 0 || in.tile * KT >= in.limit)) in.next(q, list, hi);
     if (in.x >= hi) return;
     const int st = put % STAGES, key0 = in.tile * KT, keys = min(in.limit - key0, KT);
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       cp_async_4(smem_addr(&sm.ring_scale[warp][st][0][lane]), q.c.ks + at);
       cp_async_4(smem_addr(&sm.ring_scale[warp][st][1][lane]), q.c.vs + at);
     }
-    cp_async_arrive(bar);
+    if (!(q.withhold && put == 0 && lane == 31)) cp_async_arrive(bar);
     ++put;
     in.next(q, list, hi);
   };
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       const int4 slot = sm.slot[warp][st];
       if (slot.x >= seg_end) break;
       const int key0 = slot.y, keys = slot.z;
-      if (!wait_bounded(smem_addr(&sm.full[warp][st]), (got / STAGES) & 1)) sm.failed = 1;
+      if (!wait_bounded(smem_addr(&sm.full[warp][st]), (got / STAGES) & 1, q.wait_us)) *failed = 1;
       uint8_t* kbuf = sm.ring[warp][st];
       uint8_t* vbuf = kbuf + KT * D;
       if (keys < KT) {  // rows past the copy: weights there are 0, so V must be finite
@@ -736,7 +738,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       }
     }
   }
-  if (tid == 0 && sm.failed && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
+  if (tid == 0 && *failed && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
 }
 
 // Joins the units that several CTAs hold: CTA (unit of a sequence, slice of its rows). It is launched with the kernel
@@ -887,6 +889,8 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   q.row_tiles = (int)row_tiles;
   q.units = (int)units;
   q.keep_l2 = row_tiles > 1;
+  q.withhold = (cache->format & TINFER_KV8_DEBUG_WITHHOLD) != 0;
+  q.wait_us = q.withhold ? kv8::WAIT_US_WITHHELD : kv8::WAIT_US;
   int sms = 0;
   if (!kv8::device_sms(sms)) return TINFER_ERR_CUDA;
   q.grid = std::min(sms, kv8::MAX_GRID);
@@ -894,9 +898,9 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   if (status_dev && cudaMemsetAsync(status_dev, 0, 4, st) != cudaSuccess) return TINFER_ERR_CUDA;
   cudaError_t e;
   if (prefill)
-    e = kv8::launch_prefill(q, cache->format, cache->head_dim, st);
+    e = kv8::launch_prefill(q, kv8::format_of(cache), cache->head_dim, st);
   else
-    e = cache->format == kv8::E4M3 ? kv8::launch_f<kv8::E4M3>(q, cache->head_dim, per, q_rows->dtype, st)
+    e = kv8::format_of(cache) == kv8::E4M3 ? kv8::launch_f<kv8::E4M3>(q, cache->head_dim, per, q_rows->dtype, st)
                                    : kv8::launch_f<kv8::INT8>(q, cache->head_dim, per, q_rows->dtype, st);
   return e == cudaSuccess ? TINFER_OK : TINFER_ERR_CUDA;
 }

@@ -16,6 +16,7 @@ struct AttnParams {
   float* part;   // workspace: two parts of each CTA, one of each warp; a part is [rows][d] outputs, [rows] maxima, [rows] sums
   int n_heads, group, row_tiles, units;  // units: KV heads x row tiles
   int grid, warps, keep_l2;  // warps of a CTA
+  int wait_us, withhold;     // limit of a wait; test hook: one arrival of each pipeline stays away
   float scale_log2;  // log2(e) / sqrt(d)
 };
 
@@ -31,7 +32,7 @@ constexpr int E_MIN = -85, E_MAX = 120;
 // E_MIN), computed times 2^SUM_LIFT so that terms down to 2^-39 of the former stay above 2^-146. (Its exponent may be as large as 2^8 and is
 // rounded there, by 2^-17.) Sums are rescaled in two halves for the same reason: M moves by up to 2^206, the sum by far less.
 constexpr int E_SPAN = 86, SUM_LIFT = 20;
-constexpr long long WAIT_NS = 200LL * 1000 * 1000;
+constexpr int WAIT_US = 200 * 1000, WAIT_US_WITHHELD = 5 * 1000;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -75,11 +76,11 @@ __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int limit_us) {
   if (mbar_sleep(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   while (!mbar_sleep(bar, parity))
-    if ((long long)(globaltimer() - t0) > WAIT_NS) return mbar_sleep(bar, parity);  // (time may have passed off the GPU)
+    if ((long long)(globaltimer() - t0) > limit_us * 1000LL) return mbar_sleep(bar, parity);  // (time may have passed off the GPU)
   return true;
 }
 

@@ -61,7 +61,7 @@ struct Smem {
   float4 scale[SCALE_SLOTS][KT / 16];                  // of 16 keys: K scale, V scale's exponent, mantissa, 2^-exponent
   int apart[SCALE_SLOTS];                              // whether a tile's V scales lie too far below earlier ones (E_SPAN)
   alignas(8) unsigned long long k_full[KV_STAGES], v_full[KV_STAGES], k_empty[KV_STAGES], v_empty[KV_STAGES];
-  unsigned long long s_full[3], p_full[3][2], o_full[2][2], q_full[2];  // of score buffers and row tiles, [half of the keys]
+  unsigned long long s_full[3], p_full[3][2], o_full[2][2], q_full[2], drained;  // of score buffers and row tiles, [half of the keys]
   uint32_t tmem;
   int failed;
 };
@@ -254,16 +254,18 @@ __device__ __forceinline__ void tmem_store16(uint32_t a, const uint32_t* u) {
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A wait that gives up at once when another role has: every role then runs through its loops without waiting.
-__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+struct Failed {
+  volatile int* flag;
+  int limit_us;
+};
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, const Failed& failed) {
   if (mbar_sleep(bar, parity)) return;
   const uint64_t t0 = globaltimer();
-  while (!mbar_sleep(bar, parity)) {
-    if (*failed) return;
-    if ((long long)(globaltimer() - t0) > WAIT_NS) {
-      if (!mbar_sleep(bar, parity)) *failed = 1;  // (time may have passed off the GPU)
+  while (!*failed.flag && !mbar_sleep(bar, parity))
+    if ((long long)(globaltimer() - t0) > failed.limit_us * 1000LL) {
+      if (!mbar_sleep(bar, parity)) *failed.flag = 1;  // (time may have passed off the GPU)
       return;
     }
-  }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -299,6 +301,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
       for (int h = 0; h < 2; ++h) mbar_init(smem_addr(&sm.o_full[t][h]), 1);
       mbar_init(smem_addr(&sm.q_full[t]), 4);
     }
+    mbar_init(smem_addr(&sm.drained), 1);
     sm.failed = 0;
     mbar_fence_init();
   }
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
   const long long total = build_prefix<NT>(q, prefix);  // ends with a barrier
   fence_after();
   const uint32_t tmem = sm.tmem;
-  volatile int* failed = &sm.failed;
+  const Failed failed{&sm.failed, q.wait_us};
   const long long per = run_length(total, gridDim.x);
   Walk u;
   u.init(min(per * blockIdx.x, total), min(per * (blockIdx.x + 1), total));
@@ -663,7 +666,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
         }
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.k_full[st]));
+        if (lane == 0 && !(q.withhold && t == 0 && it == 0)) mbar_arrive(smem_addr(&sm.k_full[st]));
         if (kt + 1 < u.last) load(kp, kt + 1, wk);
         wait(smem_addr(&sm.v_empty[st]), parity, failed);
         widen(smem_addr(sm.v[st]), wv, kt);
@@ -749,7 +752,13 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
   }
   fence_before();
   __syncthreads();
-  if (tid == 0 && sm.failed && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
+  if (*failed.flag) {
+    if (tid == 0 && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
+    if (warp == WARP_MMA) {  // products that nobody waited for are not to run on in memory that is given back
+      commit(elect(), smem_addr(&sm.drained));
+      wait_bounded(smem_addr(&sm.drained), 0, q.wait_us);
+    }
+  }
   if (warp == WARP_MMA) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 

@@ -389,6 +389,9 @@ tinfer_status tinfer_op_attention_noalloc(int n_heads, int n_kv_heads, int head_
  * TINFER_ERR_UNSUPPORTED before anything is launched.
  * --------------------------------------------------------------------------------------------- */
 enum { TINFER_KV8_E4M3 = 0, TINFER_KV8_INT8 = 1 };                                /* format */
+/* Test hook, added to format: in an attention over the cache each pipeline misses one arrival (its copies and
+ * products all complete), so that a wait runs out, here after 5 ms instead of 200. */
+enum { TINFER_KV8_DEBUG_WITHHOLD = 0x200 };
 enum { TINFER_DTYPE_F32 = 0, TINFER_DTYPE_F16 = 1, TINFER_DTYPE_BF16 = 2 };       /* element types */
 
 typedef struct {
@@ -431,7 +434,8 @@ tinfer_status tinfer_op_kv8_read(const tinfer_kv8* cache, int n_tokens, const in
  * overlap of the two is sound. lse_dev: fp32 [n_seqs][n_tokens][n_heads], may be NULL: the natural
  * logarithm of the sum of exp(score). workspace_dev: tinfer_kv8_attention_workspace bytes of device
  * memory, 16-byte aligned, no initial values; calls that may overlap in time (other streams, other
- * graphs) need one each. Bit 1 of *status_dev: a device wait ran out, and the outputs are not valid.
+ * graphs) need one each. Bit 1 of *status_dev: a device wait (200 ms at most) ran
+ * out, and the outputs are not valid; the kernel starts no more work then and ends.
  * n_seqs * n_kv_heads * max_ctx below 2^31, the query rows of a KV head at most 2^30, and their number in units of
  * work (row tiles times key tiles of max_ctx) below 2^30, else TINFER_ERR_UNSUPPORTED.
  * tinfer_kv8_attention_workspace returns 0 for a cache or counts that every call would refuse. */

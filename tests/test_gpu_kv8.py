@@ -689,6 +689,29 @@ def test_a_prefix_kept_in_8_bits_goes_back_to_the_engine():
     b.close()
 
 
+@pytest.mark.parametrize("hq,hk,d,t,dtype", [(8, 2, 64, 1, BF16), (32, 8, 64, 5, F32), (12, 2, 128, 1, F16), (8, 2, 64, 200, BF16),
+                                             (12, 2, 128, 300, BF16), (8, 8, 64, 64, BF16)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(hq, hk, d, t, dtype):
+    # one arrival of each pipeline stays away (every copy and product completes): the kernel gives up after 5 ms, issues
+    # nothing more and ends. Runs are tens of tiles long, and a limit for each of them would take seconds
+    import time
+    n = 40000
+    cache = filled(hk, d, [n], n, E4M3, 64, seed=3)
+    q = normal((1, t, hq, d), 4).to(dtype).cuda()
+    pos, status = ints(n - t), ints(0)
+    want = cache.attention(q, pos, status=status)
+    assert int(status) == 0
+    cache.c.format |= T.TINFER_KV8_DEBUG_WITHHOLD
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    cache.attention(q, pos, out=out, status=status)
+    torch.cuda.synchronize()
+    took = time.perf_counter() - t0
+    assert int(status) == 2 and took < 0.5, took
+    cache.c.format &= ~T.TINFER_KV8_DEBUG_WITHHOLD
+    assert torch.equal(cache.attention(q, pos, status=status), want) and int(status) == 0
+
 def test_python_layer_refuses_bad_tensors():
     cache = T.Kv8Cache(2, 64, 100, n_seqs=2)
     x, pos = torch.zeros(2, 3, 2, 64, device="cuda"), ints(0, 0)
