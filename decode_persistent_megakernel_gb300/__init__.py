@@ -26,7 +26,7 @@ TINFER_S_INFLIGHT, TINFER_S_INFLIGHT_LM, TINFER_S_L2_LOOKAHEAD, TINFER_S_L2_PACE
 TINFER_SYNC_STAMPS, TINFER_SYNC_GRID_BARRIER = 0, 1
 TINFER_NOALLOC_SCRATCH_BYTES = 1 << 20
 TINFER_KV8_E4M3, TINFER_KV8_INT8 = 0, 1
-TINFER_KV8_DEBUG_WITHHOLD = 0x200
+TINFER_KV8_KEEP_STATUS, TINFER_KV8_DEBUG_WITHHOLD = 0x100, 0x200
 TINFER_DTYPE_F32, TINFER_DTYPE_F16, TINFER_DTYPE_BF16 = range(3)
 TRACE_FIELDS = 10  # stamps per CTA and phase of the timeline (tinfer_set_trace)
 
@@ -515,7 +515,11 @@ class Kv8Cache:
 
     The cache keeps one workspace for the attention, large enough for every call (workspace_bytes(): 22 or 43 MB at
     head_dim 64 or 128): `workspace`, a uint8 tensor that the caches of several layers may share, or a new one. A call
-    that may overlap another one in time (another stream, a graph replayed beside it) passes one of its own."""
+    that may overlap another one in time (another stream, a graph replayed beside it) passes one of its own.
+
+    Calls report into `status`, an int32 tensor that each call clears, or, without one, into a word of the cache that
+    error() reads. Bit 0: positions of a sequence were outside the cache; bit 1: a wait on the device ran out, and the
+    attention's results are not valid."""
 
     def __init__(self, n_kv_heads: int, head_dim: int, max_ctx: int, n_seqs: int = 1, fmt: int = TINFER_KV8_E4M3,
                  block: int = 64, device="cuda", buffers=None, workspace=None):
@@ -540,13 +544,15 @@ class Kv8Cache:
                 raise ValueError(f"{what} is not contiguous")
         self.n_seqs, self.n_kv_heads, self.head_dim, self.max_ctx = n_seqs, n_kv_heads, head_dim, max_ctx
         self._int32, self._uint8 = torch.int32, torch.uint8
-        self.c = tinfer_kv8(fmt, n_seqs, n_kv_heads, head_dim, max_ctx, block, *(t.data_ptr() for t in buffers))
+        self.c, self._kept = (tinfer_kv8(f, n_seqs, n_kv_heads, head_dim, max_ctx, block, *(t.data_ptr() for t in buffers))
+                              for f in (fmt, fmt | TINFER_KV8_KEEP_STATUS))
         need = self.workspace_bytes(n_kv_heads, 1)
         if need == 0:
             raise TinferError(TINFER_ERR_UNSUPPORTED, "Kv8Cache")
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         self._workspace = self._check_workspace(workspace)
+        self._errors = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def _rows(self, what, t, heads=None, tokens=None) -> tinfer_rows:
         s = t.shape
@@ -568,12 +574,27 @@ class Kv8Cache:
             raise ValueError(f"{what}: a contiguous int32 tensor of {n} on {self.device} is wanted")
         return t.data_ptr()
 
+    def _status(self, status):
+        """The cache's structure and the address of the status word of a call."""
+        return (self._kept, self._errors.data_ptr()) if status is None else (self.c, self._ints("status", status, 1))
+
+    def error(self) -> int:
+        """Status bits of all calls without a `status` of their own since the last error(). Waits for the device."""
+        import torch
+        torch.cuda.synchronize(self.device)
+        bits = int(self._errors)
+        if bits:
+            self._errors.zero_()
+            torch.cuda.synchronize(self.device)
+        return bits
+
     def append(self, k, v, pos, counts=None, rope_theta: float = 0.0, status=None, stream=None) -> None:
         """Quantises rows k and v into the cache at pos (keys rotated first; rope_theta 0: they already are)."""
         kr, vr = self._rows("k", k, self.n_kv_heads), self._rows("v", v, self.n_kv_heads, k.shape[1])
+        c, word = self._status(status)
         _call("tinfer_op_kv8_append", lib().tinfer_op_kv8_append,
-              (self.c, kr, vr, k.shape[1], self._ints("pos", pos, self.n_seqs), self._ints("counts", counts, self.n_seqs),
-               rope_theta, self._ints("status", status, 1)), self.device, stream)
+              (c, kr, vr, k.shape[1], self._ints("pos", pos, self.n_seqs), self._ints("counts", counts, self.n_seqs),
+               rope_theta, word), self.device, stream)
 
     def read(self, n_tokens: int, pos, counts=None, out=None, dtype=None, status=None, stream=None):
         """Reads n_tokens tokens of each sequence from pos on back into rows (k, v): `out`, or new ones of dtype
@@ -584,9 +605,10 @@ class Kv8Cache:
                 out = tuple(torch.zeros((self.n_seqs, n_tokens, self.n_kv_heads, self.head_dim),
                                         dtype=dtype or torch.bfloat16, device=self.device) for _ in range(2))
         kr, vr = (self._rows(what, t, self.n_kv_heads, n_tokens) for what, t in zip(("k", "v"), out))
+        c, word = self._status(status)
         _call("tinfer_op_kv8_read", lib().tinfer_op_kv8_read,
-              (self.c, n_tokens, self._ints("pos", pos, self.n_seqs), self._ints("counts", counts, self.n_seqs), kr, vr,
-               self._ints("status", status, 1)), self.device, stream)
+              (c, n_tokens, self._ints("pos", pos, self.n_seqs), self._ints("counts", counts, self.n_seqs), kr, vr, word),
+              self.device, stream)
         return out
 
     def workspace_bytes(self, n_heads: int | None = None, n_tokens: int = 1) -> int:
@@ -611,10 +633,10 @@ class Kv8Cache:
                                 or not lse.is_contiguous()):
             raise ValueError("lse: a contiguous float32 tensor [n_seqs, n_tokens, n_heads] is wanted")
         workspace = self._workspace if workspace is None else self._check_workspace(workspace)
+        c, word = self._status(status)
         _call("tinfer_op_kv8_attention", lib().tinfer_op_kv8_attention,
-              (self.c, n_heads, n_tokens, qr, self._ints("pos", pos, self.n_seqs), self._ints("counts", counts, self.n_seqs),
-               rope_theta, orow, _ptr(lse), workspace.data_ptr(), workspace.numel(), self._ints("status", status, 1)),
-              self.device, stream)
+              (c, n_heads, n_tokens, qr, self._ints("pos", pos, self.n_seqs), self._ints("counts", counts, self.n_seqs),
+               rope_theta, orow, _ptr(lse), workspace.data_ptr(), workspace.numel(), word), self.device, stream)
         return out
 
 

@@ -244,6 +244,10 @@ bool words_of(std::initializer_list<const void*> pointers) {
   return true;
 }
 
+bool clear_status(const tinfer_kv8* c, int32_t* status_dev, cudaStream_t st) {
+  return !status_dev || (c->format & TINFER_KV8_KEEP_STATUS) || cudaMemsetAsync(status_dev, 0, 4, st) == cudaSuccess;
+}
+
 bool rope_of(double theta, int head_dim, Rope& out) {
   out.on = theta != 0.0;
   if (!out.on) return true;
@@ -313,7 +317,7 @@ tinfer_status tinfer_op_kv8_append(const tinfer_kv8* cache, const tinfer_rows* k
   if (k->dtype != v->dtype || !kv8::rope_of(rope_theta, cache->head_dim, q.rope)) return TINFER_ERR_INVALID_ARG;
   q.sp = kv8::Span{pos_dev, counts_dev, n_tokens, status_dev};
   cudaStream_t st = (cudaStream_t)stream;
-  if (status_dev && cudaMemsetAsync(status_dev, 0, 4, st) != cudaSuccess) return TINFER_ERR_CUDA;
+  if (!kv8::clear_status(cache, status_dev, st)) return TINFER_ERR_CUDA;
   cudaError_t e;
   if (kv8::format_of(cache) == kv8::E4M3)
     e = cache->head_dim == 64 ? kv8::launch_append<kv8::E4M3, 64>(q, k->dtype, st) : kv8::launch_append<kv8::E4M3, 128>(q, k->dtype, st);
@@ -334,7 +338,7 @@ tinfer_status tinfer_op_kv8_read(const tinfer_kv8* cache, int n_tokens, const in
   if (k->dtype != v->dtype) return TINFER_ERR_INVALID_ARG;
   q.sp = kv8::Span{pos_dev, counts_dev, n_tokens, status_dev};
   cudaStream_t st = (cudaStream_t)stream;
-  if (status_dev && cudaMemsetAsync(status_dev, 0, 4, st) != cudaSuccess) return TINFER_ERR_CUDA;
+  if (!kv8::clear_status(cache, status_dev, st)) return TINFER_ERR_CUDA;
   cudaError_t e;
   if (kv8::format_of(cache) == kv8::E4M3)
     e = cache->head_dim == 64 ? kv8::launch_read<kv8::E4M3, 64>(q, k->dtype, st) : kv8::launch_read<kv8::E4M3, 128>(q, k->dtype, st);

@@ -178,7 +178,8 @@ __device__ __forceinline__ uint32_t floats_to_codes(float a, float b, float c, f
 }
 
 // ---- host side, shared by the entry points (kv8.cu) ----------------------------------------------
-inline int format_of(const tinfer_kv8* c) { return c->format & ~TINFER_KV8_DEBUG_WITHHOLD; }
+inline int format_of(const tinfer_kv8* c) { return c->format & ~(TINFER_KV8_KEEP_STATUS | TINFER_KV8_DEBUG_WITHHOLD); }
+bool clear_status(const tinfer_kv8* c, int32_t* status_dev, cudaStream_t st);
 bool cache_of(const tinfer_kv8* c, Cache& out, tinfer_status& st);
 struct Extent {
   int seqs, tokens, heads, head_dim;

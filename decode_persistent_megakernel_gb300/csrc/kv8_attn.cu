@@ -895,7 +895,7 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   if (!kv8::device_sms(sms)) return TINFER_ERR_CUDA;
   q.grid = std::min(sms, kv8::MAX_GRID);
   cudaStream_t st = (cudaStream_t)stream;
-  if (status_dev && cudaMemsetAsync(status_dev, 0, 4, st) != cudaSuccess) return TINFER_ERR_CUDA;
+  if (!kv8::clear_status(cache, status_dev, st)) return TINFER_ERR_CUDA;
   cudaError_t e;
   if (prefill)
     e = kv8::launch_prefill(q, kv8::format_of(cache), cache->head_dim, st);

@@ -381,7 +381,7 @@ tinfer_status tinfer_op_attention_noalloc(int n_heads, int n_kv_heads, int head_
  * device when the kernels run: token i < counts[s] of sequence s stands at position pos[s] + i. So a call
  * captured in a CUDA graph follows the positions from replay to replay. A sequence whose positions are
  * outside [0, max_ctx), or its count outside [0, n_tokens], is passed over: nothing of it is read or
- * written, and bit 0 of *status_dev is set (int32, may be NULL; cleared first). Rows of tokens at or
+ * written, and bit 0 of *status_dev is set (int32, may be NULL; cleared first unless TINFER_KV8_KEEP_STATUS). Rows of tokens at or
  * past counts[s] are neither read nor written. Every call is asynchronous on `stream`, allocates nothing
  * and keeps no state between calls. rope_theta: the base of the rotary positions applied to keys as they
  * are stored and to queries (half-split pairs, as in the decode step); 0: rows come already rotated;
@@ -389,6 +389,8 @@ tinfer_status tinfer_op_attention_noalloc(int n_heads, int n_kv_heads, int head_
  * TINFER_ERR_UNSUPPORTED before anything is launched.
  * --------------------------------------------------------------------------------------------- */
 enum { TINFER_KV8_E4M3 = 0, TINFER_KV8_INT8 = 1 };                                /* format */
+/* Added to format: *status_dev is not cleared first, so that one word gathers what happens in many calls. */
+enum { TINFER_KV8_KEEP_STATUS = 0x100 };
 /* Test hook, added to format: in an attention over the cache each pipeline misses one arrival (its copies and
  * products all complete), so that a wait runs out, here after 5 ms instead of 200. */
 enum { TINFER_KV8_DEBUG_WITHHOLD = 0x200 };

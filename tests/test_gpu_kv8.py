@@ -712,6 +712,26 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(hq, hk, d, 
     cache.c.format &= ~T.TINFER_KV8_DEBUG_WITHHOLD
     assert torch.equal(cache.attention(q, pos, status=status), want) and int(status) == 0
 
+def test_the_cache_gathers_what_calls_without_a_status_report():
+    cache = filled(2, 64, [500], 500, E4M3, 64, seed=3)
+    q, x = normal((1, 3, 8, 64), 4).cuda(), normal((1, 3, 2, 64), 5).cuda()
+    assert cache.error() == 0
+    cache.attention(q, ints(498))  # past the end
+    cache.attention(q, ints(400))  # a good call does not clear it
+    assert cache.error() == 1 and cache.error() == 0
+    cache.append(x, x, ints(-1))
+    status = ints(7)
+    cache.append(x, x, ints(0), status=status)
+    assert int(status) == 0 and cache.error() == 1
+    cache.read(3, ints(499), status=status)
+    assert int(status) == 1 and cache.error() == 0
+    cache._kept.format |= T.TINFER_KV8_DEBUG_WITHHOLD
+    cache.attention(q, ints(400))
+    cache._kept.format &= ~T.TINFER_KV8_DEBUG_WITHHOLD
+    cache.read(3, ints(499))
+    assert cache.error() == 3 and cache.error() == 0
+    assert cache.attention(q, ints(400)).isfinite().all() and cache.error() == 0
+
 def test_python_layer_refuses_bad_tensors():
     cache = T.Kv8Cache(2, 64, 100, n_seqs=2)
     x, pos = torch.zeros(2, 3, 2, 64, device="cuda"), ints(0, 0)
