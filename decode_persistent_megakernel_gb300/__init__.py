@@ -530,8 +530,6 @@ class Kv8Cache:
             device = torch.device(device)
             buffers = tuple(torch.zeros(codes, dtype=torch.uint8, device=device) for _ in range(2)) + tuple(
                 torch.zeros(scales, dtype=torch.float32, device=device) for _ in range(2))
-            if device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
-                torch.cuda.current_stream(device).synchronize()  # the zeros come before an append on any stream
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = buffers
         self.device = self.k_codes.device
         if self.device.type != "cuda":
@@ -553,6 +551,10 @@ class Kv8Cache:
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         self._workspace = self._check_workspace(workspace)
         self._errors = torch.zeros(1, dtype=torch.int32, device=self.device)
+        if not torch.cuda.is_current_stream_capturing():
+            # calls may come on any stream: the zeros, and what the current stream still does with memory that is the
+            # workspace now, come before them
+            torch.cuda.current_stream(self.device).synchronize()
 
     def _rows(self, what, t, heads=None, tokens=None) -> tinfer_rows:
         s = t.shape

@@ -732,6 +732,19 @@ def test_the_cache_gathers_what_calls_without_a_status_report():
     assert cache.error() == 3 and cache.error() == 0
     assert cache.attention(q, ints(400)).isfinite().all() and cache.error() == 0
 
+def test_a_cache_over_given_buffers_is_ready_for_any_stream():
+    a = filled(2, 64, [300], 300, E4M3, 64, seed=3)
+    q, pos, s = normal((1, 3, 8, 64), 4).cuda(), ints(299), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    tmp = torch.empty(a.workspace_bytes(), dtype=torch.uint8, device="cuda").fill_(7)
+    del tmp  # its memory may be the workspace's, and the fill is yet to come
+    b = T.Kv8Cache(2, 64, 300, buffers=(a.k_codes, a.v_codes, a.k_scales, a.v_scales))
+    assert torch.cuda.current_stream().query()
+    b.attention(q, pos, stream=s)  # past the end: reported
+    torch.cuda.synchronize()
+    assert b.error() == 1
+
 def test_python_layer_refuses_bad_tensors():
     cache = T.Kv8Cache(2, 64, 100, n_seqs=2)
     x, pos = torch.zeros(2, 3, 2, 64, device="cuda"), ints(0, 0)
