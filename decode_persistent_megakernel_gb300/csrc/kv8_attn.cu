@@ -60,9 +60,10 @@ struct Shape {
 };
 
 // ---- the list of work -------------------------------------------------------------------------
-// Sequence s has units (KV head, row tile); each is FIXED empty places, which stand for what a unit costs beside its
-// tiles (its queries, its end), and ceil(len / KT) tiles. prefix[s] counts the places before it. Called by
-// all threads of a CTA; returns the total.
+// Sequence s has a unit for each KV head and each tile of its own query rows; each is FIXED empty places, which stand for
+// what a unit costs beside its tiles (its queries, its end), and ceil(len / KT) tiles (those past the last key that a unit's
+// rows see are stepped over, so a prompt's first rows count for more than they cost: up to twice the mean work for one
+// warp). prefix[s] counts the places before it. Called by all threads of a CTA; returns the total.
 constexpr int FIXED = 4;
 
 // In shared memory: prefix, then position and count of every sequence's new tokens (0, 0 for one that is passed over).
@@ -73,19 +74,25 @@ struct List {
 };
 size_t list_bytes(int n) { return (size_t)((n + 2) & ~1) * 4 + (size_t)n * 8; }
 
-template <int D>
+// Tiles of query rows of a KV head in a sequence with `count` new tokens.
+template <int ROWS>
+__device__ __forceinline__ int row_tiles_of(const AttnParams& q, int count) {
+  return q.row_tiles > 1 ? (q.group * count + ROWS - 1) / ROWS : 1;
+}
+
+template <int D, int ROWS>
 __device__ __forceinline__ int places_of(const AttnParams& q, int s, const List& list) {
   int pos, count;
   if (!span_of(q.sp, s, q.c.max_ctx, pos, count) && blockIdx.x == 0 && q.sp.status) atomicOr(q.sp.status, STATUS_BAD_POS);
   list.span[s] = make_int2(pos, count);
-  return count > 0 ? ((pos + count + Shape<D>::KT - 1) / Shape<D>::KT + FIXED) * q.units : 0;
+  return count > 0 ? ((pos + count + Shape<D>::KT - 1) / Shape<D>::KT + FIXED) * q.c.n_kv * row_tiles_of<ROWS>(q, count) : 0;
 }
 
-template <int D, int NT>
+template <int D, int ROWS, int NT>
 __device__ int build_list(const AttnParams& q, const List& list, int* scan) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = q.c.n_seqs;
   if (n <= 32) {  // every warp for itself: all write the same words, and no barrier stands before the first copy
-    const int mine = lane < n ? places_of<D>(q, lane, list) : 0;
+    const int mine = lane < n ? places_of<D, ROWS>(q, lane, list) : 0;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -101,7 +108,7 @@ __device__ int build_list(const AttnParams& q, const List& list, int* scan) {
   int carry = 0;
   for (int base = 0; base < n; base += NT) {
     const int s = base + threadIdx.x;
-    const int mine = s < n ? places_of<D>(q, s, list) : 0;
+    const int mine = s < n ? places_of<D, ROWS>(q, s, list) : 0;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -157,9 +164,10 @@ struct Place {
     rt = 0;
     limit = pos + count;
     if (q.row_tiles > 1) {
-      head = unit / q.row_tiles;
-      rt = unit - head * q.row_tiles;
-      limit = rt * ROWS >= q.group * count ? 0 : pos + min((rt * ROWS + ROWS - 1) / q.group, count - 1) + 1;
+      const int row_tiles = row_tiles_of<ROWS>(q, count);
+      head = unit / row_tiles;
+      rt = unit - head * row_tiles;
+      limit = pos + min((rt * ROWS + ROWS - 1) / q.group, count - 1) + 1;
     }
     row0 = (seq * q.c.n_kv + head) * q.c.max_ctx;
   }
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   if (tid == 0) sm.failed = 0;
   mbar_fence_init();
   if (tid < D / 2) sm.freq[tid] = q.rope.f[tid];  // (threads index it apart, which parameters do one by one)
-  const int total = build_list<D, C::NT>(q, list, sm.scan);
+  const int total = build_list<D, ROWS, C::NT>(q, list, sm.scan);
   const Deal share = deal(total, gridDim.x, NW);
   if ((long long)share.per * share.warps * blockIdx.x >= total) return;
   const int lo = warp < share.warps ? (int)min((long long)share.per * (blockIdx.x * share.warps + warp), (long long)total) : total;
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
     }
     const int seg_end = min(hi, seg.x + seg.tiles - seg.tile);
     const int head = seg.head, rt = seg.rt, pos = seg.pos, count = seg.count;
-    const int rows = min(q.group * count - rt * ROWS, ROWS);  // rows of this unit (may be <= 0)
+    const int rows = min(q.group * count - rt * ROWS, ROWS);  // rows of this unit
 
     // query rows: rotated, divided by a power of two, laid out as the scores' right operands, eight at a
     // time. A thread's operands are dimensions t D/4 .. of row g, four for each product, so it loads just those
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   if (tid == 0 && *failed && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
 }
 
-// Joins the units that several CTAs hold: CTA (unit of a sequence, slice of its rows). It is launched with the kernel
+// Joins the units that several CTAs hold: CTA (unit of a sequence as the longest one has them, slice of its rows). It is launched with the kernel
 // before it and builds its list meanwhile; 2 to 4 us after it, latency of a few dependent loads from L2.
 template <int D, int NG, typename T>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) kv8_merge_kernel(const __grid_constant__ AttnParams q) {
@@ -750,16 +758,16 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv8_merge_kernel(const __grid
   __shared__ int scan[JOIN_WARPS];
   const List list(list_raw, q.c.n_seqs);
   // the list depends on the call's inputs alone, so it is built while the parts are still being made
-  const int total = build_list<D, JOIN_WARPS * 32>(q, list, scan);
+  const int total = build_list<D, ROWS, JOIN_WARPS * 32>(q, list, scan);
   const Deal share = deal(total, q.grid, q.warps);
   const int per = share.per * share.warps;  // of a CTA
   const int seq = blockIdx.x / q.units, unit = blockIdx.x % q.units;
   const int pos = list.span[seq].x, count = list.span[seq].y;
-  const int tiles = (pos + count + KT - 1) / KT;
-  const int a = list.prefix[seq] + unit * (tiles + FIXED) + FIXED, c0 = a / per, parts = (a + tiles - 1) / per - c0 + 1;
+  const int tiles = (pos + count + KT - 1) / KT, row_tiles = row_tiles_of<ROWS>(q, count);
   const int head = unit / q.row_tiles, rt = unit % q.row_tiles;
+  const int a = list.prefix[seq] + (head * row_tiles + rt) * (tiles + FIXED) + FIXED, c0 = a / per, parts = (a + tiles - 1) / per - c0 + 1;
   pdl_wait();  // the parts are complete
-  if (count == 0 || parts <= 1) return;  // one CTA had it whole
+  if (count == 0 || rt >= row_tiles || parts <= 1) return;  // no rows, or one CTA had it whole
   join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * count - rt * ROWS, ROWS), c0, parts);
 }
 

@@ -745,6 +745,35 @@ def test_a_cache_over_given_buffers_is_ready_for_any_stream():
     torch.cuda.synchronize()
     assert b.error() == 1
 
+def time_of(call, n=5):
+    for _ in range(3):
+        call()
+    times = []
+    for _ in range(9):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(n):
+            call()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b) / n)
+    return sorted(times)[4]
+
+
+@pytest.mark.parametrize("hq,hk,d", [(32, 8, 64), (12, 2, 128)])
+def test_one_long_sequence_beside_single_tokens_is_dealt_out_evenly(hq, hk, d):
+    # a prompt's chunk and 31 decode steps in one call: no longer than a few times the two calls by themselves, and right
+    n, t, seqs = 2000, 256, 32
+    cache = filled(hk, d, [n + t] * seqs, n + t, E4M3, 64, seed=6, spread=0.3)
+    counts = [t] + [1] * (seqs - 1)
+    check_attention(cache, [n + c for c in counts], counts, hq, F32, 0.0)
+    q, pos = normal((seqs, t, hq, d), 7).cuda(), ints(*[n] * seqs)
+    out = torch.zeros_like(q)
+    mixed = time_of(lambda: cache.attention(q, pos, counts=ints(*counts), out=out))
+    chunk = time_of(lambda: cache.attention(q, pos, counts=ints(t, *[0] * (seqs - 1)), out=out))
+    step = time_of(lambda: cache.attention(q, pos, counts=ints(*[1] * seqs), out=out))
+    assert mixed < 2.5 * (chunk + step), (mixed, chunk, step)
+
 def test_python_layer_refuses_bad_tensors():
     cache = T.Kv8Cache(2, 64, 100, n_seqs=2)
     x, pos = torch.zeros(2, 3, 2, 64, device="cuda"), ints(0, 0)
