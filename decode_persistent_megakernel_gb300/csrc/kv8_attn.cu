@@ -134,11 +134,11 @@ __device__ int build_list(const AttnParams& q, const List& list, int* scan) {
 // The list is dealt out in equal runs of places to the warps of all CTAs, neighbouring runs to the warps of one CTA.
 // Short lists use fewer warps of every CTA rather than fewer CTAs.
 struct Deal {
-  int warps, per;  // warps of a CTA, places of a warp
+  int warps, per;  // warps of a CTA, places of a warp (one where the list is empty: it divides)
 };
 __device__ __forceinline__ Deal deal(int total, int grid, int max_warps) {
   const int warps = min(max((total + grid - 1) / grid, 1), max_warps);
-  return Deal{warps, (total + grid * warps - 1) / (grid * warps)};
+  return Deal{warps, max((total + grid * warps - 1) / (grid * warps), 1)};
 }
 
 // A place in the list, with what the tiles of its unit share.

@@ -774,6 +774,16 @@ def test_one_long_sequence_beside_single_tokens_is_dealt_out_evenly(hq, hk, d):
     step = time_of(lambda: cache.attention(q, pos, counts=ints(*[1] * seqs), out=out))
     assert mixed < 2.5 * (chunk + step), (mixed, chunk, step)
 
+@pytest.mark.parametrize("t,dtype", [(1, F32), (40, F32), (40, BF16), (100, BF16)])
+def test_a_call_without_any_new_token_does_nothing(t, dtype):
+    for seqs in (1, 40):
+        cache = filled(2, 64, [200] * seqs, 200, E4M3, 64, seed=3)
+        q, status = normal((seqs, t, 8, 64), 4).to(dtype).cuda(), ints(0)
+        out, lse = torch.full_like(q, 5.0), torch.full((seqs, t, 8), 5.0, device="cuda")
+        for pos, counts, bits in (([0] * seqs, [0] * seqs, 0), ([200] * seqs, [0] * seqs, 0), ([-1] * seqs, [t] * seqs, 1)):
+            cache.attention(q, ints(*pos), counts=ints(*counts), out=out, lse=lse, status=status)
+            assert int(status) == bits and bool((out == 5).all()) and bool((lse == 5).all())
+
 def test_python_layer_refuses_bad_tensors():
     cache = T.Kv8Cache(2, 64, 100, n_seqs=2)
     x, pos = torch.zeros(2, 3, 2, 64, device="cuda"), ints(0, 0)
