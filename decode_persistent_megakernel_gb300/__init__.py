@@ -524,6 +524,9 @@ class Kv8Cache:
     def __init__(self, n_kv_heads: int, head_dim: int, max_ctx: int, n_seqs: int = 1, fmt: int = TINFER_KV8_E4M3,
                  block: int = 64, device="cuda", buffers=None, workspace=None):
         import torch
+        shape = tinfer_kv8(fmt, n_seqs, n_kv_heads, head_dim, max_ctx, block, *[16] * 4)  # (addresses that are not looked at)
+        if lib().tinfer_kv8_attention_workspace(shape, n_kv_heads, 1) == 0:
+            raise TinferError(TINFER_ERR_UNSUPPORTED, "Kv8Cache")
         codes = torch.Size((n_seqs, n_kv_heads, max_ctx, head_dim))
         scales = torch.Size((n_seqs, n_kv_heads, -(-max_ctx // max(1, block))))
         if buffers is None:
@@ -545,8 +548,6 @@ class Kv8Cache:
         self.c, self._kept = (tinfer_kv8(f, n_seqs, n_kv_heads, head_dim, max_ctx, block, *(t.data_ptr() for t in buffers))
                               for f in (fmt, fmt | TINFER_KV8_KEEP_STATUS))
         need = self.workspace_bytes(n_kv_heads, 1)
-        if need == 0:
-            raise TinferError(TINFER_ERR_UNSUPPORTED, "Kv8Cache")
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         self._workspace = self._check_workspace(workspace)

@@ -833,6 +833,20 @@ cudaError_t launch_f(AttnParams& q, int head_dim, int rows, int dtype, cudaStrea
                       : launch_n<FMT, 64, 4>(q, dtype, st);
 }
 
+// Rows of a unit of work and row tiles of a KV head; false where the counts do not fit: rows of the cache (their
+// coordinates in the copies), query rows, the list of tiles and the units are counted in 32 bits.
+struct Units {
+  int rows, row_tiles;
+};
+bool units_of(const tinfer_kv8* c, int n_heads, int n_tokens, bool prefill, Units& u) {
+  const long long rows = (long long)(n_heads / c->n_kv_heads) * n_tokens;
+  if ((long long)c->n_seqs * c->n_kv_heads * c->max_ctx > 0x7FFFFFFFLL || rows > (1LL << 30)) return false;
+  u.rows = prefill ? PREFILL_ROWS : rows_per_tile(rows, c->head_dim);
+  const long long row_tiles = (rows + u.rows - 1) / u.rows, kt = 4096 / c->head_dim;
+  u.row_tiles = (int)row_tiles;
+  return row_tiles * c->n_kv_heads * c->n_seqs <= (1LL << 30) / (prefill ? 1 : (c->max_ctx + kt - 1) / kt + FIXED);
+}
+
 // Multiprocessors of the current device.
 int device_sms(int& sms) {
   int dev = 0;
@@ -851,7 +865,10 @@ extern "C" {
 size_t tinfer_kv8_attention_workspace(const tinfer_kv8* cache, int n_heads, int n_tokens) {
   kv8::Cache c;
   tinfer_status rc;
-  if (!kv8::cache_of(cache, c, rc) || n_heads < 1 || n_heads % cache->n_kv_heads || n_tokens < 1) return 0;
+  if (!kv8::cache_of(cache, c, rc) || n_heads < 1 || n_heads % cache->n_kv_heads || n_tokens < 1 || n_tokens > cache->max_ctx) return 0;
+  kv8::Units u;  // as bf16 rows, which are refused last
+  const long long rows = (long long)(n_heads / cache->n_kv_heads) * n_tokens;
+  if (!kv8::units_of(cache, n_heads, n_tokens, kv8::is_prefill(TINFER_DTYPE_BF16, cache->head_dim, rows), u)) return 0;
   // One size for every call, so that a program can keep one workspace for all: two parts of each CTA and one of each
   // of its warps (12 warps of 16 rows, or 8 of 32 at 64 dimensions), or two parts of 256 rows of each CTA.
   const size_t few = (size_t)kv8::MAX_GRID * (cache->head_dim == 128 ? (2 + 12) * 16 : (2 + 8) * 32) * (cache->head_dim + 2) * 4;
@@ -883,20 +900,12 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   q.lse = lse_dev;
   q.part = static_cast<float*>(workspace_dev);
   q.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->head_dim));
-  // rows of the cache are counted in 32 bits (their coordinates in the copies)
-  if ((long long)cache->n_seqs * cache->n_kv_heads * cache->max_ctx > 0x7FFFFFFFLL) return TINFER_ERR_UNSUPPORTED;
-  const long long rows = (long long)q.group * n_tokens;
-  const bool prefill = kv8::is_prefill(q_rows->dtype, cache->head_dim, rows);
-  const int per = prefill ? kv8::PREFILL_ROWS : kv8::rows_per_tile(rows, cache->head_dim);
-  const long long row_tiles = (rows + per - 1) / per, units = row_tiles * cache->n_kv_heads;
-  const int kt = 4096 / cache->head_dim;
-  // rows, the list of tiles and the units are counted in 32 bits
-  if (rows > (1LL << 30)) return TINFER_ERR_UNSUPPORTED;
-  if (units * cache->n_seqs > (1LL << 30) / (prefill ? 1 : (cache->max_ctx + kt - 1) / kt + kv8::FIXED))
-    return TINFER_ERR_UNSUPPORTED;
-  q.row_tiles = (int)row_tiles;
-  q.units = (int)units;
-  q.keep_l2 = row_tiles > 1;
+  const bool prefill = kv8::is_prefill(q_rows->dtype, cache->head_dim, (long long)q.group * n_tokens);
+  kv8::Units u;
+  if (!kv8::units_of(cache, n_heads, n_tokens, prefill, u)) return TINFER_ERR_UNSUPPORTED;
+  q.row_tiles = u.row_tiles;
+  q.units = u.row_tiles * cache->n_kv_heads;
+  q.keep_l2 = u.row_tiles > 1;
   q.withhold = (cache->format & TINFER_KV8_DEBUG_WITHHOLD) != 0;
   q.wait_us = q.withhold ? kv8::WAIT_US_WITHHELD : kv8::WAIT_US;
   int sms = 0;
@@ -908,8 +917,8 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
   if (prefill)
     e = kv8::launch_prefill(q, kv8::format_of(cache), cache->head_dim, st);
   else
-    e = kv8::format_of(cache) == kv8::E4M3 ? kv8::launch_f<kv8::E4M3>(q, cache->head_dim, per, q_rows->dtype, st)
-                                   : kv8::launch_f<kv8::INT8>(q, cache->head_dim, per, q_rows->dtype, st);
+    e = kv8::format_of(cache) == kv8::E4M3 ? kv8::launch_f<kv8::E4M3>(q, cache->head_dim, u.rows, q_rows->dtype, st)
+                                   : kv8::launch_f<kv8::INT8>(q, cache->head_dim, u.rows, q_rows->dtype, st);
   return e == cudaSuccess ? TINFER_OK : TINFER_ERR_CUDA;
 }
 

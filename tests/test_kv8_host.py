@@ -100,6 +100,24 @@ def test_bad_angles_heads_and_workspaces_are_refused():
     assert T.tinfer_op_kv8_attention(big, 1024, 1, rows(), A, None, 0.0, rows(2 * A, ss=65536), None, A, 1 << 40) == NO
 
 
+def test_no_workspace_for_what_every_attention_refuses():
+    ws = T.tinfer_kv8_attention_workspace
+    assert ws(cache(), 4, 100) > 0 and ws(cache(), 4, 101) == 0               # more tokens than the cache holds
+    big = dict(n_seqs=128, n_kv_heads=1, max_ctx=1 << 24)                    # 2^31 rows, and one sequence less
+    assert ws(cache(**big), 1, 1) == 0 and ws(cache(**{**big, "n_seqs": 127}), 1, 1) > 0
+    assert ws(cache(n_kv_heads=1, max_ctx=1 << 24, n_seqs=1), 65, 1 << 24) == 0  # more than 2^30 query rows of a KV head
+    for c, heads, tokens in ((cache(**big), 1, 1), (cache(n_kv_heads=1, max_ctx=1 << 24, n_seqs=1), 65, 1 << 24)):
+        for dtype in (T.TINFER_DTYPE_F32, T.TINFER_DTYPE_BF16):
+            r = rows(dtype=dtype, ss=1 << 40, ts=1 << 14, hs=64)
+            assert T.tinfer_op_kv8_attention(c, heads, tokens, r, A, None, 0.0, r, None, A, 1 << 30) in (NO, BAD)
+
+
+def test_a_cache_that_every_attention_refuses_is_not_made():
+    with pytest.raises(T.TinferError):  # refused before 275 GB are asked for
+        T.Kv8Cache(1, 64, 1 << 24, n_seqs=128)
+    with pytest.raises(T.TinferError):
+        T.Kv8Cache(1, 64, 100, fmt=5)
+
 @pytest.mark.parametrize("over,want", [
     (dict(rows=0), BAD), (dict(vocab=0), BAD), (dict(dtype=7), BAD), (dict(logits=None), BAD), (dict(logits=A + 2), BAD),
     (dict(row_stride=99), BAD), (dict(top_k=-1), BAD), (dict(top_k=33), BAD), (dict(targets=None), BAD),
