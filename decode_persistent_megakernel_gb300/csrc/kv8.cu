@@ -315,6 +315,7 @@ tinfer_status tinfer_op_kv8_append(const tinfer_kv8* cache, const tinfer_rows* k
   const kv8::Extent x{cache->n_seqs, n_tokens, cache->n_kv_heads, cache->head_dim};
   if (!kv8::rows_of(k, x, false, q.k) || !kv8::rows_of(v, x, false, q.v)) return TINFER_ERR_INVALID_ARG;
   if (k->dtype != v->dtype || !kv8::rope_of(rope_theta, cache->head_dim, q.rope)) return TINFER_ERR_INVALID_ARG;
+  if (cache->k_codes == cache->v_codes || cache->k_scales == cache->v_scales) return TINFER_ERR_INVALID_ARG;
   q.sp = kv8::Span{pos_dev, counts_dev, n_tokens, status_dev};
   cudaStream_t st = (cudaStream_t)stream;
   if (!kv8::clear_status(cache, status_dev, st)) return TINFER_ERR_CUDA;
@@ -335,7 +336,7 @@ tinfer_status tinfer_op_kv8_read(const tinfer_kv8* cache, int n_tokens, const in
     return TINFER_ERR_INVALID_ARG;
   const kv8::Extent x{cache->n_seqs, n_tokens, cache->n_kv_heads, cache->head_dim};
   if (!kv8::rows_of(k, x, true, q.k) || !kv8::rows_of(v, x, true, q.v)) return TINFER_ERR_INVALID_ARG;
-  if (k->dtype != v->dtype) return TINFER_ERR_INVALID_ARG;
+  if (k->dtype != v->dtype || k->data == v->data) return TINFER_ERR_INVALID_ARG;
   q.sp = kv8::Span{pos_dev, counts_dev, n_tokens, status_dev};
   cudaStream_t st = (cudaStream_t)stream;
   if (!kv8::clear_status(cache, status_dev, st)) return TINFER_ERR_CUDA;

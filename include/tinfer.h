@@ -366,8 +366,8 @@ tinfer_status tinfer_op_attention_noalloc(int n_heads, int n_kv_heads, int head_
  * occur); TINFER_KV8_INT8: signed integers -127..127.
  *
  * The buffers are caller-owned device memory. k_codes, v_codes: [n_seqs][n_kv_heads][max_ctx][head_dim],
- * 16-byte aligned; k_scales, v_scales: fp32 [n_seqs][n_kv_heads][ceil(max_ctx / block)]. They need no
- * initial values: a block is defined by the append that writes its first position. head_dim 64 or 128,
+ * 16-byte aligned; k_scales, v_scales: fp32 [n_seqs][n_kv_heads][ceil(max_ctx / block)]; the four share no
+ * memory. They need no initial values: a block is defined by the append that writes its first position. head_dim 64 or 128,
  * block 16, 32, 64 or 128, n_seqs <= 1024, n_kv_heads <= 1024, max_ctx <= 2^24.
  *
  * A tinfer_rows names rows of head_dim contiguous elements: the row of (sequence, token, head) starts
@@ -422,8 +422,8 @@ tinfer_status tinfer_op_kv8_append(const tinfer_kv8* cache, const tinfer_rows* k
                                    int n_tokens, const int32_t* pos_dev, const int32_t* counts_dev,
                                    double rope_theta, int32_t* status_dev, void* stream);
 
-/* Reads tokens [pos[s], pos[s] + counts[s]) of every sequence back into rows k and v: code * scale in
- * fp32, rounded once to the rows' dtype. Nothing is rotated back. */
+/* Reads tokens [pos[s], pos[s] + counts[s]) of every sequence back into rows k and v, which share no memory:
+ * code * scale in fp32, rounded once to the rows' dtype. Nothing is rotated back. */
 tinfer_status tinfer_op_kv8_read(const tinfer_kv8* cache, int n_tokens, const int32_t* pos_dev,
                                  const int32_t* counts_dev, const tinfer_rows* k, const tinfer_rows* v,
                                  int32_t* status_dev, void* stream);

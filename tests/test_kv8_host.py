@@ -118,6 +118,13 @@ def test_a_cache_that_every_attention_refuses_is_not_made():
     with pytest.raises(T.TinferError):
         T.Kv8Cache(1, 64, 100, fmt=5)
 
+def test_keys_and_values_written_to_one_place_are_refused():
+    r = rows(ss=1024)
+    assert T.tinfer_op_kv8_read(cache(), 3, A, None, r, r) == BAD
+    k = rows(2 * A)
+    for same in (dict(v_codes=A, k_scales=2 * A), dict(v_scales=2 * A, k_scales=2 * A, k_codes=3 * A)):
+        assert T.tinfer_op_kv8_append(cache(**same), k, k, 3, A, None, 0.0) == BAD
+
 @pytest.mark.parametrize("over,want", [
     (dict(rows=0), BAD), (dict(vocab=0), BAD), (dict(dtype=7), BAD), (dict(logits=None), BAD), (dict(logits=A + 2), BAD),
     (dict(row_stride=99), BAD), (dict(top_k=-1), BAD), (dict(top_k=33), BAD), (dict(targets=None), BAD),
