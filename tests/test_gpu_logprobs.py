@@ -169,6 +169,59 @@ def test_streams_and_graphs():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+# From 229 rows on (152 multiprocessors) one CTA of 512 threads walks a whole row. At 2^18 logits a thread adds 512
+# terms and 9 joins follow, 521 * 2^-24; its sums are rescaled by each of 2^18 / 512 / 16 = 32 turns at most, each time
+# off by the exponential and two roundings, 32 * (2^-22 + 2^-23); the rest as above.
+ROW_SUM = 521 * 2.0 ** -24 + 32 * (2.0 ** -22 + 2.0 ** -23) + 2.0 ** -18
+
+
+def check_whole_rows(x, k, seed=0):
+    rows, vocab = x.shape
+    targets = torch.randint(0, vocab, (rows,), generator=torch.Generator().manual_seed(seed), dtype=torch.int32).cuda()
+    logp, h, ids, top = T.logprobs(x, targets, top_k=k)
+    for a in range(0, rows, 128):  # (the reference on the GPU: elementary operations in 64 bits)
+        y = x[a:a + 128].double()
+        m = y.amax(dim=1, keepdim=True)
+        e = torch.exp(y - m)
+        norm = torch.log(e.sum(dim=1))
+        p = e / e.sum(dim=1, keepdim=True)
+        z = (m - y).clamp_max(1e30)
+        mean = torch.where(p > 0, p * z, 0.0).sum(dim=1)
+        want = (y - m).gather(1, targets[a:a + 128].long()[:, None])[:, 0] - norm
+        assert bool(((logp[a:a + 128] - want).abs() <= ROW_SUM + want.abs() * 2.0 ** -22)[want.isfinite()].all())
+        assert torch.equal(logp[a:a + 128].isinf(), want.isinf())
+        assert bool(((h[a:a + 128] - norm - mean).abs() <= ROW_SUM * (2 + 2 * mean) + (norm + mean) * 2.0 ** -22).all())
+        if k:
+            v, i = torch.sort(y, dim=1, descending=True, stable=True)
+            assert torch.equal(ids[a:a + 128].long(), i[:, :k])
+            t = v[:, :k] - m - norm[:, None]
+            assert bool(((top[a:a + 128] - t).abs() <= ROW_SUM + t.abs() * 2.0 ** -22).all())
+
+
+@pytest.mark.parametrize("k", [0, 1, 20, 32])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,vocab,pad", [(230, 128256, 0), (600, 128256, 3), (256, 262144, 0), (150, 151936, 8), (100, 262144, 0)])
+def test_many_rows_of_large_vocabularies(rows, vocab, pad, dtype, k):
+    g = torch.Generator(device="cuda").manual_seed(rows + k)
+    x = (2.5 * torch.randn((rows, vocab + pad), generator=g, device="cuda")).to(dtype)[:, :vocab]
+    x[:, torch.randperm(vocab, generator=g, device="cuda")[:500]] = -math.inf
+    check_whole_rows(x, k)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [128256, 262144])
+def test_many_rows_with_ties_and_rising_logits(vocab, dtype):
+    rows, k, i = 240, 32, torch.arange(vocab, device="cuda")
+    x = torch.zeros((rows, vocab), dtype=dtype, device="cuda")
+    x[1::6] = (i % 7).to(dtype)                 # thousands of equal largest logits: more than are listed
+    x[2::6] = (i * (20.0 / vocab)).to(dtype)    # rising: every turn's maximum is a new one
+    x[3::6] = (i * (-20.0 / vocab)).to(dtype)
+    x[4::6, ::1024] = 1.0                       # the large ones in the hands of few threads
+    x[5::6, 5:5 + 600] = 3.0                    # more equal ones side by side than are listed
+    check_whole_rows(x, k)
+    x[:, ::2] = -math.inf                       # and half of the tokens masked
+    check_whole_rows(x, k)
+
 def test_scores_of_the_decode_step():
     # the engine's logits of a step: its greedy token is the first alternative, its log probability the target's
     cfg = synth.config("tiny", max_ctx=8)
