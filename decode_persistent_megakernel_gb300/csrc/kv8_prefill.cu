@@ -278,6 +278,7 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 
 template <int FMT, int D, typename T>
 __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_constant__ AttnParams q) {
+  static_assert(std::is_same_v<T, __nv_bfloat16>, "rows are loaded and results packed as bf16");
   constexpr int NT = Roles<D>::NT;
   constexpr int BUFFERS = Roles<D>::BUFFERS, O_AT = BUFFERS * KT;
   constexpr int WARP_MMA = Roles<D>::MMA, NT_WIDEN = Roles<D>::WIDEN * 32;
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           w[i] = (ALL % NT_WIDEN == 0 || item < ALL) && key < u.keys ? *reinterpret_cast<const uint4*>(p + (size_t)key * D + item % CPR * 16) : make_uint4(0, 0, 0, 0);
         }
       };
-      auto widen = [&](uint32_t to, const uint4 (&w)[ITEMS], int kt) {
+      auto widen = [&](uint32_t to, const uint4 (&w)[ITEMS]) {
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
           const int item = t + NT_WIDEN * i, row = item / CPR, c = item % CPR;
@@ -644,7 +645,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
         const uint32_t parity = ((it / KV_STAGES) & 1) ^ 1;
         load(vp, kt, wv);
         wait(smem_addr(&sm.k_empty[st]), parity, failed);
-        widen(smem_addr(sm.k[st]), wk, kt);
+        widen(smem_addr(sm.k[st]), wk);
         if (t < KT / 16) {
           const int key = kt * KT + 16 * t;
           float4 f = make_float4(0.f, 0.f, 0.f, 1.f);
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
         if (lane == 0 && !(q.withhold && t == 0 && it == 0)) mbar_arrive(smem_addr(&sm.k_full[st]));
         if (kt + 1 < u.last) load(kp, kt + 1, wk);
         wait(smem_addr(&sm.v_empty[st]), parity, failed);
-        widen(smem_addr(sm.v[st]), wv, kt);
+        widen(smem_addr(sm.v[st]), wv);
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.v_full[st]));
