@@ -651,7 +651,7 @@ def logprobs(logits, targets=None, top_k: int = 0, stream=None):
     if logits.dim() != 2 or logits.stride(1) != 1 or logits.device.type != "cuda":
         raise ValueError("logits: [rows, vocab] on a CUDA device with contiguous rows is wanted")
     rows, vocab = logits.shape
-    dev = logits.device
+    dev, dtype = logits.device, _dtype(logits)
     if targets is not None and (targets.dtype != torch.int32 or targets.shape != (rows,) or targets.device != dev
                                 or not targets.is_contiguous()):
         raise ValueError(f"targets: a contiguous int32 tensor [{rows}] on {dev} is wanted")
@@ -660,7 +660,9 @@ def logprobs(logits, targets=None, top_k: int = 0, stream=None):
         entropy = torch.empty(rows, dtype=torch.float32, device=dev)
         ids = torch.empty((rows, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
         top = torch.empty((rows, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
+    if rows == 0 and 0 <= top_k <= 32:
+        return logp, entropy, ids, top  # nothing to launch
     _call("tinfer_op_logprobs", lib().tinfer_op_logprobs,
-          (rows, vocab, _dtype(logits), logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _ptr(targets), top_k,
+          (rows, vocab, dtype, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _ptr(targets), top_k,
            _ptr(logp), entropy.data_ptr(), _ptr(ids), _ptr(top)), dev, stream)
     return logp, entropy, ids, top

@@ -222,6 +222,13 @@ def test_many_rows_with_ties_and_rising_logits(vocab, dtype):
     x[:, ::2] = -math.inf                       # and half of the tokens masked
     check_whole_rows(x, k)
 
+def test_no_rows_give_empty_results():
+    logp, h, ids, top = T.logprobs(torch.zeros((0, 500), device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"), top_k=3)
+    assert logp.shape == (0,) and h.shape == (0,) and ids.shape == (0, 3) and top.shape == (0, 3)
+    for bad in (dict(logits=torch.zeros((0, 500), device="cuda"), top_k=33), dict(logits=torch.zeros((0, 500), device="cuda").double())):
+        with pytest.raises((ValueError, T.TinferError)):
+            T.logprobs(**bad)
+
 def test_scores_of_the_decode_step():
     # the engine's logits of a step: its greedy token is the first alternative, its log probability the target's
     cfg = synth.config("tiny", max_ctx=8)
