@@ -3,7 +3,7 @@
 //   o_i = sum_{j <= pos+i} softmax_j(q_i . k_j / sqrt(d)) v_j,   k_j = ck_j * sk[j / block], v_j = cv_j * sv[j / block]
 //
 // The n_tokens x group query rows that share a KV head are the rows of one matrix: every code is read
-// and widened once for all of them. The work is a flat list of key tiles (sequence, KV head, row tile,
+// and widened once for each tile of 8, 16 or 32 of them (16 at most at 128 dimensions). The work is a flat list of key tiles (sequence, KV head, row tile,
 // tile of KT keys); each warp takes an equal run of it, whatever the sequences' lengths, so that one long
 // sequence spreads over the GPU and a ragged batch stays even. The warps of a CTA have neighbouring runs and join
 // the parts of a unit that lie in them; a CTA whose run covers a unit only in part leaves (m, l, o) in the
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv8_merge_kernel(const __grid
   const int a = list.prefix[seq] + (head * row_tiles + rt) * (tiles + FIXED) + FIXED, c0 = a / per, parts = (a + tiles - 1) / per - c0 + 1;
   pdl_wait();  // the parts are complete
   if (count == 0 || rt >= row_tiles || parts <= 1) return;  // no rows, or one CTA had it whole
-  join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * count - rt * ROWS, ROWS), c0, parts);
+  join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * count - rt * ROWS, ROWS), c0, parts, WEIGHT_SHIFT);
 }
 
 // ---------------------------------------------------------------------------------------- host

@@ -90,7 +90,7 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int 
 constexpr int JOIN_WARPS = 8;
 
 template <int D, int ROWS, typename T>
-__device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int rows, int c0, int parts) {
+__device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int rows, int c0, int parts, int weight_shift) {
   constexpr int N = D / 32, NW = JOIN_WARPS;
   __shared__ alignas(16) float acc_s[NW][D];
   __shared__ float sum_s[NW], top_s[NW];
@@ -104,7 +104,7 @@ __device__ void join_parts(const AttnParams& q, int seq, int head, int row0, int
 #pragma unroll
     for (int i = 0; i < N; ++i) store_one(dst + i, y[i] * inv);
     if (q.lse && lane == 0)
-      q.lse[((size_t)seq * q.sp.n_tokens + tok) * q.n_heads + hq] = (log2f(sum) + top - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
+      q.lse[((size_t)seq * q.sp.n_tokens + tok) * q.n_heads + hq] = (log2f(sum) + top - (float)weight_shift) * 0.6931471805599453f;
   };
   auto load = [&](const float* p, int row, float (&f)[N]) {
 #pragma unroll

@@ -15,20 +15,21 @@
 // The softmax and the second product go by halves of 64 keys, so that the first half's product runs under the
 // second half's exponentials. (Scores by halves as well cost a 128-row operand read twice: 115 us for the 4096-token prompt against 114.)
 //
-// A row's running maximum is replaced only when it would nearly double: the outputs in tensor memory are then rescaled
-// by the row's thread, after the exponentials, when the product before is done and the scores have left their registers
-// (before them: 112 us for the 4096-token prompt against 105). Weights are held times 2^WEIGHT_SHIFT, below 2^16 with the
-// mantissa of their V scale: fp16 keeps 11 bits of them down to 2^-28 and steps of 2^-38 below. A maximum
-// that may lag behind by 2^4 (2^8) leaves 4 (7) bits less of the keys far below the largest, and takes 103 us (99).
+// A row's running maximum is replaced only where one of its warp's would grow by nearly 2^2, and then all of them are: the
+// outputs in tensor memory are rescaled by the rows' threads after the exponentials, when the product before is done and
+// the scores have left their registers. Weights are held times 2^SHIFT, below 2^16 with the mantissa of their V scale: a
+// key far below the largest is held to 2^-38 of it. The 4096-token prompt takes 102 us; 105 with rows by themselves
+// and maxima that lag by 2 (2^-39), 99 with a lag of 2^8, which leaves 2^-32, and 112 rescaled before the exponentials.
 //
 // Work is dealt out in equal runs over all CTAs by the number of keys that the units see (a causal prompt's
 // last rows see the whole prompt, its first almost nothing); a unit cut by a run's end leaves parts that
 // prefill_merge_kernel joins.
 //
-// Measured: 4096-token prompt, 12 heads of 128 over 2, int8 (51.6 GFLOP): 98 us, 0.27 of the measured bf16 rate; 512 tokens over
-// 8192 keys, 32 heads of 64 over 8, e4m3 (33.3 GFLOP): 67 us, 0.26. Bound by the chain of a row tile: scores from
+// Measured: 4096-token prompt, 12 heads of 128 over 2, int8 (51.6 GFLOP): 102 us, 0.26 of the measured bf16 rate; 512 tokens over
+// 8192 keys, 32 heads of 64 over 8, e4m3 (33.3 GFLOP): 69 us, 0.25. Bound by the chain of a row tile: scores from
 // tensor memory, maximum, exponentials, weights, product (about 3800 clocks for 128 keys at 64 dimensions, 5500 at
-// 128), which the other row tile's covers in part. The legacy warp products of kv8_attn.cu took 590 and 192 us.
+// 128), which the other row tile's covers in part. 13 warps leave a thread 128
+// registers, of which the softmax spills 80 to 200 bytes. The legacy warp products of kv8_attn.cu took 590 and 192 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -49,7 +50,8 @@ struct Roles {
 };
 constexpr int FETCH = 4;           // key tiles that are fetched into L2 ahead (64 rows of 32 x 4000 keys 111 -> 102 us)
 constexpr int KV_STAGES = 2, SCALE_SLOTS = 4;
-constexpr float GROW = 0.99f;      // a maximum may lag behind by 2^GROW: 2^(WEIGHT_SHIFT + GROW) 2 is below fp16's 65504
+constexpr int SHIFT = 13;          // of the weights
+constexpr float GROW = 1.99f;      // a maximum may lag behind by 2^GROW: 2^(SHIFT + GROW) 2 is below fp16's 65504
 constexpr int FIXED_KEYS = 768;    // what a unit costs beside its keys, in keys (4096-token prompt: 98 us, 109 with 384)
 
 template <int D>
@@ -471,14 +473,14 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
 #pragma unroll
           for (int j = 0; j < HALF / 16; ++j) top = fmaxf(top, fmaf(m[j], f[j].x * scale, f[j].y));
           float shrink = 1.f;
-          if (top > ref + GROW || ref == -INFINITY) {  // (also the row's first keys)
-            const float half = ref == -INFINITY ? 1.f : half_shrink(ref, top);
+          if (__any_sync(~0u, top > ref + GROW || ref == -INFINITY)) {  // (also the row's first keys); all of a warp's maxima at once
+            const float now = fmaxf(ref, top), half = ref == -INFINITY ? 1.f : half_shrink(ref, now);
             shrink = half * half;
-            ref = top;
+            ref = now;
             sum = sum * half * half;
           }
           // weights, over the scores, which are all in registers
-          const float from = ref == -INFINITY ? 0.f : ref - (float)WEIGHT_SHIFT;
+          const float from = ref == -INFINITY ? 0.f : ref - (float)SHIFT;
           auto weights = [&](auto cut, auto apart) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -585,7 +587,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           part[ROWS * D + row] = ref;
           part[ROWS * D + ROWS + row] = sum;
         } else if (q.lse) {
-          q.lse[((size_t)u.seq * q.sp.n_tokens + tok) * q.n_heads + hq] = (log2f(sum) + ref - (float)WEIGHT_SHIFT) * 0.6931471805599453f;
+          q.lse[((size_t)u.seq * q.sp.n_tokens + tok) * q.n_heads + hq] = (log2f(sum) + ref - (float)SHIFT) * 0.6931471805599453f;
         }
       }
     }
@@ -779,7 +781,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) prefill_merge_kernel(const __
   }
   pdl_wait();
   if (parts <= 1) return;
-  join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * sp.count - rt * ROWS, ROWS), c0, parts);
+  join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * sp.count - rt * ROWS, ROWS), c0, parts, SHIFT);
 }
 
 template <int FMT, int D, typename T>
@@ -817,8 +819,8 @@ cudaError_t launch_f(AttnParams& q, int head_dim, cudaStream_t st) {
 
 // bf16 rows beyond one row tile of the other kernel, or four at 128 dimensions. fp32 and fp16 rows stay there: their
 // two-part operands keep the precision of their type, which one fp16 operand would not. Here against there, in us, at 40
-// rows of 8 heads of 64: 500 keys 17 : 22, 8000 keys 19 : 30, 32 sequences of 4000 keys 102 : 115; at 24 rows the last
-// takes 100 : 69. Two heads of 128, 64 rows: 22 : 21, 23 : 20, 50 : 65; 128 rows: 25 : 21, 27 : 31, 57 : 106.
+// rows of 8 heads of 64: 500 keys 18 : 22, 8000 keys 20 : 30, 32 sequences of 4000 keys 109 : 117; at 24 rows the last
+// takes 108 : 70. Two heads of 128, 64 rows: 23 : 22, 24 : 20, 53 : 66; 128 rows: 27 : 21, 28 : 31, 61 : 110.
 bool is_prefill(int dtype, int head_dim, long long rows) { return dtype == TINFER_DTYPE_BF16 && rows > (head_dim == 64 ? 32 : 64); }
 size_t prefill_workspace(int head_dim) { return (size_t)MAX_GRID * 2 * PREFILL_ROWS * (head_dim + 2) * 4; }
 
