@@ -24,13 +24,15 @@ constexpr int WEIGHT_SHIFT = 14;    // weights are held times 2^14: fp16 keeps 1
 // Exponents of V scales that enter the running maximum. Of a row whose keys all have the smallest one the
 // sum of the softmax is 2^(WEIGHT_SHIFT - E_MIN) for each key: 2^24 keys stay below fp32's 2^128. A smaller
 // scale's remainder makes its weights smaller than 1, a scale of 0 makes them 0 and counts in the sum.
-constexpr int E_MIN = -85, E_MAX = 120;
+// An append leaves scales of up to 2^123 (the largest number / 127, doubled); a mantissa beyond 2 would overflow fp16.
+constexpr int E_MIN = -85, E_MAX = 126;
 // The sum of the softmax takes a weight 2^(x + e - M) times 2^-e. Where e lies far below the largest exponent that M may
 // come from, that weight falls below 2^-126 and is lost although its key may have the row's largest score: of keys with
 // e no more than E_SPAN below, what is lost is below 2^-40 of the largest score's term. A tile with others
-// sums 2^(x - M) itself, an exponential more for each key: between 2^-107 for the largest score and 2^(WEIGHT_SHIFT -
-// E_MIN), computed times 2^SUM_LIFT so that terms down to 2^-39 of the former stay above 2^-146. (Its exponent may be as large as 2^8 and is
-// rounded there, by 2^-17.) Sums are rescaled in two halves for the same reason: M moves by up to 2^206, the sum by far less.
+// sums 2^(x - M) itself, an exponential more for each key: between 2^-109 for the largest score and 2^(WEIGHT_SHIFT -
+// E_MIN), computed times 2^SUM_LIFT so that terms down to 2^-37 of the former stay above 2^-146. (Its exponent may be as
+// large as 2^8 and is rounded there, by 2^-17.) Sums are rescaled in two halves for the same reason: M moves by up to
+// 2^208, the sum by far less.
 constexpr int E_SPAN = 86, SUM_LIFT = 20;
 constexpr int WAIT_US = 200 * 1000, WAIT_US_WITHHELD = 5 * 1000;
 

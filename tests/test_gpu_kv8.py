@@ -486,6 +486,23 @@ def test_many_keys_far_below_the_leading_one(below, t, d):
     far, _ = R.attend_bounds(want, size, mean, d, n, BF16, v_top(cache, 0, n))
     assert bool(((got - want).abs() <= far).all()), float((got / want - 1).abs().max())
 
+@pytest.mark.parametrize("t,dtype", [(1, F32), (1, BF16), (40, F32), (5, BF16), (100, BF16)])
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 64), (2, 1, 128)])
+def test_values_near_the_types_end(hq, hk, d, fmt, t, dtype):
+    # blocks begun with almost the largest numbers and grown by the largest: V scales of up to 2^122
+    n = 320
+    cache = T.Kv8Cache(hk, d, n, fmt=fmt, block=32)
+    k, v = normal((1, n, hk, d), 1), torch.rand((1, n, hk, d), generator=torch.Generator().manual_seed(2)) * 2 - 1
+    v *= 3.2e38
+    v[0, 0::32, :, 3], v[0, 31::32, :, 3] = 3.39e38, 3.4028e38
+    for a in range(0, n, 32):
+        for b, e in ((a, a + 31), (a + 31, a + 32)):
+            cache.append(k[:, b:e].cuda(), v[:, b:e].cuda(), ints(b))
+    if fmt == INT8:
+        assert float(cache.v_scales.max()) > 2.0 ** 122
+    check_attention(cache, [n], [t], hq, dtype, 10000.0)
+
 @pytest.mark.parametrize("dtype,t", [(F32, 40), (BF16, 40), (BF16, 150)])
 def test_a_spoilt_block_reaches_the_rows_that_see_it_alone(dtype, t):
     block, n = 16, 200
