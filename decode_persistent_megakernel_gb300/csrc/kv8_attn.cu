@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
       top = max(top, __shfl_xor_sync(~0u, top, 1));
       top = max(top, __shfl_xor_sync(~0u, top, 2));
-      const int e2 = top ? min(max((int)(top >> 23) - 126, -100), 126) : 0;  // every magnitude below 2^e2 (below 4 2^e2 at the type's end)
+      // (from 2^-120 on, so that the power, its inverse and the scores' factor are normal numbers: 11 bits are left at 2^-126)
+      const int e2 = top ? min(max((int)(top >> 23) - 126, -120), 126) : 0;  // every magnitude below 2^e2 (below 4 2^e2 at the type's end)
       const float down = __uint_as_float((uint32_t)(127 - e2) << 23), up = q.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll
       for (int k = 0; k < MD; ++k)

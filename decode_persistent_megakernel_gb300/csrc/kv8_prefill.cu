@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
           for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(x[i]) & 0x7FFFFFFFu);
         }
         // a rotation makes no magnitude larger than sqrt(2) times the largest: one power of two of room
-        const int e2 = most ? min(max((int)(most >> 23) - 125, -100), 126) : 0;
+        const int e2 = most ? min(max((int)(most >> 23) - 125, -120), 126) : 0;
         const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
         // chunks of eight dimensions whose angles are held at once: a power of two
         int lg_pairs = 3;

@@ -404,6 +404,20 @@ def test_queries_near_the_types_end(t, dtype):
     assert bool((size < 100).all()) and bool(got.isfinite().all()) and bool(((got - want).abs() <= far).all())
 
 
+@pytest.mark.parametrize("t,dtype", [(1, F32), (1, BF16), (5, BF16), (40, F32), (150, BF16)])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 64), (2, 1, 128)])
+@pytest.mark.parametrize("down", [110, 120, 125])
+def test_queries_near_zero_against_huge_keys(hq, hk, d, t, dtype, down):
+    # as small as normal numbers get, against keys as large: ordinary scores
+    cache = filled(hk, d, [400], 400, E4M3, 64, seed=12, spread=0.2)
+    q = normal((1, t, hq, d), 13).clamp(-3, 3).to(dtype).float().mul(2.0 ** -down).to(dtype)
+    cache.k_scales.mul_(2.0 ** down)
+    got = cache.attention(q.cuda(), ints(400 - t))[0].cpu().double()
+    k, v = values(cache, 0, 400)
+    want, _, size, mean = R.attend(q[0].double(), k, v, 400 - t)
+    far, _ = R.attend_bounds(want, size, mean, d, 400, dtype, v_top(cache, 0, 400))
+    assert bool((size < 100).all()) and bool(got.isfinite().all()) and bool(((got - want).abs() <= far).all())
+
 @pytest.mark.parametrize("hq,hk,d", [(10, 2, 64), (6, 1, 128)])
 def test_fp32_rows_keep_their_precision_over_many_keys(hq, hk, d):
     # sums that were cut off at each step would be off by half a step (2^-24) for each of the 200 or more products of 16
