@@ -815,6 +815,37 @@ def test_a_call_without_any_new_token_does_nothing(t, dtype):
             cache.attention(q, ints(*pos), counts=ints(*counts), out=out, lse=lse, status=status)
             assert int(status) == bits and bool((out == 5).all()) and bool((lse == 5).all())
 
+@pytest.mark.parametrize("hq,hk,d,t,dtype", [(8, 2, 64, 150, BF16), (12, 2, 128, 80, BF16), (8, 2, 64, 12, F32), (8, 2, 64, 70, F16)])
+def test_two_captured_calls_replayed_side_by_side_follow_their_inputs(hq, hk, d, t, dtype):
+    n, seqs = 900, 5
+    cache = filled(hk, d, [n] * seqs, n, INT8, 32, seed=3)
+    ws = [torch.empty(cache.workspace_bytes(), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    qs = [torch.zeros(seqs, t, hq, d, dtype=dtype, device="cuda") for _ in range(2)]
+    poss, counts, outs, graphs = [ints(*[0] * seqs) for _ in range(2)], [ints(*[0] * seqs) for _ in range(2)], [], []
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        outs.append(torch.zeros_like(qs[i]))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            cache.attention(qs[i], poss[i], counts=counts[i], rope_theta=10000.0, out=outs[i], workspace=ws[i])
+    for turn in range(6):
+        g = torch.Generator().manual_seed(turn)
+        for i in range(2):
+            qs[i].copy_(normal((seqs, t, hq, d), 10 * turn + i).to(dtype))
+            c = torch.randint(0, t + 1, (seqs,), generator=g, dtype=torch.int32)
+            counts[i].copy_(c)
+            poss[i].copy_((torch.rand(seqs, generator=g) * (n - c)).int())
+            outs[i].zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], cache.attention(qs[i], poss[i], counts=counts[i], rope_theta=10000.0)), (turn, i)
+    assert cache.error() == 0
+
 def test_python_layer_refuses_bad_tensors():
     cache = T.Kv8Cache(2, 64, 100, n_seqs=2)
     x, pos = torch.zeros(2, 3, 2, 64, device="cuda"), ints(0, 0)
