@@ -9,8 +9,9 @@
 // joins at its end are most of its life. Three CTAs of 40 registers on an SM took 219 us, four of 32 take 199,
 // 0.79 of the measured copy rate. One row of 128256: 7.4 us; 64 rows of 151936 bf16, 20 alternatives: 11.8.)
 //
-// Alternatives: a slice's values fall to 32 groups of threads; the k-th largest of the groups' maxima is a floor
-// that at least k values reach, and few others do (31 on average for k = 20). Only threads whose maximum reaches it
+// Alternatives: a slice's values fall to 32 groups of threads, one of each lane of all warps (so that a slice of few words
+// leaves none empty); the k-th largest of the groups' maxima is a floor that at least k values reach, and few others do
+// (31 on average for k = 20). Only threads whose maximum reaches it
 // have any: their words are dealt out and read again. Those values are listed and ranked by counting, on (value, lower id
 // first) as one 64-bit key, so that the order is exact and independent of timing. A list that overflows falls back
 // to k maxima one after another.
@@ -32,7 +33,7 @@ namespace logprobs {
 
 constexpr int NT = 512, NWARPS = NT / 32;
 constexpr int MAX_K = 32, MAX_CLUSTER = 8;
-constexpr int GROUPS = 32;             // of threads, whose maxima give the alternatives' floor: one to a lane
+constexpr int GROUPS = 32;             // of threads, whose maxima give the alternatives' floor: one of each lane
 static_assert(MAX_CLUSTER * MAX_K <= NT, "a thread for every alternative of the slices");
 static_assert(MAX_K <= GROUPS, "a floor for every k");
 constexpr int LIST = 512;             // listed candidates of a slice, at most
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(NT, 4) logprobs_kernel(const __grid_constant__
   constexpr int N = 16 / sizeof(T);  // elements of a word
   constexpr int AHEAD = sizeof(T);   // words of a thread in flight: 16 elements, and 32 registers for four CTAs on an SM
   __shared__ Part red[NWARPS];
-  __shared__ float group_top[GROUPS], floor_s;
+  __shared__ float lane_top[NWARPS][GROUPS], floor_s;
   __shared__ int listed, owners;
   __shared__ uint16_t owner[NT];
   __shared__ unsigned long long list[LIST];
@@ -193,10 +194,7 @@ __global__ void __launch_bounds__(NT, 4) logprobs_kernel(const __grid_constant__
   const float target_x = target_in ? value(x[target]) : 0.f;
   const float mine = p.m;
   auto other = [&](int o) { return Part{__shfl_xor_sync(~0u, p.m, o), __shfl_xor_sync(~0u, p.s0, o), __shfl_xor_sync(~0u, p.s1, o)}; };
-  float top = mine;  // of this thread's group
-#pragma unroll
-  for (int o = 1; o < NT / GROUPS; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  if (tid % (NT / GROUPS) == 0) group_top[tid / (NT / GROUPS)] = top;
+  if (q.k) lane_top[warp][lane] = mine;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) p = join(p, other(o));
   if (lane == 0) red[warp] = p;
@@ -207,7 +205,9 @@ __global__ void __launch_bounds__(NT, 4) logprobs_kernel(const __grid_constant__
     for (int o = 1; o < NWARPS; o *= 2) p = join(p, other(o));
   } else if (warp == 1 && q.k) {
     // the floor of the alternatives: the k-th largest of the groups' maxima, ties by the group
-    const float g = group_top[lane];
+    float g = lane_top[0][lane];
+#pragma unroll
+    for (int w = 1; w < NWARPS; ++w) g = fmaxf(g, lane_top[w][lane]);
     int above = 0;
 #pragma unroll
     for (int o = 1; o < GROUPS; ++o) {

@@ -229,6 +229,32 @@ def test_no_rows_give_empty_results():
         with pytest.raises((ValueError, T.TinferError)):
             T.logprobs(**bad)
 
+@pytest.mark.parametrize("rows,vocab,dtype", [(1, 600, torch.bfloat16), (1, 2048, torch.bfloat16), (64, 2048, torch.float16),
+                                              (500, 1000, torch.float32), (500, 2048, torch.bfloat16)])
+def test_alternatives_of_a_small_vocabulary_take_no_pass_each(rows, vocab, dtype):
+    # 32 alternatives by a floor and ranks, not by one maximum after another: far less than 32 times what one costs more
+    x = (2.5 * torch.randn((rows, vocab), generator=torch.Generator().manual_seed(vocab))).to(dtype).cuda()
+    check(x, 32)
+    graphs, stream = [], torch.cuda.Stream()
+    for k in (1, 32):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            for _ in range(20):
+                T.logprobs(x, None, top_k=k)
+    times = []
+    for g in graphs:
+        g.replay()
+        runs = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            g.replay()
+            b.record()
+            b.synchronize()
+            runs.append(a.elapsed_time(b))
+        times.append(sorted(runs)[2])
+    assert times[1] < 3 * times[0], times
+
 def test_scores_of_the_decode_step():
     # the engine's logits of a step: its greedy token is the first alternative, its log probability the target's
     cfg = synth.config("tiny", max_ctx=8)
