@@ -2,12 +2,12 @@
 //
 //   o_i = sum_{j <= pos+i} softmax_j(q_i . k_j / sqrt(d)) v_j,   k_j = ck_j * sk[j / block], v_j = cv_j * sv[j / block]
 //
-// The n_tokens x group query rows that share a KV head are the rows of one matrix: every code is read
-// and widened once for each tile of 8, 16 or 32 of them (16 at most at 128 dimensions). The work is a flat list of key tiles (sequence, KV head, row tile,
-// tile of KT keys); each warp takes an equal run of it, whatever the sequences' lengths, so that one long
-// sequence spreads over the GPU and a ragged batch stays even. The warps of a CTA have neighbouring runs and join
-// the parts of a unit that lie in them; a CTA whose run covers a unit only in part leaves (m, l, o) in the
-// workspace, and kv8_merge_kernel joins these parts in order, so results do not depend on timing.
+// The n_tokens x group query rows that share a KV head are the rows of one matrix: every code is read and widened once
+// for each tile of 8, 16 or 32 of them (16 at most at 128 dimensions). The work is a flat list of key tiles
+// (sequence, KV head, row tile, tile of KT keys); each warp takes an equal run of it, whatever the sequences'
+// lengths and counts, so that one long sequence spreads over the GPU and a ragged batch stays even. The warps of a
+// CTA have neighbouring runs and join the parts of a unit that lie in them; a CTA whose run covers a unit only in
+// part leaves (m, l, o) in the workspace, and kv8_merge_kernel joins these parts in order, so results do not depend on timing.
 //
 // Each warp streams its own tiles: a ring of bulk asynchronous copies per warp that runs on across the
 // boundaries of the units, no barrier between the warps until their runs end. Products run on the
@@ -20,17 +20,22 @@
 // magnitude, which keeps it in fp16's range, and multiplied back in the scores' fp32 scale. Query and
 // weight are rounded to fp16 (off by 2^-11 at most) for bf16 queries, whose own result is rounded by 2^-8; for
 // fp32 and fp16 queries both enter as two fp16 parts (high and the remainder: 2^-22), with twice the
-// products. Scores, maxima, sums and outputs are fp32.
+// products. Scores, maxima, sums and outputs are fp32. (bf16 rows leave the sums of a run of keys to the tensor instruction,
+// which cuts them off: 2.6e-6 over 8000 keys; fp32 and fp16 rows add each tile's rounded, 4e-7.)
 //
 // A key's V scale 2^e * f (1 <= f < 2) enters its weight: the running maximum M is taken over x + e (x
 // the score in units of log 2), the weight of V is w * f with w = 2^(x + e - M), and the sum of the
-// softmax adds w * 2^-e. So weights are near 1 where they matter whatever the scales of the blocks are.
+// softmax adds w * 2^-e. So weights are near 1 where they matter whatever the scales of the blocks are; where they
+// are 2^86 and more apart, the sums take exponentials of their own (E_SPAN).
 //
-// Measured: 64 sequences of 16 to 8192 keys, 8 KV heads of 64 with 5 query heads each, int8, bf16 queries (270 MB): 57 us
-// with the join, 0.71 of the measured copy rate, bound by the instructions that widen, scale and exponentiate (two
-// issued a clock). One sequence of 131001 keys, 2 heads of 128 (67 MB): 22 us, bound by the chain of each warp's few
-// tiles (1.4 a clock) and the join. 1152 keys, one token: 9 us, all latency. Earlier forms of the first took 116 us
-// (queries as the products' rows), 92 (keys as rows) and 83 (runs by warps, without a unit's fixed cost).
+// Measured: 64 sequences of 16 to 8192 keys, 8 KV heads of 64 with 5 query heads each, int8, bf16 queries (270 MB): 56 us
+// with the join, 0.72 of the measured copy rate; 61 with fp32 or fp16 queries. Two of four issue slots are used and no pipe is
+// busy for more than half of the time: what 8 to 12 warps, all that the registers allow, leave uncovered of the latency
+// of a tile's steps (widening, products, maximum, exponentials). One sequence of 131001 keys, 2 heads of 128 (67 MB): 23 us,
+// bound by the chain of each warp's few tiles (1.4 a clock) and the join. 1152 keys, one token: 9 us, all latency.
+// Earlier forms of the first took 116 us (queries as the products' rows), 92 (keys as rows) and 83 (runs by
+// warps, without a unit's fixed cost). Kernels of 32 rows spill (170 to 670 bytes of stores at 255 registers), of two-part
+// operands also those of 16 rows (150 to 190), and at 128 dimensions of 8 (100).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -417,7 +417,8 @@ typedef struct {
  * a new block). Codes are x / scale in fp32, rounded to the nearest code, ties to even. A NaN or an
  * infinity among the values makes the block's scale NaN, and so everything read from the block until
  * it is started again. Codes of positions past the new ones are left as they were and mean nothing
- * until they are written. */
+ * until they are written. The rotation is off by 2^-19 of a pair's size at most, far less than a code's
+ * half step, but a rotated key next to a tie of two codes may become either. */
 tinfer_status tinfer_op_kv8_append(const tinfer_kv8* cache, const tinfer_rows* k, const tinfer_rows* v,
                                    int n_tokens, const int32_t* pos_dev, const int32_t* counts_dev,
                                    double rope_theta, int32_t* status_dev, void* stream);
@@ -431,8 +432,14 @@ tinfer_status tinfer_op_kv8_read(const tinfer_kv8* cache, int n_tokens, const in
 /* Attention of n_tokens query tokens of each sequence over the cache, whose positions up to the last
  * query's must have been appended: token i of sequence s attends to positions [0, pos[s] + i], scale
  * 1/sqrt(head_dim), query head h reading KV head h / (n_heads / n_kv_heads). q and out: rows of n_heads
- * heads, one dtype; fp32 and fp16 queries are multiplied in fp32-like precision (two fp16 parts), bf16
- * ones in fp16 (scores have to stay in fp32's range). out may be q itself, with the same strides, and no other
+ * heads, one dtype. Scores, maxima and sums are fp32: scores, and the largest magnitude of a query row times
+ * that of a key block, have to stay in its range; V scales may lie as far apart as they can. fp32 and fp16
+ * queries and weights are multiplied as two fp16 parts (2^-22); bf16 ones as one: the rotated query and each
+ * weight are rounded to 11 bits, and weights far below the row's largest to 2^-38 of it, all below the
+ * rounding of the bf16 result. More than 32 bf16 rows (tokens times query heads of a KV head; 64 at head_dim
+ * 128) go to the large tensor products: a 4096-token prompt takes 102 us in bf16 and 810 in fp32 or fp16, so
+ * a program that need not keep a prompt's 24 bits (the prefill product's fp32 rows, say) converts them first.
+ * out may be q itself, with the same strides, and no other
  * overlap of the two is sound. lse_dev: fp32 [n_seqs][n_tokens][n_heads], may be NULL: the natural
  * logarithm of the sum of exp(score). workspace_dev: tinfer_kv8_attention_workspace bytes of device
  * memory, 16-byte aligned, no initial values; calls that may overlap in time (other streams, other
@@ -459,7 +466,8 @@ tinfer_status tinfer_op_kv8_attention(const tinfer_kv8* cache, int n_heads, int 
  * are left, the rest is id -1 with -infinity). A row whose tokens are all masked has logp -infinity
  * and entropy 0. A row with a NaN or +infinity has NaN, and ids -1. logp_dev, entropy_dev and targets_dev
  * may be NULL (logp_dev needs targets_dev); top_k in [0, 32], the top outputs NULL when it is 0.
- * Results do not depend on timing.
+ * Results do not depend on timing. Sums are fp32: a logp or an entropy near 0 is known to about 1e-7, not to
+ * its own 24 bits.
  * Asynchronous on `stream`, no workspace. vocab <= 2^18, else TINFER_ERR_UNSUPPORTED. */
 tinfer_status tinfer_op_logprobs(int rows, int vocab, int dtype, const void* logits_dev, long long row_stride,
                                  const int32_t* targets_dev, int top_k, float* logp_dev, float* entropy_dev,
