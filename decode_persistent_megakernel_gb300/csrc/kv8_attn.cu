@@ -66,9 +66,9 @@ struct Shape {
 
 // ---- the list of work -------------------------------------------------------------------------
 // Sequence s has a unit for each KV head and each tile of its own query rows; each is FIXED empty places, which stand for
-// what a unit costs beside its tiles (its queries, its end), and ceil(len / KT) tiles (those past the last key that a unit's
-// rows see are stepped over, so a prompt's first rows count for more than they cost: up to twice the mean work for one
-// warp). prefix[s] counts the places before it. Called by all threads of a CTA; returns the total.
+// what a unit costs beside its tiles (its queries, its end), and a place for each key tile that its rows may see, so
+// that a prompt's first rows, which see few keys, count for little. prefix[s] counts the places before it. Called
+// by all threads of a CTA; returns the total.
 constexpr int FIXED = 4;
 
 // In shared memory: prefix, then position and count of every sequence's new tokens (0, 0 for one that is passed over).
@@ -79,18 +79,46 @@ struct List {
 };
 size_t list_bytes(int n) { return (size_t)((n + 2) & ~1) * 4 + (size_t)n * 8; }
 
-// Tiles of query rows of a KV head in a sequence with `count` new tokens.
-template <int ROWS>
-__device__ __forceinline__ int row_tiles_of(const AttnParams& q, int count) {
-  return q.row_tiles > 1 ? (q.group * count + ROWS - 1) / ROWS : 1;
-}
+// The units of a KV head in one sequence. The last row of row tile rt sees pos + 1 + j keys, j = (rt ROWS + ROWS - 1) / group,
+// and j / KT = rt / m with m = group KT / ROWS (ROWS divides KT), so base + rt / m tiles hold them, and are easily summed.
+template <int D, int ROWS>
+struct RowTiles {
+  static_assert(Shape<D>::KT % ROWS == 0, "row tiles that see one key tile more come in groups of m");
+  int n, base, m;
+  __device__ __forceinline__ RowTiles(const AttnParams& q, int pos, int count) {
+    constexpr int KT = Shape<D>::KT;
+    n = q.row_tiles > 1 ? (q.group * count + ROWS - 1) / ROWS : 1;
+    base = n > 1 ? pos / KT + 2 : (pos + count + KT - 1) / KT;
+    m = q.group * (KT / ROWS);
+  }
+  __device__ __forceinline__ int tiles(int rt) const { return n == 1 ? base : base + rt / m; }
+  __device__ __forceinline__ int before(int rt) const {  // places of the row tiles before rt
+    if (n == 1) return rt * (base + FIXED);
+    const int k = rt / m;
+    return rt * (base + FIXED) + k * (rt - m) - m * (k * (k - 1) / 2);
+  }
+  // KV head, row tile, tile of keys (negative: an empty place) and tiles of the unit at place `in` of the sequence. Not
+  // inlined: it runs once for a unit, and its registers would be the products'.
+  __device__ __noinline__ int4 place(int in) const {
+    const int per_head = before(n), head = in / per_head, off = in - head * per_head;
+    int a = 0, b = n;  // before(a) <= off < before(b)
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if (before(mid) <= off) a = mid;
+      else b = mid;
+    }
+    return make_int4(head, a, off - before(a) - FIXED, tiles(a));
+  }
+};
 
 template <int D, int ROWS>
 __device__ __forceinline__ int places_of(const AttnParams& q, int s, const List& list) {
   int pos, count;
   if (!span_of(q.sp, s, q.c.max_ctx, pos, count) && blockIdx.x == 0 && q.sp.status) atomicOr(q.sp.status, STATUS_BAD_POS);
   list.span[s] = make_int2(pos, count);
-  return count > 0 ? ((pos + count + Shape<D>::KT - 1) / Shape<D>::KT + FIXED) * q.c.n_kv * row_tiles_of<ROWS>(q, count) : 0;
+  if (count == 0) return 0;
+  const RowTiles<D, ROWS> r(q, pos, count);
+  return r.before(r.n) * q.c.n_kv;
 }
 
 template <int D, int ROWS, int NT>
@@ -149,7 +177,7 @@ __device__ __forceinline__ Deal deal(int total, int grid, int max_warps) {
 // A place in the list, with what the tiles of its unit share.
 template <int D, int ROWS>
 struct Place {
-  int x, seq, unit, tile, tiles;  // tile < 0: an empty place; tiles: of one unit of this sequence
+  int x, seq, tile, tiles;        // tile < 0: an empty place; tiles: of the unit
   int limit;                      // keys that some row of the unit sees
   int row0;                       // the KV head's first row among all rows of the cache
   int pos, count, head, rt;       // the sequence's new tokens; KV head and row tile of the unit
@@ -161,17 +189,20 @@ struct Place {
     const int2 span = list.span[seq];
     pos = span.x;
     count = span.y;
-    tiles = (pos + count + Shape<D>::KT - 1) / Shape<D>::KT;
+    const RowTiles<D, ROWS> r(q, pos, count);
     const int in = at - list.prefix[seq];
-    unit = in / (tiles + FIXED);
-    tile = in - unit * (tiles + FIXED) - FIXED;
-    head = unit;
-    rt = 0;
-    limit = pos + count;
-    if (q.row_tiles > 1) {
-      const int row_tiles = row_tiles_of<ROWS>(q, count);
-      head = unit / row_tiles;
-      rt = unit - head * row_tiles;
+    if (r.n == 1) {
+      tiles = r.base;
+      head = in / (tiles + FIXED);
+      rt = 0;
+      tile = in - head * (tiles + FIXED) - FIXED;
+      limit = pos + count;
+    } else {
+      const int4 p = r.place(in);
+      head = p.x;
+      rt = p.y;
+      tile = p.z;
+      tiles = p.w;
       limit = pos + min((rt * ROWS + ROWS - 1) / q.group, count - 1) + 1;
     }
     row0 = (seq * q.c.n_kv + head) * q.c.max_ctx;
@@ -755,25 +786,28 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
   if (tid == 0 && *failed && q.sp.status) atomicOr(q.sp.status, STATUS_TIMEOUT);
 }
 
-// Joins the units that several CTAs hold: CTA (unit of a sequence as the longest one has them, slice of its rows). It is launched with the kernel
-// before it and builds its list meanwhile; 2 to 4 us after it, latency of a few dependent loads from L2.
+// Joins the units that several CTAs hold: CTA (unit, as the sequence with the most tokens has them, slice of its rows).
+// It is launched with the kernel before it and builds its list meanwhile; 2 to 4 us after it, latency of a few dependent
+// loads from L2. CTAs without a unit leave at once: in a call of one 256-token chunk and 31 single tokens they are 31 of 32.
 template <int D, int NG, typename T>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) kv8_merge_kernel(const __grid_constant__ AttnParams q) {
-  constexpr int KT = Shape<D>::KT, ROWS = 8 * NG;
+  constexpr int ROWS = 8 * NG;
   extern __shared__ int list_raw[];
   __shared__ int scan[JOIN_WARPS];
-  const List list(list_raw, q.c.n_seqs);
+  const int seq = blockIdx.x / q.units, unit = blockIdx.x % q.units, head = unit / q.row_tiles, rt = unit % q.row_tiles;
+  int pos, count;
+  span_of(q.sp, seq, q.c.max_ctx, pos, count);
+  const RowTiles<D, ROWS> r(q, pos, count);
+  const bool there = count > 0 && rt < r.n;
+  if (!there && (blockIdx.x || blockIdx.y)) return;  // (one CTA waits, so that the kernel never ends before the other)
   // the list depends on the call's inputs alone, so it is built while the parts are still being made
+  const List list(list_raw, q.c.n_seqs);
   const int total = build_list<D, ROWS, JOIN_WARPS * 32>(q, list, scan);
   const Deal share = deal(total, q.grid, q.warps);
   const int per = share.per * share.warps;  // of a CTA
-  const int seq = blockIdx.x / q.units, unit = blockIdx.x % q.units;
-  const int pos = list.span[seq].x, count = list.span[seq].y;
-  const int tiles = (pos + count + KT - 1) / KT, row_tiles = row_tiles_of<ROWS>(q, count);
-  const int head = unit / q.row_tiles, rt = unit % q.row_tiles;
-  const int a = list.prefix[seq] + (head * row_tiles + rt) * (tiles + FIXED) + FIXED, c0 = a / per, parts = (a + tiles - 1) / per - c0 + 1;
+  const int a = list.prefix[seq] + head * r.before(r.n) + r.before(rt) + FIXED, c0 = a / per, parts = (a + r.tiles(rt) - 1) / per - c0 + 1;
   pdl_wait();  // the parts are complete
-  if (count == 0 || rt >= row_tiles || parts <= 1) return;  // no rows, or one CTA had it whole
+  if (!there || parts <= 1) return;  // no rows, or one CTA had it whole
   join_parts<D, ROWS, T>(q, seq, head, rt * ROWS, min(q.group * count - rt * ROWS, ROWS), c0, parts, WEIGHT_SHIFT);
 }
 
@@ -840,7 +874,7 @@ cudaError_t launch_f(AttnParams& q, int head_dim, int rows, int dtype, cudaStrea
 }
 
 // Rows of a unit of work and row tiles of a KV head; false where the counts do not fit: rows of the cache (their
-// coordinates in the copies), query rows, the list of tiles and the units are counted in 32 bits.
+// coordinates in the copies), query rows, the list of tiles (2^30 and one place for each unit) and the units are counted in 32 bits.
 struct Units {
   int rows, row_tiles;
 };

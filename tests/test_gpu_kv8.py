@@ -846,6 +846,19 @@ def test_two_captured_calls_replayed_side_by_side_follow_their_inputs(hq, hk, d,
             assert torch.equal(outs[i], cache.attention(qs[i], poss[i], counts=counts[i], rope_theta=10000.0)), (turn, i)
     assert cache.error() == 0
 
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 64), (12, 2, 128)])
+def test_a_prompt_is_dealt_out_by_the_keys_that_its_rows_see(hq, hk, d):
+    # T key tiles hold the prompt; a row tile from position 0 on sees T / 2 of them on average, one of as many rows behind the
+    # prompt 3 T / 2. With a unit's own cost of up to 16 tiles, equal runs take (64 + 16) / (192 + 16) = 0.39 of the time at T = 128;
+    # where every row tile counts by all of its T places, some warp has a run without empty ones: half
+    n = 8192
+    cache = filled(hk, d, [2 * n], 2 * n, E4M3, 64, seed=6, spread=0.3)
+    q = normal((1, n, hq, d), 7).cuda()
+    out, first, second = torch.zeros_like(q), ints(0), ints(n)
+    ahead = time_of(lambda: cache.attention(q, first, out=out))
+    behind = time_of(lambda: cache.attention(q, second, out=out))
+    assert ahead < 0.45 * behind, (ahead, behind)
+
 def test_python_layer_refuses_bad_tensors():
     cache = T.Kv8Cache(2, 64, 100, n_seqs=2)
     x, pos = torch.zeros(2, 3, 2, 64, device="cuda"), ints(0, 0)
