@@ -768,11 +768,12 @@ __global__ void __launch_bounds__(Roles<D>::NT, 1) prefill_kernel(const __grid_c
 template <int D, typename T>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) prefill_merge_kernel(const __grid_constant__ AttnParams q) {
   extern __shared__ long long prefix64[];
-  const long long total = build_prefix<JOIN_WARPS * 32>(q, prefix64);
-  const long long per = run_length(total, q.grid);
   const int seq = blockIdx.x / q.units, unit = blockIdx.x % q.units, head = unit / q.row_tiles, rt = unit % q.row_tiles;
   Span64 sp;
   sp.of(q, seq);
+  if (rt >= sp.n && (blockIdx.x || blockIdx.y)) return;  // (one CTA waits, so that the kernel never ends before the other)
+  const long long total = build_prefix<JOIN_WARPS * 32>(q, prefix64);
+  const long long per = run_length(total, q.grid);
   int c0 = 0, parts = 0;
   if (rt < sp.n) {
     const long long start = prefix64[seq] + head * sp.before(sp.n) + sp.before(rt) + FIXED_KEYS;
