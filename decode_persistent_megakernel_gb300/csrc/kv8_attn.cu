@@ -34,8 +34,8 @@
 // of a tile's steps (widening, products, maximum, exponentials). One sequence of 131001 keys, 2 heads of 128 (67 MB): 23 us,
 // bound by the chain of each warp's few tiles (1.4 a clock) and the join. 1152 keys, one token: 9 us, all latency.
 // Earlier forms of the first took 116 us (queries as the products' rows), 92 (keys as rows) and 83 (runs by
-// warps, without a unit's fixed cost). Kernels of 32 rows spill (170 to 670 bytes of stores at 255 registers), of two-part
-// operands also those of 16 rows (150 to 190), and at 128 dimensions of 8 (100).
+// warps, without a unit's fixed cost). Kernels of 32 rows spill (190 bytes of stores at 255 registers, 680 with two-part
+// operands), of two-part operands also those of 16 rows (190 to 210), and at 128 dimensions of 8 (110).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -600,8 +600,9 @@ __global__ void __launch_bounds__(Cfg<D, NG, SPLIT>::NT, 1) kv8_attn_kernel(cons
       // ---- o^T += V^T weights, 16 keys at a time; an 8 x 8 transpose turns the scores' layout (keys by
       // rows) into that of a right operand (keys down the columns)
       // The instruction's own sums are cut off, not rounded, which adds up over a long run of keys: two-part operands, whose
-      // precision it would spoil, take a tile's products by themselves (32 sequences of 8000 keys, fp32: off by 4e-7 where
-      // they were off by 2.6e-6, in the same 52 us; at 128 dimensions, whose registers run short, 37 us against 35)
+      // precision it would spoil, take a tile's products by themselves (32 sequences of 8000 keys, 40 heads of 64 over 8, fp32,
+      // 262 MB: off by 4e-7 where they were off by 2.6e-6, in the same 52 us; 12 heads of 128 over 2, whose registers run
+      // short, 131 MB: 37 us against 35)
       float part[SPLIT == 2 ? MD : 1][NG][4];
       if (SPLIT == 2) {
 #pragma unroll

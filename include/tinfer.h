@@ -437,7 +437,7 @@ tinfer_status tinfer_op_kv8_read(const tinfer_kv8* cache, int n_tokens, const in
  * queries and weights are multiplied as two fp16 parts (2^-22); bf16 ones as one: the rotated query and each
  * weight are rounded to 11 bits, and weights far below the row's largest to 2^-38 of it, all below the
  * rounding of the bf16 result. More than 32 bf16 rows (tokens times query heads of a KV head; 64 at head_dim
- * 128) go to the large tensor products: a 4096-token prompt takes 102 us in bf16 and 810 in fp32 or fp16, so
+ * 128) go to the large tensor products: a 4096-token prompt takes 102 us in bf16 and 470 in fp32 or fp16, so
  * a program that need not keep a prompt's 24 bits (the prefill product's fp32 rows, say) converts them first.
  * out may be q itself, with the same strides, and no other
  * overlap of the two is sound. lse_dev: fp32 [n_seqs][n_tokens][n_heads], may be NULL: the natural
