@@ -516,6 +516,7 @@ class Kv8Cache:
     The cache keeps one workspace for the attention, large enough for every call (workspace_bytes(): 22 or 43 MB at
     head_dim 64 or 128): `workspace`, a uint8 tensor that the caches of several layers may share, or a new one. A call
     that may overlap another one in time (another stream, a graph replayed beside it) passes one of its own.
+    Keep the cache until its work on other streams than the one it was made on has ended, and as long as graphs replay it.
 
     Calls report into `status`, an int32 tensor that each call clears, or, without one, into a word of the cache that
     error() reads. Bit 0: positions of a sequence were outside the cache; bit 1: a wait on the device ran out, and the
