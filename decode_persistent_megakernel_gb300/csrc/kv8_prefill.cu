@@ -13,7 +13,7 @@
 // Tensor memory: two (three at 64 dimensions) 128-column score buffers and two D-column outputs. Products are issued
 // by one warp and run in order, so new scores may follow the product that read the weights lying in their place.
 // The softmax and the second product go by halves of 64 keys, so that the first half's product runs under the
-// second half's exponentials. (Scores by halves as well cost a 128-row operand read twice: 115 us for the 4096-token prompt against 114.)
+// second half's exponentials. (Scores by halves as well cost a 128-row operand read twice, and gained nothing.)
 //
 // A row's running maximum is replaced only where one of its warp's would grow by nearly 2^2, and then all of them are: the
 // outputs in tensor memory are rescaled by the rows' threads after the exponentials, when the product before is done and
@@ -48,11 +48,11 @@ struct Roles {
   static constexpr int BUFFERS = D == 64 ? 3 : 2;       // of 128 x 128 scores in tensor memory, beside two outputs of D columns
   static constexpr int ANGLES = D == 64 ? 4096 : 1472;  // of a tile: all of 128 tokens, or of 23 (or 8 at a time)
 };
-constexpr int FETCH = 4;           // key tiles that are fetched into L2 ahead (64 rows of 32 x 4000 keys 111 -> 102 us)
+constexpr int FETCH = 4;           // key tiles that are fetched into L2 ahead (64 rows of 32 x 4000 keys, 8 heads of 64: 114 -> 108 us)
 constexpr int KV_STAGES = 2, SCALE_SLOTS = 4;
 constexpr int SHIFT = 13;          // of the weights
 constexpr float GROW = 1.99f;      // a maximum may lag behind by 2^GROW: 2^(SHIFT + GROW) 2 is below fp16's 65504
-constexpr int FIXED_KEYS = 768;    // what a unit costs beside its keys, in keys (4096-token prompt: 98 us, 109 with 384)
+constexpr int FIXED_KEYS = 768;    // what a unit costs beside its keys, in keys (4096-token prompt: 102 us, 114 with 384)
 
 template <int D>
 struct Smem {
@@ -797,7 +797,7 @@ cudaError_t launch_t(AttnParams& q, cudaStream_t st) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   // a CTA for 32 rows of few parts each, four rows of a warp; for fewer rows where units are few and have many parts
-  // (72 rows of 8000 keys, two heads of 128: 42 us by 32 rows, 24 by one)
+  // (72 rows of 8000 keys, two heads of 128: 42 us by 32 rows, 25 by one)
   const int units = q.c.n_seqs * q.units;
   cfg.gridDim = dim3((unsigned)units, (unsigned)std::min(std::max(512 / units, ROWS / 32), std::min(ROWS, q.group * q.sp.n_tokens)));
   cfg.blockDim = dim3(JOIN_WARPS * 32);
