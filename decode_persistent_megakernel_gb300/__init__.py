@@ -38,7 +38,7 @@ EXPORTS = [
     "tinfer_packed_row_bytes", "tinfer_pack_matrix", "tinfer_op_gemv", "tinfer_op_attention",
     "tinfer_op_attention_noalloc", "tinfer_op_gemv_batch", "tinfer_moe_packed_bytes", "tinfer_pack_moe", "tinfer_op_moe",
     "tinfer_op_gemm_bf16", "tinfer_op_kv8_append", "tinfer_op_kv8_read", "tinfer_kv8_attention_workspace",
-    "tinfer_op_kv8_attention", "tinfer_op_logprobs",
+    "tinfer_op_kv8_attention", "tinfer_op_logprobs", "tinfer_op_qk_norm_rope",
 ]
 
 
@@ -123,6 +123,7 @@ def lib():
             "tinfer_op_kv8_read": ([kvp, I, P, P, rowp, rowp, P, P], I),
             "tinfer_kv8_attention_workspace": ([kvp, I, I], Z),
             "tinfer_op_kv8_attention": ([kvp, I, I, rowp, P, P, D, rowp, P, P, Z, P, P], I),
+            "tinfer_op_qk_norm_rope": ([I, I, I, I, I, I, rowp, rowp, P, P, D, D, P, P, rowp, rowp, P, P], I),
             "tinfer_op_logprobs": ([I, I, I, P, LL, P, I, P, P, P, P, P], I),
         }
         for name, (args, res) in sig.items():
@@ -323,6 +324,14 @@ def tinfer_op_logprobs(rows, vocab, dtype, logits, row_stride, targets, top_k, l
                        stream=None) -> int:
     return lib().tinfer_op_logprobs(rows, vocab, dtype, _ptr(logits), row_stride, _ptr(targets), top_k, _ptr(logp),
                                     _ptr(entropy), _ptr(top_ids), _ptr(top_logp), _stream(stream))
+
+
+def tinfer_op_qk_norm_rope(n_seqs, n_tokens, n_heads, n_kv_heads, head_dim, rotary_dim, q: tinfer_rows, k: tinfer_rows,
+                           q_gain, k_gain, eps, rope_theta, pos, counts, q_out: tinfer_rows, k_out: tinfer_rows,
+                           status=None, stream=None) -> int:
+    return lib().tinfer_op_qk_norm_rope(n_seqs, n_tokens, n_heads, n_kv_heads, head_dim, rotary_dim, q, k, _ptr(q_gain),
+                                        _ptr(k_gain), eps, rope_theta, _ptr(pos), _ptr(counts), q_out, k_out, _ptr(status),
+                                        _stream(stream))
 
 
 def make_config(c: dict, exec_mode: int = TINFER_MEGAKERNEL) -> tinfer_config:
@@ -667,3 +676,57 @@ def logprobs(logits, targets=None, top_k: int = 0, stream=None):
           (rows, vocab, dtype, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _ptr(targets), top_k,
            _ptr(logp), entropy.data_ptr(), _ptr(ids), _ptr(top)), dev, stream)
     return logp, entropy, ids, top
+
+
+def _int32s(what, t, n, device):
+    """Address of an int32 argument of n values (None: no argument)."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous int32 tensor of {n} on {device} is wanted")
+    return t.data_ptr()
+
+
+def qk_norm_rope(q, k, q_gain=None, k_gain=None, pos=None, counts=None, eps: float = 1e-6, rope_theta: float = 0.0,
+                 rotary_dim: int | None = None, out=None, dtype=None, status=None, stream=None):
+    """(q, k) with each head divided by its root mean square, scaled by the gains and rotated to its position
+    (tinfer_op_qk_norm_rope): what goes to Kv8Cache.append and Kv8Cache.attention with rope_theta 0 in models that normalise
+    queries and keys. q and k are rows [n_seqs, n_tokens, heads, head_dim] as in Kv8Cache, the gains float32 [head_dim]
+    (None: ones), pos and counts int32 [n_seqs] (pos may be None where nothing is rotated). The first rotary_dim
+    elements of a head are rotated (None: all), none with rope_theta 0. Results go to `out` ((q, k) itself: in place), or to new
+    tensors of `dtype` (that of q when None), zero where a sequence has fewer tokens. status: int32 tensor, bit 0: positions or
+    counts of a sequence were bad and it was passed over."""
+    import torch
+    device = q.device
+    if device.type != "cuda":
+        raise ValueError("q is not on a CUDA device")
+    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+        raise ValueError(f"rows [n_seqs, n_tokens, heads, head_dim] are wanted, got {tuple(q.shape)} and {tuple(k.shape)}")
+    n_seqs, n_tokens, n_heads, head_dim = q.shape
+    if out is None:
+        with _making(stream, device):
+            out = tuple(torch.zeros(t.shape, dtype=dtype or q.dtype, device=device) for t in (q, k))
+    if pos is None:
+        if rope_theta:
+            raise ValueError("pos is wanted where rows are rotated")
+        with _making(stream, device):
+            pos = torch.zeros(n_seqs, dtype=torch.int32, device=device)
+
+    def rows(what, t, like):
+        if t.device != device or t.shape != like.shape or t.stride(3) != 1:
+            raise ValueError(f"{what}: rows {tuple(like.shape)} with contiguous elements on {device} are wanted")
+        return tinfer_rows(t.data_ptr(), _dtype(t), *t.stride()[:3])
+
+    for what, g in (("q_gain", q_gain), ("k_gain", k_gain)):
+        if g is not None:
+            _on(what, g, device, torch.float32, (head_dim,))
+            if not g.is_contiguous():
+                raise ValueError(f"{what} is not contiguous")
+    args = (n_seqs, n_tokens, n_heads, k.shape[2], head_dim, head_dim if rotary_dim is None else rotary_dim,
+            rows("q", q, q), rows("k", k, k), _ptr(q_gain), _ptr(k_gain), eps, rope_theta,
+            _int32s("pos", pos, n_seqs, device), _int32s("counts", counts, n_seqs, device), rows("out[0]", out[0], q),
+            rows("out[1]", out[1], k), _int32s("status", status, 1, device))
+    if n_seqs and n_tokens:  # (else nothing to launch)
+        _call("tinfer_op_qk_norm_rope", lib().tinfer_op_qk_norm_rope, args, device, stream)
+    return out

@@ -473,6 +473,28 @@ tinfer_status tinfer_op_logprobs(int rows, int vocab, int dtype, const void* log
                                  const int32_t* targets_dev, int top_k, float* logp_dev, float* entropy_dev,
                                  int32_t* top_ids_dev, float* top_logp_dev, void* stream);
 
+/* Norms of queries and keys head by head with the rotary position, in one pass (models that normalise q and k
+ * between the projections and the attention): for each row x of q and k
+ *   y = R(pos) (x g / sqrt(mean(x^2) + eps)),   the mean over the row's head_dim elements,
+ * R the rotary position of the decode step (half-split pairs: element i with i + rotary_dim / 2) on the first
+ * rotary_dim elements, the others passed on; rope_theta 0: no rotation, else at least 1. The results go to
+ * tinfer_op_kv8_append and tinfer_op_kv8_attention with rope_theta 0. q, k and their outputs are rows as above (of n_heads and n_kv_heads
+ * heads); q and k have one dtype, the outputs the same, or any where q and k are fp32. q_gain_dev, k_gain_dev: fp32
+ * [head_dim], NULL: ones. pos_dev, counts_dev and status_dev as above; positions and counts are bad where pos < 0, a
+ * count is outside [0, n_tokens] or their sum is beyond 2^31 - 1. *status_dev is cleared first. An output may be its own
+ * input (the same rows, strides and dtype: in place); no other overlap is sound.
+ * Computed in fp32 and rounded once: off by a few 2^-24 of a pair's size. A row whose squares leave fp32's range is
+ * computed in fp64. A row with a NaN or an infinity gives what the formula gives (a NaN there, with an infinity 0 elsewhere),
+ * and a row of zeros with eps 0 gives NaN. eps >= 0. Asynchronous on `stream`, no workspace.
+ * head_dim and rotary_dim multiples of 16, head_dim at most 256, heads at most 1024, n_seqs and n_tokens at most 2^24, else
+ * TINFER_ERR_UNSUPPORTED. */
+tinfer_status tinfer_op_qk_norm_rope(int n_seqs, int n_tokens, int n_heads, int n_kv_heads, int head_dim,
+                                     int rotary_dim, const tinfer_rows* q, const tinfer_rows* k,
+                                     const float* q_gain_dev, const float* k_gain_dev, double eps,
+                                     double rope_theta, const int32_t* pos_dev, const int32_t* counts_dev,
+                                     const tinfer_rows* q_out, const tinfer_rows* k_out, int32_t* status_dev,
+                                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,233 @@
+"""Norms of queries and keys with the rotary position on the GPU against a plain implementation in 64 bits.
+
+Tolerance, in units of 2^-24 of the size |u| + |v| of a rotated pair (u, v): a sum of 256 squares takes 16 additions in a
+lane and 4 across lanes, each at most 1, halved by the root: 10; the mean's division, the epsilon's addition and the root 2;
+the products with the factor and the gain 2; the angle (2^-25 half turns, pi 2^-25 = 1.6) and the cosine's own error (2 of
+the largest) 3.6; the rotation's two roundings 2: together below 20. The result is rounded to its type by half a step."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import decode_persistent_megakernel_gb300 as T  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+OFF = 20 * 2.0 ** -24
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    T.build()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def reference(x, gain, pos, eps, theta, rotary):
+    """y and the size of each element's pair; x [s][t][h][d], float64 on the CPU."""
+    x = x.double().cpu()
+    y = x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) * (1.0 if gain is None else gain.double().cpu())
+    if not theta or not rotary:
+        return y, y.abs()
+    half = rotary // 2
+    f = theta ** (-2.0 * torch.arange(half, dtype=torch.float64) / rotary)
+    a = ((pos.cpu().double()[:, None] + torch.arange(x.shape[1]))[..., None] * f)[:, :, None, :]
+    u, v, rest = y[..., :half], y[..., half:rotary], y[..., rotary:]
+    size = u.abs() + v.abs()
+    c, s = torch.cos(a), torch.sin(a)
+    return torch.cat([u * c - v * s, v * c + u * s, rest], -1), torch.cat([size, size, rest.abs()], -1)
+
+
+def close(got, ref, size):
+    half = torch.finfo(got.dtype).eps / 2
+    tiny = torch.finfo(got.dtype).smallest_normal * torch.finfo(got.dtype).eps  # a step of the subnormals
+    err = (got.cpu().double() - ref).abs()
+    bound = (size * OFF) * (1 + half) + ref.abs() * half + tiny
+    assert bool((err <= bound).all()), float((err - bound).max())
+
+
+def check(q, k, gq, gk, pos, counts=None, eps=1e-6, theta=10000.0, rotary=None, **kw):
+    rotary_dim = q.shape[-1] if rotary is None else rotary
+    given = [t.clone() for t in (q, k)]
+    got = T.qk_norm_rope(q, k, gq, gk, pos, counts=counts, eps=eps, rope_theta=theta, rotary_dim=rotary, **kw)
+    t = torch.arange(q.shape[1])
+    n = torch.full((q.shape[0],), q.shape[1]) if counts is None else counts.cpu()
+    valid = (t[None, :] < n[:, None])[:, :, None, None]
+    for y, x, g in zip(got, given, (gq, gk)):
+        ref, size = reference(x, g, pos, eps, theta, rotary_dim)
+        close(torch.where(valid.to(y.device), y, 0), torch.where(valid, ref, 0.0), torch.where(valid, size, 0.0))
+    return got
+
+
+def rows(s, t, h, d, dtype, seed, scale=2.0):
+    return (scale * torch.randn((s, t, h, d), generator=gen(seed))).to(dtype).cuda()
+
+
+def gains(d, seed):
+    return (1 + 0.3 * torch.randn(d, generator=gen(seed))).cuda()
+
+
+def at(s, lo, hi, seed=0):
+    return torch.randint(lo, hi + 1, (s,), generator=gen(seed), dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [16, 32, 48, 64, 80, 96, 128, 192, 256])
+def test_sizes_and_types(dtype, d):
+    for s, t, hq, hk in ((1, 1, 1, 1), (3, 5, 5, 2), (2, 37, 7, 7), (1, 300, 40, 8)):
+        q, k = rows(s, t, hq, d, dtype, d), rows(s, t, hk, d, dtype, d + 1)
+        for rotary in sorted({0, 16, d // 32 * 16, d}):
+            check(q, k, gains(d, 1), gains(d, 2), at(s, 0, 9000), rotary=rotary)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_tokens(dtype):
+    q, k = rows(3, 4001, 12, 128, dtype, 5), rows(3, 4001, 2, 128, dtype, 6)
+    check(q, k, gains(128, 1), gains(128, 2), at(3, 0, 100000), torch.tensor([4001, 0, 1234], dtype=torch.int32).cuda())
+
+
+def test_without_gains_rotation_or_positions():
+    q, k = rows(2, 9, 4, 64, torch.float32, 1), rows(2, 9, 2, 64, torch.float32, 2)
+    check(q, k, None, None, at(2, 0, 50), theta=0.0)
+    a = T.qk_norm_rope(q, k)
+    b = T.qk_norm_rope(q, k, torch.ones(64, device="cuda"), torch.ones(64, device="cuda"), at(2, 5, 9), rope_theta=0.0)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_fp32_rows_to_16_bits(dtype):
+    q, k = rows(2, 33, 8, 64, torch.float32, 1), rows(2, 33, 4, 64, torch.float32, 2)
+    check(q, k, gains(64, 1), gains(64, 2), at(2, 0, 500), dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_of_a_fused_projection_in_place_and_apart(dtype):
+    s, t, hq, hk, d = 3, 21, 6, 2, 64
+    qkv = rows(s, t, hq + 2 * hk, d, dtype, 3)
+    pos, counts = at(s, 0, 99), torch.tensor([21, 4, 0], dtype=torch.int32).cuda()
+    apart = check(qkv[:, :, :hq], qkv[:, :, hq:hq + hk], gains(d, 1), gains(d, 2), pos, counts)
+    before = qkv.clone()
+    q, k = qkv[:, :, :hq], qkv[:, :, hq:hq + hk]
+    check(q, k, gains(d, 1), gains(d, 2), pos, counts, out=(q, k))
+    for i, n in enumerate(counts.tolist()):  # rows past a sequence's last and the values are left as they were
+        assert torch.equal(qkv[i, n:], before[i, n:])
+        assert torch.equal(qkv[i, :n, :hq], apart[0][i, :n]) and torch.equal(qkv[i, :n, hq:hq + hk], apart[1][i, :n])
+    assert torch.equal(qkv[:, :, hq + hk:], before[:, :, hq + hk:])
+    # heads before tokens, the layout of a cache
+    q, k = rows(s, hq, t, d, dtype, 4).transpose(1, 2), rows(s, hk, t, d, dtype, 5).transpose(1, 2)
+    out = (torch.zeros((s, hq, t, d), dtype=dtype, device="cuda").transpose(1, 2),
+           torch.zeros((s, hk, t, d), dtype=dtype, device="cuda").transpose(1, 2))
+    check(q, k, gains(d, 1), gains(d, 2), pos, counts, out=out)
+    one = rows(1, 1, 1, d, dtype, 6)  # one query row for all
+    check(one.expand(s, t, hq, d), one.expand(s, t, hk, d), None, None, pos, None)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_values_at_the_types_ends(dtype):
+    q, k = rows(1, 6, 4, 128, dtype, 1), rows(1, 6, 2, 128, dtype, 2)
+    for i, scale in enumerate((1e-38, 1e-25, 1e-12, 1e18, 1e30, 1e37)):
+        q[:, i] = (q[:, i].double() * scale).to(dtype)
+        k[:, i] = (k[:, i].double() * scale).to(dtype)
+    q[0, 2, 1] = 0
+    pos = at(1, 70, 70)
+    for eps in (1e-6, 1e-35):
+        check(q, k, gains(128, 1), gains(128, 2), pos, eps=eps)
+    q[0, 2, 1] = 1
+    check(q, k, gains(128, 1), gains(128, 2), pos, eps=0.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_that_are_not_finite_spoil_themselves_alone(dtype):
+    q, k = rows(2, 9, 8, 64, dtype, 1), rows(2, 9, 4, 64, dtype, 2)
+    pos = at(2, 0, 99)
+    want = T.qk_norm_rope(q, k, None, None, pos, rope_theta=10000.0)
+    q[0, 3, 2, 5], q[1, 8, 7, 63], k[0, 0, 1, 0], k[1, 2, 3, 40] = float("nan"), float("inf"), float("-inf"), float("nan")
+    got = T.qk_norm_rope(q, k, None, None, pos, rope_theta=10000.0)
+    for g, w, bad in zip(got, want, (((0, 3, 2), (1, 8, 7)), ((0, 0, 1), (1, 2, 3)))):
+        for b in bad:
+            assert bool(g[b].isnan().any())
+            w[b] = g[b]
+        assert torch.equal(g.nan_to_num(7.0), w.nan_to_num(7.0))
+    assert bool(T.qk_norm_rope(torch.zeros_like(q), k, eps=0.0)[0].isnan().all())
+
+
+def test_far_positions():
+    q, k = rows(4, 3, 2, 64, torch.float32, 1), rows(4, 3, 2, 64, torch.float32, 2)
+    check(q, k, None, None, torch.tensor([0, 1, 999999, 1 << 24], dtype=torch.int32).cuda(), theta=1e6)
+    q2, k2 = q[:1], k[:1]  # the last position of all
+    a = T.qk_norm_rope(q2, k2, None, None, torch.tensor([2 ** 31 - 4], dtype=torch.int32).cuda(), rope_theta=10000.0)
+    assert all(bool(t.isfinite().all()) for t in a)
+
+
+def test_bad_positions_and_counts_are_passed_over_and_reported():
+    s, t = 5, 4
+    q, k = rows(s, t, 4, 64, torch.float32, 1), rows(s, t, 2, 64, torch.float32, 2)
+    pos = torch.tensor([3, -1, 5, 6, 2 ** 31 - 2], dtype=torch.int32).cuda()
+    counts = torch.tensor([4, 4, 5, -1, 3], dtype=torch.int32).cuda()
+    status = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    out = tuple(torch.full_like(x, 7.0) for x in (q, k))
+    T.qk_norm_rope(q, k, None, None, pos, counts, rope_theta=10000.0, out=out, status=status)
+    assert int(status) == 1
+    want = T.qk_norm_rope(q[:1], k[:1], None, None, pos[:1], rope_theta=10000.0, status=status)
+    assert int(status) == 0
+    for o, w in zip(out, want):
+        assert torch.equal(o[:1], w) and bool((o[1:] == 7).all())
+
+
+def test_results_do_not_depend_on_the_neighbours():
+    """A token's row is the same alone and among many, so that a prompt's chunks meet."""
+    q, k = rows(1, 2000, 12, 64, torch.bfloat16, 1), rows(1, 2000, 2, 64, torch.bfloat16, 2)
+    pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = gains(64, 1)
+    whole = T.qk_norm_rope(q, k, g, g, pos, rope_theta=10000.0)
+    part = T.qk_norm_rope(q[:, 777:800], k[:, 777:800], g, g, pos + 777, rope_theta=10000.0)
+    one = T.qk_norm_rope(q[:, 1999:], k[:, 1999:], g, g, pos + 1999, rope_theta=10000.0)
+    for w, p, o in zip(whole, part, one):
+        assert torch.equal(w[:, 777:800], p) and torch.equal(w[:, 1999:], o)
+
+
+def test_side_stream_and_captured_graph_follow_the_positions():
+    q, k = rows(2, 3, 8, 64, torch.float32, 1), rows(2, 3, 2, 64, torch.float32, 2)
+    pos = torch.tensor([5, 60], dtype=torch.int32).cuda()
+    out = tuple(torch.zeros_like(x) for x in (q, k))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    T.qk_norm_rope(q, k, None, None, pos, rope_theta=10000.0, out=out, stream=side)
+    side.synchronize()
+    want = T.qk_norm_rope(q, k, None, None, pos, rope_theta=10000.0)
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        T.qk_norm_rope(q, k, None, None, pos, rope_theta=10000.0, out=out)
+    for step in (0, 7, 4000):
+        pos.copy_(torch.tensor([step, 2 * step], dtype=torch.int32))
+        q.mul_(1.5)
+        graph.replay()
+        want = T.qk_norm_rope(q, k, None, None, pos, rope_theta=10000.0)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_no_tokens():
+    q = torch.zeros((2, 0, 4, 64), device="cuda")
+    a, b = T.qk_norm_rope(q, q[:, :, :2], None, None, torch.zeros(2, dtype=torch.int32, device="cuda"), rope_theta=1e4)
+    assert a.shape == q.shape and b.shape == (2, 0, 2, 64)
+
+
+def test_keys_go_to_the_cache():
+    """Normalised and rotated keys in the cache are those that the cache rotates itself, within its half step."""
+    s, t, hk, d, theta = 2, 40, 2, 64, 10000.0
+    q, k, v = (rows(s, t, h, d, torch.float32, i) for i, h in enumerate((4, hk, hk)))
+    pos = torch.tensor([0, 100], dtype=torch.int32).cuda()
+    _, turned = T.qk_norm_rope(q, k, None, gains(d, 1), pos, rope_theta=theta)
+    _, plain = T.qk_norm_rope(q, k, None, gains(d, 1), pos, rope_theta=0.0)
+    got = []
+    for x, base in ((turned, 0.0), (plain, theta)):
+        cache = T.Kv8Cache(hk, d, 200, n_seqs=s, fmt=T.TINFER_KV8_INT8, block=16)
+        cache.append(x, v, pos, rope_theta=base)
+        got.append(cache.read(t, pos, dtype=torch.float32)[0])
+        assert cache.error() == 0
+    step = turned.abs().amax() / 127
+    assert float((got[0] - got[1]).abs().amax()) <= float(step) * 1.01
+    assert float((got[0] - turned).abs().amax()) <= float(step) * 0.51
