@@ -3,10 +3,15 @@
 //   y = R(pos) (x g / sqrt(mean(x^2) + eps))      mean over the head's head_dim elements, R on its first rotary_dim
 //
 // Bound by HBM for prompts (every element read and written once), by launch latency for a step. L lanes share a row (a
-// power of two, 16 elements a lane: eight and their rotary partners, so that a pair never leaves its thread); the groups
-// of L lanes of a CTA are dealt to its TT tokens, and the groups of one token to its heads. A token's angles are computed
-// once for all its heads, into shared memory, while the first rows are on their way; a thread keeps those of its pairs
-// in registers over its heads. Elements are read and written by the same thread, so rows may be normalised in place.
+// power of two, 16 elements a lane: eight and their rotary partners, so that a pair never leaves its thread). A thread
+// keeps its head and walks over tokens of one sequence, so its gains stay in registers and its addresses move by one
+// addition; the angles of the CTA's tokens are computed once for all heads, into shared memory, while the first rows are
+// on their way. Elements are read and written by the same thread, so rows may be normalised in place.
+//
+// Measured: 8 sequences of 4095 tokens, 14 heads of 128, bf16 (235 MB): 48.5 us, 0.72 of the measured copy rate; one token of 40
+// heads of 64, fp32: 3.5 us. The first took 105 us with several heads to a thread (the frequencies, read one by one from
+// the parameters for each few tokens), 64 to 76 with a token to a warp (addresses, gains and angles anew for each
+// token: 370 instructions a turn). Two rows in flight take 50.7, four 54 (they spill), 16 turns 49.4, 5 turns 51.5.
 #include <algorithm>
 #include <cmath>
 
@@ -15,133 +20,170 @@
 namespace tinfer {
 namespace head_norm {
 
-constexpr int NT = 256, MAX_D = 256, MAX_TT = 8;
-constexpr int ROWS = 2;  // rows of a thread in flight
+constexpr int MAX_NT = 256, MAX_D = 256;
+constexpr int ANGLES = 4096;  // rotary pairs of the tokens of a CTA, at most
+constexpr int IN_FLIGHT = 3;  // rows of a thread on their way
 
 struct Params {
   kv8::Rows q, k, q_out, k_out;
   kv8::Span sp;
   const float* q_gain;  // may be null: ones
   const float* k_gain;
-  int n_heads, heads;   // query heads, query and KV heads
-  int d, rotary, lanes, tt, tiles;  // lanes of a row, tokens of a CTA, CTAs of a sequence
-  float eps;
+  int n_heads, heads;      // query heads, query and KV heads
+  int d, rotary, lanes;    // lanes: of a row
+  int per, blocks;         // heads of a CTA, CTAs of a token
+  int slots, chunk, chunks;  // tokens of a CTA at a time and in all; CTAs of a sequence's tokens
+  float eps, inv_d;
   unsigned long long freq[MAX_D / 2];  // as in kv8::Rope
 };
 
-// A row's factor 1 / sqrt(mean + eps) where the sum of squares leaves fp32's good range (values beyond 2^49 or below
-// 2^-49 at most): in fp64, which holds every square of an fp32. Rows like that are rare; others pay one comparison.
-__device__ __noinline__ double wide_factor(const float (&x)[16], bool here, int lanes, int d, float eps) {
-  double s = 0.0;
-  if (here)
-    for (int e = 0; e < 16; ++e) s += (double)x[e] * (double)x[e];
-  for (int o = lanes >> 1; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-  return 1.0 / sqrt(s / d + (double)eps);
+// Eight values to 16-byte aligned memory, two to a conversion.
+__device__ __forceinline__ void store(float* p, const float2* x) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+}
+__device__ __forceinline__ void store(__half* p, const float2* x) {
+  __half2 h[4] = {__float22half2_rn(x[0]), __float22half2_rn(x[1]), __float22half2_rn(x[2]), __float22half2_rn(x[3])};
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+}
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float2* x) {
+  __nv_bfloat162 h[4] = {__float22bfloat162_rn(x[0]), __float22bfloat162_rn(x[1]), __float22bfloat162_rn(x[2]),
+                         __float22bfloat162_rn(x[3])};
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
 }
 
 template <typename TI, typename TO>
-__global__ void __launch_bounds__(NT) head_norm_kernel(const __grid_constant__ Params p) {
-  __shared__ float2 angle[MAX_TT * MAX_D / 2];
-  __shared__ __align__(16) float gain[2][MAX_D];
-  const int seq = (int)(blockIdx.x / p.tiles), t0 = (int)(blockIdx.x % p.tiles) * p.tt;
+__global__ void __launch_bounds__(MAX_NT, 2) head_norm_kernel(const __grid_constant__ Params p) {
+  constexpr int WORDS = sizeof(TI) / 2;  // 16-byte words of eight elements
+  // of each token: the first four cosines of every lane, the other four, and so the sines: a warp's reads of 16 bytes a
+  // lane then cover every bank once
+  __shared__ __align__(16) float4 angle[ANGLES / 2];
+  __shared__ unsigned long long freq[MAX_D / 2];
+  const int block = blockIdx.x % p.blocks, rest = blockIdx.x / p.blocks;
+  const int seq = rest / p.chunks, t0 = (rest - seq * p.chunks) * p.chunk;
   const int pos = p.sp.pos[seq], count = p.sp.counts ? p.sp.counts[seq] : p.sp.n_tokens;
   if (pos < 0 || count < 0 || count > p.sp.n_tokens || (long long)pos + count > 0x7FFFFFFFLL) {
     if (threadIdx.x == 0 && p.sp.status) atomicOr(p.sp.status, kv8::STATUS_BAD_POS);
     return;
   }
   if (t0 >= count) return;
-  const int lane = threadIdx.x & (p.lanes - 1), group = threadIdx.x / p.lanes, groups = NT / p.lanes / p.tt;
-  const int tok = t0 + group / groups, first = group % groups;
-  const bool here = lane * 16 < p.d, live = tok < count;
+  const int t1 = min(t0 + p.chunk, count), across = p.per * p.lanes;
+  const int slot = threadIdx.x / across, head = block * p.per + (threadIdx.x - slot * across) / p.lanes;
+  const int lane = threadIdx.x & (p.lanes - 1);
+  const bool live = lane * 16 < p.d && head < p.heads, is_k = head >= p.n_heads;
   // elements c and c2 of the lane, eight each: rotary partners, or, past the rotated ones, 16 in a row
   const bool turned = lane * 16 < p.rotary;
   const int c = turned ? lane * 8 : lane * 16, c2 = turned ? p.rotary / 2 + lane * 8 : lane * 16 + 8;
+  const kv8::Rows &ri = is_k ? p.k : p.q, &ro = is_k ? p.k_out : p.q_out;
+  const long long at = is_k ? head - p.n_heads : head;
+  const TI* src = static_cast<const TI*>(ri.data) + seq * ri.ss + (t0 + slot) * ri.ts + at * ri.hs + c;
+  TO* dst = static_cast<TO*>(ro.data) + seq * ro.ss + (t0 + slot) * ro.ts + at * ro.hs + c;
+  const long long src_step = ri.ts * p.slots, dst_step = ro.ts * p.slots;
 
-  float x[ROWS][16];
-  auto load = [&](int i, int head) {
-    if (live && here && head < p.heads) {
-      const bool is_k = head >= p.n_heads;
-      const kv8::Rows& r = is_k ? p.k : p.q;
-      const TI* src = static_cast<const TI*>(r.data) + seq * r.ss + tok * r.ts + (is_k ? head - p.n_heads : head) * r.hs;
-      kv8::load8(src + c, reinterpret_cast<float(&)[8]>(x[i][0]));
-      kv8::load8(src + c2, reinterpret_cast<float(&)[8]>(x[i][8]));
-    } else {
+  uint4 raw[IN_FLIGHT][2 * WORDS];  // rows on their way, as they lie in memory
+  int ahead = t0 + slot;            // token of the next one
+  auto load = [&](uint4 (&to)[2 * WORDS]) {
+    if (live && ahead < t1) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[i][e] = 0.f;
+      for (int w = 0; w < WORDS; ++w) {
+        to[w] = reinterpret_cast<const uint4*>(src)[w];
+        to[WORDS + w] = reinterpret_cast<const uint4*>(src + (c2 - c))[w];
+      }
+      src += src_step;
     }
+    ahead += p.slots;
   };
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) load(i, first + i * groups);
-
-  const int half = p.rotary / 2;
-  for (int i = threadIdx.x; i < p.tt * half; i += NT) {
+  for (int i = 0; i < IN_FLIGHT; ++i) {
+#pragma unroll
+    for (int w = 0; w < 2 * WORDS; ++w) raw[i][w] = make_uint4(0u, 0u, 0u, 0u);
+    load(raw[i]);
+  }
+  float2 gain[8];
+  const float* g = is_k ? p.k_gain : p.q_gain;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    gain[e] = live && g ? make_float2(g[(e < 4 ? c : c2 - 8) + 2 * e], g[(e < 4 ? c : c2 - 8) + 2 * e + 1]) : make_float2(1.f, 1.f);
+  const int half = p.rotary / 2, turning = half / 8;  // turning: lanes that rotate
+  for (int i = threadIdx.x; i < half; i += blockDim.x) freq[i] = p.freq[i];  // (threads index it apart)
+  __syncthreads();
+  for (int i = threadIdx.x; i < (t1 - t0) * half; i += blockDim.x) {
     const int t = i / half, f = i - t * half;
     float cs, sn;
-    const unsigned long long ph = p.freq[f] * (unsigned long long)(unsigned)(pos + t0 + t);
-    sincospif((float)(int)(unsigned)(ph >> 32) * 4.656612873077393e-10f, &sn, &cs);
-    angle[i] = make_float2(cs, sn);
-  }
-  for (int i = threadIdx.x; i < p.d; i += NT) {
-    gain[0][i] = p.q_gain ? p.q_gain[i] : 1.f;
-    gain[1][i] = p.k_gain ? p.k_gain[i] : 1.f;
+    sincospif((float)(int)(unsigned)((freq[f] * (unsigned long long)(unsigned)(pos + t0 + t)) >> 32) * 4.656612873077393e-10f, &sn, &cs);
+    float* to = reinterpret_cast<float*>(angle + t * (half / 2) + (f / 4 & 1) * turning + f / 8) + (f & 3);
+    to[0] = cs;
+    to[8 * turning] = sn;
   }
   __syncthreads();
-  float2 a[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) a[e] = turned ? angle[(tok - t0) * half + c + e] : make_float2(1.f, 0.f);
 
-  for (int h0 = first;; h0 += ROWS * groups) {
+  for (int t = t0 + slot; __any_sync(~0u, t < t1);) {
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const int head = h0 + i * groups;
-      float s = 0.f;
+    for (int i = 0; i < IN_FLIGHT; ++i, t += p.slots) {
+      float2 x[8];
+      kv8::load8(reinterpret_cast<const TI*>(&raw[i][0]), reinterpret_cast<float(&)[8]>(x[0]));
+      kv8::load8(reinterpret_cast<const TI*>(&raw[i][WORDS]), reinterpret_cast<float(&)[8]>(x[4]));
+      load(raw[i]);
+      const bool here = live && t < t1;
+      float2 s2 = __fmul2_rn(x[0], x[0]);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s = fmaf(x[i][e], x[i][e], s);
+      for (int e = 1; e < 8; ++e) s2 = fma2(x[e], x[e], s2);
+      float s = live ? s2.x + s2.y : 0.f;
       for (int o = p.lanes >> 1; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-      const float mean = s / (float)p.d + p.eps;
-      float r = __frsqrt_rn(mean);
+      const float mean = fmaf(s, p.inv_d, p.eps);
+      float r = rsqrtf(mean);
+      r = fmaf(0.5f * r, fmaf(-mean * r, r, 1.f), r);  // (Newton's step: off by less than 2^-23.9 then)
+      // a sum of squares that leaves fp32's good range (values beyond 2^49 or below 2^-49 at most) is taken again in
+      // fp64, which holds every square of an fp32; rows like that are rare, the others pay a comparison
       const bool odd = !(mean > 1e-30f && s < 1e30f);
-      if (__any_sync(~0u, odd)) {  // (a whole warp, as the sums of its rows cross lanes)
-        const double w = wide_factor(x[i], here, p.lanes, p.d, p.eps);
+      if (__any_sync(~0u, odd && here)) {  // (a whole warp, as the sums of its rows cross lanes)
+        double w = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w += (double)x[e].x * (double)x[e].x + (double)x[e].y * (double)x[e].y;
+        if (!live) w = 0.0;
+        for (int o = p.lanes >> 1; o; o >>= 1) w += __shfl_xor_sync(~0u, w, o);
+        w = 1.0 / sqrt(w / p.d + (double)p.eps);
         if (odd) {
           r = 1.f;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[i][e] = (float)((double)x[i][e] * w);
+          for (int e = 0; e < 8; ++e) x[e] = make_float2((float)((double)x[e].x * w), (float)((double)x[e].y * w));
         }
       }
-      if (!live || !here || head >= p.heads) continue;
-      const bool is_k = head >= p.n_heads;
-      const float* g = gain[is_k];
-      float y[16];
+      if (here) {
+        const float2 r2 = make_float2(r, r);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = x[i][e] * r * g[(e < 8 ? c : c2 - 8) + e];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = y[e], v = y[8 + e];
+        for (int e = 0; e < 8; ++e) x[e] = __fmul2_rn(__fmul2_rn(x[e], r2), gain[e]);
         if (turned) {
-          y[e] = u * a[e].x - v * a[e].y;
-          y[8 + e] = v * a[e].x + u * a[e].y;
-        }
-      }
-      const kv8::Rows& o = is_k ? p.k_out : p.q_out;
-      TO* dst = static_cast<TO*>(o.data) + seq * o.ss + tok * o.ts + (is_k ? head - p.n_heads : head) * o.hs;
-      kv8::store8(dst + c, y);
-      kv8::store8(dst + c2, y + 8);
-    }
-    if (h0 + ROWS * groups - first >= p.heads) break;  // (alike for the whole CTA: groups share the shuffles' warps)
+          const float4* a = angle + (t - t0) * (half / 2) + lane;
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) load(i, h0 + (ROWS + i) * groups);
+          for (int h = 0; h < 2; ++h) {
+            const float4 cs = a[h * turning], sn = a[(2 + h) * turning];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 ce = e ? make_float2(cs.z, cs.w) : make_float2(cs.x, cs.y);
+              const float2 se = e ? make_float2(sn.z, sn.w) : make_float2(sn.x, sn.y);
+              const float2 u = x[2 * h + e], v = x[4 + 2 * h + e], vs = __fmul2_rn(v, se);
+              x[2 * h + e] = fma2(u, ce, make_float2(-vs.x, -vs.y));
+              x[4 + 2 * h + e] = fma2(u, se, __fmul2_rn(v, ce));
+            }
+          }
+        }
+        store(dst, x);
+        store(dst + (c2 - c), x + 4);
+        dst += dst_step;
+      }
+    }
   }
 }
 
-cudaError_t launch(const Params& p, int in, int out, unsigned grid, cudaStream_t st) {
+cudaError_t launch(const Params& p, int in, int out, unsigned grid, unsigned nt, cudaStream_t st) {
   using H = __half;
   using B = __nv_bfloat16;
-  if (in == TINFER_DTYPE_F32 && out == TINFER_DTYPE_F32) head_norm_kernel<float, float><<<grid, NT, 0, st>>>(p);
-  else if (in == TINFER_DTYPE_F32 && out == TINFER_DTYPE_F16) head_norm_kernel<float, H><<<grid, NT, 0, st>>>(p);
-  else if (in == TINFER_DTYPE_F32) head_norm_kernel<float, B><<<grid, NT, 0, st>>>(p);
-  else if (in == TINFER_DTYPE_F16) head_norm_kernel<H, H><<<grid, NT, 0, st>>>(p);
-  else head_norm_kernel<B, B><<<grid, NT, 0, st>>>(p);
+  if (in == TINFER_DTYPE_F32 && out == TINFER_DTYPE_F32) head_norm_kernel<float, float><<<grid, nt, 0, st>>>(p);
+  else if (in == TINFER_DTYPE_F32 && out == TINFER_DTYPE_F16) head_norm_kernel<float, H><<<grid, nt, 0, st>>>(p);
+  else if (in == TINFER_DTYPE_F32) head_norm_kernel<float, B><<<grid, nt, 0, st>>>(p);
+  else if (in == TINFER_DTYPE_F16) head_norm_kernel<H, H><<<grid, nt, 0, st>>>(p);
+  else head_norm_kernel<B, B><<<grid, nt, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -162,7 +204,7 @@ extern "C" tinfer_status tinfer_op_qk_norm_rope(int n_seqs, int n_tokens, int n_
   if (rope_theta != 0.0 && (!(rope_theta >= 1.0) || !(rope_theta <= 1e30))) return TINFER_ERR_INVALID_ARG;
   if (rotary_dim < 0 || rotary_dim > head_dim || (rotary_dim & 1)) return TINFER_ERR_INVALID_ARG;
   if (head_dim % 16 || head_dim > head_norm::MAX_D || rotary_dim % 16) return TINFER_ERR_UNSUPPORTED;
-  if (n_heads > 1024 || n_kv_heads > 1024 || n_seqs > (1 << 24) || n_tokens > (1 << 24)) return TINFER_ERR_UNSUPPORTED;
+  if (n_heads > 1024 || n_kv_heads > 1024 || (long long)n_seqs * n_tokens > (1 << 24)) return TINFER_ERR_UNSUPPORTED;
   const kv8::Extent xq{n_seqs, n_tokens, n_heads, head_dim}, xk{n_seqs, n_tokens, n_kv_heads, head_dim};
   head_norm::Params p{};
   if (!kv8::rows_of(q, xq, false, p.q) || !kv8::rows_of(k, xk, false, p.k) || !kv8::rows_of(q_out, xq, true, p.q_out) ||
@@ -178,21 +220,27 @@ extern "C" tinfer_status tinfer_op_qk_norm_rope(int n_seqs, int n_tokens, int n_
   p.d = head_dim;
   p.rotary = rope_theta == 0.0 ? 0 : rotary_dim;
   p.eps = (float)eps;
+  p.inv_d = 1.f / (float)head_dim;
   for (p.lanes = 1; p.lanes * 16 < head_dim;) p.lanes *= 2;
   for (int i = 0; i < p.rotary / 2; ++i)  // turns of 2^-64; see kv8::Rope
     p.freq[i] = (unsigned long long)(std::pow(rope_theta, -2.0 * i / p.rotary) * 0.15915494309189533577 * 18446744073709551616.0);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return TINFER_ERR_CUDA;
-  // a token to a CTA while the tokens are too few to fill the GPU so; else as many as leave each group of lanes three
-  // heads, whose loads follow one another and share the angles
-  const long long tokens = (long long)n_seqs * n_tokens;
-  p.tt = 1;
-  while (tokens > 4LL * sms * p.tt && p.tt < head_norm::MAX_TT && p.tt * 2 <= n_tokens && 3 * (head_norm::NT / p.lanes / p.tt) > p.heads) p.tt *= 2;
-  p.tiles = (n_tokens + p.tt - 1) / p.tt;
-  if ((long long)p.tiles * n_seqs > 0x7FFFFFFFLL) return TINFER_ERR_UNSUPPORTED;
+  // a CTA has whole warps of heads, as many of a token's as it has threads for, and several tokens at a time where
+  // heads are few; it walks over as many tokens as leave four CTAs for each SM, up to 8 turns and the angles' room
+  const int rows = 32 / p.lanes, most = head_norm::MAX_NT / p.lanes;
+  p.blocks = (p.heads + most - 1) / most;
+  p.per = ((p.heads + p.blocks - 1) / p.blocks + rows - 1) / rows * rows;
+  p.slots = std::min(most / p.per, n_tokens);
+  const int half = std::max(p.rotary / 2, 1), room = std::min(8, head_norm::ANGLES / half / p.slots);
+  const long long per_turn = (long long)n_seqs * ((n_tokens + p.slots - 1) / p.slots) * p.blocks;
+  p.chunk = p.slots * (int)std::max<long long>(1, std::min<long long>(room, per_turn / (4 * sms)));
+  p.chunks = (n_tokens + p.chunk - 1) / p.chunk;
+  const long long grid = (long long)n_seqs * p.chunks * p.blocks;
+  if (grid > 0x7FFFFFFFLL) return TINFER_ERR_UNSUPPORTED;
   cudaStream_t st = (cudaStream_t)stream;
   if (status_dev && cudaMemsetAsync(status_dev, 0, 4, st) != cudaSuccess) return TINFER_ERR_CUDA;
-  const cudaError_t e = head_norm::launch(p, q->dtype, q_out->dtype, (unsigned)(p.tiles * n_seqs), st);
+  const cudaError_t e = head_norm::launch(p, q->dtype, q_out->dtype, (unsigned)grid, (unsigned)(p.slots * p.per * p.lanes), st);
   return e == cudaSuccess ? TINFER_OK : TINFER_ERR_CUDA;
 }

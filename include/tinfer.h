@@ -486,7 +486,7 @@ tinfer_status tinfer_op_logprobs(int rows, int vocab, int dtype, const void* log
  * Computed in fp32 and rounded once: off by a few 2^-24 of a pair's size. A row whose squares leave fp32's range is
  * computed in fp64. A row with a NaN or an infinity gives what the formula gives (a NaN there, with an infinity 0 elsewhere),
  * and a row of zeros with eps 0 gives NaN. eps >= 0. Asynchronous on `stream`, no workspace.
- * head_dim and rotary_dim multiples of 16, head_dim at most 256, heads at most 1024, n_seqs and n_tokens at most 2^24, else
+ * head_dim and rotary_dim multiples of 16, head_dim at most 256, heads at most 1024, n_seqs * n_tokens at most 2^24, else
  * TINFER_ERR_UNSUPPORTED. */
 tinfer_status tinfer_op_qk_norm_rope(int n_seqs, int n_tokens, int n_heads, int n_kv_heads, int head_dim,
                                      int rotary_dim, const tinfer_rows* q, const tinfer_rows* k,
