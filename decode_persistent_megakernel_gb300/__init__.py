@@ -27,6 +27,7 @@ TINFER_SYNC_STAMPS, TINFER_SYNC_GRID_BARRIER = 0, 1
 TINFER_NOALLOC_SCRATCH_BYTES = 1 << 20
 TINFER_KV8_E4M3, TINFER_KV8_INT8 = 0, 1
 TINFER_KV8_KEEP_STATUS, TINFER_KV8_DEBUG_WITHHOLD = 0x100, 0x200
+TINFER_MOE_RENORMALISE, TINFER_MOE_KEEP_STATUS, TINFER_MOE_DEBUG_WITHHOLD = 1, 0x100, 0x200
 TINFER_DTYPE_F32, TINFER_DTYPE_F16, TINFER_DTYPE_BF16 = range(3)
 TRACE_FIELDS = 10  # stamps per CTA and phase of the timeline (tinfer_set_trace)
 
@@ -39,6 +40,7 @@ EXPORTS = [
     "tinfer_op_attention_noalloc", "tinfer_op_gemv_batch", "tinfer_moe_packed_bytes", "tinfer_pack_moe", "tinfer_op_moe",
     "tinfer_op_gemm_bf16", "tinfer_op_kv8_append", "tinfer_op_kv8_read", "tinfer_kv8_attention_workspace",
     "tinfer_op_kv8_attention", "tinfer_op_logprobs", "tinfer_op_qk_norm_rope",
+    "tinfer_moe_layer_workspace", "tinfer_op_moe_layer",
 ]
 
 
@@ -77,6 +79,12 @@ class tinfer_rows(ctypes.Structure):
         (n, ctypes.c_longlong) for n in ("seq_stride", "token_stride", "head_stride")]
 
 
+class tinfer_moe(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "weight_format", "group_size", "scale_dtype", "n_experts", "top_k", "hidden", "ffn_e", "router_dtype", "flags")] + [
+        (n, ctypes.c_void_p) for n in ("router", "gu_packed", "down_packed")]
+
+
 _lib = None
 
 
@@ -89,6 +97,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I, D, Z, LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_double, ctypes.c_size_t, ctypes.c_longlong
         cfgp = ctypes.POINTER(tinfer_config)
+        moep = ctypes.POINTER(tinfer_moe)
         kvp, rowp = ctypes.POINTER(tinfer_kv8), ctypes.POINTER(tinfer_rows)
         sig = {
             "tinfer_status_string": ([I], ctypes.c_char_p),
@@ -124,6 +133,8 @@ def lib():
             "tinfer_kv8_attention_workspace": ([kvp, I, I], Z),
             "tinfer_op_kv8_attention": ([kvp, I, I, rowp, P, P, D, rowp, P, P, Z, P, P], I),
             "tinfer_op_qk_norm_rope": ([I, I, I, I, I, I, rowp, rowp, P, P, D, D, P, P, rowp, rowp, P, P], I),
+            "tinfer_moe_layer_workspace": ([moep, I], Z),
+            "tinfer_op_moe_layer": ([moep, I, I, P, LL, P, LL, I, P, P, P, Z, P, P], I),
             "tinfer_op_logprobs": ([I, I, I, P, LL, P, I, P, P, P, P, P], I),
         }
         for name, (args, res) in sig.items():
@@ -332,6 +343,16 @@ def tinfer_op_qk_norm_rope(n_seqs, n_tokens, n_heads, n_kv_heads, head_dim, rota
     return lib().tinfer_op_qk_norm_rope(n_seqs, n_tokens, n_heads, n_kv_heads, head_dim, rotary_dim, q, k, _ptr(q_gain),
                                         _ptr(k_gain), eps, rope_theta, _ptr(pos), _ptr(counts), q_out, k_out, _ptr(status),
                                         _stream(stream))
+
+
+def tinfer_moe_layer_workspace(layer: tinfer_moe, n_tokens) -> int:
+    return lib().tinfer_moe_layer_workspace(layer, n_tokens)
+
+
+def tinfer_op_moe_layer(layer: tinfer_moe, n_tokens, dtype, x, x_stride, y, y_stride, accumulate, ids, weights, workspace,
+                        workspace_bytes, status=None, stream=None) -> int:
+    return lib().tinfer_op_moe_layer(layer, n_tokens, dtype, _ptr(x), x_stride, _ptr(y), y_stride, int(accumulate), _ptr(ids),
+                                     _ptr(weights), _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream))
 
 
 def make_config(c: dict, exec_mode: int = TINFER_MEGAKERNEL) -> tinfer_config:
@@ -730,3 +751,124 @@ def qk_norm_rope(q, k, q_gain=None, k_gain=None, pos=None, counts=None, eps: flo
     if n_seqs and n_tokens:  # (else nothing to launch)
         _call("tinfer_op_qk_norm_rope", lib().tinfer_op_qk_norm_rope, args, device, stream)
     return out
+
+
+class MoeLayer:
+    """A mixture-of-experts layer of up to max_tokens tokens a call (tinfer_op_moe_layer): router, choice of the experts, their
+    SwiGLU products and weighted sum. router: bfloat16 or float32 [n_experts, hidden]; wg, wu [n_experts, ffn, hidden] and
+    wd [n_experts, hidden, ffn]: bfloat16, or uint8 of half the last size with 4-bit weights (element 2j in the low half of byte j) and
+    scales (sg, su, sd), float16 or bfloat16 [n_experts, rows, inputs / group]. The layer keeps the router and a packed copy of the
+    experts, which may be dropped then.
+
+    It also keeps a workspace: a uint8 tensor `workspace` that layers called one after another may share (at least workspace_bytes()
+    of the largest, its first 256 bytes 0), or a new one. A call that may overlap another one in time (another stream, a
+    graph replayed beside it) passes one of its own. Keep the layer until its work has ended, and as long as graphs replay it.
+
+    Calls report into `status`, an int32 tensor that each call clears, or, without one, into a word of the layer that error()
+    reads: bit 1, a wait on the device ran out, and the results are not valid."""
+
+    def __init__(self, router, wg, wu, wd, top_k: int, scales=None, group: int = 0, renormalise: bool = True,
+                 max_tokens: int = 64, workspace=None):
+        import torch
+        self.device = device = router.device
+        if device.type != "cuda":
+            raise ValueError("the layer lives on a CUDA device")
+        if router.dim() != 2 or wg.dim() != 3:
+            raise ValueError("router [n_experts, hidden] and wg, wu, wd [n_experts, rows, inputs] are wanted")
+        n_experts, hidden = router.shape
+        ffn = wg.shape[1]
+        int4 = wg.dtype == torch.uint8
+        if int4 and group < 1:
+            raise ValueError("group: the inputs of a scale are wanted")
+        half = 2 if int4 else 1
+        sizes = {"wg": (n_experts, ffn, hidden), "wu": (n_experts, ffn, hidden), "wd": (n_experts, hidden, ffn)}
+        given = {"router": router, "wg": wg, "wu": wu, "wd": wd}
+        for (what, shape), t in zip(sizes.items(), (wg, wu, wd)):
+            _on(what, t, device, torch.uint8 if int4 else torch.bfloat16, (*shape[:2], shape[2] // half))
+        if int4:
+            if scales is None or scales[0].dtype not in (torch.float16, torch.bfloat16):
+                raise ValueError("scales: (sg, su, sd), float16 or bfloat16, are wanted")
+            for what, shape, t in zip(("sg", "su", "sd"), sizes.values(), scales):
+                _on(what, t, device, scales[0].dtype, (*shape[:2], shape[2] // group))
+                given[what] = t
+        for what, t in given.items():
+            if not t.is_contiguous():
+                raise ValueError(f"{what} is not contiguous")
+        sg, su, sd = scales if int4 else (None,) * 3
+        router_dtype = _dtype(router)
+        fmt = TINFER_INT4 if int4 else TINFER_BF16
+        scale_dtype = TINFER_SCALE_BF16 if int4 and sg.dtype == torch.bfloat16 else TINFER_SCALE_FP16
+        flags = TINFER_MOE_RENORMALISE if renormalise else 0
+        shape = (fmt, group if int4 else 0, scale_dtype, n_experts, top_k, hidden, ffn, router_dtype)
+        need = lib().tinfer_moe_layer_workspace(tinfer_moe(*shape, flags, *[16] * 3), max_tokens)  # (addresses that are not looked at)
+        if need == 0:
+            raise TinferError(TINFER_ERR_UNSUPPORTED, "MoeLayer")
+        self.n_experts, self.top_k, self.hidden, self.ffn, self.max_tokens = n_experts, top_k, hidden, ffn, max_tokens
+        with torch.cuda.device(device):
+            self.router = router.clone()
+            self.gate_up, self.down = (torch.empty(tinfer_moe_packed_bytes(fmt, group, n_experts, hidden, ffn, which),
+                                                   dtype=torch.uint8, device=device) for which in (0, 1))
+            _check(tinfer_pack_moe(fmt, group, scale_dtype, n_experts, hidden, ffn, wg, sg, wu, su, wd, sd, self.gate_up, self.down,
+                                   torch.cuda.current_stream(device)), "tinfer_pack_moe")
+            self._errors = torch.zeros(1, dtype=torch.int32, device=device)
+            if workspace is None:
+                workspace = torch.zeros(need, dtype=torch.uint8, device=device)
+            self._uint8 = torch.uint8
+            self._workspace = self._check_workspace(workspace)
+            addresses = [t.data_ptr() for t in (self.router, self.gate_up, self.down)]
+            self.c, self._kept = (tinfer_moe(*shape, flags | f, *addresses) for f in (0, TINFER_MOE_KEEP_STATUS))
+            # calls may come on any stream, and the given weights may go
+            torch.cuda.current_stream(device).synchronize()
+
+    def workspace_bytes(self, n_tokens: int | None = None) -> int:
+        return lib().tinfer_moe_layer_workspace(self.c, n_tokens or self.max_tokens)
+
+    def _check_workspace(self, t):
+        if t.dtype != self._uint8 or t.device != self.device or not t.is_contiguous():
+            raise ValueError("workspace: a contiguous uint8 tensor on the layer's device is wanted")
+        return t
+
+    def error(self) -> int:
+        """Status bits of all calls without a `status` of their own since the last error(). Waits for the device; after a wait
+        that ran out it also clears the layer's workspace for the next call."""
+        import torch
+        torch.cuda.synchronize(self.device)
+        bits = int(self._errors)
+        if bits:
+            self._errors.zero_()
+            self._workspace[:256].zero_()
+            torch.cuda.synchronize(self.device)
+        return bits
+
+    def __call__(self, x, out=None, accumulate: bool = False, ids=None, weights=None, workspace=None, status=None, stream=None):
+        """(y, ids, weights) of the rows x [n_tokens, hidden]: y in `out` (rows like x, x itself: in place; a new tensor when None;
+        added to what it holds with accumulate), the chosen experts int32 and their weights float32 [n_tokens, top_k]."""
+        import torch
+        if x.dim() != 2 or x.shape[1] != self.hidden or x.device != self.device or (self.hidden > 1 and x.stride(1) != 1):
+            raise ValueError(f"x: rows [n_tokens, {self.hidden}] with contiguous elements on {self.device} are wanted")
+        n = x.shape[0]
+        dtype = _dtype(x)
+        if accumulate and out is None:
+            raise ValueError("out is wanted to add to")
+        with _making(stream, self.device):
+            if out is None:
+                out = torch.empty((n, self.hidden), dtype=x.dtype, device=self.device)
+            if ids is None:
+                ids = torch.empty((n, self.top_k), dtype=torch.int32, device=self.device)
+            if weights is None:
+                weights = torch.empty((n, self.top_k), dtype=torch.float32, device=self.device)
+        _on("out", out, self.device, x.dtype, x.shape)
+        for what, t, dt in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
+            _on(what, t, self.device, dt, (n, self.top_k))
+            if not t.is_contiguous():
+                raise ValueError(f"{what} is not contiguous")
+        if out.stride(1) != 1:
+            raise ValueError("out: the elements of a row are not contiguous")
+        if n == 0:
+            return out, ids, weights  # nothing to launch
+        workspace = self._workspace if workspace is None else self._check_workspace(workspace)
+        c, word = (self._kept, self._errors.data_ptr()) if status is None else (self.c, _int32s("status", status, 1, self.device))
+        _call("tinfer_op_moe_layer", lib().tinfer_op_moe_layer,
+              (c, n, dtype, x.data_ptr(), x.stride(0), out.data_ptr(), out.stride(0), int(accumulate), ids.data_ptr(),
+               weights.data_ptr(), workspace.data_ptr(), workspace.numel(), word), self.device, stream)
+        return out, ids, weights

@@ -1,0 +1,870 @@
+// moe_layer.cu -- a whole mixture-of-experts layer for a few tokens, in one persistent cooperative kernel.
+//
+//   l = Wr x,  p = softmax(l),  e_1 .. e_k the largest p (equal ones by the lower id),  w_i = p_{e_i} (or p_{e_i} / sum_j p_{e_j})
+//   y = sum_i w_i Wd_{e_i} (silu(Wg_{e_i} x) * (Wu_{e_i} x))
+//
+// Bound by HBM: the weights of each chosen expert once, whatever the number of its tokens. Four phases between barriers
+// of the whole grid: the router's products, the gate and up products of the chosen experts, their down products, and each
+// token's sum over its experts in the order of its choice (so that results never depend on timing).
+//
+// Products. The tokens of an expert (16 at most at a time) are the columns and 16 or 32 weight rows the rows of the
+// warp-level tensor instruction (m16n8k16, bf16, fp32 accumulation): with so few columns its rate is not the limit, and the
+// weights go from shared memory to the product without being stored again. A bf16 weight is an operand as it is; a 4-bit one
+// becomes q - 8 exactly, and its group's scale multiplies the sum of 32 products. Activations in fp32 enter as three
+// bf16 parts of 8 bits each, which hold every bit down to 2^-133; fp16 ones as two, bf16 ones as they are. The SwiGLU outputs are kept in
+// fp32 and enter as three parts, or as two (2^-17) where the result is rounded to 16 bits anyway.
+//
+// A CTA takes a run of items, each G tiles of rows; a tile's inputs are split over 16 / G warps, whose sums meet in shared
+// memory. Each warp streams its own part of the weights through a ring of asynchronous copies that runs on across items,
+// experts and, into the down products, across the barrier: no warp waits for another's copies. The activations stay in
+// shared memory.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+#include <type_traits>
+
+#include "engine.h"
+#include "kv8.cuh"
+#include "ptx.cuh"
+#include "tinfer.h"
+
+namespace tinfer {
+namespace moe {
+
+constexpr int NT = 512, NW = NT / 32;
+constexpr int MAX_TOKENS = 64, MAX_K = 16, MAX_EXPERTS = 512, MAX_WIDTH = 16384;
+constexpr int STAGES = 5;        // units of a warp under way
+constexpr int COLS = 16;         // tokens of an expert at a time: two blocks of eight columns
+constexpr int SMEM = 227 * 1024;
+constexpr int STATUS_TIMEOUT = 2;
+constexpr int WAIT_US = 200 * 1000, WAIT_US_WITHHELD = 5 * 1000;
+
+template <int FMT>
+struct Shape {  // a unit: TM * 16 rows of UB bytes (UK inputs), and two words of scales for each row
+  static constexpr int TM = FMT == TINFER_INT4 ? 2 : 1;
+  static constexpr int RT = 16 * TM;
+  static constexpr int UB = FMT == TINFER_INT4 ? 32 : 64, UK = FMT == TINFER_INT4 ? 64 : 32;
+  static constexpr int SLOT = RT * UB + (FMT == TINFER_INT4 ? RT * 8 : 0);
+  static constexpr int RING = NW * STAGES * SLOT;
+  static constexpr int RP = RT + 4;  // column of a warp's sums, padded so that its lanes' stores meet no bank twice
+  static constexpr int RED = NW * COLS * RP * 4;
+};
+
+// A product's matrices: `rows` packed rows of rb bytes for each expert, K inputs.
+struct Matrix {
+  const uint8_t* w;
+  int rows, rb, k;
+  int g, items;  // tiles of an item, items of an expert
+  int cap;       // tokens at a time
+};
+
+struct Params {
+  Matrix up, down;
+  const void* router;
+  int router_f32;
+  const void* x;
+  void* y;
+  long long x_stride, y_stride;
+  int accumulate;
+  int tokens, experts, top_k, hidden, ffn, renormalise;
+  int group, scale_bf16;
+  int* ids;        // outputs, may be null
+  float* weights;
+  unsigned* sync;  // counters of the three barriers and of the CTAs that have left; 0 between calls
+  double* logits;  // [tokens][experts]
+  float* h;        // [tokens * top_k][ffn]
+  float* part;     // [tokens * top_k][hidden]
+  int* status;
+  int resident;    // all tokens stay in shared memory for the gate and up products
+  int b_bytes;     // shared memory of the activations
+  int wait_us, withhold;
+};
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---- barriers of the grid -------------------------------------------------------------------------
+// One counter for each; arrival and wait apart, so that work that needs no other CTA stands between them.
+__device__ __forceinline__ void grid_arrive(const Params& p, int which) {
+  __syncthreads();
+  if (threadIdx.x == 0 && !(p.withhold && which == 0 && blockIdx.x == 0)) red_add_release(p.sync + which, 1u);
+}
+__device__ __forceinline__ bool grid_wait(const Params& p, int which, int* failed) {
+  if (threadIdx.x == 0) {
+    const uint64_t t0 = globaltimer();
+    while (ld_acquire(p.sync + which) < gridDim.x)
+      if ((long long)(globaltimer() - t0) > p.wait_us * 1000LL && ld_acquire(p.sync + which) < gridDim.x) {
+        if (p.status) atomicOr(p.status, STATUS_TIMEOUT);
+        *failed = 1;
+        break;
+      }
+  }
+  __syncthreads();
+  return !*failed;
+}
+
+// ---- the router -----------------------------------------------------------------------------------
+// Sum and its error: 48 bits, so that experts are told apart as in fp64 (which the device has at a hundredth of the rate).
+struct Pair {
+  float s, c;
+  __device__ __forceinline__ void add(float a, float b) {  // + a * b: the product's error by a fused multiply, the sum's by Knuth's
+    const float p = a * b, e = fmaf(a, b, -p);
+    const float t = __fadd_rn(s, p), z = __fsub_rn(t, s);
+    c = __fadd_rn(c, __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z))));
+    s = t;
+  }
+};
+
+template <typename XT, typename WT, int N>
+__device__ void route(const Params& p, int expert, int m0) {
+  const int lane = threadIdx.x & 31;
+  const WT* w = static_cast<const WT*>(p.router) + (size_t)expert * p.hidden;
+  const XT* x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = static_cast<const XT*>(p.x) + min(m0 + i, p.tokens - 1) * p.x_stride;
+  Pair acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = Pair{0.f, 0.f};
+#pragma unroll 2
+  for (int c = lane * 8; c < p.hidden; c += 256) {
+    float a[8], b[N][8];
+    kv8::load8(w + c, a);
+#pragma unroll
+    for (int i = 0; i < N; ++i) kv8::load8(x[i] + c, b[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i].add(a[e], b[i][e]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    double d = (double)acc[i].s + (double)acc[i].c;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
+    if (lane == 0 && m0 + i < p.tokens) p.logits[(size_t)(m0 + i) * p.experts + expert] = d;
+  }
+}
+template <typename XT, int N>
+__device__ __forceinline__ void route_any(const Params& p, int expert, int m0) {
+  if (p.router_f32) route<XT, float, N>(p, expert, m0);
+  else route<XT, __nv_bfloat16, N>(p, expert, m0);
+}
+
+// Logits as keys in the order of their values; 1: NaN, 0: already chosen.
+__device__ __forceinline__ unsigned long long key_of(double x) {
+  if (x != x) return 1ull;
+  const unsigned long long b = (unsigned long long)__double_as_longlong(x + 0.0);
+  return b >> 63 ? ~b : b | (1ull << 63);
+}
+__device__ __forceinline__ double value_of(unsigned long long k) {
+  return __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k));
+}
+
+// ---- shared memory --------------------------------------------------------------------------------
+struct Lists {
+  float* weight;       // of an entry (token * top_k + place)
+  uint16_t* expert;    // of an entry
+  uint16_t* sorted;    // entries by expert, then token
+  uint32_t *up, *down;  // groups of an expert's entries: expert | first << 10 | n << 21
+  int padded;           // entries, to whole words of eight; no expert's past their end
+  __host__ __device__ static int bytes(int entries) { return (entries + 7) / 8 * 128; }
+  __device__ Lists(unsigned char* at, int n) : padded((n + 7) / 8 * 8) {
+    weight = reinterpret_cast<float*>(at);
+    up = reinterpret_cast<uint32_t*>(at + 4 * padded);
+    down = reinterpret_cast<uint32_t*>(at + 8 * padded);
+    expert = reinterpret_cast<uint16_t*>(at + 12 * padded);
+    sorted = expert + padded;
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(int e, F&& f) const {  // f(entry) for the entries of an expert in order
+    for (int i = 0; i < padded; i += 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(expert + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if ((int)(w[j] & 0xFFFFu) == e) f(i + 2 * j);
+        if ((int)(w[j] >> 16) == e) f(i + 2 * j + 1);
+      }
+    }
+  }
+};
+
+// The chosen experts and weights of all tokens, by every CTA for itself: eight lanes to a token.
+template <int FMT>
+__device__ void choose(const Params& p, unsigned long long* keys, const Lists& l) {
+  for (int i = p.tokens * p.top_k + threadIdx.x; i < l.padded; i += NT) l.expert[i] = 0xFFFF;
+  const int per_round = min(NT / 8, Shape<FMT>::RING / 8 / p.experts), sub = threadIdx.x & 7;
+  for (int m0 = 0; m0 < p.tokens; m0 += per_round) {
+    const int n = min(per_round, p.tokens - m0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n * p.experts; i += NT) keys[i] = key_of(__ldcg(p.logits + (size_t)m0 * p.experts + i));
+    __syncthreads();
+    const int t = threadIdx.x >> 3;
+    unsigned long long* mine = keys + (size_t)min(t, n - 1) * p.experts;
+    const int at = (m0 + t) * p.top_k;
+    double top = 0.0;
+    float sum = 0.f;
+    bool nan = false;
+    for (int s = 0; s < p.top_k; ++s) {
+      unsigned long long best = 0;
+      int id = 0x7FFFFFFF;
+      for (int e = sub; e < p.experts; e += 8) {
+        const unsigned long long k = mine[e];
+        nan |= k == 1;
+        if (k > best) {
+          best = k;
+          id = e;
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 8; o *= 2) {
+        const unsigned long long k = __shfl_xor_sync(~0u, best, o);
+        const int other = __shfl_xor_sync(~0u, id, o);
+        if (k > best || (k == best && other < id)) {
+          best = k;
+          id = other;
+        }
+      }
+      if (s == 0) {
+        top = value_of(best);
+        if (!p.renormalise)
+          for (int e = sub; e < p.experts; e += 8) sum += expf((float)(value_of(mine[e]) - top));
+      }
+      const float x = expf((float)(value_of(best) - top));
+      if (p.renormalise) sum += x;
+      __syncwarp();  // (every lane has read the keys)
+      if (t < n && sub == 0) {
+        mine[id] = 0;
+        l.weight[at + s] = x;
+        l.expert[at + s] = (uint16_t)id;
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2) {
+      if (!p.renormalise) sum += __shfl_xor_sync(~0u, sum, o);
+      nan |= __shfl_xor_sync(~0u, nan, o);
+    }
+    if (t < n)
+      for (int s = sub; s < p.top_k; s += 8) l.weight[at + s] = nan ? __uint_as_float(0x7FC00000u) : l.weight[at + s] / sum;
+  }
+  __syncthreads();
+}
+
+// Entries by expert, and the groups of at most `cap` of them; counts of the groups in total[0], total[1].
+__device__ void sort_entries(const Params& p, const Lists& l, int* total, unsigned long long* scan) {
+  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+  int count = 0;
+  if (e < p.experts)
+    l.each(e, [&](int) { ++count; });
+  const int groups_up = (count + p.up.cap - 1) / p.up.cap, groups_down = (count + p.down.cap - 1) / p.down.cap;
+  const unsigned long long mine = (unsigned long long)count | (unsigned long long)groups_up << 20 | (unsigned long long)groups_down << 40;
+  unsigned long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const unsigned long long y = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  unsigned long long before = 0, all = 0;
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += scan[w];
+    all += scan[w];
+  }
+  before += incl - mine;
+  const int first = (int)(before & 0xFFFFF);
+  int at = first;
+  if (count) l.each(e, [&](int i) { l.sorted[at++] = (uint16_t)i; });
+  for (int g = 0; g < groups_up; ++g)
+    l.up[(int)(before >> 20 & 0xFFFFF) + g] = (uint32_t)e | (uint32_t)(first + g * p.up.cap) << 10 | (uint32_t)min(p.up.cap, count - g * p.up.cap) << 21;
+  for (int g = 0; g < groups_down; ++g)
+    l.down[(int)(before >> 40) + g] = (uint32_t)e | (uint32_t)(first + g * p.down.cap) << 10 | (uint32_t)min(p.down.cap, count - g * p.down.cap) << 21;
+  if (e == 0) {
+    total[0] = (int)(all >> 20 & 0xFFFFF);
+    total[1] = (int)(all >> 40);
+  }
+  __syncthreads();
+}
+
+// ---- the stream of weights ------------------------------------------------------------------------
+// A warp's units in order: those of its tile and inputs in each item of the CTA's run.
+template <int FMT>
+struct Stream {
+  using S = Shape<FMT>;
+  int item, end, unit, lo, hi, tile;  // next to issue; units of the warp in an item; its tile within an item
+  const uint8_t* src;                 // first row of the tile, null: past the matrix
+  int put;                            // slot of the next one
+  __device__ void start(const Matrix& m, const uint32_t* groups, int n_groups) {
+    const int warp = threadIdx.x >> 5, kw = NW / m.g, part = warp % kw, units = (m.k + S::UK - 1) / S::UK;
+    const long long all = (long long)n_groups * m.items;
+    tile = warp / kw;
+    lo = unit = part * units / kw;
+    hi = (part + 1) * units / kw;
+    item = (int)(all * blockIdx.x / gridDim.x);
+    end = (int)(all * (blockIdx.x + 1) / gridDim.x);
+    put = 0;
+    place(m, groups);
+  }
+  __device__ __forceinline__ void place(const Matrix& m, const uint32_t* groups) {
+    if (item >= end) return;
+    const int g = item / m.items, row = ((item - g * m.items) * m.g + tile) * S::RT;
+    src = row < m.rows ? m.w + ((size_t)(groups[g] & 1023) * m.rows + row) * m.rb : nullptr;
+  }
+  __device__ __forceinline__ void issue(const Params& p, const Matrix& m, const uint32_t* groups, uint32_t ring) {
+    while (item < end && (unit >= hi || !src)) {
+      unit = lo;
+      ++item;
+      place(m, groups);
+      if (lo >= hi) item = end;  // (a warp without inputs)
+    }
+    if (item < end) {
+      const int lane = threadIdx.x & 31;
+      const uint32_t dst = ring + put * S::SLOT;
+      if (FMT == TINFER_INT4) {
+        const uint8_t* from = src + unit * S::UB;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int id = lane + 32 * j, row = id >> 1, c = id & 1;
+          cp_async_16(dst + row * 32 + (c ^ (row >> 2 & 1)) * 16, from + (size_t)row * m.rb + c * 16);
+        }
+        const uint8_t* scales = src + (size_t)lane * m.rb + m.k / 2;
+        const int per = p.group >> 5;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int block = min(2 * unit + s, m.k / 32 - 1);
+          cp_async_4(dst + S::RT * S::UB + s * S::RT * 4 + lane * 4, scales + (block / per & ~1) * 2);
+        }
+      } else {
+        const uint8_t* from = src + unit * S::UB;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int id = lane + 32 * j, row = id >> 2, c = id & 3;
+          cp_async_16(dst + row * 64 + c * 16, from + (size_t)row * m.rb + c * 16);
+        }
+      }
+      ++unit;
+    }
+    cp_async_commit();
+    put = put + 1 == STAGES ? 0 : put + 1;
+  }
+};
+
+// ---- activations as operands ----------------------------------------------------------------------
+// Eight neighbouring inputs of a token as the second operand of two products, in PARTS bf16 parts whose sum they are. 4-bit
+// weights come as inputs i and i + 4 of a word, so theirs are paired alike.
+template <int FMT, int PARTS>
+__device__ __forceinline__ void operand(const float* x, uint32_t (&b)[PARTS][4]) {
+  float v[8];
+  kv8::load8(x, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float u = FMT == TINFER_INT4 ? v[i] : v[2 * i], w = FMT == TINFER_INT4 ? v[i + 4] : v[2 * i + 1];
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+      if (q == PARTS - 1 && PARTS == 2) {  // the rest, rounded
+        const __nv_bfloat162 r = __floats2bfloat162_rn(u, w);
+        b[q][i] = *reinterpret_cast<const uint32_t*>(&r);
+      } else {  // the upper 16 bits of an fp32 are its first eight, cut off
+        b[q][i] = __byte_perm(__float_as_uint(u), __float_as_uint(w), 0x7632);
+        u -= __uint_as_float(__float_as_uint(u) & 0xFFFF0000u);
+        w -= __uint_as_float(__float_as_uint(w) & 0xFFFF0000u);
+      }
+    }
+  }
+}
+template <int FMT>
+__device__ __forceinline__ void operand(const __nv_bfloat16* x, uint32_t (&b)[1][4]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(x);
+  if (FMT == TINFER_INT4) {
+    b[0][0] = __byte_perm(v.x, v.z, 0x5410);
+    b[0][1] = __byte_perm(v.x, v.z, 0x7632);
+    b[0][2] = __byte_perm(v.y, v.w, 0x5410);
+    b[0][3] = __byte_perm(v.y, v.w, 0x7632);
+  } else {
+    b[0][0] = v.x;
+    b[0][1] = v.y;
+    b[0][2] = v.z;
+    b[0][3] = v.w;
+  }
+}
+template <int FMT, int PARTS, typename BT>
+__device__ __forceinline__ void operand_any(const BT* x, uint32_t (&b)[PARTS][4]) {
+  if constexpr (sizeof(BT) == 2) operand<FMT>(x, b);
+  else operand<FMT, PARTS>(x, b);
+}
+
+// Elements of a token's row in shared memory: padded so that eight tokens' reads of 16 bytes a lane meet no bank twice.
+template <typename BT>
+__host__ __device__ constexpr int row_of(int k) {
+  return sizeof(BT) == 2 ? (k + 63) / 64 * 64 + 32 : k + 4;
+}
+
+// ---- one unit: acc += 16 or 32 rows x up to 16 tokens ----------------------------------------------
+template <int FMT, int PARTS, int NB, typename BT>
+__device__ __forceinline__ void multiply(const Params& p, const Matrix& m, const unsigned char* slot, const BT* const (&x)[NB],
+                                         int unit, float (&acc)[Shape<FMT>::TM][NB][4]) {
+  using S = Shape<FMT>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if constexpr (FMT == TINFER_INT4) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (unit * 64 + s * 32 >= m.k) break;
+      uint32_t a[2][2][4];  // [tile][product][operand register]
+      float scale[2][2];
+      const int odd = ((2 * unit + s) / (p.group >> 5)) & 1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = i * 16 + r * 8 + g;
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(slot + row * 32 + (s ^ (row >> 2 & 1)) * 16 + t * 4);
+          const uint32_t bias = 0x43084308u;  // 136 = 128 + 8: a nibble under the exponent of 128 reads 128 + q
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t q = (w >> (4 * j) & 0x000F000Fu) | 0x43004300u;
+            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&q), *reinterpret_cast<const __nv_bfloat162*>(&bias));
+            a[i][j >> 1][2 * (j & 1) + r] = *reinterpret_cast<const uint32_t*>(&d);
+          }
+          const uint32_t sw = *reinterpret_cast<const uint32_t*>(slot + S::RT * S::UB + s * S::RT * 4 + row * 4);
+          const uint32_t sh = odd ? sw >> 16 : sw & 0xFFFFu;
+          scale[i][r] = p.scale_bf16 ? __uint_as_float(sh << 16) : __half2float(__ushort_as_half((unsigned short)sh));
+        }
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        uint32_t b[PARTS][4];
+        operand_any<FMT, PARTS>(x[n] + unit * 64 + s * 32 + t * 8, b);
+        float d[2][4] = {};
+#pragma unroll
+        for (int q = PARTS - 1; q >= 0; --q)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) mma_bf16(d[i], a[i][h], b[q][2 * h], b[q][2 * h + 1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][n][r] = fmaf(scale[i][r >> 1], d[i][r], acc[i][n][r]);
+      }
+    }
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(slot + g * 64 + t * 16), v = *reinterpret_cast<const uint4*>(slot + (g + 8) * 64 + t * 16);
+    const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      uint32_t b[PARTS][4];
+      operand_any<FMT, PARTS>(x[n] + unit * 32 + t * 8, b);
+      float d[2][4] = {};  // (the instruction cuts its sums off: long ones are added rounded, and the small parts come first)
+#pragma unroll
+      for (int q = PARTS - 1; q >= 0; --q) {
+        mma_bf16(d[0], a0, b[q][0], b[q][1]);
+        mma_bf16(d[1], a1, b[q][2], b[q][3]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[0][n][r] += d[0][r] + d[1][r];
+    }
+  }
+}
+
+// ---- a phase of products --------------------------------------------------------------------------
+// Walks over the CTA's items. Stage: brings a group's activations to shared memory where they are not there yet and names
+// the row of each; Epilogue: takes the sums of (rows of an item, column).
+template <int FMT, int PARTS, typename BT, typename Stage, typename Epilogue>
+__device__ void products(const Params& p, const Matrix& m, const uint32_t* groups, Stream<FMT>& in, const unsigned char* ring_p,
+                         uint32_t ring, const BT* acts, int row_size, float* red, Stage&& stage, Epilogue&& epilogue,
+                         int first, int last) {
+  using S = Shape<FMT>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int kw = NW / m.g, lo = in.lo, hi = in.hi;
+  int got = 0, group = -1;
+  for (int item = first; item < last; ++item) {
+    const int now = item / m.items, it = item - now * m.items;
+    const uint32_t entry = groups[now];
+    const int n = (int)(entry >> 21), at = (int)(entry >> 10 & 2047);
+    if (now != group) {
+      stage(at, n);
+      group = now;
+    }
+    const int row0 = (it * m.g + in.tile) * S::RT;
+    float acc[S::TM][2][4];
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][b][r] = 0.f;
+    auto run = [&](auto blocks) {
+      constexpr int NB = decltype(blocks)::value;
+      const BT* x[NB];
+      float part[S::TM][NB][4] = {};
+#pragma unroll
+      for (int b = 0; b < NB; ++b) x[b] = acts + (size_t)stage.row(at, min(b * 8 + g, n - 1)) * row_size;
+      if (row0 < m.rows)
+        for (int u = lo; u < hi; ++u) {
+          cp_async_wait<STAGES - 1>();
+          __syncwarp();
+          multiply<FMT, PARTS, NB>(p, m, ring_p + got * S::SLOT, x, u, part);
+          __syncwarp();
+          in.issue(p, m, groups, ring);
+          got = got + 1 == STAGES ? 0 : got + 1;
+        }
+#pragma unroll
+      for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][b][r] = part[i][b][r];
+    };
+    if (n <= 8) run(std::integral_constant<int, 1>{});
+    else run(std::integral_constant<int, 2>{});
+    __syncthreads();  // (the last item's sums have been read)
+    float* mine = red + warp * COLS * S::RP;
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (b * 8 < n) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) mine[(b * 8 + 2 * t + (r & 1)) * S::RP + i * 16 + g + (r >> 1) * 8] = acc[i][b][r];
+        }
+    __syncthreads();
+    epilogue(it, at, n, kw);
+  }
+}
+
+template <int FMT, typename XT>
+__global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant__ Params p) {
+  using S = Shape<FMT>;
+  using BT = std::conditional_t<std::is_same_v<XT, __nv_bfloat16>, __nv_bfloat16, float>;
+  constexpr int UP_PARTS = std::is_same_v<XT, float> ? 3 : std::is_same_v<XT, __half> ? 2 : 1;
+  constexpr int DOWN_PARTS = std::is_same_v<XT, float> ? 3 : 2;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int failed, total[2];
+  __shared__ unsigned long long scan[NW];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  unsigned char* ring_p = smem + warp * STAGES * S::SLOT;
+  const uint32_t ring = smem_addr(ring_p);
+  float* red = reinterpret_cast<float*>(smem + S::RING);
+  unsigned char* acts = smem + S::RING + S::RED;
+  const Lists lists(acts + p.b_bytes, p.tokens * p.top_k);
+  if (tid == 0) failed = 0;
+
+  // ---- the router's products, a warp for an expert and up to four tokens
+  {
+    const int warps = gridDim.x * NW, quads = (p.tokens + 3) / 4;
+    const bool alone = p.experts * p.tokens <= warps;
+    const int tasks = p.experts * (alone ? p.tokens : quads);
+    for (int i = warp * gridDim.x + blockIdx.x; i < tasks; i += warps) {
+      const int m = i / p.experts, e = i - m * p.experts;
+      if (alone) route_any<XT, 1>(p, e, m);
+      else route_any<XT, 4>(p, e, 4 * m);
+    }
+  }
+  grid_arrive(p, 0);
+
+  // tokens as rows of shared memory; `which` names the token of a row
+  const int up_row = row_of<BT>(p.hidden);
+  BT* tokens = reinterpret_cast<BT*>(acts);
+  auto bring = [&](int n, auto which) {
+    const int words = p.hidden / 8;
+    for (int i = tid; i < n * words; i += NT) {
+      const int r = i / words, c = (i - r * words) * 8;
+      const XT* src = static_cast<const XT*>(p.x) + which(r) * p.x_stride + c;
+      if constexpr (std::is_same_v<XT, __nv_bfloat16>) {
+        *reinterpret_cast<uint4*>(tokens + (size_t)r * up_row + c) = *reinterpret_cast<const uint4*>(src);
+      } else {
+        float v[8];
+        kv8::load8(src, v);
+        kv8::store8(reinterpret_cast<float*>(tokens) + (size_t)r * up_row + c, v);
+      }
+    }
+  };
+  if (p.resident) bring(p.tokens, [](int r) { return r; });
+  if (!grid_wait(p, 0, &failed)) return;
+
+  choose<FMT>(p, reinterpret_cast<unsigned long long*>(smem), lists);
+  if (blockIdx.x == 0) {
+    for (int i = tid; i < p.tokens * p.top_k; i += NT) {
+      if (p.ids) p.ids[i] = lists.expert[i];
+      if (p.weights) p.weights[i] = lists.weight[i];
+    }
+  }
+  sort_entries(p, lists, total, scan);
+
+  // ---- gate and up
+  auto range = [&](const Matrix& m, int groups, int cta) { return (int)((long long)groups * m.items * cta / gridDim.x); };
+  Stream<FMT> in;
+  in.start(p.up, lists.up, total[0]);
+#pragma unroll 1
+  for (int i = 0; i < STAGES; ++i) in.issue(p, p.up, lists.up, ring);
+  struct UpStage {
+    const Params& p;
+    const Lists& l;
+    decltype(bring)& load;
+    __device__ void operator()(int at, int n) {
+      if (p.resident) return;
+      __syncthreads();
+      load(n, [&](int r) { return l.sorted[at + r] / p.top_k; });
+      __syncthreads();
+    }
+    __device__ int row(int at, int col) const { return p.resident ? l.sorted[at + col] / p.top_k : col; }
+  } up_stage{p, lists, bring};
+  products<FMT, UP_PARTS, BT>(
+      p, p.up, lists.up, in, ring_p, ring, tokens, up_row, red, up_stage,
+      [&](int it, int at, int n, int kw) {
+        constexpr int PAIRS = S::RT / 2;
+        for (int o = (tid + it * 64) & (NT - 1); o < p.up.g * PAIRS * n; o += NT) {
+          const int pair = o % PAIRS, rest = o / PAIRS, col = rest % n, tile = rest / n;
+          const int i = (it * p.up.g + tile) * PAIRS + pair;
+          if (i >= p.ffn) continue;
+          float2 s = make_float2(0.f, 0.f);
+          for (int w = 0; w < kw; ++w) {
+            const float2 v = *reinterpret_cast<const float2*>(red + (tile * kw + w) * COLS * S::RP + col * S::RP + 2 * pair);
+            s.x += v.x;
+            s.y += v.y;
+          }
+          const float e = expf(-fabsf(s.x));  // (of what does not overflow, so that far gates fade out and are not cut off)
+          p.h[(size_t)lists.sorted[at + col] * p.ffn + i] = (s.x < 0.f ? s.x * e : s.x) / (1.f + e) * s.y;
+        }
+      },
+      range(p.up, total[0], blockIdx.x), range(p.up, total[0], blockIdx.x + 1));
+
+  // ---- down; its first weights come while the others finish
+  cp_async_wait<0>();
+  __syncwarp();
+  grid_arrive(p, 1);
+  in.start(p.down, lists.down, total[1]);
+#pragma unroll 1
+  for (int i = 0; i < STAGES; ++i) in.issue(p, p.down, lists.down, ring);
+  if (!grid_wait(p, 1, &failed)) {
+    cp_async_wait<0>();
+    return;
+  }
+  const int down_row = row_of<float>(p.ffn);
+  struct DownStage {
+    const Params& p;
+    const Lists& l;
+    float* acts;
+    int row_size;
+    __device__ void operator()(int at, int n) {
+      __syncthreads();
+      const int words = p.ffn / 4;
+      for (int i = threadIdx.x; i < n * words; i += NT) {
+        const int r = i / words, c = (i - r * words) * 4;
+        *reinterpret_cast<float4*>(acts + (size_t)r * row_size + c) =
+            __ldcg(reinterpret_cast<const float4*>(p.h + (size_t)l.sorted[at + r] * p.ffn + c));
+      }
+      __syncthreads();
+    }
+    __device__ int row(int, int col) const { return col; }
+  } down_stage{p, lists, reinterpret_cast<float*>(acts), down_row};
+  products<FMT, DOWN_PARTS, float>(
+      p, p.down, lists.down, in, ring_p, ring, reinterpret_cast<const float*>(acts), down_row, red, down_stage,
+      [&](int it, int at, int n, int kw) {
+        for (int o = (tid + it * 64) & (NT - 1); o < p.down.g * S::RT * n; o += NT) {
+          const int row = o % S::RT, rest = o / S::RT, col = rest % n, tile = rest / n;
+          const int i = (it * p.down.g + tile) * S::RT + row;
+          if (i >= p.hidden) continue;
+          float s = 0.f;
+          for (int w = 0; w < kw; ++w) s += red[(tile * kw + w) * COLS * S::RP + col * S::RP + row];
+          p.part[(size_t)lists.sorted[at + col] * p.hidden + i] = s;
+        }
+      },
+      range(p.down, total[1], blockIdx.x), range(p.down, total[1], blockIdx.x + 1));
+  cp_async_wait<0>();
+  grid_arrive(p, 2);
+  if (!grid_wait(p, 2, &failed)) return;
+
+  // ---- each token's sum, its experts in order
+  const int words = p.hidden / 4;
+  for (int i = blockIdx.x * NT + tid; i < p.tokens * words; i += gridDim.x * NT) {
+    const int t = i / words, c = (i - t * words) * 4;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < p.top_k; ++s) {
+      const int e = t * p.top_k + s;
+      const float w = lists.weight[e];
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + (size_t)e * p.hidden + c));
+      y[0] = fmaf(w, v.x, y[0]);
+      y[1] = fmaf(w, v.y, y[1]);
+      y[2] = fmaf(w, v.z, y[2]);
+      y[3] = fmaf(w, v.w, y[3]);
+    }
+    XT* dst = static_cast<XT*>(p.y) + t * p.y_stride + c;
+    if (p.accumulate)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] += (float)dst[e];
+    kv8::store4(dst, y);
+  }
+  __syncthreads();
+  if (tid == 0 && atom_add_acq_rel(p.sync + 3, 1u) == gridDim.x - 1)  // the last to leave: the counters are as they were
+    for (int i = 0; i < 4; ++i) p.sync[i] = 0;
+}
+
+// ---------------------------------------------------------------------------------------- host
+
+// Tiles of an item: the more, the fewer warps share a tile's inputs; each has four units of an item then, or what there is.
+int tiles_of_item(int units) {
+  int g = 1;
+  while (g < NW && units * g < 4 * NW) g *= 2;
+  return g;
+}
+
+template <int FMT, typename XT>
+cudaError_t launch_t(Params& p, int sms, int smem, cudaStream_t st) {
+  const void* fn = reinterpret_cast<const void*>(&moe_layer_kernel<FMT, XT>);
+  static std::mutex mu;
+  static bool raised[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !raised[dev]) {
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM - 1024);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) raised[dev] = true;
+    }
+  }
+  void* args[] = {&p};
+  return cudaLaunchCooperativeKernel(fn, dim3((unsigned)sms), dim3(NT), args, (size_t)smem, st);
+}
+
+struct Sizes {
+  size_t logits, h, part, total;
+};
+Sizes sizes_of(const tinfer_moe* m, int tokens) {
+  Sizes s;
+  s.logits = 256;
+  s.h = s.logits + align_up((size_t)tokens * m->n_experts * 8, 256);
+  s.part = s.h + align_up((size_t)tokens * m->top_k * m->ffn_e * 4, 256);
+  s.total = s.part + align_up((size_t)tokens * m->top_k * m->hidden * 4, 256);
+  return s;
+}
+
+tinfer_status check(const tinfer_moe* m, int tokens) {
+  if (!m || m->n_experts < 1 || m->top_k < 1 || m->top_k > m->n_experts || m->hidden < 1 || m->ffn_e < 1 || tokens < 1) return TINFER_ERR_INVALID_ARG;
+  if (m->weight_format != TINFER_BF16 && m->weight_format != TINFER_INT4) return TINFER_ERR_INVALID_ARG;
+  if (m->flags & ~(TINFER_MOE_RENORMALISE | TINFER_MOE_KEEP_STATUS | TINFER_MOE_DEBUG_WITHHOLD)) return TINFER_ERR_INVALID_ARG;
+  if (m->weight_format == TINFER_INT4 && m->scale_dtype != TINFER_SCALE_FP16 && m->scale_dtype != TINFER_SCALE_BF16) return TINFER_ERR_INVALID_ARG;
+  if (m->router_dtype != TINFER_DTYPE_F32 && m->router_dtype != TINFER_DTYPE_BF16) return TINFER_ERR_INVALID_ARG;
+  if (!m->gu_packed || !m->down_packed || !m->router) return TINFER_ERR_INVALID_ARG;
+  for (const void* p : {m->gu_packed, m->down_packed, m->router})
+    if (reinterpret_cast<uintptr_t>(p) & 15) return TINFER_ERR_INVALID_ARG;
+  if (tokens > MAX_TOKENS || m->top_k > MAX_K || m->n_experts > MAX_EXPERTS) return TINFER_ERR_UNSUPPORTED;
+  if (m->hidden % 32 || m->ffn_e % 32 || m->hidden > MAX_WIDTH || m->ffn_e > MAX_WIDTH) return TINFER_ERR_UNSUPPORTED;
+  if (!packed_row_bytes(m->weight_format, m->hidden, m->group_size) || !packed_row_bytes(m->weight_format, m->ffn_e, m->group_size))
+    return TINFER_ERR_UNSUPPORTED;
+  return TINFER_OK;
+}
+
+template <int FMT>
+tinfer_status run(const tinfer_moe* m, int tokens, int dtype, Params& p, cudaStream_t st) {
+  using S = Shape<FMT>;
+  auto matrix = [&](const void* w, int rows, int k) {
+    Matrix x{};
+    x.w = static_cast<const uint8_t*>(w);
+    x.rows = rows;
+    x.k = k;
+    x.rb = (int)packed_row_bytes(m->weight_format, k, m->group_size);
+    x.g = tiles_of_item((k + S::UK - 1) / S::UK);
+    x.items = (rows / S::RT + x.g - 1) / x.g;
+    return x;
+  };
+  p.up = matrix(m->gu_packed, 2 * m->ffn_e, m->hidden);
+  p.down = matrix(m->down_packed, m->hidden, m->ffn_e);
+  const int entries = tokens * m->top_k, lists = Lists::bytes(entries);
+  const int room = (SMEM - 1024 - S::RING - S::RED - lists) / 128 * 128;
+  const int up_row = dtype == TINFER_DTYPE_BF16 ? row_of<__nv_bfloat16>(m->hidden) * 2 : row_of<float>(m->hidden) * 4;
+  const int down_row = row_of<float>(m->ffn_e) * 4;
+  p.up.cap = std::min(COLS, room / up_row);
+  p.down.cap = std::min(COLS, room / down_row);
+  if (p.up.cap < 1 || p.down.cap < 1) return TINFER_ERR_UNSUPPORTED;
+  p.resident = tokens * up_row <= room;
+  if (p.resident) p.up.cap = COLS;
+  p.b_bytes = (int)align_up((size_t)std::max(p.resident ? tokens * up_row : p.up.cap * up_row, p.down.cap * down_row), 128);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return TINFER_ERR_CUDA;
+  const int smem = S::RING + S::RED + p.b_bytes + lists;
+  const cudaError_t e = dtype == TINFER_DTYPE_F32   ? launch_t<FMT, float>(p, sms, smem, st)
+                        : dtype == TINFER_DTYPE_F16 ? launch_t<FMT, __half>(p, sms, smem, st)
+                                                    : launch_t<FMT, __nv_bfloat16>(p, sms, smem, st);
+  return e == cudaSuccess ? TINFER_OK : TINFER_ERR_CUDA;
+}
+
+}  // namespace moe
+}  // namespace tinfer
+
+using namespace tinfer;
+
+extern "C" size_t tinfer_moe_layer_workspace(const tinfer_moe* m, int n_tokens) {
+  return moe::check(m, n_tokens) == TINFER_OK ? moe::sizes_of(m, n_tokens).total : 0;
+}
+
+extern "C" tinfer_status tinfer_op_moe_layer(const tinfer_moe* m, int n_tokens, int dtype, const void* x_dev, long long x_stride,
+                                             void* y_dev, long long y_stride, int accumulate, int32_t* ids_dev,
+                                             float* weights_dev, void* workspace_dev, size_t workspace_bytes,
+                                             int32_t* status_dev, void* stream) {
+  const tinfer_status rc = moe::check(m, n_tokens);
+  if (rc != TINFER_OK) return rc;
+  const int size = dtype == TINFER_DTYPE_F32 ? 4 : dtype == TINFER_DTYPE_F16 || dtype == TINFER_DTYPE_BF16 ? 2 : 0;
+  if (!size || !x_dev || !y_dev || !workspace_dev || (accumulate != 0 && accumulate != 1)) return TINFER_ERR_INVALID_ARG;
+  for (const void* p : {x_dev, (const void*)y_dev, (const void*)workspace_dev})
+    if (reinterpret_cast<uintptr_t>(p) & 15) return TINFER_ERR_INVALID_ARG;
+  if (!kv8::words_of({ids_dev, weights_dev, status_dev})) return TINFER_ERR_INVALID_ARG;
+  if (n_tokens == 1) x_stride = y_stride = m->hidden;  // (one row: not looked at)
+  for (long long s : {x_stride, y_stride})
+    if (s < 0 || s % (16 / size) || s > (1LL << 40)) return TINFER_ERR_INVALID_ARG;
+  if (y_stride < m->hidden) return TINFER_ERR_INVALID_ARG;
+  const moe::Sizes s = moe::sizes_of(m, n_tokens);
+  if (workspace_bytes < s.total) return TINFER_ERR_INVALID_ARG;
+  moe::Params p{};
+  unsigned char* ws = static_cast<unsigned char*>(workspace_dev);
+  p.router = m->router;
+  p.router_f32 = m->router_dtype == TINFER_DTYPE_F32;
+  p.x = x_dev;
+  p.y = y_dev;
+  p.x_stride = x_stride;
+  p.y_stride = y_stride;
+  p.accumulate = accumulate;
+  p.tokens = n_tokens;
+  p.experts = m->n_experts;
+  p.top_k = m->top_k;
+  p.hidden = m->hidden;
+  p.ffn = m->ffn_e;
+  p.renormalise = (m->flags & TINFER_MOE_RENORMALISE) != 0;
+  p.group = m->weight_format == TINFER_INT4 ? m->group_size : 32;
+  p.scale_bf16 = m->scale_dtype == TINFER_SCALE_BF16;
+  p.ids = ids_dev;
+  p.weights = weights_dev;
+  p.sync = reinterpret_cast<unsigned*>(ws);
+  p.logits = reinterpret_cast<double*>(ws + s.logits);
+  p.h = reinterpret_cast<float*>(ws + s.h);
+  p.part = reinterpret_cast<float*>(ws + s.part);
+  p.status = status_dev;
+  p.withhold = (m->flags & TINFER_MOE_DEBUG_WITHHOLD) != 0;
+  p.wait_us = p.withhold ? moe::WAIT_US_WITHHELD : moe::WAIT_US;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (status_dev && !(m->flags & TINFER_MOE_KEEP_STATUS) && cudaMemsetAsync(status_dev, 0, 4, st) != cudaSuccess) return TINFER_ERR_CUDA;
+  return m->weight_format == TINFER_INT4 ? moe::run<TINFER_INT4>(m, n_tokens, dtype, p, st)
+                                         : moe::run<TINFER_BF16>(m, n_tokens, dtype, p, st);
+}

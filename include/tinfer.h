@@ -495,6 +495,41 @@ tinfer_status tinfer_op_qk_norm_rope(int n_seqs, int n_tokens, int n_heads, int 
                                      const tinfer_rows* q_out, const tinfer_rows* k_out, int32_t* status_dev,
                                      void* stream);
 
+/* A whole mixture-of-experts layer for a few tokens (the decode step of several sequences, drafted tokens verified), in one
+ * cooperative launch: for each row x of n_tokens rows,
+ *   l = Wr x,  p = softmax(l),  e_1 .. e_k the largest of p in order, equal ones by the lower id,
+ *   w_i = p[e_i], or with TINFER_MOE_RENORMALISE p[e_i] / sum_j p[e_j],
+ *   y = sum_i w_i Wd[e_i] (silu(Wg[e_i] x) * (Wu[e_i] x))      (accumulate 0; 1: y += the same)
+ * The router Wr is [n_experts][hidden], bf16 or fp32 (router_dtype), 16-byte aligned; gu_packed and down_packed are the experts as
+ * tinfer_pack_moe leaves them, bf16 or int4. x_dev and y_dev: rows of `dtype` (fp32, fp16 or bf16), x_stride and y_stride elements
+ * apart (multiples of 16 bytes; not looked at for one token), 16-byte aligned; y may be x (the same rows: in place), no other overlap is sound.
+ * ids_dev (int32) and weights_dev (fp32), [n_tokens][top_k], may be NULL: the experts chosen and their weights.
+ * Logits are computed to about 2^-45 of the sum of their products' sizes, so that the choice is that of fp64. Weights of
+ * the experts and x enter exactly, products are added in fp32, the SwiGLU outputs enter exactly for fp32 rows and rounded
+ * to 2^-17 for the others (bits below 2^-133 do not enter); the result is rounded once. Experts are summed in the order of choice: results do not depend on timing
+ * or on the other tokens' rows. A token with a NaN or an infinity has NaN results and ids that mean nothing; others are not touched.
+ * workspace_dev: tinfer_moe_layer_workspace bytes (0 for a layer or count that every call would refuse), 16-byte aligned. Its
+ * first 256 bytes have to be 0 before the first call and are 0 again after each; calls of several layers and counts may share one, but not calls
+ * that may overlap in time (other streams, other graphs). Bit 1 of *status_dev (int32, may be NULL; cleared first unless
+ * TINFER_MOE_KEEP_STATUS): a wait on the device (200 ms at most) ran out, the results are not valid and the workspace's first 256 bytes
+ * have to be cleared. Asynchronous on `stream`; the launch needs every SM, so it waits for earlier work of other streams.
+ * n_tokens <= 64, top_k <= 16, n_experts <= 512, hidden and ffn_e multiples of 32 up to 16384 (int4: and of the group), of
+ * which one row of activations has to fit shared memory, else TINFER_ERR_UNSUPPORTED. */
+enum { TINFER_MOE_RENORMALISE = 1, TINFER_MOE_KEEP_STATUS = 0x100 };              /* flags */
+/* Test hook, added to flags: one CTA's arrival at the first barrier stays away, so that the waits run out, after 5 ms. */
+enum { TINFER_MOE_DEBUG_WITHHOLD = 0x200 };
+typedef struct {
+  int weight_format, group_size, scale_dtype; /* as in tinfer_pack_moe */
+  int n_experts, top_k, hidden, ffn_e;
+  int router_dtype, flags;
+  const void *router, *gu_packed, *down_packed;
+} tinfer_moe;
+size_t tinfer_moe_layer_workspace(const tinfer_moe* layer, int n_tokens);
+tinfer_status tinfer_op_moe_layer(const tinfer_moe* layer, int n_tokens, int dtype, const void* x_dev,
+                                  long long x_stride, void* y_dev, long long y_stride, int accumulate,
+                                  int32_t* ids_dev, float* weights_dev, void* workspace_dev,
+                                  size_t workspace_bytes, int32_t* status_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

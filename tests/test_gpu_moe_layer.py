@@ -1,0 +1,376 @@
+"""The whole mixture-of-experts layer on the GPU against a plain implementation in 64 bits.
+
+Tolerance. A sum of K products of exact operands, added in fp32 by the tensor instruction in any order, is off by at most
+K 2^-23 sum |w x| (a truncation a term); for 4-bit weights of which 32 products each are scaled, by K 2^-23 + 2^-23 more of
+the scaled sizes. Gate and up errors a, b become |u| 1.1 a + |silu(g)| b of h = silu(g) u (|silu'| < 1.1), with 2^-20 |h| for the
+function itself. h enters exactly (fp32 rows) or to 2^-17; the down product adds as the others do, the weights (2^-22) and
+the sum over the experts (k 2^-24) their own. The result is rounded to its type by half a step.
+That bound is loose, so there are also rows with one input only, whose sums are exact: there the
+whole chain is off by 2^-19 (2^-16 where h is rounded) and a half step."""
+import threading
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import decode_persistent_megakernel_gb300 as T  # noqa: E402
+import synth  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+FORMATS = [("bf16", 0, None), ("int4", 32, torch.float16), ("int4", 64, torch.float16), ("int4", 64, torch.bfloat16),
+           ("int4", 128, torch.bfloat16)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    T.build()
+
+
+class Case:
+    """Seeded weights, the layer over them, and the layer's values in 64 bits."""
+
+    def __init__(self, experts, k, hidden, ffn, fmt="bf16", group=0, sdt=None, renormalise=True, seed=0, max_tokens=64,
+                 router=None, router_dtype=torch.bfloat16):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.k, self.renormalise, self.ffn = k, renormalise, ffn
+
+        def weight(rows, cols):
+            if fmt == "bf16":
+                return (torch.randn((experts, rows, cols), generator=g, device="cuda") * cols ** -0.5).bfloat16(), None
+            w = torch.randint(0, 256, (experts, rows, cols // 2), generator=g, device="cuda", dtype=torch.uint8)
+            s = torch.randn((experts, rows, cols // group), generator=g, device="cuda").abs() * 0.2 * cols ** -0.5
+            return w, s.to(sdt)
+
+        def dense(w, s):
+            if s is None:
+                return w.double()
+            q = torch.stack([w & 15, w >> 4], -1).flatten(-2).double() - 8
+            return q * s.double().repeat_interleave(group, -1)
+
+        (wg, sg), (wu, su), (wd, sd) = weight(ffn, hidden), weight(ffn, hidden), weight(hidden, ffn)
+        self.router = (torch.randn((experts, hidden), generator=g, device="cuda") * hidden ** -0.5) if router is None else router
+        self.router = self.router.to(router_dtype)
+        self.layer = T.MoeLayer(self.router, wg, wu, wd, k, scales=None if sg is None else (sg, su, sd), group=group,
+                                renormalise=renormalise, max_tokens=max_tokens)
+        self.w = [dense(*p) for p in ((wg, sg), (wu, su), (wd, sd))]
+        self.scaled = fmt == "int4"
+
+    def reference(self, x, h_off):
+        """y, ids, weights and the bound of y's error before its rounding."""
+        x = x.double()
+        logits = x @ self.router.double().T
+        v, ids = torch.sort(logits, dim=1, descending=True, stable=True)
+        v, ids = v[:, :self.k], ids[:, :self.k]
+        e = torch.exp(v - v[:, :1])
+        w = e / (e.sum(1, keepdim=True) if self.renormalise else torch.exp(logits - v[:, :1]).sum(1, keepdim=True))
+        y, bound = torch.zeros_like(x), torch.zeros_like(x)
+        wg, wu, wd = self.w
+        more = 1 if self.scaled else 0
+        for i in sorted(set(ids.flatten().tolist())):
+            who, slot = (ids == i).nonzero(as_tuple=True)
+            xs = x[who]
+            a, u = xs @ wg[i].T, xs @ wu[i].T
+            unit = (x.shape[1] + more) * 2.0 ** -23
+            da, du = unit * (xs.abs() @ wg[i].abs().T), unit * (xs.abs() @ wu[i].abs().T)
+            s = a * torch.sigmoid(a)
+            h = s * u
+            dh = u.abs() * 1.1 * da + s.abs() * du + 1.1 * da * du + (h_off + 2.0 ** -20) * h.abs()
+            o = h @ wd[i].T
+            do = dh @ wd[i].abs().T + (self.ffn + more) * 2.0 ** -23 * (h.abs() @ wd[i].abs().T)
+            share = w[who, slot][:, None]
+            y.index_add_(0, who, o * share)
+            bound.index_add_(0, who, (do + (2.0 ** -22 + self.k * 2.0 ** -24) * o.abs()) * share)
+        return y, ids, w, bound
+
+    def check(self, x, **kw):
+        ref, ids, w, bound = self.reference(x, 0.0 if x.dtype == torch.float32 else 2.0 ** -17)
+        y, gi, gw = self.layer(x, **kw)
+        torch.cuda.synchronize()
+        assert self.layer.error() == 0
+        assert torch.equal(gi.long(), ids)
+        assert bool(((gw.double() - w).abs() <= w * 2.0 ** -21 + 1e-38).all())
+        half = torch.finfo(x.dtype).eps / 2
+        off = (y.double() - ref).abs()
+        assert bool((off <= bound * (1 + half) + ref.abs() * half + 1e-30).all()), float((off / (bound + ref.abs() * half + 1e-30)).max())
+        return y, gi, gw
+
+
+def rows(m, h, dtype, seed=0):
+    return torch.randn((m, h), generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("fmt,group,sdt", FORMATS)
+def test_types_and_formats(fmt, group, sdt, dtype):
+    c = Case(16, 4, 512, 256, fmt, group, sdt)
+    for m in (1, 2, 7, 8, 9, 16, 33, 64):
+        c.check(rows(m, 512, dtype, m))
+
+
+@pytest.mark.parametrize("experts,k,hidden,ffn", [(1, 1, 32, 32), (2, 2, 64, 96), (3, 1, 96, 32), (5, 5, 160, 224), (40, 7, 288, 416),
+                                                  (512, 16, 64, 32), (300, 3, 32, 64), (8, 2, 4096, 64), (4, 1, 64, 4096),
+                                                  (8, 8, 2560, 1536), (3, 2, 8192, 32)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sizes(experts, k, hidden, ffn, dtype):
+    c = Case(experts, k, hidden, ffn)
+    for m in (1, 5, 23, 64):
+        c.check(rows(m, hidden, dtype, m))
+
+
+@pytest.mark.parametrize("hidden,ffn,group", [(64, 64, 32), (96, 160, 32), (96, 192, 96), (320, 64, 64), (2048, 1024, 64), (2560, 1280, 128),
+                                              (384, 128, 128), (8192, 160, 32)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sizes_of_4_bit_experts(hidden, ffn, group, dtype):
+    c = Case(6, 2, hidden, ffn, "int4", group, torch.float16)
+    for m in (1, 3, 30):
+        c.check(rows(m, hidden, dtype, m))
+
+
+@pytest.mark.parametrize("fmt,group,sdt", [FORMATS[0], FORMATS[2]])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_64_experts_top_8(fmt, group, sdt, dtype):
+    c = Case(64, 8, 2048, 1024, fmt, group, sdt)
+    for m in (1, 8, 64):
+        c.check(rows(m, 2048, dtype, m))
+
+
+@pytest.mark.parametrize("fmt,group,sdt", [FORMATS[0], FORMATS[2]])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_all_tokens_at_one_expert(fmt, group, sdt, dtype):
+    """64 tokens of one expert take several groups of columns; the second choices differ."""
+    router = torch.randn((8, 512), generator=torch.Generator().manual_seed(3)) * 0.05
+    router[5] = 1.0
+    c = Case(8, 2, 512, 256, fmt, group, sdt, router=router.cuda())
+    for m in (9, 17, 64):
+        x = (rows(m, 512, torch.float32, m).abs() + 0.1).to(dtype)
+        _, ids, _ = c.check(x)
+        assert bool((ids[:, 0] == 5).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_weights_as_the_softmax_leaves_them_and_fp32_routers(dtype):
+    for m in (1, 13):
+        Case(24, 3, 256, 128, renormalise=False).check(rows(m, 256, dtype, 1))
+        Case(24, 3, 256, 128, router_dtype=torch.float32).check(rows(m, 256, dtype, 2))
+
+
+def test_equal_logits_go_to_the_lower_id():
+    router = torch.randn((32, 256), generator=torch.Generator().manual_seed(1)) / 16
+    router[20] = router[4]
+    router[31] = router[4]
+    router[9] = router[0]
+    for renormalise in (True, False):
+        c = Case(32, 6, 256, 64, router=router.cuda(), renormalise=renormalise)
+        c.check(rows(64, 256, torch.float32, 5))
+    c = Case(32, 6, 256, 64, router=torch.zeros((32, 256), device="cuda"))
+    _, ids, w = c.check(rows(3, 256, torch.bfloat16))
+    assert ids.tolist() == [[0, 1, 2, 3, 4, 5]] * 3 and bool((w == w[0, 0]).all())
+
+
+def test_near_logits_are_told_apart():
+    """Logits of 2048 terms that differ by 2^-40 of their size: fp32 sums would not tell them apart."""
+    h = 2048
+    x = rows(16, h, torch.float32, 1)
+    router = torch.zeros((8, h), device="cuda")
+    base = torch.randn(h, generator=torch.Generator().manual_seed(2)).cuda()
+    for e in range(8):
+        router[e] = base
+        router[e, 7] = base[7] * (1 + (5 * e % 8) * 2.0 ** -23)
+    x[:, 7] = 2.0 ** -12 * (1 + torch.arange(16, device="cuda"))
+    c = Case(8, 4, h, 64, router=router, router_dtype=torch.float32)
+    _, ids, _ = c.layer(x)
+    want = torch.sort(x.double() @ router.double().T, dim=1, descending=True, stable=True)[1][:, :4]
+    assert torch.equal(ids.long(), want)
+
+
+@pytest.mark.parametrize("fmt,group,sdt", [FORMATS[0], FORMATS[3]])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_every_bit_of_an_input_enters(fmt, group, sdt, dtype):
+    """Rows with one input: sums are exact, so that only the function, the weights and the roundings are left. 2^-19: gate and up
+    2^-24 each (a product's rounding; 2^-23 scaled), the function 2^-20, the down product, weight and sum below 2^-21."""
+    h, f = 256, 64
+    c = Case(4, 1, h, f, fmt, group, sdt)
+    m = 64
+    x = torch.zeros((m, h))
+    at = torch.randint(0, h, (m,), generator=torch.Generator().manual_seed(1))
+    x[torch.arange(m), at] = (torch.rand(m, generator=torch.Generator().manual_seed(2)) * 3 + 1) * 2.0 ** torch.randint(-6, 3, (m,)).float()
+    x = x.to(dtype).cuda()
+    c.w[2].zero_()  # one input of the down product too: its matrix is made so
+    wd = torch.zeros((4, h, f), device="cuda")
+    wd[:, torch.arange(h), torch.arange(h) % f] = 1.0
+    g = torch.Generator(device="cuda").manual_seed(7)
+    if fmt == "bf16":
+        wg, wu = (torch.randn((4, f, h), generator=g, device="cuda").bfloat16() for _ in range(2))
+        layer = T.MoeLayer(c.router, wg, wu, wd.bfloat16(), 1)
+        dg, du, dd = wg.double(), wu.double(), wd.double()
+    else:
+        q = [torch.randint(0, 16, (4, f, h), generator=g, device="cuda", dtype=torch.uint8) for _ in range(2)]
+        s = [(torch.rand((4, f, h // group), generator=g, device="cuda") + 0.5).to(sdt) for _ in range(2)]
+        qd = (wd * 3 + 8).to(torch.uint8)
+        sd = torch.ones((4, h, f // group), device="cuda").to(sdt)
+        pack = lambda a: (a[..., 0::2] | (a[..., 1::2] << 4)).contiguous()  # noqa: E731
+        layer = T.MoeLayer(c.router, pack(q[0]), pack(q[1]), pack(qd), 1, scales=(s[0], s[1], sd), group=group)
+        dg, du = ((a.double() - 8) * b.double().repeat_interleave(group, -1) for a, b in zip(q, s))
+        dd = qd.double() - 8
+    y, ids, _ = layer(x)
+    e = ids[:, 0].long()
+    xd = x.double()[:, :, None]
+    a, u = (dg[e] @ xd)[:, :, 0], (du[e] @ xd)[:, :, 0]
+    ref = (dd[e] @ (a * torch.sigmoid(a) * u)[:, :, None])[:, :, 0]
+    off = 2.0 ** -19 if dtype == torch.float32 else 2.0 ** -16
+    half = torch.finfo(dtype).eps / 2
+    tiny = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    err = (y.double() - ref).abs()
+    # where the gate is far below 0 silu is known to 2^-23 |a| of itself more: its exponential's argument. An exponential
+    # below 2^-126 is known to a step of 2^-149, times |a| and then |u|, 4 for the down weights at most; so are products below it.
+    # Bits of h below 2^-133, the smallest step of a bf16 part, do not enter: 2^-133 times the down weight
+    fade = 2.0 ** -148 * 4 * (1 + a.abs().amax(1, keepdim=True)) * (1 + u.abs().amax(1, keepdim=True)) + 2.0 ** -133 * 4
+    assert bool((err <= ref.abs() * (off + half + a.abs().amax(1, keepdim=True) * 2.0 ** -22) + tiny + fade).all())
+
+
+def test_results_do_not_depend_on_the_neighbours_nor_on_the_run():
+    for fmt, group, sdt in (FORMATS[0], FORMATS[2]):
+        c = Case(16, 4, 2048, 256, fmt, group, sdt)
+        for dtype in (torch.float32, torch.bfloat16):
+            x = rows(64, 2048, dtype, 1)
+            y, ids, w = c.layer(x)
+            again = c.layer(x)
+            assert torch.equal(y, again[0]) and torch.equal(ids, again[1]) and torch.equal(w, again[2])
+            for i in (0, 13, 63):
+                one = c.layer(x[i:i + 1])
+                assert torch.equal(one[0], y[i:i + 1]) and torch.equal(one[1], ids[i:i + 1]) and torch.equal(one[2], w[i:i + 1])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_strides_in_place_and_accumulation(dtype):
+    c = Case(8, 2, 256, 128)
+    buf = rows(9, 3 * 256, dtype, 1)
+    x = buf[:, 256:512]
+    want, ids, w = c.check(x)
+    out = torch.full((9, 512), 7.0, dtype=dtype, device="cuda")
+    c.layer(x, out=out[:, 128:384])
+    assert torch.equal(out[:, 128:384], want) and bool((out[:, :128] == 7).all()) and bool((out[:, 384:] == 7).all())
+    base = rows(9, 256, dtype, 2)
+    got, _, _ = c.layer(x, out=base.clone(), accumulate=True)
+    exact = c.layer(x.float())[0].double() + base.double()
+    assert bool(((got.double() - exact).abs() <= exact.abs() * torch.finfo(dtype).eps / 2 + want.double().abs() * 2.0 ** -14 + 1e-6).all())
+    before = buf.clone()
+    c.layer(x, out=x)
+    assert torch.equal(x, want) and torch.equal(buf[:, :256], before[:, :256]) and torch.equal(buf[:, 512:], before[:, 512:])
+    one = c.layer(base[:1].expand(5, 256))[0]
+    assert torch.equal(one, c.layer(base[:1])[0].expand(5, 256))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_that_are_not_finite_spoil_themselves_alone(dtype):
+    for fmt, group, sdt in (FORMATS[0], FORMATS[2]):
+        c = Case(8, 2, 512, 128, fmt, group, sdt)
+        x = rows(20, 512, dtype, 1)
+        want = [t.clone() for t in c.layer(x)]
+        for i, v in ((3, float("nan")), (4, float("inf")), (19, float("-inf"))):
+            x[i, 5 * i] = v
+        got = c.layer(x)
+        good = [i for i in range(20) if i not in (3, 4, 19)]
+        for a, b in zip(got, want):
+            assert torch.equal(a[good], b[good])
+        assert bool(got[0][[3, 4, 19]].isnan().all())
+        assert c.layer.error() == 0
+
+
+def test_large_and_small_inputs():
+    c = Case(8, 2, 256, 128)
+    for scale in (1e-30, 1e-12, 1e12):
+        x = rows(5, 256, torch.float32, 1) * scale
+        ref, _, _, bound = c.reference(x, 0.0)
+        y = c.layer(x)[0].double()
+        assert bool(((y - ref).abs() <= bound + ref.abs() * 2.0 ** -20 + 1e-38).all())
+
+
+def test_agrees_with_the_gathered_experts_of_one_token():
+    for fmt, group, sdt in (("bf16", 64, "fp16"), ("int4", 64, "fp16")):
+        m = synth.make_moe(16, 4, 512, 256, fmt, group, sdt, seed=2)
+        bits = lambda a, t: None if a is None else torch.from_numpy(a.view("int16") if a.dtype == "uint16" else a).cuda().view(t)  # noqa: E731
+        wt = torch.uint8 if fmt == "int4" else torch.bfloat16
+        w = [bits(m[n], wt) for n in ("wg", "wu", "wd")]
+        s = None if fmt == "bf16" else tuple(bits(m[n], torch.float16) for n in ("sg", "su", "sd"))
+        router = (torch.randn((16, 512), generator=torch.Generator().manual_seed(1)) / 20).cuda()
+        layer = T.MoeLayer(router, *w, 4, scales=s, group=group if s else 0)
+        x = torch.from_numpy(m["x"]).cuda()[None]
+        y, ids, weights = layer(x)
+        h, one = torch.empty(4 * 256, device="cuda"), torch.empty(512, device="cuda")
+        assert T.tinfer_op_moe(T.TINFER_INT4 if s else T.TINFER_BF16, group, T.TINFER_SCALE_FP16, 16, 4, 512, 256, layer.gate_up,
+                               layer.down, ids, weights, x, h, one, stream=torch.cuda.current_stream()) == 0
+        assert float((y[0] - one).abs().max()) <= 1e-5 * float(one.abs().max())
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_layer_recovers():
+    c = Case(8, 2, 256, 128)
+    x = rows(4, 256, torch.float32, 1)
+    want = c.layer(x)[0].clone()
+    c.layer._kept.flags |= T.TINFER_MOE_DEBUG_WITHHOLD
+    c.layer(x)
+    assert c.layer.error() == 2
+    c.layer._kept.flags &= ~T.TINFER_MOE_DEBUG_WITHHOLD
+    assert torch.equal(c.layer(x)[0], want) and c.layer.error() == 0
+    status = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    assert torch.equal(c.layer(x, status=status)[0], want) and int(status) == 0
+
+
+def test_captured_graphs_side_streams_and_shared_workspaces():
+    a, b = Case(16, 4, 512, 256, seed=1), Case(8, 2, 256, 128, "int4", 64, torch.float16, seed=2)
+    ws = torch.zeros(max(c.layer.workspace_bytes() for c in (a, b)), dtype=torch.uint8, device="cuda")
+    xa, xb = rows(9, 512, torch.bfloat16, 1), rows(3, 256, torch.float32, 2)
+    ya, yb = torch.empty_like(xa), torch.empty_like(xb)
+    a.layer(xa), b.layer(xb)  # (loaded before the capture)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.layer(xa, out=ya, workspace=ws)
+        b.layer(xb, out=yb, workspace=ws)
+        a.layer(ya, out=ya, workspace=ws)
+    for seed in range(4):
+        xa.copy_(rows(9, 512, torch.bfloat16, 10 + seed))
+        xb.copy_(rows(3, 256, torch.float32, 20 + seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        first = a.layer(xa)[0]
+        assert torch.equal(ya, a.layer(first)[0]) and torch.equal(yb, b.layer(xb)[0])
+    # two streams with a workspace each, many calls
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.zeros_like(ws) for _ in streams]
+    torch.cuda.synchronize()
+    outs = [[torch.empty_like(xa) for _ in range(20)] for _ in streams]
+    for i in range(20):
+        for s, w, o in zip(streams, spaces, outs):
+            a.layer(xa, out=o[i], workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, first) for each in outs for o in each)
+    assert a.layer.error() == 0 and b.layer.error() == 0
+
+
+def test_host_threads():
+    cases = [Case(16, 4, 512, 256, seed=i, max_tokens=4 + i) for i in range(3)]
+    x = rows(4, 512, torch.float32, 3)
+    want = [c.layer(x)[0].clone() for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(c, w):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                if not torch.equal(c.layer(x)[0], w):
+                    bad.append(1)
+
+    threads = [threading.Thread(target=work, args=p) for p in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_no_tokens():
+    c = Case(4, 2, 64, 32)
+    y, ids, w = c.layer(torch.zeros((0, 64), device="cuda"))
+    assert y.shape == (0, 64) and ids.shape == (0, 2) and w.shape == (0, 2)
