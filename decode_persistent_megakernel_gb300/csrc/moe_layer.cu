@@ -37,7 +37,6 @@ namespace moe {
 
 constexpr int NT = 512, NW = NT / 32;
 constexpr int MAX_TOKENS = 64, MAX_K = 16, MAX_EXPERTS = 512, MAX_WIDTH = 16384;
-constexpr int STAGES = 5;        // units of a warp under way
 constexpr int COLS = 16;         // tokens of an expert at a time: two blocks of eight columns
 constexpr int SMEM = 227 * 1024;
 constexpr int STATUS_TIMEOUT = 2;
@@ -49,6 +48,7 @@ struct Shape {  // a unit: TM * 16 rows of UB bytes (UK inputs), and two words o
   static constexpr int RT = 16 * TM;
   static constexpr int UB = FMT == TINFER_INT4 ? 32 : 64, UK = FMT == TINFER_INT4 ? 64 : 32;
   static constexpr int SLOT = RT * UB + (FMT == TINFER_INT4 ? RT * 8 : 0);
+  static constexpr int STAGES = FMT == TINFER_INT4 ? 4 : 5;  // units of a warp under way
   static constexpr int RING = NW * STAGES * SLOT;
   static constexpr int RP = RT + 4;  // column of a warp's sums, padded so that its lanes' stores meet no bank twice
   static constexpr int RED = NW * COLS * RP * 4;
@@ -124,12 +124,14 @@ __device__ __forceinline__ bool grid_wait(const Params& p, int which, int* faile
 
 // ---- the router -----------------------------------------------------------------------------------
 // Sum and its error: 48 bits, so that experts are told apart as in fp64 (which the device has at a hundredth of the rate).
+template <bool EXACT>  // a product of two bf16 has no error
 struct Pair {
   float s, c;
   __device__ __forceinline__ void add(float a, float b) {  // + a * b: the product's error by a fused multiply, the sum's by Knuth's
-    const float p = a * b, e = fmaf(a, b, -p);
+    const float p = __fmul_rn(a, b);
     const float t = __fadd_rn(s, p), z = __fsub_rn(t, s);
-    c = __fadd_rn(c, __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z))));
+    const float e = __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z));
+    c = __fadd_rn(c, EXACT ? e : __fadd_rn(e, fmaf(a, b, -p)));
     s = t;
   }
 };
@@ -141,9 +143,10 @@ __device__ void route(const Params& p, int expert, int m0) {
   const XT* x[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = static_cast<const XT*>(p.x) + min(m0 + i, p.tokens - 1) * p.x_stride;
-  Pair acc[N];
+  using Sum = Pair<std::is_same_v<XT, __nv_bfloat16> && std::is_same_v<WT, __nv_bfloat16>>;
+  Sum acc[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = Pair{0.f, 0.f};
+  for (int i = 0; i < N; ++i) acc[i] = Sum{0.f, 0.f};
 #pragma unroll 2
   for (int c = lane * 8; c < p.hidden; c += 256) {
     float a[8], b[N][8];
@@ -169,7 +172,7 @@ __device__ __forceinline__ void route_any(const Params& p, int expert, int m0) {
   else route<XT, __nv_bfloat16, N>(p, expert, m0);
 }
 
-// Logits as keys in the order of their values; 1: NaN, 0: already chosen.
+// Logits as keys in the order of their values; 1: NaN, 0: none, or already chosen.
 __device__ __forceinline__ unsigned long long key_of(double x) {
   if (x != x) return 1ull;
   const unsigned long long b = (unsigned long long)__double_as_longlong(x + 0.0);
@@ -208,64 +211,66 @@ struct Lists {
   }
 };
 
-// The chosen experts and weights of all tokens, by every CTA for itself: eight lanes to a token.
-template <int FMT>
-__device__ void choose(const Params& p, unsigned long long* keys, const Lists& l) {
+// The chosen experts and weights of all tokens, by every CTA for itself: a warp to a token, up to N keys to a lane. The
+// largest is found by its upper word, which rarely leaves more than one lane to look at.
+template <int N>
+__device__ void choose_one(const Params& p, int t, const Lists& l) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long key[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) key[i] = lane + 32 * i < p.experts ? key_of(__ldcg(p.logits + (size_t)t * p.experts + lane + 32 * i)) : 0ull;
+  bool nan = false;
+  float all = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) nan |= key[i] == 1;
+  unsigned long long mine = 0;  // the key of the place that is the lane's
+  for (int s = 0; s < p.top_k; ++s) {
+    unsigned long long best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+    const unsigned hi = (unsigned)(best >> 32), top = __reduce_max_sync(~0u, hi);
+    unsigned who = __ballot_sync(~0u, hi == top);
+    int id = at * 32 + lane;
+    if (who & (who - 1)) {  // (alike for the warp)
+      const unsigned lo = hi == top ? (unsigned)best : 0u, low = __reduce_max_sync(~0u, lo);
+      who = __ballot_sync(~0u, hi == top && lo == low);
+      id = (int)__reduce_min_sync(~0u, who >> lane & 1 ? (unsigned)id : 0x7FFFFFFFu);
+    } else {
+      id = __shfl_sync(~0u, id, __ffs(who) - 1);
+    }
+    best = __shfl_sync(~0u, best, id & 31);
+    if (s == 0 && !p.renormalise) {
+      const double first = value_of(best);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (key[i]) all += expf((float)(value_of(key[i]) - first));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane + 32 * i == id) key[i] = 0;
+    if (lane == s) {
+      mine = best;
+      l.expert[t * p.top_k + s] = (uint16_t)id;
+    }
+  }
+  const unsigned long long first = __shfl_sync(~0u, mine, 0);
+  const float w = lane < p.top_k ? expf((float)(value_of(mine) - value_of(first))) : 0.f;
+  if (p.renormalise) all = w;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) all += __shfl_xor_sync(~0u, all, o);
+  nan = __any_sync(~0u, nan);
+  if (lane < p.top_k) l.weight[t * p.top_k + lane] = nan ? __uint_as_float(0x7FC00000u) : w / all;
+}
+__device__ void choose(const Params& p, const Lists& l) {
   for (int i = p.tokens * p.top_k + threadIdx.x; i < l.padded; i += NT) l.expert[i] = 0xFFFF;
-  const int per_round = min(NT / 8, Shape<FMT>::RING / 8 / p.experts), sub = threadIdx.x & 7;
-  for (int m0 = 0; m0 < p.tokens; m0 += per_round) {
-    const int n = min(per_round, p.tokens - m0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n * p.experts; i += NT) keys[i] = key_of(__ldcg(p.logits + (size_t)m0 * p.experts + i));
-    __syncthreads();
-    const int t = threadIdx.x >> 3;
-    unsigned long long* mine = keys + (size_t)min(t, n - 1) * p.experts;
-    const int at = (m0 + t) * p.top_k;
-    double top = 0.0;
-    float sum = 0.f;
-    bool nan = false;
-    for (int s = 0; s < p.top_k; ++s) {
-      unsigned long long best = 0;
-      int id = 0x7FFFFFFF;
-      for (int e = sub; e < p.experts; e += 8) {
-        const unsigned long long k = mine[e];
-        nan |= k == 1;
-        if (k > best) {
-          best = k;
-          id = e;
-        }
-      }
-#pragma unroll
-      for (int o = 1; o < 8; o *= 2) {
-        const unsigned long long k = __shfl_xor_sync(~0u, best, o);
-        const int other = __shfl_xor_sync(~0u, id, o);
-        if (k > best || (k == best && other < id)) {
-          best = k;
-          id = other;
-        }
-      }
-      if (s == 0) {
-        top = value_of(best);
-        if (!p.renormalise)
-          for (int e = sub; e < p.experts; e += 8) sum += expf((float)(value_of(mine[e]) - top));
-      }
-      const float x = expf((float)(value_of(best) - top));
-      if (p.renormalise) sum += x;
-      __syncwarp();  // (every lane has read the keys)
-      if (t < n && sub == 0) {
-        mine[id] = 0;
-        l.weight[at + s] = x;
-        l.expert[at + s] = (uint16_t)id;
-      }
-      __syncwarp();
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o *= 2) {
-      if (!p.renormalise) sum += __shfl_xor_sync(~0u, sum, o);
-      nan |= __shfl_xor_sync(~0u, nan, o);
-    }
-    if (t < n)
-      for (int s = sub; s < p.top_k; s += 8) l.weight[at + s] = nan ? __uint_as_float(0x7FC00000u) : l.weight[at + s] / sum;
+  for (int t = threadIdx.x >> 5; t < p.tokens; t += NW) {
+    if (p.experts <= 64) choose_one<2>(p, t, l);
+    else choose_one<MAX_EXPERTS / 32>(p, t, l);
   }
   __syncthreads();
 }
@@ -365,7 +370,7 @@ struct Stream {
       ++unit;
     }
     cp_async_commit();
-    put = put + 1 == STAGES ? 0 : put + 1;
+    put = put + 1 == S::STAGES ? 0 : put + 1;
   }
 };
 
@@ -373,111 +378,98 @@ struct Stream {
 // Eight neighbouring inputs of a token as the second operand of two products, in PARTS bf16 parts whose sum they are. 4-bit
 // weights come as inputs i and i + 4 of a word, so theirs are paired alike.
 template <int FMT, int PARTS>
-__device__ __forceinline__ void operand(const float* x, uint32_t (&b)[PARTS][4]) {
-  float v[8];
-  kv8::load8(x, v);
+__device__ __forceinline__ void split(const float (&v)[8], uint4 (&b)[PARTS]) {
+  uint32_t w[PARTS][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float u = FMT == TINFER_INT4 ? v[i] : v[2 * i], w = FMT == TINFER_INT4 ? v[i + 4] : v[2 * i + 1];
+    float u = FMT == TINFER_INT4 ? v[i] : v[2 * i], z = FMT == TINFER_INT4 ? v[i + 4] : v[2 * i + 1];
 #pragma unroll
     for (int q = 0; q < PARTS; ++q) {
       if (q == PARTS - 1 && PARTS == 2) {  // the rest, rounded
-        const __nv_bfloat162 r = __floats2bfloat162_rn(u, w);
-        b[q][i] = *reinterpret_cast<const uint32_t*>(&r);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(u, z);
+        w[q][i] = *reinterpret_cast<const uint32_t*>(&r);
       } else {  // the upper 16 bits of an fp32 are its first eight, cut off
-        b[q][i] = __byte_perm(__float_as_uint(u), __float_as_uint(w), 0x7632);
+        w[q][i] = __byte_perm(__float_as_uint(u), __float_as_uint(z), 0x7632);
         u -= __uint_as_float(__float_as_uint(u) & 0xFFFF0000u);
-        w -= __uint_as_float(__float_as_uint(w) & 0xFFFF0000u);
+        z -= __uint_as_float(__float_as_uint(z) & 0xFFFF0000u);
       }
     }
   }
-}
-template <int FMT>
-__device__ __forceinline__ void operand(const __nv_bfloat16* x, uint32_t (&b)[1][4]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(x);
-  if (FMT == TINFER_INT4) {
-    b[0][0] = __byte_perm(v.x, v.z, 0x5410);
-    b[0][1] = __byte_perm(v.x, v.z, 0x7632);
-    b[0][2] = __byte_perm(v.y, v.w, 0x5410);
-    b[0][3] = __byte_perm(v.y, v.w, 0x7632);
-  } else {
-    b[0][0] = v.x;
-    b[0][1] = v.y;
-    b[0][2] = v.z;
-    b[0][3] = v.w;
-  }
-}
-template <int FMT, int PARTS, typename BT>
-__device__ __forceinline__ void operand_any(const BT* x, uint32_t (&b)[PARTS][4]) {
-  if constexpr (sizeof(BT) == 2) operand<FMT>(x, b);
-  else operand<FMT, PARTS>(x, b);
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) b[q] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
 }
 
-// Elements of a token's row in shared memory: padded so that eight tokens' reads of 16 bytes a lane meet no bank twice.
-template <typename BT>
-__host__ __device__ constexpr int row_of(int k) {
-  return sizeof(BT) == 2 ? (k + 63) / 64 * 64 + 32 : k + 4;
-}
+// Bytes of a row of K operands in shared memory: padded so that eight rows' reads of 16 bytes a lane meet no bank twice.
+__host__ __device__ constexpr int row_bytes(int k) { return (k + 63) / 64 * 128 + 64; }
 
-// ---- one unit: acc += 16 or 32 rows x up to 16 tokens ----------------------------------------------
-template <int FMT, int PARTS, int NB, typename BT>
-__device__ __forceinline__ void multiply(const Params& p, const Matrix& m, const unsigned char* slot, const BT* const (&x)[NB],
-                                         int unit, float (&acc)[Shape<FMT>::TM][NB][4]) {
+// ---- one unit: acc += 16 or 32 rows x TB blocks of eight columns ----------------------------------
+// x: shared-memory address of the lane's column in each block, of its first input; its Q parts lie a row apart.
+template <int FMT, int TB, int Q>
+__device__ __forceinline__ void multiply(const Params& p, const Matrix& m, uint32_t slot, const uint32_t (&x)[TB], int row_size,
+                                         int unit, float (&acc)[Shape<FMT>::TM][TB][4]) {
   using S = Shape<FMT>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if constexpr (FMT == TINFER_INT4) {
+    const int per = p.group >> 5, first = 2 * unit / per;  // (blocks of 32 inputs to a scale)
+    const bool both = 2 * unit + 1 < m.k / 32, apart = (2 * unit + 1) / per != first;
+    float d[2][TB][4] = {};
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      if (unit * 64 + s * 32 >= m.k) break;
+      if (s && !both) break;
       uint32_t a[2][2][4];  // [tile][product][operand register]
-      float scale[2][2];
-      const int odd = ((2 * unit + s) / (p.group >> 5)) & 1;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int row = i * 16 + r * 8 + g;
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(slot + row * 32 + (s ^ (row >> 2 & 1)) * 16 + t * 4);
+          const uint32_t w = lds32(slot + row * 32 + (s ^ (row >> 2 & 1)) * 16 + t * 4);
           const uint32_t bias = 0x43084308u;  // 136 = 128 + 8: a nibble under the exponent of 128 reads 128 + q
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t q = (w >> (4 * j) & 0x000F000Fu) | 0x43004300u;
-            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&q), *reinterpret_cast<const __nv_bfloat162*>(&bias));
-            a[i][j >> 1][2 * (j & 1) + r] = *reinterpret_cast<const uint32_t*>(&d);
+            const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&q), *reinterpret_cast<const __nv_bfloat162*>(&bias));
+            a[i][j >> 1][2 * (j & 1) + r] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          const uint32_t sw = *reinterpret_cast<const uint32_t*>(slot + S::RT * S::UB + s * S::RT * 4 + row * 4);
-          const uint32_t sh = odd ? sw >> 16 : sw & 0xFFFFu;
-          scale[i][r] = p.scale_bf16 ? __uint_as_float(sh << 16) : __half2float(__ushort_as_half((unsigned short)sh));
         }
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        uint32_t b[PARTS][4];
-        operand_any<FMT, PARTS>(x[n] + unit * 64 + s * 32 + t * 8, b);
-        float d[2][4] = {};
+      for (int n = 0; n < TB; ++n)
 #pragma unroll
-        for (int q = PARTS - 1; q >= 0; --q)
+        for (int q = Q - 1; q >= 0; --q) {  // (the instruction cuts its sums off: the small parts come first)
+          const uint4 b = lds128(x[n] + q * row_size + (unit * 64 + s * 32 + t * 8) * 2);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int i = 0; i < 2; ++i) mma_bf16(d[i][n], a[i][0], b.x, b.y);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) mma_bf16(d[i], a[i][h], b[q][2 * h], b[q][2 * h + 1]);
+          for (int i = 0; i < 2; ++i) mma_bf16(d[i][n], a[i][1], b.z, b.w);
+        }
+      if (s == 0 && both && !apart) continue;  // (one scale for the unit)
+      const bool odd = (s && apart ? (2 * unit + 1) / per : first) & 1;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][n][r] = fmaf(scale[i][r >> 1], d[i][r], acc[i][n][r]);
-      }
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t sw = lds32(slot + S::RT * S::UB + s * S::RT * 4 + (i * 16 + r * 8 + g) * 4);
+          const uint32_t sh = odd ? sw >> 16 : sw & 0xFFFFu;
+          const float scale = p.scale_bf16 ? __uint_as_float(sh << 16) : __half2float(__ushort_as_half((unsigned short)sh));
+#pragma unroll
+          for (int n = 0; n < TB; ++n)
+#pragma unroll
+            for (int c = 2 * r; c < 2 * r + 2; ++c) {
+              acc[i][n][c] = fmaf(scale, d[i][n][c], acc[i][n][c]);
+              d[i][n][c] = 0.f;
+            }
+        }
     }
   } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(slot + g * 64 + t * 16), v = *reinterpret_cast<const uint4*>(slot + (g + 8) * 64 + t * 16);
+    const uint4 u = lds128(slot + g * 64 + t * 16), v = lds128(slot + (g + 8) * 64 + t * 16);
     const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      uint32_t b[PARTS][4];
-      operand_any<FMT, PARTS>(x[n] + unit * 32 + t * 8, b);
+    for (int n = 0; n < TB; ++n) {
       float d[2][4] = {};  // (the instruction cuts its sums off: long ones are added rounded, and the small parts come first)
 #pragma unroll
-      for (int q = PARTS - 1; q >= 0; --q) {
-        mma_bf16(d[0], a0, b[q][0], b[q][1]);
-        mma_bf16(d[1], a1, b[q][2], b[q][3]);
+      for (int q = Q - 1; q >= 0; --q) {
+        const uint4 b = lds128(x[n] + q * row_size + (unit * 32 + t * 8) * 2);
+        mma_bf16(d[0], a0, b.x, b.y);
+        mma_bf16(d[1], a1, b.z, b.w);
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[0][n][r] += d[0][r] + d[1][r];
@@ -487,11 +479,11 @@ __device__ __forceinline__ void multiply(const Params& p, const Matrix& m, const
 
 // ---- a phase of products --------------------------------------------------------------------------
 // Walks over the CTA's items. Stage: brings a group's activations to shared memory where they are not there yet and names
-// the row of each; Epilogue: takes the sums of (rows of an item, column).
-template <int FMT, int PARTS, typename BT, typename Stage, typename Epilogue>
-__device__ void products(const Params& p, const Matrix& m, const uint32_t* groups, Stream<FMT>& in, const unsigned char* ring_p,
-                         uint32_t ring, const BT* acts, int row_size, float* red, Stage&& stage, Epilogue&& epilogue,
-                         int first, int last) {
+// the place of each there; Epilogue: takes the sums of (rows of an item, column). Up to eight parts of tokens are columns of one
+// block; of more tokens each is a column, and its parts follow one another in the same sum.
+template <int FMT, int PARTS, typename Stage, typename Epilogue>
+__device__ void products(const Params& p, const Matrix& m, const uint32_t* groups, Stream<FMT>& in, uint32_t ring, uint32_t acts,
+                         int row_size, float* red, Stage&& stage, Epilogue&& epilogue, int first, int last) {
   using S = Shape<FMT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int kw = NW / m.g, lo = in.lo, hi = in.hi;
@@ -504,65 +496,57 @@ __device__ void products(const Params& p, const Matrix& m, const uint32_t* group
       stage(at, n);
       group = now;
     }
-    const int row0 = (it * m.g + in.tile) * S::RT;
-    float acc[S::TM][2][4];
+    const int row0 = (it * m.g + in.tile) * S::RT, cols = n * PARTS <= 8 ? n * PARTS : n;
+    float* mine = red + warp * COLS * S::RP;
+    auto run = [&](auto blocks, auto packed) {
+      constexpr int TB = decltype(blocks)::value, Q = decltype(packed)::value ? 1 : PARTS;
+      uint32_t x[TB];
+      float acc[S::TM][TB][4] = {};
 #pragma unroll
-    for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][b][r] = 0.f;
-    auto run = [&](auto blocks) {
-      constexpr int NB = decltype(blocks)::value;
-      const BT* x[NB];
-      float part[S::TM][NB][4] = {};
-#pragma unroll
-      for (int b = 0; b < NB; ++b) x[b] = acts + (size_t)stage.row(at, min(b * 8 + g, n - 1)) * row_size;
+      for (int b = 0; b < TB; ++b) {
+        const int col = min(b * 8 + g, cols - 1);
+        x[b] = acts + (Q == PARTS ? stage.place(at, col) * PARTS : stage.place(at, col / PARTS) * PARTS + col % PARTS) * row_size;
+      }
       if (row0 < m.rows)
         for (int u = lo; u < hi; ++u) {
-          cp_async_wait<STAGES - 1>();
+          cp_async_wait<S::STAGES - 1>();
           __syncwarp();
-          multiply<FMT, PARTS, NB>(p, m, ring_p + got * S::SLOT, x, u, part);
+          multiply<FMT, TB, Q>(p, m, ring + got * S::SLOT, x, row_size, u, acc);
           __syncwarp();
           in.issue(p, m, groups, ring);
-          got = got + 1 == STAGES ? 0 : got + 1;
+          got = got + 1 == S::STAGES ? 0 : got + 1;
         }
+      __syncthreads();  // (the last item's sums have been read)
 #pragma unroll
       for (int i = 0; i < S::TM; ++i)
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][b][r] = part[i][b][r];
-    };
-    if (n <= 8) run(std::integral_constant<int, 1>{});
-    else run(std::integral_constant<int, 2>{});
-    __syncthreads();  // (the last item's sums have been read)
-    float* mine = red + warp * COLS * S::RP;
-#pragma unroll
-    for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        if (b * 8 < n) {
+        for (int b = 0; b < TB; ++b)
 #pragma unroll
           for (int r = 0; r < 4; ++r) mine[(b * 8 + 2 * t + (r & 1)) * S::RP + i * 16 + g + (r >> 1) * 8] = acc[i][b][r];
-        }
+    };
+    if (n > 8) run(std::integral_constant<int, 2>{}, std::false_type{});
+    else if (PARTS > 1 && n * PARTS <= 8) run(std::integral_constant<int, 1>{}, std::true_type{});
+    else run(std::integral_constant<int, 1>{}, std::false_type{});
     __syncthreads();
-    epilogue(it, at, n, kw);
+    epilogue(it, at, n, kw, n * PARTS <= 8 ? PARTS : 1);
   }
 }
+
+// Parts of the rows' elements and of the SwiGLU outputs.
+template <typename XT>
+__host__ __device__ constexpr int parts_up() { return std::is_same_v<XT, float> ? 3 : std::is_same_v<XT, __half> ? 2 : 1; }
+template <typename XT>
+__host__ __device__ constexpr int parts_down() { return std::is_same_v<XT, float> ? 3 : 2; }
 
 template <int FMT, typename XT>
 __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant__ Params p) {
   using S = Shape<FMT>;
-  using BT = std::conditional_t<std::is_same_v<XT, __nv_bfloat16>, __nv_bfloat16, float>;
-  constexpr int UP_PARTS = std::is_same_v<XT, float> ? 3 : std::is_same_v<XT, __half> ? 2 : 1;
-  constexpr int DOWN_PARTS = std::is_same_v<XT, float> ? 3 : 2;
+  constexpr int UP_PARTS = parts_up<XT>(), DOWN_PARTS = parts_down<XT>();
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int failed, total[2];
   __shared__ unsigned long long scan[NW];
   const int tid = threadIdx.x, warp = tid >> 5;
-  unsigned char* ring_p = smem + warp * STAGES * S::SLOT;
-  const uint32_t ring = smem_addr(ring_p);
+  const uint32_t ring = smem_addr(smem + warp * S::STAGES * S::SLOT);
   float* red = reinterpret_cast<float*>(smem + S::RING);
   unsigned char* acts = smem + S::RING + S::RED;
   const Lists lists(acts + p.b_bytes, p.tokens * p.top_k);
@@ -570,38 +554,35 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
 
   // ---- the router's products, a warp for an expert and up to four tokens
   {
-    const int warps = gridDim.x * NW, quads = (p.tokens + 3) / 4;
-    const bool alone = p.experts * p.tokens <= warps;
-    const int tasks = p.experts * (alone ? p.tokens : quads);
+    const int warps = gridDim.x * NW, each = p.experts * p.tokens <= warps ? 1 : p.experts * p.tokens <= 2 * warps ? 2 : 4;
+    const int tasks = p.experts * ((p.tokens + each - 1) / each);
     for (int i = warp * gridDim.x + blockIdx.x; i < tasks; i += warps) {
       const int m = i / p.experts, e = i - m * p.experts;
-      if (alone) route_any<XT, 1>(p, e, m);
+      if (each == 1) route_any<XT, 1>(p, e, m);
+      else if (each == 2) route_any<XT, 2>(p, e, 2 * m);
       else route_any<XT, 4>(p, e, 4 * m);
     }
   }
   grid_arrive(p, 0);
 
-  // tokens as rows of shared memory; `which` names the token of a row
-  const int up_row = row_of<BT>(p.hidden);
-  BT* tokens = reinterpret_cast<BT*>(acts);
+  // tokens as rows of shared memory; `which` names the token of a place
+  const int up_row = row_bytes(p.hidden);
   auto bring = [&](int n, auto which) {
     const int words = p.hidden / 8;
     for (int i = tid; i < n * words; i += NT) {
       const int r = i / words, c = (i - r * words) * 8;
-      const XT* src = static_cast<const XT*>(p.x) + which(r) * p.x_stride + c;
-      if constexpr (std::is_same_v<XT, __nv_bfloat16>) {
-        *reinterpret_cast<uint4*>(tokens + (size_t)r * up_row + c) = *reinterpret_cast<const uint4*>(src);
-      } else {
-        float v[8];
-        kv8::load8(src, v);
-        kv8::store8(reinterpret_cast<float*>(tokens) + (size_t)r * up_row + c, v);
-      }
+      float v[8];
+      uint4 b[UP_PARTS];
+      kv8::load8(static_cast<const XT*>(p.x) + which(r) * p.x_stride + c, v);
+      split<FMT, UP_PARTS>(v, b);
+#pragma unroll
+      for (int q = 0; q < UP_PARTS; ++q) *reinterpret_cast<uint4*>(acts + (size_t)(r * UP_PARTS + q) * up_row + c * 2) = b[q];
     }
   };
   if (p.resident) bring(p.tokens, [](int r) { return r; });
   if (!grid_wait(p, 0, &failed)) return;
 
-  choose<FMT>(p, reinterpret_cast<unsigned long long*>(smem), lists);
+  choose(p, lists);
   if (blockIdx.x == 0) {
     for (int i = tid; i < p.tokens * p.top_k; i += NT) {
       if (p.ids) p.ids[i] = lists.expert[i];
@@ -615,7 +596,7 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
   Stream<FMT> in;
   in.start(p.up, lists.up, total[0]);
 #pragma unroll 1
-  for (int i = 0; i < STAGES; ++i) in.issue(p, p.up, lists.up, ring);
+  for (int i = 0; i < S::STAGES; ++i) in.issue(p, p.up, lists.up, ring);
   struct UpStage {
     const Params& p;
     const Lists& l;
@@ -626,22 +607,23 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
       load(n, [&](int r) { return l.sorted[at + r] / p.top_k; });
       __syncthreads();
     }
-    __device__ int row(int at, int col) const { return p.resident ? l.sorted[at + col] / p.top_k : col; }
+    __device__ int place(int at, int col) const { return p.resident ? l.sorted[at + col] / p.top_k : col; }
   } up_stage{p, lists, bring};
-  products<FMT, UP_PARTS, BT>(
-      p, p.up, lists.up, in, ring_p, ring, tokens, up_row, red, up_stage,
-      [&](int it, int at, int n, int kw) {
+  products<FMT, UP_PARTS>(
+      p, p.up, lists.up, in, ring, smem_addr(acts), up_row, red, up_stage,
+      [&](int it, int at, int n, int kw, int each) {
         constexpr int PAIRS = S::RT / 2;
         for (int o = (tid + it * 64) & (NT - 1); o < p.up.g * PAIRS * n; o += NT) {
           const int pair = o % PAIRS, rest = o / PAIRS, col = rest % n, tile = rest / n;
           const int i = (it * p.up.g + tile) * PAIRS + pair;
           if (i >= p.ffn) continue;
           float2 s = make_float2(0.f, 0.f);
-          for (int w = 0; w < kw; ++w) {
-            const float2 v = *reinterpret_cast<const float2*>(red + (tile * kw + w) * COLS * S::RP + col * S::RP + 2 * pair);
-            s.x += v.x;
-            s.y += v.y;
-          }
+          for (int q = each - 1; q >= 0; --q)
+            for (int w = 0; w < kw; ++w) {
+              const float2 v = *reinterpret_cast<const float2*>(red + ((tile * kw + w) * COLS + col * each + q) * S::RP + 2 * pair);
+              s.x += v.x;
+              s.y += v.y;
+            }
           const float e = expf(-fabsf(s.x));  // (of what does not overflow, so that far gates fade out and are not cut off)
           p.h[(size_t)lists.sorted[at + col] * p.ffn + i] = (s.x < 0.f ? s.x * e : s.x) / (1.f + e) * s.y;
         }
@@ -654,38 +636,44 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
   grid_arrive(p, 1);
   in.start(p.down, lists.down, total[1]);
 #pragma unroll 1
-  for (int i = 0; i < STAGES; ++i) in.issue(p, p.down, lists.down, ring);
+  for (int i = 0; i < S::STAGES; ++i) in.issue(p, p.down, lists.down, ring);
   if (!grid_wait(p, 1, &failed)) {
     cp_async_wait<0>();
     return;
   }
-  const int down_row = row_of<float>(p.ffn);
+  const int down_row = row_bytes(p.ffn);
   struct DownStage {
     const Params& p;
     const Lists& l;
-    float* acts;
+    unsigned char* acts;
     int row_size;
     __device__ void operator()(int at, int n) {
       __syncthreads();
-      const int words = p.ffn / 4;
+      const int words = p.ffn / 8;
       for (int i = threadIdx.x; i < n * words; i += NT) {
-        const int r = i / words, c = (i - r * words) * 4;
-        *reinterpret_cast<float4*>(acts + (size_t)r * row_size + c) =
-            __ldcg(reinterpret_cast<const float4*>(p.h + (size_t)l.sorted[at + r] * p.ffn + c));
+        const int r = i / words, c = (i - r * words) * 8;
+        const float4* src = reinterpret_cast<const float4*>(p.h + (size_t)l.sorted[at + r] * p.ffn + c);
+        const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
+        const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        uint4 b[DOWN_PARTS];
+        split<FMT, DOWN_PARTS>(v, b);
+#pragma unroll
+        for (int q = 0; q < DOWN_PARTS; ++q) *reinterpret_cast<uint4*>(acts + (size_t)(r * DOWN_PARTS + q) * row_size + c * 2) = b[q];
       }
       __syncthreads();
     }
-    __device__ int row(int, int col) const { return col; }
-  } down_stage{p, lists, reinterpret_cast<float*>(acts), down_row};
-  products<FMT, DOWN_PARTS, float>(
-      p, p.down, lists.down, in, ring_p, ring, reinterpret_cast<const float*>(acts), down_row, red, down_stage,
-      [&](int it, int at, int n, int kw) {
+    __device__ int place(int, int col) const { return col; }
+  } down_stage{p, lists, acts, down_row};
+  products<FMT, DOWN_PARTS>(
+      p, p.down, lists.down, in, ring, smem_addr(acts), down_row, red, down_stage,
+      [&](int it, int at, int n, int kw, int each) {
         for (int o = (tid + it * 64) & (NT - 1); o < p.down.g * S::RT * n; o += NT) {
           const int row = o % S::RT, rest = o / S::RT, col = rest % n, tile = rest / n;
           const int i = (it * p.down.g + tile) * S::RT + row;
           if (i >= p.hidden) continue;
           float s = 0.f;
-          for (int w = 0; w < kw; ++w) s += red[(tile * kw + w) * COLS * S::RP + col * S::RP + row];
+          for (int q = each - 1; q >= 0; --q)
+            for (int w = 0; w < kw; ++w) s += red[((tile * kw + w) * COLS + col * each + q) * S::RP + row];
           p.part[(size_t)lists.sorted[at + col] * p.hidden + i] = s;
         }
       },
@@ -721,11 +709,20 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
 
 // ---------------------------------------------------------------------------------------- host
 
-// Tiles of an item: the more, the fewer warps share a tile's inputs; each has four units of an item then, or what there is.
-int tiles_of_item(int units) {
-  int g = 1;
-  while (g < NW && units * g < 4 * NW) g *= 2;
-  return g;
+// Tiles of an item: the more, the fewer warps share a tile's inputs. That of the fewest turns of the busiest CTA, a turn being a
+// unit of each warp and an item's end (its sums, the function and the barriers) two more.
+int tiles_of_item(int units, int tiles, int experts, int grid) {
+  int best = 1;
+  long long least = -1;
+  for (int g = 1; g <= NW; g *= 2) {
+    const long long items = (long long)experts * ((tiles + g - 1) / g), turns = (items + grid - 1) / grid;
+    const long long cost = turns * ((units * g + NW - 1) / NW + 2);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = g;
+    }
+  }
+  return best;
 }
 
 template <int FMT, typename XT>
@@ -779,13 +776,16 @@ tinfer_status check(const tinfer_moe* m, int tokens) {
 template <int FMT>
 tinfer_status run(const tinfer_moe* m, int tokens, int dtype, Params& p, cudaStream_t st) {
   using S = Shape<FMT>;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return TINFER_ERR_CUDA;
   auto matrix = [&](const void* w, int rows, int k) {
     Matrix x{};
     x.w = static_cast<const uint8_t*>(w);
     x.rows = rows;
     x.k = k;
     x.rb = (int)packed_row_bytes(m->weight_format, k, m->group_size);
-    x.g = tiles_of_item((k + S::UK - 1) / S::UK);
+    x.g = tiles_of_item((k + S::UK - 1) / S::UK, rows / S::RT, std::min(tokens * m->top_k, m->n_experts), sms);
     x.items = (rows / S::RT + x.g - 1) / x.g;
     return x;
   };
@@ -793,17 +793,14 @@ tinfer_status run(const tinfer_moe* m, int tokens, int dtype, Params& p, cudaStr
   p.down = matrix(m->down_packed, m->hidden, m->ffn_e);
   const int entries = tokens * m->top_k, lists = Lists::bytes(entries);
   const int room = (SMEM - 1024 - S::RING - S::RED - lists) / 128 * 128;
-  const int up_row = dtype == TINFER_DTYPE_BF16 ? row_of<__nv_bfloat16>(m->hidden) * 2 : row_of<float>(m->hidden) * 4;
-  const int down_row = row_of<float>(m->ffn_e) * 4;
+  const int up_row = row_bytes(m->hidden) * (dtype == TINFER_DTYPE_F32 ? parts_up<float>() : dtype == TINFER_DTYPE_F16 ? parts_up<__half>() : parts_up<__nv_bfloat16>());
+  const int down_row = row_bytes(m->ffn_e) * (dtype == TINFER_DTYPE_F32 ? parts_down<float>() : parts_down<__half>());
   p.up.cap = std::min(COLS, room / up_row);
   p.down.cap = std::min(COLS, room / down_row);
   if (p.up.cap < 1 || p.down.cap < 1) return TINFER_ERR_UNSUPPORTED;
   p.resident = tokens * up_row <= room;
   if (p.resident) p.up.cap = COLS;
   p.b_bytes = (int)align_up((size_t)std::max(p.resident ? tokens * up_row : p.up.cap * up_row, p.down.cap * down_row), 128);
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return TINFER_ERR_CUDA;
   const int smem = S::RING + S::RED + p.b_bytes + lists;
   const cudaError_t e = dtype == TINFER_DTYPE_F32   ? launch_t<FMT, float>(p, sms, smem, st)
                         : dtype == TINFER_DTYPE_F16 ? launch_t<FMT, __half>(p, sms, smem, st)

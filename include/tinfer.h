@@ -506,8 +506,8 @@ tinfer_status tinfer_op_qk_norm_rope(int n_seqs, int n_tokens, int n_heads, int 
  * ids_dev (int32) and weights_dev (fp32), [n_tokens][top_k], may be NULL: the experts chosen and their weights.
  * Logits are computed to about 2^-45 of the sum of their products' sizes, so that the choice is that of fp64. Weights of
  * the experts and x enter exactly, products are added in fp32, the SwiGLU outputs enter exactly for fp32 rows and rounded
- * to 2^-17 for the others (bits below 2^-133 do not enter); the result is rounded once. Experts are summed in the order of choice: results do not depend on timing
- * or on the other tokens' rows. A token with a NaN or an infinity has NaN results and ids that mean nothing; others are not touched.
+ * to 2^-17 for the others (bits below 2^-133 do not enter); the result is rounded once. Experts are summed in the order of choice: results do not depend on timing.
+ * (The order of additions within a product depends on how many tokens chose an expert.) A token with a NaN or an infinity has NaN results and ids that mean nothing; others are not touched.
  * workspace_dev: tinfer_moe_layer_workspace bytes (0 for a layer or count that every call would refuse), 16-byte aligned. Its
  * first 256 bytes have to be 0 before the first call and are 0 again after each; calls of several layers and counts may share one, but not calls
  * that may overlap in time (other streams, other graphs). Bit 1 of *status_dev (int32, may be NULL; cleared first unless
