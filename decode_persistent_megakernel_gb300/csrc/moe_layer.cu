@@ -48,8 +48,6 @@ struct Shape {  // a unit: TM * 16 rows of UB bytes (UK inputs), and two words o
   static constexpr int RT = 16 * TM;
   static constexpr int UB = FMT == TINFER_INT4 ? 32 : 64, UK = FMT == TINFER_INT4 ? 64 : 32;
   static constexpr int SLOT = RT * UB + (FMT == TINFER_INT4 ? RT * 8 : 0);
-  static constexpr int STAGES = FMT == TINFER_INT4 ? 4 : 5;  // units of a warp under way
-  static constexpr int RING = NW * STAGES * SLOT;
   static constexpr int RP = RT + 4;  // column of a warp's sums, padded so that its lanes' stores meet no bank twice
   static constexpr int RED = NW * COLS * RP * 4;
 };
@@ -75,10 +73,11 @@ struct Params {
   int* ids;        // outputs, may be null
   float* weights;
   unsigned* sync;  // counters of the three barriers and of the CTAs that have left; 0 between calls
-  double* logits;  // [tokens][experts]
+  float2* logits;  // [tokens][experts], each a sum of two
   float* h;        // [tokens * top_k][ffn]
   float* part;     // [tokens * top_k][hidden]
   int* status;
+  int stages;      // units of a warp under way: 4, 6 or 8
   int resident;    // all tokens stay in shared memory for the gate and up products
   int b_bytes;     // shared memory of the activations
   int wait_us, withhold;
@@ -96,7 +95,7 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -123,7 +122,8 @@ __device__ __forceinline__ bool grid_wait(const Params& p, int which, int* faile
 }
 
 // ---- the router -----------------------------------------------------------------------------------
-// Sum and its error: 48 bits, so that experts are told apart as in fp64 (which the device has at a hundredth of the rate).
+// Sum and its error: 48 bits, so that experts are told apart as in fp64 (which the device has at a hundredth of the rate: a
+// few fp64 operations on each logit took longer than the router's products).
 template <bool EXACT>  // a product of two bf16 has no error
 struct Pair {
   float s, c;
@@ -134,7 +134,17 @@ struct Pair {
     c = __fadd_rn(c, EXACT ? e : __fadd_rn(e, fmaf(a, b, -p)));
     s = t;
   }
+  __device__ __forceinline__ float2 both() const {  // the sum as the nearest fp32 and the rest, which only one pair says so
+    const float h = __fadd_rn(s, c);
+    return make_float2(h, __fsub_rn(c, __fsub_rn(h, s)));
+  }
 };
+__device__ __forceinline__ float2 add_pairs(float2 a, float2 b) {
+  Pair<true> x{a.x, a.y};
+  x.add(1.f, b.x);
+  x.c = __fadd_rn(x.c, b.y);
+  return x.both();
+}
 
 template <typename XT, typename WT, int N>
 __device__ void route(const Params& p, int expert, int m0) {
@@ -147,7 +157,7 @@ __device__ void route(const Params& p, int expert, int m0) {
   Sum acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = Sum{0.f, 0.f};
-#pragma unroll 2
+#pragma unroll 4
   for (int c = lane * 8; c < p.hidden; c += 256) {
     float a[8], b[N][8];
     kv8::load8(w + c, a);
@@ -160,9 +170,9 @@ __device__ void route(const Params& p, int expert, int m0) {
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    double d = (double)acc[i].s + (double)acc[i].c;
+    float2 d = acc[i].both();
 #pragma unroll
-    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
+    for (int o = 16; o; o >>= 1) d = add_pairs(d, make_float2(__shfl_xor_sync(~0u, d.x, o), __shfl_xor_sync(~0u, d.y, o)));
     if (lane == 0 && m0 + i < p.tokens) p.logits[(size_t)(m0 + i) * p.experts + expert] = d;
   }
 }
@@ -173,13 +183,18 @@ __device__ __forceinline__ void route_any(const Params& p, int expert, int m0) {
 }
 
 // Logits as keys in the order of their values; 1: NaN, 0: none, or already chosen.
-__device__ __forceinline__ unsigned long long key_of(double x) {
-  if (x != x) return 1ull;
-  const unsigned long long b = (unsigned long long)__double_as_longlong(x + 0.0);
-  return b >> 63 ? ~b : b | (1ull << 63);
+__device__ __forceinline__ unsigned ordered(float x) {
+  const unsigned b = __float_as_uint(x + 0.f);  // (zeros of both signs are equal)
+  return b >> 31 ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ double value_of(unsigned long long k) {
-  return __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k));
+__device__ __forceinline__ float unordered(unsigned u) { return __uint_as_float(u >> 31 ? u & 0x7FFFFFFFu : ~u); }
+__device__ __forceinline__ unsigned long long key_of(float2 x) {
+  if (!(fabsf(x.x) < INFINITY)) return x.x != x.x ? 1ull : (unsigned long long)ordered(x.x) << 32 | 0x80000000u;  // (the rest is NaN)
+  return (unsigned long long)ordered(x.x) << 32 | ordered(x.y);
+}
+// e^(a - b) of two keys
+__device__ __forceinline__ float ratio(unsigned long long a, unsigned long long b) {
+  return expf((unordered((unsigned)(a >> 32)) - unordered((unsigned)(b >> 32))) + (unordered((unsigned)a) - unordered((unsigned)b)));
 }
 
 // ---- shared memory --------------------------------------------------------------------------------
@@ -188,102 +203,124 @@ struct Lists {
   uint16_t* expert;    // of an entry
   uint16_t* sorted;    // entries by expert, then token
   uint32_t *up, *down;  // groups of an expert's entries: expert | first << 10 | n << 21
-  int padded;           // entries, to whole words of eight; no expert's past their end
   __host__ __device__ static int bytes(int entries) { return (entries + 7) / 8 * 128; }
-  __device__ Lists(unsigned char* at, int n) : padded((n + 7) / 8 * 8) {
+  __device__ Lists(unsigned char* at, int n) {
     weight = reinterpret_cast<float*>(at);
-    up = reinterpret_cast<uint32_t*>(at + 4 * padded);
-    down = reinterpret_cast<uint32_t*>(at + 8 * padded);
-    expert = reinterpret_cast<uint16_t*>(at + 12 * padded);
-    sorted = expert + padded;
-  }
-  template <typename F>
-  __device__ __forceinline__ void each(int e, F&& f) const {  // f(entry) for the entries of an expert in order
-    for (int i = 0; i < padded; i += 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(expert + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if ((int)(w[j] & 0xFFFFu) == e) f(i + 2 * j);
-        if ((int)(w[j] >> 16) == e) f(i + 2 * j + 1);
-      }
-    }
+    up = reinterpret_cast<uint32_t*>(at + 4 * n);
+    down = reinterpret_cast<uint32_t*>(at + 8 * n);
+    expert = reinterpret_cast<uint16_t*>(at + 12 * n);
+    sorted = expert + n;
   }
 };
 
-// The chosen experts and weights of all tokens, by every CTA for itself: a warp to a token, up to N keys to a lane. The
-// largest is found by its upper word, which rarely leaves more than one lane to look at.
-template <int N>
-__device__ void choose_one(const Params& p, int t, const Lists& l) {
+// The chosen experts and weights of all tokens, by every CTA for itself: a warp to a token, up to N keys to a lane.
+__device__ __forceinline__ void weigh(const Params& p, int t, const Lists& l, unsigned long long mine, float all, bool nan) {
+  // mine: the key of the lane's place; all: the lane's share of the softmax's sum, where that counts
   const int lane = threadIdx.x & 31;
-  unsigned long long key[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) key[i] = lane + 32 * i < p.experts ? key_of(__ldcg(p.logits + (size_t)t * p.experts + lane + 32 * i)) : 0ull;
-  bool nan = false;
-  float all = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) nan |= key[i] == 1;
-  unsigned long long mine = 0;  // the key of the place that is the lane's
-  for (int s = 0; s < p.top_k; ++s) {
-    unsigned long long best = key[0];
-    int at = 0;
-#pragma unroll
-    for (int i = 1; i < N; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
-    const unsigned hi = (unsigned)(best >> 32), top = __reduce_max_sync(~0u, hi);
-    unsigned who = __ballot_sync(~0u, hi == top);
-    int id = at * 32 + lane;
-    if (who & (who - 1)) {  // (alike for the warp)
-      const unsigned lo = hi == top ? (unsigned)best : 0u, low = __reduce_max_sync(~0u, lo);
-      who = __ballot_sync(~0u, hi == top && lo == low);
-      id = (int)__reduce_min_sync(~0u, who >> lane & 1 ? (unsigned)id : 0x7FFFFFFFu);
-    } else {
-      id = __shfl_sync(~0u, id, __ffs(who) - 1);
-    }
-    best = __shfl_sync(~0u, best, id & 31);
-    if (s == 0 && !p.renormalise) {
-      const double first = value_of(best);
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (key[i]) all += expf((float)(value_of(key[i]) - first));
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (lane + 32 * i == id) key[i] = 0;
-    if (lane == s) {
-      mine = best;
-      l.expert[t * p.top_k + s] = (uint16_t)id;
-    }
-  }
   const unsigned long long first = __shfl_sync(~0u, mine, 0);
-  const float w = lane < p.top_k ? expf((float)(value_of(mine) - value_of(first))) : 0.f;
+  const float w = lane < p.top_k ? ratio(mine, first) : 0.f;
   if (p.renormalise) all = w;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) all += __shfl_xor_sync(~0u, all, o);
   nan = __any_sync(~0u, nan);
   if (lane < p.top_k) l.weight[t * p.top_k + lane] = nan ? __uint_as_float(0x7FC00000u) : w / all;
 }
-__device__ void choose(const Params& p, const Lists& l) {
-  for (int i = p.tokens * p.top_k + threadIdx.x; i < l.padded; i += NT) l.expert[i] = 0xFFFF;
+// One maximum after another, found by its upper word, which rarely leaves more than one lane to look at. (Counting the keys
+// above each took longer.)
+template <int N>
+__device__ __forceinline__ void load_logits(const Params& p, int t, float2 (&x)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (t < p.tokens && lane + 32 * i < p.experts) x[i] = __ldcg(p.logits + (size_t)t * p.experts + lane + 32 * i);
+}
+template <int N>
+__device__ void choose_all(const Params& p, const Lists& l) {
+  const int lane = threadIdx.x & 31;
+  float2 x[N];
+  if (N <= 4) load_logits<N>(p, threadIdx.x >> 5, x);
   for (int t = threadIdx.x >> 5; t < p.tokens; t += NW) {
-    if (p.experts <= 64) choose_one<2>(p, t, l);
-    else choose_one<MAX_EXPERTS / 32>(p, t, l);
+    if (N > 4) load_logits<N>(p, t, x);
+    unsigned long long key[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = lane + 32 * i < p.experts ? key_of(x[i]) : 0ull;
+    if (N <= 4) load_logits<N>(p, t + NW, x);  // (the next token's)
+    bool nan = false;
+    float all = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) nan |= key[i] == 1;
+    unsigned long long mine = 0;  // the key of the place that is the lane's
+    for (int s = 0; s < p.top_k; ++s) {
+      unsigned long long best = key[0];
+      int at = 0;
+#pragma unroll
+      for (int i = 1; i < N; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          at = i;
+        }
+      const unsigned hi = (unsigned)(best >> 32), top = __reduce_max_sync(~0u, hi);
+      unsigned who = __ballot_sync(~0u, hi == top);
+      int id = at * 32 + lane;
+      if (who & (who - 1)) {  // (alike for the warp)
+        const unsigned lo = hi == top ? (unsigned)best : 0u, low = __reduce_max_sync(~0u, lo);
+        who = __ballot_sync(~0u, hi == top && lo == low);
+        id = (int)__reduce_min_sync(~0u, who >> lane & 1 ? (unsigned)id : 0x7FFFFFFFu);
+      } else {
+        id = __shfl_sync(~0u, id, __ffs(who) - 1);
+      }
+      best = __shfl_sync(~0u, best, id & 31);
+      if (s == 0 && !p.renormalise) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (key[i]) all += ratio(key[i], best);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (lane + 32 * i == id) key[i] = 0;
+      if (lane == s) {
+        mine = best;
+        l.expert[t * p.top_k + s] = (uint16_t)id;
+      }
+    }
+    weigh(p, t, l, mine, all, nan);
   }
+}
+__device__ void choose(const Params& p, const Lists& l) {
+  if (p.experts <= 64) choose_all<2>(p, l);
+  else if (p.experts <= 128) choose_all<4>(p, l);
+  else choose_all<MAX_EXPERTS / 32>(p, l);
   __syncthreads();
 }
 
-// Entries by expert, and the groups of at most `cap` of them; counts of the groups in total[0], total[1].
-__device__ void sort_entries(const Params& p, const Lists& l, int* total, unsigned long long* scan) {
-  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
-  int count = 0;
-  if (e < p.experts)
-    l.each(e, [&](int) { ++count; });
-  const int groups_up = (count + p.up.cap - 1) / p.up.cap, groups_down = (count + p.down.cap - 1) / p.down.cap;
-  const unsigned long long mine = (unsigned long long)count | (unsigned long long)groups_up << 20 | (unsigned long long)groups_down << 40;
-  unsigned long long incl = mine;
+// Entries by expert, and the groups of at most `cap` of them; counts of the groups in total[0], total[1]. scratch: counts of
+// each expert among each 32 entries.
+__device__ void sort_entries(const Params& p, const Lists& l, int* total, unsigned long long* scan, unsigned char* scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.tokens * p.top_k, rows = (n + 31) / 32;
+  uint16_t* count = reinterpret_cast<uint16_t*>(scratch);            // [rows][experts]
+  uint16_t* first = count + rows * p.experts;                        // [experts]
+  for (int i = tid; i < (rows * p.experts + 1) / 2; i += NT) reinterpret_cast<unsigned*>(count)[i] = 0;
+  __syncthreads();
+  int mine[2], rank[2];  // the thread's entries: their experts, how many of the 32 stand before them
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = tid + h * NT;
+    mine[h] = i < n ? l.expert[i] : 0xFFFF;
+    const unsigned same = __match_any_sync(~0u, mine[h]);
+    rank[h] = __popc(same & ((1u << lane) - 1));
+    if (i < n && rank[h] == 0) count[(i >> 5) * p.experts + mine[h]] = (uint16_t)__popc(same);
+  }
+  __syncthreads();
+  int all = 0;
+  if (tid < p.experts)
+    for (int r = 0; r < rows; ++r) {
+      const int c = count[r * p.experts + tid];
+      count[r * p.experts + tid] = (uint16_t)all;
+      all += c;
+    }
+  const int groups_up = (all + p.up.cap - 1) / p.up.cap, groups_down = (all + p.down.cap - 1) / p.down.cap;
+  const unsigned long long own = (unsigned long long)all | (unsigned long long)groups_up << 20 | (unsigned long long)groups_down << 40;
+  unsigned long long incl = own;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
     const unsigned long long y = __shfl_up_sync(~0u, incl, o);
@@ -291,22 +328,28 @@ __device__ void sort_entries(const Params& p, const Lists& l, int* total, unsign
   }
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  unsigned long long before = 0, all = 0;
+  unsigned long long before = 0, sum = 0;
+#pragma unroll
   for (int w = 0; w < NW; ++w) {
     if (w < warp) before += scan[w];
-    all += scan[w];
+    sum += scan[w];
   }
-  before += incl - mine;
-  const int first = (int)(before & 0xFFFFF);
-  int at = first;
-  if (count) l.each(e, [&](int i) { l.sorted[at++] = (uint16_t)i; });
+  before += incl - own;
+  const int at = (int)(before & 0xFFFFF);
+  if (tid < p.experts) first[tid] = (uint16_t)at;
   for (int g = 0; g < groups_up; ++g)
-    l.up[(int)(before >> 20 & 0xFFFFF) + g] = (uint32_t)e | (uint32_t)(first + g * p.up.cap) << 10 | (uint32_t)min(p.up.cap, count - g * p.up.cap) << 21;
+    l.up[(int)(before >> 20 & 0xFFFFF) + g] = (uint32_t)tid | (uint32_t)(at + g * p.up.cap) << 10 | (uint32_t)min(p.up.cap, all - g * p.up.cap) << 21;
   for (int g = 0; g < groups_down; ++g)
-    l.down[(int)(before >> 40) + g] = (uint32_t)e | (uint32_t)(first + g * p.down.cap) << 10 | (uint32_t)min(p.down.cap, count - g * p.down.cap) << 21;
-  if (e == 0) {
-    total[0] = (int)(all >> 20 & 0xFFFFF);
-    total[1] = (int)(all >> 40);
+    l.down[(int)(before >> 40) + g] = (uint32_t)tid | (uint32_t)(at + g * p.down.cap) << 10 | (uint32_t)min(p.down.cap, all - g * p.down.cap) << 21;
+  if (tid == 0) {
+    total[0] = (int)(sum >> 20 & 0xFFFFF);
+    total[1] = (int)(sum >> 40);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = tid + h * NT;
+    if (i < n) l.sorted[first[mine[h]] + count[(i >> 5) * p.experts + mine[h]] + rank[h]] = (uint16_t)i;
   }
   __syncthreads();
 }
@@ -319,13 +362,14 @@ struct Stream {
   int item, end, unit, lo, hi, tile;  // next to issue; units of the warp in an item; its tile within an item
   const uint8_t* src;                 // first row of the tile, null: past the matrix
   int put;                            // slot of the next one
-  __device__ void start(const Matrix& m, const uint32_t* groups, int n_groups) {
+  __device__ void start(const Params& p, const Matrix& m, const uint32_t* groups, int n_groups) {
+    stages = p.stages;
     const int warp = threadIdx.x >> 5, kw = NW / m.g, part = warp % kw, units = (m.k + S::UK - 1) / S::UK;
-    const long long all = (long long)n_groups * m.items;
+    const unsigned all = (unsigned)(n_groups * m.items);
     tile = warp / kw;
     lo = unit = part * units / kw;
     hi = (part + 1) * units / kw;
-    item = (int)(all * blockIdx.x / gridDim.x);
+    item = (int)(all * blockIdx.x / gridDim.x);  // (2^10 groups of 2^11 items on 2^10 CTAs at most)
     end = (int)(all * (blockIdx.x + 1) / gridDim.x);
     put = 0;
     place(m, groups);
@@ -334,6 +378,12 @@ struct Stream {
     if (item >= end) return;
     const int g = item / m.items, row = ((item - g * m.items) * m.g + tile) * S::RT;
     src = row < m.rows ? m.w + ((size_t)(groups[g] & 1023) * m.rows + row) * m.rb : nullptr;
+  }
+  int stages;
+  __device__ __forceinline__ void arrived() const {  // the oldest unit under way is there
+    if (stages == 8) cp_async_wait<7>();
+    else if (stages == 6) cp_async_wait<5>();
+    else cp_async_wait<3>();
   }
   __device__ __forceinline__ void issue(const Params& p, const Matrix& m, const uint32_t* groups, uint32_t ring) {
     while (item < end && (unit >= hi || !src)) {
@@ -370,7 +420,7 @@ struct Stream {
       ++unit;
     }
     cp_async_commit();
-    put = put + 1 == S::STAGES ? 0 : put + 1;
+    put = put + 1 == p.stages ? 0 : put + 1;
   }
 };
 
@@ -403,9 +453,9 @@ __device__ __forceinline__ void split(const float (&v)[8], uint4 (&b)[PARTS]) {
 __host__ __device__ constexpr int row_bytes(int k) { return (k + 63) / 64 * 128 + 64; }
 
 // ---- one unit: acc += 16 or 32 rows x TB blocks of eight columns ----------------------------------
-// x: shared-memory address of the lane's column in each block, of its first input; its Q parts lie a row apart.
+// x: the lane's column in each block; its Q parts lie a row apart.
 template <int FMT, int TB, int Q>
-__device__ __forceinline__ void multiply(const Params& p, const Matrix& m, uint32_t slot, const uint32_t (&x)[TB], int row_size,
+__device__ __forceinline__ void multiply(const Params& p, const Matrix& m, const unsigned char* slot, const unsigned char* const (&x)[TB], int row_size,
                                          int unit, float (&acc)[Shape<FMT>::TM][TB][4]) {
   using S = Shape<FMT>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -422,7 +472,7 @@ __device__ __forceinline__ void multiply(const Params& p, const Matrix& m, uint3
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int row = i * 16 + r * 8 + g;
-          const uint32_t w = lds32(slot + row * 32 + (s ^ (row >> 2 & 1)) * 16 + t * 4);
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(slot + row * 32 + (s ^ (row >> 2 & 1)) * 16 + t * 4);
           const uint32_t bias = 0x43084308u;  // 136 = 128 + 8: a nibble under the exponent of 128 reads 128 + q
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -435,7 +485,7 @@ __device__ __forceinline__ void multiply(const Params& p, const Matrix& m, uint3
       for (int n = 0; n < TB; ++n)
 #pragma unroll
         for (int q = Q - 1; q >= 0; --q) {  // (the instruction cuts its sums off: the small parts come first)
-          const uint4 b = lds128(x[n] + q * row_size + (unit * 64 + s * 32 + t * 8) * 2);
+          const uint4 b = *reinterpret_cast<const uint4*>(x[n] + q * row_size + (unit * 64 + s * 32 + t * 8) * 2);
 #pragma unroll
           for (int i = 0; i < 2; ++i) mma_bf16(d[i][n], a[i][0], b.x, b.y);
 #pragma unroll
@@ -447,7 +497,7 @@ __device__ __forceinline__ void multiply(const Params& p, const Matrix& m, uint3
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t sw = lds32(slot + S::RT * S::UB + s * S::RT * 4 + (i * 16 + r * 8 + g) * 4);
+          const uint32_t sw = *reinterpret_cast<const uint32_t*>(slot + S::RT * S::UB + s * S::RT * 4 + (i * 16 + r * 8 + g) * 4);
           const uint32_t sh = odd ? sw >> 16 : sw & 0xFFFFu;
           const float scale = p.scale_bf16 ? __uint_as_float(sh << 16) : __half2float(__ushort_as_half((unsigned short)sh));
 #pragma unroll
@@ -460,14 +510,14 @@ __device__ __forceinline__ void multiply(const Params& p, const Matrix& m, uint3
         }
     }
   } else {
-    const uint4 u = lds128(slot + g * 64 + t * 16), v = lds128(slot + (g + 8) * 64 + t * 16);
+    const uint4 u = *reinterpret_cast<const uint4*>(slot + g * 64 + t * 16), v = *reinterpret_cast<const uint4*>(slot + (g + 8) * 64 + t * 16);
     const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
 #pragma unroll
     for (int n = 0; n < TB; ++n) {
       float d[2][4] = {};  // (the instruction cuts its sums off: long ones are added rounded, and the small parts come first)
 #pragma unroll
       for (int q = Q - 1; q >= 0; --q) {
-        const uint4 b = lds128(x[n] + q * row_size + (unit * 32 + t * 8) * 2);
+        const uint4 b = *reinterpret_cast<const uint4*>(x[n] + q * row_size + (unit * 32 + t * 8) * 2);
         mma_bf16(d[0], a0, b.x, b.y);
         mma_bf16(d[1], a1, b.z, b.w);
       }
@@ -479,15 +529,20 @@ __device__ __forceinline__ void multiply(const Params& p, const Matrix& m, uint3
 
 // ---- a phase of products --------------------------------------------------------------------------
 // Walks over the CTA's items. Stage: brings a group's activations to shared memory where they are not there yet and names
-// the place of each there; Epilogue: takes the sums of (rows of an item, column). Up to eight parts of tokens are columns of one
+// the place of each there; Epilogue: takes a tile's sums, by the kw warps that share it. Up to eight parts of tokens are columns of one
 // block; of more tokens each is a column, and its parts follow one another in the same sum.
 template <int FMT, int PARTS, typename Stage, typename Epilogue>
-__device__ void products(const Params& p, const Matrix& m, const uint32_t* groups, Stream<FMT>& in, uint32_t ring, uint32_t acts,
-                         int row_size, float* red, Stage&& stage, Epilogue&& epilogue, int first, int last) {
+__device__ void products(const Params& p, const Matrix& m, const uint32_t* groups, Stream<FMT>& in, const unsigned char* ring_p,
+                         const unsigned char* acts, int row_size, float* red, Stage&& stage, Epilogue&& epilogue, int first, int last) {
   using S = Shape<FMT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int kw = NW / m.g, lo = in.lo, hi = in.hi;
+  const uint32_t ring = smem_addr(ring_p);
   int got = 0, group = -1;
+  auto meet = [&]() {  // the warps of a tile: others' tiles do not wait for it
+    if (kw > 1) named_sync(1 + in.tile, kw * 32);
+    else __syncwarp();
+  };
   for (int item = first; item < last; ++item) {
     const int now = item / m.items, it = item - now * m.items;
     const uint32_t entry = groups[now];
@@ -500,23 +555,23 @@ __device__ void products(const Params& p, const Matrix& m, const uint32_t* group
     float* mine = red + warp * COLS * S::RP;
     auto run = [&](auto blocks, auto packed) {
       constexpr int TB = decltype(blocks)::value, Q = decltype(packed)::value ? 1 : PARTS;
-      uint32_t x[TB];
+      const unsigned char* x[TB];
       float acc[S::TM][TB][4] = {};
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
         const int col = min(b * 8 + g, cols - 1);
-        x[b] = acts + (Q == PARTS ? stage.place(at, col) * PARTS : stage.place(at, col / PARTS) * PARTS + col % PARTS) * row_size;
+        x[b] = acts + (size_t)(Q == PARTS ? stage.place(at, col) * PARTS : stage.place(at, col / PARTS) * PARTS + col % PARTS) * row_size;
       }
       if (row0 < m.rows)
         for (int u = lo; u < hi; ++u) {
-          cp_async_wait<S::STAGES - 1>();
+          in.arrived();
           __syncwarp();
-          multiply<FMT, TB, Q>(p, m, ring + got * S::SLOT, x, row_size, u, acc);
+          multiply<FMT, TB, Q>(p, m, ring_p + got * S::SLOT, x, row_size, u, acc);
           __syncwarp();
           in.issue(p, m, groups, ring);
-          got = got + 1 == S::STAGES ? 0 : got + 1;
+          got = got + 1 == p.stages ? 0 : got + 1;
         }
-      __syncthreads();  // (the last item's sums have been read)
+      meet();  // (the last item's sums have been read)
 #pragma unroll
       for (int i = 0; i < S::TM; ++i)
 #pragma unroll
@@ -527,8 +582,8 @@ __device__ void products(const Params& p, const Matrix& m, const uint32_t* group
     if (n > 8) run(std::integral_constant<int, 2>{}, std::false_type{});
     else if (PARTS > 1 && n * PARTS <= 8) run(std::integral_constant<int, 1>{}, std::true_type{});
     else run(std::integral_constant<int, 1>{}, std::false_type{});
-    __syncthreads();
-    epilogue(it, at, n, kw, n * PARTS <= 8 ? PARTS : 1);
+    meet();
+    if (row0 < m.rows) epilogue(row0, at, n, kw, n * PARTS <= 8 ? PARTS : 1, red + in.tile * kw * COLS * S::RP, threadIdx.x - in.tile * kw * 32);
   }
 }
 
@@ -546,9 +601,10 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
   __shared__ int failed, total[2];
   __shared__ unsigned long long scan[NW];
   const int tid = threadIdx.x, warp = tid >> 5;
-  const uint32_t ring = smem_addr(smem + warp * S::STAGES * S::SLOT);
-  float* red = reinterpret_cast<float*>(smem + S::RING);
-  unsigned char* acts = smem + S::RING + S::RED;
+  const unsigned char* ring_p = smem + warp * p.stages * S::SLOT;
+  const uint32_t ring = smem_addr(ring_p);
+  float* red = reinterpret_cast<float*>(smem + NW * p.stages * S::SLOT);
+  unsigned char* acts = smem + NW * p.stages * S::SLOT + S::RED;
   const Lists lists(acts + p.b_bytes, p.tokens * p.top_k);
   if (tid == 0) failed = 0;
 
@@ -569,6 +625,7 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
   const int up_row = row_bytes(p.hidden);
   auto bring = [&](int n, auto which) {
     const int words = p.hidden / 8;
+#pragma unroll 4
     for (int i = tid; i < n * words; i += NT) {
       const int r = i / words, c = (i - r * words) * 8;
       float v[8];
@@ -589,14 +646,14 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
       if (p.weights) p.weights[i] = lists.weight[i];
     }
   }
-  sort_entries(p, lists, total, scan);
+  sort_entries(p, lists, total, scan, smem);
 
   // ---- gate and up
-  auto range = [&](const Matrix& m, int groups, int cta) { return (int)((long long)groups * m.items * cta / gridDim.x); };
+  auto range = [&](const Matrix& m, int groups, int cta) { return (int)((unsigned)(groups * m.items) * (unsigned)cta / gridDim.x); };
   Stream<FMT> in;
-  in.start(p.up, lists.up, total[0]);
+  in.start(p, p.up, lists.up, total[0]);
 #pragma unroll 1
-  for (int i = 0; i < S::STAGES; ++i) in.issue(p, p.up, lists.up, ring);
+  for (int i = 0; i < p.stages; ++i) in.issue(p, p.up, lists.up, ring);
   struct UpStage {
     const Params& p;
     const Lists& l;
@@ -610,22 +667,20 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
     __device__ int place(int at, int col) const { return p.resident ? l.sorted[at + col] / p.top_k : col; }
   } up_stage{p, lists, bring};
   products<FMT, UP_PARTS>(
-      p, p.up, lists.up, in, ring, smem_addr(acts), up_row, red, up_stage,
-      [&](int it, int at, int n, int kw, int each) {
+      p, p.up, lists.up, in, ring_p, acts, up_row, red, up_stage,
+      [&](int row0, int at, int n, int kw, int each, const float* sums, int thread) {
         constexpr int PAIRS = S::RT / 2;
-        for (int o = (tid + it * 64) & (NT - 1); o < p.up.g * PAIRS * n; o += NT) {
-          const int pair = o % PAIRS, rest = o / PAIRS, col = rest % n, tile = rest / n;
-          const int i = (it * p.up.g + tile) * PAIRS + pair;
-          if (i >= p.ffn) continue;
+        for (int o = thread; o < PAIRS * n; o += kw * 32) {
+          const int pair = o % PAIRS, col = o / PAIRS;
           float2 s = make_float2(0.f, 0.f);
           for (int q = each - 1; q >= 0; --q)
             for (int w = 0; w < kw; ++w) {
-              const float2 v = *reinterpret_cast<const float2*>(red + ((tile * kw + w) * COLS + col * each + q) * S::RP + 2 * pair);
+              const float2 v = *reinterpret_cast<const float2*>(sums + (w * COLS + col * each + q) * S::RP + 2 * pair);
               s.x += v.x;
               s.y += v.y;
             }
           const float e = expf(-fabsf(s.x));  // (of what does not overflow, so that far gates fade out and are not cut off)
-          p.h[(size_t)lists.sorted[at + col] * p.ffn + i] = (s.x < 0.f ? s.x * e : s.x) / (1.f + e) * s.y;
+          p.h[(size_t)lists.sorted[at + col] * p.ffn + row0 / 2 + pair] = (s.x < 0.f ? s.x * e : s.x) / (1.f + e) * s.y;
         }
       },
       range(p.up, total[0], blockIdx.x), range(p.up, total[0], blockIdx.x + 1));
@@ -634,9 +689,9 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
   cp_async_wait<0>();
   __syncwarp();
   grid_arrive(p, 1);
-  in.start(p.down, lists.down, total[1]);
+  in.start(p, p.down, lists.down, total[1]);
 #pragma unroll 1
-  for (int i = 0; i < S::STAGES; ++i) in.issue(p, p.down, lists.down, ring);
+  for (int i = 0; i < p.stages; ++i) in.issue(p, p.down, lists.down, ring);
   if (!grid_wait(p, 1, &failed)) {
     cp_async_wait<0>();
     return;
@@ -650,6 +705,7 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
     __device__ void operator()(int at, int n) {
       __syncthreads();
       const int words = p.ffn / 8;
+#pragma unroll 4
       for (int i = threadIdx.x; i < n * words; i += NT) {
         const int r = i / words, c = (i - r * words) * 8;
         const float4* src = reinterpret_cast<const float4*>(p.h + (size_t)l.sorted[at + r] * p.ffn + c);
@@ -665,16 +721,14 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
     __device__ int place(int, int col) const { return col; }
   } down_stage{p, lists, acts, down_row};
   products<FMT, DOWN_PARTS>(
-      p, p.down, lists.down, in, ring, smem_addr(acts), down_row, red, down_stage,
-      [&](int it, int at, int n, int kw, int each) {
-        for (int o = (tid + it * 64) & (NT - 1); o < p.down.g * S::RT * n; o += NT) {
-          const int row = o % S::RT, rest = o / S::RT, col = rest % n, tile = rest / n;
-          const int i = (it * p.down.g + tile) * S::RT + row;
-          if (i >= p.hidden) continue;
+      p, p.down, lists.down, in, ring_p, acts, down_row, red, down_stage,
+      [&](int row0, int at, int n, int kw, int each, const float* sums, int thread) {
+        for (int o = thread; o < S::RT * n; o += kw * 32) {
+          const int row = o % S::RT, col = o / S::RT;
           float s = 0.f;
           for (int q = each - 1; q >= 0; --q)
-            for (int w = 0; w < kw; ++w) s += red[((tile * kw + w) * COLS + col * each + q) * S::RP + row];
-          p.part[(size_t)lists.sorted[at + col] * p.hidden + i] = s;
+            for (int w = 0; w < kw; ++w) s += sums[(w * COLS + col * each + q) * S::RP + row];
+          p.part[(size_t)lists.sorted[at + col] * p.hidden + row0 + row] = s;
         }
       },
       range(p.down, total[1], blockIdx.x), range(p.down, total[1], blockIdx.x + 1));
@@ -792,16 +846,19 @@ tinfer_status run(const tinfer_moe* m, int tokens, int dtype, Params& p, cudaStr
   p.up = matrix(m->gu_packed, 2 * m->ffn_e, m->hidden);
   p.down = matrix(m->down_packed, m->hidden, m->ffn_e);
   const int entries = tokens * m->top_k, lists = Lists::bytes(entries);
-  const int room = (SMEM - 1024 - S::RING - S::RED - lists) / 128 * 128;
   const int up_row = row_bytes(m->hidden) * (dtype == TINFER_DTYPE_F32 ? parts_up<float>() : dtype == TINFER_DTYPE_F16 ? parts_up<__half>() : parts_up<__nv_bfloat16>());
   const int down_row = row_bytes(m->ffn_e) * (dtype == TINFER_DTYPE_F32 ? parts_down<float>() : parts_down<__half>());
-  p.up.cap = std::min(COLS, room / up_row);
-  p.down.cap = std::min(COLS, room / down_row);
+  // the ring takes what the activations leave: with four stages they have the most room, and deeper rings what they do not need
+  auto room = [&](int stages) { return (SMEM - 1024 - NW * stages * S::SLOT - S::RED - lists) / 128 * 128; };
+  p.up.cap = std::min(COLS, room(4) / up_row);
+  p.down.cap = std::min(COLS, room(4) / down_row);
   if (p.up.cap < 1 || p.down.cap < 1) return TINFER_ERR_UNSUPPORTED;
-  p.resident = tokens * up_row <= room;
+  p.resident = tokens * up_row <= room(4);
   if (p.resident) p.up.cap = COLS;
-  p.b_bytes = (int)align_up((size_t)std::max(p.resident ? tokens * up_row : p.up.cap * up_row, p.down.cap * down_row), 128);
-  const int smem = S::RING + S::RED + p.b_bytes + lists;
+  const int most = std::min(entries, COLS);  // tokens of an expert in one group
+  p.b_bytes = (int)align_up((size_t)std::max(p.resident ? tokens * up_row : std::min(most, p.up.cap) * up_row, std::min(most, p.down.cap) * down_row), 128);
+  for (p.stages = 8; p.stages > 4 && room(p.stages) < p.b_bytes;) p.stages -= 2;
+  const int smem = NW * p.stages * S::SLOT + S::RED + p.b_bytes + lists;
   const cudaError_t e = dtype == TINFER_DTYPE_F32   ? launch_t<FMT, float>(p, sms, smem, st)
                         : dtype == TINFER_DTYPE_F16 ? launch_t<FMT, __half>(p, sms, smem, st)
                                                     : launch_t<FMT, __nv_bfloat16>(p, sms, smem, st);
@@ -854,7 +911,7 @@ extern "C" tinfer_status tinfer_op_moe_layer(const tinfer_moe* m, int n_tokens, 
   p.ids = ids_dev;
   p.weights = weights_dev;
   p.sync = reinterpret_cast<unsigned*>(ws);
-  p.logits = reinterpret_cast<double*>(ws + s.logits);
+  p.logits = reinterpret_cast<float2*>(ws + s.logits);
   p.h = reinterpret_cast<float*>(ws + s.h);
   p.part = reinterpret_cast<float*>(ws + s.part);
   p.status = status_dev;
