@@ -43,10 +43,10 @@ constexpr int STATUS_TIMEOUT = 2;
 constexpr int WAIT_US = 200 * 1000, WAIT_US_WITHHELD = 5 * 1000;
 
 template <int FMT>
-struct Shape {  // a unit: TM * 16 rows of UB bytes (UK inputs), and two words of scales for each row
+struct Shape {  // a unit: TM * 16 rows of UB bytes (UK inputs in BLOCKS of 32), and two words of scales for each row
   static constexpr int TM = FMT == TINFER_INT4 ? 2 : 1;
   static constexpr int RT = 16 * TM;
-  static constexpr int UB = FMT == TINFER_INT4 ? 32 : 64, UK = FMT == TINFER_INT4 ? 64 : 32;
+  static constexpr int UB = FMT == TINFER_INT4 ? 64 : 128, UK = FMT == TINFER_INT4 ? 128 : 64, BLOCKS = UK / 32;
   static constexpr int SLOT = RT * UB + (FMT == TINFER_INT4 ? RT * 8 : 0);
   static constexpr int RP = RT + 4;  // column of a warp's sums, padded so that its lanes' stores meet no bank twice
   static constexpr int RED = NW * COLS * RP * 4;
@@ -57,11 +57,13 @@ struct Matrix {
   const uint8_t* w;
   int rows, rb, k;
   int g, items;  // tiles of an item, items of an expert
+  int chunks;    // 16-byte pieces of a row's weights
   int cap;       // tokens at a time
+  int lg_words;  // K / 8 rounded up to a power of two, its logarithm
 };
 
 struct Params {
-  Matrix up, down;
+  Matrix m[2];     // gate and up, down
   const void* router;
   int router_f32;
   const void* x;
@@ -70,6 +72,7 @@ struct Params {
   int accumulate;
   int tokens, experts, top_k, hidden, ffn, renormalise;
   int group, scale_bf16;
+  unsigned per_inv;  // 2^20 / (group / 32) and one more: block of 32 inputs * per_inv >> 20 is its scale
   int* ids;        // outputs, may be null
   float* weights;
   unsigned* sync;  // counters of the three barriers and of the CTAs that have left; 0 between calls
@@ -77,7 +80,7 @@ struct Params {
   float* h;        // [tokens * top_k][ffn]
   float* part;     // [tokens * top_k][hidden]
   int* status;
-  int stages;      // units of a warp under way: 4, 6 or 8
+  int stages;      // units of a warp under way: 3, 4 or 6
   int resident;    // all tokens stay in shared memory for the gate and up products
   int b_bytes;     // shared memory of the activations
   int wait_us, withhold;
@@ -157,7 +160,7 @@ __device__ void route(const Params& p, int expert, int m0) {
   Sum acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = Sum{0.f, 0.f};
-#pragma unroll 4
+#pragma unroll(N == 1 ? 4 : N == 2 ? 2 : 1)
   for (int c = lane * 8; c < p.hidden; c += 256) {
     float a[8], b[N][8];
     kv8::load8(w + c, a);
@@ -318,7 +321,7 @@ __device__ void sort_entries(const Params& p, const Lists& l, int* total, unsign
       count[r * p.experts + tid] = (uint16_t)all;
       all += c;
     }
-  const int groups_up = (all + p.up.cap - 1) / p.up.cap, groups_down = (all + p.down.cap - 1) / p.down.cap;
+  const int groups_up = (all + p.m[0].cap - 1) / p.m[0].cap, groups_down = (all + p.m[1].cap - 1) / p.m[1].cap;
   const unsigned long long own = (unsigned long long)all | (unsigned long long)groups_up << 20 | (unsigned long long)groups_down << 40;
   unsigned long long incl = own;
 #pragma unroll
@@ -338,9 +341,9 @@ __device__ void sort_entries(const Params& p, const Lists& l, int* total, unsign
   const int at = (int)(before & 0xFFFFF);
   if (tid < p.experts) first[tid] = (uint16_t)at;
   for (int g = 0; g < groups_up; ++g)
-    l.up[(int)(before >> 20 & 0xFFFFF) + g] = (uint32_t)tid | (uint32_t)(at + g * p.up.cap) << 10 | (uint32_t)min(p.up.cap, all - g * p.up.cap) << 21;
+    l.up[(int)(before >> 20 & 0xFFFFF) + g] = (uint32_t)tid | (uint32_t)(at + g * p.m[0].cap) << 10 | (uint32_t)min(p.m[0].cap, all - g * p.m[0].cap) << 21;
   for (int g = 0; g < groups_down; ++g)
-    l.down[(int)(before >> 40) + g] = (uint32_t)tid | (uint32_t)(at + g * p.down.cap) << 10 | (uint32_t)min(p.down.cap, all - g * p.down.cap) << 21;
+    l.down[(int)(before >> 40) + g] = (uint32_t)tid | (uint32_t)(at + g * p.m[1].cap) << 10 | (uint32_t)min(p.m[1].cap, all - g * p.m[1].cap) << 21;
   if (tid == 0) {
     total[0] = (int)(sum >> 20 & 0xFFFFF);
     total[1] = (int)(sum >> 40);
@@ -355,67 +358,50 @@ __device__ void sort_entries(const Params& p, const Lists& l, int* total, unsign
 }
 
 // ---- the stream of weights ------------------------------------------------------------------------
+__device__ __forceinline__ int scale_of(const Params& p, int block) { return (int)((unsigned)block * p.per_inv >> 20); }
+
 // A warp's units in order: those of its tile and inputs in each item of the CTA's run.
 template <int FMT>
 struct Stream {
   using S = Shape<FMT>;
-  int item, end, unit, lo, hi, tile;  // next to issue; units of the warp in an item; its tile within an item
-  const uint8_t* src;                 // first row of the tile, null: past the matrix
-  int put;                            // slot of the next one
-  __device__ void start(const Params& p, const Matrix& m, const uint32_t* groups, int n_groups) {
-    stages = p.stages;
-    const int warp = threadIdx.x >> 5, kw = NW / m.g, part = warp % kw, units = (m.k + S::UK - 1) / S::UK;
-    const unsigned all = (unsigned)(n_groups * m.items);
-    tile = warp / kw;
-    lo = unit = part * units / kw;
-    hi = (part + 1) * units / kw;
-    item = (int)(all * blockIdx.x / gridDim.x);  // (2^10 groups of 2^11 items on 2^10 CTAs at most)
-    end = (int)(all * (blockIdx.x + 1) / gridDim.x);
-    put = 0;
-    place(m, groups);
+  static constexpr int CHUNKS = S::UB / 16, ROWS = 32 / CHUNKS;  // 16-byte pieces of a row, rows that a warp copies at a time
+  int left, it, group, unit;  // items of the run from the next unit's on; its item within the expert, its group
+  const uint8_t* src;         // first row of its tile, null: past the matrix
+  int put;                    // its slot
+  // Byte of piece c of a row within a slot: exchanged so that a warp's reads of eight rows meet no bank twice.
+  static __device__ __forceinline__ int place_of(int row, int c) {
+    return row * S::UB + (FMT == TINFER_INT4 ? c ^ (row >> 1 & 3) : c ^ (row & 1) << 2) * 16;
   }
-  __device__ __forceinline__ void place(const Matrix& m, const uint32_t* groups) {
-    if (item >= end) return;
-    const int g = item / m.items, row = ((item - g * m.items) * m.g + tile) * S::RT;
-    src = row < m.rows ? m.w + ((size_t)(groups[g] & 1023) * m.rows + row) * m.rb : nullptr;
+  __device__ __forceinline__ void place(const Matrix& m, const uint32_t* groups, int tile) {
+    const int row = (it * m.g + tile) * S::RT;
+    src = left > 0 && row < m.rows ? m.w + ((size_t)(groups[group] & 1023) * m.rows + row) * m.rb : nullptr;
   }
-  int stages;
-  __device__ __forceinline__ void arrived() const {  // the oldest unit under way is there
-    if (stages == 8) cp_async_wait<7>();
-    else if (stages == 6) cp_async_wait<5>();
-    else cp_async_wait<3>();
-  }
-  __device__ __forceinline__ void issue(const Params& p, const Matrix& m, const uint32_t* groups, uint32_t ring) {
-    while (item < end && (unit >= hi || !src)) {
+  __device__ __forceinline__ void issue(const Params& p, const Matrix& m, const uint32_t* groups, uint32_t ring, int tile, int lo, int hi) {
+    while (left > 0 && (unit >= hi || !src)) {
       unit = lo;
-      ++item;
-      place(m, groups);
-      if (lo >= hi) item = end;  // (a warp without inputs)
+      --left;
+      if (++it == m.items) {
+        it = 0;
+        ++group;
+      }
+      place(m, groups, tile);
     }
-    if (item < end) {
-      const int lane = threadIdx.x & 31;
-      const uint32_t dst = ring + put * S::SLOT;
+    if (left > 0) {
+      const int lane = threadIdx.x & 31, row = lane / CHUNKS, c = lane % CHUNKS;
+      const uint32_t slot = ring + put * S::SLOT, dst = slot + place_of(row, c);
+      const uint8_t* from = src + unit * S::UB + row * m.rb + c * 16;
+      if (unit * CHUNKS + c < m.chunks) {  // (not past the row)
+#pragma unroll
+        for (int j = 0; j < S::RT / ROWS; ++j) {
+          cp_async_16(dst + j * ROWS * S::UB, from);
+          from += ROWS * m.rb;
+        }
+      }
       if (FMT == TINFER_INT4) {
-        const uint8_t* from = src + unit * S::UB;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int id = lane + 32 * j, row = id >> 1, c = id & 1;
-          cp_async_16(dst + row * 32 + (c ^ (row >> 2 & 1)) * 16, from + (size_t)row * m.rb + c * 16);
-        }
-        const uint8_t* scales = src + (size_t)lane * m.rb + m.k / 2;
-        const int per = p.group >> 5;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int block = min(2 * unit + s, m.k / 32 - 1);
-          cp_async_4(dst + S::RT * S::UB + s * S::RT * 4 + lane * 4, scales + (block / per & ~1) * 2);
-        }
-      } else {
-        const uint8_t* from = src + unit * S::UB;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int id = lane + 32 * j, row = id >> 2, c = id & 3;
-          cp_async_16(dst + row * 64 + c * 16, from + (size_t)row * m.rb + c * 16);
-        }
+        const uint8_t* scales = src + lane * m.rb + m.k / 2;
+        const int first = scale_of(p, 4 * unit) & ~1, last = scale_of(p, min(4 * unit + 3, m.chunks - 1)) & ~1;
+        cp_async_4(slot + S::RT * S::UB + lane * 4, scales + first * 2);
+        cp_async_4(slot + S::RT * S::UB + S::RT * 4 + lane * 4, scales + last * 2);
       }
       ++unit;
     }
@@ -423,6 +409,11 @@ struct Stream {
     put = put + 1 == p.stages ? 0 : put + 1;
   }
 };
+__device__ __forceinline__ void oldest_arrived(int stages) {
+  if (stages == 6) cp_async_wait<5>();
+  else if (stages == 4) cp_async_wait<3>();
+  else cp_async_wait<2>();
+}
 
 // ---- activations as operands ----------------------------------------------------------------------
 // Eight neighbouring inputs of a token as the second operand of two products, in PARTS bf16 parts whose sum they are. 4-bit
@@ -453,26 +444,25 @@ __device__ __forceinline__ void split(const float (&v)[8], uint4 (&b)[PARTS]) {
 __host__ __device__ constexpr int row_bytes(int k) { return (k + 63) / 64 * 128 + 64; }
 
 // ---- one unit: acc += 16 or 32 rows x TB blocks of eight columns ----------------------------------
-// x: the lane's column in each block; its Q parts lie a row apart.
-template <int FMT, int TB, int Q>
-__device__ __forceinline__ void multiply(const Params& p, const Matrix& m, const unsigned char* slot, const unsigned char* const (&x)[TB], int row_size,
-                                         int unit, float (&acc)[Shape<FMT>::TM][TB][4]) {
+// x: the lane's column in each block; its parts lie a row apart.
+template <int FMT, int TB, int PARTS>
+__device__ __forceinline__ void multiply(const Params& p, const Matrix& m, const unsigned char* slot, const unsigned char* const (&x)[2],
+                                         int row_size, int unit, float (&acc)[Shape<FMT>::TM][2][4]) {
   using S = Shape<FMT>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if constexpr (FMT == TINFER_INT4) {
-    const int per = p.group >> 5, first = 2 * unit / per;  // (blocks of 32 inputs to a scale)
-    const bool both = 2 * unit + 1 < m.k / 32, apart = (2 * unit + 1) / per != first;
+    const int first = scale_of(p, 4 * unit) & ~1;
     float d[2][TB][4] = {};
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (s && !both) break;
+    for (int s = 0; s < 4; ++s) {
+      const int block = 4 * unit + s;
+      if (block >= m.chunks) break;
       uint32_t a[2][2][4];  // [tile][product][operand register]
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = i * 16 + r * 8 + g;
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(slot + row * 32 + (s ^ (row >> 2 & 1)) * 16 + t * 4);
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(slot + Stream<FMT>::place_of(i * 16 + r * 8 + g, s) + t * 4);
           const uint32_t bias = 0x43084308u;  // 136 = 128 + 8: a nibble under the exponent of 128 reads 128 + q
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -482,23 +472,23 @@ __device__ __forceinline__ void multiply(const Params& p, const Matrix& m, const
           }
         }
 #pragma unroll
-      for (int n = 0; n < TB; ++n)
+      for (int q = PARTS - 1; q >= 0; --q)  // (the instruction cuts its sums off: the small parts come first)
 #pragma unroll
-        for (int q = Q - 1; q >= 0; --q) {  // (the instruction cuts its sums off: the small parts come first)
-          const uint4 b = *reinterpret_cast<const uint4*>(x[n] + q * row_size + (unit * 64 + s * 32 + t * 8) * 2);
+        for (int n = 0; n < TB; ++n) {
+          const uint4 b = *reinterpret_cast<const uint4*>(x[n] + q * row_size + (block * 32 + t * 8) * 2);
 #pragma unroll
           for (int i = 0; i < 2; ++i) mma_bf16(d[i][n], a[i][0], b.x, b.y);
 #pragma unroll
           for (int i = 0; i < 2; ++i) mma_bf16(d[i][n], a[i][1], b.z, b.w);
         }
-      if (s == 0 && both && !apart) continue;  // (one scale for the unit)
-      const bool odd = (s && apart ? (2 * unit + 1) / per : first) & 1;
+      const int scale_id = scale_of(p, block);
+      if ((s & 1) == 0 && block + 1 < m.chunks && scale_of(p, block + 1) == scale_id) continue;  // (64 products to an addition at most)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t sw = *reinterpret_cast<const uint32_t*>(slot + S::RT * S::UB + s * S::RT * 4 + (i * 16 + r * 8 + g) * 4);
-          const uint32_t sh = odd ? sw >> 16 : sw & 0xFFFFu;
+          const unsigned char* at = slot + S::RT * S::UB + ((scale_id & ~1) == first ? 0 : S::RT * 4) + (i * 16 + r * 8 + g) * 4;
+          const uint32_t sw = *reinterpret_cast<const uint32_t*>(at), sh = scale_id & 1 ? sw >> 16 : sw & 0xFFFFu;
           const float scale = p.scale_bf16 ? __uint_as_float(sh << 16) : __half2float(__ushort_as_half((unsigned short)sh));
 #pragma unroll
           for (int n = 0; n < TB; ++n)
@@ -510,80 +500,26 @@ __device__ __forceinline__ void multiply(const Params& p, const Matrix& m, const
         }
     }
   } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(slot + g * 64 + t * 16), v = *reinterpret_cast<const uint4*>(slot + (g + 8) * 64 + t * 16);
-    const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
 #pragma unroll
-    for (int n = 0; n < TB; ++n) {
-      float d[2][4] = {};  // (the instruction cuts its sums off: long ones are added rounded, and the small parts come first)
+    for (int s = 0; s < 2; ++s) {
+      if (unit * 8 + s * 4 >= m.chunks) break;
+      const uint4 u = *reinterpret_cast<const uint4*>(slot + Stream<FMT>::place_of(g, s * 4 + t)),
+                  v = *reinterpret_cast<const uint4*>(slot + Stream<FMT>::place_of(g + 8, s * 4 + t));
+      const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+      float d[TB][2][4] = {};  // (the instruction cuts its sums off: long ones are added rounded, and the small parts come first)
 #pragma unroll
-      for (int q = Q - 1; q >= 0; --q) {
-        const uint4 b = *reinterpret_cast<const uint4*>(x[n] + q * row_size + (unit * 32 + t * 8) * 2);
-        mma_bf16(d[0], a0, b.x, b.y);
-        mma_bf16(d[1], a1, b.z, b.w);
-      }
+      for (int q = PARTS - 1; q >= 0; --q)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[0][n][r] += d[0][r] + d[1][r];
-    }
-  }
-}
-
-// ---- a phase of products --------------------------------------------------------------------------
-// Walks over the CTA's items. Stage: brings a group's activations to shared memory where they are not there yet and names
-// the place of each there; Epilogue: takes a tile's sums, by the kw warps that share it. Up to eight parts of tokens are columns of one
-// block; of more tokens each is a column, and its parts follow one another in the same sum.
-template <int FMT, int PARTS, typename Stage, typename Epilogue>
-__device__ void products(const Params& p, const Matrix& m, const uint32_t* groups, Stream<FMT>& in, const unsigned char* ring_p,
-                         const unsigned char* acts, int row_size, float* red, Stage&& stage, Epilogue&& epilogue, int first, int last) {
-  using S = Shape<FMT>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int kw = NW / m.g, lo = in.lo, hi = in.hi;
-  const uint32_t ring = smem_addr(ring_p);
-  int got = 0, group = -1;
-  auto meet = [&]() {  // the warps of a tile: others' tiles do not wait for it
-    if (kw > 1) named_sync(1 + in.tile, kw * 32);
-    else __syncwarp();
-  };
-  for (int item = first; item < last; ++item) {
-    const int now = item / m.items, it = item - now * m.items;
-    const uint32_t entry = groups[now];
-    const int n = (int)(entry >> 21), at = (int)(entry >> 10 & 2047);
-    if (now != group) {
-      stage(at, n);
-      group = now;
-    }
-    const int row0 = (it * m.g + in.tile) * S::RT, cols = n * PARTS <= 8 ? n * PARTS : n;
-    float* mine = red + warp * COLS * S::RP;
-    auto run = [&](auto blocks, auto packed) {
-      constexpr int TB = decltype(blocks)::value, Q = decltype(packed)::value ? 1 : PARTS;
-      const unsigned char* x[TB];
-      float acc[S::TM][TB][4] = {};
-#pragma unroll
-      for (int b = 0; b < TB; ++b) {
-        const int col = min(b * 8 + g, cols - 1);
-        x[b] = acts + (size_t)(Q == PARTS ? stage.place(at, col) * PARTS : stage.place(at, col / PARTS) * PARTS + col % PARTS) * row_size;
-      }
-      if (row0 < m.rows)
-        for (int u = lo; u < hi; ++u) {
-          in.arrived();
-          __syncwarp();
-          multiply<FMT, TB, Q>(p, m, ring_p + got * S::SLOT, x, row_size, u, acc);
-          __syncwarp();
-          in.issue(p, m, groups, ring);
-          got = got + 1 == p.stages ? 0 : got + 1;
+        for (int n = 0; n < TB; ++n) {
+          const uint4 b = *reinterpret_cast<const uint4*>(x[n] + q * row_size + (unit * 64 + s * 32 + t * 8) * 2);
+          mma_bf16(d[n][0], a0, b.x, b.y);
+          mma_bf16(d[n][1], a1, b.z, b.w);
         }
-      meet();  // (the last item's sums have been read)
 #pragma unroll
-      for (int i = 0; i < S::TM; ++i)
+      for (int n = 0; n < TB; ++n)
 #pragma unroll
-        for (int b = 0; b < TB; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) mine[(b * 8 + 2 * t + (r & 1)) * S::RP + i * 16 + g + (r >> 1) * 8] = acc[i][b][r];
-    };
-    if (n > 8) run(std::integral_constant<int, 2>{}, std::false_type{});
-    else if (PARTS > 1 && n * PARTS <= 8) run(std::integral_constant<int, 1>{}, std::true_type{});
-    else run(std::integral_constant<int, 1>{}, std::false_type{});
-    meet();
-    if (row0 < m.rows) epilogue(row0, at, n, kw, n * PARTS <= 8 ? PARTS : 1, red + in.tile * kw * COLS * S::RP, threadIdx.x - in.tile * kw * 32);
+        for (int r = 0; r < 4; ++r) acc[0][n][r] += d[n][0][r] + d[n][1][r];
+    }
   }
 }
 
@@ -621,22 +557,33 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
   }
   grid_arrive(p, 0);
 
-  // tokens as rows of shared memory; `which` names the token of a place
-  const int up_row = row_bytes(p.hidden);
-  auto bring = [&](int n, auto which) {
-    const int words = p.hidden / 8;
-#pragma unroll 4
-    for (int i = tid; i < n * words; i += NT) {
-      const int r = i / words, c = (i - r * words) * 8;
+  // activations to shared memory: places 0 .. n - 1, of which `which` names the token or the entry
+  auto bring = [&](int phase, int n, auto which) {
+    const Matrix& m = p.m[phase];
+    const int size = row_bytes(m.k);
+#pragma unroll 2
+    for (int i = tid; i < n << m.lg_words; i += NT) {
+      const int r = i >> m.lg_words, c = (i & ((1 << m.lg_words) - 1)) * 8;
+      if (c >= m.k) continue;
       float v[8];
-      uint4 b[UP_PARTS];
-      kv8::load8(static_cast<const XT*>(p.x) + which(r) * p.x_stride + c, v);
-      split<FMT, UP_PARTS>(v, b);
+      if (phase == 0) {
+        kv8::load8(static_cast<const XT*>(p.x) + which(r) * p.x_stride + c, v);
+        uint4 b[UP_PARTS];
+        split<FMT, UP_PARTS>(v, b);
 #pragma unroll
-      for (int q = 0; q < UP_PARTS; ++q) *reinterpret_cast<uint4*>(acts + (size_t)(r * UP_PARTS + q) * up_row + c * 2) = b[q];
+        for (int q = 0; q < UP_PARTS; ++q) *reinterpret_cast<uint4*>(acts + (size_t)(r * UP_PARTS + q) * size + c * 2) = b[q];
+      } else {
+        const float4* src = reinterpret_cast<const float4*>(p.h + (size_t)which(r) * p.ffn + c);
+        const float4 u = __ldcg(src), w = __ldcg(src + 1);
+        const float z[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+        uint4 b[DOWN_PARTS];
+        split<FMT, DOWN_PARTS>(z, b);
+#pragma unroll
+        for (int q = 0; q < DOWN_PARTS; ++q) *reinterpret_cast<uint4*>(acts + (size_t)(r * DOWN_PARTS + q) * size + c * 2) = b[q];
+      }
     }
   };
-  if (p.resident) bring(p.tokens, [](int r) { return r; });
+  if (p.resident) bring(0, p.tokens, [](int r) { return r; });
   if (!grid_wait(p, 0, &failed)) return;
 
   choose(p, lists);
@@ -648,99 +595,149 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
   }
   sort_entries(p, lists, total, scan, smem);
 
-  // ---- gate and up
-  auto range = [&](const Matrix& m, int groups, int cta) { return (int)((unsigned)(groups * m.items) * (unsigned)cta / gridDim.x); };
-  Stream<FMT> in;
-  in.start(p, p.up, lists.up, total[0]);
+  // ---- gate and up, then down
 #pragma unroll 1
-  for (int i = 0; i < p.stages; ++i) in.issue(p, p.up, lists.up, ring);
-  struct UpStage {
-    const Params& p;
-    const Lists& l;
-    decltype(bring)& load;
-    __device__ void operator()(int at, int n) {
-      if (p.resident) return;
-      __syncthreads();
-      load(n, [&](int r) { return l.sorted[at + r] / p.top_k; });
-      __syncthreads();
-    }
-    __device__ int place(int at, int col) const { return p.resident ? l.sorted[at + col] / p.top_k : col; }
-  } up_stage{p, lists, bring};
-  products<FMT, UP_PARTS>(
-      p, p.up, lists.up, in, ring_p, acts, up_row, red, up_stage,
-      [&](int row0, int at, int n, int kw, int each, const float* sums, int thread) {
-        constexpr int PAIRS = S::RT / 2;
-        for (int o = thread; o < PAIRS * n; o += kw * 32) {
-          const int pair = o % PAIRS, col = o / PAIRS;
-          float2 s = make_float2(0.f, 0.f);
-          for (int q = each - 1; q >= 0; --q)
-            for (int w = 0; w < kw; ++w) {
-              const float2 v = *reinterpret_cast<const float2*>(sums + (w * COLS + col * each + q) * S::RP + 2 * pair);
-              s.x += v.x;
-              s.y += v.y;
-            }
-          const float e = expf(-fabsf(s.x));  // (of what does not overflow, so that far gates fade out and are not cut off)
-          p.h[(size_t)lists.sorted[at + col] * p.ffn + row0 / 2 + pair] = (s.x < 0.f ? s.x * e : s.x) / (1.f + e) * s.y;
+  for (int phase = 0; phase < 2; ++phase) {
+    const Matrix& m = p.m[phase];
+    const uint32_t* groups = phase ? lists.down : lists.up;
+    const int lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int kw = NW / m.g, tile = warp / kw, units = (m.k + S::UK - 1) / S::UK, size = row_bytes(m.k), all_parts = phase ? DOWN_PARTS : UP_PARTS;
+    const int lo = warp % kw * units / kw, hi = (warp % kw + 1) * units / kw;
+    const unsigned all = (unsigned)(total[phase] * m.items);  // (2^10 groups of 2^11 items on 2^10 CTAs at most)
+    const int first = (int)(all * blockIdx.x / gridDim.x), last = (int)(all * (blockIdx.x + 1) / gridDim.x);
+    Stream<FMT> in;
+    in.group = first / m.items;
+    in.it = first - in.group * m.items;
+    in.left = lo < hi ? last - first : 0;
+    in.unit = lo;
+    in.put = 0;
+    in.place(m, groups, tile);
+    auto meet = [&]() {  // the warps of a tile: others' tiles do not wait for it
+      if (kw > 1) named_sync(1 + tile, kw * 32);
+      else __syncwarp();
+    };
+    // the item at work (it of the expert's, for n entries from `at` on), the next unit and the end of those here
+    int group = in.group, it = in.it - 1, left = last - first + 1, unit = 0, end = 0, got = 0, n = 0, at = 0, parts = 1, row0 = 0, named = -1;
+    const unsigned char* x[2] = {acts, acts};
+    float acc[S::TM][2][4];
+    float* mine = red + warp * COLS * S::RP;
+    const float* sums = red + tile * kw * COLS * S::RP;
+#pragma unroll 1
+    for (int step = -p.stages;; ++step) {  // (the first fill the ring)
+      if (step >= 0) {
+        if (step == 0) {
+if (phase && !grid_wait(p, 1, &failed)) {
+            cp_async_wait<0>();
+            return;
+          }
         }
-      },
-      range(p.up, total[0], blockIdx.x), range(p.up, total[0], blockIdx.x + 1));
-
-  // ---- down; its first weights come while the others finish
-  cp_async_wait<0>();
-  __syncwarp();
-  grid_arrive(p, 1);
-  in.start(p, p.down, lists.down, total[1]);
-#pragma unroll 1
-  for (int i = 0; i < p.stages; ++i) in.issue(p, p.down, lists.down, ring);
-  if (!grid_wait(p, 1, &failed)) {
-    cp_async_wait<0>();
-    return;
-  }
-  const int down_row = row_bytes(p.ffn);
-  struct DownStage {
-    const Params& p;
-    const Lists& l;
-    unsigned char* acts;
-    int row_size;
-    __device__ void operator()(int at, int n) {
-      __syncthreads();
-      const int words = p.ffn / 8;
-#pragma unroll 4
-      for (int i = threadIdx.x; i < n * words; i += NT) {
-        const int r = i / words, c = (i - r * words) * 8;
-        const float4* src = reinterpret_cast<const float4*>(p.h + (size_t)l.sorted[at + r] * p.ffn + c);
-        const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
-        const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        uint4 b[DOWN_PARTS];
-        split<FMT, DOWN_PARTS>(v, b);
+        while (unit >= end) {
+          if (n) {  // an item ends: the sums of the tile's warps meet
+            meet();  // (the last item's have been read)
 #pragma unroll
-        for (int q = 0; q < DOWN_PARTS; ++q) *reinterpret_cast<uint4*>(acts + (size_t)(r * DOWN_PARTS + q) * row_size + c * 2) = b[q];
-      }
-      __syncthreads();
-    }
-    __device__ int place(int, int col) const { return col; }
-  } down_stage{p, lists, acts, down_row};
-  products<FMT, DOWN_PARTS>(
-      p, p.down, lists.down, in, ring_p, acts, down_row, red, down_stage,
-      [&](int row0, int at, int n, int kw, int each, const float* sums, int thread) {
-        for (int o = thread; o < S::RT * n; o += kw * 32) {
-          const int row = o % S::RT, col = o / S::RT;
-          float s = 0.f;
-          for (int q = each - 1; q >= 0; --q)
-            for (int w = 0; w < kw; ++w) s += sums[(w * COLS + col * each + q) * S::RP + row];
-          p.part[(size_t)lists.sorted[at + col] * p.hidden + row0 + row] = s;
+            for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                if (b == 0 || n > 8) {
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) mine[(b * 8 + 2 * t + (r & 1)) * S::RP + i * 16 + g + (r >> 1) * 8] = acc[i][b][r];
+                }
+            meet();
+            const int each = parts == all_parts ? 1 : all_parts, thread = tid - tile * kw * 32;
+            if (row0 < m.rows) {
+              if (phase == 0) {
+                constexpr int PAIRS = S::RT / 2;
+#pragma unroll 1
+                for (int o = thread; o < PAIRS * n; o += kw * 32) {
+                  const int pair = o % PAIRS, col = o / PAIRS;
+                  float2 s = make_float2(0.f, 0.f);
+                  for (int q = each - 1; q >= 0; --q)
+#pragma unroll 4
+                    for (int w = 0; w < kw; ++w) {
+                      const float2 v = *reinterpret_cast<const float2*>(sums + (w * COLS + col * each + q) * S::RP + 2 * pair);
+                      s.x += v.x;
+                      s.y += v.y;
+                    }
+                  const float e = expf(-fabsf(s.x));  // (of what does not overflow, so that far gates fade out and are not cut off)
+                  p.h[(size_t)lists.sorted[at + col] * p.ffn + row0 / 2 + pair] = (s.x < 0.f ? s.x * e : s.x) / (1.f + e) * s.y;
+                }
+              } else {
+#pragma unroll 1
+                for (int o = thread; o < S::RT * n; o += kw * 32) {
+                  const int row = o % S::RT, col = o / S::RT;
+                  float s = 0.f;
+                  for (int q = each - 1; q >= 0; --q)
+#pragma unroll 4
+                    for (int w = 0; w < kw; ++w) s += sums[(w * COLS + col * each + q) * S::RP + row];
+                  p.part[(size_t)lists.sorted[at + col] * p.hidden + row0 + row] = s;
+                }
+              }
+            }
+          }
+          if (--left == 0) break;
+          if (++it == m.items) {
+            it = 0;
+            ++group;
+          }
+          if (group != named) {  // its tokens: up to eight parts of them are columns of one block, of more each token is one
+            named = group;
+            n = (int)(groups[group] >> 21);
+            at = (int)(groups[group] >> 10 & 2047);
+            const bool here = phase == 0 && p.resident, packed = n * all_parts <= 8;
+            if (!here) {
+              __syncthreads();
+              if (phase == 0) bring(0, n, [&](int r) { return lists.sorted[at + r] / p.top_k; });
+              else bring(1, n, [&](int r) { return lists.sorted[at + r]; });
+              __syncthreads();
+            }
+            parts = packed ? 1 : all_parts;
+            const int cols = packed ? n * all_parts : n;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int col = min(b * 8 + g, cols - 1), tok = packed ? col / all_parts : col;
+              x[b] = acts + (size_t)((here ? lists.sorted[at + tok] / p.top_k : tok) * all_parts + (packed ? col - tok * all_parts : 0)) * size;
+            }
+          }
+          row0 = (it * m.g + tile) * S::RT;
+          unit = lo;
+          end = row0 < m.rows ? hi : lo;
+#pragma unroll
+          for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[i][b][r] = 0.f;
         }
-      },
-      range(p.down, total[1], blockIdx.x), range(p.down, total[1], blockIdx.x + 1));
-  cp_async_wait<0>();
-  grid_arrive(p, 2);
+        if (left == 0) break;
+oldest_arrived(p.stages);
+        __syncwarp();
+        const unsigned char* slot = ring_p + got * S::SLOT;
+        if (parts == 1) {
+          if (n <= 8) multiply<FMT, 1, 1>(p, m, slot, x, size, unit, acc);
+          else if (UP_PARTS == 1) multiply<FMT, 2, 1>(p, m, slot, x, size, unit, acc);
+        } else {
+          if (n <= 8) multiply<FMT, 1, DOWN_PARTS>(p, m, slot, x, size, unit, acc);
+          else multiply<FMT, 2, DOWN_PARTS>(p, m, slot, x, size, unit, acc);
+        }
+        __syncwarp();
+        ++unit;
+        got = got + 1 == p.stages ? 0 : got + 1;
+      }
+      in.issue(p, m, groups, ring, tile, lo, hi);
+    }
+cp_async_wait<0>();
+    __syncwarp();
+    grid_arrive(p, 1 + phase);  // (the down products' first weights come while other CTAs are still at the gate and up products)
+  }
   if (!grid_wait(p, 2, &failed)) return;
 
   // ---- each token's sum, its experts in order
   const int words = p.hidden / 4;
+#pragma unroll 1
   for (int i = blockIdx.x * NT + tid; i < p.tokens * words; i += gridDim.x * NT) {
     const int t = i / words, c = (i - t * words) * 4;
     float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int s = 0; s < p.top_k; ++s) {
       const int e = t * p.top_k + s;
       const float w = lists.weight[e];
@@ -841,23 +838,25 @@ tinfer_status run(const tinfer_moe* m, int tokens, int dtype, Params& p, cudaStr
     x.rb = (int)packed_row_bytes(m->weight_format, k, m->group_size);
     x.g = tiles_of_item((k + S::UK - 1) / S::UK, rows / S::RT, std::min(tokens * m->top_k, m->n_experts), sms);
     x.items = (rows / S::RT + x.g - 1) / x.g;
+    x.chunks = FMT == TINFER_INT4 ? k / 32 : k / 8;
+    while ((8 << x.lg_words) < k) ++x.lg_words;
     return x;
   };
-  p.up = matrix(m->gu_packed, 2 * m->ffn_e, m->hidden);
-  p.down = matrix(m->down_packed, m->hidden, m->ffn_e);
+  p.m[0] = matrix(m->gu_packed, 2 * m->ffn_e, m->hidden);
+  p.m[1] = matrix(m->down_packed, m->hidden, m->ffn_e);
   const int entries = tokens * m->top_k, lists = Lists::bytes(entries);
   const int up_row = row_bytes(m->hidden) * (dtype == TINFER_DTYPE_F32 ? parts_up<float>() : dtype == TINFER_DTYPE_F16 ? parts_up<__half>() : parts_up<__nv_bfloat16>());
   const int down_row = row_bytes(m->ffn_e) * (dtype == TINFER_DTYPE_F32 ? parts_down<float>() : parts_down<__half>());
-  // the ring takes what the activations leave: with four stages they have the most room, and deeper rings what they do not need
+  // the ring takes what the activations leave: with three stages they have the most room, and deeper rings what they do not need
   auto room = [&](int stages) { return (SMEM - 1024 - NW * stages * S::SLOT - S::RED - lists) / 128 * 128; };
-  p.up.cap = std::min(COLS, room(4) / up_row);
-  p.down.cap = std::min(COLS, room(4) / down_row);
-  if (p.up.cap < 1 || p.down.cap < 1) return TINFER_ERR_UNSUPPORTED;
-  p.resident = tokens * up_row <= room(4);
-  if (p.resident) p.up.cap = COLS;
+  p.m[0].cap = std::min(COLS, room(3) / up_row);
+  p.m[1].cap = std::min(COLS, room(3) / down_row);
+  if (p.m[0].cap < 1 || p.m[1].cap < 1) return TINFER_ERR_UNSUPPORTED;
+  p.resident = tokens * up_row <= room(3);
+  if (p.resident) p.m[0].cap = COLS;
   const int most = std::min(entries, COLS);  // tokens of an expert in one group
-  p.b_bytes = (int)align_up((size_t)std::max(p.resident ? tokens * up_row : std::min(most, p.up.cap) * up_row, std::min(most, p.down.cap) * down_row), 128);
-  for (p.stages = 8; p.stages > 4 && room(p.stages) < p.b_bytes;) p.stages -= 2;
+  p.b_bytes = (int)align_up((size_t)std::max(p.resident ? tokens * up_row : std::min(most, p.m[0].cap) * up_row, std::min(most, p.m[1].cap) * down_row), 128);
+  p.stages = room(6) >= p.b_bytes ? 6 : room(4) >= p.b_bytes ? 4 : 3;
   const int smem = NW * p.stages * S::SLOT + S::RED + p.b_bytes + lists;
   const cudaError_t e = dtype == TINFER_DTYPE_F32   ? launch_t<FMT, float>(p, sms, smem, st)
                         : dtype == TINFER_DTYPE_F16 ? launch_t<FMT, __half>(p, sms, smem, st)
@@ -907,6 +906,7 @@ extern "C" tinfer_status tinfer_op_moe_layer(const tinfer_moe* m, int n_tokens, 
   p.ffn = m->ffn_e;
   p.renormalise = (m->flags & TINFER_MOE_RENORMALISE) != 0;
   p.group = m->weight_format == TINFER_INT4 ? m->group_size : 32;
+  p.per_inv = (1u << 20) / (unsigned)(p.group / 32) + 1;
   p.scale_bf16 = m->scale_dtype == TINFER_SCALE_BF16;
   p.ids = ids_dev;
   p.weights = weights_dev;
