@@ -40,7 +40,7 @@ EXPORTS = [
     "tinfer_op_attention_noalloc", "tinfer_op_gemv_batch", "tinfer_moe_packed_bytes", "tinfer_pack_moe", "tinfer_op_moe",
     "tinfer_op_gemm_bf16", "tinfer_op_kv8_append", "tinfer_op_kv8_read", "tinfer_kv8_attention_workspace",
     "tinfer_op_kv8_attention", "tinfer_op_logprobs", "tinfer_op_qk_norm_rope",
-    "tinfer_moe_layer_workspace", "tinfer_op_moe_layer",
+    "tinfer_moe_layer_workspace", "tinfer_op_moe_layer", "tinfer_op_sample",
 ]
 
 
@@ -83,6 +83,11 @@ class tinfer_moe(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in (
         "weight_format", "group_size", "scale_dtype", "n_experts", "top_k", "hidden", "ffn_e", "router_dtype", "flags")] + [
         (n, ctypes.c_void_p) for n in ("router", "gu_packed", "down_packed")]
+
+
+class tinfer_sampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int), ("top_p", ctypes.c_float), ("min_p", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("temperature_dev", "top_k_dev", "top_p_dev", "min_p_dev")]
 
 
 _lib = None
@@ -135,6 +140,7 @@ def lib():
             "tinfer_op_qk_norm_rope": ([I, I, I, I, I, I, rowp, rowp, P, P, D, D, P, P, rowp, rowp, P, P], I),
             "tinfer_moe_layer_workspace": ([moep, I], Z),
             "tinfer_op_moe_layer": ([moep, I, I, P, LL, P, LL, I, P, P, P, Z, P, P], I),
+            "tinfer_op_sample": ([I, I, I, P, LL, P, ctypes.POINTER(tinfer_sampling), P, P, P], I),
             "tinfer_op_logprobs": ([I, I, I, P, LL, P, I, P, P, P, P, P], I),
         }
         for name, (args, res) in sig.items():
@@ -353,6 +359,11 @@ def tinfer_op_moe_layer(layer: tinfer_moe, n_tokens, dtype, x, x_stride, y, y_st
                         workspace_bytes, status=None, stream=None) -> int:
     return lib().tinfer_op_moe_layer(layer, n_tokens, dtype, _ptr(x), x_stride, _ptr(y), y_stride, int(accumulate), _ptr(ids),
                                      _ptr(weights), _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream))
+
+
+def tinfer_op_sample(rows, vocab, dtype, logits, row_stride, u, sampling: tinfer_sampling, ids, logp=None, stream=None) -> int:
+    return lib().tinfer_op_sample(rows, vocab, dtype, _ptr(logits), row_stride, _ptr(u), sampling, _ptr(ids), _ptr(logp),
+                                  _stream(stream))
 
 
 def make_config(c: dict, exec_mode: int = TINFER_MEGAKERNEL) -> tinfer_config:
@@ -872,3 +883,36 @@ class MoeLayer:
               (c, n, dtype, x.data_ptr(), x.stride(0), out.data_ptr(), out.stride(0), int(accumulate), ids.data_ptr(),
                weights.data_ptr(), workspace.data_ptr(), workspace.numel(), word), self.device, stream)
         return out, ids, weights
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, stream=None):
+    """(ids, logp) of the next token of each row of logits [rows, vocab], drawn from the numbers u, float32 [rows] in [0, 1)
+    (tinfer_op_sample): int32 ids and the logarithms of their shares of the weights that temperature, top_k, top_p and min_p leave.
+    Each of these is a number, or a tensor [rows] (int32 for top_k, float32 for the others) with one for each row. out: (ids, logp)
+    to write to instead of new tensors; its logp may be None."""
+    import torch
+    if logits.dim() != 2 or logits.stride(1) != 1 or logits.device.type != "cuda":
+        raise ValueError("logits: [rows, vocab] on a CUDA device with contiguous rows is wanted")
+    rows, vocab = logits.shape
+    dev, dtype = logits.device, _dtype(logits)
+
+    def words(what, t, dt):
+        if t.dtype != dt or t.shape != (rows,) or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{what}: a contiguous {dt} tensor [{rows}] on {dev} is wanted")
+        return t.data_ptr()
+
+    s = tinfer_sampling(1.0, 0, 1.0, 0.0)
+    for what, v in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p)):
+        if isinstance(v, torch.Tensor):
+            setattr(s, what + "_dev", words(what, v, torch.int32 if what == "top_k" else torch.float32))
+        else:
+            setattr(s, what, min(int(v), 0x7FFFFFFF) if what == "top_k" else float(v))
+    if out is None:
+        with _making(stream, dev):
+            out = torch.empty(rows, dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.float32, device=dev)
+    ids, logp = out
+    args = (rows, vocab, dtype, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, words("u", u, torch.float32), s,
+            words("out[0]", ids, torch.int32), None if logp is None else words("out[1]", logp, torch.float32))
+    if rows:  # (else nothing to launch)
+        _call("tinfer_op_sample", lib().tinfer_op_sample, args, dev, stream)
+    return ids, logp

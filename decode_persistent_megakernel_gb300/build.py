@@ -12,7 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtinfer.so")
 SOURCES = ["mega_bf16.cu", "mega_int4.cu", "kernels.cu", "api.cu", "gemm.cu", "kv8.cu", "kv8_attn.cu", "kv8_prefill.cu",
-           "logprobs.cu", "head_norm.cu", "moe_layer.cu"]
+           "logprobs.cu", "head_norm.cu", "moe_layer.cu", "sample.cu"]
 HEADERS = ["engine.h", "kernels.h", "ptx.cuh", "step.cuh", "megakernel.cuh", "kv8.cuh", "kv8_attn.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,792 @@
+// sample.cu -- the next token of each row of logits, drawn with temperature, top-k, top-p and min-p from a given number.
+//
+//   w_i = e^((x_i - max x) / T);  kept: the first k in order of value (equal ones by the lower id), of these the ones before
+//   which less than p of their sum lies, of these the ones with w >= min_p;  drawn: the first id, in the vocabulary's order, at
+//   which the kept weights' sum exceeds u times their total
+//
+// Which token that is hangs on sums of up to 2^18 weights whose borders lie 1e-6 apart, so weights are whole numbers in
+// units of 2^-45 of the largest, each known to 2^-37 of itself (two-part fp32 arithmetic: the device's fp64 rate is
+// a hundredth of it), and sums are exact: a draw is that of 64-bit arithmetic but for u within some 1e-11 of a border, and does
+// not depend on the order of additions.
+//
+// A row is one CTA's, or, where rows are few, a cluster's of up to 8 in slices. One pass finds the maximum. With top-k, the
+// k-th largest of the threads' maxima is a floor that few others reach: those are listed, sorted and resolved in the first CTA.
+// Without it, a pass counts the logits by their distance from the maximum, which places the border of the nucleus to a few
+// bins; a second pass adds the weights above them exactly and lists those within, whose order decides. Lists that overflow (thousands
+// of equal logits at a border) fall back to a search of the border bit by bit. The drawn token is found by the slices' sums, a
+// warp's, and then its words'. The passes after the first read from L2; the weights' 50 instructions a logit bound them.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "tinfer.h"
+
+namespace cg = cooperative_groups;
+
+namespace tinfer {
+namespace sample {
+
+using u64 = unsigned long long;
+constexpr int NT = 512, NWARPS = NT / 32, MAX_CLUSTER = 8;
+constexpr int MAX_VOCAB = 1 << 18;
+constexpr int LIST = 2048;           // listed candidates of a row, at most
+constexpr int BINS = 2048;           // of the distance from the maximum, in units of log2 of the weight
+constexpr float PER_LOG2 = 51.2f;    // bins to a factor of two: weights down to 2^-40 are told apart
+constexpr float WINDOW = 1.f / 512;  // of the sum, either side of the nucleus' border: bins' own weights are known to 0.7% at worst
+static_assert(LIST == 4 * NT && BINS == 4 * NT, "four to a thread");
+
+struct Params {
+  const void* logits;
+  long long row_stride;
+  const float* u;
+  tinfer_sampling s;
+  int* ids;
+  float* logp;  // may be null
+  int rows, vocab, slice;
+};
+
+struct Smem {
+  unsigned hist[BINS];
+  u64 key[LIST], mass[LIST];        // the first CTA's list; `mass` also a CTA's own candidates before they go there
+  float2 table[64];                 // 2^(i / 64) in two parts
+  u64 sums[MAX_CLUSTER][NWARPS];    // kept weights of each warp of the cluster (in the first CTA)
+  u64 red[NWARPS], cross[2][MAX_CLUSTER];
+  float redf[NWARPS], crossf[MAX_CLUSTER];
+  uint16_t owner[NT];
+  int owners, own, listed, count[2];
+  unsigned floor_key;
+  int lo, hi, rank, warp;
+  u64 tau, rest, total_s;  // tau: (key, ~id) of the last token kept
+  float ch, cl;
+  u64 least;                        // weights below are not kept
+};
+
+// Logits as whole numbers in their order, zeros of both signs equal; above 0 for all.
+__device__ __forceinline__ unsigned ordered(float x) {
+  const unsigned b = __float_as_uint(x + 0.f);
+  return b >> 31 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(unsigned u) { return __uint_as_float(u >> 31 ? u & 0x7FFFFFFFu : ~u); }
+__device__ __forceinline__ u64 pair_of(float x, int id) { return (u64)ordered(x) << 32 | (unsigned)~id; }
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// e^((x - m) / T) in units of 2^-45, rounded. ch + cl = log2(e) / T. The difference is taken in two parts (Knuth), and so its
+// product with ch + cl; its 64ths of a power of two come from the table, the rest r <= 2^-7 from four terms of the exponential's
+// series: e^(a + ra) - 1 = a + q with a = r ln 2 rounded. Off by 2^-37.5 of itself at most.
+__device__ __forceinline__ u64 weight(float x, float m, float ch, float cl, const float2* table) {
+  const float d = __fsub_rn(x, m), b = __fsub_rn(d, x);
+  const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(m, b));
+  const float p = __fmul_rn(d, ch);
+  const float e = fmaf(dl, ch, fmaf(d, cl, fmaf(d, ch, -p)));
+  constexpr float ROUND = 196608.f;  // 1.5 * 2^17: adding it leaves whole 64ths
+  const float t = __fadd_rn(p, ROUND), f = __fsub_rn(p, __fsub_rn(t, ROUND));
+  const int k = __float_as_int(t) - __float_as_int(ROUND);
+  constexpr float L = 0.693147182f, LL = -1.90465421e-9f;  // ln 2 in two parts
+  const float a = __fmul_rn(f, L);
+  const float ra = fmaf(e, L, fmaf(f, LL, fmaf(f, L, -a)));
+  const float g = __fmul_rn(__fmul_rn(a, a), fmaf(a, fmaf(a, 1.f / 24, 1.f / 6), 0.5f));  // e^a - 1 - a
+  const float q = __fadd_rn(g, fmaf(ra, __fadd_rn(a, g), ra));
+  const float2 h = table[k & 63];
+  const float pa = __fmul_rn(h.x, a);
+  const float lo = __fadd_rn(fmaf(h.y, a, fmaf(h.x, q, h.y)), fmaf(h.x, a, -pa));
+  const float u = __fadd_rn(pa, lo), ul = __fsub_rn(lo, __fsub_rn(u, pa));
+  // h.x + u + ul as a whole number of 2^-45: u to 2^-23 by adding 1.5, what is left to 2^-45 by adding 1.5 * 2^-22
+  const float s = __fadd_rn(u, 1.5f), s2 = __fadd_rn(__fadd_rn(__fsub_rn(u, __fsub_rn(s, 1.5f)), ul), 3.57627869e-7f);
+  const int high = __float_as_int(h.x) - 0x3F800000 + 0x800000 + (__float_as_int(s) - 0x3FC00000);
+  const long long w = ((long long)high << 22) + (__float_as_int(s2) - 0x34C00000);
+  const int shift = min(-(k >> 6), 63);  // (far ones, whose k means nothing, give 0)
+  return p > -46.5f ? (u64)((w * 2 >> shift) + 1) >> 1 : 0ull;
+}
+__device__ __noinline__ u64 weight_once(float x, float m, float ch, float cl, const float2* table) { return weight(x, m, ch, cl, table); }
+
+__device__ __forceinline__ int bin_of(float x, float m, float ch) {
+  return (int)fminf((m - x) * ch * PER_LOG2, (float)(BINS - 1));
+}
+
+__device__ __forceinline__ void unpack(const uint4& w, float (&x)[4], const float*) {
+  x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void unpack(const uint4& w, float (&x)[8], const __half*) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void unpack(const uint4& w, float (&x)[8], const __nv_bfloat16*) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+// The slice of a CTA as 16-byte words, from that of its first element to that of its last; of the words at its ends only the
+// slice's own elements are read, the others stand for masked tokens. Each warp has a run of `per` words.
+template <typename T>
+struct Slice {
+  static constexpr int N = 16 / sizeof(T);
+  const T* x;
+  const uint4* base;
+  int a, len, mis, words, per;
+  __device__ Slice(const T* row, int from, int n) : x(row), a(from), len(n) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(row + from);
+    mis = (int)(p & 15) / (int)sizeof(T);
+    words = n ? (mis + n + N - 1) / N : 0;
+    per = (words + NWARPS - 1) / NWARPS;
+    base = reinterpret_cast<const uint4*>(p & ~(uintptr_t)15);
+  }
+  __device__ __forceinline__ uint4 word(int w) const {
+    if (w * N >= mis && (w + 1) * N <= mis + len) return __ldg(base + w);
+    union {
+      uint4 u;
+      T e[N];
+    } y;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = w * N + i - mis;
+      y.e[i] = at >= 0 && at < len ? x[a + at] : (T)(-INFINITY);
+    }
+    return y.u;
+  }
+  __device__ __forceinline__ int id(int w, int i) const { return a + w * N + i - mis; }
+  __device__ __forceinline__ int first(int warp) const { return min(warp * per, words); }
+  // f(logit, id) for the words [w0, w1) of a warp, a word to a lane, AHEAD under way
+  template <int AHEAD, typename F>
+  __device__ __forceinline__ void walk(int w0, int w1, F&& f) const {
+#pragma unroll 1
+    for (int w = w0 + (threadIdx.x & 31); w < w1; w += 32 * AHEAD) {
+      uint4 y[AHEAD];
+#pragma unroll
+      for (int h = 0; h < AHEAD; ++h)
+        if (w + 32 * h < w1) y[h] = word(w + 32 * h);
+#pragma unroll
+      for (int h = 0; h < AHEAD; ++h) {
+        if (w + 32 * h >= w1) break;
+        float v[N];
+        unpack(y[h], v, x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f(v[i], id(w + 32 * h, i));
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+// Inclusive sums over the threads of a CTA.
+__device__ u64 block_scan(u64 v, u64* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const u64 y = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();
+  if (lane == 31) red[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) v += red[w];
+  return v;
+}
+// Sorts n (a power of two) numbers, the largest first.
+__device__ __noinline__ void sort_down(u64* a, int n) {
+  for (int size = 2; size <= n; size *= 2)
+    for (int step = size / 2; step; step /= 2) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < n / 2; i += NT) {
+        const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
+        const u64 x = a[lo], y = a[hi];
+        if ((x < y) == ((lo & size) == 0)) {
+          a[lo] = y;
+          a[hi] = x;
+        }
+      }
+    }
+  __syncthreads();
+}
+
+template <typename T>
+struct Draw {
+  const Params& q;
+  Smem& sm;
+  cg::cluster_group cluster;
+  const Slice<T> in;
+  int rank, size, row, tid, lane, warp, parity;
+  float m, ch, cl, temperature;
+  u64 tau;    // tokens with (key, ~id) from here on are kept
+  u64 least;  // of these the ones with weights from here on
+
+  __device__ Draw(const Params& p, Smem& s, const Slice<T>& slice, int r)
+      : q(p), sm(s), cluster(cg::this_cluster()), in(slice), rank((int)cluster.block_rank()), size((int)cluster.num_blocks()), row(r),
+        tid(threadIdx.x), lane(tid & 31), warp(tid >> 5), parity(0), tau(0) {}
+  __device__ __forceinline__ void meet() {
+    if (size > 1) cluster.sync();
+    else __syncthreads();
+  }
+  template <typename V>
+  __device__ __forceinline__ V* in_first(V* p) { return size > 1 ? cluster.map_shared_rank(p, 0) : p; }
+  template <typename V>
+  __device__ __forceinline__ void tell(V* p, V v) {  // to every CTA, by one thread
+    for (int r = 0; r < size; ++r) *(size > 1 ? cluster.map_shared_rank(p, r) : p) = v;
+  }
+  __device__ u64 sum(u64 v) {  // over the cluster
+    v = warp_sum(v);
+    __syncthreads();
+    if (lane == 0) sm.red[warp] = v;
+    __syncthreads();
+    if (tid == 0) {
+      u64 all = 0;
+      for (int w = 0; w < NWARPS; ++w) all += sm.red[w];
+      tell(&sm.cross[parity][rank], all);
+    }
+    meet();
+    u64 all = 0;
+    for (int r = 0; r < size; ++r) all += sm.cross[parity][r];
+    parity ^= 1;
+    return all;
+  }
+  __device__ __forceinline__ bool kept(float x, int id) const { return pair_of(x, id) >= tau; }
+  // What a token adds: its weight if it is kept (KIND 0), one if it has this key (KIND 1)
+  __device__ __forceinline__ u64 measure(int kind, unsigned key, float x, int id) const {
+    if (x == -INFINITY || !kept(x, id)) return 0;
+    if (kind) return ordered(x) == key;
+    const u64 w = weight_once(x, m, ch, cl, sm.table);
+    return w >= least ? w : 0;
+  }
+  // The sums of the warps' runs, to the first CTA.
+  __device__ __noinline__ void tally(int kind, unsigned key) {
+    u64 s = 0;
+    in.template walk<1>(in.first(warp), in.first(warp + 1), [&](float x, int id) { s += measure(kind, key, x, id); });
+    s = warp_sum(s);
+    meet();
+    if (lane == 0) in_first(&sm.sums[rank][warp])[0] = s;
+    meet();
+  }
+  // The token at which the tallied sums exceed `target`: f(id, its part, the total) is called by one thread of the cluster.
+  template <typename F>
+  __device__ __forceinline__ void find(int kind, unsigned key, u64 target, F&& f) {
+    if (warp == 0) {
+      u64 s[4], before = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = lane * 4 + i;
+        s[i] = e < size * NWARPS ? in_first(&sm.sums[0][0])[e] : 0;
+        before += s[i];
+      }
+      const u64 mine = before;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const u64 y = __shfl_up_sync(~0u, before, o);
+        if (lane >= o) before += y;
+      }
+      before -= mine;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (before <= target && target < before + s[i]) {
+          sm.rank = (lane * 4 + i) / NWARPS;
+          sm.warp = (lane * 4 + i) % NWARPS;
+          sm.rest = target - before;
+        }
+        before += s[i];
+      }
+    }
+    __syncthreads();
+    if (rank != sm.rank) return;
+    // that warp's run, dealt out to all of the CTA; then one warp walks over its part
+    int w0 = in.first(sm.warp), w1 = in.first(sm.warp + 1);
+    const int per = (w1 - w0 + NWARPS - 1) / NWARPS;
+    u64 s = 0;
+    in.template walk<1>(min(w0 + warp * per, w1), min(w0 + (warp + 1) * per, w1), [&](float x, int id) { s += measure(kind, key, x, id); });
+    s = warp_sum(s);
+    if (lane == 0) sm.red[warp] = s;
+    __syncthreads();
+    u64 rest = sm.rest;
+    int part = 0;
+    while (part < NWARPS - 1 && rest >= sm.red[part]) rest -= sm.red[part++];
+    if (warp != part) return;
+    const int end = min(w0 + (part + 1) * per, w1);
+#pragma unroll 1
+    for (int w = w0 + part * per; w < end; w += 32) {
+      float v[Slice<T>::N];
+      u64 own = 0;
+      if (w + lane < end) {
+        unpack(in.word(w + lane), v, in.x);
+#pragma unroll 1
+        for (int i = 0; i < Slice<T>::N; ++i) own += measure(kind, key, v[i], in.id(w + lane, i));
+      }
+      u64 incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const u64 y = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned over = __ballot_sync(~0u, incl > rest);
+      if (!over) {
+        rest -= __shfl_sync(~0u, incl, 31);
+        continue;
+      }
+      if (lane == __ffs(over) - 1) {
+        u64 left = rest - (incl - own);
+        for (int i = 0; i < Slice<T>::N; ++i) {
+          const u64 s1 = measure(kind, key, v[i], in.id(w + lane, i));
+          if (left < s1) {
+            f(in.id(w + lane, i), s1);
+            break;
+          }
+          left -= s1;
+        }
+      }
+      break;
+    }
+  }
+  // The border, bit by bit: the last kept token is the one at which the count (or the weights) of the kept ones reaches
+  // `limit`. For lists that overflow.
+  __device__ __noinline__ void search(bool mass, u64 limit) {
+    auto measured = [&](unsigned from) {
+      u64 s = 0;
+      in.template walk<1>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
+        if (x > -INFINITY && kept(x, id) && ordered(x) >= from) s += mass ? weight_once(x, m, ch, cl, sm.table) : 1;
+      });
+      return sum(s);
+    };
+    if (measured(0) < limit) return;  // all
+    unsigned key = 0;
+    for (int bit = 31; bit >= 0; --bit)
+      if (measured(key | 1u << bit) >= limit) key |= 1u << bit;
+    const u64 above = key == 0xFFFFFFFFu ? 0 : measured(key + 1);
+    const u64 each = mass ? weight_once(unordered(key), m, ch, cl, sm.table) : 1;
+    const u64 nth = (limit - above - 1) / each;  // of the tokens with this key, in order
+    tally(1, key);
+    find(1, key, nth, [&](int id, u64) { tell(&sm.tau, (u64)key << 32 | (unsigned)~id); });
+    meet();
+    tau = sm.tau;
+  }
+  // A CTA's candidates (in sm.mass) to the first CTA's list; the row's number of them.
+  __device__ __forceinline__ int collect() {
+    __syncthreads();
+    const int n = sm.own;
+    if (tid == 0) sm.count[1] = n ? atomicAdd(in_first(&sm.listed), n) : 0;
+    __syncthreads();
+    const int at = sm.count[1];
+    u64* list = in_first(sm.key);
+    if (n <= LIST)
+      for (int i = tid; i < n; i += NT)
+        if (at + i < LIST) list[at + i] = sm.mass[i];
+    meet();
+    const int all = *in_first(&sm.listed);
+    meet();  // (it may be cleared again)
+    return all;
+  }
+  // All tallied sums.
+  __device__ __forceinline__ u64 tallied() {
+    if (warp == 0) {
+      u64 s = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += lane + 32 * i < size * NWARPS ? in_first(&sm.sums[0][0])[lane + 32 * i] : 0;
+      s = warp_sum(s);
+      if (lane == 0) sm.total_s = s;
+    }
+    __syncthreads();
+    return sm.total_s;
+  }
+  __device__ __forceinline__ void take(float x, int id) {
+    const int i = atomicAdd(&sm.own, 1);
+    if (i < LIST) sm.mass[i] = pair_of(x, id);
+  }
+  // In the first CTA: the list of n sorted, weights of its first `use` in sm.mass, the thread's four inclusive sums.
+  __device__ __forceinline__ int resolve(int n, int use, u64 (&incl)[4]) {
+    int pow2 = 64;
+    while (pow2 < n) pow2 *= 2;
+    for (int i = n + tid; i < pow2; i += NT) sm.key[i] = 0;
+    sort_down(sm.key, pow2);
+    u64 s = 0;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const int e = tid * 4 + i;
+      const u64 w = e < use ? weight_once(unordered((unsigned)(sm.key[e] >> 32)), m, ch, cl, sm.table) : 0;
+      if (e < LIST) sm.mass[e] = w;
+      s += w;
+    }
+    u64 at = block_scan(s, sm.red) - s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) incl[i] = at += sm.mass[tid * 4 + i];
+    return pow2;
+  }
+  __device__ __forceinline__ void write(int id, u64 w, u64 total) {
+    q.ids[row] = id;
+    if (!q.logp) return;
+    // of a likely token by its distance from 1, of others by the logit, so that small and large results have their own bits
+    const float missing = (float)(total - w) / (float)total;
+    q.logp[row] = missing < 0.5f ? log1pf(-missing)
+                                 : -((m - (float)in.x[id]) / fminf(fmaxf(temperature, 1e-30f), 1e30f) + logf((float)total * 2.842170943e-14f));  // 2^-45
+  }
+  __device__ void run();
+};
+
+// A fraction of a sum: floor and whether something was cut off. f in [0, 1).
+__device__ __forceinline__ u64 part_of(float f, u64 total, bool& more) {
+  const u64 x = __float2ull_rz(f * 18446744073709551616.f);
+  more = x * total != 0;
+  return __umul64hi(x, total);
+}
+
+template <typename T>
+__device__ __forceinline__ void Draw<T>::run() {
+  // ---- the row's request
+  temperature = q.s.temperature_dev ? q.s.temperature_dev[row] : q.s.temperature;
+  const int k_given = q.s.top_k_dev ? q.s.top_k_dev[row] : q.s.top_k;
+  const float p = q.s.top_p_dev ? q.s.top_p_dev[row] : q.s.top_p, low = q.s.min_p_dev ? q.s.min_p_dev[row] : q.s.min_p;
+  float u = q.u[row];
+  u = u > 0.f ? u : 0.f;  // (NaN too)
+  const int k = k_given > 0 && k_given < q.vocab ? k_given : 0;
+  const bool nucleus = p < 1.f;
+  if (tid < 64) {
+    const double v = exp2(tid / 64.0);
+    const float h = (float)v;
+    sm.table[tid] = make_float2(h, (float)(v - (double)h));
+  }
+  if (tid == 64) {
+    const double c = 1.4426950408889634074 / (double)fminf(fmaxf(temperature, 1e-30f), 1e30f);
+    sm.ch = (float)c;
+    sm.cl = (float)(c - (double)sm.ch);
+    sm.least = low > 0.f ? (u64)ceil((double)fminf(low, 1.f) * 35184372088832.0) : 0;  // 2^45
+  }
+  if (tid == 0) {
+    sm.own = sm.listed = sm.owners = sm.warp = 0;
+    sm.rank = -1;
+  }
+  for (int i = tid; i < BINS; i += NT) sm.hist[i] = 0;
+
+  // ---- the maximum
+  float mine = -INFINITY;
+  in.template walk<4>(in.first(warp), in.first(warp + 1), [&](float x, int) { mine = max_nan(mine, x); });
+  float top = mine;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+  if (lane == 0) sm.redf[warp] = top;
+  __syncthreads();
+  for (int w = 0; w < NWARPS; ++w) top = max_nan(top, sm.redf[w]);
+  meet();  // (every CTA has started)
+  if (tid == 0) tell(&sm.crossf[rank], top);
+  meet();
+  m = sm.crossf[0];
+  for (int r = 1; r < size; ++r) m = max_nan(m, sm.crossf[r]);
+  ch = sm.ch;
+  cl = sm.cl;
+  least = sm.least;
+  if (!(fabsf(m) < INFINITY) || !(temperature >= 0.f)) {  // nothing to draw from
+    if (rank == 0 && tid == 0) {
+      q.ids[row] = -1;
+      if (q.logp) q.logp[row] = __uint_as_float(0x7FC00000u);
+    }
+    return;
+  }
+  if (temperature == 0.f) {  // the likeliest
+    tally(1, ordered(m));
+    find(1, ordered(m), 0, [&](int id, u64) { write(id, 1, 1); });
+    return;
+  }
+
+  // ---- few candidates: those from a floor on, in a list of the first CTA
+  bool few = k ? k <= NT * size : least && !nucleus;
+  if (few) {
+    unsigned floor_key = 1;
+    if (k) {
+      // the k-th largest of the threads' maxima, to 16 bits, is reached by k tokens
+      unsigned* all = reinterpret_cast<unsigned*>(in_first(sm.mass));
+      all[rank * NT + tid] = mine > -INFINITY ? ordered(mine) : 0;
+      meet();
+      if (rank == 0) {
+        unsigned own[MAX_CLUSTER], key = 0;
+        for (int r = 0; r < MAX_CLUSTER; ++r) own[r] = r < size ? reinterpret_cast<unsigned*>(sm.mass)[r * NT + tid] : 0;
+#pragma unroll 1
+        for (int bit = 31; bit >= 16; --bit) {
+          const unsigned from = key | 1u << bit;
+          int n = 0;
+#pragma unroll
+          for (int r = 0; r < MAX_CLUSTER; ++r) n += own[r] >= from;
+          n = (int)__reduce_add_sync(~0u, (unsigned)n);
+          if (lane == 0) sm.red[warp] = (u64)n;
+          __syncthreads();
+          n = 0;
+#pragma unroll
+          for (int w = 0; w < NWARPS; ++w) n += (int)sm.red[w];
+          if (n >= k) key = from;
+          __syncthreads();
+        }
+        if (tid == 0) tell(&sm.floor_key, key > 1u ? key : 1u);
+      }
+      meet();
+      floor_key = sm.floor_key;
+    }
+    // with min-p alone: the tokens whose weights may reach it
+    const float reach = k ? INFINITY : (fmaxf(-log2f(fminf(low, 1.f)), 0.f) + 1e-3f) / ch;
+    auto candidate = [&](float x) { return x > -INFINITY && ordered(x) >= floor_key && m - x <= reach; };
+    if (candidate(mine)) sm.owner[atomicAdd(&sm.owners, 1)] = (uint16_t)tid;
+    __syncthreads();
+    const int turns = (in.per + 31) / 32;
+    for (int item = tid; item < sm.owners * turns; item += NT) {
+      const int o = sm.owner[item / turns], w = in.first(o >> 5) + (o & 31) + item % turns * 32;
+      if (w >= in.first((o >> 5) + 1)) continue;
+      float v[Slice<T>::N];
+      unpack(in.word(w), v, in.x);
+#pragma unroll
+      for (int i = 0; i < Slice<T>::N; ++i)
+        if (candidate(v[i])) take(v[i], in.id(w, i));
+    }
+    const int n = collect();
+    few = n <= LIST;
+    if (few) {
+      if (rank) return;  // (nothing more is written to the others' memory)
+      const int use = k ? min(k, n) : n;
+      u64 incl[4];
+      const int pow2 = resolve(n, use, incl);
+      if (tid == (use - 1) / 4) sm.total_s = incl[(use - 1) % 4];
+      __syncthreads();
+      u64 limit = ~0ull;
+      if (nucleus) {
+        bool more;
+        limit = p > 0.f ? part_of(p, sm.total_s, more) : 0;
+        if (p > 0.f && more) ++limit;
+        limit = limit ? limit : 1;
+      }
+      int keep = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = tid * 4 + i;
+        const u64 w = sm.mass[e];
+        keep += e < use && incl[i] - w < limit && (w >= least || e == 0);
+      }
+      keep = (int)block_scan((u64)keep, sm.red);
+      if (tid == NT - 1) sm.count[0] = keep;
+      __syncthreads();
+      keep = sm.count[0];
+      if (tid == (keep - 1) / 4) sm.total_s = incl[(keep - 1) % 4];
+      // the kept ones in the vocabulary's order: sorted by ~id, with their places
+      for (int i = tid; i < pow2; i += NT) sm.key[i] = i < keep ? (u64)(unsigned)sm.key[i] << 32 | (unsigned)i : 0;
+      int small = 64;
+      while (small < keep) small *= 2;
+      sort_down(sm.key, small);
+      const u64 total = sm.total_s;
+      bool more;
+      const u64 target = part_of(fminf(u, 0.99999994f), total, more);
+      u64 s = 0, w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = tid * 4 + i;
+        w[i] = e < keep ? sm.mass[(unsigned)sm.key[e]] : 0;
+        s += w[i];
+      }
+      u64 at = block_scan(s, sm.red) - s;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (at <= target && target < at + w[i]) write((int)~(unsigned)(sm.key[tid * 4 + i] >> 32), w[i], total);
+        at += w[i];
+      }
+      return;
+    }
+    if (tid == 0) sm.own = 0;
+    if (rank == 0 && tid == 0) sm.listed = 0;
+    meet();
+  }
+
+  // ---- many: the nucleus' border to a few bins
+  if (k) search(false, (u64)k);
+  int lo = BINS, hi = BINS;
+  if (nucleus) {
+    in.template walk<2>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
+      if (x > -INFINITY && kept(x, id)) atomicAdd(&sm.hist[bin_of(x, m, ch)], 1u);
+    });
+    __syncthreads();
+    if (rank) {
+      unsigned* all = in_first(sm.hist);
+      for (int i = tid; i < BINS; i += NT)
+        if (sm.hist[i]) atomicAdd(all + i, sm.hist[i]);
+    }
+    meet();
+    if (rank == 0) {
+      float w[4], s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += w[i] = (float)sm.hist[tid * 4 + i] * exp2f(-((float)(tid * 4 + i) + 0.5f) / PER_LOG2);
+      float incl = s;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const float y = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) sm.redf[warp] = incl;
+      if (tid == 0) sm.lo = sm.hi = BINS - 1;
+      __syncthreads();
+      float all = 0.f;
+      for (int i = 0; i < NWARPS; ++i) {
+        if (i < warp) incl += sm.redf[i];
+        all += sm.redf[i];
+      }
+      float at = incl - s;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        at += w[i];
+        if (at >= (p - WINDOW) * all) atomicMin(&sm.lo, tid * 4 + i);
+        if (at >= (p + WINDOW) * all) atomicMin(&sm.hi, tid * 4 + i);
+      }
+      __syncthreads();
+      const int a = sm.lo, b = sm.hi;
+      __syncthreads();
+      if (tid == 0) {
+        tell(&sm.lo, a);
+        tell(&sm.hi, b);
+      }
+    }
+    meet();
+    lo = sm.lo;
+    hi = sm.hi;
+  }
+
+  // ---- the weights: all, those above the border's bins, and of these what min-p keeps; the tokens within the bins
+  u64 all = 0, above = 0, keep = 0;
+  in.template walk<1>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
+    if (!kept(x, id)) return;
+    const u64 w = weight(x, m, ch, cl, sm.table);
+    all += w;
+    const int b = nucleus ? bin_of(x, m, ch) : 0;
+    if (b < lo) {
+      above += w;
+      keep += w >= least ? w : 0;
+    } else if (b <= hi && x > -INFINITY) {
+      take(x, id);
+    }
+  });
+  keep = warp_sum(keep);
+  if (lane == 0) in_first(&sm.sums[rank][warp])[0] = keep;
+  if (nucleus) {
+    all = sum(all);
+    above = sum(above);
+    bool more;
+    u64 limit = p > 0.f ? part_of(p, all, more) : 0;
+    if (p > 0.f && more) ++limit;
+    limit = limit ? limit : 1;
+    const int n = collect();
+    if (rank == 0) {
+      bool found = n <= LIST && n > 0 && above < limit;
+      if (found) {
+        u64 incl[4];
+        resolve(n, n, incl);
+        int inside = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) inside += tid * 4 + i < n && above + incl[i] - sm.mass[tid * 4 + i] < limit;
+        inside = (int)block_scan((u64)inside, sm.red);
+        if (tid == NT - 1) {
+          sm.count[0] = inside;
+          sm.total_s = incl[3];
+        }
+        __syncthreads();
+        inside = sm.count[0];
+        found = inside < n || hi == BINS - 1 || above + sm.total_s >= limit;
+        if (found) {
+          // their weights belong to the warps that hold them
+          for (int i = tid; i < inside; i += NT) {
+            if (sm.mass[i] < least) continue;
+            const int id = (int)~(unsigned)sm.key[i], r = id / q.slice;
+            const Slice<T> s(in.x, r * q.slice, min(q.slice, q.vocab - r * q.slice));
+            atomicAdd(&sm.sums[r][(s.mis + id - s.a) / Slice<T>::N / s.per], sm.mass[i]);
+          }
+          if (tid == 0) tell(&sm.tau, sm.key[inside - 1]);
+        }
+      }
+      if (tid == 0 && !found) tell(&sm.tau, (u64)0);
+      __syncthreads();
+    }
+    meet();
+    if (sm.tau) {
+      tau = sm.tau;
+    } else {
+      search(true, limit);
+      tally(0, 0);
+    }
+  } else {
+    meet();
+  }
+
+  // ---- the draw
+  const u64 total = tallied();
+  bool more;
+  find(0, 0, part_of(fminf(u, 0.99999994f), total, more), [&](int id, u64 w) { write(id, w, total); });
+}
+
+template <typename T>
+__global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ Params q) {
+  __shared__ Smem sm;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks(), row = (int)(blockIdx.x / size);
+  const int a = min(rank * q.slice, q.vocab), len = min(q.slice, q.vocab - a);
+  Draw<T> d(q, sm, Slice<T>(static_cast<const T*>(q.logits) + row * q.row_stride, a, len), row);
+  d.run();
+  if (size > 1) cluster.sync();  // no CTA leaves while others use its memory
+}
+
+template <typename T>
+cudaError_t launch(const Params& q, int cluster, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(q.rows * cluster));
+  cfg.blockDim = dim3(NT);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, q);
+}
+
+}  // namespace sample
+}  // namespace tinfer
+
+using namespace tinfer;
+
+extern "C" tinfer_status tinfer_op_sample(int rows, int vocab, int dtype, const void* logits_dev, long long row_stride,
+                                          const float* u_dev, const tinfer_sampling* sampling, int32_t* ids_dev, float* logp_dev,
+                                          void* stream) {
+  if (rows < 1 || vocab < 1 || !logits_dev || !u_dev || !sampling || !ids_dev || row_stride < 0 || row_stride > (1LL << 40))
+    return TINFER_ERR_INVALID_ARG;
+  const int size = dtype == TINFER_DTYPE_F32 ? 4 : dtype == TINFER_DTYPE_F16 || dtype == TINFER_DTYPE_BF16 ? 2 : 0;
+  if (!size || reinterpret_cast<uintptr_t>(logits_dev) % size) return TINFER_ERR_INVALID_ARG;
+  const tinfer_sampling& s = *sampling;
+  for (const void* p : {(const void*)u_dev, (const void*)ids_dev, (const void*)logp_dev, (const void*)s.temperature_dev,
+                        (const void*)s.top_k_dev, (const void*)s.top_p_dev, (const void*)s.min_p_dev})
+    if (reinterpret_cast<uintptr_t>(p) & 3) return TINFER_ERR_INVALID_ARG;
+  if (!s.temperature_dev && !(s.temperature >= 0.f)) return TINFER_ERR_INVALID_ARG;
+  if (!s.top_k_dev && s.top_k < 0) return TINFER_ERR_INVALID_ARG;
+  if (!s.top_p_dev && !(s.top_p >= 0.f)) return TINFER_ERR_INVALID_ARG;
+  if (!s.min_p_dev && !(s.min_p >= 0.f && s.min_p <= 1.f)) return TINFER_ERR_INVALID_ARG;
+  if (vocab > sample::MAX_VOCAB || rows > (1 << 27)) return TINFER_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return TINFER_ERR_CUDA;
+  // a CTA to a row, or for few rows as many more as run at once, while each has a few words for every thread
+  const long long bytes = (long long)vocab * size;
+  int cluster = 1;
+  while (cluster < sample::MAX_CLUSTER && 2LL * rows * cluster <= 2 * sms && bytes / cluster > 16 * 1024) cluster *= 2;
+  sample::Params q{logits_dev, row_stride, u_dev, s, ids_dev, logp_dev, rows, vocab, ((vocab + cluster - 1) / cluster + 7) / 8 * 8};
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = dtype == TINFER_DTYPE_F32   ? sample::launch<float>(q, cluster, st)
+                        : dtype == TINFER_DTYPE_F16 ? sample::launch<__half>(q, cluster, st)
+                                                    : sample::launch<__nv_bfloat16>(q, cluster, st);
+  return e == cudaSuccess ? TINFER_OK : TINFER_ERR_CUDA;
+}

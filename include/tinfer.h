@@ -530,6 +530,34 @@ tinfer_status tinfer_op_moe_layer(const tinfer_moe* layer, int n_tokens, int dty
                                   int32_t* ids_dev, float* weights_dev, void* workspace_dev,
                                   size_t workspace_bytes, int32_t* status_dev, void* stream);
 
+/* The next token of each row of logits ([rows][vocab] of `dtype`, rows row_stride elements apart, 0 for several draws from one;
+ * any element alignment), drawn from one given number u in [0, 1) for each row:
+ *   w_i = e^((x_i - max x) / temperature)
+ *   kept are the first top_k tokens in order of value, equal ones by the lower id (0, or the vocabulary and more: all);
+ *   of these those before which, in that order, less than top_p of their weights' sum lies (1 and more: all; the first always);
+ *   of these those with w_i >= min_p (0: all);
+ *   ids_dev[r]: the first token in the order of ids at which the kept weights' sum exceeds u times their total;
+ *   logp_dev[r] (may be NULL): the logarithm of its share of that total.
+ * temperature 0 takes the likeliest token, equal ones by the lower id (logp 0). A logit of -infinity is a masked token and never drawn. A row
+ * with a NaN or +infinity, or nothing but masked tokens, gives id -1 and logp NaN. u outside [0, 1) counts as the nearest number inside,
+ * NaN as 0; temperatures between 0 and 1e-30 as 1e-30, those beyond 1e30 as that; weights below 2^-46 as 0.
+ * Each parameter is one for all rows or, where its pointer is not NULL, one for each ([rows] on the device, read when the
+ * kernel runs). There, a negative or NaN temperature gives id -1 and logp NaN, top_k below 1 and NaN mean all, min_p is clamped to 1.
+ * Weights are whole numbers of 2^-45 of the largest, off by 2^-37 of themselves at most, and sums are exact: the draw is the
+ * definition's unless a border is within some 1e-11 of the sum, and depends neither on timing nor on other rows.
+ * u_dev: fp32 [rows]; ids_dev: int32 [rows]. Asynchronous on `stream`, no workspace. vocab <= 2^18, else TINFER_ERR_UNSUPPORTED. */
+typedef struct {
+  float temperature;
+  int top_k;
+  float top_p, min_p;
+  const float* temperature_dev;
+  const int32_t* top_k_dev;
+  const float *top_p_dev, *min_p_dev;
+} tinfer_sampling;
+tinfer_status tinfer_op_sample(int rows, int vocab, int dtype, const void* logits_dev, long long row_stride,
+                               const float* u_dev, const tinfer_sampling* sampling, int32_t* ids_dev,
+                               float* logp_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,275 @@
+"""Drawn tokens on the GPU against a plain implementation in 64 bits.
+
+Ids have to be equal. The kernel's weights are off by 2^-37 of themselves, the reference's by 2^-52: a draw could differ where u
+times the total lies within 2^-36 of a border, which of the rows here (a few thousand, some hundred thousand borders of
+1e-5 of the sum apart at most) none is expected to do. logp: the share is off by 2^-36 and rounded (2^-24), the logarithm by
+2 of its last places, 2^-22 relative."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import decode_persistent_megakernel_gb300 as T  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+LAST = 1.0 - 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    T.build()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def column(v, rows):
+    if not torch.is_tensor(v):
+        v = torch.full((rows,), v, device="cuda", dtype=torch.int32 if isinstance(v, int) else torch.float32)
+    return v.double()[:, None]
+
+
+def reference(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """ids and logp; x [rows, vocab] on the GPU, finite rows with temperatures above 0."""
+    rows, vocab = x.shape
+    t, k, p, low = (column(v, rows) for v in (temperature, top_k, top_p, min_p))
+    v, order = torch.sort(x.float(), dim=1, descending=True, stable=True)
+    w = torch.exp((v.double() - v[:, :1].double()) / t.clamp(1e-30, 1e30))
+    n = torch.where(k > 0, k, float(vocab))
+    w = w * (torch.arange(vocab, device="cuda") < n)
+    upto = torch.cumsum(w, 1)
+    first = torch.arange(vocab, device="cuda") == 0
+    w = w * (first | (upto - w < p * upto[:, -1:]) | (p >= 1))
+    w = w * (w >= low.clamp(max=1.0))
+    back = torch.zeros_like(w).scatter_(1, order, w)
+    upto = torch.cumsum(back, 1)
+    total = upto[:, -1:].contiguous()
+    at = torch.searchsorted(upto, (u.double().clamp(0, LAST)[:, None] * total).contiguous(), right=True).clamp(max=vocab - 1)
+    return at[:, 0], torch.log(back.gather(1, at) / total)[:, 0]
+
+
+def check(x, u, **kw):
+    ids, logp = T.sample(x, u, **kw)
+    want, lw = reference(x, u, **kw)
+    assert torch.equal(ids.long(), want), (kw, (ids.long() != want).nonzero()[:5].tolist())
+    assert bool(((logp.double() - lw).abs() <= lw.abs() * 2.0 ** -22 + 2.0 ** -35).all()), kw
+    return ids, logp
+
+
+def logits(rows, vocab, dtype, seed, spread=2.5):
+    return (torch.randn((rows, vocab), generator=gen(seed), device="cuda") * spread).to(dtype)
+
+
+def uniform(rows, seed):
+    return torch.rand(rows, generator=gen(seed + 1000), device="cuda")
+
+
+REQUESTS = [dict(), dict(temperature=0.5), dict(temperature=1.7), dict(top_k=1), dict(top_k=2), dict(top_k=50), dict(top_k=300),
+            dict(top_p=0.9), dict(top_p=0.3), dict(top_p=0.999), dict(min_p=0.05), dict(min_p=0.5),
+            dict(temperature=0.7, top_k=40, top_p=0.95), dict(top_k=20, min_p=0.1), dict(top_p=0.8, min_p=0.02),
+            dict(temperature=1.3, top_k=100, top_p=0.7, min_p=0.01)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [1, 2, 3, 7, 8, 9, 63, 257, 2048, 5003, 32000, 128256, 262144])
+def test_sizes_types_and_requests(vocab, dtype):
+    for i, kw in enumerate(REQUESTS):
+        for rows in (1, 5) if vocab < 30000 else (3,):
+            check(logits(rows, vocab, dtype, vocab + i), uniform(rows, i), **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(400, 3000), (200, 50257), (64, 151936), (700, 257)])
+def test_many_rows(rows, vocab, dtype):
+    for i, kw in enumerate(REQUESTS[::3] + [dict(top_p=0.95), dict(top_k=1000)]):
+        check(logits(rows, vocab, dtype, rows + i), uniform(rows, i), **kw)
+
+
+@pytest.mark.parametrize("k", [511, 512, 513, 1024, 2047, 2048, 2049, 5000, 31999, 32000, 40000, 2 ** 31 - 1])
+def test_large_top_k(k):
+    for rows, dtype in ((2, torch.float32), (300, torch.bfloat16)):
+        check(logits(rows, 32000, dtype, k % 1000), uniform(rows, 3), top_k=k)
+        check(logits(rows, 32000, dtype, k % 1000 + 1), uniform(rows, 4), top_k=k, top_p=0.8, min_p=0.001)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_requests_of_their_own(dtype):
+    rows, vocab = 150, 20000
+    g = gen(5)
+    x = logits(rows, vocab, dtype, 1)
+    t = torch.rand(rows, generator=g, device="cuda") * 1.5 + 0.2
+    k = torch.randint(0, 200, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    k[::7] = 0
+    p = torch.rand(rows, generator=g, device="cuda") * 1.2
+    low = torch.rand(rows, generator=g, device="cuda") * 0.1
+    low[::3] = 0
+    check(x, uniform(rows, 2), temperature=t, top_k=k, top_p=p, min_p=low)
+    check(x, uniform(rows, 3), temperature=0.9, top_k=k, top_p=0.9, min_p=low)
+    check(x, uniform(rows, 4), temperature=t, top_p=p)
+    t[5], k[6], p[7], low[8] = 0.0, -3, float("nan"), 7.0
+    k[7], low[7] = 0, 0.0
+    ids, logp = T.sample(x, uniform(rows, 5), temperature=t, top_k=k, top_p=p, min_p=low)
+    t[5], p[7] = 1e-9, 1.0
+    k[6] = 0
+    want, lw = reference(x, uniform(rows, 5), t, k, p, low)
+    assert torch.equal(ids.long(), want) and bool(((logp - lw).abs() <= lw.abs() * 2.0 ** -22 + 2.0 ** -35).all())
+    t[9], t[10] = -1.0, float("nan")
+    ids, logp = T.sample(x, uniform(rows, 5), temperature=t)
+    assert ids[9:11].tolist() == [-1, -1] and bool(logp[9:11].isnan().all()) and bool((ids[11:] >= 0).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [10, 3001, 128256])
+def test_greedy_takes_the_lowest_id(vocab, dtype):
+    x = logits(6, vocab, dtype, vocab)
+    x[1, vocab // 2:] = x[1].max()
+    x[2] = 0
+    x[3, ::2] = -float("inf")
+    want = x.float().argmax(1)
+    want[1] = min(int(want[1]), vocab // 2)
+    want[2] = 0
+    for kw in (dict(temperature=0.0), dict(temperature=0), dict(temperature=0.0, top_k=5, top_p=0.5, min_p=0.5)):
+        ids, logp = T.sample(x, uniform(6, 1), **kw)
+        assert torch.equal(ids.long(), want) and bool((logp == 0).all())
+    for kw in (dict(top_k=1), dict(top_p=0.0)):
+        ids, logp = T.sample(x, uniform(6, 1), **kw)
+        assert torch.equal(ids.long(), want) and bool((logp == 0).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [100, 30000, 262144])
+def test_equal_logits(vocab, dtype):
+    """Ties at the border go by the lower id, however many there are."""
+    rows = 7
+    x = torch.zeros((rows, vocab), dtype=dtype, device="cuda")
+    for kw in (dict(), dict(top_k=10), dict(top_k=vocab - 1), dict(top_p=0.5), dict(top_p=0.999), dict(min_p=1.0), dict(min_p=0.3),
+               dict(top_k=vocab // 2, top_p=0.25), dict(top_k=77, top_p=0.4, min_p=0.9)):
+        check(x, uniform(rows, 1), **kw)
+    x[:, vocab // 3:vocab // 2] = 1.0  # two levels
+    x[:, -vocab // 4:] = -float("inf")
+    for kw in (dict(), dict(top_k=10), dict(top_k=vocab // 4), dict(top_p=0.2), dict(top_p=0.7), dict(top_p=0.99), dict(min_p=0.5),
+               dict(min_p=0.3), dict(top_k=vocab // 2, top_p=0.9), dict(temperature=0.1, top_p=0.9)):
+        check(x, uniform(rows, 2), **kw)
+
+
+@pytest.mark.parametrize("levels", [3, 40])
+def test_few_levels_of_many_tokens(levels):
+    x = (torch.randint(0, levels, (20, 100000), generator=gen(levels), device="cuda").float() / 4).bfloat16()
+    for kw in (dict(top_p=0.6), dict(top_p=0.97), dict(top_k=700), dict(top_k=9000, top_p=0.5), dict(temperature=0.3, top_p=0.9, min_p=0.01)):
+        check(x, uniform(20, 3), **kw)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_masks(dtype):
+    rows, vocab = 9, 40000
+    low = torch.finfo(dtype).min
+    x = logits(rows, vocab, dtype, 1)
+    x[:, 5000:39000] = -float("inf")
+    x[1, 1:] = -float("inf")
+    x[2, :-1] = -float("inf")
+    x[3, 100:] = low
+    x[4, :39999] = low
+    x[5] = low
+    x[6, ::2] = low
+    for kw in REQUESTS + [dict(top_k=1500), dict(top_k=6000), dict(temperature=5.0, top_p=0.99), dict(temperature=0.02)]:
+        ids, _ = check(x, uniform(rows, 2), **kw)
+        assert ids[1] == 0 and ids[2] == vocab - 1 and ids[4] == vocab - 1
+
+
+def test_rows_without_an_answer():
+    for dtype in TYPES:
+        x = logits(8, 3000, dtype, 1)
+        x[1], x[2, 77], x[3, 2999], x[4, 0] = -float("inf"), float("nan"), float("inf"), -float("nan")
+        for kw in (dict(), dict(top_k=5), dict(top_p=0.5), dict(min_p=0.1), dict(temperature=0.0)):
+            ids, logp = T.sample(x, uniform(8, 1), **kw)
+            assert ids[1:5].tolist() == [-1] * 4 and bool(logp[1:5].isnan().all())
+            good = torch.tensor([0, 5, 6, 7], device="cuda")
+            again = T.sample(x[good], uniform(8, 1)[good].contiguous(), **kw)
+            assert torch.equal(again[0], ids[good]) and torch.equal(again[1], logp[good])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_ends_of_u(dtype):
+    x = logits(9, 5000, dtype, 4)
+    x[:, :3] = -float("inf")
+    x[:, -2:] = -float("inf")
+    u = torch.tensor([0.0, LAST, 1.0, 2.0, -1.0, float("nan"), 2.0 ** -30, 1e-45, float("inf")], device="cuda")
+    inside = torch.tensor([0.0, LAST, LAST, LAST, 0.0, 0.0, 2.0 ** -30, 1e-45, LAST], device="cuda")
+    for kw in REQUESTS:
+        ids, logp = T.sample(x, u, **kw)
+        again = check(x, inside, **kw)
+        assert torch.equal(ids, again[0]) and torch.equal(logp, again[1])
+        assert bool((ids >= 3).all()) and bool((ids < 4998).all())
+
+
+def test_shares_of_the_draws():
+    """Evenly spaced numbers draw each token as often as its share says."""
+    n = 4096
+    x = logits(1, 500, torch.float32, 9).expand(n, 500)
+    u = (torch.arange(n, device="cuda") + 0.5) / n
+    for kw in (dict(), dict(temperature=0.6, top_k=30), dict(top_p=0.9), dict(min_p=0.02)):
+        ids, logp = check(x, u, **kw)
+        got = torch.bincount(ids.long(), minlength=500).double()
+        share = torch.zeros(500, dtype=torch.float64, device="cuda")
+        share[ids.long()] = torch.exp(logp.double())
+        assert float((got - n * share).abs().max()) <= 1.01
+        assert bool((ids[1:] >= ids[:-1]).all())
+
+
+@pytest.mark.parametrize("spread,offset,temperature", [(1e-3, 0.0, 1.0), (3.0, 1e4, 1.0), (300.0, -500.0, 50.0), (1e-4, 7.0, 1e-5),
+                                                       (1e30, 0.0, 1e30), (2.0, 0.0, 1e-3), (1.0, 0.0, 1e6)])
+def test_large_and_small_logits(spread, offset, temperature):
+    x = logits(40, 9000, torch.float32, 3, spread) + offset
+    for kw in (dict(), dict(top_p=0.9), dict(top_k=64, top_p=0.5), dict(min_p=0.2)):
+        check(x, uniform(40, 5), temperature=temperature, **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("first,pad", [(0, 1), (1, 0), (3, 5), (7, 2), (5, 8)])
+def test_rows_at_any_alignment(dtype, first, pad):
+    for vocab in (5, 100, 4001, 50001):
+        buf = torch.full((6 * (vocab + pad) + first + 64,), 1e30, dtype=dtype, device="cuda")  # beside the rows: huge
+        x = buf[first:first + 6 * (vocab + pad)].view(6, vocab + pad)[:, :vocab]
+        x.copy_(logits(6, vocab, dtype, first))
+        for kw in (dict(), dict(top_k=20), dict(top_p=0.9), dict(min_p=0.1)):
+            check(x, uniform(6, first), **kw)
+
+
+def test_runs_agree_streams_and_graphs():
+    x, u = logits(30, 60000, torch.bfloat16, 1), uniform(30, 1)
+    t = torch.full((30,), 0.8, device="cuda")
+    for kw in (dict(top_p=0.95), dict(top_k=50, top_p=0.9)):
+        want = T.sample(x, u, temperature=t, **kw)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        other = T.sample(x, u, temperature=t, stream=side, **kw)
+        side.synchronize()
+        assert torch.equal(want[0], other[0]) and torch.equal(want[1], other[1])
+        out = torch.empty(30, dtype=torch.int32, device="cuda"), torch.empty(30, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            T.sample(x, u, temperature=t, out=out, **kw)
+        for seed in range(3):
+            u.copy_(uniform(30, 10 + seed))
+            t.fill_(0.5 + seed)
+            x.copy_(logits(30, 60000, torch.bfloat16, 20 + seed))
+            graph.replay()
+            want = check(x, u, temperature=t, **kw)
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+        T.sample(x, u, out=(out[0], None))
+
+
+def test_no_rows():
+    ids, logp = T.sample(torch.zeros((0, 100), device="cuda"), torch.zeros(0, device="cuda"))
+    assert ids.shape == (0,) and logp.shape == (0,)
+
+
+def test_agrees_with_the_scores():
+    x = logits(5, 50000, torch.float32, 2)
+    ids, logp = T.sample(x, uniform(5, 2))
+    assert float((T.logprobs(x, ids)[0] - logp).abs().max()) < 1e-5
+    assert math.isfinite(float(logp.sum()))
