@@ -37,7 +37,10 @@ constexpr int MAX_VOCAB = 1 << 18;
 constexpr int LIST = 2048;           // listed candidates of a row, at most
 constexpr int BINS = 2048;           // of the distance from the maximum, in units of log2 of the weight
 constexpr float PER_LOG2 = 51.2f;    // bins to a factor of two: weights down to 2^-40 are told apart
-constexpr float WINDOW = 1.f / 512;  // of the sum, either side of the nucleus' border: bins' own weights are known to 0.7% at worst
+// Of the sum, either side of the nucleus' border: a bin's weight is taken from its tokens' number and mean distance, too low by
+// 2.3e-5 of itself at most (its width of 0.0135 squared, over 8).
+constexpr float WINDOW = 4e-5f;
+constexpr int PLACES = 256;          // of a bin, that distances within it are rounded to
 static_assert(LIST == 4 * NT && BINS == 4 * NT, "four to a thread");
 
 struct Params {
@@ -52,7 +55,7 @@ struct Params {
 
 struct Smem {
   unsigned hist[BINS];
-  u64 key[LIST], mass[LIST];        // the first CTA's list; `mass` also a CTA's own candidates before they go there
+  u64 key[LIST], mass[LIST];        // the first CTA's list; `key` also the bins' sums of distances, `mass` a CTA's own candidates
   float2 table[64];                 // 2^(i / 64) in two parts
   u64 sums[MAX_CLUSTER][NWARPS];    // kept weights of each warp of the cluster (in the first CTA)
   u64 red[NWARPS], cross[2][MAX_CLUSTER];
@@ -64,6 +67,26 @@ struct Smem {
   u64 tau, rest, total_s;  // tau: (key, ~id) of the last token kept
   float ch, cl;
   u64 least;                        // weights below are not kept
+};
+
+// 2^(i / 64) in two parts, each the nearest fp32.
+__constant__ float2 POWERS[64] = {
+    {1.f, 0.f}, {1.01088929f, -5.71160541e-09f}, {1.0218972f, -4.81155986e-08f}, {1.03302491f, -2.80908932e-08f},
+    {1.04427373f, 4.83347016e-08f}, {1.05564523f, -4.90716943e-08f}, {1.06714046f, -5.93375198e-08f}, {1.07876074f, 5.46159455e-08f},
+    {1.09050775f, -1.30775399e-08f}, {1.10238254f, 4.260502e-08f}, {1.1143868f, -5.43554002e-08f}, {1.12652159f, 3.12364143e-08f},
+    {1.13878858f, 5.38622231e-08f}, {1.15118921f, 2.19222827e-08f}, {1.1637249f, -4.05144149e-08f}, {1.17639697f, 2.56697508e-08f},
+    {1.18920708f, 3.79763527e-08f}, {1.20215678f, -5.06975653e-08f}, {1.21524739f, -3.26739489e-08f}, {1.22848058f, -4.13620036e-08f},
+    {1.24185777f, 4.4968381e-08f}, {1.25538075f, 7.32223748e-09f}, {1.26905096f, 1.41933332e-09f}, {1.28287005f, -3.81662169e-08f},
+    {1.29683959f, -4.01899953e-08f}, {1.31096125f, -3.49657157e-08f}, {1.32523668f, -3.49637332e-08f}, {1.33966756f, -3.46167397e-08f},
+    {1.35425556f, -1.01233493e-08f}, {1.36900246f, -3.84588184e-08f}, {1.38390994f, -5.87557736e-08f}, {1.39897966f, 8.68943406e-09f},
+    {1.41421354f, 2.4203235e-08f}, {1.42961335f, -1.34299292e-08f}, {1.44518077f, 3.32419994e-08f}, {1.46091783f, -3.62865755e-08f},
+    {1.47682619f, -4.50089885e-08f}, {1.49290776f, -3.42362014e-08f}, {1.50916445f, -2.49593732e-08f}, {1.52559817f, -1.76285688e-08f},
+    {1.54221082f, 8.07090483e-09f}, {1.55900443f, -2.57646651e-08f}, {1.5759809f, -5.66102543e-08f}, {1.59314215f, -4.90313679e-10f},
+    {1.61049032f, 9.83621717e-09f}, {1.62802744f, -1.72600831e-08f}, {1.64575553f, -5.12497209e-08f}, {1.66367662f, -3.92029875e-08f},
+    {1.68179286f, -2.47553267e-08f}, {1.70010638f, -2.86514723e-08f}, {1.71861935f, -4.8496176e-08f}, {1.73733389f, -5.85022342e-08f},
+    {1.75625217f, -9.23577037e-09f}, {1.77537644f, 5.34319788e-08f}, {1.79470909f, -1.14150449e-08f}, {1.81425214f, 3.73625824e-08f},
+    {1.8340081f, -1.1239278e-08f}, {1.85397911f, 1.43656118e-08f}, {1.87416768f, -4.66300563e-08f}, {1.89457595f, 2.81033845e-08f},
+    {1.91520655f, 9.84532811e-09f}, {1.93606174f, 5.3570723e-08f}, {1.95714414f, -1.70218044e-08f}, {1.97845602f, 6.03272632e-09f},
 };
 
 // Logits as whole numbers in their order, zeros of both signs equal; above 0 for all.
@@ -109,9 +132,8 @@ __device__ __forceinline__ u64 weight(float x, float m, float ch, float cl, cons
 }
 __device__ __noinline__ u64 weight_once(float x, float m, float ch, float cl, const float2* table) { return weight(x, m, ch, cl, table); }
 
-__device__ __forceinline__ int bin_of(float x, float m, float ch) {
-  return (int)fminf((m - x) * ch * PER_LOG2, (float)(BINS - 1));
-}
+__device__ __forceinline__ float bins_off(float x, float m, float ch) { return fminf((m - x) * ch * PER_LOG2, (float)(BINS - 1)); }
+__device__ __forceinline__ int bin_of(float x, float m, float ch) { return (int)bins_off(x, m, ch); }
 
 __device__ __forceinline__ void unpack(const uint4& w, float (&x)[4], const float*) {
   x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
@@ -456,22 +478,18 @@ __device__ __forceinline__ void Draw<T>::run() {
   u = u > 0.f ? u : 0.f;  // (NaN too)
   const int k = k_given > 0 && k_given < q.vocab ? k_given : 0;
   const bool nucleus = p < 1.f;
-  if (tid < 64) {
-    const double v = exp2(tid / 64.0);
-    const float h = (float)v;
-    sm.table[tid] = make_float2(h, (float)(v - (double)h));
-  }
+  if (tid < 64) sm.table[tid] = POWERS[tid];
   if (tid == 64) {
-    const double c = 1.4426950408889634074 / (double)fminf(fmaxf(temperature, 1e-30f), 1e30f);
-    sm.ch = (float)c;
-    sm.cl = (float)(c - (double)sm.ch);
-    sm.least = low > 0.f ? (u64)ceil((double)fminf(low, 1.f) * 35184372088832.0) : 0;  // 2^45
+    constexpr float L = 1.44269502f, LL = 1.92596303e-8f;  // log2(e) in two parts
+    const float t = fminf(fmaxf(temperature, 1e-30f), 1e30f), c = __fdiv_rn(L, t);
+    sm.ch = c;
+    sm.cl = (fmaf(-c, t, L) + LL) / t;
+    sm.least = low > 0.f ? (u64)ceilf(fminf(low, 1.f) * 35184372088832.f) : 0;  // 2^45
   }
   if (tid == 0) {
     sm.own = sm.listed = sm.owners = sm.warp = 0;
     sm.rank = -1;
   }
-  for (int i = tid; i < BINS; i += NT) sm.hist[i] = 0;
 
   // ---- the maximum
   float mine = -INFINITY;
@@ -610,20 +628,33 @@ __device__ __forceinline__ void Draw<T>::run() {
   if (k) search(false, (u64)k);
   int lo = BINS, hi = BINS;
   if (nucleus) {
+    unsigned* off = reinterpret_cast<unsigned*>(sm.key);
+    for (int i = tid; i < BINS; i += NT) sm.hist[i] = off[i] = 0;
+    meet();
     in.template walk<2>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
-      if (x > -INFINITY && kept(x, id)) atomicAdd(&sm.hist[bin_of(x, m, ch)], 1u);
+      if (x > -INFINITY && kept(x, id)) {
+        const float b = bins_off(x, m, ch);
+        atomicAdd(&sm.hist[(int)b], 1u);
+        atomicAdd(&off[(int)b], (unsigned)((b - (float)(int)b) * PLACES));
+      }
     });
     __syncthreads();
     if (rank) {
-      unsigned* all = in_first(sm.hist);
+      unsigned *all = in_first(sm.hist), *all_off = in_first(off);
       for (int i = tid; i < BINS; i += NT)
-        if (sm.hist[i]) atomicAdd(all + i, sm.hist[i]);
+        if (sm.hist[i]) {
+          atomicAdd(all + i, sm.hist[i]);
+          atomicAdd(all_off + i, off[i]);
+        }
     }
     meet();
     if (rank == 0) {
       float w[4], s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s += w[i] = (float)sm.hist[tid * 4 + i] * exp2f(-((float)(tid * 4 + i) + 0.5f) / PER_LOG2);
+      for (int i = 0; i < 4; ++i) {
+        const float n = (float)sm.hist[tid * 4 + i];
+        s += w[i] = n > 0.f ? n * exp2f(-((float)(tid * 4 + i) + ((float)off[tid * 4 + i] / n + 0.5f) / PLACES) / PER_LOG2) : 0.f;
+      }
       float incl = s;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
