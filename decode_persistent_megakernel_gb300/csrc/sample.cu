@@ -23,6 +23,7 @@
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+#include <utility>
 
 #include "tinfer.h"
 
@@ -37,10 +38,11 @@ constexpr int MAX_VOCAB = 1 << 18;
 constexpr int LIST = 2048;           // listed candidates of a row, at most
 constexpr int BINS = 2048;           // of the distance from the maximum, in units of log2 of the weight
 constexpr float PER_LOG2 = 51.2f;    // bins to a factor of two: weights down to 2^-40 are told apart
-// Of the sum, either side of the nucleus' border: a bin's weight is taken from its tokens' number and mean distance, too low by
-// 2.3e-5 of itself at most (its width of 0.0135 squared, over 8).
-constexpr float WINDOW = 4e-5f;
-constexpr int PLACES = 256;          // of a bin, that distances within it are rounded to
+// A token adds its weight to its bin in units of 2^-14 of the bin's largest, linear in its distance: off by 2.3e-5 of itself for
+// the bin's curvature (its width, 0.0135 in the exponent, squared over 8) and 3e-5 for the rounding. The nucleus' border is
+// looked for as far of the sum either side of where the bins put it.
+constexpr float WINDOW = 6e-5f;
+constexpr unsigned WHOLE = 16383;    // units: 2^18 tokens of them stay below 2^32
 static_assert(LIST == 4 * NT && BINS == 4 * NT, "four to a thread");
 
 struct Params {
@@ -55,13 +57,13 @@ struct Params {
 
 struct Smem {
   unsigned hist[BINS];
-  u64 key[LIST], mass[LIST];        // the first CTA's list; `key` also the bins' sums of distances, `mass` a CTA's own candidates
+  u64 key[LIST], mass[LIST];        // the first CTA's list; `mass` also a CTA's own candidates
   float2 table[64];                 // 2^(i / 64) in two parts
   u64 sums[MAX_CLUSTER][NWARPS];    // kept weights of each warp of the cluster (in the first CTA)
   u64 red[NWARPS], cross[2][MAX_CLUSTER];
   float redf[NWARPS], crossf[MAX_CLUSTER];
   uint16_t owner[NT];
-  int owners, own, listed, count[2];
+  int owners, own, listed[2], count[2];
   unsigned floor_key;
   int lo, hi, rank, warp;
   u64 tau, rest, total_s;  // tau: (key, ~id) of the last token kept
@@ -130,10 +132,44 @@ __device__ __forceinline__ u64 weight(float x, float m, float ch, float cl, cons
   const int shift = min(-(k >> 6), 63);  // (far ones, whose k means nothing, give 0)
   return p > -46.5f ? (u64)((w * 2 >> shift) + 1) >> 1 : 0ull;
 }
+// Two at a time: the same operations on pairs of fp32.
+__device__ __forceinline__ void weights(float2 x, float m, float ch, float cl, const float2* table, u64& w0, u64& w1) {
+  auto two = [](float v) { return make_float2(v, v); };
+  auto add = [](float2 a, float2 b) { return __fadd2_rn(a, b); };
+  auto mul = [](float2 a, float2 b) { return __fmul2_rn(a, b); };
+  auto fma = [](float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); };
+  auto sub = [&](float2 a, float2 b) { return __ffma2_rn(b, two(-1.f), a); };
+  constexpr float ROUND = 196608.f, L = 0.693147182f, LL = -1.90465421e-9f;
+  const float2 d = sub(x, two(m)), b = sub(d, x);
+  const float2 dl = sub(sub(x, sub(d, b)), add(two(m), b));
+  const float2 np = mul(d, two(-ch));  // -p
+  const float2 e = fma(dl, two(ch), fma(d, two(cl), fma(d, two(ch), np)));
+  const float2 t = sub(two(ROUND), np), nf = add(np, add(t, two(-ROUND)));  // -f
+  const float2 a = mul(nf, two(-L)), na = mul(nf, two(L));
+  const float2 ra = fma(e, two(L), fma(nf, two(-LL), fma(nf, two(-L), na)));
+  const float2 g = mul(mul(a, a), fma(a, fma(a, two(1.f / 24), two(1.f / 6)), two(0.5f)));
+  const float2 q = add(g, fma(ra, add(a, g), ra));
+  const int k0 = __float_as_int(t.x) - __float_as_int(ROUND), k1 = __float_as_int(t.y) - __float_as_int(ROUND);
+  const float2 h0 = table[k0 & 63], h1 = table[k1 & 63], h = make_float2(h0.x, h1.x), hl = make_float2(h0.y, h1.y);
+  const float2 pa = mul(h, a), npa = mul(h, na);
+  const float2 lo = add(fma(hl, a, fma(h, q, hl)), fma(h, a, npa));
+  const float2 u = add(pa, lo), ul = sub(lo, add(u, npa));
+  const float2 s = add(u, two(1.5f)), s2 = add(add(sub(u, add(s, two(-1.5f))), ul), two(3.57627869e-7f));
+  auto whole = [](float h, float s, float s2, int k, float np) {
+    const int high = __float_as_int(h) - 0x3F800000 + 0x800000 + (__float_as_int(s) - 0x3FC00000);
+    const long long w = ((long long)high << 22) + (__float_as_int(s2) - 0x34C00000);
+    return np < 46.5f ? (u64)((w * 2 >> min(-(k >> 6), 63)) + 1) >> 1 : 0ull;
+  };
+  w0 = whole(h.x, s.x, s2.x, k0, np.x);
+  w1 = whole(h.y, s.y, s2.y, k1, np.y);
+}
 __device__ __noinline__ u64 weight_once(float x, float m, float ch, float cl, const float2* table) { return weight(x, m, ch, cl, table); }
 
-__device__ __forceinline__ float bins_off(float x, float m, float ch) { return fminf((m - x) * ch * PER_LOG2, (float)(BINS - 1)); }
-__device__ __forceinline__ int bin_of(float x, float m, float ch) { return (int)bins_off(x, m, ch); }
+// The distance from the maximum in 1024ths of a bin, above ROUND_BINS. per = ch * PER_LOG2 * 1024.
+constexpr float ROUND_BINS = 12582912.f;  // 1.5 * 2^23
+__device__ __forceinline__ float distance(float x, float m, float per) {
+  return __fadd_rn(fminf(__fmul_rn(m - x, per), (float)(BINS * 1024 - 1)), ROUND_BINS);
+}
 
 __device__ __forceinline__ void unpack(const uint4& w, float (&x)[4], const float*) {
   x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
@@ -186,9 +222,9 @@ struct Slice {
   }
   __device__ __forceinline__ int id(int w, int i) const { return a + w * N + i - mis; }
   __device__ __forceinline__ int first(int warp) const { return min(warp * per, words); }
-  // f(logit, id) for the words [w0, w1) of a warp, a word to a lane, AHEAD under way
+  // f(logits of a word, id of its first) for the words [w0, w1) of a warp, a word to a lane, AHEAD under way
   template <int AHEAD, typename F>
-  __device__ __forceinline__ void walk(int w0, int w1, F&& f) const {
+  __device__ __forceinline__ void walk_words(int w0, int w1, F&& f) const {
 #pragma unroll 1
     for (int w = w0 + (threadIdx.x & 31); w < w1; w += 32 * AHEAD) {
       uint4 y[AHEAD];
@@ -200,10 +236,16 @@ struct Slice {
         if (w + 32 * h >= w1) break;
         float v[N];
         unpack(y[h], v, x);
-#pragma unroll
-        for (int i = 0; i < N; ++i) f(v[i], id(w + 32 * h, i));
+        f(v, id(w + 32 * h, 0));
       }
     }
+  }
+  template <int AHEAD, typename F>
+  __device__ __forceinline__ void walk(int w0, int w1, F&& f) const {  // f(logit, id)
+    walk_words<AHEAD>(w0, w1, [&](const float(&v)[N], int first) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) f(v[i], first + i);
+    });
   }
 };
 
@@ -226,12 +268,27 @@ __device__ u64 block_scan(u64 v, u64* red) {
   for (int w = 0; w < warp; ++w) v += red[w];
   return v;
 }
-// Sorts n (a power of two) numbers, the largest first.
+// Sorts n different numbers, the largest first, in a list with room for a power of two. Few are put where as many are above them.
 __device__ __noinline__ void sort_down(u64* a, int n) {
-  for (int size = 2; size <= n; size *= 2)
+  if (n <= NT / 2) {
+    __syncthreads();
+    const u64 x = threadIdx.x < n ? a[threadIdx.x] : 0;
+    int above = 0;
+    if ((int)threadIdx.x < n)
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) above += a[i] > x;
+    __syncthreads();
+    if ((int)threadIdx.x < n) a[above] = x;
+    __syncthreads();
+    return;
+  }
+  int pow2 = NT;
+  while (pow2 < n) pow2 *= 2;
+  for (int i = n + threadIdx.x; i < pow2; i += NT) a[i] = 0;
+  for (int size = 2; size <= pow2; size *= 2)
     for (int step = size / 2; step; step /= 2) {
       __syncthreads();
-      for (int i = threadIdx.x; i < n / 2; i += NT) {
+      for (int i = threadIdx.x; i < pow2 / 2; i += NT) {
         const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
         const u64 x = a[lo], y = a[hi];
         if ((x < y) == ((lo & size) == 0)) {
@@ -284,18 +341,30 @@ struct Draw {
     return all;
   }
   __device__ __forceinline__ bool kept(float x, int id) const { return pair_of(x, id) >= tau; }
-  // What a token adds: its weight if it is kept (KIND 0), one if it has this key (KIND 1)
-  __device__ __forceinline__ u64 measure(int kind, unsigned key, float x, int id) const {
-    if (x == -INFINITY || !kept(x, id)) return 0;
-    if (kind) return ordered(x) == key;
-    const u64 w = weight_once(x, m, ch, cl, sm.table);
-    return w >= least ? w : 0;
+  // What the tokens of a word add: their weights if they are kept (KIND 0), one if they have this key (KIND 1).
+  template <int N>
+  __device__ __forceinline__ void measure(int kind, unsigned key, const float (&x)[N], int first, u64 (&w)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) weights(make_float2(x[i], x[i + 1]), m, ch, cl, sm.table, w[i], w[i + 1]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool in_play = x[i] > -INFINITY && kept(x[i], first + i);
+      w[i] = !in_play ? 0 : kind ? (u64)(ordered(x[i]) == key) : w[i] >= least ? w[i] : 0;
+    }
+  }
+  __device__ __noinline__ u64 measured(int kind, unsigned key, int w0, int w1) const {  // by a warp
+    u64 s = 0;
+    in.template walk_words<1>(w0, w1, [&](const float(&x)[Slice<T>::N], int first) {
+      u64 w[Slice<T>::N];
+      measure(kind, key, x, first, w);
+#pragma unroll
+      for (int i = 0; i < Slice<T>::N; ++i) s += w[i];
+    });
+    return warp_sum(s);
   }
   // The sums of the warps' runs, to the first CTA.
   __device__ __noinline__ void tally(int kind, unsigned key) {
-    u64 s = 0;
-    in.template walk<1>(in.first(warp), in.first(warp + 1), [&](float x, int id) { s += measure(kind, key, x, id); });
-    s = warp_sum(s);
+    const u64 s = measured(kind, key, in.first(warp), in.first(warp + 1));
     meet();
     if (lane == 0) in_first(&sm.sums[rank][warp])[0] = s;
     meet();
@@ -333,9 +402,7 @@ struct Draw {
     // that warp's run, dealt out to all of the CTA; then one warp walks over its part
     int w0 = in.first(sm.warp), w1 = in.first(sm.warp + 1);
     const int per = (w1 - w0 + NWARPS - 1) / NWARPS;
-    u64 s = 0;
-    in.template walk<1>(min(w0 + warp * per, w1), min(w0 + (warp + 1) * per, w1), [&](float x, int id) { s += measure(kind, key, x, id); });
-    s = warp_sum(s);
+    const u64 s = measured(kind, key, min(w0 + warp * per, w1), min(w0 + (warp + 1) * per, w1));
     if (lane == 0) sm.red[warp] = s;
     __syncthreads();
     u64 rest = sm.rest;
@@ -345,12 +412,13 @@ struct Draw {
     const int end = min(w0 + (part + 1) * per, w1);
 #pragma unroll 1
     for (int w = w0 + part * per; w < end; w += 32) {
-      float v[Slice<T>::N];
-      u64 own = 0;
+      u64 own = 0, each[Slice<T>::N];
       if (w + lane < end) {
+        float v[Slice<T>::N];
         unpack(in.word(w + lane), v, in.x);
-#pragma unroll 1
-        for (int i = 0; i < Slice<T>::N; ++i) own += measure(kind, key, v[i], in.id(w + lane, i));
+        measure(kind, key, v, in.id(w + lane, 0), each);
+#pragma unroll
+        for (int i = 0; i < Slice<T>::N; ++i) own += each[i];
       }
       u64 incl = own;
 #pragma unroll
@@ -365,13 +433,14 @@ struct Draw {
       }
       if (lane == __ffs(over) - 1) {
         u64 left = rest - (incl - own);
+        bool found = false;
+#pragma unroll
         for (int i = 0; i < Slice<T>::N; ++i) {
-          const u64 s1 = measure(kind, key, v[i], in.id(w + lane, i));
-          if (left < s1) {
-            f(in.id(w + lane, i), s1);
-            break;
+          if (!found && left < each[i]) {
+            found = true;
+            f(in.id(w + lane, i), each[i]);
           }
-          left -= s1;
+          left -= found ? 0 : each[i];
         }
       }
       break;
@@ -380,18 +449,18 @@ struct Draw {
   // The border, bit by bit: the last kept token is the one at which the count (or the weights) of the kept ones reaches
   // `limit`. For lists that overflow.
   __device__ __noinline__ void search(bool mass, u64 limit) {
-    auto measured = [&](unsigned from) {
+    auto reached = [&](unsigned from) {
       u64 s = 0;
       in.template walk<1>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
         if (x > -INFINITY && kept(x, id) && ordered(x) >= from) s += mass ? weight_once(x, m, ch, cl, sm.table) : 1;
       });
       return sum(s);
     };
-    if (measured(0) < limit) return;  // all
+    if (reached(0) < limit) return;  // all
     unsigned key = 0;
     for (int bit = 31; bit >= 0; --bit)
-      if (measured(key | 1u << bit) >= limit) key |= 1u << bit;
-    const u64 above = key == 0xFFFFFFFFu ? 0 : measured(key + 1);
+      if (reached(key | 1u << bit) >= limit) key |= 1u << bit;
+    const u64 above = key == 0xFFFFFFFFu ? 0 : reached(key + 1);
     const u64 each = mass ? weight_once(unordered(key), m, ch, cl, sm.table) : 1;
     const u64 nth = (limit - above - 1) / each;  // of the tokens with this key, in order
     tally(1, key);
@@ -400,10 +469,10 @@ struct Draw {
     tau = sm.tau;
   }
   // A CTA's candidates (in sm.mass) to the first CTA's list; the row's number of them.
-  __device__ __forceinline__ int collect() {
+  __device__ __forceinline__ int collect(int which) {
     __syncthreads();
     const int n = sm.own;
-    if (tid == 0) sm.count[1] = n ? atomicAdd(in_first(&sm.listed), n) : 0;
+    if (tid == 0) sm.count[1] = n ? atomicAdd(in_first(&sm.listed[which]), n) : 0;
     __syncthreads();
     const int at = sm.count[1];
     u64* list = in_first(sm.key);
@@ -411,9 +480,7 @@ struct Draw {
       for (int i = tid; i < n; i += NT)
         if (at + i < LIST) list[at + i] = sm.mass[i];
     meet();
-    const int all = *in_first(&sm.listed);
-    meet();  // (it may be cleared again)
-    return all;
+    return *in_first(&sm.listed[which]);
   }
   // All tallied sums.
   __device__ __forceinline__ u64 tallied() {
@@ -432,23 +499,18 @@ struct Draw {
     if (i < LIST) sm.mass[i] = pair_of(x, id);
   }
   // In the first CTA: the list of n sorted, weights of its first `use` in sm.mass, the thread's four inclusive sums.
-  __device__ __forceinline__ int resolve(int n, int use, u64 (&incl)[4]) {
-    int pow2 = 64;
-    while (pow2 < n) pow2 *= 2;
-    for (int i = n + tid; i < pow2; i += NT) sm.key[i] = 0;
-    sort_down(sm.key, pow2);
-    u64 s = 0;
+  __device__ __forceinline__ void resolve(int n, int use, u64 (&incl)[4]) {
+    sort_down(sm.key, n);
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      const int e = tid * 4 + i;
-      const u64 w = e < use ? weight_once(unordered((unsigned)(sm.key[e] >> 32)), m, ch, cl, sm.table) : 0;
-      if (e < LIST) sm.mass[e] = w;
-      s += w;
-    }
+    for (int i = tid; i < LIST; i += NT)
+      sm.mass[i] = i < use ? weight_once(unordered((unsigned)(sm.key[i] >> 32)), m, ch, cl, sm.table) : 0;
+    __syncthreads();
+    u64 s = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s += sm.mass[tid * 4 + i];
     u64 at = block_scan(s, sm.red) - s;
 #pragma unroll
     for (int i = 0; i < 4; ++i) incl[i] = at += sm.mass[tid * 4 + i];
-    return pow2;
   }
   __device__ __forceinline__ void write(int id, u64 w, u64 total) {
     q.ids[row] = id;
@@ -486,10 +548,13 @@ __device__ __forceinline__ void Draw<T>::run() {
     sm.cl = (fmaf(-c, t, L) + LL) / t;
     sm.least = low > 0.f ? (u64)ceilf(fminf(low, 1.f) * 35184372088832.f) : 0;  // 2^45
   }
+  for (int i = tid; i < BINS; i += NT) sm.hist[i] = 0;
   if (tid == 0) {
-    sm.own = sm.listed = sm.owners = sm.warp = 0;
+    sm.own = sm.listed[0] = sm.listed[1] = sm.owners = sm.warp = 0;
     sm.rank = -1;
   }
+
+  auto started = cluster.barrier_arrive();  // the first CTA has to run before the others write to its memory
 
   // ---- the maximum
   float mine = -INFINITY;
@@ -500,8 +565,10 @@ __device__ __forceinline__ void Draw<T>::run() {
   if (lane == 0) sm.redf[warp] = top;
   __syncthreads();
   for (int w = 0; w < NWARPS; ++w) top = max_nan(top, sm.redf[w]);
-  meet();  // (every CTA has started)
+  cluster.barrier_wait(std::move(started));
   if (tid == 0) tell(&sm.crossf[rank], top);
+  const bool by_rank = k && k <= NT * size;
+  if (by_rank) reinterpret_cast<unsigned*>(in_first(sm.mass))[rank * NT + tid] = mine > -INFINITY ? ordered(mine) : 0;
   meet();
   m = sm.crossf[0];
   for (int r = 1; r < size; ++r) m = max_nan(m, sm.crossf[r]);
@@ -522,33 +589,46 @@ __device__ __forceinline__ void Draw<T>::run() {
   }
 
   // ---- few candidates: those from a floor on, in a list of the first CTA
-  bool few = k ? k <= NT * size : least && !nucleus;
+  bool few = k ? by_rank : least && !nucleus;
   if (few) {
     unsigned floor_key = 1;
     if (k) {
-      // the k-th largest of the threads' maxima, to 16 bits, is reached by k tokens
-      unsigned* all = reinterpret_cast<unsigned*>(in_first(sm.mass));
-      all[rank * NT + tid] = mine > -INFINITY ? ordered(mine) : 0;
-      meet();
+      // the k-th largest of the threads' maxima is reached by k tokens; to nine bits from the first in which they differ from
+      // the largest on, which lets few others in
       if (rank == 0) {
-        unsigned own[MAX_CLUSTER], key = 0;
-        for (int r = 0; r < MAX_CLUSTER; ++r) own[r] = r < size ? reinterpret_cast<unsigned*>(sm.mass)[r * NT + tid] : 0;
+        unsigned own[MAX_CLUSTER], least_key = 0xFFFFFFFFu, there = 0;
+        for (int r = 0; r < MAX_CLUSTER; ++r) {
+          own[r] = r < size ? reinterpret_cast<unsigned*>(sm.mass)[r * NT + tid] : 0;
+          if (own[r]) least_key = min(least_key, own[r]);
+          there += own[r] != 0;
+        }
+        least_key = __reduce_min_sync(~0u, least_key);
+        there = __reduce_add_sync(~0u, there);
+        unsigned* counts = reinterpret_cast<unsigned*>(sm.red);
+        if (lane == 0) {
+          counts[warp] = least_key;
+          counts[NWARPS + warp] = there;
+        }
+        __syncthreads();
+        least_key = __reduce_min_sync(~0u, counts[lane & (NWARPS - 1)]);
+        there = __reduce_add_sync(~0u, lane < NWARPS ? counts[NWARPS + lane] : 0u);
+        __syncthreads();
+        const int from_bit = 31 - __clz((least_key ^ ordered(m)) | 1), to_bit = max(from_bit - 9, 0);
+        unsigned key = ordered(m) & ~(((1u << from_bit) - 1) << 1 | 1);  // (what all have in common)
 #pragma unroll 1
-        for (int bit = 31; bit >= 16; --bit) {
+        for (int bit = from_bit; bit >= to_bit; --bit) {
           const unsigned from = key | 1u << bit;
           int n = 0;
 #pragma unroll
           for (int r = 0; r < MAX_CLUSTER; ++r) n += own[r] >= from;
           n = (int)__reduce_add_sync(~0u, (unsigned)n);
-          if (lane == 0) sm.red[warp] = (u64)n;
+          counts = reinterpret_cast<unsigned*>(sm.red) + (bit & 1) * NWARPS;
+          if (lane == 0) counts[warp] = (unsigned)n;
           __syncthreads();
-          n = 0;
-#pragma unroll
-          for (int w = 0; w < NWARPS; ++w) n += (int)sm.red[w];
+          n = (int)__reduce_add_sync(~0u, lane < NWARPS ? counts[lane] : 0u);
           if (n >= k) key = from;
-          __syncthreads();
         }
-        if (tid == 0) tell(&sm.floor_key, key > 1u ? key : 1u);
+        if (tid == 0) tell(&sm.floor_key, (int)there >= k && key > 1u ? key : 1u);
       }
       meet();
       floor_key = sm.floor_key;
@@ -568,13 +648,13 @@ __device__ __forceinline__ void Draw<T>::run() {
       for (int i = 0; i < Slice<T>::N; ++i)
         if (candidate(v[i])) take(v[i], in.id(w, i));
     }
-    const int n = collect();
+    const int n = collect(0);
     few = n <= LIST;
     if (few) {
       if (rank) return;  // (nothing more is written to the others' memory)
       const int use = k ? min(k, n) : n;
       u64 incl[4];
-      const int pow2 = resolve(n, use, incl);
+      resolve(n, use, incl);
       if (tid == (use - 1) / 4) sm.total_s = incl[(use - 1) % 4];
       __syncthreads();
       u64 limit = ~0ull;
@@ -597,10 +677,8 @@ __device__ __forceinline__ void Draw<T>::run() {
       keep = sm.count[0];
       if (tid == (keep - 1) / 4) sm.total_s = incl[(keep - 1) % 4];
       // the kept ones in the vocabulary's order: sorted by ~id, with their places
-      for (int i = tid; i < pow2; i += NT) sm.key[i] = i < keep ? (u64)(unsigned)sm.key[i] << 32 | (unsigned)i : 0;
-      int small = 64;
-      while (small < keep) small *= 2;
-      sort_down(sm.key, small);
+      for (int i = tid; i < keep; i += NT) sm.key[i] = (u64)(unsigned)sm.key[i] << 32 | (unsigned)i;
+      sort_down(sm.key, keep);
       const u64 total = sm.total_s;
       bool more;
       const u64 target = part_of(fminf(u, 0.99999994f), total, more);
@@ -619,42 +697,33 @@ __device__ __forceinline__ void Draw<T>::run() {
       }
       return;
     }
+    __syncthreads();
     if (tid == 0) sm.own = 0;
-    if (rank == 0 && tid == 0) sm.listed = 0;
-    meet();
+    __syncthreads();
   }
 
   // ---- many: the nucleus' border to a few bins
   if (k) search(false, (u64)k);
   int lo = BINS, hi = BINS;
   if (nucleus) {
-    unsigned* off = reinterpret_cast<unsigned*>(sm.key);
-    for (int i = tid; i < BINS; i += NT) sm.hist[i] = off[i] = 0;
-    meet();
-    in.template walk<2>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
-      if (x > -INFINITY && kept(x, id)) {
-        const float b = bins_off(x, m, ch);
-        atomicAdd(&sm.hist[(int)b], 1u);
-        atomicAdd(&off[(int)b], (unsigned)((b - (float)(int)b) * PLACES));
+    const float per = ch * (PER_LOG2 * 1024.f);
+    in.template walk<4>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
+      if (x > -INFINITY && (!tau || kept(x, id))) {
+        const unsigned b = __float_as_uint(distance(x, m, per)) - __float_as_uint(ROUND_BINS);
+        atomicAdd(&sm.hist[b >> 10], WHOLE - ((b & 1023) * 3524 >> 14));  // (2^(-1 / PER_LOG2) = 1 - 1023 * 3524 / 2^14 / WHOLE)
       }
     });
     __syncthreads();
     if (rank) {
-      unsigned *all = in_first(sm.hist), *all_off = in_first(off);
+      unsigned* all = in_first(sm.hist);
       for (int i = tid; i < BINS; i += NT)
-        if (sm.hist[i]) {
-          atomicAdd(all + i, sm.hist[i]);
-          atomicAdd(all_off + i, off[i]);
-        }
+        if (sm.hist[i]) atomicAdd(all + i, sm.hist[i]);
     }
     meet();
     if (rank == 0) {
       float w[4], s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float n = (float)sm.hist[tid * 4 + i];
-        s += w[i] = n > 0.f ? n * exp2f(-((float)(tid * 4 + i) + ((float)off[tid * 4 + i] / n + 0.5f) / PLACES) / PER_LOG2) : 0.f;
-      }
+      for (int i = 0; i < 4; ++i) s += w[i] = (float)sm.hist[tid * 4 + i] * exp2f((float)(tid * 4 + i) * (-1.f / PER_LOG2));
       float incl = s;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
@@ -691,18 +760,30 @@ __device__ __forceinline__ void Draw<T>::run() {
 
   // ---- the weights: all, those above the border's bins, and of these what min-p keeps; the tokens within the bins
   u64 all = 0, above = 0, keep = 0;
-  in.template walk<1>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
-    if (!kept(x, id)) return;
-    const u64 w = weight(x, m, ch, cl, sm.table);
-    all += w;
-    const int b = nucleus ? bin_of(x, m, ch) : 0;
-    if (b < lo) {
-      above += w;
-      keep += w >= least ? w : 0;
-    } else if (b <= hi && x > -INFINITY) {
-      take(x, id);
+  const float per_bin = ch * (PER_LOG2 * 1024.f);
+  const float below = nucleus ? ROUND_BINS + (float)(lo * 1024) : INFINITY, within = nucleus ? ROUND_BINS + (float)(hi * 1024 + 1023) : -INFINITY;
+  in.template walk_words<1>(in.first(warp), in.first(warp + 1), [&](const float(&x)[Slice<T>::N], int first) {
+#pragma unroll 2
+    for (int i = 0; i < Slice<T>::N; i += 2) {
+      const float v0 = x[i], v1 = x[i + 1];
+      u64 w0, w1;
+      weights(make_float2(v0, v1), m, ch, cl, sm.table, w0, w1);
+      const float d0 = distance(v0, m, per_bin), d1 = distance(v1, m, per_bin);
+      bool in0 = d0 >= below && d0 <= within && v0 > -INFINITY, in1 = d1 >= below && d1 <= within && v1 > -INFINITY;
+      if (tau) {
+        if (!kept(v0, first + i)) w0 = in0 = 0;
+        if (!kept(v1, first + i + 1)) w1 = in1 = 0;
+      }
+      all += w0 + w1;
+      w0 = d0 < below ? w0 : 0;
+      w1 = d1 < below ? w1 : 0;
+      above += w0 + w1;
+      if (least) keep += (w0 >= least ? w0 : 0) + (w1 >= least ? w1 : 0);
+      if (in0) take(v0, first + i);
+      if (in1) take(v1, first + i + 1);
     }
   });
+  if (!least) keep = above;
   keep = warp_sum(keep);
   if (lane == 0) in_first(&sm.sums[rank][warp])[0] = keep;
   if (nucleus) {
@@ -712,7 +793,7 @@ __device__ __forceinline__ void Draw<T>::run() {
     u64 limit = p > 0.f ? part_of(p, all, more) : 0;
     if (p > 0.f && more) ++limit;
     limit = limit ? limit : 1;
-    const int n = collect();
+    const int n = collect(1);
     if (rank == 0) {
       bool found = n <= LIST && n > 0 && above < limit;
       if (found) {
@@ -810,10 +891,13 @@ extern "C" tinfer_status tinfer_op_sample(int rows, int vocab, int dtype, const 
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return TINFER_ERR_CUDA;
-  // a CTA to a row, or for few rows as many more as run at once, while each has a few words for every thread
+  // a CTA to a row, or for few rows as many more as there are SMs, while each has a few words for every thread. Requests that go
+  // over all weights several times take two to an SM (64 rows of 151936 bf16, top-p 0.95: 94 us, 105 with one; 37 rows of
+  // 32000 without it: 25 us, 20 with one, whose barriers and search then are most of it)
+  const bool heavy = (s.top_p_dev || s.top_p < 1.f) && !s.top_k_dev && s.top_k == 0;
   const long long bytes = (long long)vocab * size;
   int cluster = 1;
-  while (cluster < sample::MAX_CLUSTER && 2LL * rows * cluster <= 2 * sms && bytes / cluster > 16 * 1024) cluster *= 2;
+  while (cluster < sample::MAX_CLUSTER && 2LL * rows * cluster <= (heavy ? 2 : 1) * sms && bytes / cluster > 16 * 1024) cluster *= 2;
   sample::Params q{logits_dev, row_stride, u_dev, s, ids_dev, logp_dev, rows, vocab, ((vocab + cluster - 1) / cluster + 7) / 8 * 8};
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = dtype == TINFER_DTYPE_F32   ? sample::launch<float>(q, cluster, st)
