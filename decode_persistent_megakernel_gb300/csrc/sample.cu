@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <initializer_list>
 #include <utility>
@@ -43,7 +44,9 @@ constexpr float PER_LOG2 = 51.2f;    // bins to a factor of two: weights down to
 // looked for as far of the sum either side of where the bins put it.
 constexpr float WINDOW = 6e-5f;
 constexpr unsigned WHOLE = 16383;    // units: 2^18 tokens of them stay below 2^32
-static_assert(LIST == 4 * NT && BINS == 4 * NT, "four to a thread");
+constexpr int PER = LIST / NT;       // of a list, or of the bins, to a thread
+static_assert(LIST == BINS, "alike for both");
+constexpr int MAXIMA = 2;            // of a thread: more than one, so that a CTA alone has enough for large top-k
 
 struct Params {
   const void* logits;
@@ -90,6 +93,8 @@ __constant__ float2 POWERS[64] = {
     {1.8340081f, -1.1239278e-08f}, {1.85397911f, 1.43656118e-08f}, {1.87416768f, -4.66300563e-08f}, {1.89457595f, 2.81033845e-08f},
     {1.91520655f, 9.84532811e-09f}, {1.93606174f, 5.3570723e-08f}, {1.95714414f, -1.70218044e-08f}, {1.97845602f, 6.03272632e-09f},
 };
+
+static_assert(offsetof(Smem, mass) == offsetof(Smem, key) + sizeof(u64) * LIST && MAX_CLUSTER * MAXIMA * NT * 4 <= 2 * LIST * 8, "room for the maxima");
 
 // Logits as whole numbers in their order, zeros of both signs equal; above 0 for all.
 __device__ __forceinline__ unsigned ordered(float x) {
@@ -498,8 +503,8 @@ struct Draw {
     const int i = atomicAdd(&sm.own, 1);
     if (i < LIST) sm.mass[i] = pair_of(x, id);
   }
-  // In the first CTA: the list of n sorted, weights of its first `use` in sm.mass, the thread's four inclusive sums.
-  __device__ __forceinline__ void resolve(int n, int use, u64 (&incl)[4]) {
+  // In the first CTA: the list of n sorted, weights of its first `use` in sm.mass, the thread's inclusive sums.
+  __device__ __forceinline__ void resolve(int n, int use, u64 (&incl)[PER]) {
     sort_down(sm.key, n);
 #pragma unroll 1
     for (int i = tid; i < LIST; i += NT)
@@ -507,10 +512,10 @@ struct Draw {
     __syncthreads();
     u64 s = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s += sm.mass[tid * 4 + i];
+    for (int i = 0; i < PER; ++i) s += sm.mass[tid * PER + i];
     u64 at = block_scan(s, sm.red) - s;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) incl[i] = at += sm.mass[tid * 4 + i];
+    for (int i = 0; i < PER; ++i) incl[i] = at += sm.mass[tid * PER + i];
   }
   __device__ __forceinline__ void write(int id, u64 w, u64 total) {
     q.ids[row] = id;
@@ -557,8 +562,16 @@ __device__ __forceinline__ void Draw<T>::run() {
   auto started = cluster.barrier_arrive();  // the first CTA has to run before the others write to its memory
 
   // ---- the maximum
-  float mine = -INFINITY;
-  in.template walk<4>(in.first(warp), in.first(warp + 1), [&](float x, int) { mine = max_nan(mine, x); });
+  float each[MAXIMA] = {-INFINITY, -INFINITY};  // of the thread's words in turn
+  in.template walk_words<4>(in.first(warp), in.first(warp + 1), [&](const float(&x)[Slice<T>::N], int) {
+    float y = x[0];
+#pragma unroll
+    for (int i = 1; i < Slice<T>::N; ++i) y = max_nan(y, x[i]);
+    const float other = each[0];
+    each[0] = max_nan(each[1], y);
+    each[1] = other;
+  });
+  const float mine = max_nan(each[0], each[1]);
   float top = mine;
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
@@ -567,8 +580,11 @@ __device__ __forceinline__ void Draw<T>::run() {
   for (int w = 0; w < NWARPS; ++w) top = max_nan(top, sm.redf[w]);
   cluster.barrier_wait(std::move(started));
   if (tid == 0) tell(&sm.crossf[rank], top);
-  const bool by_rank = k && k <= NT * size;
-  if (by_rank) reinterpret_cast<unsigned*>(in_first(sm.mass))[rank * NT + tid] = mine > -INFINITY ? ordered(mine) : 0;
+  const bool by_rank = k && k <= MAXIMA * NT * size;
+  unsigned* maxima = reinterpret_cast<unsigned*>(in_first(sm.key));  // (reaching into `mass`)
+  if (by_rank)
+#pragma unroll
+    for (int i = 0; i < MAXIMA; ++i) maxima[(rank * MAXIMA + i) * NT + tid] = each[i] > -INFINITY ? ordered(each[i]) : 0;
   meet();
   m = sm.crossf[0];
   for (int r = 1; r < size; ++r) m = max_nan(m, sm.crossf[r]);
@@ -596,9 +612,10 @@ __device__ __forceinline__ void Draw<T>::run() {
       // the k-th largest of the threads' maxima is reached by k tokens; to nine bits from the first in which they differ from
       // the largest on, which lets few others in
       if (rank == 0) {
-        unsigned own[MAX_CLUSTER], least_key = 0xFFFFFFFFu, there = 0;
-        for (int r = 0; r < MAX_CLUSTER; ++r) {
-          own[r] = r < size ? reinterpret_cast<unsigned*>(sm.mass)[r * NT + tid] : 0;
+        unsigned own[MAX_CLUSTER * MAXIMA], least_key = 0xFFFFFFFFu, there = 0;
+#pragma unroll
+        for (int r = 0; r < MAX_CLUSTER * MAXIMA; ++r) {
+          own[r] = r < size * MAXIMA ? maxima[r * NT + tid] : 0;
           if (own[r]) least_key = min(least_key, own[r]);
           there += own[r] != 0;
         }
@@ -620,7 +637,7 @@ __device__ __forceinline__ void Draw<T>::run() {
           const unsigned from = key | 1u << bit;
           int n = 0;
 #pragma unroll
-          for (int r = 0; r < MAX_CLUSTER; ++r) n += own[r] >= from;
+          for (int r = 0; r < MAX_CLUSTER * MAXIMA; ++r) n += own[r] >= from;
           n = (int)__reduce_add_sync(~0u, (unsigned)n);
           counts = reinterpret_cast<unsigned*>(sm.red) + (bit & 1) * NWARPS;
           if (lane == 0) counts[warp] = (unsigned)n;
@@ -653,9 +670,9 @@ __device__ __forceinline__ void Draw<T>::run() {
     if (few) {
       if (rank) return;  // (nothing more is written to the others' memory)
       const int use = k ? min(k, n) : n;
-      u64 incl[4];
+      u64 incl[PER];
       resolve(n, use, incl);
-      if (tid == (use - 1) / 4) sm.total_s = incl[(use - 1) % 4];
+      if (tid == (use - 1) / PER) sm.total_s = incl[(use - 1) % PER];
       __syncthreads();
       u64 limit = ~0ull;
       if (nucleus) {
@@ -666,8 +683,8 @@ __device__ __forceinline__ void Draw<T>::run() {
       }
       int keep = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = tid * 4 + i;
+      for (int i = 0; i < PER; ++i) {
+        const int e = tid * PER + i;
         const u64 w = sm.mass[e];
         keep += e < use && incl[i] - w < limit && (w >= least || e == 0);
       }
@@ -675,24 +692,24 @@ __device__ __forceinline__ void Draw<T>::run() {
       if (tid == NT - 1) sm.count[0] = keep;
       __syncthreads();
       keep = sm.count[0];
-      if (tid == (keep - 1) / 4) sm.total_s = incl[(keep - 1) % 4];
+      if (tid == (keep - 1) / PER) sm.total_s = incl[(keep - 1) % PER];
       // the kept ones in the vocabulary's order: sorted by ~id, with their places
       for (int i = tid; i < keep; i += NT) sm.key[i] = (u64)(unsigned)sm.key[i] << 32 | (unsigned)i;
       sort_down(sm.key, keep);
       const u64 total = sm.total_s;
       bool more;
       const u64 target = part_of(fminf(u, 0.99999994f), total, more);
-      u64 s = 0, w[4];
+      u64 s = 0, w[PER];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = tid * 4 + i;
+      for (int i = 0; i < PER; ++i) {
+        const int e = tid * PER + i;
         w[i] = e < keep ? sm.mass[(unsigned)sm.key[e]] : 0;
         s += w[i];
       }
       u64 at = block_scan(s, sm.red) - s;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (at <= target && target < at + w[i]) write((int)~(unsigned)(sm.key[tid * 4 + i] >> 32), w[i], total);
+      for (int i = 0; i < PER; ++i) {
+        if (at <= target && target < at + w[i]) write((int)~(unsigned)(sm.key[tid * PER + i] >> 32), w[i], total);
         at += w[i];
       }
       return;
@@ -707,7 +724,7 @@ __device__ __forceinline__ void Draw<T>::run() {
   int lo = BINS, hi = BINS;
   if (nucleus) {
     const float per = ch * (PER_LOG2 * 1024.f);
-    in.template walk<4>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
+    in.template walk<2>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
       if (x > -INFINITY && (!tau || kept(x, id))) {
         const unsigned b = __float_as_uint(distance(x, m, per)) - __float_as_uint(ROUND_BINS);
         atomicAdd(&sm.hist[b >> 10], WHOLE - ((b & 1023) * 3524 >> 14));  // (2^(-1 / PER_LOG2) = 1 - 1023 * 3524 / 2^14 / WHOLE)
@@ -721,9 +738,9 @@ __device__ __forceinline__ void Draw<T>::run() {
     }
     meet();
     if (rank == 0) {
-      float w[4], s = 0.f;
+      float w[PER], s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s += w[i] = (float)sm.hist[tid * 4 + i] * exp2f((float)(tid * 4 + i) * (-1.f / PER_LOG2));
+      for (int i = 0; i < PER; ++i) s += w[i] = (float)sm.hist[tid * PER + i] * exp2f((float)(tid * PER + i) * (-1.f / PER_LOG2));
       float incl = s;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
@@ -740,10 +757,10 @@ __device__ __forceinline__ void Draw<T>::run() {
       }
       float at = incl - s;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < PER; ++i) {
         at += w[i];
-        if (at >= (p - WINDOW) * all) atomicMin(&sm.lo, tid * 4 + i);
-        if (at >= (p + WINDOW) * all) atomicMin(&sm.hi, tid * 4 + i);
+        if (at >= (p - WINDOW) * all) atomicMin(&sm.lo, tid * PER + i);
+        if (at >= (p + WINDOW) * all) atomicMin(&sm.hi, tid * PER + i);
       }
       __syncthreads();
       const int a = sm.lo, b = sm.hi;
@@ -797,15 +814,15 @@ __device__ __forceinline__ void Draw<T>::run() {
     if (rank == 0) {
       bool found = n <= LIST && n > 0 && above < limit;
       if (found) {
-        u64 incl[4];
+        u64 incl[PER];
         resolve(n, n, incl);
         int inside = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) inside += tid * 4 + i < n && above + incl[i] - sm.mass[tid * 4 + i] < limit;
+        for (int i = 0; i < PER; ++i) inside += tid * PER + i < n && above + incl[i] - sm.mass[tid * PER + i] < limit;
         inside = (int)block_scan((u64)inside, sm.red);
         if (tid == NT - 1) {
           sm.count[0] = inside;
-          sm.total_s = incl[3];
+          sm.total_s = incl[PER - 1];
         }
         __syncthreads();
         inside = sm.count[0];
@@ -894,7 +911,7 @@ extern "C" tinfer_status tinfer_op_sample(int rows, int vocab, int dtype, const 
   // a CTA to a row, or for few rows as many more as there are SMs, while each has a few words for every thread. Requests that go
   // over all weights several times take two to an SM (64 rows of 151936 bf16, top-p 0.95: 94 us, 105 with one; 37 rows of
   // 32000 without it: 25 us, 20 with one, whose barriers and search then are most of it)
-  const bool heavy = (s.top_p_dev || s.top_p < 1.f) && !s.top_k_dev && s.top_k == 0;
+  const bool heavy = (s.top_p_dev || s.top_p < 1.f) && (s.top_k_dev || s.top_k == 0);
   const long long bytes = (long long)vocab * size;
   int cluster = 1;
   while (cluster < sample::MAX_CLUSTER && 2LL * rows * cluster <= (heavy ? 2 : 1) * sms && bytes / cluster > 16 * 1024) cluster *= 2;
