@@ -827,6 +827,13 @@ tinfer_status check(const tinfer_moe* m, int tokens) {
 template <int FMT>
 tinfer_status run(const tinfer_moe* m, int tokens, int dtype, Params& p, cudaStream_t st) {
   using S = Shape<FMT>;
+  const int entries = tokens * m->top_k, lists = Lists::bytes(entries);
+  const int up_row = row_bytes(m->hidden) * (dtype == TINFER_DTYPE_F32 ? parts_up<float>() : dtype == TINFER_DTYPE_F16 ? parts_up<__half>() : parts_up<__nv_bfloat16>());
+  const int down_row = row_bytes(m->ffn_e) * (dtype == TINFER_DTYPE_F32 ? parts_down<float>() : parts_down<__half>());
+  // the ring takes what the activations leave: with three stages they have the most room, and deeper rings what they do not need
+  auto room = [&](int stages) { return (SMEM - 1024 - NW * stages * S::SLOT - S::RED - lists) / 128 * 128; };
+  const int up_cap = std::min(COLS, room(3) / up_row), down_cap = std::min(COLS, room(3) / down_row);
+  if (up_cap < 1 || down_cap < 1) return TINFER_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return TINFER_ERR_CUDA;
@@ -844,14 +851,8 @@ tinfer_status run(const tinfer_moe* m, int tokens, int dtype, Params& p, cudaStr
   };
   p.m[0] = matrix(m->gu_packed, 2 * m->ffn_e, m->hidden);
   p.m[1] = matrix(m->down_packed, m->hidden, m->ffn_e);
-  const int entries = tokens * m->top_k, lists = Lists::bytes(entries);
-  const int up_row = row_bytes(m->hidden) * (dtype == TINFER_DTYPE_F32 ? parts_up<float>() : dtype == TINFER_DTYPE_F16 ? parts_up<__half>() : parts_up<__nv_bfloat16>());
-  const int down_row = row_bytes(m->ffn_e) * (dtype == TINFER_DTYPE_F32 ? parts_down<float>() : parts_down<__half>());
-  // the ring takes what the activations leave: with three stages they have the most room, and deeper rings what they do not need
-  auto room = [&](int stages) { return (SMEM - 1024 - NW * stages * S::SLOT - S::RED - lists) / 128 * 128; };
-  p.m[0].cap = std::min(COLS, room(3) / up_row);
-  p.m[1].cap = std::min(COLS, room(3) / down_row);
-  if (p.m[0].cap < 1 || p.m[1].cap < 1) return TINFER_ERR_UNSUPPORTED;
+  p.m[0].cap = up_cap;
+  p.m[1].cap = down_cap;
   p.resident = tokens * up_row <= room(3);
   if (p.resident) p.m[0].cap = COLS;
   const int most = std::min(entries, COLS);  // tokens of an expert in one group

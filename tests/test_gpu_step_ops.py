@@ -1,0 +1,129 @@
+"""A decoding step of several sequences, from the queries' and keys' projections to the next token, with the operators as they are
+used together: head norms with the rotation, the 8-bit cache and its attention, the batched projections, a mixture-of-experts
+layer, the LM head and the draw; eagerly and captured in one graph that follows positions, tokens and draws from replay to replay.
+
+Against the same step in 64 bits. The cache's own rounding is taken as it is: the step in 64 bits attends to the keys and values read
+back from it, which in turn have to be the step's own within half of the cache's 8-bit step. What is left is the operators' rounding, 2^-18 of
+a vector's size and less in each of the eight, passed on by weights that keep sizes: 2^-14 of the logits' size bounds it, where a
+wrong head, position, expert or order is off by the size itself."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import decode_persistent_megakernel_gb300 as T  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+S, H, HQ, HK, D, E, K, F, V, CTX = 4, 512, 8, 2, 64, 8, 2, 256, 2048, 40
+THETA, EPS = 10000.0, 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    T.build()
+
+
+def weight(g, rows, cols):
+    return (torch.randn((rows, cols), generator=g, device="cuda") * cols ** -0.5).bfloat16()
+
+
+class Model:
+    def __init__(self, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.embed = torch.randn((V, H), generator=g, device="cuda").bfloat16()
+        self.wqkv, self.wo, self.head = weight(g, (HQ + 2 * HK) * D, H), weight(g, H, HQ * D), weight(g, V, H) * 3
+        self.gq, self.gk = (1 + 0.2 * torch.randn(D, generator=g, device="cuda") for _ in range(2))
+        self.router = weight(g, E, H) * 2
+        self.w = [torch.stack([weight(g, *s) for _ in range(E)]) for s in ((F, H), (F, H), (H, F))]
+        self.layer = T.MoeLayer(self.router, *self.w, K, max_tokens=S)
+
+    def reference(self, tokens, pos, held):
+        """Logits [S, V] in 64 bits, and the step's keys and values; held: the cache's, [S, pos + 1, HK, D]."""
+        x = self.embed[tokens].double()
+        qkv = (x @ self.wqkv.double().T).view(S, HQ + 2 * HK, D)
+
+        def turned(y, gain):
+            y = y / torch.sqrt((y * y).mean(-1, keepdim=True) + EPS) * gain.double()
+            f = THETA ** (-2.0 * torch.arange(D // 2, device="cuda", dtype=torch.float64) / D)
+            a = (pos.double()[:, None] * f)[:, None, :]
+            u, v = y[..., :D // 2], y[..., D // 2:]
+            return torch.cat([u * a.cos() - v * a.sin(), v * a.cos() + u * a.sin()], -1)
+
+        q, k, v = turned(qkv[:, :HQ], self.gq), turned(qkv[:, HQ:HQ + HK], self.gk), qkv[:, HQ + HK:]
+        ks, vs = (t.double().repeat_interleave(HQ // HK, 2) for t in held)
+        p = torch.softmax(torch.einsum("shd,snhd->shn", q, ks) / D ** 0.5, -1)
+        x = x + torch.einsum("shn,snhd->shd", p, vs).reshape(S, -1) @ self.wo.double().T
+        logits = x @ self.router.double().T
+        top, ids = torch.topk(logits, K, dim=1)
+        share = torch.softmax(top, 1)
+        y = torch.zeros_like(x)
+        for s in range(S):
+            for e, w in zip(ids[s].tolist(), share[s]):
+                wg, wu, wd = (m[e].double() for m in self.w)
+                a = wg @ x[s]
+                y[s] += w * (wd @ (a * torch.sigmoid(a) * (wu @ x[s])))
+        return (x + y) @ self.head.double().T, k, v
+
+
+class Step:
+    """The step's buffers; everything that a replay needs stays in place."""
+
+    def __init__(self, model):
+        self.m = model
+        z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+        self.x, self.qkv, self.q, self.k = z(S, H), z(S, (HQ + 2 * HK) * D), z(S, 1, HQ, D), z(S, 1, HK, D)
+        self.a, self.logits, self.logp = z(S, 1, HQ, D), z(S, V), z(S)
+        self.tokens, self.pos = (torch.zeros(S, dtype=torch.int32, device="cuda") for _ in range(2))
+        self.u, self.temperature = z(S), z(S)
+        self.cache = T.Kv8Cache(HK, D, CTX, n_seqs=S, fmt=T.TINFER_KV8_INT8, block=16)
+
+    def run(self):
+        m, st = self.m, torch.cuda.current_stream()
+        torch.index_select(m.embed.float(), 0, self.tokens, out=self.x)
+        T._check(T.tinfer_op_gemv_batch(T.TINFER_BF16, 0, 0, (HQ + 2 * HK) * D, H, S, m.wqkv, self.x, None, T.TINFER_EPI_STORE, self.qkv, st), "qkv")
+        qkv = self.qkv.view(S, 1, HQ + 2 * HK, D)
+        T.qk_norm_rope(qkv[:, :, :HQ], qkv[:, :, HQ:HQ + HK], m.gq, m.gk, self.pos, eps=EPS, rope_theta=THETA, out=(self.q, self.k))
+        self.cache.append(self.k, qkv[:, :, HQ + HK:], self.pos)
+        self.cache.attention(self.q, self.pos, out=self.a)
+        T._check(T.tinfer_op_gemv_batch(T.TINFER_BF16, 0, 0, H, HQ * D, S, m.wo, self.a, None, T.TINFER_EPI_RESIDUAL, self.x, st), "o")
+        m.layer(self.x, out=self.x, accumulate=True)
+        T._check(T.tinfer_op_gemv_batch(T.TINFER_BF16, 0, 0, V, H, S, m.head, self.x, None, T.TINFER_EPI_STORE, self.logits, st), "head")
+        T.sample(self.logits, self.u, temperature=self.temperature, top_k=50, top_p=0.9, min_p=0.01, out=(self.tokens, self.logp))
+        self.pos.add_(1)
+
+
+def test_a_decoding_step_end_to_end():
+    model = Model(1)
+    first = torch.tensor([5, 77, 1234, 2047], dtype=torch.int32, device="cuda")
+    eager, captured = Step(model), Step(model)
+    draws = torch.rand((CTX, S), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    captured.run()  # (loads what the capture may not)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured.run()
+    for st in (eager, captured):
+        st.tokens.copy_(first)
+        st.pos.zero_()
+        st.temperature.copy_(torch.tensor([1.0, 0.7, 0.0, 1.5]))
+    zero = torch.zeros(S, dtype=torch.int32, device="cuda")
+    for step in range(20):
+        fed = eager.tokens.clone().long()
+        for st in (eager, captured):
+            st.u.copy_(draws[step])
+        eager.run()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(eager.tokens, captured.tokens) and torch.equal(eager.logits, captured.logits), step
+        assert torch.equal(eager.logp, captured.logp) and torch.equal(eager.pos, captured.pos)
+        held = eager.cache.read(step + 1, zero, dtype=torch.float32)
+        want, k, v = model.reference(fed, torch.full((S,), step, device="cuda"), held)
+        off = (eager.logits.double() - want).norm(dim=1) / want.norm(dim=1)
+        assert float(off.max()) < 2.0 ** -14, (step, off.tolist())
+        for mine, kept, scales in ((k, held[0], eager.cache.k_scales), (v, held[1], eager.cache.v_scales)):
+            unit = scales[:, :, step // 16].double()[:, :, None]
+            assert bool(((kept[:, step].double() - mine).abs() <= unit * 0.51).all())
+        # the draw is that of the logits that came out
+        x = eager.logits
+        greedy = int(x[2].argmax())
+        assert int(eager.tokens[2]) == greedy
+        assert bool((torch.gather(x, 1, eager.tokens.long()[:, None])[:, 0] >= torch.topk(x, 50, dim=1).values[:, -1]).all())
+    assert model.layer.error() == 0 and eager.cache.error() == 0 and captured.cache.error() == 0

@@ -40,3 +40,66 @@ def norm(n_seqs=2, n_tokens=3, n_heads=4, n_kv_heads=2, head_dim=64, rotary_dim=
 ])
 def test_head_norms_refuse(over, want):
     assert norm(**over) == want
+
+
+def moe(over, n_tokens=4, dtype=F32, x=A, xs=256, y=2 * A, ys=256, accumulate=0, ids=None, weights=None, ws=3 * A, ws_bytes=1 << 30,
+        status=None):
+    m = dict(weight_format=T.TINFER_INT4, group_size=64, scale_dtype=T.TINFER_SCALE_FP16, n_experts=8, top_k=2, hidden=256, ffn_e=128,
+             router_dtype=BF16, flags=T.TINFER_MOE_RENORMALISE, router=A, gu_packed=A, down_packed=A)
+    m.update(over)
+    layer = T.tinfer_moe(*(m[n] for n, _ in T.tinfer_moe._fields_))
+    return (T.tinfer_op_moe_layer(layer, n_tokens, dtype, x, xs, y, ys, accumulate, ids, weights, ws, ws_bytes, status),
+            T.tinfer_moe_layer_workspace(layer, n_tokens))
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(weight_format=2), BAD), (dict(scale_dtype=2), BAD), (dict(n_experts=0), BAD), (dict(top_k=0), BAD), (dict(top_k=9), BAD),
+    (dict(hidden=0), BAD), (dict(ffn_e=-32), BAD), (dict(router_dtype=F16), BAD), (dict(flags=2), BAD), (dict(router=None), BAD),
+    (dict(gu_packed=None), BAD), (dict(down_packed=A + 8), BAD), (dict(router=A + 2), BAD), (dict(group_size=48), NO),
+    (dict(group_size=0), NO), (dict(group_size=512), NO), (dict(n_experts=513), NO), (dict(n_experts=32, top_k=17), NO),
+    (dict(hidden=272), NO), (dict(weight_format=T.TINFER_BF16, hidden=264), NO), (dict(weight_format=T.TINFER_BF16, ffn_e=16), NO),
+    (dict(weight_format=T.TINFER_BF16, hidden=16416), NO), (dict(ffn_e=32768), NO),
+])
+def test_bad_layers_are_refused(over, want):
+    assert moe(over) == (want, 0)
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(n_tokens=0), BAD), (dict(n_tokens=-1), BAD), (dict(n_tokens=65), NO), (dict(dtype=3), BAD), (dict(x=None), BAD),
+    (dict(y=None), BAD), (dict(ws=None), BAD), (dict(x=A + 8), BAD), (dict(y=A + 4), BAD), (dict(ws=A + 8), BAD), (dict(ids=A + 2), BAD),
+    (dict(weights=A + 1), BAD), (dict(status=A + 2), BAD), (dict(accumulate=2), BAD), (dict(xs=258), BAD), (dict(xs=-256), BAD),
+    (dict(ys=128), BAD), (dict(ys=0), BAD), (dict(dtype=F16, xs=260), BAD), (dict(ws_bytes=1000), BAD),
+])
+def test_bad_rows_of_a_layer_are_refused(over, want):
+    assert moe({}, **over)[0] == want
+
+
+def test_a_row_of_activations_has_to_fit_shared_memory():
+    wide = dict(hidden=16384, ffn_e=64)
+    assert moe(wide, xs=16384, ys=16384)[0] == NO  # three parts of an fp32 row: 96 KiB a token beside the ring
+    assert moe({})[1] > 0
+
+
+def draw(rows=3, vocab=100, dtype=F32, logits=A, stride=100, u=A, ids=A, logp=None, **request):
+    s = T.tinfer_sampling(1.0, 0, 1.0, 0.0)
+    for n, v in request.items():
+        setattr(s, n, v)
+    return T.tinfer_op_sample(rows, vocab, dtype, logits, stride, u, s, ids, logp)
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(rows=0), BAD), (dict(vocab=0), BAD), (dict(dtype=3), BAD), (dict(logits=None), BAD), (dict(logits=A + 2), BAD),
+    (dict(dtype=BF16, logits=A + 1), BAD), (dict(stride=-1), BAD), (dict(u=None), BAD), (dict(u=A + 2), BAD), (dict(ids=None), BAD),
+    (dict(ids=A + 1), BAD), (dict(logp=A + 2), BAD), (dict(temperature=-1.0), BAD), (dict(temperature=float("nan")), BAD),
+    (dict(top_k=-1), BAD), (dict(top_p=-0.5), BAD), (dict(top_p=float("nan")), BAD), (dict(min_p=-0.1), BAD), (dict(min_p=1.5), BAD),
+    (dict(temperature_dev=A + 2), BAD), (dict(top_k_dev=A + 1), BAD), (dict(top_p_dev=A + 3), BAD), (dict(min_p_dev=A + 2), BAD),
+    (dict(vocab=(1 << 18) + 1, stride=1 << 19), NO), (dict(rows=(1 << 27) + 1), NO),
+])
+def test_draws_refuse(over, want):
+    assert draw(**over) == want
+
+
+def test_a_request_is_wanted():
+    assert T.lib().tinfer_op_sample(1, 1, 0, A, 1, A, None, A, None, None) == BAD
+    assert T.lib().tinfer_op_moe_layer(None, 1, 0, A, 1, A, 1, 0, None, None, A, 1 << 20, None, None) == BAD
+    assert T.lib().tinfer_moe_layer_workspace(None, 1) == 0
