@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from .build import build  # noqa: F401  (bound here once: a later import of the submodule leaves the name alone)
 
@@ -137,7 +138,7 @@ def lib():
             "tinfer_op_kv8_read": ([kvp, I, P, P, rowp, rowp, P, P], I),
             "tinfer_kv8_attention_workspace": ([kvp, I, I], Z),
             "tinfer_op_kv8_attention": ([kvp, I, I, rowp, P, P, D, rowp, P, P, Z, P, P], I),
-            "tinfer_op_qk_norm_rope": ([I, I, I, I, I, I, rowp, rowp, P, P, D, D, P, P, rowp, rowp, P, P], I),
+            "tinfer_op_qk_norm_rope": ([I, I, I, I, I, I, P, P, P, P, D, D, P, P, P, P, P, P], I),
             "tinfer_moe_layer_workspace": ([moep, I], Z),
             "tinfer_op_moe_layer": ([moep, I, I, P, LL, P, LL, I, P, P, P, Z, P, P], I),
             "tinfer_op_sample": ([I, I, I, P, LL, P, ctypes.POINTER(tinfer_sampling), P, P, P], I),
@@ -346,6 +347,7 @@ def tinfer_op_logprobs(rows, vocab, dtype, logits, row_stride, targets, top_k, l
 def tinfer_op_qk_norm_rope(n_seqs, n_tokens, n_heads, n_kv_heads, head_dim, rotary_dim, q: tinfer_rows, k: tinfer_rows,
                            q_gain, k_gain, eps, rope_theta, pos, counts, q_out: tinfer_rows, k_out: tinfer_rows,
                            status=None, stream=None) -> int:
+    q, k, q_out, k_out = (ctypes.addressof(r) for r in (q, k, q_out, k_out))
     return lib().tinfer_op_qk_norm_rope(n_seqs, n_tokens, n_heads, n_kv_heads, head_dim, rotary_dim, q, k, _ptr(q_gain),
                                         _ptr(k_gain), eps, rope_theta, _ptr(pos), _ptr(counts), q_out, k_out, _ptr(status),
                                         _stream(stream))
@@ -495,14 +497,19 @@ class Engine:
 
 # ------------------------------------------------------------------ the 8-bit cache and token scores on tensors
 
-_DTYPES: dict = {}  # torch dtype -> TINFER_DTYPE_*
+_DTYPES: dict = {}  # torch dtype -> TINFER_DTYPE_*, and torch.int32
+
+
+def _dtypes() -> None:
+    import torch
+    _DTYPES.update({torch.float32: TINFER_DTYPE_F32, torch.float16: TINFER_DTYPE_F16, torch.bfloat16: TINFER_DTYPE_BF16,
+                    "int32": torch.int32})
 
 
 def _dtype(t) -> int:
     """TINFER_DTYPE_* of a tensor (ValueError for the others)."""
     if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: TINFER_DTYPE_F32, torch.float16: TINFER_DTYPE_F16, torch.bfloat16: TINFER_DTYPE_BF16})
+        _dtypes()
     d = _DTYPES.get(t.dtype)
     if d is None:
         raise ValueError(f"float32, float16 or bfloat16 is wanted, got {t.dtype}")
@@ -712,12 +719,16 @@ def logprobs(logits, targets=None, top_k: int = 0, stream=None):
 
 def _int32s(what, t, n, device):
     """Address of an int32 argument of n values (None: no argument)."""
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.numel() != n or t.device != device or not t.is_contiguous():
+    if not _DTYPES:
+        _dtypes()
+    if t.dtype != _DTYPES["int32"] or t.numel() != n or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous int32 tensor of {n} on {device} is wanted")
     return t.data_ptr()
+
+
+_ROWS = struct.Struct("@" + "Pi4xqqq" * 4)  # four tinfer_rows one after another: packing them takes a third of four structures' time
 
 
 def qk_norm_rope(q, k, q_gain=None, k_gain=None, pos=None, counts=None, eps: float = 1e-6, rope_theta: float = 0.0,
@@ -729,36 +740,36 @@ def qk_norm_rope(q, k, q_gain=None, k_gain=None, pos=None, counts=None, eps: flo
     elements of a head are rotated (None: all), none with rope_theta 0. Results go to `out` ((q, k) itself: in place), or to new
     tensors of `dtype` (that of q when None), zero where a sequence has fewer tokens. status: int32 tensor, bit 0: positions or
     counts of a sequence were bad and it was passed over."""
-    import torch
-    device = q.device
+    device, sq, sk = q.device, q.shape, k.shape
     if device.type != "cuda":
         raise ValueError("q is not on a CUDA device")
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
-        raise ValueError(f"rows [n_seqs, n_tokens, heads, head_dim] are wanted, got {tuple(q.shape)} and {tuple(k.shape)}")
-    n_seqs, n_tokens, n_heads, head_dim = q.shape
-    if out is None:
-        with _making(stream, device):
-            out = tuple(torch.zeros(t.shape, dtype=dtype or q.dtype, device=device) for t in (q, k))
-    if pos is None:
-        if rope_theta:
+    if len(sq) != 4 or len(sk) != 4 or sq[0] != sk[0] or sq[1] != sk[1] or sq[3] != sk[3]:
+        raise ValueError(f"rows [n_seqs, n_tokens, heads, head_dim] are wanted, got {tuple(sq)} and {tuple(sk)}")
+    n_seqs, n_tokens, n_heads, head_dim = sq
+    if out is None or pos is None:
+        import torch
+        if pos is None and rope_theta:
             raise ValueError("pos is wanted where rows are rotated")
         with _making(stream, device):
-            pos = torch.zeros(n_seqs, dtype=torch.int32, device=device)
-
-    def rows(what, t, like):
-        if t.device != device or t.shape != like.shape or t.stride(3) != 1:
-            raise ValueError(f"{what}: rows {tuple(like.shape)} with contiguous elements on {device} are wanted")
-        return tinfer_rows(t.data_ptr(), _dtype(t), *t.stride()[:3])
-
+            if out is None:
+                out = tuple(torch.zeros(t.shape, dtype=dtype or q.dtype, device=device) for t in (q, k))
+            if pos is None:
+                pos = torch.zeros(n_seqs, dtype=torch.int32, device=device)
+    packed = []
+    for what, t, shape in (("q", q, sq), ("k", k, sk), ("out[0]", out[0], sq), ("out[1]", out[1], sk)):
+        stride = t.stride()
+        if t.device != device or t.shape != shape or stride[3] != 1:
+            raise ValueError(f"{what}: rows {tuple(shape)} with contiguous elements on {device} are wanted")
+        packed += (t.data_ptr(), _dtype(t), stride[0], stride[1], stride[2])
+    rows = (ctypes.c_char * _ROWS.size)()
+    _ROWS.pack_into(rows, 0, *packed)
+    at = ctypes.addressof(rows)
     for what, g in (("q_gain", q_gain), ("k_gain", k_gain)):
-        if g is not None:
-            _on(what, g, device, torch.float32, (head_dim,))
-            if not g.is_contiguous():
-                raise ValueError(f"{what} is not contiguous")
-    args = (n_seqs, n_tokens, n_heads, k.shape[2], head_dim, head_dim if rotary_dim is None else rotary_dim,
-            rows("q", q, q), rows("k", k, k), _ptr(q_gain), _ptr(k_gain), eps, rope_theta,
-            _int32s("pos", pos, n_seqs, device), _int32s("counts", counts, n_seqs, device), rows("out[0]", out[0], q),
-            rows("out[1]", out[1], k), _int32s("status", status, 1, device))
+        if g is not None and (g.device != device or _dtype(g) != TINFER_DTYPE_F32 or g.shape != (head_dim,) or not g.is_contiguous()):
+            raise ValueError(f"{what}: a contiguous float32 tensor [{head_dim}] on {device} is wanted")
+    args = (n_seqs, n_tokens, n_heads, sk[2], head_dim, head_dim if rotary_dim is None else rotary_dim, at, at + 40,
+            _ptr(q_gain), _ptr(k_gain), eps, rope_theta, _int32s("pos", pos, n_seqs, device),
+            _int32s("counts", counts, n_seqs, device), at + 80, at + 120, _int32s("status", status, 1, device))
     if n_seqs and n_tokens:  # (else nothing to launch)
         _call("tinfer_op_qk_norm_rope", lib().tinfer_op_qk_norm_rope, args, device, stream)
     return out
@@ -824,7 +835,7 @@ class MoeLayer:
             self._errors = torch.zeros(1, dtype=torch.int32, device=device)
             if workspace is None:
                 workspace = torch.zeros(need, dtype=torch.uint8, device=device)
-            self._uint8 = torch.uint8
+            self._uint8, self._int32, self._float32 = torch.uint8, torch.int32, torch.float32
             self._workspace = self._check_workspace(workspace)
             addresses = [t.data_ptr() for t in (self.router, self.gate_up, self.down)]
             self.c, self._kept = (tinfer_moe(*shape, flags | f, *addresses) for f in (0, TINFER_MOE_KEEP_STATUS))
@@ -851,36 +862,45 @@ class MoeLayer:
             torch.cuda.synchronize(self.device)
         return bits
 
+    def _new(self, x, out, ids, weights):
+        import torch
+        n = x.shape[0]
+        if out is None:
+            out = torch.empty((n, self.hidden), dtype=x.dtype, device=self.device)
+        if ids is None:
+            ids = torch.empty((n, self.top_k), dtype=torch.int32, device=self.device)
+        if weights is None:
+            weights = torch.empty((n, self.top_k), dtype=torch.float32, device=self.device)
+        return out, ids, weights
+
     def __call__(self, x, out=None, accumulate: bool = False, ids=None, weights=None, workspace=None, status=None, stream=None):
         """(y, ids, weights) of the rows x [n_tokens, hidden]: y in `out` (rows like x, x itself: in place; a new tensor when None;
         added to what it holds with accumulate), the chosen experts int32 and their weights float32 [n_tokens, top_k]."""
-        import torch
-        if x.dim() != 2 or x.shape[1] != self.hidden or x.device != self.device or (self.hidden > 1 and x.stride(1) != 1):
-            raise ValueError(f"x: rows [n_tokens, {self.hidden}] with contiguous elements on {self.device} are wanted")
-        n = x.shape[0]
+        shape, stride, device = x.shape, x.stride(), self.device
+        if len(shape) != 2 or shape[1] != self.hidden or x.device != device or stride[1] != 1:
+            raise ValueError(f"x: rows [n_tokens, {self.hidden}] with contiguous elements on {device} are wanted")
+        n = shape[0]
         dtype = _dtype(x)
-        if accumulate and out is None:
-            raise ValueError("out is wanted to add to")
-        with _making(stream, self.device):
-            if out is None:
-                out = torch.empty((n, self.hidden), dtype=x.dtype, device=self.device)
-            if ids is None:
-                ids = torch.empty((n, self.top_k), dtype=torch.int32, device=self.device)
-            if weights is None:
-                weights = torch.empty((n, self.top_k), dtype=torch.float32, device=self.device)
-        _on("out", out, self.device, x.dtype, x.shape)
-        for what, t, dt in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
-            _on(what, t, self.device, dt, (n, self.top_k))
-            if not t.is_contiguous():
-                raise ValueError(f"{what} is not contiguous")
-        if out.stride(1) != 1:
-            raise ValueError("out: the elements of a row are not contiguous")
+        if out is None or ids is None or weights is None:
+            if accumulate and out is None:
+                raise ValueError("out is wanted to add to")
+            if stream is None:
+                out, ids, weights = self._new(x, out, ids, weights)
+            else:
+                with _making(stream, device):
+                    out, ids, weights = self._new(x, out, ids, weights)
+        to = out.stride()
+        if out.shape != shape or out.dtype != x.dtype or out.device != device or to[1] != 1:
+            raise ValueError(f"out: rows {tuple(shape)} like x are wanted")
+        if (ids.dtype != self._int32 or weights.dtype != self._float32 or ids.shape != (n, self.top_k) or weights.shape != ids.shape
+                or ids.device != device or weights.device != device or not ids.is_contiguous() or not weights.is_contiguous()):
+            raise ValueError(f"ids and weights: contiguous int32 and float32 tensors [{n}, {self.top_k}] on {device} are wanted")
         if n == 0:
             return out, ids, weights  # nothing to launch
         workspace = self._workspace if workspace is None else self._check_workspace(workspace)
         c, word = (self._kept, self._errors.data_ptr()) if status is None else (self.c, _int32s("status", status, 1, self.device))
         _call("tinfer_op_moe_layer", lib().tinfer_op_moe_layer,
-              (c, n, dtype, x.data_ptr(), x.stride(0), out.data_ptr(), out.stride(0), int(accumulate), ids.data_ptr(),
+              (c, n, dtype, x.data_ptr(), stride[0], out.data_ptr(), to[0], int(accumulate), ids.data_ptr(),
                weights.data_ptr(), workspace.data_ptr(), workspace.numel(), word), self.device, stream)
         return out, ids, weights
 
@@ -891,28 +911,33 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, 
     Each of these is a number, or a tensor [rows] (int32 for top_k, float32 for the others) with one for each row. out: (ids, logp)
     to write to instead of new tensors; its logp may be None."""
     import torch
-    if logits.dim() != 2 or logits.stride(1) != 1 or logits.device.type != "cuda":
+    shape, stride, dev = logits.shape, logits.stride(), logits.device
+    if len(shape) != 2 or stride[1] != 1 or dev.type != "cuda":
         raise ValueError("logits: [rows, vocab] on a CUDA device with contiguous rows is wanted")
-    rows, vocab = logits.shape
-    dev, dtype = logits.device, _dtype(logits)
+    rows, vocab = shape
+    dtype = _dtype(logits)
 
     def words(what, t, dt):
         if t.dtype != dt or t.shape != (rows,) or t.device != dev or not t.is_contiguous():
             raise ValueError(f"{what}: a contiguous {dt} tensor [{rows}] on {dev} is wanted")
         return t.data_ptr()
 
-    s = tinfer_sampling(1.0, 0, 1.0, 0.0)
-    for what, v in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p)):
+    given, at = [1.0, 0, 1.0, 0.0], [None] * 4
+    for i, (what, v) in enumerate((("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p))):
         if isinstance(v, torch.Tensor):
-            setattr(s, what + "_dev", words(what, v, torch.int32 if what == "top_k" else torch.float32))
+            at[i] = words(what, v, torch.int32 if i == 1 else torch.float32)
         else:
-            setattr(s, what, min(int(v), 0x7FFFFFFF) if what == "top_k" else float(v))
+            given[i] = min(int(v), 0x7FFFFFFF) if i == 1 else float(v)
     if out is None:
-        with _making(stream, dev):
+        if stream is None:
             out = torch.empty(rows, dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.float32, device=dev)
+        else:
+            with _making(stream, dev):
+                out = torch.empty(rows, dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.float32, device=dev)
     ids, logp = out
-    args = (rows, vocab, dtype, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, words("u", u, torch.float32), s,
-            words("out[0]", ids, torch.int32), None if logp is None else words("out[1]", logp, torch.float32))
+    args = (rows, vocab, dtype, logits.data_ptr(), stride[0] if rows > 1 else vocab, words("u", u, torch.float32),
+            tinfer_sampling(*given, *at), words("out[0]", ids, torch.int32),
+            None if logp is None else words("out[1]", logp, torch.float32))
     if rows:  # (else nothing to launch)
         _call("tinfer_op_sample", lib().tinfer_op_sample, args, dev, stream)
     return ids, logp

@@ -38,11 +38,14 @@ constexpr int NT = 512, NWARPS = NT / 32, MAX_CLUSTER = 8;
 constexpr int MAX_VOCAB = 1 << 18;
 constexpr int LIST = 2048;           // listed candidates of a row, at most
 constexpr int BINS = 2048;           // of the distance from the maximum, in units of log2 of the weight
-constexpr float PER_LOG2 = 51.2f;    // bins to a factor of two: weights down to 2^-40 are told apart
-// A token adds its weight to its bin in units of 2^-14 of the bin's largest, linear in its distance: off by 2.3e-5 of itself for
-// the bin's curvature (its width, 0.0135 in the exponent, squared over 8) and 3e-5 for the rounding. The nucleus' border is
-// looked for as far of the sum either side of where the bins put it.
-constexpr float WINDOW = 6e-5f;
+constexpr float RANGE = 40.f;        // that they span at most: weights down to 2^-40 are told apart
+constexpr float MASK = -6e4f;        // logits from here down are taken for masks when the bins' span is chosen
+// A token adds its weight to its bin in units of 2^-14 of the bin's largest, linear in its distance: off by 2.3e-5 of itself at most for
+// the bin's curvature (its width, 0.0135 in the exponent, squared over 8), 3e-5 for the rounding and 7e-6 for the distance's, all
+// with one sign where logits are equal or on the lattice of a 16-bit type: 6e-5 of what lies above the nucleus' border, or,
+// counted from the other end, below it, and as much of the sum that the border is a part of. As far either side of where
+// the bins put it the border is looked for, and by what their fp32 sums are off.
+constexpr float WINDOW = 1.2e-4f, SUMS = 2e-6f;
 constexpr unsigned WHOLE = 16383;    // units: 2^18 tokens of them stay below 2^32
 constexpr int PER = LIST / NT;       // of a list, or of the bins, to a thread
 static_assert(LIST == BINS, "alike for both");
@@ -64,7 +67,7 @@ struct Smem {
   float2 table[64];                 // 2^(i / 64) in two parts
   u64 sums[MAX_CLUSTER][NWARPS];    // kept weights of each warp of the cluster (in the first CTA)
   u64 red[NWARPS], cross[2][MAX_CLUSTER];
-  float redf[NWARPS], crossf[MAX_CLUSTER];
+  float redf[NWARPS], redl[NWARPS], crossf[2][MAX_CLUSTER];
   uint16_t owner[NT];
   int owners, own, listed[2], count[2];
   unsigned floor_key;
@@ -170,7 +173,7 @@ __device__ __forceinline__ void weights(float2 x, float m, float ch, float cl, c
 }
 __device__ __noinline__ u64 weight_once(float x, float m, float ch, float cl, const float2* table) { return weight(x, m, ch, cl, table); }
 
-// The distance from the maximum in 1024ths of a bin, above ROUND_BINS. per = ch * PER_LOG2 * 1024.
+// The distance from the maximum in 1024ths of a bin, above ROUND_BINS. per: 1024 bins to a factor of two of the weight, times ch.
 constexpr float ROUND_BINS = 12582912.f;  // 1.5 * 2^23
 __device__ __forceinline__ float distance(float x, float m, float per) {
   return __fadd_rn(fminf(__fmul_rn(m - x, per), (float)(BINS * 1024 - 1)), ROUND_BINS);
@@ -452,18 +455,49 @@ struct Draw {
     }
   }
   // The border, bit by bit: the last kept token is the one at which the count (or the weights) of the kept ones reaches
-  // `limit`. For lists that overflow.
-  __device__ __noinline__ void search(bool mass, u64 limit) {
+  // `limit`. For lists that overflow. Tokens whose distance is not in [below, within] do not count; false: those that do
+  // fall short of the limit.
+  __device__ __noinline__ bool search(bool mass, u64 limit, float per, float below, float within) {
+    auto counts = [&](float x, int id) {
+      const float d = distance(x, m, per);
+      return x > -INFINITY && d >= below && d <= within && kept(x, id);
+    };
     auto reached = [&](unsigned from) {
       u64 s = 0;
       in.template walk<1>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
-        if (x > -INFINITY && kept(x, id) && ordered(x) >= from) s += mass ? weight_once(x, m, ch, cl, sm.table) : 1;
+        if (ordered(x) >= from && counts(x, id)) s += mass ? weight_once(x, m, ch, cl, sm.table) : 1;
       });
       return sum(s);
     };
-    if (reached(0) < limit) return;  // all
-    unsigned key = 0;
-    for (int bit = 31; bit >= 0; --bit)
+    if (reached(0) < limit) return false;
+    // the bits that all of them share need no search
+    unsigned most = 0, least_key = 0xFFFFFFFFu;
+    in.template walk<1>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
+      if (counts(x, id)) {
+        most = max(most, ordered(x));
+        least_key = min(least_key, ordered(x));
+      }
+    });
+    most = __reduce_max_sync(~0u, most);
+    least_key = __reduce_min_sync(~0u, least_key);
+    if (lane == 0) sm.red[warp] = (u64)most << 32 | least_key;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 0; w < NWARPS; ++w) {
+        most = max(most, (unsigned)(sm.red[w] >> 32));
+        least_key = min(least_key, (unsigned)sm.red[w]);
+      }
+      tell(&sm.cross[parity][rank], (u64)most << 32 | least_key);
+    }
+    meet();
+    for (int r = 0; r < size; ++r) {
+      most = max(most, (unsigned)(sm.cross[parity][r] >> 32));
+      least_key = min(least_key, (unsigned)sm.cross[parity][r]);
+    }
+    parity ^= 1;
+    const int top = 31 - __clz((most ^ least_key) | 1);
+    unsigned key = most & ~((2u << top) - 1);
+    for (int bit = top; bit >= 0; --bit)
       if (reached(key | 1u << bit) >= limit) key |= 1u << bit;
     const u64 above = key == 0xFFFFFFFFu ? 0 : reached(key + 1);
     const u64 each = mass ? weight_once(unordered(key), m, ch, cl, sm.table) : 1;
@@ -472,6 +506,7 @@ struct Draw {
     find(1, key, nth, [&](int id, u64) { tell(&sm.tau, (u64)key << 32 | (unsigned)~id); });
     meet();
     tau = sm.tau;
+    return true;
   }
   // A CTA's candidates (in sm.mass) to the first CTA's list; the row's number of them.
   __device__ __forceinline__ int collect(int which) {
@@ -563,10 +598,14 @@ __device__ __forceinline__ void Draw<T>::run() {
 
   // ---- the maximum
   float each[MAXIMA] = {-INFINITY, -INFINITY};  // of the thread's words in turn
+  float least_x = INFINITY;
   in.template walk_words<4>(in.first(warp), in.first(warp + 1), [&](const float(&x)[Slice<T>::N], int) {
     float y = x[0];
 #pragma unroll
     for (int i = 1; i < Slice<T>::N; ++i) y = max_nan(y, x[i]);
+    if (nucleus)
+#pragma unroll
+      for (int i = 0; i < Slice<T>::N; ++i) least_x = fminf(least_x, x[i] > MASK ? x[i] : INFINITY);
     const float other = each[0];
     each[0] = max_nan(each[1], y);
     each[1] = other;
@@ -574,20 +613,36 @@ __device__ __forceinline__ void Draw<T>::run() {
   const float mine = max_nan(each[0], each[1]);
   float top = mine;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
-  if (lane == 0) sm.redf[warp] = top;
+  for (int o = 16; o; o >>= 1) {
+    top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+    least_x = fminf(least_x, __shfl_xor_sync(~0u, least_x, o));
+  }
+  if (lane == 0) {
+    sm.redf[warp] = top;
+    sm.redl[warp] = least_x;
+  }
   __syncthreads();
-  for (int w = 0; w < NWARPS; ++w) top = max_nan(top, sm.redf[w]);
+  for (int w = 0; w < NWARPS; ++w) {
+    top = max_nan(top, sm.redf[w]);
+    least_x = fminf(least_x, sm.redl[w]);
+  }
   cluster.barrier_wait(std::move(started));
-  if (tid == 0) tell(&sm.crossf[rank], top);
+  if (tid == 0) {
+    tell(&sm.crossf[0][rank], top);
+    tell(&sm.crossf[1][rank], least_x);
+  }
   const bool by_rank = k && k <= MAXIMA * NT * size;
   unsigned* maxima = reinterpret_cast<unsigned*>(in_first(sm.key));  // (reaching into `mass`)
   if (by_rank)
 #pragma unroll
     for (int i = 0; i < MAXIMA; ++i) maxima[(rank * MAXIMA + i) * NT + tid] = each[i] > -INFINITY ? ordered(each[i]) : 0;
   meet();
-  m = sm.crossf[0];
-  for (int r = 1; r < size; ++r) m = max_nan(m, sm.crossf[r]);
+  m = sm.crossf[0][0];
+  least_x = sm.crossf[1][0];
+  for (int r = 1; r < size; ++r) {
+    m = max_nan(m, sm.crossf[0][r]);
+    least_x = fminf(least_x, sm.crossf[1][r]);
+  }
   ch = sm.ch;
   cl = sm.cl;
   least = sm.least;
@@ -720,14 +775,16 @@ __device__ __forceinline__ void Draw<T>::run() {
   }
 
   // ---- many: the nucleus' border to a few bins
-  if (k) search(false, (u64)k);
+  if (k) search(false, (u64)k, 1.f, -INFINITY, INFINITY);
   int lo = BINS, hi = BINS;
+  // the bins span the row's own range, so that a row of near logits does not fall into a few of them
+  const float per_log2 = (float)BINS / fminf(fmaxf((m - least_x) * ch * 1.001f, 1e-6f), RANGE), per = ch * per_log2 * 1024.f;
   if (nucleus) {
-    const float per = ch * (PER_LOG2 * 1024.f);
+    const unsigned slope = (unsigned)((1.f - exp2f(-1.f / per_log2)) * (WHOLE * 16.f) + 0.5f);  // of a bin's weights, in 2^-14 of a unit to a 1024th
     in.template walk<2>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
       if (x > -INFINITY && (!tau || kept(x, id))) {
         const unsigned b = __float_as_uint(distance(x, m, per)) - __float_as_uint(ROUND_BINS);
-        atomicAdd(&sm.hist[b >> 10], WHOLE - ((b & 1023) * 3524 >> 14));  // (2^(-1 / PER_LOG2) = 1 - 1023 * 3524 / 2^14 / WHOLE)
+        atomicAdd(&sm.hist[b >> 10], WHOLE - ((b & 1023) * slope + 8192 >> 14));
       }
     });
     __syncthreads();
@@ -740,7 +797,7 @@ __device__ __forceinline__ void Draw<T>::run() {
     if (rank == 0) {
       float w[PER], s = 0.f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) s += w[i] = (float)sm.hist[tid * PER + i] * exp2f((float)(tid * PER + i) * (-1.f / PER_LOG2));
+      for (int i = 0; i < PER; ++i) s += w[i] = (float)sm.hist[tid * PER + i] * exp2f((float)(tid * PER + i) * (-1.f / per_log2));
       float incl = s;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
@@ -756,11 +813,12 @@ __device__ __forceinline__ void Draw<T>::run() {
         all += sm.redf[i];
       }
       float at = incl - s;
+      const float window = fmaxf(WINDOW * fminf(p, 1.f - p), SUMS);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         at += w[i];
-        if (at >= (p - WINDOW) * all) atomicMin(&sm.lo, tid * PER + i);
-        if (at >= (p + WINDOW) * all) atomicMin(&sm.hi, tid * PER + i);
+        if (at >= (p - window) * all) atomicMin(&sm.lo, tid * PER + i);
+        if (at >= (p + window) * all) atomicMin(&sm.hi, tid * PER + i);
       }
       __syncthreads();
       const int a = sm.lo, b = sm.hi;
@@ -777,7 +835,6 @@ __device__ __forceinline__ void Draw<T>::run() {
 
   // ---- the weights: all, those above the border's bins, and of these what min-p keeps; the tokens within the bins
   u64 all = 0, above = 0, keep = 0;
-  const float per_bin = ch * (PER_LOG2 * 1024.f);
   const float below = nucleus ? ROUND_BINS + (float)(lo * 1024) : INFINITY, within = nucleus ? ROUND_BINS + (float)(hi * 1024 + 1023) : -INFINITY;
   in.template walk_words<1>(in.first(warp), in.first(warp + 1), [&](const float(&x)[Slice<T>::N], int first) {
 #pragma unroll 2
@@ -785,7 +842,7 @@ __device__ __forceinline__ void Draw<T>::run() {
       const float v0 = x[i], v1 = x[i + 1];
       u64 w0, w1;
       weights(make_float2(v0, v1), m, ch, cl, sm.table, w0, w1);
-      const float d0 = distance(v0, m, per_bin), d1 = distance(v1, m, per_bin);
+      const float d0 = distance(v0, m, per), d1 = distance(v1, m, per);
       bool in0 = d0 >= below && d0 <= within && v0 > -INFINITY, in1 = d1 >= below && d1 <= within && v1 > -INFINITY;
       if (tau) {
         if (!kept(v0, first + i)) w0 = in0 = 0;
@@ -845,7 +902,7 @@ __device__ __forceinline__ void Draw<T>::run() {
     if (sm.tau) {
       tau = sm.tau;
     } else {
-      search(true, limit);
+      if (above >= limit || !search(true, limit - above, per, below, within)) search(true, limit, per, -INFINITY, INFINITY);
       tally(0, 0);
     }
   } else {
