@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import sys
 
 from .build import build  # noqa: F401  (bound here once: a later import of the submodule leaves the name alone)
 
@@ -519,7 +520,7 @@ def _dtype(t) -> int:
 def _call(what, fn, args, device, stream) -> None:
     """Calls fn(*args, stream) with `device` current, on `stream` or torch's current one; raises on an error status.
     The raw getters are what torch.cuda's own wrappers call: a step's small calls are a few microseconds on the GPU."""
-    import torch
+    torch = sys.modules["torch"]  # (there is a tensor)
     index = device.index
     stream = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
     if torch._C._cuda_getDevice() == index:
@@ -718,9 +719,7 @@ def logprobs(logits, targets=None, top_k: int = 0, stream=None):
 
 
 def _int32s(what, t, n, device):
-    """Address of an int32 argument of n values (None: no argument)."""
-    if t is None:
-        return None
+    """Address of an int32 argument of n values."""
     if not _DTYPES:
         _dtypes()
     if t.dtype != _DTYPES["int32"] or t.numel() != n or t.device != device or not t.is_contiguous():
@@ -755,21 +754,28 @@ def qk_norm_rope(q, k, q_gain=None, k_gain=None, pos=None, counts=None, eps: flo
                 out = tuple(torch.zeros(t.shape, dtype=dtype or q.dtype, device=device) for t in (q, k))
             if pos is None:
                 pos = torch.zeros(n_seqs, dtype=torch.int32, device=device)
-    packed = []
-    for what, t, shape in (("q", q, sq), ("k", k, sk), ("out[0]", out[0], sq), ("out[1]", out[1], sk)):
-        stride = t.stride()
-        if t.device != device or t.shape != shape or stride[3] != 1:
-            raise ValueError(f"{what}: rows {tuple(shape)} with contiguous elements on {device} are wanted")
-        packed += (t.data_ptr(), _dtype(t), stride[0], stride[1], stride[2])
-    rows = (ctypes.c_char * _ROWS.size)()
-    _ROWS.pack_into(rows, 0, *packed)
+    qo, ko = out
+    tq, tk, tqo, tko = q.stride(), k.stride(), qo.stride(), ko.stride()
+    if (k.device != device or qo.device != device or ko.device != device or qo.shape != sq or ko.shape != sk or tq[3] != 1
+            or tk[3] != 1 or tqo[3] != 1 or tko[3] != 1):
+        raise ValueError(f"q, k and their outputs: rows {tuple(sq)} and {tuple(sk)} with contiguous elements on {device} are wanted")
+    dt, dto = _dtype(q), _dtype(qo)
+    if k.dtype != q.dtype or ko.dtype != qo.dtype:
+        raise ValueError("q and k, and their outputs, have one dtype each")
+    rows = (ctypes.c_char * 160)()
+    _ROWS.pack_into(rows, 0, q.data_ptr(), dt, tq[0], tq[1], tq[2], k.data_ptr(), dt, tk[0], tk[1], tk[2],
+                    qo.data_ptr(), dto, tqo[0], tqo[1], tqo[2], ko.data_ptr(), dto, tko[0], tko[1], tko[2])
     at = ctypes.addressof(rows)
-    for what, g in (("q_gain", q_gain), ("k_gain", k_gain)):
-        if g is not None and (g.device != device or _dtype(g) != TINFER_DTYPE_F32 or g.shape != (head_dim,) or not g.is_contiguous()):
-            raise ValueError(f"{what}: a contiguous float32 tensor [{head_dim}] on {device} is wanted")
+    gains = [None, None]
+    for i, g in enumerate((q_gain, k_gain)):
+        if g is not None:
+            if g.device != device or _dtype(g) != TINFER_DTYPE_F32 or g.shape != (head_dim,) or not g.is_contiguous():
+                raise ValueError(f"gains: contiguous float32 tensors [{head_dim}] on {device} are wanted")
+            gains[i] = g.data_ptr()
     args = (n_seqs, n_tokens, n_heads, sk[2], head_dim, head_dim if rotary_dim is None else rotary_dim, at, at + 40,
-            _ptr(q_gain), _ptr(k_gain), eps, rope_theta, _int32s("pos", pos, n_seqs, device),
-            _int32s("counts", counts, n_seqs, device), at + 80, at + 120, _int32s("status", status, 1, device))
+            gains[0], gains[1], eps, rope_theta, _int32s("pos", pos, n_seqs, device),
+            None if counts is None else _int32s("counts", counts, n_seqs, device), at + 80, at + 120,
+            None if status is None else _int32s("status", status, 1, device))
     if n_seqs and n_tokens:  # (else nothing to launch)
         _call("tinfer_op_qk_norm_rope", lib().tinfer_op_qk_norm_rope, args, device, stream)
     return out

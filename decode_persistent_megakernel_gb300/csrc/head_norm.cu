@@ -8,10 +8,10 @@
 // addition; the angles of the CTA's tokens are computed once for all heads, into shared memory, while the first rows are
 // on their way. Elements are read and written by the same thread, so rows may be normalised in place.
 //
-// Measured: 8 sequences of 4095 tokens, 14 heads of 128, bf16 (235 MB): 48.5 us, 0.72 of the measured copy rate; one token of 40
+// Measured: 8 sequences of 4095 tokens, 14 heads of 128, bf16 (235 MB): 47.9 us, 0.72 of the measured copy rate; one token of 40
 // heads of 64, fp32: 3.5 us. The first took 105 us with several heads to a thread (the frequencies, read one by one from
 // the parameters for each few tokens), 64 to 76 with a token to a warp (addresses, gains and angles anew for each
-// token: 370 instructions a turn). Two rows in flight take 50.7, four 54 (they spill), 16 turns 49.4, 5 turns 51.5.
+// token: 370 instructions a turn). Two rows in flight take 50.7, four 54 (they spill), 8 turns 48.4, 16 turns 49.4, 5 turns 51.5.
 #include <algorithm>
 #include <cmath>
 
@@ -222,18 +222,29 @@ extern "C" tinfer_status tinfer_op_qk_norm_rope(int n_seqs, int n_tokens, int n_
   p.eps = (float)eps;
   p.inv_d = 1.f / (float)head_dim;
   for (p.lanes = 1; p.lanes * 16 < head_dim;) p.lanes *= 2;
-  for (int i = 0; i < p.rotary / 2; ++i)  // turns of 2^-64; see kv8::Rope
-    p.freq[i] = (unsigned long long)(std::pow(rope_theta, -2.0 * i / p.rotary) * 0.15915494309189533577 * 18446744073709551616.0);
+  // turns of 2^-64 (see kv8::Rope); a program's calls have one base and width, and the powers would be most of a call
+  static thread_local struct {
+    double theta;
+    int rotary;
+    unsigned long long freq[head_norm::MAX_D / 2];
+  } last{};
+  if (p.rotary && (last.theta != rope_theta || last.rotary != p.rotary)) {
+    for (int i = 0; i < p.rotary / 2; ++i)
+      last.freq[i] = (unsigned long long)(std::pow(rope_theta, -2.0 * i / p.rotary) * 0.15915494309189533577 * 18446744073709551616.0);
+    last.theta = rope_theta;
+    last.rotary = p.rotary;
+  }
+  std::copy(last.freq, last.freq + p.rotary / 2, p.freq);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return TINFER_ERR_CUDA;
   // a CTA has whole warps of heads, as many of a token's as it has threads for, and several tokens at a time where
-  // heads are few; it walks over as many tokens as leave four CTAs for each SM, up to 8 turns and the angles' room
+  // heads are few; it walks over as many tokens as leave four CTAs for each SM, up to 12 turns and the angles' room
   const int rows = 32 / p.lanes, most = head_norm::MAX_NT / p.lanes;
   p.blocks = (p.heads + most - 1) / most;
   p.per = ((p.heads + p.blocks - 1) / p.blocks + rows - 1) / rows * rows;
   p.slots = std::min(most / p.per, n_tokens);
-  const int half = std::max(p.rotary / 2, 1), room = std::min(8, head_norm::ANGLES / half / p.slots);
+  const int half = std::max(p.rotary / 2, 1), room = std::min(12, head_norm::ANGLES / half / p.slots);
   const long long per_turn = (long long)n_seqs * ((n_tokens + p.slots - 1) / p.slots) * p.blocks;
   p.chunk = p.slots * (int)std::max<long long>(1, std::min<long long>(room, per_turn / (4 * sms)));
   p.chunks = (n_tokens + p.chunk - 1) / p.chunk;
