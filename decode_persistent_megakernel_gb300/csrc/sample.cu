@@ -66,7 +66,7 @@ struct Smem {
   u64 key[LIST], mass[LIST];        // the first CTA's list; `mass` also a CTA's own candidates
   float2 table[64];                 // 2^(i / 64) in two parts
   u64 sums[MAX_CLUSTER][NWARPS];    // kept weights of each warp of the cluster (in the first CTA)
-  u64 red[NWARPS], cross[2][MAX_CLUSTER];
+  u64 red[NWARPS], red2[NWARPS], cross[2][MAX_CLUSTER], cross2[2][MAX_CLUSTER];
   float redf[NWARPS], redl[NWARPS], crossf[2][MAX_CLUSTER];
   uint16_t owner[NT];
   int owners, own, listed[2], count[2];
@@ -165,8 +165,9 @@ __device__ __forceinline__ void weights(float2 x, float m, float ch, float cl, c
   const float2 s = add(u, two(1.5f)), s2 = add(add(sub(u, add(s, two(-1.5f))), ul), two(3.57627869e-7f));
   auto whole = [](float h, float s, float s2, int k, float np) {
     const int high = __float_as_int(h) - 0x3F800000 + 0x800000 + (__float_as_int(s) - 0x3FC00000);
-    const long long w = ((long long)high << 22) + (__float_as_int(s2) - 0x34C00000);
-    return np < 46.5f ? (u64)((w * 2 >> min(-(k >> 6), 63)) + 1) >> 1 : 0ull;
+    const int rest = __float_as_int(s2) - 0x34C00000;
+    const long long w2 = ((long long)high << 23) + (rest + rest);  // twice the whole number
+    return np < 46.5f ? (u64)((w2 >> min(-(k >> 6), 63)) + 1) >> 1 : 0ull;
   };
   w0 = whole(h.x, s.x, s2.x, k0, np.x);
   w1 = whole(h.y, s.y, s2.y, k1, np.y);
@@ -332,21 +333,35 @@ struct Draw {
   __device__ __forceinline__ void tell(V* p, V v) {  // to every CTA, by one thread
     for (int r = 0; r < size; ++r) *(size > 1 ? cluster.map_shared_rank(p, r) : p) = v;
   }
-  __device__ u64 sum(u64 v) {  // over the cluster
-    v = warp_sum(v);
+  __device__ void sums(u64& a, u64& b) {  // over the cluster
+    a = warp_sum(a);
+    b = warp_sum(b);
     __syncthreads();
-    if (lane == 0) sm.red[warp] = v;
+    if (lane == 0) {
+      sm.red[warp] = a;
+      sm.red2[warp] = b;
+    }
     __syncthreads();
-    if (tid == 0) {
-      u64 all = 0;
-      for (int w = 0; w < NWARPS; ++w) all += sm.red[w];
-      tell(&sm.cross[parity][rank], all);
+    if (warp == 0) {
+      a = warp_sum(lane < NWARPS ? sm.red[lane] : 0);
+      b = warp_sum(lane < NWARPS ? sm.red2[lane] : 0);
+      if (lane == 0) {
+        tell(&sm.cross[parity][rank], a);
+        tell(&sm.cross2[parity][rank], b);
+      }
     }
     meet();
-    u64 all = 0;
-    for (int r = 0; r < size; ++r) all += sm.cross[parity][r];
+    a = b = 0;
+    for (int r = 0; r < size; ++r) {
+      a += sm.cross[parity][r];
+      b += sm.cross2[parity][r];
+    }
     parity ^= 1;
-    return all;
+  }
+  __device__ u64 sum(u64 v) {
+    u64 none = 0;
+    sums(v, none);
+    return v;
   }
   __device__ __forceinline__ bool kept(float x, int id) const { return pair_of(x, id) >= tau; }
   // What the tokens of a word add: their weights if they are kept (KIND 0), one if they have this key (KIND 1).
@@ -633,9 +648,15 @@ __device__ __forceinline__ void Draw<T>::run() {
   }
   const bool by_rank = k && k <= MAXIMA * NT * size;
   unsigned* maxima = reinterpret_cast<unsigned*>(in_first(sm.key));  // (reaching into `mass`)
-  if (by_rank)
+  const int lists = k > NT * size ? size * MAXIMA : size;  // of maxima: a thread's one, or both where one of each is too few
+  if (by_rank) {
+    if (lists == size) {
+      maxima[rank * NT + tid] = mine > -INFINITY ? ordered(mine) : 0;
+    } else {
 #pragma unroll
-    for (int i = 0; i < MAXIMA; ++i) maxima[(rank * MAXIMA + i) * NT + tid] = each[i] > -INFINITY ? ordered(each[i]) : 0;
+      for (int i = 0; i < MAXIMA; ++i) maxima[(rank * MAXIMA + i) * NT + tid] = each[i] > -INFINITY ? ordered(each[i]) : 0;
+    }
+  }
   meet();
   m = sm.crossf[0][0];
   least_x = sm.crossf[1][0];
@@ -664,13 +685,13 @@ __device__ __forceinline__ void Draw<T>::run() {
   if (few) {
     unsigned floor_key = 1;
     if (k) {
-      // the k-th largest of the threads' maxima is reached by k tokens; to nine bits from the first in which they differ from
-      // the largest on, which lets few others in
+      // the k-th largest of the threads' maxima is reached by k tokens; to ten bits from the first in which they differ on,
+      // which lets few others in
       if (rank == 0) {
         unsigned own[MAX_CLUSTER * MAXIMA], least_key = 0xFFFFFFFFu, there = 0;
 #pragma unroll
         for (int r = 0; r < MAX_CLUSTER * MAXIMA; ++r) {
-          own[r] = r < size * MAXIMA ? maxima[r * NT + tid] : 0;
+          own[r] = r < lists ? maxima[r * NT + tid] : 0;
           if (own[r]) least_key = min(least_key, own[r]);
           there += own[r] != 0;
         }
@@ -685,20 +706,33 @@ __device__ __forceinline__ void Draw<T>::run() {
         least_key = __reduce_min_sync(~0u, counts[lane & (NWARPS - 1)]);
         there = __reduce_add_sync(~0u, lane < NWARPS ? counts[NWARPS + lane] : 0u);
         __syncthreads();
-        const int from_bit = 31 - __clz((least_key ^ ordered(m)) | 1), to_bit = max(from_bit - 9, 0);
-        unsigned key = ordered(m) & ~(((1u << from_bit) - 1) << 1 | 1);  // (what all have in common)
+        int bit = 30 - __clz((least_key ^ ordered(m)) | 1);  // of pairs of bits, the lower one; the first pair holds that bit
+        bit = max(bit, 0);
+        unsigned key = bit < 30 ? ordered(m) & ~((4u << bit) - 1) : 0;  // (what all have in common)
 #pragma unroll 1
-        for (int bit = from_bit; bit >= to_bit; --bit) {
-          const unsigned from = key | 1u << bit;
-          int n = 0;
+        for (int turn = 0; turn < 5; ++turn) {
+          // how many reach each of the pair's three values, two counts to a word (there are 2^13 at most)
+          const unsigned step = 1u << bit;
+          unsigned n12 = 0, n3 = 0;
 #pragma unroll
-          for (int r = 0; r < MAX_CLUSTER * MAXIMA; ++r) n += own[r] >= from;
-          n = (int)__reduce_add_sync(~0u, (unsigned)n);
-          counts = reinterpret_cast<unsigned*>(sm.red) + (bit & 1) * NWARPS;
-          if (lane == 0) counts[warp] = (unsigned)n;
+          for (int r = 0; r < MAX_CLUSTER * MAXIMA; ++r) {
+            if (r >= lists) break;
+            n12 += (own[r] >= key + step ? 1u : 0u) + (own[r] >= key + 2 * step ? 1u << 16 : 0u);
+            n3 += own[r] >= key + 3 * step;
+          }
+          n12 = __reduce_add_sync(~0u, n12);
+          n3 = __reduce_add_sync(~0u, n3);
+          unsigned* counts = reinterpret_cast<unsigned*>(turn & 1 ? sm.red2 : sm.red);
+          if (lane == 0) {
+            counts[warp] = n12;
+            counts[NWARPS + warp] = n3;
+          }
           __syncthreads();
-          n = (int)__reduce_add_sync(~0u, lane < NWARPS ? counts[lane] : 0u);
-          if (n >= k) key = from;
+          n12 = __reduce_add_sync(~0u, lane < NWARPS ? counts[lane] : 0u);
+          n3 = __reduce_add_sync(~0u, lane < NWARPS ? counts[NWARPS + lane] : 0u);
+          key += ((int)n3 >= k ? 3 : (int)(n12 >> 16) >= k ? 2 : (int)(n12 & 0xFFFF) >= k ? 1 : 0) * step;
+          if (bit == 0) break;
+          bit = max(bit - 2, 0);
         }
         if (tid == 0) tell(&sm.floor_key, (int)there >= k && key > 1u ? key : 1u);
       }
@@ -813,12 +847,19 @@ __device__ __forceinline__ void Draw<T>::run() {
         all += sm.redf[i];
       }
       float at = incl - s;
+      int first_lo = BINS - 1, first_hi = BINS - 1;
       const float window = fmaxf(WINDOW * fminf(p, 1.f - p), SUMS);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         at += w[i];
-        if (at >= (p - window) * all) atomicMin(&sm.lo, tid * PER + i);
-        if (at >= (p + window) * all) atomicMin(&sm.hi, tid * PER + i);
+        if (at >= (p - window) * all) first_lo = min(first_lo, tid * PER + i);
+        if (at >= (p + window) * all) first_hi = min(first_hi, tid * PER + i);
+      }
+      first_lo = __reduce_min_sync(~0u, first_lo);
+      first_hi = __reduce_min_sync(~0u, first_hi);
+      if (lane == 0) {
+        atomicMin(&sm.lo, first_lo);
+        atomicMin(&sm.hi, first_hi);
       }
       __syncthreads();
       const int a = sm.lo, b = sm.hi;
@@ -861,8 +902,7 @@ __device__ __forceinline__ void Draw<T>::run() {
   keep = warp_sum(keep);
   if (lane == 0) in_first(&sm.sums[rank][warp])[0] = keep;
   if (nucleus) {
-    all = sum(all);
-    above = sum(above);
+    sums(all, above);
     bool more;
     u64 limit = p > 0.f ? part_of(p, all, more) : 0;
     if (p > 0.f && more) ++limit;
