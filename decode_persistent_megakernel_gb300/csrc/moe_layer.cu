@@ -17,7 +17,12 @@
 // A CTA takes a run of items, each G tiles of rows; a tile's inputs are split over 16 / G warps, whose sums meet in shared
 // memory. Each warp streams its own part of the weights through a ring of asynchronous copies that runs on across items,
 // experts and, into the down products, across the barrier: no warp waits for another's copies. The activations stay in
-// shared memory.
+// shared memory, split into their parts once; the parts of one or two tokens are columns of one product.
+//
+// Measured (64 experts of 1024, top 8, hidden 2048): 8 fp32 tokens over bf16 experts (529 MB) 98 us, 0.80 of the measured copy rate, of
+// which the products are 84; 64 bf16 tokens (806 MB) 192; one fp32 token over 4-bit experts (27 MB) 27, the chain of
+// the phases. Parts split again at each use took 140, 230 and 42; units of 1 KiB 108, 220 and 30. The code of a phase is
+// kept small where it runs once: instruction fetch was the largest stall of the first form, and is still that of one token.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
