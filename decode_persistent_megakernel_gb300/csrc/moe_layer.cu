@@ -43,6 +43,7 @@ namespace moe {
 constexpr int NT = 512, NW = NT / 32;
 constexpr int MAX_TOKENS = 64, MAX_K = 16, MAX_EXPERTS = 512, MAX_WIDTH = 16384;
 constexpr int COLS = 16;         // tokens of an expert at a time: two blocks of eight columns
+constexpr unsigned SHARED = 4;   // one of so many items is shared out
 constexpr int SMEM = 227 * 1024;
 constexpr int STATUS_TIMEOUT = 2;
 constexpr int WAIT_US = 200 * 1000, WAIT_US_WITHHELD = 5 * 1000;
@@ -80,7 +81,7 @@ struct Params {
   unsigned per_inv;  // 2^20 / (group / 32) and one more: block of 32 inputs * per_inv >> 20 is its scale
   int* ids;        // outputs, may be null
   float* weights;
-  unsigned* sync;  // counters of the three barriers and of the CTAs that have left; 0 between calls
+  unsigned* sync;  // counters of the three barriers, of the CTAs that have left and of the items shared out; 0 between calls
   float2* logits;  // [tokens][experts], each a sum of two
   float* h;        // [tokens * top_k][ffn]
   float* part;     // [tokens * top_k][hidden]
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
   using S = Shape<FMT>;
   constexpr int UP_PARTS = parts_up<XT>(), DOWN_PARTS = parts_down<XT>();
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int failed, total[2];
+  __shared__ int failed, ticket, total[2];
   __shared__ unsigned long long scan[NW];
   const int tid = threadIdx.x, warp = tid >> 5;
   const unsigned char* ring_p = smem + warp * p.stages * S::SLOT;
@@ -608,130 +609,147 @@ __global__ void __launch_bounds__(NT, 1) moe_layer_kernel(const __grid_constant_
     const int lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int kw = NW / m.g, tile = warp / kw, units = (m.k + S::UK - 1) / S::UK, size = row_bytes(m.k), all_parts = phase ? DOWN_PARTS : UP_PARTS;
     const int lo = warp % kw * units / kw, hi = (warp % kw + 1) * units / kw;
-    const unsigned all = (unsigned)(total[phase] * m.items);  // (2^10 groups of 2^11 items on 2^10 CTAs at most)
-    const int first = (int)(all * blockIdx.x / gridDim.x), last = (int)(all * (blockIdx.x + 1) / gridDim.x);
-    Stream<FMT> in;
-    in.group = first / m.items;
-    in.it = first - in.group * m.items;
-    in.left = lo < hi ? last - first : 0;
-    in.unit = lo;
-    in.put = 0;
-    in.place(m, groups, tile);
+    // A run of the items to each CTA, and where there are several, the last of all of them one by one to whoever is
+    // done: SMs get unequal shares of the memory's rate, by a fifth and more (64 bf16 tokens: 195 us with runs alone, 191, 177, 180 and 188
+    // with a sixth, quarter, third and half shared out). Which CTA has an item does not change its sums.
+    const unsigned all = (unsigned)(total[phase] * m.items);  // (2^10 groups of 2^11 items at most)
+    const unsigned shared_items = all >= 4 * gridDim.x ? all / SHARED : 0, own = all - shared_items;
+    int first = (int)(own * blockIdx.x / gridDim.x), last = (int)(own * (blockIdx.x + 1) / gridDim.x);  // (2^10 CTAs at most)
     auto meet = [&]() {  // the warps of a tile: others' tiles do not wait for it
       if (kw > 1) named_sync(1 + tile, kw * 32);
       else __syncwarp();
     };
-    // the item at work (it of the expert's, for n entries from `at` on), the next unit and the end of those here
-    int group = in.group, it = in.it - 1, left = last - first + 1, unit = 0, end = 0, got = 0, n = 0, at = 0, parts = 1, row0 = 0, named = -1;
+    // of the group whose activations are in place: its n entries from `at` on
+    int named = -1, n = 0, at = 0, parts = 1;
     const unsigned char* x[2] = {acts, acts};
     float acc[S::TM][2][4];
     float* mine = red + warp * COLS * S::RP;
     const float* sums = red + tile * kw * COLS * S::RP;
 #pragma unroll 1
-    for (int step = -p.stages;; ++step) {  // (the first fill the ring)
-      if (step >= 0) {
-        if (step == 0) {
-if (phase && !grid_wait(p, 1, &failed)) {
-            cp_async_wait<0>();
-            return;
+    for (bool waited = false;; waited = true) {
+      if (shared_items && tid == 0) ticket = (int)atomicAdd(p.sync + 4 + phase, 1u);  // for the next turn
+      Stream<FMT> in;
+      in.group = first / m.items;
+      in.it = first - in.group * m.items;
+      in.left = lo < hi ? last - first : 0;
+      in.unit = lo;
+      in.put = 0;
+      in.place(m, groups, tile);
+      // the item at work (it of the group's), the next unit and the end of those here
+      int group = in.group, it = in.it - 1, left = last - first + 1, unit = 0, end = 0, got = 0, row0 = 0;
+      bool open = false;
+#pragma unroll 1
+      for (int step = -p.stages;; ++step) {  // (the first fill the ring)
+        if (step >= 0) {
+          if (step == 0) {
+            if (phase && !waited && !grid_wait(p, 1, &failed)) {
+              cp_async_wait<0>();
+              return;
+            }
           }
-        }
-        while (unit >= end) {
-          if (n) {  // an item ends: the sums of the tile's warps meet
-            meet();  // (the last item's have been read)
+          while (unit >= end) {
+            if (open) {  // an item ends: the sums of the tile's warps meet
+              meet();  // (the last item's have been read)
+#pragma unroll
+              for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                  if (b == 0 || n > 8) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) mine[(b * 8 + 2 * t + (r & 1)) * S::RP + i * 16 + g + (r >> 1) * 8] = acc[i][b][r];
+                  }
+              meet();
+              const int each = parts == all_parts ? 1 : all_parts, thread = tid - tile * kw * 32;
+              if (row0 < m.rows) {
+                if (phase == 0) {
+                  constexpr int PAIRS = S::RT / 2;
+#pragma unroll 1
+                  for (int o = thread; o < PAIRS * n; o += kw * 32) {
+                    const int pair = o % PAIRS, col = o / PAIRS;
+                    float2 s = make_float2(0.f, 0.f);
+                    for (int q = each - 1; q >= 0; --q)
+#pragma unroll 4
+                      for (int w = 0; w < kw; ++w) {
+                        const float2 v = *reinterpret_cast<const float2*>(sums + (w * COLS + col * each + q) * S::RP + 2 * pair);
+                        s.x += v.x;
+                        s.y += v.y;
+                      }
+                    const float e = expf(-fabsf(s.x));  // (of what does not overflow, so that far gates fade out and are not cut off)
+                    p.h[(size_t)lists.sorted[at + col] * p.ffn + row0 / 2 + pair] = (s.x < 0.f ? s.x * e : s.x) / (1.f + e) * s.y;
+                  }
+                } else {
+#pragma unroll 1
+                  for (int o = thread; o < S::RT * n; o += kw * 32) {
+                    const int row = o % S::RT, col = o / S::RT;
+                    float s = 0.f;
+                    for (int q = each - 1; q >= 0; --q)
+#pragma unroll 4
+                      for (int w = 0; w < kw; ++w) s += sums[(w * COLS + col * each + q) * S::RP + row];
+                    p.part[(size_t)lists.sorted[at + col] * p.hidden + row0 + row] = s;
+                  }
+                }
+              }
+            }
+            if (--left == 0) break;
+            if (++it == m.items) {
+              it = 0;
+              ++group;
+            }
+            if (group != named) {  // its tokens: up to eight parts of them are columns of one block, of more each token is one
+              named = group;
+              n = (int)(groups[group] >> 21);
+              at = (int)(groups[group] >> 10 & 2047);
+              const bool here = phase == 0 && p.resident, packed = n * all_parts <= 8;
+              if (!here) {
+                __syncthreads();
+                if (phase == 0) bring(0, n, [&](int r) { return lists.sorted[at + r] / p.top_k; });
+                else bring(1, n, [&](int r) { return lists.sorted[at + r]; });
+                __syncthreads();
+              }
+              parts = packed ? 1 : all_parts;
+              const int cols = packed ? n * all_parts : n;
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const int col = min(b * 8 + g, cols - 1), tok = packed ? col / all_parts : col;
+                x[b] = acts + (size_t)((here ? lists.sorted[at + tok] / p.top_k : tok) * all_parts + (packed ? col - tok * all_parts : 0)) * size;
+              }
+            }
+            open = true;
+            row0 = (it * m.g + tile) * S::RT;
+            unit = lo;
+            end = row0 < m.rows ? hi : lo;
 #pragma unroll
             for (int i = 0; i < S::TM; ++i)
 #pragma unroll
               for (int b = 0; b < 2; ++b)
-                if (b == 0 || n > 8) {
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) mine[(b * 8 + 2 * t + (r & 1)) * S::RP + i * 16 + g + (r >> 1) * 8] = acc[i][b][r];
-                }
-            meet();
-            const int each = parts == all_parts ? 1 : all_parts, thread = tid - tile * kw * 32;
-            if (row0 < m.rows) {
-              if (phase == 0) {
-                constexpr int PAIRS = S::RT / 2;
-#pragma unroll 1
-                for (int o = thread; o < PAIRS * n; o += kw * 32) {
-                  const int pair = o % PAIRS, col = o / PAIRS;
-                  float2 s = make_float2(0.f, 0.f);
-                  for (int q = each - 1; q >= 0; --q)
-#pragma unroll 4
-                    for (int w = 0; w < kw; ++w) {
-                      const float2 v = *reinterpret_cast<const float2*>(sums + (w * COLS + col * each + q) * S::RP + 2 * pair);
-                      s.x += v.x;
-                      s.y += v.y;
-                    }
-                  const float e = expf(-fabsf(s.x));  // (of what does not overflow, so that far gates fade out and are not cut off)
-                  p.h[(size_t)lists.sorted[at + col] * p.ffn + row0 / 2 + pair] = (s.x < 0.f ? s.x * e : s.x) / (1.f + e) * s.y;
-                }
-              } else {
-#pragma unroll 1
-                for (int o = thread; o < S::RT * n; o += kw * 32) {
-                  const int row = o % S::RT, col = o / S::RT;
-                  float s = 0.f;
-                  for (int q = each - 1; q >= 0; --q)
-#pragma unroll 4
-                    for (int w = 0; w < kw; ++w) s += sums[(w * COLS + col * each + q) * S::RP + row];
-                  p.part[(size_t)lists.sorted[at + col] * p.hidden + row0 + row] = s;
-                }
-              }
-            }
+                for (int r = 0; r < 4; ++r) acc[i][b][r] = 0.f;
           }
-          if (--left == 0) break;
-          if (++it == m.items) {
-            it = 0;
-            ++group;
+          if (left == 0) break;
+  oldest_arrived(p.stages);
+          __syncwarp();
+          const unsigned char* slot = ring_p + got * S::SLOT;
+          if (parts == 1) {
+            if (n <= 8) multiply<FMT, 1, 1>(p, m, slot, x, size, unit, acc);
+            else if (UP_PARTS == 1) multiply<FMT, 2, 1>(p, m, slot, x, size, unit, acc);
+          } else {
+            if (n <= 8) multiply<FMT, 1, DOWN_PARTS>(p, m, slot, x, size, unit, acc);
+            else multiply<FMT, 2, DOWN_PARTS>(p, m, slot, x, size, unit, acc);
           }
-          if (group != named) {  // its tokens: up to eight parts of them are columns of one block, of more each token is one
-            named = group;
-            n = (int)(groups[group] >> 21);
-            at = (int)(groups[group] >> 10 & 2047);
-            const bool here = phase == 0 && p.resident, packed = n * all_parts <= 8;
-            if (!here) {
-              __syncthreads();
-              if (phase == 0) bring(0, n, [&](int r) { return lists.sorted[at + r] / p.top_k; });
-              else bring(1, n, [&](int r) { return lists.sorted[at + r]; });
-              __syncthreads();
-            }
-            parts = packed ? 1 : all_parts;
-            const int cols = packed ? n * all_parts : n;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const int col = min(b * 8 + g, cols - 1), tok = packed ? col / all_parts : col;
-              x[b] = acts + (size_t)((here ? lists.sorted[at + tok] / p.top_k : tok) * all_parts + (packed ? col - tok * all_parts : 0)) * size;
-            }
-          }
-          row0 = (it * m.g + tile) * S::RT;
-          unit = lo;
-          end = row0 < m.rows ? hi : lo;
-#pragma unroll
-          for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[i][b][r] = 0.f;
+          __syncwarp();
+          ++unit;
+          got = got + 1 == p.stages ? 0 : got + 1;
         }
-        if (left == 0) break;
-oldest_arrived(p.stages);
-        __syncwarp();
-        const unsigned char* slot = ring_p + got * S::SLOT;
-        if (parts == 1) {
-          if (n <= 8) multiply<FMT, 1, 1>(p, m, slot, x, size, unit, acc);
-          else if (UP_PARTS == 1) multiply<FMT, 2, 1>(p, m, slot, x, size, unit, acc);
-        } else {
-          if (n <= 8) multiply<FMT, 1, DOWN_PARTS>(p, m, slot, x, size, unit, acc);
-          else multiply<FMT, 2, DOWN_PARTS>(p, m, slot, x, size, unit, acc);
-        }
-        __syncwarp();
-        ++unit;
-        got = got + 1 == p.stages ? 0 : got + 1;
+        in.issue(p, m, groups, ring, tile, lo, hi);
       }
-      in.issue(p, m, groups, ring, tile, lo, hi);
+      cp_async_wait<0>();
+      if (!shared_items) break;
+      __syncthreads();
+      first = (int)own + ticket;
+      last = first + 1;
+      __syncthreads();  // (the ticket has been read)
+      if ((unsigned)first >= all) break;
     }
-cp_async_wait<0>();
-    __syncwarp();
     grid_arrive(p, 1 + phase);  // (the down products' first weights come while other CTAs are still at the gate and up products)
   }
   if (!grid_wait(p, 2, &failed)) return;
@@ -760,7 +778,7 @@ cp_async_wait<0>();
   }
   __syncthreads();
   if (tid == 0 && atom_add_acq_rel(p.sync + 3, 1u) == gridDim.x - 1)  // the last to leave: the counters are as they were
-    for (int i = 0; i < 4; ++i) p.sync[i] = 0;
+    for (int i = 0; i < 6; ++i) p.sync[i] = 0;
 }
 
 // ---------------------------------------------------------------------------------------- host
