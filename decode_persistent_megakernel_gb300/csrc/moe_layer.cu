@@ -14,14 +14,17 @@
 // bf16 parts of 8 bits each, which hold every bit down to 2^-133; fp16 ones as two, bf16 ones as they are. The SwiGLU outputs are kept in
 // fp32 and enter as three parts, or as two (2^-17) where the result is rounded to 16 bits anyway.
 //
-// A CTA takes a run of items, each G tiles of rows; a tile's inputs are split over 16 / G warps, whose sums meet in shared
+// A CTA takes a run of items, each G tiles of rows, and then, one at a time, items of the quarter that no CTA owns: SMs
+// get unequal shares of the memory's rate, and with runs alone the slowest CTA ended 20 % after the mean (64 tokens: 195 us
+// for 177). A tile's inputs are split over 16 / G warps, whose sums meet in shared
 // memory. Each warp streams its own part of the weights through a ring of asynchronous copies that runs on across items,
 // experts and, into the down products, across the barrier: no warp waits for another's copies. The activations stay in
 // shared memory, split into their parts once; the parts of one or two tokens are columns of one product.
 //
 // Measured (64 experts of 1024, top 8, hidden 2048): 8 fp32 tokens over bf16 experts (529 MB) 98 us, 0.80 of the measured copy rate, of
-// which the products are 84; 64 bf16 tokens (806 MB) 192; one fp32 token over 4-bit experts (27 MB) 27, the chain of
-// the phases. Parts split again at each use took 140, 230 and 42; units of 1 KiB 108, 220 and 30. The code of a phase is
+// which the products are 84; 64 bf16 tokens (806 MB) 177, 0.67; one fp32 token over 4-bit experts (27 MB) 27, the chain of
+// the phases. Before the shared quarter, parts split again at each use took 140, 230 and 42, units of 1 KiB 108, 220 and 30,
+// against 100, 195 and 27. The code of a phase is
 // kept small where it runs once: instruction fetch was the largest stall of the first form, and is still that of one token.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
