@@ -28,6 +28,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <initializer_list>
+#include <type_traits>
 #include <utility>
 
 #include "tinfer.h"
@@ -52,6 +53,10 @@ constexpr float MASK = -6e4f;        // logits from here down are taken for mask
 constexpr float WINDOW = 1.2e-4f, SUMS = 2e-6f;
 constexpr unsigned WHOLE = 16383;    // units: 2^18 tokens of them stay below 2^32
 constexpr int PER = LIST / NT;       // of a list, or of the bins, to a thread
+// bf16 logits have few values: the ones whose weights are above 0, from the maximum down but for those near zero, have a place each
+// in a table. 13 factors of two either side of zero leave a value in 4000 of a row like N(0, 1) between them.
+constexpr int PLACES = 3328, PLACES_PER = (PLACES + NT - 1) / NT;
+constexpr int BY_VALUE = 4 * PLACES;  // of rows with so many tokens; below, the table costs as much as it saves
 static_assert(LIST == BINS, "alike for both");
 constexpr int MAXIMA = 2;            // of a thread: more than one, so that a CTA alone has enough for large top-k
 
@@ -66,10 +71,18 @@ struct Params {
 };
 
 struct Smem {
-  unsigned hist[BINS];
-  u64 key[LIST], mass[LIST];        // the first CTA's list; `mass` also a CTA's own candidates
+  union {
+    struct {
+      u64 key[LIST], mass[LIST];    // the first CTA's list; `mass` also a CTA's own candidates
+      unsigned hist[BINS];
+    };
+    struct {
+      u64 weight[PLACES];           // of each place, and its tokens
+      unsigned tokens[PLACES];
+    };
+  };
   float2 table[64];                 // 2^(i / 64) in two parts
-  u64 sums[MAX_CLUSTER][NWARPS];    // kept weights of each warp of the cluster (in the first CTA)
+  u64 sums[2][MAX_CLUSTER][NWARPS];  // of each warp of the cluster (in the first CTA): kept weights; tokens with a key
   u64 red[NWARPS], red2[NWARPS], cross[2][MAX_CLUSTER], cross2[2][MAX_CLUSTER];
   float redf[NWARPS], redl[NWARPS], crossf[2][MAX_CLUSTER];
   uint16_t owner[NT];
@@ -77,6 +90,7 @@ struct Smem {
   unsigned floor_key;
   int lo, hi, rank, warp;
   u64 tau, rest, total_s;  // tau: (key, ~id) of the last token kept
+  u64 middle;              // weights of the tokens without a place
   float ch, cl;
   u64 least;                        // weights below are not kept
 };
@@ -238,6 +252,14 @@ struct Slice {
   // f(logits of a word, id of its first) for the words [w0, w1) of a warp, a word to a lane, AHEAD under way
   template <int AHEAD, typename F>
   __device__ __forceinline__ void walk_words(int w0, int w1, F&& f) const {
+    walk_raw<AHEAD>(w0, w1, [&](const uint4& y, int w) {
+      float v[N];
+      unpack(y, v, x);
+      f(v, id(w, 0));
+    });
+  }
+  template <int AHEAD, typename F>
+  __device__ __forceinline__ void walk_raw(int w0, int w1, F&& f) const {  // f(word, its number)
 #pragma unroll 1
     for (int w = w0 + (threadIdx.x & 31); w < w1; w += 32 * AHEAD) {
       uint4 y[AHEAD];
@@ -247,9 +269,7 @@ struct Slice {
 #pragma unroll
       for (int h = 0; h < AHEAD; ++h) {
         if (w + 32 * h >= w1) break;
-        float v[N];
-        unpack(y[h], v, x);
-        f(v, id(w + 32 * h, 0));
+        f(y[h], w + 32 * h);
       }
     }
   }
@@ -393,7 +413,7 @@ struct Draw {
   __device__ __noinline__ void tally(int kind, unsigned key) {
     const u64 s = measured(kind, key, in.first(warp), in.first(warp + 1));
     meet();
-    if (lane == 0) in_first(&sm.sums[rank][warp])[0] = s;
+    if (lane == 0) in_first(&sm.sums[kind][rank][warp])[0] = s;
     meet();
   }
   // The token at which the tallied sums exceed `target`: f(id, its part, the total) is called by one thread of the cluster.
@@ -404,7 +424,7 @@ struct Draw {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int e = lane * 4 + i;
-        s[i] = e < size * NWARPS ? in_first(&sm.sums[0][0])[e] : 0;
+        s[i] = e < size * NWARPS ? in_first(&sm.sums[kind][0][0])[e] : 0;
         before += s[i];
       }
       const u64 mine = before;
@@ -546,7 +566,7 @@ struct Draw {
     if (warp == 0) {
       u64 s = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s += lane + 32 * i < size * NWARPS ? in_first(&sm.sums[0][0])[lane + 32 * i] : 0;
+      for (int i = 0; i < 4; ++i) s += lane + 32 * i < size * NWARPS ? in_first(&sm.sums[0][0][0])[lane + 32 * i] : 0;
       s = warp_sum(s);
       if (lane == 0) sm.total_s = s;
     }
@@ -571,6 +591,10 @@ struct Draw {
 #pragma unroll
     for (int i = 0; i < PER; ++i) incl[i] = at += sm.mass[tid * PER + i];
   }
+  // Rows of bf16 without top-k: the border of the nucleus from the number of tokens of each value, then the kept weights by looking
+  // them up; the warps' sums and tau are left for the draw. False: the border lies among the values without a place (or
+  // zeros of both signs have places of their own), and nothing is left but a clean count of bins.
+  __device__ __noinline__ bool values(float p, bool nucleus);
   __device__ __forceinline__ void write(int id, u64 w, u64 total) {
     q.ids[row] = id;
     if (!q.logp) return;
@@ -587,6 +611,180 @@ __device__ __forceinline__ u64 part_of(float f, u64 total, bool& more) {
   const u64 x = __float2ull_rz(f * 18446744073709551616.f);
   more = x * total != 0;
   return __umul64hi(x, total);
+}
+
+// The place of a bf16 value, by its distance d from the maximum in the values' order: d itself before `middle`, which the values from
+// there to the one before `resume` share; then on from middle + 1; `out` and more: weight 0. Two at a time in 16 bits each, which no
+// carry leaves in the end.
+struct Places {
+  int top, middle, resume, out;
+  uint32_t top2, middle2, resume2, out2;
+  __device__ __forceinline__ uint32_t of(uint32_t w) const {
+    const uint32_t s = (w >> 15) & 0x00010001u, d = top2 - (w ^ (s * 0x7FFFu + 0x80008000u));
+    return __vminu2(__vminu2(d, middle2) + (__vmaxu2(d, resume2) - resume2), out2);
+  }
+  __device__ __forceinline__ float value(int place) const {
+    const unsigned o = top - (place < middle ? place : place + resume - middle);
+    return unordered(o << 16 | (o & 0x8000u ? 0 : 0xFFFFu));
+  }
+  // False: zeros of both signs, which are equal, would have different places.
+  __device__ __forceinline__ bool set(float m, float ch) {
+    top = (int)(ordered(m) >> 16);
+    const int far = max((int)(ordered(m - 47.f / ch) >> 16), 0x0080);  // (weights are 0 from 46.5 factors of two on)
+    const int values = top - far + 1, zero = top - 0x8000, most = PLACES - 2;
+    const int gap = max(values - most, 1);
+    middle = values <= most ? values : max(1, min(zero - gap / 2, values - gap));
+    resume = middle + gap - 1;  // the last one that shares
+    out = middle + 1 + max(values - 1 - resume, 0);
+    top2 = top * 0x10001u;
+    middle2 = middle * 0x10001u;
+    resume2 = resume * 0x10001u;
+    out2 = out * 0x10001u;
+    return zero < 0 || zero >= values || (middle <= zero && zero < resume);
+  }
+};
+
+template <typename T>
+__device__ bool Draw<T>::values(float p, bool nucleus) {
+  Places at;
+  if (!at.set(m, ch)) {
+    __syncthreads();
+    for (int i = tid; i < BINS; i += NT) sm.hist[i] = 0;
+    meet();
+    return false;
+  }
+  const int w0 = in.first(warp), w1 = in.first(warp + 1);
+  auto each_of = [&](const uint4& y, auto&& f) {  // f(place, logit)
+    const uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t two = at.of(u[i]);
+      f((int)(two & 0xFFFF), __uint_as_float(u[i] << 16));
+      f((int)(two >> 16), __uint_as_float(u[i] & 0xFFFF0000u));
+    }
+  };
+  // what the tokens without a place add, of words that have some
+  auto rest_of = [&](const uint4& y, u64 from) {
+    u64 s = 0;
+    each_of(y, [&](int place, float x) {
+      if (place != at.middle) return;
+      const u64 w = weight_once(x, m, ch, cl, sm.table);
+      s += w >= from ? w : 0;
+    });
+    return s;
+  };
+  if (nucleus) {
+    u64 middle = 0;
+    in.template walk_raw<2>(w0, w1, [&](const uint4& y, int) {
+      bool any = false;
+      each_of(y, [&](int place, float) {
+        if (place < at.out) atomicAdd(&sm.tokens[place], 1u);
+        any |= place == at.middle;
+      });
+      if (any) middle += rest_of(y, 0);
+    });
+    middle = warp_sum(middle);
+    if (lane == 0 && middle) atomicAdd(in_first(&sm.middle), middle);
+  }
+  for (int e = tid * size + rank; e < at.out; e += NT * size)
+    tell(&sm.weight[e], e == at.middle ? 0ull : weight_once(at.value(e), m, ch, cl, sm.table));
+  int border = at.out;
+  if (nucleus) {
+    __syncthreads();
+    if (rank) {
+      unsigned* all = in_first(sm.tokens);
+      for (int i = tid; i < at.out; i += NT)
+        if (sm.tokens[i]) atomicAdd(all + i, sm.tokens[i]);
+    }
+    meet();
+    if (rank == 0) {
+      u64 w[PLACES_PER], s = 0;
+#pragma unroll
+      for (int i = 0; i < PLACES_PER; ++i) {
+        const int e = tid * PLACES_PER + i;
+        w[i] = e >= at.out ? 0 : e == at.middle ? sm.middle : sm.weight[e] * sm.tokens[e];
+        s += w[i];
+      }
+      const u64 incl = block_scan(s, sm.red);
+      if (tid == NT - 1) sm.total_s = incl;
+      __syncthreads();
+      bool more;
+      u64 limit = p > 0.f ? part_of(p, sm.total_s, more) : 0;
+      if (p > 0.f && more) ++limit;
+      limit = limit ? limit : 1;
+      u64 before = incl - s;
+      if (before < limit && limit <= incl) {
+#pragma unroll
+        for (int i = 0; i < PLACES_PER; ++i) {
+          if (before < limit && limit <= before + w[i]) {
+            const int e = tid * PLACES_PER + i;
+            const u64 nth = e == at.middle ? 0 : (limit - before - 1) / sm.weight[e];  // of the tokens with this value, in order
+            tell(&sm.lo, e);
+            tell(&sm.hi, e == at.middle || nth + 1 == sm.tokens[e] ? -1 : (int)nth);
+          }
+          before += w[i];
+        }
+      }
+    }
+    meet();
+    border = sm.lo;
+    if (border == at.middle) {
+      for (int i = tid; i < BINS; i += NT) sm.hist[i] = 0;
+      meet();
+      return false;
+    }
+  } else {
+    meet();
+  }
+  u64 keep = 0;
+  unsigned ties = 0;
+  in.template walk_raw<2>(w0, w1, [&](const uint4& y, int) {
+    bool any = false;
+    each_of(y, [&](int place, float) {
+      if (place < border) {
+        const u64 w = sm.weight[place];
+        keep += w >= least ? w : 0;
+      }
+      ties += place == border;
+      any |= place == at.middle;
+    });
+    if (any && at.middle < border) keep += rest_of(y, least);
+  });
+  u64 each = border < at.out ? sm.weight[border] : 0;
+  each = each >= least ? each : 0;
+  const int nth = nucleus ? sm.hi : -1;
+  const unsigned key = nucleus ? ordered(at.value(border)) : 0;
+  keep = warp_sum(keep);
+  ties = nucleus ? __reduce_add_sync(~0u, ties) : 0;
+  if (lane == 0) {
+    in_first(&sm.sums[0][rank][warp])[0] = nth < 0 ? keep + each * ties : keep;
+    if (nth >= 0) in_first(&sm.sums[1][rank][warp])[0] = ties;
+  }
+  tau = (u64)key << 32;
+  meet();
+  if (nth >= 0) {
+    find(1, key, (u64)nth, [&](int id, u64) { tell(&sm.tau, (u64)key << 32 | (unsigned)~id); });
+    if (rank == 0 && warp == 0) {  // of the border's tokens the warps before the last one's keep all
+      int before = 0, own[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) before += own[i] = lane * 4 + i < size * NWARPS ? (int)(&sm.sums[1][0][0])[lane * 4 + i] : 0;
+      const int mine = before;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(~0u, before, o);
+        if (lane >= o) before += y;
+      }
+      before -= mine;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (lane * 4 + i < size * NWARPS) (&sm.sums[0][0][0])[lane * 4 + i] += each * (u64)max(0, min(own[i], nth + 1 - before));
+        before += own[i];
+      }
+    }
+    meet();
+    tau = sm.tau;
+  }
+  return true;
 }
 
 template <typename T>
@@ -607,9 +805,14 @@ __device__ __forceinline__ void Draw<T>::run() {
     sm.cl = (fmaf(-c, t, L) + LL) / t;
     sm.least = low > 0.f ? (u64)ceilf(fminf(low, 1.f) * 35184372088832.f) : 0;  // 2^45
   }
-  for (int i = tid; i < BINS; i += NT) sm.hist[i] = 0;
+  const bool by_value = std::is_same_v<T, __nv_bfloat16> && q.vocab >= BY_VALUE;
+  if (by_value && nucleus && !k)
+    for (int i = tid; i < PLACES; i += NT) sm.tokens[i] = 0;
+  else
+    for (int i = tid; i < BINS; i += NT) sm.hist[i] = 0;
   if (tid == 0) {
     sm.own = sm.listed[0] = sm.listed[1] = sm.owners = sm.warp = 0;
+    sm.middle = 0;
     sm.rank = -1;
   }
 
@@ -812,145 +1015,152 @@ __device__ __forceinline__ void Draw<T>::run() {
     __syncthreads();
   }
 
-  // ---- many: the nucleus' border to a few bins
-  if (k) search(false, (u64)k, 1.f, -INFINITY, INFINITY);
-  int lo = BINS, hi = BINS;
-  // the bins span the row's own range, so that a row of near logits does not fall into a few of them
-  const float per_log2 = (float)BINS / fminf(fmaxf((m - least_x) * ch * 1.001f, 1e-6f), RANGE), per = ch * per_log2 * 1024.f;
-  if (nucleus) {
-    const unsigned slope = (unsigned)((1.f - exp2f(-1.f / per_log2)) * (WHOLE * 16.f) + 0.5f);  // of a bin's weights, in 2^-14 of a unit to a 1024th
-    in.template walk<2>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
-      if (x > -INFINITY && (!tau || kept(x, id))) {
-        const unsigned b = __float_as_uint(distance(x, m, per)) - __float_as_uint(ROUND_BINS);
-        atomicAdd(&sm.hist[b >> 10], WHOLE - ((b & 1023) * slope + 8192 >> 14));
-      }
-    });
-    __syncthreads();
-    if (rank) {
-      unsigned* all = in_first(sm.hist);
-      for (int i = tid; i < BINS; i += NT)
-        if (sm.hist[i]) atomicAdd(all + i, sm.hist[i]);
-    }
-    meet();
-    if (rank == 0) {
-      float w[PER], s = 0.f;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) s += w[i] = (float)sm.hist[tid * PER + i] * exp2f((float)(tid * PER + i) * (-1.f / per_log2));
-      float incl = s;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const float y = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) sm.redf[warp] = incl;
-      if (tid == 0) sm.lo = sm.hi = BINS - 1;
-      __syncthreads();
-      float all = 0.f;
-      for (int i = 0; i < NWARPS; ++i) {
-        if (i < warp) incl += sm.redf[i];
-        all += sm.redf[i];
-      }
-      float at = incl - s;
-      int first_lo = BINS - 1, first_hi = BINS - 1;
-      const float window = fmaxf(WINDOW * fminf(p, 1.f - p), SUMS);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        at += w[i];
-        if (at >= (p - window) * all) first_lo = min(first_lo, tid * PER + i);
-        if (at >= (p + window) * all) first_hi = min(first_hi, tid * PER + i);
-      }
-      first_lo = __reduce_min_sync(~0u, first_lo);
-      first_hi = __reduce_min_sync(~0u, first_hi);
-      if (lane == 0) {
-        atomicMin(&sm.lo, first_lo);
-        atomicMin(&sm.hi, first_hi);
-      }
-      __syncthreads();
-      const int a = sm.lo, b = sm.hi;
-      __syncthreads();
-      if (tid == 0) {
-        tell(&sm.lo, a);
-        tell(&sm.hi, b);
-      }
-    }
-    meet();
-    lo = sm.lo;
-    hi = sm.hi;
+  // ---- many
+  bool done = false;
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    if (by_value && !k) done = values(p, nucleus);
   }
-
-  // ---- the weights: all, those above the border's bins, and of these what min-p keeps; the tokens within the bins
-  u64 all = 0, above = 0, keep = 0;
-  const float below = nucleus ? ROUND_BINS + (float)(lo * 1024) : INFINITY, within = nucleus ? ROUND_BINS + (float)(hi * 1024 + 1023) : -INFINITY;
-  in.template walk_words<1>(in.first(warp), in.first(warp + 1), [&](const float(&x)[Slice<T>::N], int first) {
-#pragma unroll 2
-    for (int i = 0; i < Slice<T>::N; i += 2) {
-      const float v0 = x[i], v1 = x[i + 1];
-      u64 w0, w1;
-      weights(make_float2(v0, v1), m, ch, cl, sm.table, w0, w1);
-      const float d0 = distance(v0, m, per), d1 = distance(v1, m, per);
-      bool in0 = d0 >= below && d0 <= within && v0 > -INFINITY, in1 = d1 >= below && d1 <= within && v1 > -INFINITY;
-      if (tau) {
-        if (!kept(v0, first + i)) w0 = in0 = 0;
-        if (!kept(v1, first + i + 1)) w1 = in1 = 0;
+  if (!done) {
+    // ---- the nucleus' border to a few bins
+    if (k) search(false, (u64)k, 1.f, -INFINITY, INFINITY);
+    int lo = BINS, hi = BINS;
+    // the bins span the row's own range, so that a row of near logits does not fall into a few of them
+    const float per_log2 = (float)BINS / fminf(fmaxf((m - least_x) * ch * 1.001f, 1e-6f), RANGE), per = ch * per_log2 * 1024.f;
+    if (nucleus) {
+      const unsigned slope = (unsigned)((1.f - exp2f(-1.f / per_log2)) * (WHOLE * 16.f) + 0.5f);  // of a bin's weights, in 2^-14 of a unit to a 1024th
+      in.template walk<2>(in.first(warp), in.first(warp + 1), [&](float x, int id) {
+        if (x > -INFINITY && (!tau || kept(x, id))) {
+          const unsigned b = __float_as_uint(distance(x, m, per)) - __float_as_uint(ROUND_BINS);
+          atomicAdd(&sm.hist[b >> 10], WHOLE - ((b & 1023) * slope + 8192 >> 14));
+        }
+      });
+      __syncthreads();
+      if (rank) {
+        unsigned* all = in_first(sm.hist);
+        for (int i = tid; i < BINS; i += NT)
+          if (sm.hist[i]) atomicAdd(all + i, sm.hist[i]);
       }
-      all += w0 + w1;
-      w0 = d0 < below ? w0 : 0;
-      w1 = d1 < below ? w1 : 0;
-      above += w0 + w1;
-      if (least) keep += (w0 >= least ? w0 : 0) + (w1 >= least ? w1 : 0);
-      if (in0) take(v0, first + i);
-      if (in1) take(v1, first + i + 1);
-    }
-  });
-  if (!least) keep = above;
-  keep = warp_sum(keep);
-  if (lane == 0) in_first(&sm.sums[rank][warp])[0] = keep;
-  if (nucleus) {
-    sums(all, above);
-    bool more;
-    u64 limit = p > 0.f ? part_of(p, all, more) : 0;
-    if (p > 0.f && more) ++limit;
-    limit = limit ? limit : 1;
-    const int n = collect(1);
-    if (rank == 0) {
-      bool found = n <= LIST && n > 0 && above < limit;
-      if (found) {
-        u64 incl[PER];
-        resolve(n, n, incl);
-        int inside = 0;
+      meet();
+      if (rank == 0) {
+        float w[PER], s = 0.f;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) inside += tid * PER + i < n && above + incl[i] - sm.mass[tid * PER + i] < limit;
-        inside = (int)block_scan((u64)inside, sm.red);
-        if (tid == NT - 1) {
-          sm.count[0] = inside;
-          sm.total_s = incl[PER - 1];
+        for (int i = 0; i < PER; ++i) s += w[i] = (float)sm.hist[tid * PER + i] * exp2f((float)(tid * PER + i) * (-1.f / per_log2));
+        float incl = s;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const float y = __shfl_up_sync(~0u, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (lane == 31) sm.redf[warp] = incl;
+        if (tid == 0) sm.lo = sm.hi = BINS - 1;
+        __syncthreads();
+        float all = 0.f;
+        for (int i = 0; i < NWARPS; ++i) {
+          if (i < warp) incl += sm.redf[i];
+          all += sm.redf[i];
+        }
+        float at = incl - s;
+        int first_lo = BINS - 1, first_hi = BINS - 1;
+        const float window = fmaxf(WINDOW * fminf(p, 1.f - p), SUMS);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          at += w[i];
+          if (at >= (p - window) * all) first_lo = min(first_lo, tid * PER + i);
+          if (at >= (p + window) * all) first_hi = min(first_hi, tid * PER + i);
+        }
+        first_lo = __reduce_min_sync(~0u, first_lo);
+        first_hi = __reduce_min_sync(~0u, first_hi);
+        if (lane == 0) {
+          atomicMin(&sm.lo, first_lo);
+          atomicMin(&sm.hi, first_hi);
         }
         __syncthreads();
-        inside = sm.count[0];
-        found = inside < n || hi == BINS - 1 || above + sm.total_s >= limit;
-        if (found) {
-          // their weights belong to the warps that hold them
-          for (int i = tid; i < inside; i += NT) {
-            if (sm.mass[i] < least) continue;
-            const int id = (int)~(unsigned)sm.key[i], r = id / q.slice;
-            const Slice<T> s(in.x, r * q.slice, min(q.slice, q.vocab - r * q.slice));
-            atomicAdd(&sm.sums[r][(s.mis + id - s.a) / Slice<T>::N / s.per], sm.mass[i]);
-          }
-          if (tid == 0) tell(&sm.tau, sm.key[inside - 1]);
+        const int a = sm.lo, b = sm.hi;
+        __syncthreads();
+        if (tid == 0) {
+          tell(&sm.lo, a);
+          tell(&sm.hi, b);
         }
       }
-      if (tid == 0 && !found) tell(&sm.tau, (u64)0);
-      __syncthreads();
+      meet();
+      lo = sm.lo;
+      hi = sm.hi;
     }
-    meet();
-    if (sm.tau) {
-      tau = sm.tau;
+
+    // ---- the weights: all, those above the border's bins, and of these what min-p keeps; the tokens within the bins
+    u64 all = 0, above = 0, keep = 0;
+    const float below = nucleus ? ROUND_BINS + (float)(lo * 1024) : INFINITY, within = nucleus ? ROUND_BINS + (float)(hi * 1024 + 1023) : -INFINITY;
+    in.template walk_words<1>(in.first(warp), in.first(warp + 1), [&](const float(&x)[Slice<T>::N], int first) {
+#pragma unroll 2
+      for (int i = 0; i < Slice<T>::N; i += 2) {
+        const float v0 = x[i], v1 = x[i + 1];
+        u64 w0, w1;
+        weights(make_float2(v0, v1), m, ch, cl, sm.table, w0, w1);
+        const float d0 = distance(v0, m, per), d1 = distance(v1, m, per);
+        bool in0 = d0 >= below && d0 <= within && v0 > -INFINITY, in1 = d1 >= below && d1 <= within && v1 > -INFINITY;
+        if (tau) {
+          if (!kept(v0, first + i)) w0 = in0 = 0;
+          if (!kept(v1, first + i + 1)) w1 = in1 = 0;
+        }
+        all += w0 + w1;
+        w0 = d0 < below ? w0 : 0;
+        w1 = d1 < below ? w1 : 0;
+        above += w0 + w1;
+        if (least) keep += (w0 >= least ? w0 : 0) + (w1 >= least ? w1 : 0);
+        if (in0) take(v0, first + i);
+        if (in1) take(v1, first + i + 1);
+      }
+    });
+    if (!least) keep = above;
+    keep = warp_sum(keep);
+    if (lane == 0) in_first(&sm.sums[0][rank][warp])[0] = keep;
+    if (nucleus) {
+      sums(all, above);
+      bool more;
+      u64 limit = p > 0.f ? part_of(p, all, more) : 0;
+      if (p > 0.f && more) ++limit;
+      limit = limit ? limit : 1;
+      const int n = collect(1);
+      if (rank == 0) {
+        bool found = n <= LIST && n > 0 && above < limit;
+        if (found) {
+          u64 incl[PER];
+          resolve(n, n, incl);
+          int inside = 0;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) inside += tid * PER + i < n && above + incl[i] - sm.mass[tid * PER + i] < limit;
+          inside = (int)block_scan((u64)inside, sm.red);
+          if (tid == NT - 1) {
+            sm.count[0] = inside;
+            sm.total_s = incl[PER - 1];
+          }
+          __syncthreads();
+          inside = sm.count[0];
+          found = inside < n || hi == BINS - 1 || above + sm.total_s >= limit;
+          if (found) {
+            // their weights belong to the warps that hold them
+            for (int i = tid; i < inside; i += NT) {
+              if (sm.mass[i] < least) continue;
+              const int id = (int)~(unsigned)sm.key[i], r = id / q.slice;
+              const Slice<T> s(in.x, r * q.slice, min(q.slice, q.vocab - r * q.slice));
+              atomicAdd(&sm.sums[0][r][(s.mis + id - s.a) / Slice<T>::N / s.per], sm.mass[i]);
+            }
+            if (tid == 0) tell(&sm.tau, sm.key[inside - 1]);
+          }
+        }
+        if (tid == 0 && !found) tell(&sm.tau, (u64)0);
+        __syncthreads();
+      }
+      meet();
+      if (sm.tau) {
+        tau = sm.tau;
+      } else {
+        if (above >= limit || !search(true, limit - above, per, below, within)) search(true, limit, per, -INFINITY, INFINITY);
+        tally(0, 0);
+      }
     } else {
-      if (above >= limit || !search(true, limit - above, per, below, within)) search(true, limit, per, -INFINITY, INFINITY);
-      tally(0, 0);
+      meet();
     }
-  } else {
-    meet();
   }
 
   // ---- the draw

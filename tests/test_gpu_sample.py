@@ -273,3 +273,43 @@ def test_agrees_with_the_scores():
     ids, logp = T.sample(x, uniform(5, 2))
     assert float((T.logprobs(x, ids)[0] - logp).abs().max()) < 1e-5
     assert math.isfinite(float(logp.sum()))
+
+
+@pytest.mark.parametrize("rows", [3, 160])
+@pytest.mark.parametrize("kind", ["near zero", "zeros", "largest zero", "negative", "tiny", "far", "ties", "masks", "all one value"])
+def test_16_bit_values_of_every_range(rows, kind):
+    """Rows whose border lies near zero, among zeros of both signs, in ties of thousands, next to masks of several values."""
+    vocab = 16000 if rows > 3 else 70003
+    x = torch.randn((rows, vocab), generator=gen(31), device="cuda") * 2.5
+    if kind == "near zero":
+        x = x * 1e-5
+        x[:, 7] = 8.0
+    elif kind == "zeros":
+        x = torch.where(x > 0, 0.0, -0.0)
+        x[:, 11:vocab:97] = 2.0
+        x[:, 5:vocab:31] = -3.0
+    elif kind == "largest zero":
+        x = -x.abs()
+        x[:, 3:vocab:5001] = 0.0
+        x[:, 4:vocab:5001] = -0.0
+    elif kind == "negative":
+        x = x - 40.0
+    elif kind == "tiny":
+        x = x * 1e-30
+    elif kind == "far":
+        x = x + 1000.0
+        x[:, ::2] = -1000.0
+    elif kind == "ties":
+        x = x.round()
+    elif kind == "masks":
+        x[:, ::3] = float("-inf")
+        x[:, 1::3] = torch.finfo(torch.bfloat16).min
+        x[:, 2::9] = -1e4
+    elif kind == "all one value":
+        x = torch.full_like(x, -1.25)
+    x = x.to(torch.bfloat16)
+    for i, kw in enumerate([dict(), dict(top_p=0.9), dict(top_p=0.5, min_p=0.01), dict(min_p=0.3), dict(top_p=0.99, temperature=0.2),
+                            dict(top_p=1e-4), dict(top_p=0.9999999, temperature=30.0), dict(top_p=0.7, temperature=1e-3)]):
+        check(x, uniform(rows, 400 + i), **kw)
+    check(x, torch.full((rows,), LAST, device="cuda"), top_p=0.6)
+    check(x, torch.zeros(rows, device="cuda"), top_p=0.6)
