@@ -70,31 +70,6 @@ struct Params {
   int rows, vocab, slice;
 };
 
-struct Smem {
-  union {
-    struct {
-      u64 key[LIST], mass[LIST];    // the first CTA's list; `mass` also a CTA's own candidates
-      unsigned hist[BINS];
-    };
-    struct {
-      u64 weight[PLACES];           // of each place, and its tokens
-      unsigned tokens[PLACES];
-    };
-  };
-  float2 table[64];                 // 2^(i / 64) in two parts
-  u64 sums[2][MAX_CLUSTER][NWARPS];  // of each warp of the cluster (in the first CTA): kept weights; tokens with a key
-  u64 red[NWARPS], red2[NWARPS], cross[2][MAX_CLUSTER], cross2[2][MAX_CLUSTER];
-  float redf[NWARPS], redl[NWARPS], crossf[2][MAX_CLUSTER];
-  uint16_t owner[NT];
-  int owners, own, listed[2], count[2];
-  unsigned floor_key;
-  int lo, hi, rank, warp;
-  u64 tau, rest, total_s;  // tau: (key, ~id) of the last token kept
-  u64 middle;              // weights of the tokens without a place
-  float ch, cl;
-  u64 least;                        // weights below are not kept
-};
-
 // 2^(i / 64) in two parts, each the nearest fp32.
 __constant__ float2 POWERS[64] = {
     {1.f, 0.f}, {1.01088929f, -5.71160541e-09f}, {1.0218972f, -4.81155986e-08f}, {1.03302491f, -2.80908932e-08f},
@@ -114,8 +89,6 @@ __constant__ float2 POWERS[64] = {
     {1.8340081f, -1.1239278e-08f}, {1.85397911f, 1.43656118e-08f}, {1.87416768f, -4.66300563e-08f}, {1.89457595f, 2.81033845e-08f},
     {1.91520655f, 9.84532811e-09f}, {1.93606174f, 5.3570723e-08f}, {1.95714414f, -1.70218044e-08f}, {1.97845602f, 6.03272632e-09f},
 };
-
-static_assert(offsetof(Smem, mass) == offsetof(Smem, key) + sizeof(u64) * LIST && MAX_CLUSTER * MAXIMA * NT * 4 <= 2 * LIST * 8, "room for the maxima");
 
 // Logits as whole numbers in their order, zeros of both signs equal; above 0 for all.
 __device__ __forceinline__ unsigned ordered(float x) {
@@ -227,6 +200,7 @@ struct Slice {
   const T* x;
   const uint4* base;
   int a, len, mis, words, per;
+  Slice() = default;
   __device__ Slice(const T* row, int from, int n) : x(row), a(from), len(n) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(row + from);
     mis = (int)(p & 15) / (int)sizeof(T);
@@ -333,20 +307,101 @@ __device__ __noinline__ void sort_down(u64* a, int n) {
   __syncthreads();
 }
 
+// The place of a bf16 value, by its distance d from the maximum in the values' order: d itself before `middle`, which the values from
+// there to the one before `resume` share; then on from middle + 1; `out` and more: weight 0. Two at a time in 16 bits each, which no
+// carry leaves in the end.
+struct Places {
+  int top, middle, resume, out;
+  uint32_t top2, middle2, resume2, out2;
+  __device__ __forceinline__ uint32_t of(uint32_t w) const {
+    const uint32_t s = (w >> 15) & 0x00010001u, d = top2 - (w ^ (s * 0x7FFFu + 0x80008000u));
+    return __vminu2(__vminu2(d, middle2) + (__vmaxu2(d, resume2) - resume2), out2);
+  }
+  __device__ __forceinline__ float value(int place) const {
+    const unsigned o = top - (place < middle ? place : place + resume - middle);
+    return unordered(o << 16 | (o & 0x8000u ? 0 : 0xFFFFu));
+  }
+  // False: zeros of both signs, which are equal, would have different places.
+  __device__ __forceinline__ bool set(float m, float ch) {
+    top = (int)(ordered(m) >> 16);
+    const int far = max((int)(ordered(m - 47.f / ch) >> 16), 0x0080);  // (weights are 0 from 46.5 factors of two on)
+    const int values = top - far + 1, zero = top - 0x8000, most = PLACES - 2;
+    const int gap = max(values - most, 1);
+    middle = values <= most ? values : max(1, min(zero - gap / 2, values - gap));
+    resume = middle + gap - 1;  // the last one that shares
+    out = middle + 1 + max(values - 1 - resume, 0);
+    top2 = top * 0x10001u;
+    middle2 = middle * 0x10001u;
+    resume2 = resume * 0x10001u;
+    out2 = out * 0x10001u;
+    return zero < 0 || zero >= values || (middle <= zero && zero < resume);
+  }
+};
+
+// What all threads of a CTA know alike. It is in shared memory for the functions that are not inlined: members of an object
+// there would be each thread's own in local memory, which the logits push out of L1 (700 clocks to a token in `measure`).
 template <typename T>
-struct Draw {
-  const Params& q;
-  Smem& sm;
-  cg::cluster_group cluster;
-  const Slice<T> in;
-  int rank, size, row, tid, lane, warp, parity;
-  float m, ch, cl, temperature;
+struct State {
+  Slice<T> in;
+  int* ids;
+  float* logp;
+  float temperature, m, ch, cl;
   u64 tau;    // tokens with (key, ~id) from here on are kept
   u64 least;  // of these the ones with weights from here on
+  int rank, size, row, looked_up;  // looked_up: weights are in the table
+  Places at;
+};
 
-  __device__ Draw(const Params& p, Smem& s, const Slice<T>& slice, int r)
-      : q(p), sm(s), cluster(cg::this_cluster()), in(slice), rank((int)cluster.block_rank()), size((int)cluster.num_blocks()), row(r),
-        tid(threadIdx.x), lane(tid & 31), warp(tid >> 5), parity(0), tau(0) {}
+template <typename T>
+struct Smem {
+  State<T> state;
+  union {
+    struct {
+      u64 key[LIST], mass[LIST];    // the first CTA's list; `mass` also a CTA's own candidates
+      unsigned hist[BINS];
+    };
+    struct {
+      u64 weight[PLACES];           // of each place, and its tokens
+      unsigned tokens[PLACES];
+    };
+  };
+  float2 table[64];                 // 2^(i / 64) in two parts
+  u64 sums[2][MAX_CLUSTER][NWARPS];  // of each warp of the cluster (in the first CTA): kept weights; tokens with a key
+  u64 red[NWARPS], red2[NWARPS], cross[2][MAX_CLUSTER], cross2[2][MAX_CLUSTER];
+  float redf[NWARPS], redl[NWARPS], crossf[2][MAX_CLUSTER];
+  uint16_t owner[NT];
+  int owners, own, listed[2], count[2];
+  unsigned floor_key;
+  int lo, hi, rank, warp;
+  u64 tau, rest, total_s;  // tau: (key, ~id) of the last token kept
+  u64 middle;              // weights of the tokens without a place
+  float ch, cl;
+  u64 least;
+};
+static_assert(offsetof(Smem<float>, mass) == offsetof(Smem<float>, key) + sizeof(u64) * LIST && MAX_CLUSTER * MAXIMA * NT * 4 <= 2 * LIST * 8,
+              "room for the maxima");
+template <typename T>
+__device__ __forceinline__ Smem<T>& shared() {
+  __shared__ Smem<T> sm;
+  return sm;
+}
+
+template <typename T>
+struct Draw : State<T> {
+  using S = State<T>;
+  using S::in, S::ids, S::logp, S::temperature, S::m, S::ch, S::cl, S::tau, S::least, S::rank, S::size, S::row, S::looked_up, S::at;
+  Smem<T>& sm;
+  cg::cluster_group cluster;
+  int tid, lane, warp, parity;
+
+  __device__ __forceinline__ explicit Draw(const S& state)
+      : S(state), sm(shared<T>()), cluster(cg::this_cluster()), tid(threadIdx.x), lane(tid & 31), warp(tid >> 5), parity(0) {}
+  __device__ __forceinline__ void keep_from(u64 t) {
+    tau = t;
+    __syncthreads();
+    if (tid == 0) sm.state.tau = t;
+    __syncthreads();
+  }
   __device__ __forceinline__ void meet() {
     if (size > 1) cluster.sync();
     else __syncthreads();
@@ -388,37 +443,45 @@ struct Draw {
     return v;
   }
   __device__ __forceinline__ bool kept(float x, int id) const { return pair_of(x, id) >= tau; }
-  // What the tokens of a word add: their weights if they are kept (KIND 0), one if they have this key (KIND 1).
-  template <int N>
-  __device__ __forceinline__ void measure(int kind, unsigned key, const float (&x)[N], int first, u64 (&w)[N]) const {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) weights(make_float2(x[i], x[i + 1]), m, ch, cl, sm.table, w[i], w[i + 1]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const bool in_play = x[i] > -INFINITY && kept(x[i], first + i);
-      w[i] = !in_play ? 0 : kind ? (u64)(ordered(x[i]) == key) : w[i] >= least ? w[i] : 0;
-    }
-  }
-  __device__ __noinline__ u64 measured(int kind, unsigned key, int w0, int w1) const {  // by a warp
-    u64 s = 0;
-    in.template walk_words<1>(w0, w1, [&](const float(&x)[Slice<T>::N], int first) {
-      u64 w[Slice<T>::N];
-      measure(kind, key, x, first, w);
-#pragma unroll
-      for (int i = 0; i < Slice<T>::N; ++i) s += w[i];
-    });
-    return warp_sum(s);
+  // What a token adds: its weight if it is kept (KIND 0), one if it has this key (KIND 1).
+  static __device__ __noinline__ u64 measure(int kind, unsigned key, float x, int id) {
+    const Smem<T>& sm = shared<T>();
+    const S& s = sm.state;
+    if (!(x > -INFINITY) || pair_of(x, id) < s.tau) return 0;
+    if (kind) return ordered(x) == key;
+    u64 w;
+    const int place = s.looked_up ? s.at.of(__float_as_uint(x) >> 16) & 0xFFFF : 0;
+    if (s.looked_up && place != s.at.middle) w = place < s.at.out ? sm.weight[place] : 0;
+    else w = weight_once(x, s.m, s.ch, s.cl, sm.table);
+    return w >= s.least ? w : 0;
   }
   // The sums of the warps' runs, to the first CTA.
-  __device__ __noinline__ void tally(int kind, unsigned key) {
-    const u64 s = measured(kind, key, in.first(warp), in.first(warp + 1));
+  static __device__ __noinline__ void tally(int kind, unsigned key) { Draw(shared<T>().state).tally_here(kind, key); }
+  __device__ __forceinline__ void tally_here(int kind, unsigned key) {
+    u64 s = 0;
+    in.template walk_words<1>(in.first(warp), in.first(warp + 1), [&](const float(&x)[Slice<T>::N], int first) {
+#pragma unroll
+      for (int i = 0; i < Slice<T>::N; i += 2) {
+        u64 w0 = ordered(x[i]) == key, w1 = ordered(x[i + 1]) == key;
+        if (!kind) {
+          weights(make_float2(x[i], x[i + 1]), m, ch, cl, sm.table, w0, w1);
+          w0 = w0 >= least ? w0 : 0;
+          w1 = w1 >= least ? w1 : 0;
+        }
+        s += (x[i] > -INFINITY && kept(x[i], first + i) ? w0 : 0) + (x[i + 1] > -INFINITY && kept(x[i + 1], first + i + 1) ? w1 : 0);
+      }
+    });
+    s = warp_sum(s);
     meet();
     if (lane == 0) in_first(&sm.sums[kind][rank][warp])[0] = s;
     meet();
   }
-  // The token at which the tallied sums exceed `target`: f(id, its part, the total) is called by one thread of the cluster.
-  template <typename F>
-  __device__ __forceinline__ void find(int kind, unsigned key, u64 target, F&& f) {
+  // The token at which the tallied sums exceed `target`: it is the answer, of this total, or without one the last one kept. What
+  // a word adds is taken token by token: little is left to be measured, and code that runs once costs more than what it does.
+  static __device__ __noinline__ void find(int kind, unsigned key, u64 target, u64 total) {
+    Draw(shared<T>().state).find_here(kind, key, target, total);
+  }
+  __device__ __forceinline__ void find_here(int kind, unsigned key, u64 target, u64 total) {
     if (warp == 0) {
       u64 s[4], before = 0;
 #pragma unroll
@@ -449,7 +512,12 @@ struct Draw {
     // that warp's run, dealt out to all of the CTA; then one warp walks over its part
     int w0 = in.first(sm.warp), w1 = in.first(sm.warp + 1);
     const int per = (w1 - w0 + NWARPS - 1) / NWARPS;
-    const u64 s = measured(kind, key, min(w0 + warp * per, w1), min(w0 + (warp + 1) * per, w1));
+    u64 s = 0;
+    in.template walk_words<1>(min(w0 + warp * per, w1), min(w0 + (warp + 1) * per, w1), [&](const float(&x)[Slice<T>::N], int first) {
+#pragma unroll
+      for (int i = 0; i < Slice<T>::N; ++i) s += measure(kind, key, x[i], first + i);
+    });
+    s = warp_sum(s);
     if (lane == 0) sm.red[warp] = s;
     __syncthreads();
     u64 rest = sm.rest;
@@ -463,9 +531,8 @@ struct Draw {
       if (w + lane < end) {
         float v[Slice<T>::N];
         unpack(in.word(w + lane), v, in.x);
-        measure(kind, key, v, in.id(w + lane, 0), each);
 #pragma unroll
-        for (int i = 0; i < Slice<T>::N; ++i) own += each[i];
+        for (int i = 0; i < Slice<T>::N; ++i) own += each[i] = measure(kind, key, v[i], in.id(w + lane, i));
       }
       u64 incl = own;
 #pragma unroll
@@ -480,15 +547,18 @@ struct Draw {
       }
       if (lane == __ffs(over) - 1) {
         u64 left = rest - (incl - own);
-        bool found = false;
+        int token = -1;
+        u64 mass = 0;
 #pragma unroll
         for (int i = 0; i < Slice<T>::N; ++i) {
-          if (!found && left < each[i]) {
-            found = true;
-            f(in.id(w + lane, i), each[i]);
+          if (token < 0 && left < each[i]) {
+            token = in.id(w + lane, i);
+            mass = each[i];
           }
-          left -= found ? 0 : each[i];
+          left -= token < 0 ? each[i] : 0;
         }
+        if (total) write(token, mass, total);
+        else tell(&sm.tau, (u64)key << 32 | (unsigned)~token);
       }
       break;
     }
@@ -496,7 +566,19 @@ struct Draw {
   // The border, bit by bit: the last kept token is the one at which the count (or the weights) of the kept ones reaches
   // `limit`. For lists that overflow. Tokens whose distance is not in [below, within] do not count; false: those that do
   // fall short of the limit.
-  __device__ __noinline__ bool search(bool mass, u64 limit, float per, float below, float within) {
+  __device__ __forceinline__ bool search(bool mass, u64 limit, float per, float below, float within) {
+    const int y = search_apart(parity, mass, limit, per, below, within);
+    parity = y & 1;
+    if (y & 2) keep_from(sm.tau);
+    return y & 2;
+  }
+  static __device__ __noinline__ int search_apart(int parity, bool mass, u64 limit, float per, float below, float within) {
+    Draw d(shared<T>().state);
+    d.parity = parity;
+    const bool done = d.search_here(mass, limit, per, below, within);
+    return d.parity | (done ? 2 : 0);
+  }
+  __device__ __forceinline__ bool search_here(bool mass, u64 limit, float per, float below, float within) {
     auto counts = [&](float x, int id) {
       const float d = distance(x, m, per);
       return x > -INFINITY && d >= below && d <= within && kept(x, id);
@@ -542,9 +624,8 @@ struct Draw {
     const u64 each = mass ? weight_once(unordered(key), m, ch, cl, sm.table) : 1;
     const u64 nth = (limit - above - 1) / each;  // of the tokens with this key, in order
     tally(1, key);
-    find(1, key, nth, [&](int id, u64) { tell(&sm.tau, (u64)key << 32 | (unsigned)~id); });
+    find(1, key, nth, 0);
     meet();
-    tau = sm.tau;
     return true;
   }
   // A CTA's candidates (in sm.mass) to the first CTA's list; the row's number of them.
@@ -594,16 +675,17 @@ struct Draw {
   // Rows of bf16 without top-k: the border of the nucleus from the number of tokens of each value, then the kept weights by looking
   // them up; the warps' sums and tau are left for the draw. False: the border lies among the values without a place (or
   // zeros of both signs have places of their own), and nothing is left but a clean count of bins.
-  __device__ __noinline__ bool values(float p, bool nucleus);
+  static __device__ __noinline__ bool values(float p, bool nucleus) { return Draw(shared<T>().state).values_here(p, nucleus); }
+  __device__ __forceinline__ bool values_here(float p, bool nucleus);
   __device__ __forceinline__ void write(int id, u64 w, u64 total) {
-    q.ids[row] = id;
-    if (!q.logp) return;
+    ids[row] = id;
+    if (!logp) return;
     // of a likely token by its distance from 1, of others by the logit, so that small and large results have their own bits
     const float missing = (float)(total - w) / (float)total;
-    q.logp[row] = missing < 0.5f ? log1pf(-missing)
+    logp[row] = missing < 0.5f ? log1pf(-missing)
                                  : -((m - (float)in.x[id]) / fminf(fmaxf(temperature, 1e-30f), 1e30f) + logf((float)total * 2.842170943e-14f));  // 2^-45
   }
-  __device__ void run();
+  __device__ __forceinline__ void run(const Params& q);
 };
 
 // A fraction of a sum: floor and whether something was cut off. f in [0, 1).
@@ -613,40 +695,8 @@ __device__ __forceinline__ u64 part_of(float f, u64 total, bool& more) {
   return __umul64hi(x, total);
 }
 
-// The place of a bf16 value, by its distance d from the maximum in the values' order: d itself before `middle`, which the values from
-// there to the one before `resume` share; then on from middle + 1; `out` and more: weight 0. Two at a time in 16 bits each, which no
-// carry leaves in the end.
-struct Places {
-  int top, middle, resume, out;
-  uint32_t top2, middle2, resume2, out2;
-  __device__ __forceinline__ uint32_t of(uint32_t w) const {
-    const uint32_t s = (w >> 15) & 0x00010001u, d = top2 - (w ^ (s * 0x7FFFu + 0x80008000u));
-    return __vminu2(__vminu2(d, middle2) + (__vmaxu2(d, resume2) - resume2), out2);
-  }
-  __device__ __forceinline__ float value(int place) const {
-    const unsigned o = top - (place < middle ? place : place + resume - middle);
-    return unordered(o << 16 | (o & 0x8000u ? 0 : 0xFFFFu));
-  }
-  // False: zeros of both signs, which are equal, would have different places.
-  __device__ __forceinline__ bool set(float m, float ch) {
-    top = (int)(ordered(m) >> 16);
-    const int far = max((int)(ordered(m - 47.f / ch) >> 16), 0x0080);  // (weights are 0 from 46.5 factors of two on)
-    const int values = top - far + 1, zero = top - 0x8000, most = PLACES - 2;
-    const int gap = max(values - most, 1);
-    middle = values <= most ? values : max(1, min(zero - gap / 2, values - gap));
-    resume = middle + gap - 1;  // the last one that shares
-    out = middle + 1 + max(values - 1 - resume, 0);
-    top2 = top * 0x10001u;
-    middle2 = middle * 0x10001u;
-    resume2 = resume * 0x10001u;
-    out2 = out * 0x10001u;
-    return zero < 0 || zero >= values || (middle <= zero && zero < resume);
-  }
-};
-
 template <typename T>
-__device__ bool Draw<T>::values(float p, bool nucleus) {
-  Places at;
+__device__ __forceinline__ bool Draw<T>::values_here(float p, bool nucleus) {
   if (!at.set(m, ch)) {
     __syncthreads();
     for (int i = tid; i < BINS; i += NT) sm.hist[i] = 0;
@@ -686,8 +736,14 @@ __device__ bool Draw<T>::values(float p, bool nucleus) {
     middle = warp_sum(middle);
     if (lane == 0 && middle) atomicAdd(in_first(&sm.middle), middle);
   }
-  for (int e = tid * size + rank; e < at.out; e += NT * size)
-    tell(&sm.weight[e], e == at.middle ? 0ull : weight_once(at.value(e), m, ch, cl, sm.table));
+  // each CTA's part of the table, two at a time
+#pragma unroll 1
+  for (int e = 2 * (tid * size + rank); e < at.out; e += 2 * NT * size) {
+    u64 w, other;
+    weights(make_float2(at.value(e), at.value(e + 1)), m, ch, cl, sm.table, w, other);
+    tell(&sm.weight[e], e == at.middle ? 0ull : w);
+    if (e + 1 < at.out) tell(&sm.weight[e + 1], e + 1 == at.middle ? 0ull : other);
+  }
   int border = at.out;
   if (nucleus) {
     __syncthreads();
@@ -736,19 +792,24 @@ __device__ bool Draw<T>::values(float p, bool nucleus) {
   } else {
     meet();
   }
+  int end = border;  // of the places whose tokens are kept, those with the border's value apart
+  if (least)
+    for (int step = 2048, from = -1; step; step /= 2) {  // weights fall from place to place
+      const int e = from + step;
+      if (e >= border) continue;
+      if (e == at.middle ? sm.weight[e - 1] >= least : sm.weight[e] >= least) from = e;
+      end = from + 1;
+    }
   u64 keep = 0;
   unsigned ties = 0;
   in.template walk_raw<2>(w0, w1, [&](const uint4& y, int) {
     bool any = false;
     each_of(y, [&](int place, float) {
-      if (place < border) {
-        const u64 w = sm.weight[place];
-        keep += w >= least ? w : 0;
-      }
+      if (place < end) keep += sm.weight[place];
       ties += place == border;
       any |= place == at.middle;
     });
-    if (any && at.middle < border) keep += rest_of(y, least);
+    if (any && at.middle < end) keep += rest_of(y, least);
   });
   u64 each = border < at.out ? sm.weight[border] : 0;
   each = each >= least ? each : 0;
@@ -760,10 +821,14 @@ __device__ bool Draw<T>::values(float p, bool nucleus) {
     in_first(&sm.sums[0][rank][warp])[0] = nth < 0 ? keep + each * ties : keep;
     if (nth >= 0) in_first(&sm.sums[1][rank][warp])[0] = ties;
   }
-  tau = (u64)key << 32;
+  if (tid == 0) {
+    sm.state.at = at;
+    sm.state.looked_up = 1;
+    sm.state.tau = (u64)key << 32;
+  }
   meet();
   if (nth >= 0) {
-    find(1, key, (u64)nth, [&](int id, u64) { tell(&sm.tau, (u64)key << 32 | (unsigned)~id); });
+    find(1, key, (u64)nth, 0);
     if (rank == 0 && warp == 0) {  // of the border's tokens the warps before the last one's keep all
       int before = 0, own[4];
 #pragma unroll
@@ -782,13 +847,13 @@ __device__ bool Draw<T>::values(float p, bool nucleus) {
       }
     }
     meet();
-    tau = sm.tau;
+    keep_from(sm.tau);
   }
   return true;
 }
 
 template <typename T>
-__device__ __forceinline__ void Draw<T>::run() {
+__device__ __forceinline__ void Draw<T>::run(const Params& q) {
   // ---- the row's request
   temperature = q.s.temperature_dev ? q.s.temperature_dev[row] : q.s.temperature;
   const int k_given = q.s.top_k_dev ? q.s.top_k_dev[row] : q.s.top_k;
@@ -874,6 +939,8 @@ __device__ __forceinline__ void Draw<T>::run() {
   ch = sm.ch;
   cl = sm.cl;
   least = sm.least;
+  if (tid == 0) sm.state = *this;
+  __syncthreads();
   if (!(fabsf(m) < INFINITY) || !(temperature >= 0.f)) {  // nothing to draw from
     if (rank == 0 && tid == 0) {
       q.ids[row] = -1;
@@ -883,7 +950,7 @@ __device__ __forceinline__ void Draw<T>::run() {
   }
   if (temperature == 0.f) {  // the likeliest
     tally(1, ordered(m));
-    find(1, ordered(m), 0, [&](int id, u64) { write(id, 1, 1); });
+    find(1, ordered(m), 0, 1);
     return;
   }
 
@@ -1153,7 +1220,7 @@ __device__ __forceinline__ void Draw<T>::run() {
       }
       meet();
       if (sm.tau) {
-        tau = sm.tau;
+        keep_from(sm.tau);
       } else {
         if (above >= limit || !search(true, limit - above, per, below, within)) search(true, limit, per, -INFINITY, INFINITY);
         tally(0, 0);
@@ -1166,17 +1233,22 @@ __device__ __forceinline__ void Draw<T>::run() {
   // ---- the draw
   const u64 total = tallied();
   bool more;
-  find(0, 0, part_of(fminf(u, 0.99999994f), total, more), [&](int id, u64 w) { write(id, w, total); });
+  find(0, 0, part_of(fminf(u, 0.99999994f), total, more), total);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ Params q) {
-  __shared__ Smem sm;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks(), row = (int)(blockIdx.x / size);
-  const int a = min(rank * q.slice, q.vocab), len = min(q.slice, q.vocab - a);
-  Draw<T> d(q, sm, Slice<T>(static_cast<const T*>(q.logits) + row * q.row_stride, a, len), row);
-  d.run();
+  State<T> s{};
+  s.rank = (int)cluster.block_rank();
+  s.size = (int)cluster.num_blocks();
+  s.row = (int)(blockIdx.x / s.size);
+  const int a = min(s.rank * q.slice, q.vocab), len = min(q.slice, q.vocab - a);
+  s.in = Slice<T>(static_cast<const T*>(q.logits) + s.row * q.row_stride, a, len);
+  s.ids = q.ids;
+  s.logp = q.logp;
+  Draw<T>(s).run(q);
+  const int size = s.size;
   if (size > 1) cluster.sync();  // no CTA leaves while others use its memory
 }
 
