@@ -13,12 +13,14 @@
 // k-th largest of the threads' maxima is a floor that few others reach: those are listed, sorted and resolved in the first CTA.
 // Without it, a pass counts the logits by their distance from the maximum, which places the border of the nucleus to a few
 // bins; a second pass adds the weights above them exactly and lists those within, whose order decides. Lists that overflow (thousands
-// of equal logits at a border) fall back to a search of the border bit by bit. The drawn token is found by the slices' sums, a
-// warp's, and then its words'. The passes after the first read from L2; the weights' 50 instructions a logit bound them.
+// of equal logits at a border) fall back to a search of the border bit by bit. bf16 rows instead count their tokens by value, which
+// gives the border exactly with a weight for each value, and then look the weights up. The drawn token is found by the slices' sums, a
+// warp's, and then its words'. The passes after the first read from L2; the weights' 50 instructions a logit bound them, by
+// value the adds and loads of shared memory (9 clocks a warp's 32 logits in each pass, bank conflicts).
 //
-// Measured: one row of 128256 fp32, temperature, top 50, top-p and min-p: 16 us (cluster barriers and the list's few steps); 512 rows of
-// 128256 bf16, top 40: 59 (131 MB, 0.33 of the measured copy rate); 64 rows of 151936 bf16, top-p 0.9 to 1: 87, of which
-// the weights' pass is 24 and the bins' 10; 37 rows of 32000 fp32, no limits: 20.
+// Measured: one row of 128256 fp32, temperature, top 50, top-p and min-p: 15 us (cluster barriers and the list's few steps); 512 rows of
+// 128256 bf16, top 40: 50 (131 MB, 0.39 of the measured copy rate); 64 rows of 151936 bf16, top-p 0.9 to 1: 49 (87 by bins), of
+// which the count is 10, the table and the border 11, the kept weights 10, the two searches 14; 37 rows of 32000 fp32, no limits: 18.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -56,7 +58,9 @@ constexpr int PER = LIST / NT;       // of a list, or of the bins, to a thread
 // bf16 logits have few values: the ones whose weights are above 0, from the maximum down but for those near zero, have a place each
 // in a table. 13 factors of two either side of zero leave a value in 4000 of a row like N(0, 1) between them.
 constexpr int PLACES = 3328, PLACES_PER = (PLACES + NT - 1) / NT;
-constexpr int BY_VALUE = 4 * PLACES;  // of rows with so many tokens; below, the table costs as much as it saves
+// From rows of so many tokens on: 300 rows of 151936, top-p 0.9, take 116 us (212 by bins), 64 of 32000 31 (34), of 8192 alike,
+// 64 of 4096 21 (19): the table is as large as the row.
+constexpr int BY_VALUE = 8192;
 static_assert(LIST == BINS, "alike for both");
 constexpr int MAXIMA = 2;            // of a thread: more than one, so that a CTA alone has enough for large top-k
 
@@ -452,7 +456,7 @@ struct Draw : State<T> {
     u64 w;
     const int place = s.looked_up ? s.at.of(__float_as_uint(x) >> 16) & 0xFFFF : 0;
     if (s.looked_up && place != s.at.middle) w = place < s.at.out ? sm.weight[place] : 0;
-    else w = weight_once(x, s.m, s.ch, s.cl, sm.table);
+    else w = weight(x, s.m, s.ch, s.cl, sm.table);
     return w >= s.least ? w : 0;
   }
   // The sums of the warps' runs, to the first CTA.
