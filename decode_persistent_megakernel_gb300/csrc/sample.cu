@@ -16,7 +16,7 @@
 // of equal logits at a border) fall back to a search of the border bit by bit. bf16 rows instead count their tokens by value, which
 // gives the border exactly with a weight for each value, and then look the weights up. The drawn token is found by the slices' sums, a
 // warp's, and then its words'. The passes after the first read from L2; the weights' 50 instructions a logit bound them, by
-// value the adds and loads of shared memory (9 clocks a warp's 32 logits in each pass, bank conflicts).
+// value the adds and loads of shared memory (9 clocks to a warp's 32 logits in each pass), and then the cluster's barriers.
 //
 // Measured: one row of 128256 fp32, temperature, top 50, top-p and min-p: 15 us (cluster barriers and the list's few steps); 512 rows of
 // 128256 bf16, top 40: 50 (131 MB, 0.39 of the measured copy rate); 64 rows of 151936 bf16, top-p 0.9 to 1: 49 (87 by bins), of
